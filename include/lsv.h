@@ -48,7 +48,8 @@ typedef enum {
   LSV_ERR_WORKSPACE = 4,    /* workspace NULL or smaller than the queried size */
   LSV_ERR_CUDA = 5,         /* a CUDA runtime/driver call failed (launch, attribute, tensor map) */
   LSV_ERR_TIMEOUT = 6,      /* device: a bounded wait ran out (kernel unwound, outputs undefined) */
-  LSV_ERR_DEVICE_INDEX = 7  /* device: an index read from memory was out of range (outputs undefined) */
+  LSV_ERR_DEVICE_INDEX = 7, /* device: an index read from memory was out of range (outputs undefined) */
+  LSV_ERR_PAGES = 8         /* device: a pool had fewer free pages than a call needed (nothing changed) */
 } lsv_status;
 
 /* One MoE FFN layer: T tokens of width H; E routed experts of which each token
@@ -217,6 +218,116 @@ lsv_status lsv_gather_rows(const void *table, const int32_t *idx, int32_t n, int
 lsv_status spec_cache_append(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                              const int32_t *ctx_len, int32_t B, int32_t Q, int32_t L, int32_t row_elems,
                              lsv_stream stream);
+
+/* The paged key/value cache held in 4 bits.
+ *
+ * The verify pass streams every sequence's cache once a step; 4 bits make that
+ * stream 3.76 times shorter than bf16 (d + 4 d/64 bytes a position and head, keys
+ * and values together).  64 consecutive dims of a position, head and tensor
+ * share a scale s = bf16(max |x| / 7); a code n = rint(x / s), ties to even,
+ * limited to [-8, 7], stands for n s (s = 0: zeros).  A group that holds a NaN or
+ * an infinity stands for NaN.
+ *
+ * A page holds `page` positions (16, 32, 64, 128 or 256) of all nkv key heads,
+ * spec_q4_page_bytes(nkv, d, page) bytes in an order of the library's own; a pool
+ * is [P, page bytes] (one per layer).  table [B, M] int32 (device): entry i of row
+ * b is the page of sequence b's positions i*page .., -1 where there is none.
+ * ctx_len [B] int32 (device): the lengths, 0 <= ctx_len[b] <= M*page; 0 stands for
+ * a slot without a sequence.  In all three calls the Q (or N) rows of a sequence
+ * are its last ones: row j is position ctx_len[b] - Q + j, and rows before
+ * position 0 (a sequence shorter than Q) stand for nothing.
+ * A length outside [0, M*page], or a page outside [0, P) where one is needed,
+ * raises LSV_ERR_DEVICE_INDEX.  Supported: d in {64, 128}, 1 <= nkv <= 1024,
+ * M*page <= 2^24 (attention) or 2^30, B*M < 2^31, any pool size.
+ *
+ * spec_q4_append: k_new, v_new [B, Q, nkv, d] bf16 to the pages (Q >= 0).  Rows
+ *   that stand for nothing, and sequences or pages out of range, are not written.
+ *   Two rows of the table must not hold the same page where they are written
+ *   (spec_pages_resize sees to that).  One launch.
+ * spec_q4_read: the last N positions of every sequence back as bf16, k_out and
+ *   v_out [B, N, nkv, d]: bf16(n s).  Rows that stand for nothing, and those out of
+ *   range, are zeros.  One launch.
+ * spec_q4_attention: causal attention of the verified positions, with nh query
+ *   heads on nkv key heads (head h reads key head h / (nh / nkv)):
+ *     q, out [B, Q, nh, d] bf16
+ *     out[b,j,h] = sum_{t <= p} softmax_t(scale * q[b,j,h].k[b,t,h']) v[b,t,h'],
+ *     p = ctx_len[b] - Q + j, over the values that the codes stand for
+ *   fp32 scores and sums; the weights P s enter the second product as f16.  Rows
+ *   that stand for nothing are zeros, and so are those of a length out of range;
+ *   the positions of a page out of range are left out.  Nothing at or behind
+ *   ctx_len[b] reaches an output, whatever the pages hold there.  A row's result
+ *   depends on its query, its visible positions, B, nkv and M*page, and not on
+ *   the other rows.  1 <= Q <= 8, nh / nkv <= 16, B <= 65535, B*nkv <= 262144,
+ *   scale > 0, |q| < 2^112.  One launch, or two where a sequence is split.
+ *   ws: spec_q4_attention_workspace_size(...) bytes (0: unsupported); needs no
+ *   initialisation.
+ * Device pointers, 16-byte aligned. */
+size_t spec_q4_page_bytes(int32_t nkv, int32_t d, int32_t page);
+lsv_status spec_q4_append(const void *k_new, const void *v_new, void *pool, const int32_t *table,
+                          const int32_t *ctx_len, int32_t B, int32_t Q, int32_t nkv, int32_t d, int32_t page,
+                          int32_t M, int32_t P, lsv_stream stream);
+lsv_status spec_q4_read(const void *pool, const int32_t *table, const int32_t *ctx_len, int32_t B, int32_t N,
+                        int32_t nkv, int32_t d, int32_t page, int32_t M, int32_t P, void *k_out, void *v_out,
+                        lsv_stream stream);
+size_t spec_q4_attention_workspace_size(int32_t B, int32_t Q, int32_t M, int32_t page, int32_t nh, int32_t nkv,
+                                        int32_t d);
+lsv_status spec_q4_attention(const void *q, const void *pool, const int32_t *table, const int32_t *ctx_len, int32_t B,
+                             int32_t Q, int32_t nh, int32_t nkv, int32_t d, int32_t page, int32_t M, int32_t P,
+                             float scale, void *out, void *ws, size_t ws_bytes, lsv_stream stream);
+
+/* The pages of a paged cache.  The calls know nothing of what a page holds: they
+ * serve any cache whose page is page_bytes (a multiple of 16) in each of `layers`
+ * layers, pool [layers, P, page_bytes], all layers by one table.
+ *   table [B, M] int32: the pages of every sequence, -1 for none
+ *   ref   [P] int32: how many table entries hold a page; 0: the page is free
+ * Inputs are read as they were before the call, and each output may be its input
+ * (table_out = table, ref_out = ref).  Deterministic: new pages are the free ones
+ * of lowest number, in the order (row, entry).
+ *
+ * spec_pages_resize: row b keeps its positions 0..keep[b]-1 and gets room for the
+ *   positions up to cap[b] (int32, device; 0 <= keep[b] <= cap[b] <= M*page), ready
+ *   to be written from keep[b] on:
+ *     - entries at or behind ceil(cap / page) are given back (-1);
+ *     - entries that hold no kept position are replaced where another row holds
+ *       their page too, and filled where there was none;
+ *     - the entry of position keep[b], if it holds kept positions as well, another
+ *       row holds its page too and cap[b] > keep[b], gets a new page and, in every
+ *       layer, a copy of the old one's contents.
+ *   keep = cap = 0 gives a sequence's pages back; keep = cap = the length after a
+ *   verify step those of the rejected drafts.  Pages given back in a call are not
+ *   given out in the same call, and if every holder of a shared page goes on
+ *   writing, each gets a copy.  If the pool has too few free pages nothing changes
+ *   (the outputs equal the inputs) and LSV_ERR_PAGES is raised.
+ *   A row whose bounds are out of range stays as it is, and raises
+ *   LSV_ERR_DEVICE_INDEX; so do an entry outside [-1, P), a kept position without
+ *   a page (it gets one), and a held page that counts as free.
+ *   stats_opt [4] int32 (device): pages taken (or, with LSV_ERR_PAGES, needed),
+ *   free pages before the call, pages copied, entries given back or replaced.
+ * spec_pages_fork: row b takes the pages of row parent[b] (int32, device; -1: none)
+ *   as they were before the call: table_out[b, :] = table[parent[b], :], and the
+ *   counts follow.  The pages are shared until spec_pages_resize separates what
+ *   is written.  A parent outside [-1, B) gives an empty row and raises
+ *   LSV_ERR_DEVICE_INDEX.
+ * spec_pages_compact: the n live pages (ref > 0) go to the numbers 0..n-1: those at
+ *   or above n move, in rising order, to the free numbers below n, in every layer.
+ *   table_out, ref_out: with the new numbers.  map_opt [P] int32: the new number of
+ *   each live page, -1 for the others.  stats_opt [4] int32: n, pages moved, 0, 0.
+ *   An entry without a live page becomes -1 (and raises LSV_ERR_DEVICE_INDEX
+ *   unless it was -1).
+ * B <= 65536, P <= 2^24, B*M < 2^31, M*page <= 2^30 (page: any positive number).
+ * ws: spec_pages_workspace_size(B, M, P) bytes (0: unsupported); needs no
+ * initialisation.  Device pointers, 16-byte aligned. */
+size_t spec_pages_workspace_size(int32_t B, int32_t M, int32_t P);
+lsv_status spec_pages_resize(void *pool, int32_t layers, int64_t page_bytes, const int32_t *table, const int32_t *ref,
+                             const int32_t *keep, const int32_t *cap, int32_t B, int32_t M, int32_t P, int32_t page,
+                             int32_t *table_out, int32_t *ref_out, int32_t *stats_opt, void *ws, size_t ws_bytes,
+                             lsv_stream stream);
+lsv_status spec_pages_fork(const int32_t *table, const int32_t *ref, const int32_t *parent, int32_t B, int32_t M,
+                           int32_t P, int32_t *table_out, int32_t *ref_out, void *ws, size_t ws_bytes,
+                           lsv_stream stream);
+lsv_status spec_pages_compact(void *pool, int32_t layers, int64_t page_bytes, const int32_t *table, const int32_t *ref,
+                              int32_t B, int32_t M, int32_t P, int32_t *table_out, int32_t *ref_out, int32_t *map_opt,
+                              int32_t *stats_opt, void *ws, size_t ws_bytes, lsv_stream stream);
 
 /* Greedy verification with the verify logits produced by the verifier's output
  * layer, inside the call (the logits are never written to memory):

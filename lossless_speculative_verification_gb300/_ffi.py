@@ -15,13 +15,15 @@ LIB_PATH = os.path.join(_HERE, "_lib", "liblsv.so")
 STATUS = {
     0: "LSV_OK", 1: "LSV_ERR_INVALID_ARG", 2: "LSV_ERR_UNSUPPORTED", 3: "LSV_ERR_MISALIGNED",
     4: "LSV_ERR_WORKSPACE", 5: "LSV_ERR_CUDA", 6: "LSV_ERR_TIMEOUT", 7: "LSV_ERR_DEVICE_INDEX",
+    8: "LSV_ERR_PAGES",
 }
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE_INDEX = range(8)
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE_INDEX, ERR_PAGES = range(9)
 
 # Every function the header declares, with its ctypes signature.
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
+I64 = ctypes.c_int64
 U64 = ctypes.c_uint64
 
 
@@ -66,6 +68,15 @@ SIGNATURES = {
     "spec_cond_accept_from_histogram": (I32, [P, I32, P]),
     "spec_verify_attention": (I32, [P, P, P, P, I32, I32, I32, I32, I32, ctypes.c_float, P, P, SZ, P]),
     "spec_verify_lmhead": (I32, [P, P, P, I32, I32, I32, I32, P, P, P, P, SZ, P]),
+    "spec_q4_page_bytes": (SZ, [I32, I32, I32]),
+    "spec_q4_append": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, P]),
+    "spec_q4_read": (I32, [P, P, P, I32, I32, I32, I32, I32, I32, I32, P, P, P]),
+    "spec_q4_attention_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+    "spec_q4_attention": (I32, [P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, ctypes.c_float, P, P, SZ, P]),
+    "spec_pages_workspace_size": (SZ, [I32, I32, I32]),
+    "spec_pages_resize": (I32, [P, I32, I64, P, P, P, P, I32, I32, I32, I32, P, P, P, P, SZ, P]),
+    "spec_pages_fork": (I32, [P, P, P, I32, I32, I32, P, P, P, SZ, P]),
+    "spec_pages_compact": (I32, [P, I32, I64, P, P, I32, I32, I32, P, P, P, P, P, SZ, P]),
     "rmsnorm_residual": (I32, [P, P, P, I32, I32, ctypes.c_float, P]),
     "lsv_get_device_error": (I32, [ctypes.POINTER(I32), P]),
     "lsv_set_wait_limit_ns": (I32, [U64]),

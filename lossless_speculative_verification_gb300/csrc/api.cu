@@ -160,6 +160,7 @@ const char* lsv_status_string(lsv_status s) {
     case LSV_ERR_CUDA: return "CUDA call failed";
     case LSV_ERR_TIMEOUT: return "device wait timed out";
     case LSV_ERR_DEVICE_INDEX: return "device index out of range";
+    case LSV_ERR_PAGES: return "too few free pages";
   }
   return "unknown status";
 }

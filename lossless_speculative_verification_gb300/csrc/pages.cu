@@ -1,0 +1,618 @@
+// pages.cu -- the pages of a paged cache: giving room and taking it back, copies
+// on write, forks, and compaction.
+//
+// A pool has P pages, each with a count of the table entries that hold it (0:
+// free).  A table [B, M] has a row a sequence: entry i is the page of the
+// positions i * page .., or -1.  Every layer's cache goes by the same table.
+//
+// All three calls are scans over the table and the counts.  Nothing depends on
+// the order of atomics: new pages are the free ones of lowest number, given out
+// in the order (row, entry), and counts are sums of integers.  The calls read
+// their inputs as they were before the call, so each output may be its input.
+//
+// Two grids do the bookkeeping: the first reduces chunks of kPgChunk counts to
+// two bits a page (free, shared) and the rows to the number of pages they need;
+// the second begins each CTA with the sums of what lies before it.  The page
+// contents follow in a third, which streams a list of (source, destination)
+// pairs through the whole GPU.
+#include "internal.h"
+#include "lsv.h"
+#include "ptx.cuh"
+
+namespace lsv {
+namespace {
+
+constexpr int kPgThreads = 256;
+constexpr int kPgWarps = kPgThreads / 32;
+constexpr int kPgChunk = 4096;  // pages a CTA reduces
+constexpr int kPgChunkWords = kPgChunk / 32;
+constexpr int kPgMaxPages = 1 << 24;
+constexpr int kPgMaxRows = 1 << 16;
+constexpr int kPgCopyBytes = 16384;  // bytes a CTA copies at a time
+
+struct PgWs {
+  int* need;       // [B] pages a row takes
+  int* chunk_n;    // [chunks] free pages (resize) or live pages (compact) of a chunk
+  uint32_t* bits;  // [2, words] bit maps: free, shared
+  int* list;       // [max(B * M, P)] page numbers in order of rank (new pages; or the pages that move)
+  int* list2;      // [max(B, P)] destinations of the copies
+  int* src;        // [B] sources of the copies
+  int* rank;       // [P] which of the moving pages a page is, -1: none
+  int* count;      // copies
+  int32_t* table;  // [B, M] the table as it was, where a fork writes it in place
+  size_t total;
+};
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+PgWs pg_layout(void* base, size_t B, size_t M, size_t P) {
+  PgWs w;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t o = 0;
+  auto take = [&](size_t ints) {
+    uint8_t* at = b + o;
+    o += round256(ints * 4);
+    return at;
+  };
+  const size_t chunks = (P + kPgChunk - 1) / kPgChunk, bm = B * M;
+  w.need = reinterpret_cast<int*>(take(B));
+  w.chunk_n = reinterpret_cast<int*>(take(chunks));
+  w.bits = reinterpret_cast<uint32_t*>(take(2 * chunks * kPgChunkWords));
+  w.list = reinterpret_cast<int*>(take(bm > P ? bm : P));
+  w.list2 = reinterpret_cast<int*>(take(B > P ? B : P));
+  w.src = reinterpret_cast<int*>(take(B));
+  w.rank = reinterpret_cast<int*>(take(P));
+  w.count = reinterpret_cast<int*>(take(64));
+  w.table = reinterpret_cast<int32_t*>(take(bm));
+  w.total = o;
+  return w;
+}
+
+// Sum over the CTA; every thread gets it.
+__device__ __forceinline__ int block_sum(int v, int* tmp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int s = 0;
+#pragma unroll
+  for (int w = 0; w < kPgWarps; ++w) s += tmp[w];
+  return s;
+}
+
+// Exclusive prefix of v over the CTA's threads; *sum the total.
+__device__ __forceinline__ int block_prefix(int v, int* tmp, int* sum) {
+  const int lane = threadIdx.x & 31;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  __syncthreads();
+  if (lane == 31) tmp[threadIdx.x >> 5] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kPgWarps; ++w) {
+    if (w < (int)(threadIdx.x >> 5)) before += tmp[w];
+    all += tmp[w];
+  }
+  *sum = all;
+  return before + s - v;
+}
+
+// Sum of a[0..n) over the CTA, and of a[0..upto) in *part.
+__device__ __forceinline__ int sum_upto(const int* a, int n, int upto, int* part, int* tmp) {
+  int all = 0, pre = 0;
+  for (int i = threadIdx.x; i < n; i += kPgThreads) {
+    const int v = __ldcg(a + i);
+    all += v;
+    if (i < upto) pre += v;
+  }
+  *part = block_sum(pre, tmp);
+  return block_sum(all, tmp);
+}
+
+// What a turn does with entry i of a row: keep it, give it a new page, copy the old one into the new one.
+struct Entry {
+  bool held, fresh, copied, gone;
+};
+__device__ __forceinline__ Entry entry_of(int i, bool held, bool shared, int keep, int cap, int page) {
+  Entry e;
+  e.held = held;
+  const int kept = (keep + page - 1) / page, wanted = (cap + page - 1) / page;
+  e.copied = held && shared && i == keep / page && keep % page != 0 && cap > keep;
+  e.fresh = i < wanted && (!held || e.copied || (i >= kept && shared));
+  e.gone = held && (e.fresh || i >= wanted);
+  return e;
+}
+
+struct PgResize {
+  const int32_t *table, *ref, *keep, *cap;
+  int32_t *table_out, *ref_out, *stats;
+  int B, M, P, page, chunks;
+  PgWs w;
+  int* err;
+};
+
+// A row's bounds; false: out of range (the row stays as it is).
+__device__ __forceinline__ bool row_bounds(const PgResize& p, int b, int* keep, int* cap) {
+  *keep = __ldcg(p.keep + b);
+  *cap = __ldcg(p.cap + b);
+  return *keep >= 0 && *cap >= *keep && *cap <= (long long)p.M * p.page;
+}
+
+// Chunk c of the counts: bit maps and the number of free pages; row c of the table: the pages it needs.
+__global__ void __launch_bounds__(kPgThreads) resize_count_kernel(const PgResize p) {
+  __shared__ int tmp[kPgWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (c == 0 && threadIdx.x < 64) {
+    p.w.count[threadIdx.x] = 0;
+    if (p.stats && threadIdx.x < 4) p.stats[threadIdx.x] = 0;
+  }
+  if (c < p.chunks) {
+    int n = 0;
+    for (int i = warp; i < kPgChunkWords; i += kPgWarps) {
+      const int at = c * kPgChunk + 32 * i + lane;
+      const int r = at < p.P ? __ldcg(p.ref + at) : -1;
+      const uint32_t free = __ballot_sync(0xffffffffu, at < p.P && r <= 0), shared = __ballot_sync(0xffffffffu, r > 1);
+      if (lane == 0) {
+        p.w.bits[c * kPgChunkWords + i] = free;
+        p.w.bits[(p.chunks + c) * kPgChunkWords + i] = shared;
+        n += __popc(free);
+      }
+      if (p.ref_out != p.ref && at < p.P) p.ref_out[at] = r;
+    }
+    n = block_sum(n, tmp);
+    if (threadIdx.x == 0) p.w.chunk_n[c] = n;
+  }
+  if (c < p.B) {
+    int keep, cap, n = 0;
+    if (row_bounds(p, c, &keep, &cap)) {
+      for (int i = threadIdx.x; i < p.M; i += kPgThreads) {
+        const int pg = __ldcg(p.table + (size_t)c * p.M + i);
+        const bool held = pg >= 0 && pg < p.P;
+        if (pg < -1 || pg >= p.P || (!held && i < (keep + p.page - 1) / p.page)) set_error(p.err, kErrDeviceIndex);
+        const int r = held ? __ldcg(p.ref + pg) : 0;
+        if (held && r <= 0) set_error(p.err, kErrDeviceIndex);  // held, and counted free
+        n += entry_of(i, held, r > 1, keep, cap, p.page).fresh;
+      }
+    } else if (threadIdx.x == 0) {
+      set_error(p.err, kErrDeviceIndex);
+    }
+    n = block_sum(n, tmp);
+    if (threadIdx.x == 0) p.w.need[c] = n;
+  }
+}
+
+// Row b: its new pages' numbers, its entries, the counts.
+__global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResize p) {
+  __shared__ int tmp[kPgWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x;
+  int first, unused;
+  const int need = sum_upto(p.w.need, p.B, b, &first, tmp);
+  const int mine = __ldcg(p.w.need + b);
+  const int free = sum_upto(p.w.chunk_n, p.chunks, 0, &unused, tmp);
+  if (b == 0 && threadIdx.x == 0) {
+    if (p.stats) p.stats[0] = need, p.stats[1] = free;
+    if (need > free) set_error(p.err, kErrPages);
+  }
+  int keep, cap;
+  const bool ok = row_bounds(p, b, &keep, &cap) && need <= free;
+  const int32_t* row = p.table + (size_t)b * p.M;
+  int32_t* out = p.table_out + (size_t)b * p.M;
+  if (!ok) {
+    if (p.table_out != p.table)
+      for (int i = threadIdx.x; i < p.M; i += kPgThreads) out[i] = __ldcg(row + i);
+    return;
+  }
+  int* fresh = p.w.list + first;  // the pages of ranks first .. first + mine - 1
+  if (mine > 0) {
+    __shared__ int before_s[kPgThreads];  // free pages below each chunk of the tile
+    int below = 0;
+    for (int c0 = 0; c0 < p.chunks && below < first + mine; c0 += kPgThreads) {
+      const int c = c0 + threadIdx.x;
+      const int n = c < p.chunks ? __ldcg(p.w.chunk_n + c) : 0;
+      int all;
+      const int at = below + block_prefix(n, tmp, &all);
+      before_s[threadIdx.x] = at;
+      const int skip = block_sum(c < p.chunks && at + n <= first, tmp);  // chunks that end before the row's first
+      for (int k = skip; k < kPgThreads && c0 + k < p.chunks && before_s[k] < first + mine; ++k) {
+        uint32_t word = threadIdx.x < kPgChunkWords
+                            ? __ldcg(p.w.bits + (size_t)(c0 + k) * kPgChunkWords + threadIdx.x) : 0u;
+        int in_chunk;
+        int rank = before_s[k] + block_prefix(__popc(word), tmp, &in_chunk);
+        while (word) {
+          const int bit = __ffs(word) - 1;
+          word &= word - 1;
+          if (rank >= first && rank < first + mine) fresh[rank - first] = (c0 + k) * kPgChunk + 32 * threadIdx.x + bit;
+          ++rank;
+        }
+      }
+      below += all;
+      __syncthreads();
+    }
+    __syncthreads();
+  }
+  const uint32_t* shared = p.w.bits + (size_t)p.chunks * kPgChunkWords;
+  int given = 0, gone = 0;
+  for (int i0 = 0; i0 < p.M; i0 += kPgThreads) {
+    const int i = i0 + threadIdx.x;
+    const int pg = i < p.M ? __ldcg(row + i) : -1;
+    const bool held = pg >= 0 && pg < p.P;
+    Entry e = entry_of(i, held, held && (__ldcg(shared + (pg >> 5)) >> (pg & 31) & 1u), keep, cap, p.page);
+    if (i >= p.M) e.fresh = e.gone = e.copied = false;
+    int all;
+    const int rank = given + block_prefix(e.fresh, tmp, &all);
+    given += all;
+    if (i >= p.M) continue;
+    int to = held && !e.gone ? pg : -1;
+    if (e.fresh) {
+      to = fresh[rank];
+      atomicAdd(p.ref_out + to, 1);
+      if (e.copied) {
+        const int k = atomicAdd(p.w.count, 1);  // any order: the copies are apart
+        p.w.src[k] = pg;
+        p.w.list2[k] = to;
+      }
+    }
+    if (e.gone) {
+      atomicSub(p.ref_out + pg, 1);
+      ++gone;
+    }
+    out[i] = to;
+  }
+  if (p.stats) {
+    gone = block_sum(gone, tmp);
+    if (threadIdx.x == 0 && gone) atomicAdd(p.stats + 3, gone);
+  }
+}
+
+struct PgCopy {
+  uint8_t* pool;  // [layers, P, page_bytes]
+  const int *src, *dst, *count;
+  int layers, P;
+  size_t page_bytes;
+  int32_t* copied;  // optional: receives the number of pages
+};
+
+// Pieces of kPgCopyBytes of every listed page of every layer, dealt over the grid.
+__device__ __forceinline__ void copy_pages(const PgCopy& p) {
+  const long long pieces = (long long)((p.page_bytes + kPgCopyBytes - 1) / kPgCopyBytes);
+  const long long n = __ldcg(p.count), units = n * p.layers * pieces;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long r = u / pieces, piece = u - r * pieces, k = r / p.layers, l = r - k * p.layers;
+    const size_t off = (size_t)piece * kPgCopyBytes;
+    const size_t bytes = p.page_bytes - off < kPgCopyBytes ? p.page_bytes - off : kPgCopyBytes;
+    const uint4* s = reinterpret_cast<const uint4*>(p.pool + ((size_t)l * p.P + __ldcg(p.src + k)) * p.page_bytes + off);
+    uint4* d = reinterpret_cast<uint4*>(p.pool + ((size_t)l * p.P + __ldcg(p.dst + k)) * p.page_bytes + off);
+    constexpr int kU = kPgCopyBytes / 16 / kPgThreads;
+    uint4 v[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const size_t at = threadIdx.x + i * kPgThreads;
+      if (at * 16 < bytes) v[i] = s[at];
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const size_t at = threadIdx.x + i * kPgThreads;
+      if (at * 16 < bytes) d[at] = v[i];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPgThreads) copy_pages_kernel(const PgCopy p) {
+  pdl_wait();
+  pdl_trigger();
+  if (p.copied && blockIdx.x == 0 && threadIdx.x == 0) *p.copied = __ldcg(p.count);
+  copy_pages(p);
+}
+
+// ----------------------------------------------------------------------------- fork
+struct PgFork {
+  const int32_t *table, *ref, *parent;
+  int32_t *table_out, *ref_out;
+  int B, M, P;
+  int32_t* old;  // copy of the table where table_out is table
+  int* err;
+};
+
+__global__ void __launch_bounds__(kPgThreads) fork_save_kernel(const PgFork p) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t step = (size_t)gridDim.x * kPgThreads, at = (size_t)blockIdx.x * kPgThreads + threadIdx.x;
+  if (p.table_out == p.table)
+    for (size_t i = at; i < (size_t)p.B * p.M; i += step) p.old[i] = __ldcg(p.table + i);
+  if (p.ref_out != p.ref)
+    for (size_t i = at; i < (size_t)p.P; i += step) p.ref_out[i] = __ldcg(p.ref + i);
+}
+
+// Row b: takes its parent's pages; the pages that it held get one count for each of its children, less its own.
+__global__ void __launch_bounds__(kPgThreads) fork_rows_kernel(const PgFork p) {
+  __shared__ int tmp[kPgWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x;
+  int children = 0;
+  for (int i = threadIdx.x; i < p.B; i += kPgThreads) children += __ldcg(p.parent + i) == b;
+  const int more = block_sum(children, tmp) - 1;
+  const int from = __ldcg(p.parent + b);
+  const bool has = from >= 0 && from < p.B;
+  if ((from < -1 || from >= p.B) && threadIdx.x == 0) set_error(p.err, kErrDeviceIndex);
+  const int32_t* table = p.table_out == p.table ? p.old : p.table;
+  for (int i = threadIdx.x; i < p.M; i += kPgThreads) {
+    const int mine = __ldcg(table + (size_t)b * p.M + i);
+    if (mine >= 0 && mine < p.P) {
+      if (more) atomicAdd(p.ref_out + mine, more);
+    } else if (mine != -1) {
+      set_error(p.err, kErrDeviceIndex);
+    }
+    p.table_out[(size_t)b * p.M + i] = has ? __ldcg(table + (size_t)from * p.M + i) : -1;
+  }
+}
+
+// ----------------------------------------------------------------------------- compact
+struct PgCompact {
+  const int32_t *table, *ref;
+  int32_t *table_out, *ref_out, *map, *stats;
+  int B, M, P, chunks;
+  PgWs w;
+  PgCopy copy;
+  int* err;
+};
+
+__global__ void __launch_bounds__(kPgThreads) compact_count_kernel(const PgCompact p) {
+  __shared__ int tmp[kPgWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int n = 0;
+  for (int i = warp; i < kPgChunkWords; i += kPgWarps) {
+    const int at = c * kPgChunk + 32 * i + lane;
+    const uint32_t live = __ballot_sync(0xffffffffu, at < p.P && __ldcg(p.ref + at) > 0);
+    if (lane == 0) {
+      p.w.bits[c * kPgChunkWords + i] = live;
+      n += __popc(live);
+    }
+  }
+  n = block_sum(n, tmp);
+  if (threadIdx.x == 0) p.w.chunk_n[c] = n;
+}
+
+// Chunk c: the k-th free page below the live count goes to list2[k], the k-th live one at or above it to
+// list[k].  Live pages below the count are as many as the count less the pages that move.
+__global__ void __launch_bounds__(kPgThreads) compact_list_kernel(const PgCompact p) {
+  __shared__ int tmp[kPgWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x;
+  int before;
+  const int live = sum_upto(p.w.chunk_n, p.chunks, c, &before, tmp);
+  // live pages below number `live`
+  int under, all;
+  const int cl = live / kPgChunk;  // the chunk of that number (may lie behind the last page)
+  sum_upto(p.w.chunk_n, p.chunks, cl, &under, tmp);
+  if (cl < p.chunks) {
+    const int word = threadIdx.x, rest = live - cl * kPgChunk - 32 * word;  // pages of this word below the number
+    uint32_t v = word < kPgChunkWords ? __ldcg(p.w.bits + cl * kPgChunkWords + word) : 0u;
+    if (rest <= 0)
+      v = 0u;
+    else if (rest < 32)
+      v &= (1u << rest) - 1u;
+    under += block_sum(__popc(v), tmp);
+  }
+  uint32_t v = threadIdx.x < kPgChunkWords ? __ldcg(p.w.bits + c * kPgChunkWords + threadIdx.x) : 0u;
+  int rank = before + block_prefix(__popc(v), tmp, &all);  // live pages before this word
+  if (threadIdx.x < kPgChunkWords) {
+    const int at0 = c * kPgChunk + 32 * threadIdx.x;
+    for (int i = 0; i < 32 && at0 + i < p.P; ++i) {
+      const bool is = (v >> i) & 1u;
+      const bool moves = is && at0 + i >= live;
+      if (moves) p.w.list[rank - under] = at0 + i;
+      p.w.rank[at0 + i] = moves ? rank - under : -1;
+      if (!is && at0 + i < live) p.w.list2[at0 + i - rank] = at0 + i;
+      rank += is;
+    }
+  }
+  if (c == 0 && threadIdx.x == 0) {
+    p.w.count[0] = live - under;
+    p.w.count[1] = live;
+    if (p.stats) {
+      p.stats[0] = live;
+      p.stats[1] = live - under;
+      p.stats[2] = p.stats[3] = 0;
+    }
+  }
+}
+
+// New number of a live page: its own below the live count, else that of the free page of its rank; -1: not live.
+__device__ __forceinline__ int compact_to(const PgCompact& p, int pg, int live) {
+  if (pg < live) return (__ldcg(p.w.bits + (pg >> 5)) >> (pg & 31) & 1u) ? pg : -1;
+  const int k = __ldcg(p.w.rank + pg);
+  return k >= 0 ? __ldcg(p.w.list2 + k) : -1;
+}
+
+__global__ void __launch_bounds__(kPgThreads) compact_move_kernel(const PgCompact p) {
+  pdl_wait();
+  pdl_trigger();
+  const int moves = __ldcg(p.w.count), live = __ldcg(p.w.count + 1);
+  copy_pages(p.copy);
+  const size_t step = (size_t)gridDim.x * kPgThreads, at = (size_t)blockIdx.x * kPgThreads + threadIdx.x;
+  for (size_t i = at; i < (size_t)p.B * p.M; i += step) {
+    const int pg = __ldcg(p.table + i);
+    const bool in = pg >= 0 && pg < p.P;
+    const int to = in ? compact_to(p, pg, live) : -1;
+    if (pg != -1 && to < 0) set_error(p.err, kErrDeviceIndex);  // no page, or one that is counted free
+    p.table_out[i] = to;
+  }
+  for (size_t i = at; i < (size_t)p.P; i += step) {
+    const bool is = __ldcg(p.w.bits + (i >> 5)) >> (i & 31) & 1u;
+    if (p.map) p.map[i] = compact_to(p, (int)i, live);
+    // free pages below the live count get their count from the page that moves there
+    if (p.ref_out != p.ref && is && (int)i < live) p.ref_out[i] = __ldcg(p.ref + i);
+    if ((int)i >= live && !is) p.ref_out[i] = 0;
+  }
+  for (size_t k = at; k < (size_t)moves; k += step) {
+    const int from = __ldcg(p.w.list + k), to = __ldcg(p.w.list2 + k);
+    const int r = __ldcg(p.ref + from);
+    p.ref_out[to] = r;
+    p.ref_out[from] = 0;
+  }
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+lsv_status pg_check(int32_t B, int32_t M, int32_t P) {
+  if (B < 0 || M < 1 || P < 1) return LSV_ERR_INVALID_ARG;
+  if (B > kPgMaxRows || P > kPgMaxPages || (long long)B * M >= (1ll << 31)) return LSV_ERR_UNSUPPORTED;
+  return LSV_OK;
+}
+
+lsv_status pg_ws(void* ws, size_t bytes, int32_t B, int32_t M, int32_t P, PgWs* w) {
+  *w = pg_layout(ws, B, M, P);
+  if (!ws || bytes < w->total) return LSV_ERR_WORKSPACE;
+  return al16(ws) ? LSV_OK : LSV_ERR_MISALIGNED;
+}
+
+lsv_status pool_check(int32_t layers, int64_t page_bytes, int32_t P) {
+  if (layers < 1 || page_bytes < 1) return LSV_ERR_INVALID_ARG;
+  if (page_bytes % 16 || page_bytes > (1ll << 31) || (double)layers * P * page_bytes > 9e18) return LSV_ERR_UNSUPPORTED;
+  return LSV_OK;
+}
+
+}  // namespace
+}  // namespace lsv
+
+using namespace lsv;
+
+extern "C" {
+
+size_t spec_pages_workspace_size(int32_t B, int32_t M, int32_t P) {
+  if (pg_check(B, M, P) != LSV_OK) return 0;
+  return pg_layout(nullptr, B, M, P).total;
+}
+
+lsv_status spec_pages_resize(void* pool, int32_t layers, int64_t page_bytes, const int32_t* table, const int32_t* ref,
+                             const int32_t* keep, const int32_t* cap, int32_t B, int32_t M, int32_t P, int32_t page,
+                             int32_t* table_out, int32_t* ref_out, int32_t* stats_opt, void* ws, size_t ws_bytes,
+                             lsv_stream stream) {
+  lsv_status st = pg_check(B, M, P);
+  if (st == LSV_OK) st = pool_check(layers, page_bytes, P);
+  if (st != LSV_OK) return st;
+  if (page < 1) return LSV_ERR_INVALID_ARG;
+  if ((long long)M * page > (1ll << 30)) return LSV_ERR_UNSUPPORTED;
+  if (!pool || !ref || !ref_out || (B > 0 && (!table || !keep || !cap || !table_out))) return LSV_ERR_INVALID_ARG;
+  if (!al16(pool) || !al16(table) || !al16(ref) || !al16(keep) || !al16(cap) || !al16(table_out) || !al16(ref_out) ||
+      !al16(stats_opt))
+    return LSV_ERR_MISALIGNED;
+  PgResize p;
+  st = pg_ws(ws, ws_bytes, B, M, P, &p.w);
+  if (st != LSV_OK) return st;
+  DeviceCtx* dc = nullptr;
+  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
+  p.table = table;
+  p.ref = ref;
+  p.keep = keep;
+  p.cap = cap;
+  p.table_out = table_out;
+  p.ref_out = ref_out;
+  p.stats = stats_opt;
+  p.B = B;
+  p.M = M;
+  p.P = P;
+  p.page = page;
+  p.chunks = (P + kPgChunk - 1) / kPgChunk;
+  p.err = dc->err;
+  PgCopy c;
+  c.pool = static_cast<uint8_t*>(pool);
+  c.src = p.w.src;
+  c.dst = p.w.list2;
+  c.count = p.w.count;
+  c.layers = layers;
+  c.P = P;
+  c.page_bytes = (size_t)page_bytes;
+  c.copied = stats_opt ? stats_opt + 2 : nullptr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(resize_count_kernel, dim3(B > p.chunks ? B : p.chunks), dim3(kPgThreads), 0, s, p);
+  if (e == cudaSuccess && B > 0) e = launch_pdl(resize_assign_kernel, dim3(B), dim3(kPgThreads), 0, s, p);
+  if (e == cudaSuccess && B > 0) e = launch_pdl(copy_pages_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, c);
+  return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+}
+
+lsv_status spec_pages_fork(const int32_t* table, const int32_t* ref, const int32_t* parent, int32_t B, int32_t M,
+                           int32_t P, int32_t* table_out, int32_t* ref_out, void* ws, size_t ws_bytes,
+                           lsv_stream stream) {
+  lsv_status st = pg_check(B, M, P);
+  if (st != LSV_OK) return st;
+  if (!ref || !ref_out || (B > 0 && (!table || !parent || !table_out))) return LSV_ERR_INVALID_ARG;
+  if (!al16(table) || !al16(ref) || !al16(parent) || !al16(table_out) || !al16(ref_out)) return LSV_ERR_MISALIGNED;
+  PgWs w;
+  st = pg_ws(ws, ws_bytes, B, M, P, &w);
+  if (st != LSV_OK) return st;
+  DeviceCtx* dc = nullptr;
+  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
+  PgFork p;
+  p.table = table;
+  p.ref = ref;
+  p.parent = parent;
+  p.table_out = table_out;
+  p.ref_out = ref_out;
+  p.B = B;
+  p.M = M;
+  p.P = P;
+  p.old = w.table;
+  p.err = dc->err;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(fork_save_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, p);
+  if (e == cudaSuccess && B > 0) e = launch_pdl(fork_rows_kernel, dim3(B), dim3(kPgThreads), 0, s, p);
+  return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+}
+
+lsv_status spec_pages_compact(void* pool, int32_t layers, int64_t page_bytes, const int32_t* table, const int32_t* ref,
+                              int32_t B, int32_t M, int32_t P, int32_t* table_out, int32_t* ref_out, int32_t* map_opt,
+                              int32_t* stats_opt, void* ws, size_t ws_bytes, lsv_stream stream) {
+  lsv_status st = pg_check(B, M, P);
+  if (st == LSV_OK) st = pool_check(layers, page_bytes, P);
+  if (st != LSV_OK) return st;
+  if (!pool || !ref || !ref_out || (B > 0 && (!table || !table_out))) return LSV_ERR_INVALID_ARG;
+  if (!al16(pool) || !al16(table) || !al16(ref) || !al16(table_out) || !al16(ref_out) || !al16(map_opt) ||
+      !al16(stats_opt))
+    return LSV_ERR_MISALIGNED;
+  PgCompact p;
+  st = pg_ws(ws, ws_bytes, B, M, P, &p.w);
+  if (st != LSV_OK) return st;
+  DeviceCtx* dc = nullptr;
+  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
+  p.table = table;
+  p.ref = ref;
+  p.table_out = table_out;
+  p.ref_out = ref_out;
+  p.map = map_opt;
+  p.stats = stats_opt;
+  p.B = B;
+  p.M = M;
+  p.P = P;
+  p.chunks = (P + kPgChunk - 1) / kPgChunk;
+  p.err = dc->err;
+  p.copy.pool = static_cast<uint8_t*>(pool);
+  p.copy.src = p.w.list;
+  p.copy.dst = p.w.list2;
+  p.copy.count = p.w.count;
+  p.copy.layers = layers;
+  p.copy.P = P;
+  p.copy.page_bytes = (size_t)page_bytes;
+  p.copy.copied = nullptr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(compact_count_kernel, dim3(p.chunks), dim3(kPgThreads), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(compact_list_kernel, dim3(p.chunks), dim3(kPgThreads), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(compact_move_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, p);
+  return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -17,6 +17,7 @@ enum : int {
   kErrNone = 0,
   kErrDeviceIndex = 7,   // an index read on the device lay outside its range
   kErrTimeout = 6,       // a bounded wait ran out
+  kErrPages = 8,         // a pool had fewer free pages than a call needed
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -191,6 +192,30 @@ __device__ __forceinline__ void mma_bf16_m16n8k16_top(float (&c)[2], uint32_t a0
       : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(0.f), "f"(0.f));
   c[0] = d[0];
   c[1] = d[1];
+}
+
+// D[16x8] += A[16x16] * B[16x8], f16 inputs (subnormals kept), fp32 accumulation.
+__device__ __forceinline__ void mma_f16_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 b16 matrix over the warp: lane (g, t) gives row g, columns 2t and 2t+1, and
+// receives row g, columns 2t and 2t+1 of the transpose.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// 2^x by the exponential unit, results below the smallest normal flushed to zero.
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // ----------------------------------------------------------------------------- tcgen05

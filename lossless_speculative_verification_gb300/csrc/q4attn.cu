@@ -1,0 +1,495 @@
+// q4attn.cu -- causal attention of the verified positions over the 4-bit paged
+// cache (layout: q4.cuh), with query heads that share key heads.
+//
+// The R = Q * (nh / nkv) query rows of a key head stand in the columns of
+// m16n8k16 MMAs and the cached positions in their rows: S^T = K q^T and
+// O^T = V^T P^T, so that one fragment of dequantised keys or values serves eight
+// query rows, and twice that many with a second column tile (NT = 2).
+//
+// Dequantising costs five operations a word of eight codes: a nibble alone in
+// the low bits of an f16 is the subnormal n' 2^-24 (n' = n + 8), and 16 times
+// that one place higher, so masks alone (and one shift by 8) make MMA operands.
+//   keys: the queries are scaled to 2^14 by a power of two of their row, the odd
+//   places' share by 1/16; the accumulators start at -8 * 2^-24 * sum(q) of the
+//   group, which takes the 8 off; the group's scale multiplies the fp32 sum.
+//   values: P times the position's scale is the f16 operand.  sum(P s) of every
+//   group, from one more MMA with ones, takes the 8 off at the end, and the rows
+//   of the odd places are divided by 16 there.
+// To keep P s in the range of f16 whatever the scales are, the running maximum
+// is taken over score + exponent of the position's largest value scale, and P is
+// 2^12 at it: P s < 2^13, and what underflows is below 2^-26 of the largest term.
+//
+// A CTA's four warps take the 16-position blocks of one chunk of one key head in
+// turn; their states (maximum, sum, output) meet in shared memory, those of the
+// chunks in attn_q4_combine_kernel.  Chunks begin at fixed positions, so a row's
+// result does not depend on the other rows of the call.
+#include <math.h>
+
+#include "internal.h"
+#include "lsv.h"
+#include "ptx.cuh"
+#include "q4.cuh"
+
+namespace lsv {
+namespace {
+
+constexpr int kQaWarps = 4;
+constexpr int kQaThreads = kQaWarps * 32;
+constexpr float kQaLift = 12.0f;  // log2 of P at the running maximum
+constexpr float kQaLog2e = 1.4426950408889634f;
+constexpr int kQaMaxChunks = 1024;
+
+struct QaParams {
+  const bf16* q;           // [B, Q, nh, D]
+  const uint8_t* pool;
+  const int32_t* table;    // [B, M]
+  const int32_t* ctx_len;  // [B]
+  int B, Q, nh, nkv, grp, R, M, P, page_shift, rblocks;
+  int chunk, nchunk;  // positions of a chunk (a multiple of 16 kQaWarps), chunks of a sequence
+  float scale_log2;   // scale * log2(e)
+  bf16* out;          // [B, Q, nh, D]
+  float* o_part;      // [B * nkv, nchunk, R, D]
+  float* ml_part;     // [B * nkv, nchunk, R, 2]: maximum (log2 units), sum
+  int* err;
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Exponent of the larger of a position's value scales (a NaN one left out), at least -64.
+__device__ __forceinline__ float lift_of(uint32_t s) {
+  const uint32_t a = s & 0xFFFFu, b = s >> 16;
+  uint32_t u = max(a, b);
+  if (u >= 0x7F80u) {
+    u = min(a, b);
+    if (u >= 0x7F80u) u = 0u;
+  }
+  return (float)max((int)(u >> 7) - 127, -64);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
+  using L = Q4Block<D>;
+  constexpr int W = L::W, G = L::G;
+  constexpr int kRows = 8 * NT;
+  constexpr int kStride = D + 4;  // floats between rows of the states in shared memory
+  __shared__ float o_s[kQaWarps][kRows][kStride];
+  __shared__ float ml_s[kQaWarps][kRows][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+
+  const int split = blockIdx.y;
+  const int rb = blockIdx.x % p.rblocks, bh = blockIdx.x / p.rblocks;
+  const int b = bh / p.nkv, h = bh - b * p.nkv;
+  const int n = __ldcg(p.ctx_len + b);
+  const bool bad = n < 0 || n > (p.M << p.page_shift);
+  if (bad && threadIdx.x == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
+  const int t_begin = split * p.chunk;
+  const int r0 = rb * kRows, nrows = min(kRows, p.R - r0);
+  const int end = bad ? 0 : min(n, t_begin + p.chunk);
+  if (p.nchunk > 1 && t_begin >= end) return;  // the combine reads no state of it
+
+  // ---- the queries as B operands: column g of tile nt is row r0 + 8 nt + g
+  uint32_t qf[NT][W][4];
+  float ci[NT][G][2];  // -8 * 2^-24 * sum of the group's queries, for this lane's columns 2t, 2t + 1
+  float fq[NT][2];     // what turns the scaled sums into log2 scores
+  int lim[NT][2];      // last position the row sees
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + g;
+    const int row = r0 + r;
+    uint4 x[W];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      x[j] = r < nrows ? __ldg(reinterpret_cast<const uint4*>(
+                             p.q + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 32 * j + 8 * t))
+                       : make_uint4(0u, 0u, 0u, 0u);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
+                               __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu)));
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // the largest of the row to 2^14 .. 2^15 (a row below 2^-112 keeps what 2^126 gives it)
+    const int e = (int)(m >> 7) - 127;
+    const int k = m == 0 ? 0 : min(14 - e, 126);
+    const float f = __uint_as_float((uint32_t)(k + 127) << 23);
+    float sum[G];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) sum[gr] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float fo = (q & 1) ? f * 0.0625f : f;
+        const uint32_t v = pack_f16(__uint_as_float(xs[q] << 16) * fo, __uint_as_float(xs[q] & 0xFFFF0000u) * fo);
+        qf[nt][j][q] = v;
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        sum[j >> 1] += (back.x + back.y) * ((q & 1) ? 16.0f : 1.0f);
+      }
+    }
+    float fr = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(p.scale_log2, 24 - k);
+    int lm = r < nrows ? n - p.Q + row / p.grp : -1;
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+      sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+      sum[gr] *= -8.0f / 16777216.0f;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int src = (2 * t + c) * 4;  // a lane of column 2t + c
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) ci[nt][gr][c] = __shfl_sync(0xffffffffu, sum[gr], src);
+      fq[nt][c] = __shfl_sync(0xffffffffu, fr, src);
+      lim[nt][c] = __shfl_sync(0xffffffffu, lm, src);
+    }
+  }
+
+  float o[NT][2 * W][4];  // tiles of 16 dims: rows g (even places) and g + 8 (odd places), columns 2t, 2t + 1
+  float cs[NT][G][4];     // sum of P s of every group (all rows alike)
+  float m_run[NT][2], l_run[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.0f;
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) cs[nt][gr][c] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) m_run[nt][c] = -INFINITY, l_run[nt][c] = 0.0f;
+  }
+
+  const int per = 1 << (p.page_shift - 4);  // blocks of a page and head
+  for (int pos0 = t_begin + 16 * warp; pos0 < end; pos0 += 16 * kQaWarps) {
+    const int pg = __ldcg(p.table + (size_t)b * p.M + (pos0 >> p.page_shift));
+    if (pg < 0 || pg >= p.P) {  // the same for the whole warp
+      if (lane == 0) set_error(p.err, kErrDeviceIndex);
+      continue;
+    }
+    const uint8_t* blk = p.pool + (((size_t)pg * p.nkv + h) * per + ((pos0 >> 4) & (per - 1))) * L::kBytes;
+    const Q4Words<W> k0 = q4_load<W>(blk + lane * (4 * W)), k1 = q4_load<W>(blk + (32 + lane) * (4 * W));
+    const Q4Words<W> v0 = q4_load<W>(blk + L::kV + lane * (4 * W)), v1 = q4_load<W>(blk + L::kV + (32 + lane) * (4 * W));
+    const uint32_t ks0 = q4_load_scales<G>(blk + L::kKs + g * 2 * G), ks1 = q4_load_scales<G>(blk + L::kKs + (g + 8) * 2 * G);
+    const uint32_t vs0 = q4_load_scales<G>(blk + L::kVs + g * 2 * G), vs1 = q4_load_scales<G>(blk + L::kVs + (g + 8) * 2 * G);
+
+    // ---- scores (log2 units)
+    float x[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[nt][c] = 0.0f;
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      float acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[nt][c] = ci[nt][gr][c & 1];
+#pragma unroll
+      for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
+        const uint32_t a = k0.w[j], c = k1.w[j], a8 = a >> 8, c8 = c >> 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16_m16n8k16(acc[nt], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[nt][j][0],
+                           qf[nt][j][1]);
+          mma_f16_m16n8k16(acc[nt], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
+                           qf[nt][j][2], qf[nt][j][3]);
+        }
+      }
+      const float s0 = q4_scale(ks0, gr), s1 = q4_scale(ks1, gr);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(acc[nt][c], c < 2 ? s0 : s1, x[nt][c]);
+    }
+    // ---- the online softmax
+    const bool masked = pos0 + 15 > n - p.Q;  // some row does not see all of the block
+    const float lift0 = lift_of(vs0), lift1 = lift_of(vs1);
+    float pr[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float y[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        x[nt][c] = __fmul_rn(x[nt][c], fq[nt][c & 1]);  // not fused with what follows: the same in every form
+        if (masked && pos0 + g + (c < 2 ? 0 : 8) > lim[nt][c & 1]) x[nt][c] = -INFINITY;
+        y[c] = x[nt][c] + (c < 2 ? lift0 : lift1);
+      }
+      float corr[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float m = fmaxf(y[c], y[c + 2]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        m = fmaxf(m, m_run[nt][c]);
+        corr[c] = m == -INFINITY ? 1.0f : ex2_ftz(m_run[nt][c] - m);
+        m_run[nt][c] = m;
+        const float base = m == -INFINITY ? 0.0f : m - kQaLift;
+        pr[nt][c] = ex2_ftz(x[nt][c] - base);
+        pr[nt][c + 2] = ex2_ftz(x[nt][c + 2] - base);
+        l_run[nt][c] = fmaf(l_run[nt][c], corr[c], pr[nt][c] + pr[nt][c + 2]);
+      }
+      if (!__all_sync(0xffffffffu, corr[0] == 1.0f && corr[1] == 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < 2 * W; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[nt][i][c] *= corr[c & 1];
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          cs[nt][gr][0] *= corr[0];
+          cs[nt][gr][1] *= corr[1];
+        }
+      }
+    }
+    // ---- the weighted values
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      const float s0 = q4_scale(vs0, gr), s1 = q4_scale(vs1, gr);
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          w[c] = pr[nt][c] * (c < 2 ? s0 : s1);
+          if (masked && x[nt][c] == -INFINITY) w[c] = 0.0f;
+        }
+        pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
+        pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
+        mma_f16_m16n8k16(cs[nt][gr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nt][0], pb[nt][1]);
+      }
+#pragma unroll
+      for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
+        const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16_m16n8k16(o[nt][2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u, pb[nt][0],
+                           pb[nt][1]);
+          mma_f16_m16n8k16(o[nt][2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u,
+                           pb[nt][0], pb[nt][1]);
+        }
+      }
+    }
+  }
+
+  // ---- the warp's state: column 2t + c of tile nt is row 8 nt + 2t + c
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * nt + 2 * t + c;
+      float l = l_run[nt][c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (g == 0) {
+        ml_s[warp][r][0] = m_run[nt][c];
+        ml_s[warp][r][1] = l;
+      }
+#pragma unroll
+      for (int m = 0; m < W; ++m) {
+        const float off = -8.0f * cs[nt][m >> 1][c];
+        *reinterpret_cast<float4*>(&o_s[warp][r][32 * m + 4 * g]) =
+            make_float4(fmaf(o[nt][2 * m][c], 16777216.0f, off), fmaf(o[nt][2 * m][c + 2], 1048576.0f, off),
+                        fmaf(o[nt][2 * m + 1][c], 16777216.0f, off), fmaf(o[nt][2 * m + 1][c + 2], 1048576.0f, off));
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nrows * (D / 4); i += kQaThreads) {
+    const int r = i / (D / 4), c4 = i - r * (D / 4), row = r0 + r;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kQaWarps; ++w) mm = fmaxf(mm, ml_s[w][r][0]);
+    float ls = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kQaWarps; ++w) {
+      const float mw = ml_s[w][r][0];
+      // a warp that saw nothing adds nothing; one that saw only NaN scores adds them
+      const float f = mw == -INFINITY ? (ml_s[w][r][1] == 0.0f ? 0.0f : 1.0f) : ex2_ftz(mw - mm);
+      const float4 v = *reinterpret_cast<const float4*>(&o_s[w][r][4 * c4]);
+      ls = fmaf(ml_s[w][r][1], f, ls);
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+    if (p.nchunk == 1) {
+      const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;  // a row that sees nothing is zero
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                           hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      uint2 v;
+      v.x = *reinterpret_cast<const uint32_t*>(&lo);
+      v.y = *reinterpret_cast<const uint32_t*>(&hi);
+      *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 4 * c4) = v;
+    } else {
+      const size_t at = ((size_t)bh * p.nchunk + split) * p.R + row;
+      *reinterpret_cast<float4*>(p.o_part + at * D + 4 * c4) = acc;
+      if (c4 == 0) *reinterpret_cast<float2*>(p.ml_part + at * 2) = make_float2(mm, ls);
+    }
+  }
+}
+
+// Per (key head, sequence): the chunks' states brought to their common maximum and summed.
+constexpr int kQcThreads = 128;
+constexpr int kQcUnroll = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int bh = blockIdx.x, b = bh / p.nkv, h = bh - b * p.nkv;
+  const int n = __ldcg(p.ctx_len + b);
+  const bool bad = n < 0 || n > (p.M << p.page_shift);
+  const int parts = bad ? 0 : (n + p.chunk - 1) / p.chunk;
+  const float2* ml = reinterpret_cast<const float2*>(p.ml_part) + (size_t)bh * p.nchunk * p.R;
+  const float4* o4 = reinterpret_cast<const float4*>(p.o_part) + (size_t)bh * p.nchunk * p.R * (D / 4);
+  for (int i = blockIdx.y * kQcThreads + threadIdx.x; i < p.R * (D / 4); i += gridDim.y * kQcThreads) {
+    const int row = i / (D / 4), c4 = i - row * (D / 4);
+    float mm = -INFINITY, ls = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = 0; s0 < parts; s0 += kQcUnroll) {
+      float2 a[kQcUnroll];
+      float4 v[kQcUnroll];
+#pragma unroll
+      for (int u = 0; u < kQcUnroll; ++u) {
+        const bool in = s0 + u < parts;
+        a[u] = in ? __ldcg(ml + (size_t)(s0 + u) * p.R + row) : make_float2(-INFINITY, 0.0f);
+        v[u] = in ? __ldcg(o4 + ((size_t)(s0 + u) * p.R + row) * (D / 4) + c4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float gm = mm;
+#pragma unroll
+      for (int u = 0; u < kQcUnroll; ++u) gm = fmaxf(gm, a[u].x);
+      const float r = mm == -INFINITY ? (ls == 0.0f ? 0.0f : 1.0f) : ex2_ftz(mm - gm);
+      ls *= r;
+      acc.x *= r;
+      acc.y *= r;
+      acc.z *= r;
+      acc.w *= r;
+#pragma unroll
+      for (int u = 0; u < kQcUnroll; ++u) {
+        const float f = a[u].x == -INFINITY ? (a[u].y == 0.0f ? 0.0f : 1.0f) : ex2_ftz(a[u].x - gm);
+        ls = fmaf(a[u].y, f, ls);
+        acc.x = fmaf(v[u].x, f, acc.x);
+        acc.y = fmaf(v[u].y, f, acc.y);
+        acc.z = fmaf(v[u].z, f, acc.z);
+        acc.w = fmaf(v[u].w, f, acc.w);
+      }
+      mm = gm;
+    }
+    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                         hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 v;
+    v.x = *reinterpret_cast<const uint32_t*>(&lo);
+    v.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 4 * c4) = v;
+  }
+}
+
+// Positions of a chunk: as long as leaves about four chunks for each of the CTAs that the GPU holds at
+// once, a whole number of rounds of the four warps.  It goes by the capacity (the lengths are on the
+// device) and not by Q or the shared heads, so a row is summed in the same order alone and among others.
+int chunk_of(int B, int nkv, long long cap) {
+  constexpr int kRound = 16 * kQaWarps, kTarget = 152 * 4 * 4;
+  const long long pairs = (long long)B * nkv;
+  long long want = pairs > 0 ? (pairs * cap + kTarget - 1) / kTarget : 128;
+  const long long least = (cap + kQaMaxChunks - 1) / kQaMaxChunks;
+  if (want < least) want = least;
+  if (want < 128) want = 128;
+  if (want > 4096 && least <= 4096) want = 4096;
+  return (int)((want + kRound - 1) / kRound * kRound);
+}
+
+bool shape_ok(int B, int Q, int M, int page, int nh, int nkv, int d) {
+  return B >= 0 && B <= 65535 && Q >= 1 && Q <= kMaxAttnQ && M >= 1 && q4_page_ok(page) && (long long)M * page <= (1ll << 24) &&
+         nkv >= 1 && nkv <= 1024 && nh >= nkv && nh % nkv == 0 && nh / nkv <= 16 && q4_dim_ok(d) &&
+         (long long)B * nkv <= kAttnMaxPairs && (long long)B * M < (1ll << 31);
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int D, int NT>
+cudaError_t run(const QaParams& p, cudaStream_t s) {
+  cudaError_t e = launch_pdl(attn_q4_kernel<D, NT>, dim3(p.B * p.nkv * p.rblocks, p.nchunk), dim3(kQaThreads), 0, s, p);
+  if (e != cudaSuccess || p.nchunk == 1) return e;
+  const int slices = (p.R * (D / 4) + kQcThreads - 1) / kQcThreads;
+  return launch_pdl(attn_q4_combine_kernel<D>, dim3(p.B * p.nkv, slices), dim3(kQcThreads), 0, s, p);
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace lsv
+
+using namespace lsv;
+
+extern "C" {
+
+size_t spec_q4_attention_workspace_size(int32_t B, int32_t Q, int32_t M, int32_t page, int32_t nh, int32_t nkv,
+                                        int32_t d) {
+  if (!shape_ok(B, Q, M, page, nh, nkv, d)) return 0;
+  const long long cap = (long long)M * page;
+  const int chunk = chunk_of(B, nkv, cap);
+  const size_t parts = (size_t)B * nkv * ((cap + chunk - 1) / chunk) * (Q * (nh / nkv));
+  return 256 + round256(parts * d * 4) + round256(parts * 2 * 4);
+}
+
+lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* table, const int32_t* ctx_len, int32_t B,
+                             int32_t Q, int32_t nh, int32_t nkv, int32_t d, int32_t page, int32_t M, int32_t P,
+                             float scale, void* out, void* ws, size_t ws_bytes, lsv_stream stream) {
+  if (B < 0 || Q < 1 || nh < 1 || nkv < 1 || d < 1 || page < 1 || M < 1 || P < 1 || !(scale > 0.f) || !isfinite(scale))
+    return LSV_ERR_INVALID_ARG;
+  const size_t need = spec_q4_attention_workspace_size(B, Q, M, page, nh, nkv, d);
+  if (need == 0) return LSV_ERR_UNSUPPORTED;
+  if (B == 0) return LSV_OK;
+  if (!q || !pool || !table || !ctx_len || !out) return LSV_ERR_INVALID_ARG;
+  if (!al16(q) || !al16(pool) || !al16(table) || !al16(ctx_len) || !al16(out)) return LSV_ERR_MISALIGNED;
+  if (!ws || ws_bytes < need) return LSV_ERR_WORKSPACE;
+  if (!al16(ws)) return LSV_ERR_MISALIGNED;
+  DeviceCtx* dc = nullptr;
+  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
+  QaParams p;
+  p.q = static_cast<const bf16*>(q);
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.table = table;
+  p.ctx_len = ctx_len;
+  p.B = B;
+  p.Q = Q;
+  p.nh = nh;
+  p.nkv = nkv;
+  p.grp = nh / nkv;
+  p.R = Q * p.grp;
+  p.M = M;
+  p.P = P;
+  p.page_shift = 4;
+  while ((1 << p.page_shift) < page) ++p.page_shift;
+  const long long cap = (long long)M * page;
+  p.chunk = chunk_of(B, nkv, cap);
+  p.nchunk = (int)((cap + p.chunk - 1) / p.chunk);
+  p.scale_log2 = scale * kQaLog2e;
+  p.out = static_cast<bf16*>(out);
+  const size_t parts = (size_t)B * nkv * p.nchunk * p.R;
+  p.o_part = static_cast<float*>(ws);
+  p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(parts * d * 4));
+  p.err = dc->err;
+  const bool two = p.R > 8;
+  p.rblocks = two ? (p.R + 15) / 16 : 1;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = d == 128 ? (two ? run<128, 2>(p, s) : run<128, 1>(p, s))
+                                 : (two ? run<64, 2>(p, s) : run<64, 1>(p, s));
+  return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+}
+
+}  // extern "C"

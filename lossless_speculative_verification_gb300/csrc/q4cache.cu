@@ -1,0 +1,356 @@
+// q4cache.cu -- writing positions to the 4-bit paged cache and reading them back
+// (layout: q4.cuh).
+//
+// One warp takes one block (16 positions of a head) in the lane layout of the
+// cache, keys and values: a lane quantises what it stores, the maximum of a
+// group of 64 dims meets over the 4 lanes of a position (keys) or the 8 lanes
+// of a pair of positions (values), and whole words leave as one vector a lane.
+// Positions at the edges of the new ones share their block with others: keys and
+// scales of a position have bytes of their own, values 16-bit halves, so no
+// block is read to be written and two calls on neighbouring positions do not
+// touch each other's bytes.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "lsv.h"
+#include "ptx.cuh"
+#include "q4.cuh"
+
+namespace lsv {
+namespace {
+
+constexpr int kQwWarps = 4;
+
+// Largest |x| of packed bf16 pairs as bits: ordered like the values, and above 0x7F80 for NaN.
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t v) { return __vmaxu2(m, v & 0x7FFF7FFFu); }
+__device__ __forceinline__ uint32_t fold2(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+
+// bf16 bits of s = bf16(amax / 7).  amax / 7 in fp32 rounded again to bf16 is the correctly rounded
+// quotient: with 8 significant bits over 7 it never comes near the middle of two bf16 values.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
+  if (amax >= 0x7F80u) return kQ4NanScale;
+  const float q = __fdiv_rn(__uint_as_float(amax << 16), 7.0f);
+  return __bfloat16_as_ushort(__float2bfloat16_rn(q));
+}
+
+// The nibble of x: rint(x / s) + 8, ties to even.  Both have 8 significant bits, so x / s in fp32 rounds
+// to a half only where it is one.
+__device__ __forceinline__ uint32_t code(float x, float s, bool plain) {
+  if (!plain) return 8u;
+  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, s)), -8.0f), 7.0f)) + 8);
+}
+__device__ __forceinline__ bool plain_scale(uint32_t s) { return s != 0u && s < 0x7F80u; }
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+struct QwParams {
+  const int32_t* table;    // [B, M]
+  const int32_t* ctx_len;  // [B]
+  int B, Q, nkv, M, P, page_shift;
+  int nblk;  // blocks that Q positions can touch
+  int* err;
+};
+
+// The warp's (sequence, block, head) and the block's place; false: nothing there (*bad: an index out of range).
+struct QwPlace {
+  int b, h, n, p0, block;
+  size_t at;  // in blocks
+};
+__device__ __forceinline__ bool place(const QwParams& p, int unit, QwPlace* w, bool* bad) {
+  w->h = unit % p.nkv;
+  const int r = unit / p.nkv;
+  w->b = r / p.nblk;
+  const int bi = r - w->b * p.nblk;
+  w->n = __ldcg(p.ctx_len + w->b);
+  *bad = false;
+  if (w->n < 0 || w->n > (p.M << p.page_shift)) {
+    *bad = true;
+    return false;
+  }
+  w->p0 = w->n - p.Q;
+  w->block = q4_floor_block(w->p0) + bi;
+  if (w->block < 0 || (w->block << 4) >= w->n) return false;
+  const int pg = __ldcg(p.table + (size_t)w->b * p.M + ((w->block << 4) >> p.page_shift));
+  if (pg < 0 || pg >= p.P) {
+    *bad = true;
+    return false;
+  }
+  const int per = 1 << (p.page_shift - 4);  // blocks of a page and head
+  w->at = ((size_t)pg * p.nkv + w->h) * per + (w->block & (per - 1));
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kQwWarps * 32) q4_append_kernel(const bf16* __restrict__ k_new,
+                                                                  const bf16* __restrict__ v_new, uint8_t* pool,
+                                                                  const QwParams p) {
+  using L = Q4Block<D>;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int unit = blockIdx.x * kQwWarps + (threadIdx.x >> 5);
+  if (unit >= p.B * p.nblk * p.nkv) return;
+  QwPlace w;
+  bool bad;
+  if (!place(p, unit, &w, &bad)) {
+    if (bad && lane == 0) set_error(p.err, kErrDeviceIndex);
+    return;
+  }
+  uint8_t* blk = pool + w.at * L::kBytes;
+  const int pos0 = w.block << 4;
+  // row of position pos: (b Q + pos - p0) of [B Q, nkv, D]
+  const size_t row0 = (size_t)w.b * p.Q;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    // keys: lane (g, t) has the dims 32 j + 8 t + 0..7 of position 8 half + g
+    const int tk = 8 * half + g, pos = pos0 + tk;
+    const bool in = pos >= w.p0 && pos >= 0 && pos < w.n;
+    uint4 x[L::W];
+#pragma unroll
+    for (int j = 0; j < L::W; ++j)
+      x[j] = in ? __ldg(reinterpret_cast<const uint4*>(k_new + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 32 * j + 8 * t))
+                : make_uint4(0u, 0u, 0u, 0u);
+    Q4Words<L::W> out;
+    uint32_t sc = 0;
+#pragma unroll
+    for (int gr = 0; gr < L::G; ++gr) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 2 * gr; j < 2 * gr + 2; ++j) m = abs_max2(abs_max2(abs_max2(abs_max2(m, x[j].x), x[j].y), x[j].z), x[j].w);
+      m = fold2(m);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t sb = scale_bits(m);
+      sc |= sb << (16 * gr);
+      const float s = __uint_as_float(sb << 16);
+      const bool plain = plain_scale(sb);
+#pragma unroll
+      for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
+        const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        uint32_t word = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          word |= code(lo_f(xs[q]), s, plain) << (4 * q) | code(hi_f(xs[q]), s, plain) << (4 * q + 16);
+        out.w[j] = word;
+      }
+    }
+    if (in) {
+      q4_store<L::W>(blk + tk * (D / 2) + t * (4 * L::W), out);
+      if (t == 0) q4_store_scales<L::G>(blk + L::kKs + tk * 2 * L::G, sc);
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    // values: lane (g, t) has the dims 32 m + 4 g + 0..3 of the positions 8 half + 2 t and the one after it
+    Q4Words<L::W> out;
+#pragma unroll
+    for (int m = 0; m < L::W; ++m) out.w[m] = 0;
+    bool in[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int tk = 8 * half + 2 * t + e, pos = pos0 + tk;
+      in[e] = pos >= w.p0 && pos >= 0 && pos < w.n;
+      uint2 x[L::W];
+#pragma unroll
+      for (int m = 0; m < L::W; ++m)
+        x[m] = in[e] ? __ldg(reinterpret_cast<const uint2*>(v_new + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 32 * m + 4 * g))
+                     : make_uint2(0u, 0u);
+      uint32_t sc = 0;
+#pragma unroll
+      for (int gr = 0; gr < L::G; ++gr) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int m = 2 * gr; m < 2 * gr + 2; ++m) a = abs_max2(abs_max2(a, x[m].x), x[m].y);
+        a = fold2(a);
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 4));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 16));
+        const uint32_t sb = scale_bits(a);
+        sc |= sb << (16 * gr);
+        const float s = __uint_as_float(sb << 16);
+        const bool plain = plain_scale(sb);
+#pragma unroll
+        for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
+          const uint32_t c = code(lo_f(x[m].x), s, plain) | code(hi_f(x[m].x), s, plain) << 4 |
+                             code(lo_f(x[m].y), s, plain) << 8 | code(hi_f(x[m].y), s, plain) << 12;
+          out.w[m] |= c << (16 * e);
+        }
+      }
+      if (in[e] && g == 0) q4_store_scales<L::G>(blk + L::kVs + tk * 2 * L::G, sc);
+    }
+    uint8_t* at = blk + L::kV + (half * 32 + lane) * (4 * L::W);
+    if (in[0] && in[1]) {
+      q4_store<L::W>(at, out);
+    } else if (in[0] || in[1]) {
+#pragma unroll
+      for (int m = 0; m < L::W; ++m)
+        *reinterpret_cast<uint16_t*>(at + 4 * m + (in[1] ? 2 : 0)) =
+            static_cast<uint16_t>(in[1] ? out.w[m] >> 16 : out.w[m] & 0xFFFFu);
+    }
+  }
+}
+
+// (n - 8) s of two nibbles as packed bf16: the product has at most 12 bits, so fp32 holds it and one
+// rounding to bf16 remains.
+__device__ __forceinline__ uint32_t value2(uint32_t lo, uint32_t hi, float s) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn((static_cast<int>(lo) - 8) * s, (static_cast<int>(hi) - 8) * s);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kQwWarps * 32) q4_read_kernel(const uint8_t* __restrict__ pool, bf16* k_out,
+                                                                bf16* v_out, const QwParams p) {
+  using L = Q4Block<D>;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int unit = blockIdx.x * kQwWarps + (threadIdx.x >> 5);
+  if (unit >= p.B * p.nblk * p.nkv) return;
+  QwPlace w;
+  bool bad;
+  const bool there = place(p, unit, &w, &bad);
+  if (bad && lane == 0) set_error(p.err, kErrDeviceIndex);
+  // a bad length: the rows are zeros, laid out as if the last position were the last of a block
+  if (w.n < 0 || w.n > (p.M << p.page_shift)) {
+    w.n = p.nblk << 4;
+    w.p0 = w.n - p.Q;
+    w.block = q4_floor_block(w.p0) + (unit / p.nkv) % p.nblk;
+  }
+  const uint8_t* blk = pool + (there ? w.at * L::kBytes : 0);
+  const int pos0 = w.block * 16;
+  const size_t row0 = (size_t)w.b * p.Q;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int tk = 8 * half + g, pos = pos0 + tk;
+    if (pos >= w.p0 && pos < w.n) {
+      uint4* dst = reinterpret_cast<uint4*>(k_out + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 8 * t);
+      if (!there) {
+#pragma unroll
+        for (int j = 0; j < L::W; ++j) dst[4 * j] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        const Q4Words<L::W> c = q4_load<L::W>(blk + tk * (D / 2) + t * (4 * L::W));
+        const uint32_t sc = q4_load_scales<L::G>(blk + L::kKs + tk * 2 * L::G);
+#pragma unroll
+        for (int j = 0; j < L::W; ++j) {
+          const float s = q4_scale(sc, j >> 1);
+          uint32_t v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = value2((c.w[j] >> (4 * q)) & 15u, (c.w[j] >> (4 * q + 16)) & 15u, s);
+          dst[4 * j] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    Q4Words<L::W> c;
+    if (there) c = q4_load<L::W>(blk + L::kV + (half * 32 + lane) * (4 * L::W));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int tk = 8 * half + 2 * t + e, pos = pos0 + tk;
+      if (pos < w.p0 || pos >= w.n) continue;
+      uint2* dst = reinterpret_cast<uint2*>(v_out + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 4 * g);
+      const uint32_t sc = there ? q4_load_scales<L::G>(blk + L::kVs + tk * 2 * L::G) : 0u;
+#pragma unroll
+      for (int m = 0; m < L::W; ++m) {
+        if (!there) {
+          dst[8 * m] = make_uint2(0u, 0u);
+          continue;
+        }
+        const uint32_t x = c.w[m] >> (16 * e);
+        const float s = q4_scale(sc, m >> 1);
+        dst[8 * m] = make_uint2(value2(x & 15u, (x >> 4) & 15u, s), value2((x >> 8) & 15u, (x >> 12) & 15u, s));
+      }
+    }
+  }
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int log2i(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+// Shared by both calls: sizes, pointers, grid.
+lsv_status prepare(const void* a, const void* b, const void* pool, const int32_t* table, const int32_t* ctx_len,
+                   int32_t B, int32_t Q, int32_t nkv, int32_t d, int32_t page, int32_t M, int32_t P, QwParams* p,
+                   int* grid, bool* empty) {
+  *empty = false;
+  if (B < 0 || Q < 0 || nkv < 1 || d < 1 || page < 1 || M < 1 || P < 1) return LSV_ERR_INVALID_ARG;
+  if (!q4_dim_ok(d) || !q4_page_ok(page) || nkv > 1024 || (long long)M * page > (1ll << 30) || Q > (1 << 30) ||
+      (long long)B * M >= (1ll << 31))
+    return LSV_ERR_UNSUPPORTED;
+  const long long nblk = (Q + 14) / 16 + 1;  // the most blocks that Q consecutive positions touch
+  const long long units = (long long)B * nblk * nkv;
+  if (units >= (1ll << 31)) return LSV_ERR_UNSUPPORTED;
+  if (B == 0 || Q == 0) {
+    *empty = true;
+    return LSV_OK;
+  }
+  if (!a || !b || !pool || !table || !ctx_len) return LSV_ERR_INVALID_ARG;
+  if (!al16(a) || !al16(b) || !al16(pool) || !al16(table) || !al16(ctx_len)) return LSV_ERR_MISALIGNED;
+  DeviceCtx* dc = nullptr;
+  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
+  p->table = table;
+  p->ctx_len = ctx_len;
+  p->B = B;
+  p->Q = Q;
+  p->nkv = nkv;
+  p->M = M;
+  p->P = P;
+  p->page_shift = log2i(page);
+  p->nblk = (int)nblk;
+  p->err = dc->err;
+  *grid = (int)((units + kQwWarps - 1) / kQwWarps);
+  return LSV_OK;
+}
+
+}  // namespace
+}  // namespace lsv
+
+using namespace lsv;
+
+extern "C" {
+
+size_t spec_q4_page_bytes(int32_t nkv, int32_t d, int32_t page) {
+  if (nkv < 1 || nkv > 1024 || !q4_dim_ok(d) || !q4_page_ok(page)) return 0;
+  return (size_t)nkv * (page / kQ4Block) * q4_block_bytes(d);
+}
+
+lsv_status spec_q4_append(const void* k_new, const void* v_new, void* pool, const int32_t* table,
+                          const int32_t* ctx_len, int32_t B, int32_t Q, int32_t nkv, int32_t d, int32_t page,
+                          int32_t M, int32_t P, lsv_stream stream) {
+  QwParams p;
+  int grid = 0;
+  bool empty;
+  const lsv_status st = prepare(k_new, v_new, pool, table, ctx_len, B, Q, nkv, d, page, M, P, &p, &grid, &empty);
+  if (st != LSV_OK || empty) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      d == 128 ? launch_pdl(q4_append_kernel<128>, dim3(grid), dim3(kQwWarps * 32), 0, s, static_cast<const bf16*>(k_new),
+                            static_cast<const bf16*>(v_new), static_cast<uint8_t*>(pool), p)
+               : launch_pdl(q4_append_kernel<64>, dim3(grid), dim3(kQwWarps * 32), 0, s, static_cast<const bf16*>(k_new),
+                            static_cast<const bf16*>(v_new), static_cast<uint8_t*>(pool), p);
+  return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+}
+
+lsv_status spec_q4_read(const void* pool, const int32_t* table, const int32_t* ctx_len, int32_t B, int32_t N,
+                        int32_t nkv, int32_t d, int32_t page, int32_t M, int32_t P, void* k_out, void* v_out,
+                        lsv_stream stream) {
+  QwParams p;
+  int grid = 0;
+  bool empty;
+  const lsv_status st = prepare(k_out, v_out, pool, table, ctx_len, B, N, nkv, d, page, M, P, &p, &grid, &empty);
+  if (st != LSV_OK || empty) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      d == 128 ? launch_pdl(q4_read_kernel<128>, dim3(grid), dim3(kQwWarps * 32), 0, s, static_cast<const uint8_t*>(pool),
+                            static_cast<bf16*>(k_out), static_cast<bf16*>(v_out), p)
+               : launch_pdl(q4_read_kernel<64>, dim3(grid), dim3(kQwWarps * 32), 0, s, static_cast<const uint8_t*>(pool),
+                            static_cast<bf16*>(k_out), static_cast<bf16*>(v_out), p);
+  return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+}
+
+}  // extern "C"
