@@ -51,6 +51,7 @@ struct QaParams {
   float* o_part;      // [B * nkv, nchunk, R, D]
   float* ml_part;     // [B * nkv, nchunk, R, 2]: maximum (log2 units), sum
   int* err;
+  uint64_t wait_ns;
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -70,30 +71,106 @@ __device__ __forceinline__ float lift_of(uint32_t s) {
   return (float)max((int)(u >> 7) - 127, -64);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
+// A warp's ring of S stages of U blocks each in shared memory, filled by untiled bulk copies.
+template <int D, int NT, int U, int S>
+struct QaSmem {
   using L = Q4Block<D>;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStride = D + 4;  // floats between rows of a state, in the ring once it is drained
+  static constexpr int kRing = S * U * L::kBytes;
+  static constexpr int kMl = kRows * kStride * 4;  // byte offset of (maximum, sum) behind the rows
+  static constexpr int kWarp = kRing > kMl + kRows * 8 ? kRing : (kMl + kRows * 8 + 15) / 16 * 16;
+  static constexpr int kTotal = kQaWarps * (kWarp + S * 8 + S * 4);
+};
+
+template <int D, int NT, int U, int S, int kPerSm>
+__global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaParams p) {
+  using L = Q4Block<D>;
+  using SM = QaSmem<D, NT, U, S>;
   constexpr int W = L::W, G = L::G;
-  constexpr int kRows = 8 * NT;
-  constexpr int kStride = D + 4;  // floats between rows of the states in shared memory
-  __shared__ float o_s[kQaWarps][kRows][kStride];
-  __shared__ float ml_s[kQaWarps][kRows][2];
+  constexpr int kRows = SM::kRows;
+  constexpr int kStep = 16 * U;            // positions a warp takes at a time
+  constexpr int kBatch = 32 / U;           // steps whose pages the lanes hold
+  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * SM::kWarp;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kQaWarps * SM::kWarp) + warp * S;
+  int* here = reinterpret_cast<int*>(smem + kQaWarps * (SM::kWarp + S * 8)) + warp * S;  // which blocks a stage holds
+  if (lane < S) mbar_init(&full[lane], 1);
+  fence_barrier_init();
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
 
   const int split = blockIdx.y;
   const int rb = blockIdx.x % p.rblocks, bh = blockIdx.x / p.rblocks;
   const int b = bh / p.nkv, h = bh - b * p.nkv;
+  const int r0 = rb * kRows, nrows = min(kRows, p.R - r0);
   const int n = __ldcg(p.ctx_len + b);
+
+  // ---- the queries: column g of tile nt is row r0 + 8 nt + g, this lane has the dims 32 j + 8 t + 0..7
+  uint4 xq[NT][W];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + g, row = r0 + r;
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      xq[nt][j] = r < nrows ? __ldg(reinterpret_cast<const uint4*>(
+                                  p.q + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 32 * j + 8 * t))
+                            : make_uint4(0u, 0u, 0u, 0u);
+  }
+
   const bool bad = n < 0 || n > (p.M << p.page_shift);
   if (bad && threadIdx.x == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
   const int t_begin = split * p.chunk;
-  const int r0 = rb * kRows, nrows = min(kRows, p.R - r0);
   const int end = bad ? 0 : min(n, t_begin + p.chunk);
   if (p.nchunk > 1 && t_begin >= end) return;  // the combine reads no state of it
 
-  // ---- the queries as B operands: column g of tile nt is row r0 + 8 nt + g
+  // ---- the ring: step i of this warp is the U blocks from position first + i * kQaWarps * kStep on
+  const int first = t_begin + warp * kStep;
+  const int nsteps = first < end ? (end - first + kQaWarps * kStep - 1) / (kQaWarps * kStep) : 0;
+  const int per_shift = p.page_shift - 4;
+  // lane l has the page of block l % U of step i0 + l / U; -1: none there
+  auto pages_of = [&](int i0) {
+    const int i = i0 + lane / U, pos = first + i * (kQaWarps * kStep) + 16 * (lane % U);
+    if (i >= nsteps || pos >= end) return -1;
+    const int pg = __ldcg(p.table + (size_t)b * p.M + (pos >> p.page_shift));
+    if (pg >= 0 && pg < p.P) return pg;
+    set_error(p.err, kErrDeviceIndex);
+    return -1;
+  };
+  int pg_now = pages_of(0), pg_next = -1;
+  auto issue = [&](int i) {  // all lanes
+    const int k = i % kBatch;
+    if (k == 0) {
+      if (i > 0) pg_now = pg_next;
+      pg_next = pages_of(i + kBatch);
+    }
+    int pg[U], there = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      pg[u] = __shfl_sync(0xffffffffu, pg_now, k * U + u);
+      there |= (pg[u] >= 0) << u;
+    }
+    if (lane == 0) {
+      const int s = i % S;
+      here[s] = there;
+      mbar_arrive_expect_tx(&full[s], __popc(there) * L::kBytes);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (pg[u] >= 0) {
+          const int blk = (first >> 4) + i * (kQaWarps * U) + u;
+          bulk_load(ring + (s * U + u) * L::kBytes,
+                    p.pool + ((((size_t)pg[u] * p.nkv + h) << per_shift) + (blk & ((1 << per_shift) - 1))) * L::kBytes,
+                    L::kBytes, &full[s]);
+        }
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < S && i < nsteps; ++i) issue(i);
+  __syncwarp();
+
+  // ---- the queries as B operands
   uint32_t qf[NT][W][4];
   float ci[NT][G][2];  // -8 * 2^-24 * sum of the group's queries, for this lane's columns 2t, 2t + 1
   float fq[NT][2];     // what turns the scaled sums into log2 scores
@@ -101,16 +178,11 @@ __global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = 8 * nt + g;
-    const int row = r0 + r;
-    uint4 x[W];
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      x[j] = r < nrows ? __ldg(reinterpret_cast<const uint4*>(
-                             p.q + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 32 * j + 8 * t))
-                       : make_uint4(0u, 0u, 0u, 0u);
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
-                               __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu)));
+      const uint4 x = xq[nt][j];
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
     }
     m = max(m & 0xFFFFu, m >> 16);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -124,7 +196,7 @@ __global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
     for (int gr = 0; gr < G; ++gr) sum[gr] = 0.0f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      const uint32_t xs[4] = {xq[nt][j].x, xq[nt][j].y, xq[nt][j].z, xq[nt][j].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float fo = (q & 1) ? f * 0.0625f : f;
@@ -134,8 +206,8 @@ __global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
         sum[j >> 1] += (back.x + back.y) * ((q & 1) ? 16.0f : 1.0f);
       }
     }
-    float fr = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(p.scale_log2, 24 - k);
-    int lm = r < nrows ? n - p.Q + row / p.grp : -1;
+    const float fr = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(p.scale_log2, 24 - k);
+    const int lm = r < nrows ? n - p.Q + (r0 + r) / p.grp : -1;
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
@@ -153,8 +225,8 @@ __global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
   }
 
   float o[NT][2 * W][4];  // tiles of 16 dims: rows g (even places) and g + 8 (odd places), columns 2t, 2t + 1
-  float cs[NT][G][4];     // sum of P s of every group (all rows alike)
-  float m_run[NT][2], l_run[NT][2];
+  float cs[NT][G][2];     // sum of P s of every group
+  float m_run[NT][2], l_run[NT][2], base[NT][2];  // base: what P is 2^0 at
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -162,128 +234,167 @@ __global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.0f;
 #pragma unroll
-    for (int gr = 0; gr < G; ++gr)
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) cs[nt][gr][c] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) m_run[nt][c] = -INFINITY, l_run[nt][c] = 0.0f;
+      for (int gr = 0; gr < G; ++gr) cs[nt][gr][c] = 0.0f;
+      m_run[nt][c] = -INFINITY;
+      l_run[nt][c] = base[nt][c] = 0.0f;
+    }
   }
 
-  const int per = 1 << (p.page_shift - 4);  // blocks of a page and head
-  for (int pos0 = t_begin + 16 * warp; pos0 < end; pos0 += 16 * kQaWarps) {
-    const int pg = __ldcg(p.table + (size_t)b * p.M + (pos0 >> p.page_shift));
-    if (pg < 0 || pg >= p.P) {  // the same for the whole warp
-      if (lane == 0) set_error(p.err, kErrDeviceIndex);
-      continue;
+  int done = 0;
+#pragma unroll 1
+  for (; done < nsteps; ++done) {
+    const int st = done % S;
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (done / S) & 1, p.wait_ns))) {
+      if (lane == 0) set_error(p.err, kErrTimeout);
+      break;
     }
-    const uint8_t* blk = p.pool + (((size_t)pg * p.nkv + h) * per + ((pos0 >> 4) & (per - 1))) * L::kBytes;
-    const Q4Words<W> k0 = q4_load<W>(blk + lane * (4 * W)), k1 = q4_load<W>(blk + (32 + lane) * (4 * W));
-    const Q4Words<W> v0 = q4_load<W>(blk + L::kV + lane * (4 * W)), v1 = q4_load<W>(blk + L::kV + (32 + lane) * (4 * W));
-    const uint32_t ks0 = q4_load_scales<G>(blk + L::kKs + g * 2 * G), ks1 = q4_load_scales<G>(blk + L::kKs + (g + 8) * 2 * G);
-    const uint32_t vs0 = q4_load_scales<G>(blk + L::kVs + g * 2 * G), vs1 = q4_load_scales<G>(blk + L::kVs + (g + 8) * 2 * G);
+    const uint8_t* blk = ring + st * U * L::kBytes;
+    const int pos0 = first + done * (kQaWarps * kStep);
+    const int gone = ~here[st] & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
 
-    // ---- scores (log2 units)
-    float x[NT][4];
+    // ---- scores, before the row's factor
+    float x[U][NT][4];
+    float lift[U][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* bk = blk + u * L::kBytes;
+      const Q4Words<W> k0 = q4_load<W>(bk + lane * (4 * W)), k1 = q4_load<W>(bk + (32 + lane) * (4 * W));
+      const uint32_t ks0 = q4_load_scales<G>(bk + L::kKs + g * 2 * G), ks1 = q4_load_scales<G>(bk + L::kKs + (g + 8) * 2 * G);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[nt][c] = 0.0f;
+      for (int gr = 0; gr < G; ++gr) {
+        float acc[NT][4];
 #pragma unroll
-    for (int gr = 0; gr < G; ++gr) {
-      float acc[NT][4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int c = 0; c < 4; ++c) acc[nt][c] = ci[nt][gr][c & 1];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[nt][c] = ci[nt][gr][c & 1];
+        for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
+          const uint32_t a = k0.w[j], c = k1.w[j], a8 = a >> 8, c8 = c >> 8;
 #pragma unroll
-      for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
-        const uint32_t a = k0.w[j], c = k1.w[j], a8 = a >> 8, c8 = c >> 8;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_m16n8k16(acc[nt], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[nt][j][0],
-                           qf[nt][j][1]);
-          mma_f16_m16n8k16(acc[nt], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
-                           qf[nt][j][2], qf[nt][j][3]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_m16n8k16(acc[nt], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[nt][j][0],
+                             qf[nt][j][1]);
+            mma_f16_m16n8k16(acc[nt], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
+                             qf[nt][j][2], qf[nt][j][3]);
+          }
         }
+        const float s0 = q4_scale(ks0, gr), s1 = q4_scale(ks1, gr);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            x[u][nt][c] = gr == 0 ? __fmul_rn(acc[nt][c], c < 2 ? s0 : s1) : fmaf(acc[nt][c], c < 2 ? s0 : s1, x[u][nt][c]);
       }
-      const float s0 = q4_scale(ks0, gr), s1 = q4_scale(ks1, gr);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(acc[nt][c], c < 2 ? s0 : s1, x[nt][c]);
+      lift[u][0] = lift_of(q4_load_scales<G>(bk + L::kVs + g * 2 * G));
+      lift[u][1] = lift_of(q4_load_scales<G>(bk + L::kVs + (g + 8) * 2 * G));
     }
     // ---- the online softmax
-    const bool masked = pos0 + 15 > n - p.Q;  // some row does not see all of the block
-    const float lift0 = lift_of(vs0), lift1 = lift_of(vs1);
-    float pr[NT][4];
+    const bool masked = pos0 + kStep - 1 > n - p.Q || gone;  // some row does not see all of the step
+    uint32_t hidden[NT] = {};  // bit 4 u + c: row 2t + c % 2 does not see position g + 8 (c / 2) of block u
+    if (masked) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (pos0 + 16 * u + g + (c < 2 ? 0 : 8) > lim[nt][c & 1] || (gone >> u & 1)) hidden[nt] |= 1u << (4 * u + c);
+    }
+    float pr[U][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float y[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[nt][c] = __fmul_rn(x[nt][c], fq[nt][c & 1]);  // not fused with what follows: the same in every form
-        if (masked && pos0 + g + (c < 2 ? 0 : 8) > lim[nt][c & 1]) x[nt][c] = -INFINITY;
-        y[c] = x[nt][c] + (c < 2 ? lift0 : lift1);
-      }
-      float corr[2];
+      float top[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float m = fmaxf(y[c], y[c + 2]);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        m = fmaxf(m, m_run[nt][c]);
-        corr[c] = m == -INFINITY ? 1.0f : ex2_ftz(m_run[nt][c] - m);
-        m_run[nt][c] = m;
-        const float base = m == -INFINITY ? 0.0f : m - kQaLift;
-        pr[nt][c] = ex2_ftz(x[nt][c] - base);
-        pr[nt][c + 2] = ex2_ftz(x[nt][c + 2] - base);
-        l_run[nt][c] = fmaf(l_run[nt][c], corr[c], pr[nt][c] + pr[nt][c + 2]);
+        top[c] = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float y = fmaf(x[u][nt][c + 2 * e], fq[nt][c], lift[u][e]);
+            top[c] = masked && (hidden[nt] >> (4 * u + c + 2 * e) & 1u) ? top[c] : fmaxf(top[c], y);
+          }
+        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 4));
+        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 8));
+        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 16));
       }
-      if (!__all_sync(0xffffffffu, corr[0] == 1.0f && corr[1] == 1.0f)) {
+      if (__any_sync(0xffffffffu, top[0] > m_run[nt][0] || top[1] > m_run[nt][1])) {
+        float corr[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float m = fmaxf(m_run[nt][c], top[c]);
+          corr[c] = m == -INFINITY ? 1.0f : ex2_ftz(m_run[nt][c] - m);
+          m_run[nt][c] = m;
+          base[nt][c] = m == -INFINITY ? 0.0f : m - kQaLift;
+          l_run[nt][c] *= corr[c];
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) cs[nt][gr][c] *= corr[c];
+        }
 #pragma unroll
         for (int i = 0; i < 2 * W; ++i)
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[nt][i][c] *= corr[c & 1];
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          cs[nt][gr][0] *= corr[0];
-          cs[nt][gr][1] *= corr[1];
-        }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v = ex2_ftz(fmaf(x[u][nt][c], fq[nt][c & 1], -base[nt][c & 1]));
+          if (masked && (hidden[nt] >> (4 * u + c) & 1u)) v = 0.0f;
+          pr[u][nt][c] = v;
+          l_run[nt][c & 1] += v;
+        }
     }
     // ---- the weighted values
 #pragma unroll
-    for (int gr = 0; gr < G; ++gr) {
-      const float s0 = q4_scale(vs0, gr), s1 = q4_scale(vs1, gr);
-      uint32_t pb[NT][2];
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* bk = blk + u * L::kBytes;
+      const Q4Words<W> v0 = q4_load<W>(bk + L::kV + lane * (4 * W)), v1 = q4_load<W>(bk + L::kV + (32 + lane) * (4 * W));
+      const uint32_t vs0 = q4_load_scales<G>(bk + L::kVs + g * 2 * G), vs1 = q4_load_scales<G>(bk + L::kVs + (g + 8) * 2 * G);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          w[c] = pr[nt][c] * (c < 2 ? s0 : s1);
-          if (masked && x[nt][c] == -INFINITY) w[c] = 0.0f;
-        }
-        pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
-        pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
-        mma_f16_m16n8k16(cs[nt][gr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nt][0], pb[nt][1]);
-      }
-#pragma unroll
-      for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
-        const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+      for (int gr = 0; gr < G; ++gr) {
+        const float s0 = q4_scale(vs0, gr), s1 = q4_scale(vs1, gr);
+        uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_m16n8k16(o[nt][2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u, pb[nt][0],
-                           pb[nt][1]);
-          mma_f16_m16n8k16(o[nt][2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u,
-                           pb[nt][0], pb[nt][1]);
+          float w[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            w[c] = pr[u][nt][c] * (c < 2 ? s0 : s1);
+            if (masked && (hidden[nt] >> (4 * u + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
+          }
+          pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
+          pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
+          float ones[4] = {cs[nt][gr][0], cs[nt][gr][1], 0.0f, 0.0f};
+          mma_f16_m16n8k16(ones, 0x3C003C00u, 0u, 0x3C003C00u, 0u, pb[nt][0], pb[nt][1]);
+          cs[nt][gr][0] = ones[0];
+          cs[nt][gr][1] = ones[1];
+        }
+#pragma unroll
+        for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
+          const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_m16n8k16(o[nt][2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u,
+                             pb[nt][0], pb[nt][1]);
+            mma_f16_m16n8k16(o[nt][2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u,
+                             pb[nt][0], pb[nt][1]);
+          }
         }
       }
     }
+    __syncwarp();  // every lane has read the stage
+    if (done + S < nsteps) issue(done + S);
   }
+  // after a wait that ran out: the copies already issued land before the memory is used again
+  for (int i = done; i < nsteps && i < done + S; ++i) mbar_wait(&full[i % S], (i / S) & 1, p.wait_ns);
+  __syncwarp();
 
-  // ---- the warp's state: column 2t + c of tile nt is row 8 nt + 2t + c
+  // ---- the warp's state, in its drained ring: column 2t + c of tile nt is row 8 nt + 2t + c
+  float* o_w = reinterpret_cast<float*>(ring);
+  float* ml_w = reinterpret_cast<float*>(ring + SM::kMl);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -293,14 +404,11 @@ __global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (g == 0) {
-        ml_s[warp][r][0] = m_run[nt][c];
-        ml_s[warp][r][1] = l;
-      }
+      if (g == 0) *reinterpret_cast<float2*>(ml_w + 2 * r) = make_float2(m_run[nt][c], l);
 #pragma unroll
       for (int m = 0; m < W; ++m) {
         const float off = -8.0f * cs[nt][m >> 1][c];
-        *reinterpret_cast<float4*>(&o_s[warp][r][32 * m + 4 * g]) =
+        *reinterpret_cast<float4*>(o_w + r * SM::kStride + 32 * m + 4 * g) =
             make_float4(fmaf(o[nt][2 * m][c], 16777216.0f, off), fmaf(o[nt][2 * m][c + 2], 1048576.0f, off),
                         fmaf(o[nt][2 * m + 1][c], 16777216.0f, off), fmaf(o[nt][2 * m + 1][c + 2], 1048576.0f, off));
       }
@@ -308,18 +416,21 @@ __global__ void __launch_bounds__(kQaThreads) attn_q4_kernel(const QaParams p) {
   __syncthreads();
   for (int i = threadIdx.x; i < nrows * (D / 4); i += kQaThreads) {
     const int r = i / (D / 4), c4 = i - r * (D / 4), row = r0 + r;
+    float2 ml[kQaWarps];
     float mm = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kQaWarps; ++w) mm = fmaxf(mm, ml_s[w][r][0]);
+    for (int w = 0; w < kQaWarps; ++w) {
+      ml[w] = *reinterpret_cast<const float2*>(smem + w * SM::kWarp + SM::kMl + 8 * r);
+      mm = fmaxf(mm, ml[w].x);
+    }
     float ls = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kQaWarps; ++w) {
-      const float mw = ml_s[w][r][0];
       // a warp that saw nothing adds nothing; one that saw only NaN scores adds them
-      const float f = mw == -INFINITY ? (ml_s[w][r][1] == 0.0f ? 0.0f : 1.0f) : ex2_ftz(mw - mm);
-      const float4 v = *reinterpret_cast<const float4*>(&o_s[w][r][4 * c4]);
-      ls = fmaf(ml_s[w][r][1], f, ls);
+      const float f = ml[w].x == -INFINITY ? (ml[w].y == 0.0f ? 0.0f : 1.0f) : ex2_ftz(ml[w].x - mm);
+      const float4 v = *reinterpret_cast<const float4*>(smem + w * SM::kWarp + (r * SM::kStride + 4 * c4) * 4);
+      ls = fmaf(ml[w].y, f, ls);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z);
@@ -402,7 +513,7 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
 // once, a whole number of rounds of the four warps.  It goes by the capacity (the lengths are on the
 // device) and not by Q or the shared heads, so a row is summed in the same order alone and among others.
 int chunk_of(int B, int nkv, long long cap) {
-  constexpr int kRound = 16 * kQaWarps, kTarget = 152 * 4 * 4;
+  constexpr int kRound = 32 * kQaWarps, kTarget = 152 * 4 * 4;
   const long long pairs = (long long)B * nkv;
   long long want = pairs > 0 ? (pairs * cap + kTarget - 1) / kTarget : 128;
   const long long least = (cap + kQaMaxChunks - 1) / kQaMaxChunks;
@@ -420,13 +531,25 @@ bool shape_ok(int B, int Q, int M, int page, int nh, int nkv, int d) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <int D, int NT>
-cudaError_t run(const QaParams& p, cudaStream_t s) {
-  cudaError_t e = launch_pdl(attn_q4_kernel<D, NT>, dim3(p.B * p.nkv * p.rblocks, p.nchunk), dim3(kQaThreads), 0, s, p);
+template <int D, int NT, int U, int S, int kPerSm>
+cudaError_t run(const QaParams& p, const DeviceCtx& dc, cudaStream_t s) {
+  constexpr int kSmem = QaSmem<D, NT, U, S>::kTotal;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attn_q4_kernel<D, NT, U, S, kPerSm>), kSmem, dc.device);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_q4_kernel<D, NT, U, S, kPerSm>, dim3(p.B * p.nkv * p.rblocks, p.nchunk), dim3(kQaThreads), kSmem, s, p);
   if (e != cudaSuccess || p.nchunk == 1) return e;
   const int slices = (p.R * (D / 4) + kQcThreads - 1) / kQcThreads;
   return launch_pdl(attn_q4_combine_kernel<D>, dim3(p.B * p.nkv, slices), dim3(kQcThreads), 0, s, p);
 }
+
+#ifndef Q4_U1
+#define Q4_U1 2
+#define Q4_S1 3
+#define Q4_C1 4
+#define Q4_U2 2
+#define Q4_S2 3
+#define Q4_C2 2
+#endif
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -484,11 +607,12 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.o_part = static_cast<float*>(ws);
   p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(parts * d * 4));
   p.err = dc->err;
+  p.wait_ns = wait_limit_ns();
   const bool two = p.R > 8;
   p.rblocks = two ? (p.R + 15) / 16 : 1;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = d == 128 ? (two ? run<128, 2>(p, s) : run<128, 1>(p, s))
-                                 : (two ? run<64, 2>(p, s) : run<64, 1>(p, s));
+  const cudaError_t e = d == 128 ? (two ? run<128, 2, Q4_U2, Q4_S2, Q4_C2>(p, *dc, s) : run<128, 1, Q4_U1, Q4_S1, Q4_C1>(p, *dc, s))
+                                 : (two ? run<64, 2, Q4_U2, Q4_S2, Q4_C2>(p, *dc, s) : run<64, 1, Q4_U1, Q4_S1, Q4_C1>(p, *dc, s));
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }
 
