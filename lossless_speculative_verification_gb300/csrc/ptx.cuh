@@ -194,13 +194,13 @@ __device__ __forceinline__ void mma_bf16_m16n8k16_top(float (&c)[2], uint32_t a0
   c[1] = d[1];
 }
 
-// D[16x8] += A[16x16] * B[16x8], f16 inputs (subnormals kept), fp32 accumulation.
+// D[16x8] = A[16x16] * B[16x8] + C, f16 inputs (subnormals kept), fp32 accumulation.
 __device__ __forceinline__ void mma_f16_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                 uint32_t b0, uint32_t b1) {
+                                                 uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // Transpose of an 8x8 b16 matrix over the warp: lane (g, t) gives row g, columns 2t and 2t+1, and

@@ -25,6 +25,8 @@
 // result does not depend on the other rows of the call.
 #include <math.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "lsv.h"
 #include "ptx.cuh"
@@ -60,16 +62,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-// Exponent of the larger of a position's value scales (a NaN one left out), at least -64.
-__device__ __forceinline__ float lift_of(uint32_t s) {
-  const uint32_t a = s & 0xFFFFu, b = s >> 16;
-  uint32_t u = max(a, b);
-  if (u >= 0x7F80u) {
-    u = min(a, b);
-    if (u >= 0x7F80u) u = 0u;
-  }
-  return (float)max((int)(u >> 7) - 127, -64);
+// Bits of the larger of a position's value scales, a NaN one left out.
+__device__ __forceinline__ uint32_t larger_scale(uint32_t s) {
+  const uint32_t a = s & 0xFFFFu, b = s >> 16, u = max(a, b);
+  if (u < 0x7F80u) return u;
+  const uint32_t v = min(a, b);
+  return v < 0x7F80u ? v : 0u;
 }
+// Its exponent, at least -64.
+__device__ __forceinline__ float exponent_of(uint32_t bits) { return (float)max((int)(bits >> 7) - 127, -64); }
 
 // A warp's ring of S stages of U blocks each in shared memory, filled by untiled bulk copies.
 template <int D, int NT, int U, int S>
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     return -1;
   };
   int pg_now = pages_of(0), pg_next = -1;
-  auto issue = [&](int i) {  // all lanes
+  auto issue = [&](int i, int s) {  // all lanes: step i into stage s
     const int k = i % kBatch;
     if (k == 0) {
       if (i > 0) pg_now = pg_next;
@@ -153,7 +154,6 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       there |= (pg[u] >= 0) << u;
     }
     if (lane == 0) {
-      const int s = i % S;
       here[s] = there;
       mbar_arrive_expect_tx(&full[s], __popc(there) * L::kBytes);
 #pragma unroll
@@ -167,12 +167,12 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     }
   };
 #pragma unroll 1
-  for (int i = 0; i < S && i < nsteps; ++i) issue(i);
+  for (int i = 0; i < S && i < nsteps; ++i) issue(i, i);
   __syncwarp();
 
   // ---- the queries as B operands
   uint32_t qf[NT][W][4];
-  float ci[NT][G][2];  // -8 * 2^-24 * sum of the group's queries, for this lane's columns 2t, 2t + 1
+  float ci[NT][G][4];  // -8 * 2^-24 * sum of the group's queries, for this lane's columns 2t, 2t + 1, twice
   float fq[NT][2];     // what turns the scaled sums into log2 scores
   int lim[NT][2];      // last position the row sees
 #pragma unroll
@@ -218,14 +218,14 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     for (int c = 0; c < 2; ++c) {
       const int src = (2 * t + c) * 4;  // a lane of column 2t + c
 #pragma unroll
-      for (int gr = 0; gr < G; ++gr) ci[nt][gr][c] = __shfl_sync(0xffffffffu, sum[gr], src);
+      for (int gr = 0; gr < G; ++gr) ci[nt][gr][c] = ci[nt][gr][c + 2] = __shfl_sync(0xffffffffu, sum[gr], src);
       fq[nt][c] = __shfl_sync(0xffffffffu, fr, src);
       lim[nt][c] = __shfl_sync(0xffffffffu, lm, src);
     }
   }
 
   float o[NT][2 * W][4];  // tiles of 16 dims: rows g (even places) and g + 8 (odd places), columns 2t, 2t + 1
-  float cs[NT][G][2];     // sum of P s of every group
+  float cs[NT][G][4];     // sum of P s of every group (columns 2t, 2t + 1; the rest stays 0)
   float m_run[NT][2], l_run[NT][2], base[NT][2];  // base: what P is 2^0 at
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -236,27 +236,18 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int gr = 0; gr < G; ++gr) cs[nt][gr][c] = 0.0f;
+      for (int gr = 0; gr < G; ++gr) cs[nt][gr][c] = cs[nt][gr][c + 2] = 0.0f;
       m_run[nt][c] = -INFINITY;
       l_run[nt][c] = base[nt][c] = 0.0f;
     }
   }
 
-  int done = 0;
-#pragma unroll 1
-  for (; done < nsteps; ++done) {
-    const int st = done % S;
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (done / S) & 1, p.wait_ns))) {
-      if (lane == 0) set_error(p.err, kErrTimeout);
-      break;
-    }
-    const uint8_t* blk = ring + st * U * L::kBytes;
-    const int pos0 = first + done * (kQaWarps * kStep);
-    const int gone = ~here[st] & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
-
+  // One step: the U blocks of a stage from position pos0 on.  Masked: some row does not see all of it, or a
+  // block is not there.
+  auto step = [&](auto tag, const uint8_t* blk, int pos0, int gone) {
+    constexpr bool kMasked = decltype(tag)::value;
     // ---- scores, before the row's factor
     float x[U][NT][4];
-    float lift[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint8_t* bk = blk + u * L::kBytes;
@@ -266,18 +257,14 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       for (int gr = 0; gr < G; ++gr) {
         float acc[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[nt][c] = ci[nt][gr][c & 1];
-#pragma unroll
         for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
           const uint32_t a = k0.w[j], c = k1.w[j], a8 = a >> 8, c8 = c >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_f16_m16n8k16(acc[nt], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[nt][j][0],
-                             qf[nt][j][1]);
+                             qf[nt][j][1], j == 2 * gr ? ci[nt][gr] : acc[nt]);
             mma_f16_m16n8k16(acc[nt], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
-                             qf[nt][j][2], qf[nt][j][3]);
+                             qf[nt][j][2], qf[nt][j][3], acc[nt]);
           }
         }
         const float s0 = q4_scale(ks0, gr), s1 = q4_scale(ks1, gr);
@@ -287,20 +274,28 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
           for (int c = 0; c < 4; ++c)
             x[u][nt][c] = gr == 0 ? __fmul_rn(acc[nt][c], c < 2 ? s0 : s1) : fmaf(acc[nt][c], c < 2 ? s0 : s1, x[u][nt][c]);
       }
-      lift[u][0] = lift_of(q4_load_scales<G>(bk + L::kVs + g * 2 * G));
-      lift[u][1] = lift_of(q4_load_scales<G>(bk + L::kVs + (g + 8) * 2 * G));
     }
     // ---- the online softmax
-    const bool masked = pos0 + kStep - 1 > n - p.Q || gone;  // some row does not see all of the step
-    uint32_t hidden[NT] = {};  // bit 4 u + c: row 2t + c % 2 does not see position g + 8 (c / 2) of block u
-    if (masked) {
+    uint32_t hidden[NT];  // bit 4 u + c: row 2t + c % 2 does not see position g + 8 (c / 2) of block u
+    uint32_t big = 0;     // the largest value scale of the step
+    if (kMasked) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        hidden[nt] = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (pos0 + 16 * u + g + (c < 2 ? 0 : 8) > lim[nt][c & 1] || (gone >> u & 1)) hidden[nt] |= 1u << (4 * u + c);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; u += 2) {
+        // lane l has position l of two blocks
+        const uint32_t s = q4_load_scales<G>(blk + (U == 1 ? 0 : u + (lane >> 4)) * L::kBytes + L::kVs + (lane & 15) * 2 * G);
+        big = max(big, larger_scale(s));
+      }
+      big = __reduce_max_sync(0xffffffffu, big);
     }
     float pr[U][NT][4];
 #pragma unroll
@@ -309,16 +304,22 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         top[c] = -INFINITY;
+        uint32_t row_big = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float y = fmaf(x[u][nt][c + 2 * e], fq[nt][c], lift[u][e]);
-            top[c] = masked && (hidden[nt] >> (4 * u + c + 2 * e) & 1u) ? top[c] : fmaxf(top[c], y);
+            if (kMasked && (hidden[nt] >> (4 * u + c + 2 * e) & 1u)) continue;
+            top[c] = fmaxf(top[c], __fmul_rn(x[u][nt][c + 2 * e], fq[nt][c]));
+            if (kMasked)
+              row_big = max(row_big, larger_scale(q4_load_scales<G>(blk + u * L::kBytes + L::kVs + (g + 8 * e) * 2 * G)));
           }
-        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 4));
-        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 8));
-        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 16));
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], sh));
+          if (kMasked) row_big = max(row_big, __shfl_xor_sync(0xffffffffu, row_big, sh));
+        }
+        top[c] += exponent_of(kMasked ? row_big : big);
       }
       if (__any_sync(0xffffffffu, top[0] > m_run[nt][0] || top[1] > m_run[nt][1])) {
         float corr[2];
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v = ex2_ftz(fmaf(x[u][nt][c], fq[nt][c & 1], -base[nt][c & 1]));
-          if (masked && (hidden[nt] >> (4 * u + c) & 1u)) v = 0.0f;
+          if (kMasked && (hidden[nt] >> (4 * u + c) & 1u)) v = 0.0f;
           pr[u][nt][c] = v;
           l_run[nt][c & 1] += v;
         }
@@ -363,14 +364,11 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             w[c] = pr[u][nt][c] * (c < 2 ? s0 : s1);
-            if (masked && (hidden[nt] >> (4 * u + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
+            if (kMasked && (hidden[nt] >> (4 * u + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
           }
           pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
           pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
-          float ones[4] = {cs[nt][gr][0], cs[nt][gr][1], 0.0f, 0.0f};
-          mma_f16_m16n8k16(ones, 0x3C003C00u, 0u, 0x3C003C00u, 0u, pb[nt][0], pb[nt][1]);
-          cs[nt][gr][0] = ones[0];
-          cs[nt][gr][1] = ones[1];
+          mma_f16_m16n8k16(cs[nt][gr], 0x3C003C00u, 0u, 0x3C003C00u, 0u, pb[nt][0], pb[nt][1], cs[nt][gr]);
         }
 #pragma unroll
         for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
@@ -378,15 +376,36 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_f16_m16n8k16(o[nt][2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u,
-                             pb[nt][0], pb[nt][1]);
+                             pb[nt][0], pb[nt][1], o[nt][2 * m]);
             mma_f16_m16n8k16(o[nt][2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u,
-                             pb[nt][0], pb[nt][1]);
+                             pb[nt][0], pb[nt][1], o[nt][2 * m + 1]);
           }
         }
       }
     }
+  };
+
+  int done = 0, st = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (; done < nsteps; ++done) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], phase, p.wait_ns))) {
+      if (lane == 0) set_error(p.err, kErrTimeout);
+      break;
+    }
+    const uint8_t* blk = ring + st * U * L::kBytes;
+    const int pos0 = first + done * (kQaWarps * kStep);
+    const int gone = ~here[st] & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
+    if (pos0 + kStep - 1 > n - p.Q || gone)
+      step(std::true_type{}, blk, pos0, gone);
+    else
+      step(std::false_type{}, blk, pos0, 0);
     __syncwarp();  // every lane has read the stage
-    if (done + S < nsteps) issue(done + S);
+    if (done + S < nsteps) issue(done + S, st);
+    if (++st == S) {
+      st = 0;
+      phase ^= 1u;
+    }
   }
   // after a wait that ran out: the copies already issued land before the memory is used again
   for (int i = done; i < nsteps && i < done + S; ++i) mbar_wait(&full[i % S], (i / S) & 1, p.wait_ns);
