@@ -16,8 +16,10 @@
 //   group, from one more MMA with ones, takes the 8 off at the end, and the rows
 //   of the odd places are divided by 16 there.
 // To keep P s in the range of f16 whatever the scales are, the running maximum
-// is taken over score + exponent of the position's largest value scale, and P is
-// 2^12 at it: P s < 2^13, and what underflows is below 2^-26 of the largest term.
+// is taken over score + exponent of the largest value scale, and P is 2^8 at it.
+// It follows the true one only where that rises by more than a factor 2^6 (the
+// sums are rescaled in few steps then): P s < 2^15, and what underflows is below
+// 2^-22 of the largest term.
 //
 // A CTA's four warps take the 16-position blocks of one chunk of one key head in
 // turn; their states (maximum, sum, output) meet in shared memory, those of the
@@ -37,7 +39,8 @@ namespace {
 
 constexpr int kQaWarps = 4;
 constexpr int kQaThreads = kQaWarps * 32;
-constexpr float kQaLift = 12.0f;  // log2 of P at the running maximum
+constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
+constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
 constexpr float kQaLog2e = 1.4426950408889634f;
 constexpr int kQaMaxChunks = 1024;
 
@@ -321,11 +324,11 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
         }
         top[c] += exponent_of(kMasked ? row_big : big);
       }
-      if (__any_sync(0xffffffffu, top[0] > m_run[nt][0] || top[1] > m_run[nt][1])) {
+      if (__any_sync(0xffffffffu, top[0] > m_run[nt][0] + kQaSlack || top[1] > m_run[nt][1] + kQaSlack)) {
         float corr[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float m = fmaxf(m_run[nt][c], top[c]);
+          const float m = top[c] > m_run[nt][c] + kQaSlack ? top[c] : m_run[nt][c];
           corr[c] = m == -INFINITY ? 1.0f : ex2_ftz(m_run[nt][c] - m);
           m_run[nt][c] = m;
           base[nt][c] = m == -INFINITY ? 0.0f : m - kQaLift;
@@ -528,18 +531,22 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
   }
 }
 
-// Positions of a chunk: as long as leaves about four chunks for each of the CTAs that the GPU holds at
-// once, a whole number of rounds of the four warps.  It goes by the capacity (the lengths are on the
-// device) and not by Q or the shared heads, so a row is summed in the same order alone and among others.
+// Positions of a chunk, a whole number of steps of the four warps (128 positions).  Many chunks fill the GPU,
+// but each costs its CTA about as much as three steps (queries, first loads, the states' meeting) and the
+// combine its share: the number of chunks with the least rounds of CTAs (two an SM) times steps of a round.
+// It goes by the capacity (the lengths are on the device) and not by Q or the shared heads, so a row is summed
+// in the same order alone and among others.
 int chunk_of(int B, int nkv, long long cap) {
-  constexpr int kRound = 32 * kQaWarps, kTarget = 152 * 4 * 4;
-  const long long pairs = (long long)B * nkv;
-  long long want = pairs > 0 ? (pairs * cap + kTarget - 1) / kTarget : 128;
-  const long long least = (cap + kQaMaxChunks - 1) / kQaMaxChunks;
-  if (want < least) want = least;
-  if (want < 128) want = 128;
-  if (want > 4096 && least <= 4096) want = 4096;
-  return (int)((want + kRound - 1) / kRound * kRound);
+  constexpr int kRound = 32 * kQaWarps, kSlots = 152 * 2, kCost = 3;
+  const long long pairs = (long long)B * nkv, steps = (cap + kRound - 1) / kRound;
+  long long best = 1ll << 62, at = steps;
+  for (long long k = 1; k <= kQaMaxChunks && k <= steps; ++k) {
+    const long long len = (steps + k - 1) / k, used = (steps + len - 1) / len;
+    const long long cost = (pairs * used + kSlots - 1) / kSlots * (len + kCost);
+    if (cost < best) best = cost, at = len;
+    if (pairs * used > 8 * kSlots && k > 1) break;  // finer cuts only add CTAs
+  }
+  return (int)(at * kRound);
 }
 
 bool shape_ok(int B, int Q, int M, int page, int nh, int nkv, int d) {
