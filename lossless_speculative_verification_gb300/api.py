@@ -8,6 +8,7 @@ computation runs in the library's kernels.  Workspaces are passed explicitly
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -17,8 +18,10 @@ from ._ffi import MoeShape, MoeWeights, check
 
 
 def _stream(stream=None) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        # the current stream's handle without the Stream object around it (3 us a call less)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _ptr(t):
@@ -193,14 +196,29 @@ def spec_verify_attention(q, k_cache, v_cache, ctx_len, ws, scale=None, out=None
     return out
 
 
-def _need_here(**tensors):
-    """Every tensor on the current device, whose stream, error word and address space the call uses."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError("%s must be on the current CUDA device" % name)
+def _here(dev, *tensors):
+    """Each (tensor, dtype, name): on the current device, whose stream and error word the call uses, of that type,
+    contiguous; returns the addresses.  One pass over few attributes: these calls take microseconds."""
+    ptrs = []
+    for t, dtype, name in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError("%s must be a CUDA tensor on the current device" % name)
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
+def _stream_of(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=None)
 def spec_q4_page_bytes(nkv, d, page) -> int:
     """Bytes of a page of `page` positions of the 4-bit cache (a pool is a uint8 tensor [P, page bytes])."""
     n = _ffi.load().spec_q4_page_bytes(nkv, d, page)
@@ -209,12 +227,11 @@ def spec_q4_page_bytes(nkv, d, page) -> int:
     return int(n)
 
 
-def _need_q4(pool, table, ctx_len, B, nkv, d, page):
-    """Check a 4-bit cache's tensors; returns (M, P)."""
-    _need(pool, torch.uint8, "pool"); _need(table, torch.int32, "table"); _need(ctx_len, torch.int32, "ctx_len")
+def _q4_sizes(pool, table, ctx_len, B, nkv, d, page):
+    """(M, P) of a 4-bit cache, its shapes checked."""
     if pool.dim() != 2 or pool.shape[1] != spec_q4_page_bytes(nkv, d, page):
         raise ValueError("pool must be [P, %d] for nkv %d, d %d, page %d" % (spec_q4_page_bytes(nkv, d, page), nkv, d, page))
-    if table.dim() != 2 or table.shape[0] != B or tuple(ctx_len.shape) != (B,):
+    if table.dim() != 2 or table.shape[0] != B or ctx_len.shape != (B,):
         raise ValueError("table must be [B, M] and ctx_len [B], with B = %d" % B)
     return table.shape[1], pool.shape[0]
 
@@ -222,29 +239,30 @@ def _need_q4(pool, table, ctx_len, B, nkv, d, page):
 def spec_q4_append(k_new, v_new, pool, table, ctx_len, page, stream=None):
     """Keys and values of the Q new positions [B, Q, nkv, d] (bf16) into the 4-bit pages at
     ctx_len[b] - Q + j (ctx_len: the lengths after the append)."""
-    _need(k_new, torch.bfloat16, "k_new"); _need(v_new, torch.bfloat16, "v_new")
+    dev = torch.cuda.current_device()
+    k, v, pl, tb, cl = _here(dev, (k_new, torch.bfloat16, "k_new"), (v_new, torch.bfloat16, "v_new"),
+                             (pool, torch.uint8, "pool"), (table, torch.int32, "table"), (ctx_len, torch.int32, "ctx_len"))
     if k_new.dim() != 4 or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be [B, Q, nkv, d]")
     B, Q, nkv, d = k_new.shape
-    M, P = _need_q4(pool, table, ctx_len, B, nkv, d, page)
-    _need_here(k_new=k_new, v_new=v_new, pool=pool, table=table, ctx_len=ctx_len)
-    check("spec_q4_append", _ffi.load().spec_q4_append(_ptr(k_new), _ptr(v_new), _ptr(pool), _ptr(table), _ptr(ctx_len),
-                                                       B, Q, nkv, d, page, M, P, _stream(stream)))
+    M, P = _q4_sizes(pool, table, ctx_len, B, nkv, d, page)
+    check("spec_q4_append", _ffi.load().spec_q4_append(k, v, pl, tb, cl, B, Q, nkv, d, page, M, P, _stream_of(dev, stream)))
 
 
 def spec_q4_read(pool, table, ctx_len, N, nkv, d, page, k=None, v=None, stream=None):
     """The last N positions of every sequence of the 4-bit cache as bf16 k, v [B, N, nkv, d]: row j is
     position ctx_len[b] - N + j, rows before position 0 are zeros."""
+    dev = torch.cuda.current_device()
     B = table.shape[0]
-    M, P = _need_q4(pool, table, ctx_len, B, nkv, d, page)
-    k = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device) if k is None else k
-    v = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device) if v is None else v
-    for name, t in (("k", k), ("v", v)):
-        _need(t, torch.bfloat16, name)
-        _need_shape(t, (B, N, nkv, d), name)
-    _need_here(pool=pool, table=table, ctx_len=ctx_len, k=k, v=v)
-    check("spec_q4_read", _ffi.load().spec_q4_read(_ptr(pool), _ptr(table), _ptr(ctx_len), B, N, nkv, d, page, M, P,
-                                                   _ptr(k), _ptr(v), _stream(stream)))
+    M, P = _q4_sizes(pool, table, ctx_len, B, nkv, d, page)
+    if k is None or v is None:
+        # one allocation for what is missing
+        both = torch.empty(((k is None) + (v is None), B, N, nkv, d), dtype=torch.bfloat16, device=pool.device)
+        k, v = both[0] if k is None else k, both[-1] if v is None else v
+    _need_shape(k, (B, N, nkv, d), "k"); _need_shape(v, (B, N, nkv, d), "v")
+    pl, tb, cl, kp, vp = _here(dev, (pool, torch.uint8, "pool"), (table, torch.int32, "table"),
+                               (ctx_len, torch.int32, "ctx_len"), (k, torch.bfloat16, "k"), (v, torch.bfloat16, "v"))
+    check("spec_q4_read", _ffi.load().spec_q4_read(pl, tb, cl, B, N, nkv, d, page, M, P, kp, vp, _stream_of(dev, stream)))
     return k, v
 
 
@@ -257,18 +275,20 @@ def spec_q4_attention_workspace(B, Q, M, page, nh, nkv, d, device=None) -> torch
 
 def spec_q4_attention(q, pool, table, ctx_len, nkv, page, ws, scale=None, out=None, stream=None):
     """Causal attention of the verified positions q [B, Q, nh, d] over the 4-bit pages of nkv key heads."""
-    _need(q, torch.bfloat16, "q")
+    dev = torch.cuda.current_device()
     if q.dim() != 4:
         raise ValueError("q must be [B, Q, nh, d]")
     B, Q, nh, d = q.shape
-    M, P = _need_q4(pool, table, ctx_len, B, nkv, d, page)
-    out = torch.empty_like(q) if out is None else out
-    _need(out, torch.bfloat16, "out"); _need_shape(out, q.shape, "out"); _need(ws, torch.uint8, "ws")
-    _need_here(q=q, pool=pool, table=table, ctx_len=ctx_len, ws=ws, out=out)
+    M, P = _q4_sizes(pool, table, ctx_len, B, nkv, d, page)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have shape %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+    qp, pl, tb, cl, op, wp = _here(dev, (q, torch.bfloat16, "q"), (pool, torch.uint8, "pool"), (table, torch.int32, "table"),
+                                   (ctx_len, torch.int32, "ctx_len"), (out, torch.bfloat16, "out"), (ws, torch.uint8, "ws"))
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    check("spec_q4_attention", _ffi.load().spec_q4_attention(
-        _ptr(q), _ptr(pool), _ptr(table), _ptr(ctx_len), B, Q, nh, nkv, d, page, M, P, scale, _ptr(out), _ptr(ws),
-        ws.numel(), _stream(stream)))
+    check("spec_q4_attention", _ffi.load().spec_q4_attention(qp, pl, tb, cl, B, Q, nh, nkv, d, page, M, P, scale, op, wp,
+                                                             ws.numel(), _stream_of(dev, stream)))
     return out
 
 
@@ -279,24 +299,21 @@ def spec_pages_workspace(B, M, P, device=None) -> torch.Tensor:
     return torch.empty(int(n), dtype=torch.uint8, device=device or "cuda")
 
 
-def _need_pages(pool, table, ref, table_out, ref_out, ws):
-    """Check a page table's tensors and fill in the outputs that are the inputs."""
-    table_out = table if table_out is None else table_out
-    ref_out = ref if ref_out is None else ref_out
-    for name, t in (("table", table), ("ref", ref), ("table_out", table_out), ("ref_out", ref_out)):
-        _need(t, torch.int32, name)
+def _pages_sizes(table, ref, table_out, ref_out):
+    """(B, M, P) of a page table, its shapes checked."""
     if table.dim() != 2 or ref.dim() != 1:
         raise ValueError("table must be [B, M] and ref [P]")
-    _need_shape(table_out, table.shape, "table_out"); _need_shape(ref_out, ref.shape, "ref_out")
-    _need(ws, torch.uint8, "ws")
+    if table_out.shape != table.shape or ref_out.shape != ref.shape:
+        raise ValueError("table_out and ref_out must have the shapes of table and ref")
     B, M = table.shape
-    P = ref.shape[0]
-    if pool is None:
-        return B, M, P, 0, 0, table_out, ref_out
-    if not pool.is_cuda or not pool.is_contiguous() or pool.dim() not in (2, 3) or pool.shape[-2] != P:
-        raise ValueError("pool must be a contiguous CUDA tensor [layers, P, page] or [P, page] with P = %d" % P)
-    layers = pool.shape[0] if pool.dim() == 3 else 1
-    return B, M, P, layers, pool.shape[-1] * pool.element_size(), table_out, ref_out
+    return B, M, ref.shape[0]
+
+
+def _pool_layers(pool, P):
+    """(layers, page bytes) of a pool [layers, P, page] or [P, page] of any type."""
+    if pool.dim() not in (2, 3) or pool.shape[-2] != P:
+        raise ValueError("pool must be [layers, P, page] or [P, page] with P = %d" % P)
+    return pool.shape[0] if pool.dim() == 3 else 1, pool.shape[-1] * pool.element_size()
 
 
 def spec_pages_resize(pool, table, ref, keep, cap, page, ws, table_out=None, ref_out=None, stats=None, stream=None):
@@ -304,28 +321,35 @@ def spec_pages_resize(pool, table, ref, keep, cap, page, ws, table_out=None, ref
     given back, missing ones given out, shared ones separated (the page of position keep[b] with its contents
     in every layer of pool).  In place unless table_out and ref_out are given; returns (table_out, ref_out).
     stats [4] int32: pages taken, free before, copied, entries given back or replaced."""
-    B, M, P, layers, nbytes, table_out, ref_out = _need_pages(pool, table, ref, table_out, ref_out, ws)
-    for name, t in (("keep", keep), ("cap", cap)):
-        _need(t, torch.int32, name)
-        _need_shape(t, (B,), name)
-    _need(stats, torch.int32, "stats"); _need_shape(stats, (4,), "stats")
-    _need_here(pool=pool, table=table, ref=ref, keep=keep, cap=cap, table_out=table_out, ref_out=ref_out, ws=ws,
-               stats=stats)
-    check("spec_pages_resize", _ffi.load().spec_pages_resize(
-        _ptr(pool), layers, nbytes, _ptr(table), _ptr(ref), _ptr(keep), _ptr(cap), B, M, P, page, _ptr(table_out),
-        _ptr(ref_out), _ptr(stats), _ptr(ws), ws.numel(), _stream(stream)))
+    dev = torch.cuda.current_device()
+    table_out = table if table_out is None else table_out
+    ref_out = ref if ref_out is None else ref_out
+    i32 = torch.int32
+    pl, tb, rf, kp, cp, to, ro, st, wp = _here(
+        dev, (pool, pool.dtype, "pool"), (table, i32, "table"), (ref, i32, "ref"), (keep, i32, "keep"), (cap, i32, "cap"),
+        (table_out, i32, "table_out"), (ref_out, i32, "ref_out"), (stats, i32, "stats"), (ws, torch.uint8, "ws"))
+    B, M, P = _pages_sizes(table, ref, table_out, ref_out)
+    layers, nbytes = _pool_layers(pool, P)
+    if keep.shape != (B,) or cap.shape != (B,) or (stats is not None and stats.shape != (4,)):
+        raise ValueError("keep and cap must be [%d], stats [4]" % B)
+    check("spec_pages_resize", _ffi.load().spec_pages_resize(pl, layers, nbytes, tb, rf, kp, cp, B, M, P, page, to, ro, st,
+                                                             wp, ws.numel(), _stream_of(dev, stream)))
     return table_out, ref_out
 
 
 def spec_pages_fork(table, ref, parent, ws, table_out=None, ref_out=None, stream=None):
     """Row b takes the pages of row parent[b] (-1: none), shared; in place unless table_out and ref_out are
     given; returns (table_out, ref_out)."""
-    B, M, P, _, _, table_out, ref_out = _need_pages(None, table, ref, table_out, ref_out, ws)
-    _need(parent, torch.int32, "parent"); _need_shape(parent, (B,), "parent")
-    _need_here(table=table, ref=ref, parent=parent, table_out=table_out, ref_out=ref_out, ws=ws)
-    check("spec_pages_fork", _ffi.load().spec_pages_fork(
-        _ptr(table), _ptr(ref), _ptr(parent), B, M, P, _ptr(table_out), _ptr(ref_out), _ptr(ws), ws.numel(),
-        _stream(stream)))
+    dev = torch.cuda.current_device()
+    table_out = table if table_out is None else table_out
+    ref_out = ref if ref_out is None else ref_out
+    i32 = torch.int32
+    tb, rf, pp, to, ro, wp = _here(dev, (table, i32, "table"), (ref, i32, "ref"), (parent, i32, "parent"),
+                                   (table_out, i32, "table_out"), (ref_out, i32, "ref_out"), (ws, torch.uint8, "ws"))
+    B, M, P = _pages_sizes(table, ref, table_out, ref_out)
+    if parent.shape != (B,):
+        raise ValueError("parent must be [%d]" % B)
+    check("spec_pages_fork", _ffi.load().spec_pages_fork(tb, rf, pp, B, M, P, to, ro, wp, ws.numel(), _stream_of(dev, stream)))
     return table_out, ref_out
 
 
@@ -333,13 +357,19 @@ def spec_pages_compact(pool, table, ref, ws, table_out=None, ref_out=None, map=N
     """The n live pages to the numbers 0..n-1, in every layer of pool; in place unless table_out and ref_out are
     given; returns (table_out, ref_out).  map [P] int32: each live page's new number (-1: free).
     stats [4] int32: n, pages moved, 0, 0."""
-    B, M, P, layers, nbytes, table_out, ref_out = _need_pages(pool, table, ref, table_out, ref_out, ws)
-    _need(map, torch.int32, "map"); _need_shape(map, (P,), "map")
-    _need(stats, torch.int32, "stats"); _need_shape(stats, (4,), "stats")
-    _need_here(pool=pool, table=table, ref=ref, table_out=table_out, ref_out=ref_out, ws=ws, map=map, stats=stats)
-    check("spec_pages_compact", _ffi.load().spec_pages_compact(
-        _ptr(pool), layers, nbytes, _ptr(table), _ptr(ref), B, M, P, _ptr(table_out), _ptr(ref_out), _ptr(map),
-        _ptr(stats), _ptr(ws), ws.numel(), _stream(stream)))
+    dev = torch.cuda.current_device()
+    table_out = table if table_out is None else table_out
+    ref_out = ref if ref_out is None else ref_out
+    i32 = torch.int32
+    pl, tb, rf, to, ro, mp, st, wp = _here(
+        dev, (pool, pool.dtype, "pool"), (table, i32, "table"), (ref, i32, "ref"), (table_out, i32, "table_out"),
+        (ref_out, i32, "ref_out"), (map, i32, "map"), (stats, i32, "stats"), (ws, torch.uint8, "ws"))
+    B, M, P = _pages_sizes(table, ref, table_out, ref_out)
+    layers, nbytes = _pool_layers(pool, P)
+    if (map is not None and map.shape != (P,)) or (stats is not None and stats.shape != (4,)):
+        raise ValueError("map must be [%d], stats [4]" % P)
+    check("spec_pages_compact", _ffi.load().spec_pages_compact(pl, layers, nbytes, tb, rf, B, M, P, to, ro, mp, st, wp,
+                                                               ws.numel(), _stream_of(dev, stream)))
     return table_out, ref_out
 
 

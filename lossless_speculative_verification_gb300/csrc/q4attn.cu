@@ -84,7 +84,12 @@ struct QaSmem {
   static constexpr int kRing = S * U * L::kBytes;
   static constexpr int kMl = kRows * kStride * 4;  // byte offset of (maximum, sum) behind the rows
   static constexpr int kWarp = kRing > kMl + kRows * 8 ? kRing : (kMl + kRows * 8 + 15) / 16 * 16;
-  static constexpr int kTotal = kQaWarps * (kWarp + S * 8 + S * 4);
+  static constexpr int kQ = kQaWarps * (kWarp + S * 8 + S * 4) + 15 & ~15;  // byte offset of the queries
+  static constexpr int kQf = 0;                               // [NT][W][lane] 16 bytes: the B operands
+  static constexpr int kCi = kQf + NT * L::W * 512;           // [NT][G][t] 16 bytes: where the accumulators start
+  static constexpr int kFq = kCi + NT * L::G * 64;            // [8 NT] what turns the scaled sums into log2 scores
+  static constexpr int kLim = kFq + kRows * 4;                // [8 NT] last position the row sees
+  static constexpr int kTotal = kQ + kLim + kRows * 4;
 };
 
 template <int D, int NT, int U, int S, int kPerSm>
@@ -112,17 +117,16 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   const int r0 = rb * kRows, nrows = min(kRows, p.R - r0);
   const int n = __ldcg(p.ctx_len + b);
 
-  // ---- the queries: column g of tile nt is row r0 + 8 nt + g, this lane has the dims 32 j + 8 t + 0..7
-  uint4 xq[NT][W];
+  // ---- the queries: warp w < NT makes the operands of tile w; column g is row r0 + 8 w + g, of which this lane
+  // has the dims 32 j + 8 t + 0..7
+  uint4 xq[W];
+  const int qr = 8 * warp + g;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + g, row = r0 + r;
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      xq[nt][j] = r < nrows ? __ldg(reinterpret_cast<const uint4*>(
-                                  p.q + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 32 * j + 8 * t))
-                            : make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int j = 0; j < W; ++j)
+    xq[j] = warp < NT && qr < nrows
+                ? __ldg(reinterpret_cast<const uint4*>(
+                      p.q + (((size_t)b * p.Q + (r0 + qr) / p.grp) * p.nh + h * p.grp + (r0 + qr) % p.grp) * D + 32 * j + 8 * t))
+                : make_uint4(0u, 0u, 0u, 0u);
 
   const bool bad = n < 0 || n > (p.M << p.page_shift);
   if (bad && threadIdx.x == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
@@ -173,20 +177,13 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   for (int i = 0; i < S && i < nsteps; ++i) issue(i, i);
   __syncwarp();
 
-  // ---- the queries as B operands
-  uint32_t qf[NT][W][4];
-  float ci[NT][G][4];  // -8 * 2^-24 * sum of the group's queries, for this lane's columns 2t, 2t + 1, twice
-  float fq[NT][2];     // what turns the scaled sums into log2 scores
-  int lim[NT][2];      // last position the row sees
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + g;
+  uint8_t* qs = smem + SM::kQ;
+  if (warp < NT) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const uint4 x = xq[nt][j];
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-    }
+    for (int j = 0; j < W; ++j)
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(xq[j].x & 0x7FFF7FFFu, xq[j].y & 0x7FFF7FFFu),
+                               __vmaxu2(xq[j].z & 0x7FFF7FFFu, xq[j].w & 0x7FFF7FFFu)));
     m = max(m & 0xFFFFu, m >> 16);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -199,32 +196,38 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     for (int gr = 0; gr < G; ++gr) sum[gr] = 0.0f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const uint32_t xs[4] = {xq[nt][j].x, xq[nt][j].y, xq[nt][j].z, xq[nt][j].w};
+      const uint32_t xs[4] = {xq[j].x, xq[j].y, xq[j].z, xq[j].w};
+      uint32_t v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float fo = (q & 1) ? f * 0.0625f : f;
-        const uint32_t v = pack_f16(__uint_as_float(xs[q] << 16) * fo, __uint_as_float(xs[q] & 0xFFFF0000u) * fo);
-        qf[nt][j][q] = v;
-        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        v[q] = pack_f16(__uint_as_float(xs[q] << 16) * fo, __uint_as_float(xs[q] & 0xFFFF0000u) * fo);
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&v[q]));
         sum[j >> 1] += (back.x + back.y) * ((q & 1) ? 16.0f : 1.0f);
       }
+      *reinterpret_cast<uint4*>(qs + SM::kQf + ((warp * W + j) * 32 + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    const float fr = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(p.scale_log2, 24 - k);
-    const int lm = r < nrows ? n - p.Q + (r0 + r) / p.grp : -1;
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
-      sum[gr] *= -8.0f / 16777216.0f;
+      // the accumulators of the columns 2t', 2t' + 1 start at -8 * 2^-24 * sum of the group's queries
+      float* ci = reinterpret_cast<float*>(qs + SM::kCi + ((warp * G + gr) * 4 + (g >> 1)) * 16);
+      if (t < 2) ci[2 * t + (g & 1)] = sum[gr] * (-8.0f / 16777216.0f);
     }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int src = (2 * t + c) * 4;  // a lane of column 2t + c
-#pragma unroll
-      for (int gr = 0; gr < G; ++gr) ci[nt][gr][c] = ci[nt][gr][c + 2] = __shfl_sync(0xffffffffu, sum[gr], src);
-      fq[nt][c] = __shfl_sync(0xffffffffu, fr, src);
-      lim[nt][c] = __shfl_sync(0xffffffffu, lm, src);
+    if (t == 0) {
+      reinterpret_cast<float*>(qs + SM::kFq)[qr] =
+          m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : ldexpf(p.scale_log2, 24 - k);
+      reinterpret_cast<int*>(qs + SM::kLim)[qr] = qr < nrows ? n - p.Q + (r0 + qr) / p.grp : -1;
     }
+  }
+  __syncthreads();
+  float fq[NT][2];  // of this lane's columns 2t, 2t + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float2 v = *reinterpret_cast<const float2*>(qs + SM::kFq + (8 * nt + 2 * t) * 4);
+    fq[nt][0] = v.x;
+    fq[nt][1] = v.y;
   }
 
   float o[NT][2 * W][4];  // tiles of 16 dims: rows g (even places) and g + 8 (odd places), columns 2t, 2t + 1
@@ -249,33 +252,52 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   // block is not there.
   auto step = [&](auto tag, const uint8_t* blk, int pos0, int gone) {
     constexpr bool kMasked = decltype(tag)::value;
+    Q4Words<W> kw[U][2];
+    uint32_t ks[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        kw[u][e] = q4_load<W>(blk + u * L::kBytes + (32 * e + lane) * (4 * W));
+        ks[u][e] = q4_load_scales<G>(blk + u * L::kBytes + L::kKs + (g + 8 * e) * 2 * G);
+      }
     // ---- scores, before the row's factor
     float x[U][NT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint8_t* bk = blk + u * L::kBytes;
-      const Q4Words<W> k0 = q4_load<W>(bk + lane * (4 * W)), k1 = q4_load<W>(bk + (32 + lane) * (4 * W));
-      const uint32_t ks0 = q4_load_scales<G>(bk + L::kKs + g * 2 * G), ks1 = q4_load_scales<G>(bk + L::kKs + (g + 8) * 2 * G);
+    for (int gr = 0; gr < G; ++gr) {
+      float start[NT][4];
 #pragma unroll
-      for (int gr = 0; gr < G; ++gr) {
-        float acc[NT][4];
+      for (int nt = 0; nt < NT; ++nt) {
+        const float4 v = *reinterpret_cast<const float4*>(qs + SM::kCi + ((nt * G + gr) * 4 + t) * 16);
+        start[nt][0] = v.x, start[nt][1] = v.y, start[nt][2] = v.z, start[nt][3] = v.w;
+      }
+      float acc[U][NT][4];
 #pragma unroll
-        for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
-          const uint32_t a = k0.w[j], c = k1.w[j], a8 = a >> 8, c8 = c >> 8;
+      for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
+        uint4 qf[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) qf[nt] = *reinterpret_cast<const uint4*>(qs + SM::kQf + ((nt * W + j) * 32 + lane) * 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t a = kw[u][0].w[j], c = kw[u][1].w[j], a8 = a >> 8, c8 = c >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_m16n8k16(acc[nt], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[nt][j][0],
-                             qf[nt][j][1], j == 2 * gr ? ci[nt][gr] : acc[nt]);
-            mma_f16_m16n8k16(acc[nt], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
-                             qf[nt][j][2], qf[nt][j][3], acc[nt]);
+            mma_f16_m16n8k16(acc[u][nt], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[nt].x,
+                             qf[nt].y, j == 2 * gr ? start[nt] : acc[u][nt]);
+            mma_f16_m16n8k16(acc[u][nt], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
+                             qf[nt].z, qf[nt].w, acc[u][nt]);
           }
         }
-        const float s0 = q4_scale(ks0, gr), s1 = q4_scale(ks1, gr);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float s0 = q4_scale(ks[u][0], gr), s1 = q4_scale(ks[u][1], gr);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            x[u][nt][c] = gr == 0 ? __fmul_rn(acc[nt][c], c < 2 ? s0 : s1) : fmaf(acc[nt][c], c < 2 ? s0 : s1, x[u][nt][c]);
+            x[u][nt][c] = gr == 0 ? __fmul_rn(acc[u][nt][c], c < 2 ? s0 : s1)
+                                  : fmaf(acc[u][nt][c], c < 2 ? s0 : s1, x[u][nt][c]);
       }
     }
     // ---- the online softmax
@@ -285,11 +307,12 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         hidden[nt] = 0;
+        const int2 lim = *reinterpret_cast<const int2*>(qs + SM::kLim + (8 * nt + 2 * t) * 4);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (pos0 + 16 * u + g + (c < 2 ? 0 : 8) > lim[nt][c & 1] || (gone >> u & 1)) hidden[nt] |= 1u << (4 * u + c);
+            if (pos0 + 16 * u + g + (c < 2 ? 0 : 8) > ((c & 1) ? lim.y : lim.x) || (gone >> u & 1)) hidden[nt] |= 1u << (4 * u + c);
       }
     } else {
 #pragma unroll

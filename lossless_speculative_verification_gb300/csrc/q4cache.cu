@@ -1,8 +1,8 @@
 // q4cache.cu -- writing positions to the 4-bit paged cache and reading them back
 // (layout: q4.cuh).
 //
-// One warp takes one block (16 positions of a head) in the lane layout of the
-// cache, keys and values: a lane quantises what it stores, the maximum of a
+// One CTA takes one block (16 positions of a head), each of its warps 8 positions
+// of the keys or the values in the lane layout of the cache: a lane quantises what it stores, the maximum of a
 // group of 64 dims meets over the 4 lanes of a position (keys) or the 8 lanes
 // of a pair of positions (values), and whole words leave as one vector a lane.
 // Positions at the edges of the new ones share their block with others: keys and
@@ -33,13 +33,33 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(q));
 }
 
-// The nibble of x: rint(x / s) + 8, ties to even.  Both have 8 significant bits, so x / s in fp32 rounds
-// to a half only where it is one.
-__device__ __forceinline__ uint32_t code(float x, float s, bool plain) {
-  if (!plain) return 8u;
-  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, s)), -8.0f), 7.0f)) + 8);
+// A group's scale and the nibbles by it: rint(x / s) + 8, ties to even.
+// x and s have 8 significant bits each, so x / s is a half, or at least 2^-13 of itself away from one, and
+// x * (1 / s), 2^-23 off, falls on the right side of it.  A half itself may not: the rest x - n s is exact, and
+// where it is half a step the even one of the two neighbours is taken.
+// (up: small scales, and what they divide, are brought up by a power of two, where 1 / s is finite.)
+struct Step {
+  uint32_t bits;
+  float s, inv, half, up;
+};
+__device__ __forceinline__ Step step_of(uint32_t bits) {
+  Step r;
+  r.bits = bits;
+  const bool plain = bits != 0u && bits < 0x7F80u;  // a scale of 0 or NaN: code 8 for all
+  r.up = bits < 0x2000u ? 18446744073709551616.0f : 1.0f;
+  r.s = __uint_as_float(bits << 16) * r.up;
+  r.inv = plain ? __frcp_rn(r.s) : 0.0f;
+  r.half = plain ? 0.5f * r.s : -1.0f;
+  return r;
 }
-__device__ __forceinline__ bool plain_scale(uint32_t s) { return s != 0u && s < 0x7F80u; }
+__device__ __forceinline__ uint32_t code(const Step& r, float x) {
+  if (r.inv == 0.0f) return 8u;
+  x *= r.up;
+  float n = rintf(x * r.inv);
+  const float rest = fmaf(-n, r.s, x);
+  if (fabsf(rest) == r.half) n = 2.0f * rintf(0.5f * (n + (rest > 0.0f ? 0.5f : -0.5f)));
+  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(n, -8.0f), 7.0f)) + 8);
+}
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
@@ -80,6 +100,92 @@ __device__ __forceinline__ bool place(const QwParams& p, int unit, QwPlace* w, b
   return true;
 }
 
+// Keys of 8 positions: lane (g, t) has the dims 32 j + 8 t + 0..7 of position tk = 8 half + g.
+template <int D>
+__device__ __forceinline__ void append_keys(const bf16* __restrict__ src, bool in, uint8_t* blk, int tk, int t) {
+  using L = Q4Block<D>;
+  uint4 x[L::W];
+#pragma unroll
+  for (int j = 0; j < L::W; ++j)
+    x[j] = in ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * t)) : make_uint4(0u, 0u, 0u, 0u);
+  Q4Words<L::W> out;
+  uint32_t sc = 0;
+#pragma unroll
+  for (int gr = 0; gr < L::G; ++gr) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 2 * gr; j < 2 * gr + 2; ++j) m = abs_max2(abs_max2(abs_max2(abs_max2(m, x[j].x), x[j].y), x[j].z), x[j].w);
+    m = fold2(m);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const Step s = step_of(scale_bits(m));
+    sc |= s.bits << (16 * gr);
+#pragma unroll
+    for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
+      const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      uint32_t word = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) word |= code(s, lo_f(xs[q])) << (4 * q) | code(s, hi_f(xs[q])) << (4 * q + 16);
+      out.w[j] = word;
+    }
+  }
+  if (in) {
+    q4_store<L::W>(blk + tk * (D / 2) + t * (4 * L::W), out);
+    if (t == 0) q4_store_scales<L::G>(blk + L::kKs + tk * 2 * L::G, sc);
+  }
+}
+
+// Values of 8 positions: lane (g, t) has the dims 32 m + 4 g + 0..3 of position 8 half + 2 t and the one after it.
+template <int D>
+__device__ __forceinline__ void append_values(const bf16* __restrict__ src, size_t row, const bool (&in)[2], uint8_t* blk,
+                                              int half, int lane) {
+  using L = Q4Block<D>;
+  const int g = lane >> 2, t = lane & 3;
+  uint2 x[2][L::W];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int m = 0; m < L::W; ++m)
+      x[e][m] = in[e] ? __ldg(reinterpret_cast<const uint2*>(src + e * row + 32 * m + 4 * g)) : make_uint2(0u, 0u);
+  Q4Words<L::W> out;
+#pragma unroll
+  for (int m = 0; m < L::W; ++m) out.w[m] = 0;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t sc = 0;
+#pragma unroll
+    for (int gr = 0; gr < L::G; ++gr) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int m = 2 * gr; m < 2 * gr + 2; ++m) a = abs_max2(abs_max2(a, x[e][m].x), x[e][m].y);
+      a = fold2(a);
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 4));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 16));
+      const Step s = step_of(scale_bits(a));
+      sc |= s.bits << (16 * gr);
+#pragma unroll
+      for (int m = 2 * gr; m < 2 * gr + 2; ++m)
+        out.w[m] |= (code(s, lo_f(x[e][m].x)) | code(s, hi_f(x[e][m].x)) << 4 | code(s, lo_f(x[e][m].y)) << 8 |
+                     code(s, hi_f(x[e][m].y)) << 12)
+                    << (16 * e);
+    }
+    if (in[e] && g == 0) q4_store_scales<L::G>(blk + L::kVs + (8 * half + 2 * t + e) * 2 * L::G, sc);
+  }
+  uint8_t* at = blk + L::kV + (half * 32 + lane) * (4 * L::W);
+  if (in[0] && in[1]) {
+    q4_store<L::W>(at, out);
+  } else if (in[0] || in[1]) {
+#pragma unroll
+    for (int m = 0; m < L::W; ++m)
+      *reinterpret_cast<uint16_t*>(at + 4 * m + (in[1] ? 2 : 0)) =
+          static_cast<uint16_t>(in[1] ? out.w[m] >> 16 : out.w[m] & 0xFFFFu);
+  }
+}
+
+// A warp's share is a half block (8 positions) of the keys or of the values: the four parts of a block are the
+// CTA's warps.  Whole blocks a warp took 7.9 us for 32 x 4 positions of 10 heads, quarters 4.1 us: the call is as
+// long as one warp's chain of loads, maxima and codes.
 template <int D>
 __global__ void __launch_bounds__(kQwWarps * 32) q4_append_kernel(const bf16* __restrict__ k_new,
                                                                   const bf16* __restrict__ v_new, uint8_t* pool,
@@ -87,106 +193,25 @@ __global__ void __launch_bounds__(kQwWarps * 32) q4_append_kernel(const bf16* __
   using L = Q4Block<D>;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int unit = blockIdx.x * kQwWarps + (threadIdx.x >> 5);
-  if (unit >= p.B * p.nblk * p.nkv) return;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, half = part & 1;
   QwPlace w;
   bool bad;
-  if (!place(p, unit, &w, &bad)) {
-    if (bad && lane == 0) set_error(p.err, kErrDeviceIndex);
+  if (!place(p, blockIdx.x, &w, &bad)) {
+    if (bad && threadIdx.x == 0) set_error(p.err, kErrDeviceIndex);
     return;
   }
+  const int pos0 = (w.block << 4) + 8 * half;
+  if (pos0 + 7 < w.p0 || pos0 >= w.n) return;
   uint8_t* blk = pool + w.at * L::kBytes;
-  const int pos0 = w.block << 4;
-  // row of position pos: (b Q + pos - p0) of [B Q, nkv, D]
-  const size_t row0 = (size_t)w.b * p.Q;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    // keys: lane (g, t) has the dims 32 j + 8 t + 0..7 of position 8 half + g
-    const int tk = 8 * half + g, pos = pos0 + tk;
-    const bool in = pos >= w.p0 && pos >= 0 && pos < w.n;
-    uint4 x[L::W];
-#pragma unroll
-    for (int j = 0; j < L::W; ++j)
-      x[j] = in ? __ldg(reinterpret_cast<const uint4*>(k_new + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 32 * j + 8 * t))
-                : make_uint4(0u, 0u, 0u, 0u);
-    Q4Words<L::W> out;
-    uint32_t sc = 0;
-#pragma unroll
-    for (int gr = 0; gr < L::G; ++gr) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 2 * gr; j < 2 * gr + 2; ++j) m = abs_max2(abs_max2(abs_max2(abs_max2(m, x[j].x), x[j].y), x[j].z), x[j].w);
-      m = fold2(m);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const uint32_t sb = scale_bits(m);
-      sc |= sb << (16 * gr);
-      const float s = __uint_as_float(sb << 16);
-      const bool plain = plain_scale(sb);
-#pragma unroll
-      for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
-        const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        uint32_t word = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          word |= code(lo_f(xs[q]), s, plain) << (4 * q) | code(hi_f(xs[q]), s, plain) << (4 * q + 16);
-        out.w[j] = word;
-      }
-    }
-    if (in) {
-      q4_store<L::W>(blk + tk * (D / 2) + t * (4 * L::W), out);
-      if (t == 0) q4_store_scales<L::G>(blk + L::kKs + tk * 2 * L::G, sc);
-    }
-  }
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    // values: lane (g, t) has the dims 32 m + 4 g + 0..3 of the positions 8 half + 2 t and the one after it
-    Q4Words<L::W> out;
-#pragma unroll
-    for (int m = 0; m < L::W; ++m) out.w[m] = 0;
-    bool in[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int tk = 8 * half + 2 * t + e, pos = pos0 + tk;
-      in[e] = pos >= w.p0 && pos >= 0 && pos < w.n;
-      uint2 x[L::W];
-#pragma unroll
-      for (int m = 0; m < L::W; ++m)
-        x[m] = in[e] ? __ldg(reinterpret_cast<const uint2*>(v_new + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 32 * m + 4 * g))
-                     : make_uint2(0u, 0u);
-      uint32_t sc = 0;
-#pragma unroll
-      for (int gr = 0; gr < L::G; ++gr) {
-        uint32_t a = 0;
-#pragma unroll
-        for (int m = 2 * gr; m < 2 * gr + 2; ++m) a = abs_max2(abs_max2(a, x[m].x), x[m].y);
-        a = fold2(a);
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 4));
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 16));
-        const uint32_t sb = scale_bits(a);
-        sc |= sb << (16 * gr);
-        const float s = __uint_as_float(sb << 16);
-        const bool plain = plain_scale(sb);
-#pragma unroll
-        for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
-          const uint32_t c = code(lo_f(x[m].x), s, plain) | code(hi_f(x[m].x), s, plain) << 4 |
-                             code(lo_f(x[m].y), s, plain) << 8 | code(hi_f(x[m].y), s, plain) << 12;
-          out.w[m] |= c << (16 * e);
-        }
-      }
-      if (in[e] && g == 0) q4_store_scales<L::G>(blk + L::kVs + tk * 2 * L::G, sc);
-    }
-    uint8_t* at = blk + L::kV + (half * 32 + lane) * (4 * L::W);
-    if (in[0] && in[1]) {
-      q4_store<L::W>(at, out);
-    } else if (in[0] || in[1]) {
-#pragma unroll
-      for (int m = 0; m < L::W; ++m)
-        *reinterpret_cast<uint16_t*>(at + 4 * m + (in[1] ? 2 : 0)) =
-            static_cast<uint16_t>(in[1] ? out.w[m] >> 16 : out.w[m] & 0xFFFFu);
-    }
+  const size_t row = (size_t)p.nkv * D;
+  const bf16* src = (part < 2 ? k_new : v_new) + (long long)w.b * p.Q * row + (long long)(pos0 - w.p0) * row + w.h * D;
+  if (part < 2) {
+    const int g = lane >> 2, pos = pos0 + g;
+    append_keys<D>(src + g * (long long)row, pos >= w.p0 && pos < w.n, blk, 8 * half + g, lane & 3);
+  } else {
+    const int pos = pos0 + 2 * (lane & 3);
+    const bool in[2] = {pos >= w.p0 && pos < w.n, pos + 1 >= w.p0 && pos + 1 < w.n};
+    append_values<D>(src + (pos - pos0) * (long long)row, row, in, blk, half, lane);
   }
 }
 
@@ -203,63 +228,54 @@ __global__ void __launch_bounds__(kQwWarps * 32) q4_read_kernel(const uint8_t* _
   using L = Q4Block<D>;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int unit = blockIdx.x * kQwWarps + (threadIdx.x >> 5);
-  if (unit >= p.B * p.nblk * p.nkv) return;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, half = part & 1, g = lane >> 2, t = lane & 3;
   QwPlace w;
   bool bad;
-  const bool there = place(p, unit, &w, &bad);
-  if (bad && lane == 0) set_error(p.err, kErrDeviceIndex);
+  const bool there = place(p, blockIdx.x, &w, &bad);
+  if (bad && threadIdx.x == 0) set_error(p.err, kErrDeviceIndex);
   // a bad length: the rows are zeros, laid out as if the last position were the last of a block
   if (w.n < 0 || w.n > (p.M << p.page_shift)) {
     w.n = p.nblk << 4;
     w.p0 = w.n - p.Q;
-    w.block = q4_floor_block(w.p0) + (unit / p.nkv) % p.nblk;
+    w.block = q4_floor_block(w.p0) + (blockIdx.x / p.nkv) % p.nblk;
   }
   const uint8_t* blk = pool + (there ? w.at * L::kBytes : 0);
-  const int pos0 = w.block * 16;
-  const size_t row0 = (size_t)w.b * p.Q;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int tk = 8 * half + g, pos = pos0 + tk;
-    if (pos >= w.p0 && pos < w.n) {
-      uint4* dst = reinterpret_cast<uint4*>(k_out + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 8 * t);
-      if (!there) {
-#pragma unroll
-        for (int j = 0; j < L::W; ++j) dst[4 * j] = make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        const Q4Words<L::W> c = q4_load<L::W>(blk + tk * (D / 2) + t * (4 * L::W));
-        const uint32_t sc = q4_load_scales<L::G>(blk + L::kKs + tk * 2 * L::G);
-#pragma unroll
-        for (int j = 0; j < L::W; ++j) {
-          const float s = q4_scale(sc, j >> 1);
-          uint32_t v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = value2((c.w[j] >> (4 * q)) & 15u, (c.w[j] >> (4 * q + 16)) & 15u, s);
-          dst[4 * j] = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-      }
+  const int pos0 = w.block * 16 + 8 * half;
+  const size_t row = (size_t)p.nkv * D;
+  bf16* out = (part < 2 ? k_out : v_out) + (long long)w.b * p.Q * row + (long long)(pos0 - w.p0) * row + w.h * D;
+  if (part < 2) {
+    const int pos = pos0 + g, tk = 8 * half + g;
+    if (pos < w.p0 || pos >= w.n) return;
+    uint4* dst = reinterpret_cast<uint4*>(out + g * (long long)row + 8 * t);
+    Q4Words<L::W> c = {};
+    uint32_t sc = 0;  // scale 0: zeros
+    if (there) {
+      c = q4_load<L::W>(blk + tk * (D / 2) + t * (4 * L::W));
+      sc = q4_load_scales<L::G>(blk + L::kKs + tk * 2 * L::G);
     }
-  }
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    Q4Words<L::W> c;
+    for (int j = 0; j < L::W; ++j) {
+      const float s = q4_scale(sc, j >> 1);
+      uint32_t v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = there ? value2((c.w[j] >> (4 * q)) & 15u, (c.w[j] >> (4 * q + 16)) & 15u, s) : 0u;
+      dst[4 * j] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  } else {
+    Q4Words<L::W> c = {};
     if (there) c = q4_load<L::W>(blk + L::kV + (half * 32 + lane) * (4 * L::W));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int tk = 8 * half + 2 * t + e, pos = pos0 + tk;
+      const int pos = pos0 + 2 * t + e;
       if (pos < w.p0 || pos >= w.n) continue;
-      uint2* dst = reinterpret_cast<uint2*>(v_out + ((row0 + (pos - w.p0)) * p.nkv + w.h) * D + 4 * g);
-      const uint32_t sc = there ? q4_load_scales<L::G>(blk + L::kVs + tk * 2 * L::G) : 0u;
+      uint2* dst = reinterpret_cast<uint2*>(out + (2 * t + e) * (long long)row + 4 * g);
+      const uint32_t sc = there ? q4_load_scales<L::G>(blk + L::kVs + (8 * half + 2 * t + e) * 2 * L::G) : 0u;
 #pragma unroll
       for (int m = 0; m < L::W; ++m) {
-        if (!there) {
-          dst[8 * m] = make_uint2(0u, 0u);
-          continue;
-        }
         const uint32_t x = c.w[m] >> (16 * e);
         const float s = q4_scale(sc, m >> 1);
-        dst[8 * m] = make_uint2(value2(x & 15u, (x >> 4) & 15u, s), value2((x >> 8) & 15u, (x >> 12) & 15u, s));
+        dst[8 * m] = there ? make_uint2(value2(x & 15u, (x >> 4) & 15u, s), value2((x >> 8) & 15u, (x >> 12) & 15u, s))
+                           : make_uint2(0u, 0u);
       }
     }
   }
@@ -303,7 +319,7 @@ lsv_status prepare(const void* a, const void* b, const void* pool, const int32_t
   p->page_shift = log2i(page);
   p->nblk = (int)nblk;
   p->err = dc->err;
-  *grid = (int)((units + kQwWarps - 1) / kQwWarps);
+  *grid = (int)units;
   return LSV_OK;
 }
 
