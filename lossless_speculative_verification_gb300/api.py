@@ -255,10 +255,8 @@ def spec_q4_read(pool, table, ctx_len, N, nkv, d, page, k=None, v=None, stream=N
     dev = torch.cuda.current_device()
     B = table.shape[0]
     M, P = _q4_sizes(pool, table, ctx_len, B, nkv, d, page)
-    if k is None or v is None:
-        # one allocation for what is missing
-        both = torch.empty(((k is None) + (v is None), B, N, nkv, d), dtype=torch.bfloat16, device=pool.device)
-        k, v = both[0] if k is None else k, both[-1] if v is None else v
+    k = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device) if k is None else k
+    v = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device) if v is None else v
     _need_shape(k, (B, N, nkv, d), "k"); _need_shape(v, (B, N, nkv, d), "v")
     pl, tb, cl, kp, vp = _here(dev, (pool, torch.uint8, "pool"), (table, torch.int32, "table"),
                                (ctx_len, torch.int32, "ctx_len"), (k, torch.bfloat16, "k"), (v, torch.bfloat16, "v"))

@@ -28,6 +28,7 @@ constexpr int kPgChunk = 4096;  // pages a CTA reduces
 constexpr int kPgChunkWords = kPgChunk / 32;
 constexpr int kPgMaxPages = 1 << 24;
 constexpr int kPgMaxRows = 1 << 16;
+constexpr int kPgDeep = 4;      // entries of a row a thread has in flight
 constexpr int kPgCopyBytes = 16384;  // bytes a CTA copies at a time
 
 struct PgWs {
@@ -115,6 +116,15 @@ __device__ __forceinline__ int sum_upto(const int* a, int n, int upto, int* part
   return block_sum(all, tmp);
 }
 
+// The counts of chunk c, all loads in flight together: refs[k] of lane l is page 32 (warp + k kPgWarps) + l of it.
+__device__ __forceinline__ void load_chunk(const int32_t* ref, int P, int c, int (&refs)[kPgChunkWords / kPgWarps]) {
+#pragma unroll
+  for (int k = 0; k < kPgChunkWords / kPgWarps; ++k) {
+    const int at = c * kPgChunk + 32 * ((int)(threadIdx.x >> 5) + k * kPgWarps) + (int)(threadIdx.x & 31);
+    refs[k] = at < P ? __ldcg(ref + at) : -1;
+  }
+}
+
 // What a turn does with entry i of a row: keep it, give it a new page, copy the old one into the new one.
 struct Entry {
   bool held, fresh, copied, gone;
@@ -155,10 +165,11 @@ __global__ void __launch_bounds__(kPgThreads) resize_count_kernel(const PgResize
     if (p.stats && threadIdx.x < 4) p.stats[threadIdx.x] = 0;
   }
   if (c < p.chunks) {
-    int n = 0;
-    for (int i = warp; i < kPgChunkWords; i += kPgWarps) {
-      const int at = c * kPgChunk + 32 * i + lane;
-      const int r = at < p.P ? __ldcg(p.ref + at) : -1;
+    int n = 0, refs[kPgChunkWords / kPgWarps];
+    load_chunk(p.ref, p.P, c, refs);
+#pragma unroll
+    for (int k = 0; k < kPgChunkWords / kPgWarps; ++k) {
+      const int i = warp + k * kPgWarps, at = c * kPgChunk + 32 * i + lane, r = refs[k];
       const uint32_t free = __ballot_sync(0xffffffffu, at < p.P && r <= 0), shared = __ballot_sync(0xffffffffu, r > 1);
       if (lane == 0) {
         p.w.bits[c * kPgChunkWords + i] = free;
@@ -173,13 +184,24 @@ __global__ void __launch_bounds__(kPgThreads) resize_count_kernel(const PgResize
   if (c < p.B) {
     int keep, cap, n = 0;
     if (row_bounds(p, c, &keep, &cap)) {
-      for (int i = threadIdx.x; i < p.M; i += kPgThreads) {
-        const int pg = __ldcg(p.table + (size_t)c * p.M + i);
-        const bool held = pg >= 0 && pg < p.P;
-        if (pg < -1 || pg >= p.P || (!held && i < (keep + p.page - 1) / p.page)) set_error(p.err, kErrDeviceIndex);
-        const int r = held ? __ldcg(p.ref + pg) : 0;
-        if (held && r <= 0) set_error(p.err, kErrDeviceIndex);  // held, and counted free
-        n += entry_of(i, held, r > 1, keep, cap, p.page).fresh;
+      for (int i0 = 0; i0 < p.M; i0 += kPgThreads * kPgDeep) {
+        int pg[kPgDeep], r[kPgDeep];
+#pragma unroll
+        for (int k = 0; k < kPgDeep; ++k) {
+          const int i = i0 + k * kPgThreads + threadIdx.x;
+          pg[k] = i < p.M ? __ldcg(p.table + (size_t)c * p.M + i) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kPgDeep; ++k) r[k] = pg[k] >= 0 && pg[k] < p.P ? __ldcg(p.ref + pg[k]) : 0;
+#pragma unroll
+        for (int k = 0; k < kPgDeep; ++k) {
+          const int i = i0 + k * kPgThreads + threadIdx.x;
+          if (i >= p.M) continue;
+          const bool held = pg[k] >= 0 && pg[k] < p.P;
+          if (pg[k] < -1 || pg[k] >= p.P || (!held && i < (keep + p.page - 1) / p.page)) set_error(p.err, kErrDeviceIndex);
+          if (held && r[k] <= 0) set_error(p.err, kErrDeviceIndex);  // held, and counted free
+          n += entry_of(i, held, r[k] > 1, keep, cap, p.page).fresh;
+        }
       }
     } else if (threadIdx.x == 0) {
       set_error(p.err, kErrDeviceIndex);
@@ -241,32 +263,56 @@ __global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResiz
     __syncthreads();
   }
   const uint32_t* shared = p.w.bits + (size_t)p.chunks * kPgChunkWords;
+  __shared__ int fresh_s[kPgDeep][kPgWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int given = 0, gone = 0;
-  for (int i0 = 0; i0 < p.M; i0 += kPgThreads) {
-    const int i = i0 + threadIdx.x;
-    const int pg = i < p.M ? __ldcg(row + i) : -1;
-    const bool held = pg >= 0 && pg < p.P;
-    Entry e = entry_of(i, held, held && (__ldcg(shared + (pg >> 5)) >> (pg & 31) & 1u), keep, cap, p.page);
-    if (i >= p.M) e.fresh = e.gone = e.copied = false;
-    int all;
-    const int rank = given + block_prefix(e.fresh, tmp, &all);
-    given += all;
-    if (i >= p.M) continue;
-    int to = held && !e.gone ? pg : -1;
-    if (e.fresh) {
-      to = fresh[rank];
-      atomicAdd(p.ref_out + to, 1);
-      if (e.copied) {
-        const int k = atomicAdd(p.w.count, 1);  // any order: the copies are apart
-        p.w.src[k] = pg;
-        p.w.list2[k] = to;
+  for (int i0 = 0; i0 < p.M; i0 += kPgThreads * kPgDeep) {
+    int pg[kPgDeep];
+    uint32_t bit[kPgDeep], ballot[kPgDeep];
+    Entry e[kPgDeep];
+#pragma unroll
+    for (int k = 0; k < kPgDeep; ++k) {
+      const int i = i0 + k * kPgThreads + threadIdx.x;
+      pg[k] = i < p.M ? __ldcg(row + i) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kPgDeep; ++k) bit[k] = pg[k] >= 0 && pg[k] < p.P ? __ldcg(shared + (pg[k] >> 5)) >> (pg[k] & 31) & 1u : 0u;
+    __syncthreads();  // the last round's counts are read
+#pragma unroll
+    for (int k = 0; k < kPgDeep; ++k) {
+      const int i = i0 + k * kPgThreads + threadIdx.x;
+      e[k] = entry_of(i, pg[k] >= 0 && pg[k] < p.P, bit[k], keep, cap, p.page);
+      if (i >= p.M) e[k].fresh = e[k].gone = e[k].copied = false;
+      ballot[k] = __ballot_sync(0xffffffffu, e[k].fresh);
+      if (lane == 0) fresh_s[k][warp] = __popc(ballot[k]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPgDeep; ++k) {
+      const int i = i0 + k * kPgThreads + threadIdx.x;
+      int rank = given + __popc(ballot[k] & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kPgWarps; ++w) {
+        if (w < warp) rank += fresh_s[k][w];
+        given += fresh_s[k][w];
       }
+      if (i >= p.M) continue;
+      int to = e[k].held && !e[k].gone ? pg[k] : -1;
+      if (e[k].fresh) {
+        to = fresh[rank];
+        atomicAdd(p.ref_out + to, 1);
+        if (e[k].copied) {
+          const int at = atomicAdd(p.w.count, 1);  // any order: the copies are apart
+          p.w.src[at] = pg[k];
+          p.w.list2[at] = to;
+        }
+      }
+      if (e[k].gone) {
+        atomicSub(p.ref_out + pg[k], 1);
+        ++gone;
+      }
+      out[i] = to;
     }
-    if (e.gone) {
-      atomicSub(p.ref_out + pg, 1);
-      ++gone;
-    }
-    out[i] = to;
   }
   if (p.stats) {
     gone = block_sum(gone, tmp);
@@ -346,6 +392,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_rows_kernel(const PgFork p) {
   const bool has = from >= 0 && from < p.B;
   if ((from < -1 || from >= p.B) && threadIdx.x == 0) set_error(p.err, kErrDeviceIndex);
   const int32_t* table = p.table_out == p.table ? p.old : p.table;
+#pragma unroll 4
   for (int i = threadIdx.x; i < p.M; i += kPgThreads) {
     const int mine = __ldcg(table + (size_t)b * p.M + i);
     if (mine >= 0 && mine < p.P) {
@@ -372,10 +419,12 @@ __global__ void __launch_bounds__(kPgThreads) compact_count_kernel(const PgCompa
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int n = 0;
-  for (int i = warp; i < kPgChunkWords; i += kPgWarps) {
-    const int at = c * kPgChunk + 32 * i + lane;
-    const uint32_t live = __ballot_sync(0xffffffffu, at < p.P && __ldcg(p.ref + at) > 0);
+  int n = 0, refs[kPgChunkWords / kPgWarps];
+  load_chunk(p.ref, p.P, c, refs);
+#pragma unroll
+  for (int k = 0; k < kPgChunkWords / kPgWarps; ++k) {
+    const int i = warp + k * kPgWarps;
+    const uint32_t live = __ballot_sync(0xffffffffu, refs[k] > 0);
     if (lane == 0) {
       p.w.bits[c * kPgChunkWords + i] = live;
       n += __popc(live);
