@@ -11,6 +11,8 @@
 // touch each other's bytes.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "lsv.h"
 #include "ptx.cuh"
@@ -26,52 +28,48 @@ constexpr uint32_t kSmallScale = 0x0D80u;  // 2^-100 in bf16
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t v) { return __vmaxu2(m, v & 0x7FFF7FFFu); }
 __device__ __forceinline__ uint32_t fold2(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
 
-// bf16 bits of s = bf16(amax / 7).  amax / 7 in fp32 rounded again to bf16 is the correctly rounded
-// quotient: with 8 significant bits over 7 it never comes near the middle of two bf16 values.
+// bf16 bits of s = bf16(amax / 7).  With 8 significant bits over 7 the quotient is never within 2^-12 of the
+// middle of two bf16 values, so amax * (1 / 7) in fp32, rounded again, is the correctly rounded one.
 __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
   if (amax >= 0x7F80u) return kQ4NanScale;
-  const float q = __fdiv_rn(__uint_as_float(amax << 16), 7.0f);
-  return __bfloat16_as_ushort(__float2bfloat16_rn(q));
+  return __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(amax << 16) * (1.0f / 7.0f)));
 }
 
-// A group's scale and the nibbles by it: rint(x / s) + 8, ties to even.
-// x and s have 8 significant bits each, so x / s is a half, or at least 2^-13 of itself away from one, and
-// x * (1 / s), 2^-23 off, falls on the right side of it.  A half itself may not: the rest x - n s is exact, and
-// where it is half a step and n odd, the neighbour on the rest's side is the even one.  Adding 1.5 * 2^23 rounds
-// to a whole number on the FMA pipe (conversions run at an eighth of its rate: 28 us for eight prompts of 1156
-// positions with them, 19 us without).
+// A group's scale and the whole numbers by it: n = rint(x / s), ties to even.
+// x * (1 / s) may be off by an ulp or two; the rest x - q s is exact (q and s have 32 bits together, and the rest
+// few), and rest / s added to q rounds to x / s, exactly where that is a half (one correction of a quotient by its
+// remainder, as Markstein describes).  Adding 1.5 * 2^23 then rounds to even.  All of it runs on the FMA pipe:
+// with conversions the append of eight prompts of 1156 positions took 24 us, with a test for ties 19 us.
 struct Step {
   uint32_t bits;
-  float s, inv, half;
+  float s, inv;
 };
 constexpr float kRound = 12582912.0f;
 __device__ __forceinline__ Step step_of(uint32_t bits) {
   Step r;
   r.bits = bits;
-  // a scale of 0 or NaN: n = 0 for all; below 2^-100, see codes4
-  const bool plain = bits >= kSmallScale && bits < 0x7F80u;
   r.s = __uint_as_float(bits << 16);
-  r.inv = plain ? __frcp_rn(r.s) : 0.0f;
-  r.half = plain ? 0.5f * r.s : -1.0f;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.inv) : "f"(r.s));
   return r;
 }
 __device__ __forceinline__ float whole(const Step& r, float x) {
-  const float t = fmaf(x, r.inv, kRound);
-  float n = t - kRound;
-  const float rest = fmaf(-n, r.s, x);
-  if (fabsf(rest) == r.half && (__float_as_uint(t) & 1u)) n += copysignf(1.0f, rest);
-  return n;
+  float q = x * r.inv;
+  q = fmaf(fmaf(-q, r.s, x), r.inv, q);
+  return (q + kRound) - kRound;
 }
-// The nibbles of four values in 16 bits, the first in the lowest place.
+// Scales that 1 / s and 7 steps do for.
+__device__ __forceinline__ bool plain_scale(uint32_t bits) { return bits >= kSmallScale && bits < 0x7F80u; }
+
+// The nibbles of four values in 16 bits, the first in the lowest place.  kPlain: the scale is plain.
+template <bool kPlain>
 __device__ __forceinline__ uint32_t codes4(const Step& r, float x0, float x1, float x2, float x3) {
-  const bool plain = r.bits >= kSmallScale && r.bits < 0x7F80u;
-  if (!plain) {
-    // infinite products and NaN would not be 0 times what they are; small scales, whose reciprocal may overflow
-    // and whose rounding may leave more than 7 steps, divide
+  if (!kPlain && !plain_scale(r.bits)) {
+    // a scale of 0 or NaN: n = 0 for all; small scales, whose reciprocal may overflow and whose own rounding may
+    // leave more than 7 steps, divide
     if (r.bits == 0u || r.bits >= 0x7F80u) return 0x8888u;
     const float x[4] = {x0, x1, x2, x3};
     uint32_t v = 0;
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < 4; ++i)
       v |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x[i], r.s)), -8.0f), 7.0f)) + 8) << (4 * i);
     return v;
@@ -133,6 +131,8 @@ __device__ __forceinline__ void append_keys(const bf16* __restrict__ src, bool i
     x[j] = in ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * t)) : make_uint4(0u, 0u, 0u, 0u);
   Q4Words<L::W> out;
   uint32_t sc = 0;
+  Step st[L::G];
+  bool plain = true;
 #pragma unroll
   for (int gr = 0; gr < L::G; ++gr) {
     uint32_t m = 0;
@@ -141,14 +141,20 @@ __device__ __forceinline__ void append_keys(const bf16* __restrict__ src, bool i
     m = fold2(m);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const Step s = step_of(scale_bits(m));
-    sc |= s.bits << (16 * gr);
-#pragma unroll
-    for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
-      out.w[j] = codes4(s, lo_f(x[j].x), lo_f(x[j].y), lo_f(x[j].z), lo_f(x[j].w)) |
-                 codes4(s, hi_f(x[j].x), hi_f(x[j].y), hi_f(x[j].z), hi_f(x[j].w)) << 16;
-    }
+    st[gr] = step_of(scale_bits(m));
+    sc |= st[gr].bits << (16 * gr);
+    plain = plain && plain_scale(st[gr].bits);
   }
+  auto words = [&](auto tag) {
+#pragma unroll
+    for (int j = 0; j < L::W; ++j)
+      out.w[j] = codes4<decltype(tag)::value>(st[j >> 1], lo_f(x[j].x), lo_f(x[j].y), lo_f(x[j].z), lo_f(x[j].w)) |
+                 codes4<decltype(tag)::value>(st[j >> 1], hi_f(x[j].x), hi_f(x[j].y), hi_f(x[j].z), hi_f(x[j].w)) << 16;
+  };
+  if (__all_sync(0xffffffffu, plain || !in))  // (positions that are not there are not stored)
+    words(std::true_type{});
+  else
+    words(std::false_type{});
   if (in) {
     q4_store<L::W>(blk + tk * (D / 2) + t * (4 * L::W), out);
     if (t == 0) q4_store_scales<L::G>(blk + L::kKs + tk * 2 * L::G, sc);
@@ -168,8 +174,8 @@ __device__ __forceinline__ void append_values(const bf16* __restrict__ src, size
     for (int m = 0; m < L::W; ++m)
       x[e][m] = in[e] ? __ldg(reinterpret_cast<const uint2*>(src + e * row + 32 * m + 4 * g)) : make_uint2(0u, 0u);
   Q4Words<L::W> out;
-#pragma unroll
-  for (int m = 0; m < L::W; ++m) out.w[m] = 0;
+  Step st[2][L::G];
+  bool plain = true;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     uint32_t sc = 0;
@@ -182,14 +188,23 @@ __device__ __forceinline__ void append_values(const bf16* __restrict__ src, size
       a = max(a, __shfl_xor_sync(0xffffffffu, a, 4));
       a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
       a = max(a, __shfl_xor_sync(0xffffffffu, a, 16));
-      const Step s = step_of(scale_bits(a));
-      sc |= s.bits << (16 * gr);
-#pragma unroll
-      for (int m = 2 * gr; m < 2 * gr + 2; ++m)
-        out.w[m] |= codes4(s, lo_f(x[e][m].x), hi_f(x[e][m].x), lo_f(x[e][m].y), hi_f(x[e][m].y)) << (16 * e);
+      st[e][gr] = step_of(scale_bits(a));
+      sc |= st[e][gr].bits << (16 * gr);
+      plain = plain && (plain_scale(st[e][gr].bits) || !in[e]);
     }
     if (in[e] && g == 0) q4_store_scales<L::G>(blk + L::kVs + (8 * half + 2 * t + e) * 2 * L::G, sc);
   }
+  auto words = [&](auto tag) {
+    constexpr bool kPlain = decltype(tag)::value;
+#pragma unroll
+    for (int m = 0; m < L::W; ++m)
+      out.w[m] = codes4<kPlain>(st[0][m >> 1], lo_f(x[0][m].x), hi_f(x[0][m].x), lo_f(x[0][m].y), hi_f(x[0][m].y)) |
+                 codes4<kPlain>(st[1][m >> 1], lo_f(x[1][m].x), hi_f(x[1][m].x), lo_f(x[1][m].y), hi_f(x[1][m].y)) << 16;
+  };
+  if (__all_sync(0xffffffffu, plain))
+    words(std::true_type{});
+  else
+    words(std::false_type{});
   uint8_t* at = blk + L::kV + (half * 32 + lane) * (4 * L::W);
   if (in[0] && in[1]) {
     q4_store<L::W>(at, out);
@@ -233,10 +248,12 @@ __global__ void __launch_bounds__(kQwWarps * 32) q4_append_kernel(const bf16* __
   }
 }
 
-// (n - 8) s of two nibbles as packed bf16: the product has at most 12 bits, so fp32 holds it and one
-// rounding to bf16 remains.
-__device__ __forceinline__ uint32_t value2(uint32_t lo, uint32_t hi, float s) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn((static_cast<int>(lo) - 8) * s, (static_cast<int>(hi) - 8) * s);
+// (n - 8) s of the nibbles in bits 0..3 and 16..19, by the scales in the halves of s: as bf16, 128 + n' is the
+// nibble beneath an exponent, less 136 is exact, and the product is rounded once.
+__device__ __forceinline__ uint32_t value2(uint32_t w, uint32_t s) {
+  const uint32_t b = (w & 0x000F000Fu) | 0x43004300u, o = 0x43084308u;
+  const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&o)),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&s));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -266,35 +283,39 @@ __global__ void __launch_bounds__(kQwWarps * 32) q4_read_kernel(const uint8_t* _
     if (pos < w.p0 || pos >= w.n) return;
     uint4* dst = reinterpret_cast<uint4*>(out + g * (long long)row + 8 * t);
     Q4Words<L::W> c = {};
-    uint32_t sc = 0;  // scale 0: zeros
+    uint32_t sc = 0;
     if (there) {
       c = q4_load<L::W>(blk + tk * (D / 2) + t * (4 * L::W));
       sc = q4_load_scales<L::G>(blk + L::kKs + tk * 2 * L::G);
     }
 #pragma unroll
     for (int j = 0; j < L::W; ++j) {
-      const float s = q4_scale(sc, j >> 1);
-      uint32_t v[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = there ? value2((c.w[j] >> (4 * q)) & 15u, (c.w[j] >> (4 * q + 16)) & 15u, s) : 0u;
-      dst[4 * j] = make_uint4(v[0], v[1], v[2], v[3]);
+      const uint32_t s = __byte_perm(sc, 0, (j >> 1) ? 0x3232 : 0x1010);
+      dst[4 * j] = there ? make_uint4(value2(c.w[j], s), value2(c.w[j] >> 4, s), value2(c.w[j] >> 8, s), value2(c.w[j] >> 12, s))
+                         : make_uint4(0u, 0u, 0u, 0u);
     }
   } else {
     Q4Words<L::W> c = {};
-    if (there) c = q4_load<L::W>(blk + L::kV + (half * 32 + lane) * (4 * L::W));
+    uint32_t sc[2] = {0u, 0u};
+    if (there) {
+      c = q4_load<L::W>(blk + L::kV + (half * 32 + lane) * (4 * L::W));
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int pos = pos0 + 2 * t + e;
-      if (pos < w.p0 || pos >= w.n) continue;
-      uint2* dst = reinterpret_cast<uint2*>(out + (2 * t + e) * (long long)row + 4 * g);
-      const uint32_t sc = there ? q4_load_scales<L::G>(blk + L::kVs + (8 * half + 2 * t + e) * 2 * L::G) : 0u;
+      for (int e = 0; e < 2; ++e) sc[e] = q4_load_scales<L::G>(blk + L::kVs + (8 * half + 2 * t + e) * 2 * L::G);
+    }
+    const int pos = pos0 + 2 * t;
+    const bool in[2] = {pos >= w.p0 && pos < w.n, pos + 1 >= w.p0 && pos + 1 < w.n};
+    uint2* dst = reinterpret_cast<uint2*>(out + (2 * t) * (long long)row + 4 * g);
 #pragma unroll
-      for (int m = 0; m < L::W; ++m) {
-        const uint32_t x = c.w[m] >> (16 * e);
-        const float s = q4_scale(sc, m >> 1);
-        dst[8 * m] = there ? make_uint2(value2(x & 15u, (x >> 4) & 15u, s), value2((x >> 8) & 15u, (x >> 12) & 15u, s))
-                           : make_uint2(0u, 0u);
-      }
+    for (int m = 0; m < L::W; ++m) {
+      // both positions at a time, then apart
+      const uint32_t s = __byte_perm(sc[0], sc[1], (m >> 1) ? 0x7632 : 0x5410);
+      uint32_t v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = there ? value2(c.w[m] >> (4 * q), s) : 0u;
+      if (in[0]) dst[8 * m] = make_uint2(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410));
+      if (in[1])
+        *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(dst + 8 * m) + row) =
+            make_uint2(__byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
     }
   }
 }
