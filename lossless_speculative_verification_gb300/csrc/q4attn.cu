@@ -86,7 +86,7 @@ struct QaSmem {
   static constexpr int kWarp = kRing > kMl + kRows * 8 ? kRing : (kMl + kRows * 8 + 15) / 16 * 16;
   static constexpr int kQ = kQaWarps * (kWarp + S * 8 + S * 4) + 15 & ~15;  // byte offset of the queries
   static constexpr int kQf = 0;                               // [NT][W][lane] 16 bytes: the B operands
-  static constexpr int kCi = kQf + NT * L::W * 512;           // [NT][G][t] 16 bytes: where the accumulators start
+  static constexpr int kCi = kQf + NT * L::W * 512;           // [G][4 or 8] 16 bytes: where the accumulators start
   static constexpr int kFq = kCi + NT * L::G * 64;            // [8 NT] what turns the scaled sums into log2 scores
   static constexpr int kLim = kFq + kRows * 4;                // [8 NT] last position the row sees
   static constexpr int kTotal = kQ + kLim + kRows * 4;
@@ -211,9 +211,10 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     for (int gr = 0; gr < G; ++gr) {
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
       sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
-      // the accumulators of the columns 2t', 2t' + 1 start at -8 * 2^-24 * sum of the group's queries
-      float* ci = reinterpret_cast<float*>(qs + SM::kCi + ((warp * G + gr) * 4 + (g >> 1)) * 16);
-      if (t < 2) ci[2 * t + (g & 1)] = sum[gr] * (-8.0f / 16777216.0f);
+      // the accumulators start at -8 * 2^-24 * sum of the group's queries: those of the columns 2t', 2t' + 1 twice
+      // (NT = 1), or of the row g and the row g + 8 twice each
+      float* ci = reinterpret_cast<float*>(qs + SM::kCi + (NT == 1 ? gr * 4 + (g >> 1) : gr * 8 + g) * 16);
+      if (t < 2) ci[NT == 1 ? 2 * t + (g & 1) : 2 * warp + t] = sum[gr] * (-8.0f / 16777216.0f);
     }
     if (t == 0) {
       reinterpret_cast<float*>(qs + SM::kFq)[qr] =
@@ -222,189 +223,228 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     }
   }
   __syncthreads();
-  float fq[NT][2];  // of this lane's columns 2t, 2t + 1
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float2 v = *reinterpret_cast<const float2*>(qs + SM::kFq + (8 * nt + 2 * t) * 4);
-    fq[nt][0] = v.x;
-    fq[nt][1] = v.y;
-  }
+  // this lane's two rows: the columns 2t, 2t + 1 (NT = 1), or the rows g and g + 8
+  const int row_a = NT == 1 ? 2 * t : g, row_b = NT == 1 ? 2 * t + 1 : g + 8;
+  const float fq[2] = {*reinterpret_cast<const float*>(qs + SM::kFq + row_a * 4),
+                       *reinterpret_cast<const float*>(qs + SM::kFq + row_b * 4)};
 
-  float o[NT][2 * W][4];  // tiles of 16 dims: rows g (even places) and g + 8 (odd places), columns 2t, 2t + 1
-  float cs[NT][G][4];     // sum of P s of every group (columns 2t, 2t + 1; the rest stays 0)
-  float m_run[NT][2], l_run[NT][2], base[NT][2];  // base: what P is 2^0 at
+  // NT = 1: tiles of 16 dims, rows g (even places) and g + 8 (odd places), columns 2t, 2t + 1 the query rows.
+  // NT = 2: tiles of 8 dims, [4 m + place] column c the dim 32 m + 4 c + place, rows g and g + 8 the query rows.
+  constexpr int kTiles = NT == 1 ? 2 * W : 4 * W;
+  float o[kTiles][4];
+  float cs[G][4];  // sum of P s of every group
+  float m_run[2] = {-INFINITY, -INFINITY}, base[2] = {0.0f, 0.0f};  // base: what P is 2^0 at
+  float l_run[2][NT] = {};  // sums of P over this lane's positions (NT = 2: the even and the odd ones apart, so
+                            // that both forms add in the same order)
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-    for (int i = 0; i < 2 * W; ++i)
+    for (int c = 0; c < 4; ++c) o[i][c] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.0f;
+  for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-      for (int gr = 0; gr < G; ++gr) cs[nt][gr][c] = cs[nt][gr][c + 2] = 0.0f;
-      m_run[nt][c] = -INFINITY;
-      l_run[nt][c] = base[nt][c] = 0.0f;
-    }
-  }
+    for (int c = 0; c < 4; ++c) cs[gr][c] = 0.0f;
 
   // One step: the U blocks of a stage from position pos0 on.  Masked: some row does not see all of it, or a
-  // block is not there.
+  // block is not there.  Element c of the scores' tile (u, e): NT = 1 (e = 0): position g + 8 (c / 2) and row
+  // c % 2; NT = 2: position 8 e + 2t + c % 2 and row c / 2, of this lane's.
   auto step = [&](auto tag, const uint8_t* blk, int pos0, int gone) {
     constexpr bool kMasked = decltype(tag)::value;
-    Q4Words<W> kw[U][2];
-    uint32_t ks[U][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        kw[u][e] = q4_load<W>(blk + u * L::kBytes + (32 * e + lane) * (4 * W));
-        ks[u][e] = q4_load_scales<G>(blk + u * L::kBytes + L::kKs + (g + 8 * e) * 2 * G);
-      }
+    auto row_of = [](int c) { return NT == 1 ? (c & 1) : (c >> 1); };
     // ---- scores, before the row's factor
     float x[U][NT][4];
+    {
+      Q4Words<W> kw[U][2];
+      uint32_t ks[U][2][G == 2 ? 2 : 1];  // scales of this lane's positions: G = 2 [position], G = 1 both in one
 #pragma unroll
-    for (int gr = 0; gr < G; ++gr) {
-      float start[NT][4];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float4 v = *reinterpret_cast<const float4*>(qs + SM::kCi + ((nt * G + gr) * 4 + t) * 16);
-        start[nt][0] = v.x, start[nt][1] = v.y, start[nt][2] = v.z, start[nt][3] = v.w;
-      }
-      float acc[U][NT][4];
-#pragma unroll
-      for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
-        uint4 qf[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) qf[nt] = *reinterpret_cast<const uint4*>(qs + SM::kQf + ((nt * W + j) * 32 + lane) * 16);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t a = kw[u][0].w[j], c = kw[u][1].w[j], a8 = a >> 8, c8 = c >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_m16n8k16(acc[u][nt], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[nt].x,
-                             qf[nt].y, j == 2 * gr ? start[nt] : acc[u][nt]);
-            mma_f16_m16n8k16(acc[u][nt], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
-                             qf[nt].z, qf[nt].w, acc[u][nt]);
+        for (int e = 0; e < 2; ++e) {
+          const uint8_t* bk = blk + u * L::kBytes;
+          kw[u][e] = q4_load<W>(bk + (32 * e + lane) * (4 * W));
+          if constexpr (NT == 1) {
+            ks[u][e][0] = q4_load_scales<G>(bk + L::kKs + (g + 8 * e) * 2 * G);
+          } else if constexpr (G == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(bk + L::kKs + (8 * e + 2 * t) * 4);
+            ks[u][e][0] = v.x, ks[u][e][1] = v.y;
+          } else {
+            ks[u][e][0] = *reinterpret_cast<const uint32_t*>(bk + L::kKs + (8 * e + 2 * t) * 2);
           }
         }
-      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float s0 = q4_scale(ks[u][0], gr), s1 = q4_scale(ks[u][1], gr);
+      for (int gr = 0; gr < G; ++gr) {
+        const float4 sv = *reinterpret_cast<const float4*>(qs + SM::kCi + (NT == 1 ? gr * 4 + t : gr * 8 + g) * 16);
+        float start[4] = {sv.x, sv.y, sv.z, sv.w};
+        float acc[U][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
+          uint4 qf[NT];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            x[u][nt][c] = gr == 0 ? __fmul_rn(acc[u][nt][c], c < 2 ? s0 : s1)
-                                  : fmaf(acc[u][nt][c], c < 2 ? s0 : s1, x[u][nt][c]);
-      }
-    }
-    // ---- the online softmax
-    uint32_t hidden[NT];  // bit 4 u + c: row 2t + c % 2 does not see position g + 8 (c / 2) of block u
-    uint32_t big = 0;     // the largest value scale of the step
-    if (kMasked) {
+          for (int nt = 0; nt < NT; ++nt) qf[nt] = *reinterpret_cast<const uint4*>(qs + SM::kQf + ((nt * W + j) * 32 + lane) * 16);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        hidden[nt] = 0;
-        const int2 lim = *reinterpret_cast<const int2*>(qs + SM::kLim + (8 * nt + 2 * t) * 4);
+          for (int u = 0; u < U; ++u) {
+            if constexpr (NT == 1) {
+              const uint32_t a = kw[u][0].w[j], c = kw[u][1].w[j], a8 = a >> 8, c8 = c >> 8;
+              mma_f16_m16n8k16(acc[u][0], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[0].x,
+                               qf[0].y, j == 2 * gr ? start : acc[u][0]);
+              mma_f16_m16n8k16(acc[u][0], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
+                               qf[0].z, qf[0].w, acc[u][0]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t a = kw[u][e].w[j], a8 = a >> 8;
+                mma_f16_m16n8k16(acc[u][e], qf[0].x, qf[NT - 1].x, qf[0].y, qf[NT - 1].y, a & 0x000F000Fu,
+                                 a & 0x00F000F0u, j == 2 * gr ? start : acc[u][e]);
+                mma_f16_m16n8k16(acc[u][e], qf[0].z, qf[NT - 1].z, qf[0].w, qf[NT - 1].w, a8 & 0x000F000Fu,
+                                 a8 & 0x00F000F0u, acc[u][e]);
+              }
+            }
+          }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (pos0 + 16 * u + g + (c < 2 ? 0 : 8) > ((c & 1) ? lim.y : lim.x) || (gone >> u & 1)) hidden[nt] |= 1u << (4 * u + c);
+          for (int e = 0; e < NT; ++e)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float s = NT == 1 ? q4_scale(ks[u][c >> 1][0], gr)
+                                      : G == 2 ? q4_scale(ks[u][e][c & (G - 1)], gr) : q4_scale(ks[u][e][0], c & 1);
+              x[u][e][c] = gr == 0 ? __fmul_rn(acc[u][e][c], s) : fmaf(acc[u][e][c], s, x[u][e][c]);
+            }
       }
+    }
+    // ---- the online softmax
+    uint32_t hidden = 0;  // bit 8 u + 4 e + c: the row does not see the position
+    uint32_t big[2] = {0u, 0u};  // the largest value scale of the step, of what the row sees
+    if (kMasked) {
+      const int lim[2] = {*reinterpret_cast<const int*>(qs + SM::kLim + row_a * 4),
+                          *reinterpret_cast<const int*>(qs + SM::kLim + row_b * 4)};
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < NT; ++e)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int in_blk = NT == 1 ? g + 8 * (c >> 1) : 8 * e + 2 * t + (c & 1);
+            if (pos0 + 16 * u + in_blk > lim[row_of(c)] || (gone >> u & 1))
+              hidden |= 1u << (8 * u + 4 * e + c);
+            else
+              big[row_of(c)] = max(big[row_of(c)],
+                                   larger_scale(q4_load_scales<G>(blk + u * L::kBytes + L::kVs + in_blk * 2 * G)));
+          }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int sh = NT == 1 ? 4 : 1; sh < (NT == 1 ? 32 : 4); sh <<= 1)
+          big[r] = max(big[r], __shfl_xor_sync(0xffffffffu, big[r], sh));
     } else {
 #pragma unroll
       for (int u = 0; u < U; u += 2) {
         // lane l has position l of two blocks
         const uint32_t s = q4_load_scales<G>(blk + (U == 1 ? 0 : u + (lane >> 4)) * L::kBytes + L::kVs + (lane & 15) * 2 * G);
-        big = max(big, larger_scale(s));
+        big[0] = max(big[0], larger_scale(s));
       }
-      big = __reduce_max_sync(0xffffffffu, big);
+      big[0] = big[1] = __reduce_max_sync(0xffffffffu, big[0]);
     }
-    float pr[U][NT][4];
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float top[2];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        top[c] = -INFINITY;
-        uint32_t row_big = 0;
+      for (int e = 0; e < NT; ++e)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int c = 0; c < 4; ++c)
+          if (!kMasked || !(hidden >> (8 * u + 4 * e + c) & 1u)) top[row_of(c)] = fmaxf(top[row_of(c)], x[u][e][c]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (kMasked && (hidden[nt] >> (4 * u + c + 2 * e) & 1u)) continue;
-            top[c] = fmaxf(top[c], __fmul_rn(x[u][nt][c + 2 * e], fq[nt][c]));
-            if (kMasked)
-              row_big = max(row_big, larger_scale(q4_load_scales<G>(blk + u * L::kBytes + L::kVs + (g + 8 * e) * 2 * G)));
-          }
+    for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) {
-          top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], sh));
-          if (kMasked) row_big = max(row_big, __shfl_xor_sync(0xffffffffu, row_big, sh));
-        }
-        top[c] += exponent_of(kMasked ? row_big : big);
-      }
-      if (__any_sync(0xffffffffu, top[0] > m_run[nt][0] + kQaSlack || top[1] > m_run[nt][1] + kQaSlack)) {
-        float corr[2];
+      for (int sh = NT == 1 ? 4 : 1; sh < (NT == 1 ? 32 : 4); sh <<= 1)
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], sh));
+      top[r] = fmaf(top[r], fq[r], exponent_of(big[r]));
+    }
+    if (__any_sync(0xffffffffu, top[0] > m_run[0] + kQaSlack || top[1] > m_run[1] + kQaSlack)) {
+      float corr[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float m = top[c] > m_run[nt][c] + kQaSlack ? top[c] : m_run[nt][c];
-          corr[c] = m == -INFINITY ? 1.0f : ex2_ftz(m_run[nt][c] - m);
-          m_run[nt][c] = m;
-          base[nt][c] = m == -INFINITY ? 0.0f : m - kQaLift;
-          l_run[nt][c] *= corr[c];
+      for (int r = 0; r < 2; ++r) {
+        const float m = top[r] > m_run[r] + kQaSlack ? top[r] : m_run[r];
+        corr[r] = m == -INFINITY ? 1.0f : ex2_ftz(m_run[r] - m);
+        m_run[r] = m;
+        base[r] = m == -INFINITY ? 0.0f : m - kQaLift;
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) cs[nt][gr][c] *= corr[c];
-        }
-#pragma unroll
-        for (int i = 0; i < 2 * W; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[nt][i][c] *= corr[c & 1];
+        for (int i = 0; i < NT; ++i) l_run[r][i] *= corr[r];
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) cs[gr][c] *= corr[row_of(c)];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][c] *= corr[row_of(c)];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < NT; ++e)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float v = ex2_ftz(fmaf(x[u][nt][c], fq[nt][c & 1], -base[nt][c & 1]));
-          if (kMasked && (hidden[nt] >> (4 * u + c) & 1u)) v = 0.0f;
-          pr[u][nt][c] = v;
-          l_run[nt][c & 1] += v;
+          float v = ex2_ftz(fmaf(x[u][e][c], fq[row_of(c)], -base[row_of(c)]));
+          if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) v = 0.0f;
+          x[u][e][c] = v;
+          l_run[row_of(c)][NT == 1 ? 0 : (c & 1)] += v;
         }
-    }
     // ---- the weighted values
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint8_t* bk = blk + u * L::kBytes;
       const Q4Words<W> v0 = q4_load<W>(bk + L::kV + lane * (4 * W)), v1 = q4_load<W>(bk + L::kV + (32 + lane) * (4 * W));
-      const uint32_t vs0 = q4_load_scales<G>(bk + L::kVs + g * 2 * G), vs1 = q4_load_scales<G>(bk + L::kVs + (g + 8) * 2 * G);
+      uint32_t vs[2][G == 2 ? 2 : 1];  // like ks
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (NT == 1) {
+          vs[e][0] = q4_load_scales<G>(bk + L::kVs + (g + 8 * e) * 2 * G);
+        } else if constexpr (G == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(bk + L::kVs + (8 * e + 2 * t) * 4);
+          vs[e][0] = v.x, vs[e][1] = v.y;
+        } else {
+          vs[e][0] = *reinterpret_cast<const uint32_t*>(bk + L::kVs + (8 * e + 2 * t) * 2);
+        }
+      }
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
-        const float s0 = q4_scale(vs0, gr), s1 = q4_scale(vs1, gr);
-        uint32_t pb[NT][2];
+        uint32_t pp[NT][2];  // P s in f16: [e][row pair]
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int e = 0; e < NT; ++e) {
           float w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            w[c] = pr[u][nt][c] * (c < 2 ? s0 : s1);
-            if (kMasked && (hidden[nt] >> (4 * u + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
+            const float s = NT == 1 ? q4_scale(vs[c >> 1][0], gr)
+                                    : G == 2 ? q4_scale(vs[e][c & (G - 1)], gr) : q4_scale(vs[e][0], c & 1);
+            w[c] = x[u][e][c] * s;
+            if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
           }
-          pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
-          pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
-          mma_f16_m16n8k16(cs[nt][gr], 0x3C003C00u, 0u, 0x3C003C00u, 0u, pb[nt][0], pb[nt][1], cs[nt][gr]);
+          pp[e][0] = pack_f16(w[0], w[1]);
+          pp[e][1] = pack_f16(w[2], w[3]);
         }
+        if constexpr (NT == 1) {
+          const uint32_t b0 = movmatrix_trans(pp[0][0]), b1 = movmatrix_trans(pp[0][1]);
+          mma_f16_m16n8k16(cs[gr], 0x3C003C00u, 0u, 0x3C003C00u, 0u, b0, b1, cs[gr]);
 #pragma unroll
-        for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
-          const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+          for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
+            const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+            mma_f16_m16n8k16(o[2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u, b0, b1, o[2 * m]);
+            mma_f16_m16n8k16(o[2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u, b0, b1,
+                             o[2 * m + 1]);
+          }
+        } else {
+          const uint32_t a0 = pp[0][0], a1 = pp[0][1], a2 = pp[NT - 1][0], a3 = pp[NT - 1][1];
+          mma_f16_m16n8k16(cs[gr], a0, a1, a2, a3, 0x3C003C00u, 0x3C003C00u, cs[gr]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_m16n8k16(o[nt][2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u,
-                             pb[nt][0], pb[nt][1], o[nt][2 * m]);
-            mma_f16_m16n8k16(o[nt][2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u,
-                             pb[nt][0], pb[nt][1], o[nt][2 * m + 1]);
+          for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
+            const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+            mma_f16_m16n8k16(o[4 * m], a0, a1, a2, a3, a & 0x000F000Fu, c & 0x000F000Fu, o[4 * m]);
+            mma_f16_m16n8k16(o[4 * m + 1], a0, a1, a2, a3, a & 0x00F000F0u, c & 0x00F000F0u, o[4 * m + 1]);
+            mma_f16_m16n8k16(o[4 * m + 2], a0, a1, a2, a3, a8 & 0x000F000Fu, c8 & 0x000F000Fu, o[4 * m + 2]);
+            mma_f16_m16n8k16(o[4 * m + 3], a0, a1, a2, a3, a8 & 0x00F000F0u, c8 & 0x00F000F0u, o[4 * m + 3]);
           }
         }
       }
@@ -437,27 +477,41 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   for (int i = done; i < nsteps && i < done + S; ++i) mbar_wait(&full[i % S], (i / S) & 1, p.wait_ns);
   __syncwarp();
 
-  // ---- the warp's state, in its drained ring: column 2t + c of tile nt is row 8 nt + 2t + c
+  // ---- the warp's state, in its drained ring
   float* o_w = reinterpret_cast<float*>(ring);
   float* ml_w = reinterpret_cast<float*>(ring + SM::kMl);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = 8 * nt + 2 * t + c;
-      float l = l_run[nt][c];
+  for (int r = 0; r < 2; ++r) {
+    const int row = r ? row_b : row_a;
+    float l = l_run[r][0];
+    if constexpr (NT == 1) {
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (g == 0) *reinterpret_cast<float2*>(ml_w + 2 * r) = make_float2(m_run[nt][c], l);
+      if (g == 0) *reinterpret_cast<float2*>(ml_w + 2 * row) = make_float2(m_run[r], l);
+    } else {
+      l += l_run[r][NT - 1];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (t == 0) *reinterpret_cast<float2*>(ml_w + 2 * row) = make_float2(m_run[r], l);
+    }
 #pragma unroll
-      for (int m = 0; m < W; ++m) {
-        const float off = -8.0f * cs[nt][m >> 1][c];
-        *reinterpret_cast<float4*>(o_w + r * SM::kStride + 32 * m + 4 * g) =
-            make_float4(fmaf(o[nt][2 * m][c], 16777216.0f, off), fmaf(o[nt][2 * m][c + 2], 1048576.0f, off),
-                        fmaf(o[nt][2 * m + 1][c], 16777216.0f, off), fmaf(o[nt][2 * m + 1][c + 2], 1048576.0f, off));
+    for (int m = 0; m < W; ++m) {
+      const float off = -8.0f * cs[m >> 1][NT == 1 ? r : 2 * r];
+      constexpr float kEven = 16777216.0f, kOdd = 1048576.0f;
+      if constexpr (NT == 1) {
+        *reinterpret_cast<float4*>(o_w + row * SM::kStride + 32 * m + 4 * g) =
+            make_float4(fmaf(o[2 * m][r], kEven, off), fmaf(o[2 * m][r + 2], kOdd, off),
+                        fmaf(o[2 * m + 1][r], kEven, off), fmaf(o[2 * m + 1][r + 2], kOdd, off));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<float4*>(o_w + row * SM::kStride + 32 * m + 8 * t + 4 * c) =
+              make_float4(fmaf(o[4 * m][2 * r + c], kEven, off), fmaf(o[(4 * m + 1) % kTiles][2 * r + c], kOdd, off),
+                          fmaf(o[(4 * m + 2) % kTiles][2 * r + c], kEven, off), fmaf(o[(4 * m + 3) % kTiles][2 * r + c], kOdd, off));
       }
     }
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < nrows * (D / 4); i += kQaThreads) {
     const int r = i / (D / 4), c4 = i - r * (D / 4), row = r0 + r;
@@ -597,7 +651,7 @@ cudaError_t run(const QaParams& p, const DeviceCtx& dc, cudaStream_t s) {
 #define Q4_C1 4
 #define Q4_U2 2
 #define Q4_S2 3
-#define Q4_C2 2
+#define Q4_C2 3
 #endif
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
