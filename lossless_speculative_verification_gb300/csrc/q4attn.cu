@@ -21,10 +21,14 @@
 // sums are rescaled in few steps then): P s < 2^15, and what underflows is below
 // 2^-22 of the largest term.
 //
-// A CTA's four warps take the 16-position blocks of one chunk of one key head in
-// turn; their states (maximum, sum, output) meet in shared memory, those of the
-// chunks in attn_q4_combine_kernel.  Chunks begin at fixed positions, so a row's
-// result does not depend on the other rows of the call.
+// A CTA's four warps take the steps (32 positions) of one chunk of one key head
+// in turn, each from a ring of its own; their states (maximum, sum, output) meet
+// in shared memory, those of the chunks in the cluster or in
+// attn_q4_combine_kernel.  Chunks begin at fixed positions and both forms add in
+// the same order, so a row's result does not depend on the other rows of the call.
+// Bound by the issue of instructions (57 % of the slots, 711 a step of 32
+// positions and 16 rows, 160 of them dequantising; the tensor cores 43 %): 16 x 32K
+// positions of 8 key heads take 148 us, 3.7 TB/s of cache.
 #include <math.h>
 
 #include <type_traits>
@@ -42,7 +46,7 @@ constexpr int kQaThreads = kQaWarps * 32;
 constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
 constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
 constexpr float kQaLog2e = 1.4426950408889634f;
-constexpr int kQaMaxChunks = 1024;
+constexpr int kQaMaxSteps = 4096;  // steps of 128 positions in a chunk, at most
 
 struct QaParams {
   const bf16* q;           // [B, Q, nh, D]
@@ -50,6 +54,7 @@ struct QaParams {
   const int32_t* table;    // [B, M]
   const int32_t* ctx_len;  // [B]
   int B, Q, nh, nkv, grp, R, M, P, page_shift, rblocks;
+  int mode;
   int chunk, nchunk;  // positions of a chunk (a multiple of 16 kQaWarps), chunks of a sequence
   float scale_log2;   // scale * log2(e)
   bf16* out;          // [B, Q, nh, D]
@@ -65,6 +70,34 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+// How the chunks' states meet: there is one chunk, the chunks' CTAs are a cluster, or a second kernel merges them.
+enum : int { kQaDirect = 0, kQaCluster = 1, kQaParts = 2 };
+constexpr int kQaCluster8 = 8;  // chunks of a cluster, at most
+
+// A state of four output columns of a row: maximum, sum, unnormalised output.
+struct QaState {
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // adds another's (maximum, sum), output; m is the maximum of all already
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    // one that saw nothing adds nothing; one that saw only NaN scores adds them
+    const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2_ftz(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
+  }
+  __device__ __forceinline__ void store(const QaParams& p, int b, int h, int row, int D, int c4) const {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing is zero
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    uint2 v;
+    v.x = *reinterpret_cast<const uint32_t*>(&lo);
+    v.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 4 * c4) = v;
+  }
+};
+
 // Bits of the larger of a position's value scales, a NaN one left out.
 __device__ __forceinline__ uint32_t larger_scale(uint32_t s) {
   const uint32_t a = s & 0xFFFFu, b = s >> 16, u = max(a, b);
@@ -75,47 +108,66 @@ __device__ __forceinline__ uint32_t larger_scale(uint32_t s) {
 // Its exponent, at least -64.
 __device__ __forceinline__ float exponent_of(uint32_t bits) { return (float)max((int)(bits >> 7) - 127, -64); }
 
-// A warp's ring of S stages of U blocks each in shared memory, filled by untiled bulk copies.
-template <int D, int NT, int U, int S>
+// A warp's ring of S stages in shared memory, each the K steps of U blocks that it takes next, filled by untiled
+// bulk copies.
+template <int D, int NT, int U, int K, int S>
 struct QaSmem {
   using L = Q4Block<D>;
   static constexpr int kRows = 8 * NT;
   static constexpr int kStride = D + 4;  // floats between rows of a state, in the ring once it is drained
-  static constexpr int kRing = S * U * L::kBytes;
+  static constexpr int kStage = K * U * L::kBytes;
+  static constexpr int kRing = S * kStage;
   static constexpr int kMl = kRows * kStride * 4;  // byte offset of (maximum, sum) behind the rows
   static constexpr int kWarp = kRing > kMl + kRows * 8 ? kRing : (kMl + kRows * 8 + 15) / 16 * 16;
-  static constexpr int kQ = kQaWarps * (kWarp + S * 8 + S * 4) + 15 & ~15;  // byte offset of the queries
-  static constexpr int kQf = 0;                               // [NT][W][lane] 16 bytes: the B operands
+  static constexpr int kBars = kQaWarps * kWarp;                     // [warp][S] mbarriers
+  static constexpr int kHere = kBars + kQaWarps * S * 8;             // [warp][S] which blocks a stage holds
+  static constexpr int kQf = (kHere + kQaWarps * S * 4 + 15) / 16 * 16;  // [NT][W][lane] 16 bytes: the B operands
   static constexpr int kCi = kQf + NT * L::W * 512;           // [G][4 or 8] 16 bytes: where the accumulators start
   static constexpr int kFq = kCi + NT * L::G * 64;            // [8 NT] what turns the scaled sums into log2 scores
   static constexpr int kLim = kFq + kRows * 4;                // [8 NT] last position the row sees
-  static constexpr int kTotal = kQ + kLim + kRows * 4;
+  static constexpr int kMlAll = kLim + kRows * 4;             // [8 NT][2] (maximum, sum) of the CTA
+  static constexpr int kTotal = kMlAll + kRows * 8;
 };
 
-template <int D, int NT, int U, int S, int kPerSm>
+template <int D, int NT, int U, int K, int S, int kPerSm>
 __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaParams p) {
   using L = Q4Block<D>;
-  using SM = QaSmem<D, NT, U, S>;
+  using SM = QaSmem<D, NT, U, K, S>;
   constexpr int W = L::W, G = L::G;
   constexpr int kRows = SM::kRows;
   constexpr int kStep = 16 * U;            // positions a warp takes at a time
-  constexpr int kBatch = 32 / U;           // steps whose pages the lanes hold
+  constexpr int kRound = kStep * kQaWarps;
+  constexpr int kBlocks = K * U;           // blocks of a stage
+  constexpr int kBatch = 32 / kBlocks;     // stages whose pages the lanes hold
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * SM::kWarp;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kQaWarps * SM::kWarp) + warp * S;
-  int* here = reinterpret_cast<int*>(smem + kQaWarps * (SM::kWarp + S * 8)) + warp * S;  // which blocks a stage holds
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars) + warp * S;
+  int* here = reinterpret_cast<int*>(smem + SM::kHere) + warp * S;
   if (lane < S) mbar_init(&full[lane], 1);
   fence_barrier_init();
   __syncwarp();
-  pdl_wait();
-  pdl_trigger();
-
   const int split = blockIdx.y;
   const int rb = blockIdx.x % p.rblocks, bh = blockIdx.x / p.rblocks;
   const int b = bh / p.nkv, h = bh - b * p.nkv;
   const int r0 = rb * kRows, nrows = min(kRows, p.R - r0);
+  const int t_begin = split * p.chunk;
+  // step i of this warp is the U blocks from position first + i * kRound on, a stage K steps
+  const int first = t_begin + warp * kStep;
+  const int per_shift = p.page_shift - 4;
+  const int cap = min(p.M << p.page_shift, t_begin + p.chunk);
+  // lane l has block l % kBlocks of stage i + l / kBlocks
+  auto pos_of = [&](int i) {
+    return first + ((i + lane / kBlocks) * K + lane % kBlocks / U) * kRound + 16 * (lane % U);
+  };
+  auto entry_of = [&](int i) {
+    const int pos = pos_of(i);
+    return pos < cap ? __ldcg(p.table + (size_t)b * p.M + (pos >> p.page_shift)) : -1;
+  };
+  pdl_wait();
+  pdl_trigger();
   const int n = __ldcg(p.ctx_len + b);
+  int pg_now = entry_of(0);  // beside the length's load, before it is known how many of them there are
 
   // ---- the queries: warp w < NT makes the operands of tile w; column g is row r0 + 8 w + g, of which this lane
   // has the dims 32 j + 8 t + 0..7
@@ -130,54 +182,44 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 
   const bool bad = n < 0 || n > (p.M << p.page_shift);
   if (bad && threadIdx.x == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
-  const int t_begin = split * p.chunk;
   const int end = bad ? 0 : min(n, t_begin + p.chunk);
-  if (p.nchunk > 1 && t_begin >= end) return;  // the combine reads no state of it
+  if (p.mode == kQaParts && t_begin >= end) return;  // the combine reads no state of it
 
-  // ---- the ring: step i of this warp is the U blocks from position first + i * kQaWarps * kStep on
-  const int first = t_begin + warp * kStep;
-  const int nsteps = first < end ? (end - first + kQaWarps * kStep - 1) / (kQaWarps * kStep) : 0;
-  const int per_shift = p.page_shift - 4;
-  // lane l has the page of block l % U of step i0 + l / U; -1: none there
-  auto pages_of = [&](int i0) {
-    const int i = i0 + lane / U, pos = first + i * (kQaWarps * kStep) + 16 * (lane % U);
-    if (i >= nsteps || pos >= end) return -1;
-    const int pg = __ldcg(p.table + (size_t)b * p.M + (pos >> p.page_shift));
+  // ---- the ring
+  const int nsteps = first < end ? (end - first + kRound - 1) / kRound : 0;
+  const int nstages = (nsteps + K - 1) / K;
+  auto checked = [&](int pg, int i) {  // the page of this lane's block, -1: none
+    if (pos_of(i) >= end) return -1;
     if (pg >= 0 && pg < p.P) return pg;
     set_error(p.err, kErrDeviceIndex);
     return -1;
   };
-  int pg_now = pages_of(0), pg_next = -1;
-  auto issue = [&](int i, int s) {  // all lanes: step i into stage s
+  pg_now = checked(pg_now, 0);
+  int pg_next = -1;
+  auto issue = [&](int i, int s) {  // all lanes: stage i of the warp into stage s of the ring
     const int k = i % kBatch;
     if (k == 0) {
-      if (i > 0) pg_now = pg_next;
-      pg_next = pages_of(i + kBatch);
+      if (i > 0) pg_now = checked(pg_next, i);
+      pg_next = entry_of(i + kBatch);
     }
-    int pg[U], there = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      pg[u] = __shfl_sync(0xffffffffu, pg_now, k * U + u);
-      there |= (pg[u] >= 0) << u;
-    }
+    const int l = lane % kBlocks, pg = __shfl_sync(0xffffffffu, pg_now, k * kBlocks + l);
+    const uint32_t there = __ballot_sync(0xffffffffu, lane < kBlocks && pg >= 0);
     if (lane == 0) {
       here[s] = there;
       mbar_arrive_expect_tx(&full[s], __popc(there) * L::kBytes);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (pg[u] >= 0) {
-          const int blk = (first >> 4) + i * (kQaWarps * U) + u;
-          bulk_load(ring + (s * U + u) * L::kBytes,
-                    p.pool + ((((size_t)pg[u] * p.nkv + h) << per_shift) + (blk & ((1 << per_shift) - 1))) * L::kBytes,
-                    L::kBytes, &full[s]);
-        }
+    }
+    __syncwarp();
+    if (there >> lane & 1u) {
+      const int blk = ((first + (i * K + l / U) * kRound) >> 4) + l % U;
+      bulk_load(ring + s * SM::kStage + l * L::kBytes,
+                p.pool + ((((size_t)pg * p.nkv + h) << per_shift) + (blk & ((1 << per_shift) - 1))) * L::kBytes, L::kBytes,
+                &full[s]);
     }
   };
 #pragma unroll 1
-  for (int i = 0; i < S && i < nsteps; ++i) issue(i, i);
-  __syncwarp();
+  for (int i = 0; i < S && i < nstages; ++i) issue(i, i);
 
-  uint8_t* qs = smem + SM::kQ;
+  uint8_t* qs = smem;
   if (warp < NT) {
     uint32_t m = 0;
 #pragma unroll
@@ -454,27 +496,31 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   int done = 0, st = 0;
   uint32_t phase = 0;
 #pragma unroll 1
-  for (; done < nsteps; ++done) {
+  for (; done < nstages; ++done) {
     if (!__all_sync(0xffffffffu, mbar_wait(&full[st], phase, p.wait_ns))) {
       if (lane == 0) set_error(p.err, kErrTimeout);
       break;
     }
-    const uint8_t* blk = ring + st * U * L::kBytes;
-    const int pos0 = first + done * (kQaWarps * kStep);
-    const int gone = ~here[st] & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
-    if (pos0 + kStep - 1 > n - p.Q || gone)
-      step(std::true_type{}, blk, pos0, gone);
-    else
-      step(std::false_type{}, blk, pos0, 0);
+    const int there = here[st];
+#pragma unroll 1
+    for (int k = 0; k < K && done * K + k < nsteps; ++k) {
+      const uint8_t* blk = ring + st * SM::kStage + k * (U * L::kBytes);
+      const int pos0 = first + (done * K + k) * kRound;
+      const int gone = ~(there >> (k * U)) & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
+      if (pos0 + kStep - 1 > n - p.Q || gone)
+        step(std::true_type{}, blk, pos0, gone);
+      else
+        step(std::false_type{}, blk, pos0, 0);
+    }
     __syncwarp();  // every lane has read the stage
-    if (done + S < nsteps) issue(done + S, st);
+    if (done + S < nstages) issue(done + S, st);
     if (++st == S) {
       st = 0;
       phase ^= 1u;
     }
   }
   // after a wait that ran out: the copies already issued land before the memory is used again
-  for (int i = done; i < nsteps && i < done + S; ++i) mbar_wait(&full[i % S], (i / S) & 1, p.wait_ns);
+  for (int i = done; i < nstages && i < done + S; ++i) mbar_wait(&full[i % S], (i / S) & 1, p.wait_ns);
   __syncwarp();
 
   // ---- the warp's state, in its drained ring
@@ -516,39 +562,52 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   for (int i = threadIdx.x; i < nrows * (D / 4); i += kQaThreads) {
     const int r = i / (D / 4), c4 = i - r * (D / 4), row = r0 + r;
     float2 ml[kQaWarps];
-    float mm = -INFINITY;
+    float4* at0 = reinterpret_cast<float4*>(smem + (r * SM::kStride + 4 * c4) * 4);
+    QaState acc;
 #pragma unroll
     for (int w = 0; w < kQaWarps; ++w) {
       ml[w] = *reinterpret_cast<const float2*>(smem + w * SM::kWarp + SM::kMl + 8 * r);
-      mm = fmaxf(mm, ml[w].x);
+      acc.m = fmaxf(acc.m, ml[w].x);
     }
-    float ls = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kQaWarps; ++w) {
-      // a warp that saw nothing adds nothing; one that saw only NaN scores adds them
-      const float f = ml[w].x == -INFINITY ? (ml[w].y == 0.0f ? 0.0f : 1.0f) : ex2_ftz(ml[w].x - mm);
-      const float4 v = *reinterpret_cast<const float4*>(smem + w * SM::kWarp + (r * SM::kStride + 4 * c4) * 4);
-      ls = fmaf(ml[w].y, f, ls);
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
-    }
-    if (p.nchunk == 1) {
-      const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;  // a row that sees nothing is zero
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
-                           hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      uint2 v;
-      v.x = *reinterpret_cast<const uint32_t*>(&lo);
-      v.y = *reinterpret_cast<const uint32_t*>(&hi);
-      *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 4 * c4) = v;
-    } else {
+    for (int w = 0; w < kQaWarps; ++w) acc.add(ml[w], *(at0 + w * (SM::kWarp / 16)));
+    if (p.mode == kQaDirect) {
+      acc.store(p, b, h, row, D, c4);
+    } else if (p.mode == kQaParts) {
       const size_t at = ((size_t)bh * p.nchunk + split) * p.R + row;
-      *reinterpret_cast<float4*>(p.o_part + at * D + 4 * c4) = acc;
-      if (c4 == 0) *reinterpret_cast<float2*>(p.ml_part + at * 2) = make_float2(mm, ls);
+      *reinterpret_cast<float4*>(p.o_part + at * D + 4 * c4) = acc.o;
+      if (c4 == 0) *reinterpret_cast<float2*>(p.ml_part + at * 2) = make_float2(acc.m, acc.l);
+    } else {
+      *at0 = acc.o;  // nobody else reads this place of warp 0's state
+      if (c4 == 0) *reinterpret_cast<float2*>(smem + SM::kMlAll + 8 * r) = make_float2(acc.m, acc.l);
     }
   }
+  if (p.mode != kQaCluster) return;
+  // ---- the chunks' CTAs are a cluster: each takes a share of the outputs and reads it from all of them
+  cluster_sync();
+  const int parts = min(p.nchunk, max(1, bad ? 0 : (n + p.chunk - 1) / p.chunk));
+  if (split < parts) {
+    const uint32_t mine = smem_u32(smem);
+    for (int i = split * kQaThreads + threadIdx.x; i < nrows * (D / 4); i += parts * kQaThreads) {
+      const int r = i / (D / 4), c4 = i - r * (D / 4);
+      float2 ml[kQaCluster8];
+      float4 v[kQaCluster8];
+      QaState acc;
+#pragma unroll
+      for (int k = 0; k < kQaCluster8; ++k)
+        if (k < parts) {
+          const uint32_t at = mapa_shared(mine, k);
+          ml[k] = ld_shared_cluster_f2(at + SM::kMlAll + 8 * r);
+          v[k] = ld_shared_cluster_f4(at + (r * SM::kStride + 4 * c4) * 4);
+          acc.m = fmaxf(acc.m, ml[k].x);
+        }
+#pragma unroll
+      for (int k = 0; k < kQaCluster8; ++k)
+        if (k < parts) acc.add(ml[k], v[k]);
+      acc.store(p, b, h, r0 + r, D, c4);
+    }
+  }
+  cluster_sync();  // no CTA leaves while another reads its memory
 }
 
 // Per (key head, sequence): the chunks' states brought to their common maximum and summed.
@@ -567,8 +626,7 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
   const float4* o4 = reinterpret_cast<const float4*>(p.o_part) + (size_t)bh * p.nchunk * p.R * (D / 4);
   for (int i = blockIdx.y * kQcThreads + threadIdx.x; i < p.R * (D / 4); i += gridDim.y * kQcThreads) {
     const int row = i / (D / 4), c4 = i - row * (D / 4);
-    float mm = -INFINITY, ls = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    QaState all;
     for (int s0 = 0; s0 < parts; s0 += kQcUnroll) {
       float2 a[kQcUnroll];
       float4 v[kQcUnroll];
@@ -578,52 +636,53 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
         a[u] = in ? __ldcg(ml + (size_t)(s0 + u) * p.R + row) : make_float2(-INFINITY, 0.0f);
         v[u] = in ? __ldcg(o4 + ((size_t)(s0 + u) * p.R + row) * (D / 4) + c4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
-      float gm = mm;
+      QaState acc;
+      acc.m = all.m;
 #pragma unroll
-      for (int u = 0; u < kQcUnroll; ++u) gm = fmaxf(gm, a[u].x);
-      const float r = mm == -INFINITY ? (ls == 0.0f ? 0.0f : 1.0f) : ex2_ftz(mm - gm);
-      ls *= r;
-      acc.x *= r;
-      acc.y *= r;
-      acc.z *= r;
-      acc.w *= r;
+      for (int u = 0; u < kQcUnroll; ++u) acc.m = fmaxf(acc.m, a[u].x);
+      acc.add(make_float2(all.m, all.l), all.o);
 #pragma unroll
-      for (int u = 0; u < kQcUnroll; ++u) {
-        const float f = a[u].x == -INFINITY ? (a[u].y == 0.0f ? 0.0f : 1.0f) : ex2_ftz(a[u].x - gm);
-        ls = fmaf(a[u].y, f, ls);
-        acc.x = fmaf(v[u].x, f, acc.x);
-        acc.y = fmaf(v[u].y, f, acc.y);
-        acc.z = fmaf(v[u].z, f, acc.z);
-        acc.w = fmaf(v[u].w, f, acc.w);
-      }
-      mm = gm;
+      for (int u = 0; u < kQcUnroll; ++u) acc.add(a[u], v[u]);
+      all = acc;
     }
-    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
-                         hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    uint2 v;
-    v.x = *reinterpret_cast<const uint32_t*>(&lo);
-    v.y = *reinterpret_cast<const uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 4 * c4) = v;
+    all.store(p, b, h, row, D, c4);
   }
 }
 
-// Positions of a chunk, a whole number of steps of the four warps (128 positions).  Many chunks fill the GPU,
-// but each costs its CTA about as much as three steps (queries, first loads, the states' meeting) and the
-// combine its share: the number of chunks with the least rounds of CTAs (two an SM) times steps of a round.
-// It goes by the capacity (the lengths are on the device) and not by Q or the shared heads, so a row is summed
-// in the same order alone and among others.
-int chunk_of(int B, int nkv, long long cap) {
-  constexpr int kRound = 32 * kQaWarps, kSlots = 152 * 2, kCost = 3;
+// The cut of a sequence: positions of a chunk, a whole number of steps of the four warps (128 positions), and
+// how the chunks meet.  Many chunks fill the GPU and make the chains of steps short, but each costs its CTA about
+// as much as three steps (queries, first loads, the states' meeting): the cut with the least rounds of CTAs (three
+// an SM; one at least) times steps of a round.  Where all CTAs are on the GPU at once and a sequence has at most
+// eight, its chunks are a cluster; else a second kernel merges them, about three steps more (clusters that wait for
+// room leave SMs idle).  Measured: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 14.0 us,
+// 8 merged by a kernel 15.7, 4 chunks 18.9; 32 of up to 2304, 10 key heads: 2 chunks 23.5, 1 chunk 27.4, 4 chunks
+// 24.5 (in clusters 30.3); 16 of 32K, 8 key heads: 7 chunks 148 (in clusters 186), 16 chunks 154.
+// The cut goes by the capacity (the lengths are on the device) and not by Q or the shared heads, so a row is
+// summed in the same order alone and among others.
+struct Cut {
+  int chunk, nchunk, mode;
+};
+Cut cut_of(int B, int nkv, long long cap) {
+  constexpr int kRound = 32 * kQaWarps, kSlots = 152 * 3, kCost = 3, kTwo = 3;
   const long long pairs = (long long)B * nkv, steps = (cap + kRound - 1) / kRound;
+  const long long most = (steps + kQaMaxSteps - 1) / kQaMaxSteps;
   long long best = 1ll << 62, at = steps;
-  for (long long k = 1; k <= kQaMaxChunks && k <= steps; ++k) {
+  auto clustered = [&](long long used) { return used <= kQaCluster8 && pairs * used <= kSlots; };
+  auto consider = [&](long long k) {
+    k = k < most ? most : k > steps ? steps : k;
     const long long len = (steps + k - 1) / k, used = (steps + len - 1) / len;
-    const long long cost = (pairs * used + kSlots - 1) / kSlots * (len + kCost);
+    const long long cost = (pairs * used > kSlots ? pairs * used : kSlots) * (len + kCost) +
+                           (used == 1 || clustered(used) ? 0 : kTwo * kSlots);
     if (cost < best) best = cost, at = len;
-    if (pairs * used > 8 * kSlots && k > 1) break;  // finer cuts only add CTAs
-  }
-  return (int)(at * kRound);
+  };
+  consider(1);
+  if (clustered(kQaCluster8)) consider(kQaCluster8);
+  for (int r = 1; r <= 8 && pairs > 0; ++r) consider(r * kSlots / pairs);
+  Cut c;
+  c.chunk = (int)(at * kRound);
+  c.nchunk = (int)((steps + at - 1) / at);
+  c.mode = c.nchunk == 1 ? kQaDirect : clustered(c.nchunk) ? kQaCluster : kQaParts;
+  return c;
 }
 
 bool shape_ok(int B, int Q, int M, int page, int nh, int nkv, int d) {
@@ -634,25 +693,31 @@ bool shape_ok(int B, int Q, int M, int page, int nh, int nkv, int d) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <int D, int NT, int U, int S, int kPerSm>
+template <int D, int NT, int U, int K, int S, int kPerSm>
 cudaError_t run(const QaParams& p, const DeviceCtx& dc, cudaStream_t s) {
-  constexpr int kSmem = QaSmem<D, NT, U, S>::kTotal;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(attn_q4_kernel<D, NT, U, S, kPerSm>), kSmem, dc.device);
+  constexpr int kSmem = QaSmem<D, NT, U, K, S>::kTotal;
+  auto kernel = attn_q4_kernel<D, NT, U, K, S, kPerSm>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kSmem, dc.device);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_q4_kernel<D, NT, U, S, kPerSm>, dim3(p.B * p.nkv * p.rblocks, p.nchunk), dim3(kQaThreads), kSmem, s, p);
-  if (e != cudaSuccess || p.nchunk == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.B * p.nkv * p.rblocks, p.nchunk);
+  cfg.blockDim = dim3(kQaThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = p.nchunk;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.mode == kQaCluster ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess || p.mode != kQaParts) return e;
   const int slices = (p.R * (D / 4) + kQcThreads - 1) / kQcThreads;
   return launch_pdl(attn_q4_combine_kernel<D>, dim3(p.B * p.nkv, slices), dim3(kQcThreads), 0, s, p);
 }
-
-#ifndef Q4_U1
-#define Q4_U1 2
-#define Q4_S1 3
-#define Q4_C1 4
-#define Q4_U2 2
-#define Q4_S2 3
-#define Q4_C2 3
-#endif
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -666,9 +731,8 @@ extern "C" {
 size_t spec_q4_attention_workspace_size(int32_t B, int32_t Q, int32_t M, int32_t page, int32_t nh, int32_t nkv,
                                         int32_t d) {
   if (!shape_ok(B, Q, M, page, nh, nkv, d)) return 0;
-  const long long cap = (long long)M * page;
-  const int chunk = chunk_of(B, nkv, cap);
-  const size_t parts = (size_t)B * nkv * ((cap + chunk - 1) / chunk) * (Q * (nh / nkv));
+  const Cut cut = cut_of(B, nkv, (long long)M * page);
+  const size_t parts = cut.mode == kQaParts ? (size_t)B * nkv * cut.nchunk * (Q * (nh / nkv)) : 0;
   return 256 + round256(parts * d * 4) + round256(parts * 2 * 4);
 }
 
@@ -701,9 +765,10 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.P = P;
   p.page_shift = 4;
   while ((1 << p.page_shift) < page) ++p.page_shift;
-  const long long cap = (long long)M * page;
-  p.chunk = chunk_of(B, nkv, cap);
-  p.nchunk = (int)((cap + p.chunk - 1) / p.chunk);
+  const Cut cut = cut_of(B, nkv, (long long)M * page);
+  p.chunk = cut.chunk;
+  p.nchunk = cut.nchunk;
+  p.mode = cut.mode;
   p.scale_log2 = scale * kQaLog2e;
   p.out = static_cast<bf16*>(out);
   const size_t parts = (size_t)B * nkv * p.nchunk * p.R;
@@ -711,11 +776,11 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(parts * d * 4));
   p.err = dc->err;
   p.wait_ns = wait_limit_ns();
-  const bool two = p.R > 8;
+  const bool two = p.R > 8;  // the rows of an MMA, or its columns (half the MMAs for up to eight rows)
   p.rblocks = two ? (p.R + 15) / 16 : 1;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = d == 128 ? (two ? run<128, 2, Q4_U2, Q4_S2, Q4_C2>(p, *dc, s) : run<128, 1, Q4_U1, Q4_S1, Q4_C1>(p, *dc, s))
-                                 : (two ? run<64, 2, Q4_U2, Q4_S2, Q4_C2>(p, *dc, s) : run<64, 1, Q4_U1, Q4_S1, Q4_C1>(p, *dc, s));
+  const cudaError_t e = d == 128 ? (two ? run<128, 2, 2, 2, 2, 3>(p, *dc, s) : run<128, 1, 2, 1, 3, 4>(p, *dc, s))
+                                 : (two ? run<64, 2, 2, 2, 2, 3>(p, *dc, s) : run<64, 1, 2, 1, 3, 4>(p, *dc, s));
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }
 

@@ -17,6 +17,13 @@ rule on RMSNorm(x).  Every step runs in the library's kernels
 spec_verify_attention, moe_verify_layer, spec_verify_lmhead); this module only
 orders the calls and owns the buffers, so that a verify pass (and a draft +
 verify step) can be replayed as one CUDA graph.
+
+The keys and values stand in contiguous bf16 caches, or, with cache="q4", in the
+paged 4-bit cache: one pool of pages for every layer, one page table for all of
+them (spec_q4_append, spec_q4_attention).  Then reserve() gives every sequence
+its pages before a pass and takes the rejected drafts' pages back after it,
+fork() lets sequences go on from one prefix, and compact() moves the live pages
+together (spec_pages_resize, spec_pages_fork, spec_pages_compact).
 """
 from __future__ import annotations
 
@@ -33,12 +40,16 @@ def _dev(bits, device):
 
 
 class Decoder:
-    """Device weights and per-layer key/value caches [B, L, nh, d] of a synthetic decoder
-    (synth.DecoderProblem).  verify() runs one verify pass over Q positions per sequence, for the
-    first tokens.shape[0] <= B sequences."""
+    """Device weights and per-layer key/value caches of a synthetic decoder (synth.DecoderProblem):
+    [B, L, nh, d] bf16, or with cache="q4" pages of `page` positions, `pages` of them (as many as B
+    sequences of L positions need unless given), all free at first.  verify() runs one verify pass
+    over Q positions per sequence, for the first tokens.shape[0] <= B sequences."""
 
-    def __init__(self, prob, B: int, L: int, device="cuda"):
+    def __init__(self, prob, B: int, L: int, device="cuda", cache: str = "bf16", page: int = 64, pages: int | None = None):
+        if cache not in ("bf16", "q4"):
+            raise ValueError("cache must be 'bf16' or 'q4'")
         self.prob, self.B, self.L, self.device = prob, B, L, device
+        self.cache, self.page = cache, page
         d = prob.dims
         self.H, self.nh = d.H, prob.nh
         self.hd = d.H // prob.nh
@@ -50,9 +61,18 @@ class Decoder:
             t = {n: _dev(lw[n], device) for n in ("w_q", "w_k", "w_v", "w_o")}
             t["moe"] = api.weights(*[_dev(lw[n], device) for n in ("w_router", "w_gate_up", "w_down", "ws_gate_up",
                                                                     "ws_down")])
-            t["kc"] = torch.zeros((B, L, self.nh, self.hd), dtype=torch.bfloat16, device=device)
-            t["vc"] = torch.zeros_like(t["kc"])
+            if cache == "bf16":
+                t["kc"] = torch.zeros((B, L, self.nh, self.hd), dtype=torch.bfloat16, device=device)
+                t["vc"] = torch.zeros_like(t["kc"])
             self.layers.append(t)
+        if cache == "q4":
+            M = -(-L // page)
+            P = B * M if pages is None else pages
+            self.pool = torch.zeros((len(self.layers), P, api.spec_q4_page_bytes(self.nh, self.hd, page)),
+                                    dtype=torch.uint8, device=device)
+            self.table = torch.full((B, M), -1, dtype=torch.int32, device=device)
+            self.ref = torch.zeros(P, dtype=torch.int32, device=device)
+            self.pws = api.spec_pages_workspace(B, M, P, device)
         dw = dict(prob.draft)
         dw["emb"], dw["w_vocab"] = prob.emb, prob.w_vocab
         self.draft_w = {n: (self.emb if n == "emb" else self.w_vocab if n == "w_vocab" else _dev(dw[n], device))
@@ -62,9 +82,30 @@ class Decoder:
     def fill_caches(self, seed: int):
         """N(0, 1) keys and values everywhere (the entries of a prefix that is not replayed)."""
         g = torch.Generator(device=self.device).manual_seed(seed)
+        if self.cache == "q4":
+            full = torch.full((self.B,), self.L, dtype=torch.int32, device=self.device)
+            self.reserve(torch.zeros_like(full), full)
+            for pool in self.pool:
+                k, v = (torch.randn((self.B, self.L, self.nh, self.hd), generator=g, device=self.device).to(torch.bfloat16)
+                        for _ in range(2))
+                api.spec_q4_append(k, v, pool, self.table, full, self.page)
+            return
         for t in self.layers:
             t["kc"].copy_(torch.randn(t["kc"].shape, generator=g, device=self.device).to(torch.bfloat16))
             t["vc"].copy_(torch.randn(t["vc"].shape, generator=g, device=self.device).to(torch.bfloat16))
+
+    def reserve(self, keep, cap, stats=None):
+        """Pages for the positions 0..cap[b]-1 of every sequence, of which keep[b] are kept (int32 [B]); see
+        spec_pages_resize."""
+        api.spec_pages_resize(self.pool, self.table, self.ref, keep, cap, self.page, self.pws, stats=stats)
+
+    def fork(self, parent):
+        """Sequence b goes on from sequence parent[b] (-1: none); int32 [B]."""
+        api.spec_pages_fork(self.table, self.ref, parent, self.pws)
+
+    def compact(self, stats=None):
+        """The live pages to the lowest numbers of the pool."""
+        api.spec_pages_compact(self.pool, self.table, self.ref, self.pws, stats=stats)
 
     def buffers(self, B: int, Q: int):
         """The activations, workspaces and outputs of a pass over Q positions of B sequences."""
@@ -76,7 +117,11 @@ class Decoder:
                                                                                      "a", "o", "y")}
             b["sh"] = api.shape(T, H, d.E, d.k, d.S, d.I)
             b["mws"] = api.workspace(b["sh"], dev)
-            b["aws"] = api.spec_verify_attention_workspace(B, Q, self.L, self.nh, self.hd, dev)
+            if self.cache == "q4":
+                b["aws"] = api.spec_q4_attention_workspace(B, Q, self.table.shape[1], self.page, self.nh, self.nh, self.hd,
+                                                           dev)
+            else:
+                b["aws"] = api.spec_verify_attention_workspace(B, Q, self.L, self.nh, self.hd, dev)
             b["lws"] = api.spec_verify_lmhead_workspace(B, Q - 1, self.V, H, dev)
             b["argmax"] = torch.zeros((B, Q), dtype=torch.int32, device=dev)
             b["alen"] = torch.zeros(B, dtype=torch.int32, device=dev)
@@ -87,7 +132,8 @@ class Decoder:
     def verify(self, tokens, ctx_after, drafts):
         """One verify pass.  tokens [B, Q] int32: input 0 is each sequence's last committed token,
         inputs 1..Q-1 its drafts (drafts [B, Q-1] int32, the same tokens); ctx_after [B] int32: the
-        cache lengths once the Q positions are appended.  Returns the pass's buffers: argmax [B, Q]
+        cache lengths once the Q positions are appended (with the 4-bit cache reserve() comes before, and 0
+        stands for a slot without a sequence).  Returns the pass's buffers: argmax [B, Q]
         (the greedy token after each input), alen [B], comm [B, Q] (the rule's outputs), x [B*Q, H]
         (the last residual stream, the draft block's next input state)."""
         B, Q = tokens.shape
@@ -95,14 +141,20 @@ class Decoder:
         nh, hd = self.nh, self.hd
         api.gather_rows(self.emb, tokens.reshape(-1), out=b["x"])
         y = b["zero"]
-        for t in self.layers:
+        for i, t in enumerate(self.layers):
             api.rmsnorm_residual(b["x"], y, h=b["h"])
             for n in ("q", "k", "v"):
                 api.dense_matmul(b["h"], t["w_" + n], out=b[n])
-            kc, vc = t["kc"][:B], t["vc"][:B]
-            api.spec_cache_append(b["k"].view(B, Q, nh, hd), b["v"].view(B, Q, nh, hd), kc, vc, ctx_after)
-            api.spec_verify_attention(b["q"].view(B, Q, nh, hd), kc, vc, ctx_after, b["aws"],
-                                      out=b["a"].view(B, Q, nh, hd))
+            if self.cache == "q4":
+                api.spec_q4_append(b["k"].view(B, Q, nh, hd), b["v"].view(B, Q, nh, hd), self.pool[i], self.table[:B],
+                                   ctx_after, self.page)
+                api.spec_q4_attention(b["q"].view(B, Q, nh, hd), self.pool[i], self.table[:B], ctx_after, nh, self.page,
+                                      b["aws"], out=b["a"].view(B, Q, nh, hd))
+            else:
+                kc, vc = t["kc"][:B], t["vc"][:B]
+                api.spec_cache_append(b["k"].view(B, Q, nh, hd), b["v"].view(B, Q, nh, hd), kc, vc, ctx_after)
+                api.spec_verify_attention(b["q"].view(B, Q, nh, hd), kc, vc, ctx_after, b["aws"],
+                                          out=b["a"].view(B, Q, nh, hd))
             api.dense_matmul(b["a"], t["w_o"], out=b["o"])
             api.rmsnorm_residual(b["x"], b["o"], h=b["h"])
             api.moe_verify_layer(b["h"], t["moe"], b["sh"], b["mws"], out=b["y"])
@@ -113,7 +165,7 @@ class Decoder:
         return b
 
     def launches_per_verify(self, B: int, Q: int) -> int:
-        """Library kernel launches of one verify pass (the MoE layer: 3 up to 256 tokens)."""
+        """Library kernel launches of one verify pass (the MoE layer: 3 up to 256 tokens; the bf16 cache)."""
         T = B * Q
         moe = 3 if T <= 256 else (4 if T * self.prob.dims.k <= 8192 else 6)
         return 1 + len(self.layers) * (1 + 3 + 1 + 2 + 1 + 1 + moe) + 1 + 2
