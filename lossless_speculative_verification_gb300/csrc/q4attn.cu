@@ -121,7 +121,7 @@ struct QaSmem {
   static constexpr int kWarp = kRing > kMl + kRows * 8 ? kRing : (kMl + kRows * 8 + 15) / 16 * 16;
   static constexpr int kBars = kQaWarps * kWarp;                     // [warp][S] mbarriers
   static constexpr int kHere = kBars + kQaWarps * S * 8;             // [warp][S] which blocks a stage holds
-  static constexpr int kQf = (kHere + kQaWarps * S * 4 + 15) / 16 * 16;  // [NT][W][lane] 16 bytes: the B operands
+  static constexpr int kQf = (kHere + kQaWarps * S * 4 + 15) / 16 * 16;  // [W][NT][lane] 16 bytes: the queries
   static constexpr int kCi = kQf + NT * L::W * 512;           // [G][4 or 8] 16 bytes: where the accumulators start
   static constexpr int kFq = kCi + NT * L::G * 64;            // [8 NT] what turns the scaled sums into log2 scores
   static constexpr int kLim = kFq + kRows * 4;                // [8 NT] last position the row sees
@@ -216,8 +216,9 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
                 &full[s]);
     }
   };
-#pragma unroll 1
-  for (int i = 0; i < S && i < nstages; ++i) issue(i, i);
+  // every warp's first stage before anyone's second: with all stages at once the first arrives behind the others'
+  // later ones (32 x 4 positions over page-shaped caches: after 4.0 us)
+  if (nstages > 0) issue(0, 0);
 
   uint8_t* qs = smem;
   if (warp < NT) {
@@ -247,7 +248,14 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
         const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&v[q]));
         sum[j >> 1] += (back.x + back.y) * ((q & 1) ? 16.0f : 1.0f);
       }
-      *reinterpret_cast<uint4*>(qs + SM::kQf + ((warp * W + j) * 32 + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+      // NT = 1: the B operands of both halves of a word; NT = 2: the A operands of each, rows g and g + 8 by turns
+      if constexpr (NT == 1) {
+        *reinterpret_cast<uint4*>(qs + SM::kQf + (j * 32 + lane) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint32_t*>(qs + SM::kQf + ((2 * j + (q >> 1)) * 32 + lane) * 16 + (2 * (q & 1) + warp) * 4) = v[q];
+      }
     }
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
@@ -265,6 +273,9 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     }
   }
   __syncthreads();
+#pragma unroll 1
+  for (int i = 1; i < S && i < nstages; ++i) issue(i, i);
+  __syncwarp();
   // this lane's two rows: the columns 2t, 2t + 1 (NT = 1), or the rows g and g + 8
   const int row_a = NT == 1 ? 2 * t : g, row_b = NT == 1 ? 2 * t + 1 : g + 8;
   const float fq[2] = {*reinterpret_cast<const float*>(qs + SM::kFq + row_a * 4),
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
         for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
           uint4 qf[NT];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) qf[nt] = *reinterpret_cast<const uint4*>(qs + SM::kQf + ((nt * W + j) * 32 + lane) * 16);
+          for (int i = 0; i < NT; ++i) qf[i] = *reinterpret_cast<const uint4*>(qs + SM::kQf + ((NT * j + i) * 32 + lane) * 16);
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if constexpr (NT == 1) {
@@ -335,9 +346,9 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const uint32_t a = kw[u][e].w[j], a8 = a >> 8;
-                mma_f16_m16n8k16(acc[u][e], qf[0].x, qf[NT - 1].x, qf[0].y, qf[NT - 1].y, a & 0x000F000Fu,
-                                 a & 0x00F000F0u, j == 2 * gr ? start : acc[u][e]);
-                mma_f16_m16n8k16(acc[u][e], qf[0].z, qf[NT - 1].z, qf[0].w, qf[NT - 1].w, a8 & 0x000F000Fu,
+                mma_f16_m16n8k16(acc[u][e], qf[0].x, qf[0].y, qf[0].z, qf[0].w, a & 0x000F000Fu, a & 0x00F000F0u,
+                                 j == 2 * gr ? start : acc[u][e]);
+                mma_f16_m16n8k16(acc[u][e], qf[NT - 1].x, qf[NT - 1].y, qf[NT - 1].z, qf[NT - 1].w, a8 & 0x000F000Fu,
                                  a8 & 0x00F000F0u, acc[u][e]);
               }
             }
