@@ -258,9 +258,11 @@ lsv_status spec_cache_append(const void *k_new, const void *v_new, void *k_cache
  *   ctx_len[b] reaches an output, whatever the pages hold there.  A row's result
  *   depends on its query, its visible positions, B, nkv and M*page, and not on
  *   the other rows.  1 <= Q <= 8, nh / nkv <= 16, B <= 65535, B*nkv <= 262144,
- *   scale > 0, |q| < 2^112.  One launch, or two where a sequence is split.
- *   ws: spec_q4_attention_workspace_size(...) bytes (0: unsupported); needs no
- *   initialisation.
+ *   scale > 0, |q| < 2^112.  One launch, or two where a sequence is split far.
+ *   ws: spec_q4_attention_workspace_size(...) bytes (0: unsupported).  Its first
+ *   64 KiB hold counters, at the same place for every shape: zero before the first
+ *   use; every call leaves them zero again, so one workspace serves any later call
+ *   whose size fits.
  * Device pointers, 16-byte aligned. */
 size_t spec_q4_page_bytes(int32_t nkv, int32_t d, int32_t page);
 lsv_status spec_q4_append(const void *k_new, const void *v_new, void *pool, const int32_t *table,

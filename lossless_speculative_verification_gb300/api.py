@@ -265,10 +265,11 @@ def spec_q4_read(pool, table, ctx_len, N, nkv, d, page, k=None, v=None, stream=N
 
 
 def spec_q4_attention_workspace(B, Q, M, page, nh, nkv, d, device=None) -> torch.Tensor:
+    """Workspace of spec_q4_attention, zeroed (its counters must start at zero; every call leaves them zero)."""
     n = _ffi.load().spec_q4_attention_workspace_size(B, Q, M, page, nh, nkv, d)
     if n == 0:
         raise ValueError("unsupported 4-bit attention shape")
-    return torch.empty(int(n), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(int(n), dtype=torch.uint8, device=device or "cuda")
 
 
 def spec_q4_attention(q, pool, table, ctx_len, nkv, page, ws, scale=None, out=None, stream=None):

@@ -46,6 +46,8 @@ constexpr int kQaThreads = kQaWarps * 32;
 constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
 constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
 constexpr float kQaLog2e = 1.4426950408889634f;
+constexpr int kQaCounters = 16384;  // tiles of rows whose CTAs may be counted; their counters lead the workspace
+constexpr int kQaMaxTiles = 8;      // tiles of 16 rows of a key head, at most (8 queries x 16 heads)
 constexpr int kQaMaxSteps = 4096;  // steps of 128 positions in a chunk, at most
 
 struct QaParams {
@@ -58,6 +60,7 @@ struct QaParams {
   int chunk, nchunk;  // positions of a chunk (a multiple of 16 kQaWarps), chunks of a sequence
   float scale_log2;   // scale * log2(e)
   bf16* out;          // [B, Q, nh, D]
+  int* arrived;       // [B * nkv * rblocks] CTAs that have written their state; 0 before and after a call
   float* o_part;      // [B * nkv, nchunk, R, D]
   float* ml_part;     // [B * nkv, nchunk, R, 2]: maximum (log2 units), sum
   int* err;
@@ -70,8 +73,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-// How the chunks' states meet: there is one chunk, the chunks' CTAs are a cluster, or a second kernel merges them.
-enum : int { kQaDirect = 0, kQaCluster = 1, kQaParts = 2 };
+// How the chunks' states meet: there is one chunk, the chunks' CTAs are a cluster, the last CTA of a tile of rows to
+// arrive merges them, or a second kernel does.
+enum : int { kQaDirect = 0, kQaCluster = 1, kQaLast = 2, kQaParts = 3 };
 constexpr int kQaCluster8 = 8;  // chunks of a cluster, at most
 
 // A state of four output columns of a row: maximum, sum, unnormalised output.
@@ -97,6 +101,33 @@ struct QaState {
     *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Q + row / p.grp) * p.nh + h * p.grp + row % p.grp) * D + 4 * c4) = v;
   }
 };
+
+// The chunks' states of four output columns of a row, brought to their common maximum and summed.
+constexpr int kQcUnroll = 8;
+__device__ __forceinline__ QaState merge_parts(const QaParams& p, int parts, int bh, int row, int D, int c4) {
+  const float2* ml = reinterpret_cast<const float2*>(p.ml_part) + (size_t)bh * p.nchunk * p.R;
+  const float4* o4 = reinterpret_cast<const float4*>(p.o_part) + (size_t)bh * p.nchunk * p.R * (D / 4);
+  QaState all;
+  for (int s0 = 0; s0 < parts; s0 += kQcUnroll) {
+    float2 a[kQcUnroll];
+    float4 v[kQcUnroll];
+#pragma unroll
+    for (int u = 0; u < kQcUnroll; ++u) {
+      const bool in = s0 + u < parts;
+      a[u] = in ? __ldcg(ml + (size_t)(s0 + u) * p.R + row) : make_float2(-INFINITY, 0.0f);
+      v[u] = in ? __ldcg(o4 + ((size_t)(s0 + u) * p.R + row) * (D / 4) + c4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    QaState acc;
+    acc.m = all.m;
+#pragma unroll
+    for (int u = 0; u < kQcUnroll; ++u) acc.m = fmaxf(acc.m, a[u].x);
+    acc.add(make_float2(all.m, all.l), all.o);
+#pragma unroll
+    for (int u = 0; u < kQcUnroll; ++u) acc.add(a[u], v[u]);
+    all = acc;
+  }
+  return all;
+}
 
 // Bits of the larger of a position's value scales, a NaN one left out.
 __device__ __forceinline__ uint32_t larger_scale(uint32_t s) {
@@ -183,7 +214,8 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   const bool bad = n < 0 || n > (p.M << p.page_shift);
   if (bad && threadIdx.x == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
   const int end = bad ? 0 : min(n, t_begin + p.chunk);
-  if (p.mode == kQaParts && t_begin >= end) return;  // the combine reads no state of it
+  const int parts = bad ? 0 : (n + p.chunk - 1) / p.chunk;
+  if (p.mode >= kQaLast && split >= max(parts, 1)) return;  // nobody reads a state of it
 
   // ---- the ring
   const int nsteps = first < end ? (end - first + kRound - 1) / kRound : 0;
@@ -582,9 +614,9 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     }
 #pragma unroll
     for (int w = 0; w < kQaWarps; ++w) acc.add(ml[w], *(at0 + w * (SM::kWarp / 16)));
-    if (p.mode == kQaDirect) {
+    if (p.mode == kQaDirect || (p.mode == kQaLast && parts <= 1)) {
       acc.store(p, b, h, row, D, c4);
-    } else if (p.mode == kQaParts) {
+    } else if (p.mode != kQaCluster) {
       const size_t at = ((size_t)bh * p.nchunk + split) * p.R + row;
       *reinterpret_cast<float4*>(p.o_part + at * D + 4 * c4) = acc.o;
       if (c4 == 0) *reinterpret_cast<float2*>(p.ml_part + at * 2) = make_float2(acc.m, acc.l);
@@ -593,20 +625,39 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       if (c4 == 0) *reinterpret_cast<float2*>(smem + SM::kMlAll + 8 * r) = make_float2(acc.m, acc.l);
     }
   }
+  if constexpr (NT == 1) {
+    if (p.mode == kQaLast && parts > 1) {
+      __shared__ int last;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        int* count = p.arrived + blockIdx.x;
+        last = atomicAdd(count, 1) == parts - 1;
+        if (last) *count = 0;  // as the next call wants it
+      }
+      __syncthreads();
+      if (!last) return;
+      __threadfence();
+      for (int i = threadIdx.x; i < nrows * (D / 4); i += kQaThreads) {
+        const int r = i / (D / 4), c4 = i - r * (D / 4);
+        merge_parts(p, parts, bh, r0 + r, D, c4).store(p, b, h, r0 + r, D, c4);
+      }
+    }
+  }
   if (p.mode != kQaCluster) return;
   // ---- the chunks' CTAs are a cluster: each takes a share of the outputs and reads it from all of them
   cluster_sync();
-  const int parts = min(p.nchunk, max(1, bad ? 0 : (n + p.chunk - 1) / p.chunk));
-  if (split < parts) {
+  const int live = max(1, parts);
+  if (split < live) {
     const uint32_t mine = smem_u32(smem);
-    for (int i = split * kQaThreads + threadIdx.x; i < nrows * (D / 4); i += parts * kQaThreads) {
+    for (int i = split * kQaThreads + threadIdx.x; i < nrows * (D / 4); i += live * kQaThreads) {
       const int r = i / (D / 4), c4 = i - r * (D / 4);
       float2 ml[kQaCluster8];
       float4 v[kQaCluster8];
       QaState acc;
 #pragma unroll
       for (int k = 0; k < kQaCluster8; ++k)
-        if (k < parts) {
+        if (k < live) {
           const uint32_t at = mapa_shared(mine, k);
           ml[k] = ld_shared_cluster_f2(at + SM::kMlAll + 8 * r);
           v[k] = ld_shared_cluster_f4(at + (r * SM::kStride + 4 * c4) * 4);
@@ -614,16 +665,15 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
         }
 #pragma unroll
       for (int k = 0; k < kQaCluster8; ++k)
-        if (k < parts) acc.add(ml[k], v[k]);
+        if (k < live) acc.add(ml[k], v[k]);
       acc.store(p, b, h, r0 + r, D, c4);
     }
   }
   cluster_sync();  // no CTA leaves while another reads its memory
 }
 
-// Per (key head, sequence): the chunks' states brought to their common maximum and summed.
+// Per (key head, sequence): the chunks' states merged.
 constexpr int kQcThreads = 128;
-constexpr int kQcUnroll = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaParams p) {
@@ -633,30 +683,9 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
   const int n = __ldcg(p.ctx_len + b);
   const bool bad = n < 0 || n > (p.M << p.page_shift);
   const int parts = bad ? 0 : (n + p.chunk - 1) / p.chunk;
-  const float2* ml = reinterpret_cast<const float2*>(p.ml_part) + (size_t)bh * p.nchunk * p.R;
-  const float4* o4 = reinterpret_cast<const float4*>(p.o_part) + (size_t)bh * p.nchunk * p.R * (D / 4);
   for (int i = blockIdx.y * kQcThreads + threadIdx.x; i < p.R * (D / 4); i += gridDim.y * kQcThreads) {
     const int row = i / (D / 4), c4 = i - row * (D / 4);
-    QaState all;
-    for (int s0 = 0; s0 < parts; s0 += kQcUnroll) {
-      float2 a[kQcUnroll];
-      float4 v[kQcUnroll];
-#pragma unroll
-      for (int u = 0; u < kQcUnroll; ++u) {
-        const bool in = s0 + u < parts;
-        a[u] = in ? __ldcg(ml + (size_t)(s0 + u) * p.R + row) : make_float2(-INFINITY, 0.0f);
-        v[u] = in ? __ldcg(o4 + ((size_t)(s0 + u) * p.R + row) * (D / 4) + c4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
-      QaState acc;
-      acc.m = all.m;
-#pragma unroll
-      for (int u = 0; u < kQcUnroll; ++u) acc.m = fmaxf(acc.m, a[u].x);
-      acc.add(make_float2(all.m, all.l), all.o);
-#pragma unroll
-      for (int u = 0; u < kQcUnroll; ++u) acc.add(a[u], v[u]);
-      all = acc;
-    }
-    all.store(p, b, h, row, D, c4);
+    merge_parts(p, parts, bh, row, D, c4).store(p, b, h, row, D, c4);
   }
 }
 
@@ -664,8 +693,8 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
 // how the chunks meet.  Many chunks fill the GPU and make the chains of steps short, but each costs its CTA about
 // as much as three steps (queries, first loads, the states' meeting): the cut with the least rounds of CTAs (three
 // an SM; one at least) times steps of a round.  Where all CTAs are on the GPU at once and a sequence has at most
-// eight, its chunks are a cluster; else a second kernel merges them, about three steps more (clusters that wait for
-// room leave SMs idle).  Measured: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 14.0 us,
+// eight, its chunks are a cluster; else the last CTA of up to eight merges them, for up to eight rows (clusters that
+// wait for room leave SMs idle), and otherwise a second kernel, about three steps more.  All add in the same order.  Measured: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 14.0 us,
 // 8 merged by a kernel 15.7, 4 chunks 18.9; 32 of up to 2304, 10 key heads: 2 chunks 23.5, 1 chunk 27.4, 4 chunks
 // 24.5 (in clusters 30.3); 16 of 32K, 8 key heads: 7 chunks 148 (in clusters 186), 16 chunks 154.
 // The cut goes by the capacity (the lengths are on the device) and not by Q or the shared heads, so a row is
@@ -683,7 +712,7 @@ Cut cut_of(int B, int nkv, long long cap) {
     k = k < most ? most : k > steps ? steps : k;
     const long long len = (steps + k - 1) / k, used = (steps + len - 1) / len;
     const long long cost = (pairs * used > kSlots ? pairs * used : kSlots) * (len + kCost) +
-                           (used == 1 || clustered(used) ? 0 : kTwo * kSlots);
+                           (used == 1 || clustered(used) ? 0 : (used <= kQcUnroll ? 1 : kTwo) * kSlots);
     if (cost < best) best = cost, at = len;
   };
   consider(1);
@@ -692,7 +721,10 @@ Cut cut_of(int B, int nkv, long long cap) {
   Cut c;
   c.chunk = (int)(at * kRound);
   c.nchunk = (int)((steps + at - 1) / at);
-  c.mode = c.nchunk == 1 ? kQaDirect : clustered(c.nchunk) ? kQaCluster : kQaParts;
+  c.mode = c.nchunk == 1 ? kQaDirect
+           : clustered(c.nchunk) ? kQaCluster
+           : c.nchunk <= kQcUnroll && pairs * kQaMaxTiles <= kQaCounters ? kQaLast
+                                                                         : kQaParts;
   return c;
 }
 
@@ -743,8 +775,8 @@ size_t spec_q4_attention_workspace_size(int32_t B, int32_t Q, int32_t M, int32_t
                                         int32_t d) {
   if (!shape_ok(B, Q, M, page, nh, nkv, d)) return 0;
   const Cut cut = cut_of(B, nkv, (long long)M * page);
-  const size_t parts = cut.mode == kQaParts ? (size_t)B * nkv * cut.nchunk * (Q * (nh / nkv)) : 0;
-  return 256 + round256(parts * d * 4) + round256(parts * 2 * 4);
+  const size_t parts = cut.mode >= kQaLast ? (size_t)B * nkv * cut.nchunk * (Q * (nh / nkv)) : 0;
+  return kQaCounters * 4 + round256(parts * d * 4) + round256(parts * 2 * 4);
 }
 
 lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* table, const int32_t* ctx_len, int32_t B,
@@ -779,12 +811,14 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   const Cut cut = cut_of(B, nkv, (long long)M * page);
   p.chunk = cut.chunk;
   p.nchunk = cut.nchunk;
-  p.mode = cut.mode;
+  // (merging up to sixteen rows keeps a last CTA for longer than a second kernel takes: 137 us for 133.5)
+  p.mode = cut.mode == kQaLast && p.R > 8 ? kQaParts : cut.mode;
   p.scale_log2 = scale * kQaLog2e;
   p.out = static_cast<bf16*>(out);
   const size_t parts = (size_t)B * nkv * p.nchunk * p.R;
-  p.o_part = static_cast<float*>(ws);
-  p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(parts * d * 4));
+  p.arrived = static_cast<int*>(ws);
+  p.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kQaCounters * 4);
+  p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kQaCounters * 4 + round256(parts * d * 4));
   p.err = dc->err;
   p.wait_ns = wait_limit_ns();
   const bool two = p.R > 8;  // the rows of an MMA, or its columns (half the MMAs for up to eight rows)

@@ -201,6 +201,25 @@ def test_attention_long(d, Q, nkv, grp, n):
     check(c, queries(c, Q, grp))
 
 
+# how a sequence's chunks meet goes by the batch, the key heads and the capacity: one chunk; a cluster; the last CTA of
+# several rounds of them; a second kernel
+@pytest.mark.parametrize("lens,nkv,page,M", [
+    ((100, 0, 128), 2, 32, 4),
+    ((900, 1024, 1, 0, 517), 2, 64, 16),
+    (tuple(range(30, 1230, 40)), 10, 64, 20),
+    ((3000, 17, 9000, 6000), 1, 128, 80),
+])
+@pytest.mark.parametrize("Q,grp", [(2, 1), (3, 4)])
+def test_attention_however_the_chunks_meet(lens, nkv, page, M, Q, grp):
+    c = Cache(lens, nkv, 64, page, M=M)
+    q = queries(c, Q, grp)
+    got = check(c, q)
+    ws = api.spec_q4_attention_workspace(c.B, Q, M, page, nkv * grp, nkv, 64)
+    for _ in range(3):                                          # the order in which CTAs end does not show
+        np.testing.assert_array_equal(c.attend(q, ws=ws), got)
+    assert int(ws[:65536].count_nonzero()) == 0
+
+
 def test_attention_peaked_and_scaled():
     c = Cache([700, 333], 2, 128, 32, seed=4)
     check(c, queries(c, 4, 2, std=6.0), what="peaked")
@@ -316,9 +335,11 @@ def test_empty_batch_streams_graphs_and_one_workspace_for_all():
     assert api.spec_q4_attention(q, c.pool, none, i32([]), 2, 16, ws).shape == (0, 2, 2, 64)
     a, b = queries(c, 1, 2), queries(c, 8, 1, seed=2)
     ra, rb = c.attend(a), c.attend(b)
-    ws.fill_(255)
-    np.testing.assert_array_equal(c.attend(a, ws=ws), ra)
-    np.testing.assert_array_equal(c.attend(b, ws=ws), rb)
+    ws[65536:].fill_(255)                                       # behind the counters nothing is wanted
+    for _ in range(2):
+        np.testing.assert_array_equal(c.attend(a, ws=ws), ra)
+        np.testing.assert_array_equal(c.attend(b, ws=ws), rb)
+    assert int(ws[:65536].count_nonzero()) == 0
     side = torch.cuda.Stream()
     out = torch.empty((2, 8, 2, 64), dtype=torch.bfloat16, device="cuda")
     torch.cuda.synchronize()
