@@ -255,11 +255,17 @@ def spec_q4_read(pool, table, ctx_len, N, nkv, d, page, k=None, v=None, stream=N
     dev = torch.cuda.current_device()
     B = table.shape[0]
     M, P = _q4_sizes(pool, table, ctx_len, B, nkv, d, page)
-    k = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device) if k is None else k
-    v = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device) if v is None else v
-    _need_shape(k, (B, N, nkv, d), "k"); _need_shape(v, (B, N, nkv, d), "v")
-    pl, tb, cl, kp, vp = _here(dev, (pool, torch.uint8, "pool"), (table, torch.int32, "table"),
-                               (ctx_len, torch.int32, "ctx_len"), (k, torch.bfloat16, "k"), (v, torch.bfloat16, "v"))
+    pl, tb, cl = _here(dev, (pool, torch.uint8, "pool"), (table, torch.int32, "table"), (ctx_len, torch.int32, "ctx_len"))
+    out = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t is None:
+            t = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device)
+        else:
+            _need_shape(t, (B, N, nkv, d), name)
+            _here(dev, (t, torch.bfloat16, name))
+        out.append(t)
+    k, v = out
+    kp, vp = k.data_ptr(), v.data_ptr()
     check("spec_q4_read", _ffi.load().spec_q4_read(pl, tb, cl, B, N, nkv, d, page, M, P, kp, vp, _stream_of(dev, stream)))
     return k, v
 

@@ -414,11 +414,9 @@ struct PgCompact {
   int* err;
 };
 
-__global__ void __launch_bounds__(kPgThreads) compact_count_kernel(const PgCompact p) {
-  __shared__ int tmp[kPgWarps];
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Chunk c of the counts: its bit map and the number of live pages.
+__device__ __forceinline__ void compact_count(const PgCompact& p, int c, int* tmp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int n = 0, refs[kPgChunkWords / kPgWarps];
   load_chunk(p.ref, p.P, c, refs);
 #pragma unroll
@@ -434,6 +432,13 @@ __global__ void __launch_bounds__(kPgThreads) compact_count_kernel(const PgCompa
   if (threadIdx.x == 0) p.w.chunk_n[c] = n;
 }
 
+__global__ void __launch_bounds__(kPgThreads) compact_count_kernel(const PgCompact p) {
+  __shared__ int tmp[kPgWarps];
+  pdl_wait();
+  pdl_trigger();
+  compact_count(p, blockIdx.x, tmp);
+}
+
 // Chunk c: the k-th free page below the live count goes to list2[k], the k-th live one at or above it to
 // list[k].  Live pages below the count are as many as the count less the pages that move.
 __global__ void __launch_bounds__(kPgThreads) compact_list_kernel(const PgCompact p) {
@@ -441,6 +446,10 @@ __global__ void __launch_bounds__(kPgThreads) compact_list_kernel(const PgCompac
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x;
+  if (p.chunks == 1) {  // a pool of one chunk needs no launch before this one
+    compact_count(p, 0, tmp);
+    __syncthreads();
+  }
   int before;
   const int live = sum_upto(p.w.chunk_n, p.chunks, c, &before, tmp);
   // live pages below number `live`
@@ -618,7 +627,8 @@ lsv_status spec_pages_fork(const int32_t* table, const int32_t* ref, const int32
   p.old = w.table;
   p.err = dc->err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(fork_save_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, p);
+  cudaError_t e = cudaSuccess;
+  if (table_out == table || ref_out != ref) e = launch_pdl(fork_save_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, p);
   if (e == cudaSuccess && B > 0) e = launch_pdl(fork_rows_kernel, dim3(B), dim3(kPgThreads), 0, s, p);
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }
@@ -658,7 +668,8 @@ lsv_status spec_pages_compact(void* pool, int32_t layers, int64_t page_bytes, co
   p.copy.page_bytes = (size_t)page_bytes;
   p.copy.copied = nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(compact_count_kernel, dim3(p.chunks), dim3(kPgThreads), 0, s, p);
+  cudaError_t e = cudaSuccess;
+  if (p.chunks > 1) e = launch_pdl(compact_count_kernel, dim3(p.chunks), dim3(kPgThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(compact_list_kernel, dim3(p.chunks), dim3(kPgThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(compact_move_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, p);
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
