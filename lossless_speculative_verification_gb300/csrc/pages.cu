@@ -219,12 +219,13 @@ __global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResiz
   const int b = blockIdx.x;
   int first, unused;
   const int need = sum_upto(p.w.need, p.B, b, &first, tmp);
-  const int mine = __ldcg(p.w.need + b);
+  const int mine = b < p.B ? __ldcg(p.w.need + b) : 0;
   const int free = sum_upto(p.w.chunk_n, p.chunks, 0, &unused, tmp);
   if (b == 0 && threadIdx.x == 0) {
     if (p.stats) p.stats[0] = need, p.stats[1] = free;
     if (need > free) set_error(p.err, kErrPages);
   }
+  if (b >= p.B) return;  // no rows at all
   int keep, cap;
   const bool ok = row_bounds(p, b, &keep, &cap) && need <= free;
   const int32_t* row = p.table + (size_t)b * p.M;
@@ -598,7 +599,7 @@ lsv_status spec_pages_resize(void* pool, int32_t layers, int64_t page_bytes, con
   c.copied = stats_opt ? stats_opt + 2 : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(resize_count_kernel, dim3(B > p.chunks ? B : p.chunks), dim3(kPgThreads), 0, s, p);
-  if (e == cudaSuccess && B > 0) e = launch_pdl(resize_assign_kernel, dim3(B), dim3(kPgThreads), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(resize_assign_kernel, dim3(B > 0 ? B : 1), dim3(kPgThreads), 0, s, p);
   if (e == cudaSuccess && B > 0) e = launch_pdl(copy_pages_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, c);
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }

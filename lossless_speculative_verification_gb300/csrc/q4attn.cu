@@ -13,8 +13,8 @@
 //   places' share by 1/16; the accumulators start at -8 * 2^-24 * sum(q) of the
 //   group, which takes the 8 off; the group's scale multiplies the fp32 sum.
 //   values: P times the position's scale is the f16 operand.  sum(P s) of every
-//   group, from one more MMA with ones, takes the 8 off at the end, and the rows
-//   of the odd places are divided by 16 there.
+//   group, from one more MMA with ones, takes the 8 off every 16 steps, and the
+//   rows of the odd places are divided by 16 at the end.
 // To keep P s in the range of f16 whatever the scales are, the running maximum
 // is taken over score + exponent of the largest value scale, and P is 2^8 at it.
 // It follows the true one only where that rises by more than a factor 2^6 (the
@@ -46,9 +46,10 @@ constexpr int kQaThreads = kQaWarps * 32;
 constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
 constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
 constexpr float kQaLog2e = 1.4426950408889634f;
+constexpr int kQaCentre = 16;       // steps between two centrings
 constexpr int kQaCounters = 16384;  // tiles of rows whose CTAs may be counted; their counters lead the workspace
 constexpr int kQaMaxTiles = 8;      // tiles of 16 rows of a key head, at most (8 queries x 16 heads)
-constexpr int kQaMaxSteps = 4096;  // steps of 128 positions in a chunk, at most
+constexpr int kQaMaxSteps = 256;    // steps of 128 positions in a chunk, at most: 512 sums in a row in an accumulator
 
 struct QaParams {
   const bf16* q;           // [B, Q, nh, D]
@@ -536,6 +537,25 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     }
   };
 
+  // Takes the 8 of the nibbles off what is summed so far.  Left to the end, the sums of n + 8 of a long chunk would
+  // be hundreds of times those of n, and lose as many times their last bit (32768 positions of about equal weight:
+  // 7.2e-3 of the output, against 1.7e-3 of its own rounding).
+  auto centre = [&]() {
+    constexpr float kEven = -8.0f / 16777216.0f, kOdd = -8.0f / 1048576.0f;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool odd = NT == 1 ? c >= 2 : (i & 1) != 0;
+        const int gr = (NT == 1 ? i / 2 : i / 4) >> 1;
+        o[i][c] = fmaf(cs[gr][NT == 1 ? (c & 1) : 2 * (c >> 1)], odd ? kOdd : kEven, o[i][c]);
+      }
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) cs[gr][c] = 0.0f;
+  };
+
   int done = 0, st = 0;
   uint32_t phase = 0;
 #pragma unroll 1
@@ -554,6 +574,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
         step(std::true_type{}, blk, pos0, gone);
       else
         step(std::false_type{}, blk, pos0, 0);
+      if ((done * K + k) % kQaCentre == kQaCentre - 1) centre();
     }
     __syncwarp();  // every lane has read the stage
     if (done + S < nstages) issue(done + S, st);

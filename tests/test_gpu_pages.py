@@ -222,8 +222,9 @@ def test_no_rows():
     none, e = i32(np.zeros((0, 3))), i32([])
     pool, r = torch.zeros((1, 10, 16), dtype=torch.uint8, device="cuda"), i32([0] * 9 + [2])
     out = torch.full((10,), -7, dtype=torch.int32, device="cuda")
-    api.spec_pages_resize(pool, none, r, e, e, 4, ws, ref_out=out)
-    assert torch.equal(out, r)
+    st = torch.full((4,), -7, dtype=torch.int32, device="cuda")
+    api.spec_pages_resize(pool, none, r, e, e, 4, ws, ref_out=out, stats=st)
+    assert torch.equal(out, r) and host(st).tolist() == [0, 9, 0, 0]
     out.fill_(-7)
     api.spec_pages_fork(none, r, e, ws, ref_out=out)
     assert torch.equal(out, r)

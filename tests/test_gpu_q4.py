@@ -4,7 +4,7 @@ Codes, scales and their places are exact (bytes are compared).  The attention's 
 what the kernel rounds (A = sum p |v|, S = sum p s, the weights' mean of |v| and of the scales):
   the output to bf16                                     2^-8 |out|
   the weights P s to f16 (half a step, 2^-11)            2^-11 A
-  the fp32 sums over codes 0..15 that take 8 S off at the end: at most 64 MMAs in a row in a warp, each adding its
+  the fp32 sums over codes 0..15 from which 8 S are taken: at most 64 MMAs in a row in a warp, each adding its
   16 products and its accumulator at 2^-23 of the largest       64 * 2^-23 * (15 + 8) S < 2^-12 S
   scores in fp32, of size X = scale sum |q k|: d + 8 roundings at 2^-23, twice (numerator and sum): 2 * 136 * 2^-23 X A
 """
@@ -209,15 +209,41 @@ def test_attention_long(d, Q, nkv, grp, n):
     (tuple(range(30, 1230, 40)), 10, 64, 20),
     ((3000, 17, 9000, 6000), 1, 128, 80),
 ])
-@pytest.mark.parametrize("Q,grp", [(2, 1), (3, 4)])
-def test_attention_however_the_chunks_meet(lens, nkv, page, M, Q, grp):
-    c = Cache(lens, nkv, 64, page, M=M)
+@pytest.mark.parametrize("d,Q,grp", [(64, 2, 1), (64, 3, 4), (128, 1, 2), (128, 1, 9)])
+def test_attention_however_the_chunks_meet(lens, nkv, page, M, d, Q, grp):
+    c = Cache(lens, nkv, d, page, M=M)
     q = queries(c, Q, grp)
     got = check(c, q)
-    ws = api.spec_q4_attention_workspace(c.B, Q, M, page, nkv * grp, nkv, 64)
+    ws = api.spec_q4_attention_workspace(c.B, Q, M, page, nkv * grp, nkv, d)
     for _ in range(3):                                          # the order in which CTAs end does not show
         np.testing.assert_array_equal(c.attend(q, ws=ws), got)
     assert int(ws[:65536].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("Q,grp", [(1, 1), (3, 5)])
+def test_sums_over_the_longest_chunk(Q, grp):
+    # 456 (sequence, key head) pairs: one chunk each, of 32768 positions; flat weights over values of mean 0, where a
+    # sum that loses its low bits shows.  32 MMAs between two times that the 8 S are taken off (32 * 2^-23 * 23 S),
+    # 512 MMAs into an accumulator that has them off (512 * 2^-23 A)
+    lens = [0] * 56 + [32768]
+    rs = np.random.default_rng(0)
+    k, v = (rs.normal(size=(1, 32768, 8, 64)) for _ in range(2))
+    one = Cache([32768], 8, 64, 128, k=k, v=v)
+    q = np.zeros((57, Q, 8 * grp, 64), np.uint16)
+    q[56] = bits(rs.normal(size=(Q, 8 * grp, 64)) * 0.05)
+    table = np.full((57, one.M), -1, np.int32)
+    table[56] = one.tb
+    ws = api.spec_q4_attention_workspace(57, Q, one.M, 128, 8 * grp, 8, 64)
+    got = api.spec_q4_attention(dev(q), one.pool, i32(table), i32(lens), 8, 128, ws).float().cpu().numpy().astype(np.float64)
+    assert (got[:56] == 0).all()
+    kf, vf = one.values()
+    ref, A = q4.attention(q4.bf16_f64(q[56:]), kf, vf, one.lens, 1 / 8)
+    S = np.repeat(q4.bf16_f64(q4.quantise(one.v)[1]), 64, -1).max()
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -11 * A + 32 * 2.0 ** -23 * 23 * S + (512 + 272) * 2.0 ** -23 * A
+    assert (np.abs(got[56:] - ref) <= tol).all()
+    # over all elements little more than the rounding of the output, whose steps' rms is 2^-8 / sqrt(3) of the power of
+    # two below a value, and so at most that of the value
+    assert np.linalg.norm(got[56:] - ref) <= 2.0 ** -8 / np.sqrt(3) * np.linalg.norm(ref)
 
 
 def test_attention_peaked_and_scaled():
