@@ -92,43 +92,37 @@ struct QwParams {
   int* err;
 };
 
-// The warp's (sequence, block, head) and the block's place; false: nothing there (*bad: an index out of range).
+// A CTA's (sequence, block, head), and the entry of the block's page.  The entry's load is only begun here: what
+// depends on the length alone (the rows to append) is loaded beside it.
 struct QwPlace {
   int b, h, n, p0, block;
-  size_t at;  // in blocks
+  bool any;  // some position of the block exists and is one of the Q
+  int pg;
 };
-__device__ __forceinline__ bool place(const QwParams& p, int unit, QwPlace* w, bool* bad) {
-  w->h = unit % p.nkv;
+__device__ __forceinline__ bool length_ok(const QwParams& p, int n) { return n >= 0 && n <= (p.M << p.page_shift); }
+__device__ __forceinline__ QwPlace place(const QwParams& p, int unit) {
+  QwPlace w;
+  w.h = unit % p.nkv;
   const int r = unit / p.nkv;
-  w->b = r / p.nblk;
-  const int bi = r - w->b * p.nblk;
-  w->n = __ldcg(p.ctx_len + w->b);
-  *bad = false;
-  if (w->n < 0 || w->n > (p.M << p.page_shift)) {
-    *bad = true;
-    return false;
-  }
-  w->p0 = w->n - p.Q;
-  w->block = q4_floor_block(w->p0) + bi;
-  if (w->block < 0 || (w->block << 4) >= w->n) return false;
-  const int pg = __ldcg(p.table + (size_t)w->b * p.M + ((w->block << 4) >> p.page_shift));
-  if (pg < 0 || pg >= p.P) {
-    *bad = true;
-    return false;
-  }
+  w.b = r / p.nblk;
+  const int bi = r - w.b * p.nblk;
+  w.n = __ldcg(p.ctx_len + w.b);
+  w.p0 = w.n - p.Q;
+  w.block = q4_floor_block(w.p0) + bi;
+  w.any = length_ok(p, w.n) && w.block >= 0 && (w.block << 4) < w.n;
+  w.pg = w.any ? __ldcg(p.table + (size_t)w.b * p.M + ((w.block << 4) >> p.page_shift)) : -1;
+  return w;
+}
+// The block's place in the pool, in blocks.
+__device__ __forceinline__ size_t block_of(const QwParams& p, const QwPlace& w) {
   const int per = 1 << (p.page_shift - 4);  // blocks of a page and head
-  w->at = ((size_t)pg * p.nkv + w->h) * per + (w->block & (per - 1));
-  return true;
+  return ((size_t)w.pg * p.nkv + w.h) * per + (w.block & (per - 1));
 }
 
 // Keys of 8 positions: lane (g, t) has the dims 32 j + 8 t + 0..7 of position tk = 8 half + g.
 template <int D>
-__device__ __forceinline__ void append_keys(const bf16* __restrict__ src, bool in, uint8_t* blk, int tk, int t) {
+__device__ __forceinline__ void append_keys(const uint4 (&x)[Q4Block<D>::W], bool in, uint8_t* blk, int tk, int t) {
   using L = Q4Block<D>;
-  uint4 x[L::W];
-#pragma unroll
-  for (int j = 0; j < L::W; ++j)
-    x[j] = in ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * t)) : make_uint4(0u, 0u, 0u, 0u);
   Q4Words<L::W> out;
   uint32_t sc = 0;
   Step st[L::G];
@@ -163,16 +157,10 @@ __device__ __forceinline__ void append_keys(const bf16* __restrict__ src, bool i
 
 // Values of 8 positions: lane (g, t) has the dims 32 m + 4 g + 0..3 of position 8 half + 2 t and the one after it.
 template <int D>
-__device__ __forceinline__ void append_values(const bf16* __restrict__ src, size_t row, const bool (&in)[2], uint8_t* blk,
-                                              int half, int lane) {
+__device__ __forceinline__ void append_values(const uint2 (&x)[2][Q4Block<D>::W], const bool (&in)[2], uint8_t* blk, int half,
+                                              int lane) {
   using L = Q4Block<D>;
   const int g = lane >> 2, t = lane & 3;
-  uint2 x[2][L::W];
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int m = 0; m < L::W; ++m)
-      x[e][m] = in[e] ? __ldg(reinterpret_cast<const uint2*>(src + e * row + 32 * m + 4 * g)) : make_uint2(0u, 0u);
   Q4Words<L::W> out;
   Step st[2][L::G];
   bool plain = true;
@@ -216,35 +204,55 @@ __device__ __forceinline__ void append_values(const bf16* __restrict__ src, size
   }
 }
 
+// Twelve CTAs an SM: a CTA is one chain of loads (length, entry and rows, then the codes), and what is in flight on
+// an SM is what its CTAs have begun (eight prompts of 1156 positions: 16 us with ten, 15 with twelve).
 // A warp's share is a half block (8 positions) of the keys or of the values: the four parts of a block are the
 // CTA's warps.  Whole blocks a warp took 7.9 us for 32 x 4 positions of 10 heads, quarters 4.1 us: the call is as
 // long as one warp's chain of loads, maxima and codes.
 template <int D>
-__global__ void __launch_bounds__(kQwWarps * 32) q4_append_kernel(const bf16* __restrict__ k_new,
+__global__ void __launch_bounds__(kQwWarps * 32, 12) q4_append_kernel(const bf16* __restrict__ k_new,
                                                                   const bf16* __restrict__ v_new, uint8_t* pool,
                                                                   const QwParams p) {
   using L = Q4Block<D>;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, half = part & 1;
-  QwPlace w;
-  bool bad;
-  if (!place(p, blockIdx.x, &w, &bad)) {
-    if (bad && threadIdx.x == 0) set_error(p.err, kErrDeviceIndex);
+  const QwPlace w = place(p, blockIdx.x);
+  if (!w.any) {
+    if (threadIdx.x == 0 && !length_ok(p, w.n)) set_error(p.err, kErrDeviceIndex);
     return;
   }
-  const int pos0 = (w.block << 4) + 8 * half;
+  const int pos0 = (w.block << 4) + 8 * half, g = lane >> 2, t = lane & 3;
   if (pos0 + 7 < w.p0 || pos0 >= w.n) return;
-  uint8_t* blk = pool + w.at * L::kBytes;
   const size_t row = (size_t)p.nkv * D;
   const bf16* src = (part < 2 ? k_new : v_new) + (long long)w.b * p.Q * row + (long long)(pos0 - w.p0) * row + w.h * D;
   if (part < 2) {
-    const int g = lane >> 2, pos = pos0 + g;
-    append_keys<D>(src + g * (long long)row, pos >= w.p0 && pos < w.n, blk, 8 * half + g, lane & 3);
+    const int pos = pos0 + g;
+    const bool in = pos >= w.p0 && pos < w.n;
+    uint4 x[L::W];
+#pragma unroll
+    for (int j = 0; j < L::W; ++j)
+      x[j] = in ? __ldg(reinterpret_cast<const uint4*>(src + g * (long long)row + 32 * j + 8 * t)) : make_uint4(0u, 0u, 0u, 0u);
+    if (w.pg < 0 || w.pg >= p.P) {
+      if (lane == 0) set_error(p.err, kErrDeviceIndex);
+      return;
+    }
+    append_keys<D>(x, in, pool + block_of(p, w) * L::kBytes, 8 * half + g, t);
   } else {
-    const int pos = pos0 + 2 * (lane & 3);
+    const int pos = pos0 + 2 * t;
     const bool in[2] = {pos >= w.p0 && pos < w.n, pos + 1 >= w.p0 && pos + 1 < w.n};
-    append_values<D>(src + (pos - pos0) * (long long)row, row, in, blk, half, lane);
+    uint2 x[2][L::W];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int m = 0; m < L::W; ++m)
+        x[e][m] = in[e] ? __ldg(reinterpret_cast<const uint2*>(src + (2 * t + e) * (long long)row + 32 * m + 4 * g))
+                        : make_uint2(0u, 0u);
+    if (w.pg < 0 || w.pg >= p.P) {
+      if (lane == 0) set_error(p.err, kErrDeviceIndex);
+      return;
+    }
+    append_values<D>(x, in, pool + block_of(p, w) * L::kBytes, half, lane);
   }
 }
 
@@ -264,17 +272,15 @@ __global__ void __launch_bounds__(kQwWarps * 32) q4_read_kernel(const uint8_t* _
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, half = part & 1, g = lane >> 2, t = lane & 3;
-  QwPlace w;
-  bool bad;
-  const bool there = place(p, blockIdx.x, &w, &bad);
-  if (bad && threadIdx.x == 0) set_error(p.err, kErrDeviceIndex);
-  // a bad length: the rows are zeros, laid out as if the last position were the last of a block
-  if (w.n < 0 || w.n > (p.M << p.page_shift)) {
+  QwPlace w = place(p, blockIdx.x);
+  const bool there = w.any && w.pg >= 0 && w.pg < p.P, bad = !length_ok(p, w.n);
+  if (threadIdx.x == 0 && (bad || (w.any && !there))) set_error(p.err, kErrDeviceIndex);
+  if (bad) {  // the rows are zeros, laid out as if the last position were the last of a block
     w.n = p.nblk << 4;
     w.p0 = w.n - p.Q;
     w.block = q4_floor_block(w.p0) + (blockIdx.x / p.nkv) % p.nblk;
   }
-  const uint8_t* blk = pool + (there ? w.at * L::kBytes : 0);
+  const uint8_t* blk = pool + (there ? block_of(p, w) * L::kBytes : 0);
   const int pos0 = w.block * 16 + 8 * half;
   const size_t row = (size_t)p.nkv * D;
   bf16* out = (part < 2 ? k_out : v_out) + (long long)w.b * p.Q * row + (long long)(pos0 - w.p0) * row + w.h * D;
