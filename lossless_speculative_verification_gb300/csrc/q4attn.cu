@@ -26,9 +26,10 @@
 // in shared memory, those of the chunks in the cluster or in
 // attn_q4_combine_kernel.  Chunks begin at fixed positions and both forms add in
 // the same order, so a row's result does not depend on the other rows of the call.
-// Bound by the issue of instructions (57 % of the slots, 711 a step of 32
-// positions and 16 rows, 160 of them dequantising; the tensor cores 43 %): 16 x 32K
-// positions of 8 key heads take 148 us, 3.7 TB/s of cache.
+// A step of 16 rows is 600 instructions, 160 of them dequantising; 16 x 32K
+// positions of 8 key heads take 135 us, 4.0 TB/s of cache, with 53 % of the issue
+// slots, 50 % of the ALU and 48 % of the tensor pipe taken: what bounds it is how
+// far three CTAs an SM (168 registers a thread) overlap them.
 #include <math.h>
 
 #include <type_traits>
@@ -715,9 +716,11 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
 // as much as three steps (queries, first loads, the states' meeting): the cut with the least rounds of CTAs (three
 // an SM; one at least) times steps of a round.  Where all CTAs are on the GPU at once and a sequence has at most
 // eight, its chunks are a cluster; else the last CTA of up to eight merges them, for up to eight rows (clusters that
-// wait for room leave SMs idle), and otherwise a second kernel, about three steps more.  All add in the same order.  Measured: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 14.0 us,
-// 8 merged by a kernel 15.7, 4 chunks 18.9; 32 of up to 2304, 10 key heads: 2 chunks 23.5, 1 chunk 27.4, 4 chunks
-// 24.5 (in clusters 30.3); 16 of 32K, 8 key heads: 7 chunks 148 (in clusters 186), 16 chunks 154.
+// wait for room leave SMs idle), and otherwise a second kernel, about three steps more.  All add in the same order.
+// Measured, us: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 13.7, merged by the last 14.7,
+// 4 chunks 19.2, 16 by a kernel 14.0; 32 of up to 2304, 10 key heads: 2 chunks merged by the last 21.5, by a kernel 23.1,
+// in clusters 27.3, 1 chunk 27.4, 4 chunks 23.8; 16 of 32K, 8 key heads and 16 rows: 7 chunks by a kernel 135, 8 chunks
+// 139, 8 in clusters 166, 16 chunks 141; one of 300, 10 key heads: 4 chunks in a cluster 4.8, by a kernel 6.5.
 // The cut goes by the capacity (the lengths are on the device) and not by Q or the shared heads, so a row is
 // summed in the same order alone and among others.
 struct Cut {

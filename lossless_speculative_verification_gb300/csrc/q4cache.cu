@@ -38,8 +38,8 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
 // A group's scale and the whole numbers by it: n = rint(x / s), ties to even.
 // x * (1 / s) may be off by an ulp or two; the rest x - q s is exact (q and s have 32 bits together, and the rest
 // few), and rest / s added to q rounds to x / s, exactly where that is a half (one correction of a quotient by its
-// remainder, as Markstein describes).  Adding 1.5 * 2^23 then rounds to even.  All of it runs on the FMA pipe:
-// with conversions the append of eight prompts of 1156 positions took 24 us, with a test for ties 19 us.
+// remainder, as Markstein describes).  Adding 1.5 * 2^23 then rounds to even.  All of it runs on the FMA pipe: with
+// a division and conversions eight prompts of 1156 positions were appended in 28 us, with a test for ties in 24.
 struct Step {
   uint32_t bits;
   float s, inv;
@@ -207,8 +207,8 @@ __device__ __forceinline__ void append_values(const uint2 (&x)[2][Q4Block<D>::W]
 // Twelve CTAs an SM: a CTA is one chain of loads (length, entry and rows, then the codes), and what is in flight on
 // an SM is what its CTAs have begun (eight prompts of 1156 positions: 16 us with ten, 15 with twelve).
 // A warp's share is a half block (8 positions) of the keys or of the values: the four parts of a block are the
-// CTA's warps.  Whole blocks a warp took 7.9 us for 32 x 4 positions of 10 heads, quarters 4.1 us: the call is as
-// long as one warp's chain of loads, maxima and codes.
+// CTA's warps.  32 x 4 positions of 10 heads were written and read back in 17.6 us with whole blocks a warp, in 9.2
+// with quarters: the call is as long as one warp's chain of loads, maxima and codes.
 template <int D>
 __global__ void __launch_bounds__(kQwWarps * 32, 12) q4_append_kernel(const bf16* __restrict__ k_new,
                                                                   const bf16* __restrict__ v_new, uint8_t* pool,
