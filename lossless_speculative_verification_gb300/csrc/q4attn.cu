@@ -1,10 +1,10 @@
 // q4attn.cu -- causal attention of the verified positions over the 4-bit paged
 // cache (layout: q4.cuh), with query heads that share key heads.
 //
-// The R = Q * (nh / nkv) query rows of a key head stand in the columns of
-// m16n8k16 MMAs and the cached positions in their rows: S^T = K q^T and
-// O^T = V^T P^T, so that one fragment of dequantised keys or values serves eight
-// query rows, and twice that many with a second column tile (NT = 2).
+// The R = Q * (nh / nkv) query rows of a key head go through m16n8k16 MMAs in
+// tiles.  Up to eight rows (NT = 1) are the MMAs' columns and the cached positions
+// their rows, S^T = K q^T and O^T = V^T P^T; sixteen (NT = 2) are their rows,
+// S = q K^T and O = P V, which needs no transposes and wastes nothing.
 //
 // Dequantising costs five operations a word of eight codes: a nibble alone in
 // the low bits of an f16 is the subnormal n' 2^-24 (n' = n + 8), and 16 times
@@ -23,8 +23,7 @@
 //
 // A CTA's four warps take the steps (32 positions) of one chunk of one key head
 // in turn, each from a ring of its own; their states (maximum, sum, output) meet
-// in shared memory, those of the chunks in the cluster or in
-// attn_q4_combine_kernel.  Chunks begin at fixed positions and both forms add in
+// in shared memory, those of the chunks as cut_of says.  Chunks begin at fixed positions and both forms add in
 // the same order, so a row's result does not depend on the other rows of the call.
 // A step of 16 rows is 600 instructions, 160 of them dequantising; 16 x 32K
 // positions of 8 key heads take 135 us, 4.0 TB/s of cache, with 53 % of the issue
@@ -47,6 +46,7 @@ constexpr int kQaThreads = kQaWarps * 32;
 constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
 constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
 constexpr float kQaLog2e = 1.4426950408889634f;
+constexpr uint64_t kQaDrainNs = 2000000000ull;
 constexpr int kQaCentre = 16;       // steps between two centrings
 constexpr int kQaCounters = 16384;  // tiles of rows whose CTAs may be counted; their counters lead the workspace
 constexpr int kQaMaxTiles = 8;      // tiles of 16 rows of a key head, at most (8 queries x 16 heads)
@@ -584,8 +584,10 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       phase ^= 1u;
     }
   }
-  // after a wait that ran out: the copies already issued land before the memory is used again
-  for (int i = done; i < nstages && i < done + S; ++i) mbar_wait(&full[i % S], (i / S) & 1, p.wait_ns);
+  // after a wait that ran out: the copies already issued land before the memory is used again (however short the
+  // caller's limit is)
+  for (int i = done; i < nstages && i < done + S; ++i)
+    mbar_wait(&full[i % S], (i / S) & 1, p.wait_ns > kQaDrainNs ? p.wait_ns : kQaDrainNs);
   __syncwarp();
 
   // ---- the warp's state, in its drained ring

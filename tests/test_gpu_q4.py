@@ -269,30 +269,32 @@ def test_attention_of_values_of_any_size(grp):
     assert np.abs(got[0, :5]).max() < 8
 
 
-def test_what_is_no_number_reaches_only_the_rows_that_see_it():
+@pytest.mark.parametrize("d,grp", [(128, 1), (128, 2), (64, 1), (64, 3)])
+def test_what_is_no_number_reaches_only_the_rows_that_see_it(d, grp):
     rs = np.random.default_rng(8)
-    k, v = rs.normal(size=(2, 1, 150, 2, 128))
-    base = Cache([150], 2, 128, 64, k=k, v=v)
-    q = queries(base, 5, 2)
+    k, v = rs.normal(size=(2, 1, 150, 2, d))
+    base = Cache([150], 2, d, 64, k=k, v=v)
+    q = queries(base, 5, grp)
     ref = base.attend(q)
     for which in (0, 1):
         for x in (np.nan, np.inf, -np.inf):
             k2, v2 = k.copy(), v.copy()
-            (k2, v2)[which][0, 147, 1, 9] = x                   # rows 2, 3, 4 see position 147; heads 2, 3 its key head
-            got = Cache([150], 2, 128, 64, k=k2, v=v2).attend(q)
+            (k2, v2)[which][0, 147, 1, 9] = x                   # rows 2, 3, 4 see position 147; key head 1's heads
+            got = Cache([150], 2, d, 64, k=k2, v=v2).attend(q)
             np.testing.assert_array_equal(got[0, :2], ref[0, :2])
-            np.testing.assert_array_equal(got[0, :, :2], ref[0, :, :2])
-            assert np.isnan(got[0, 2:, 2:, :64]).all()
+            np.testing.assert_array_equal(got[0, :, :grp], ref[0, :, :grp])
+            assert np.isnan(got[0, 2:, grp:, :64]).all()
             if which == 0:
-                assert np.isnan(got[0, 2:, 2:, 64:]).all()
+                assert np.isnan(got[0, 2:, grp:, 64:]).all()
             else:                                               # the values' other group is what it was
-                np.testing.assert_allclose(got[0, 2:, 2:, 64:], ref[0, 2:, 2:, 64:], rtol=2.0 ** -7, atol=1e-4)
-    q2 = q4.bf16_f64(q)
-    q2[0, 1, 3, 7] = np.nan
-    got = base.attend(bits(q2))
-    assert np.isnan(got[0, 1, 3]).all()
-    got[0, 1, 3] = ref[0, 1, 3]
-    np.testing.assert_array_equal(got, ref)
+                np.testing.assert_allclose(got[0, 2:, grp:, 64:], ref[0, 2:, grp:, 64:], rtol=2.0 ** -7, atol=1e-4)
+    for x in (np.nan, np.inf):
+        q2 = q4.bf16_f64(q)
+        q2[0, 1, -1, 7] = x
+        got = base.attend(bits(q2))
+        assert np.isnan(got[0, 1, -1]).all()
+        got[0, 1, -1] = ref[0, 1, -1]
+        np.testing.assert_array_equal(got, ref)
 
 
 def test_a_row_does_not_depend_on_the_others():
