@@ -28,6 +28,12 @@ constexpr int kPgChunk = 4096;  // pages a CTA reduces
 constexpr int kPgChunkWords = kPgChunk / 32;
 constexpr int kPgMaxPages = 1 << 24;
 constexpr int kPgMaxRows = 1 << 16;
+// Forks of few rows, entries and counts are one launch of a cluster instead of two of a grid: 2.9 us for 2.6 on the
+// GPU, 7.9 for 9.6 with the host's calls (32 rows of 36).  (A resize in that form took 16.1 us for 13.4.)
+constexpr int kPgCluster = 8;        // CTAs of the cluster
+constexpr int kPgGroups = 4;         // rows that each takes at a time
+constexpr int kPgFewRows = 64;
+constexpr int kPgFewInts = 1 << 16;
 constexpr int kPgDeep = 4;      // entries of a row a thread has in flight
 // Bytes a CTA copies at a time, all of them in flight, and the CTAs an SM has for it: 979 MB of moves take 158 us with
 // two CTAs of 32 KB, 166 with four of 16 KB or 32 KB, 167 with two of 64 KB, 188 with one of 32 KB.
@@ -72,58 +78,77 @@ PgWs pg_layout(void* base, size_t B, size_t M, size_t P) {
   return w;
 }
 
-// Sum over the CTA; every thread gets it.
-__device__ __forceinline__ int block_sum(int v, int* tmp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int w = 0; w < kPgWarps; ++w) s += tmp[w];
-  return s;
-}
-
-// Exclusive prefix of v over the CTA's threads; *sum the total.
-__device__ __forceinline__ int block_prefix(int v, int* tmp, int* sum) {
-  const int lane = threadIdx.x & 31;
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += u;
+// A group of kPgThreads threads that takes a row or a chunk: a CTA, or a quarter of one (the cluster form).
+struct PgShared {
+  int tmp[kPgWarps];
+  int before[kPgThreads];        // free pages below each chunk of a tile of chunks
+  int fresh[kPgDeep][kPgWarps];  // new pages of each warp's entries
+};
+template <int kGroups>
+struct Group {
+  int tid, id;
+  PgShared* sh;
+  __device__ __forceinline__ explicit Group(PgShared* all)
+      : tid((int)threadIdx.x % kPgThreads), id((int)threadIdx.x / kPgThreads), sh(all + id) {}
+  __device__ __forceinline__ void sync() const {
+    if (kGroups == 1)
+      __syncthreads();
+    else
+      named_bar_sync(1 + id, kPgThreads);
   }
-  __syncthreads();
-  if (lane == 31) tmp[threadIdx.x >> 5] = s;
-  __syncthreads();
-  int before = 0, all = 0;
+  __device__ __forceinline__ int lane() const { return tid & 31; }
+  __device__ __forceinline__ int warp() const { return tid >> 5; }
+  // Sum over the group; every thread gets it.
+  __device__ __forceinline__ int sum(int v) const {
 #pragma unroll
-  for (int w = 0; w < kPgWarps; ++w) {
-    if (w < (int)(threadIdx.x >> 5)) before += tmp[w];
-    all += tmp[w];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    sync();
+    if (lane() == 0) sh->tmp[warp()] = v;
+    sync();
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) s += sh->tmp[w];
+    return s;
   }
-  *sum = all;
-  return before + s - v;
-}
-
-// Sum of a[0..n) over the CTA, and of a[0..upto) in *part.
-__device__ __forceinline__ int sum_upto(const int* a, int n, int upto, int* part, int* tmp) {
-  int all = 0, pre = 0;
-  for (int i = threadIdx.x; i < n; i += kPgThreads) {
-    const int v = __ldcg(a + i);
-    all += v;
-    if (i < upto) pre += v;
+  // Exclusive prefix of v over the group's threads; *all the total.
+  __device__ __forceinline__ int prefix(int v, int* all) const {
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane() >= o) s += u;
+    }
+    sync();
+    if (lane() == 31) sh->tmp[warp()] = s;
+    sync();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) {
+      if (w < warp()) before += sh->tmp[w];
+      total += sh->tmp[w];
+    }
+    *all = total;
+    return before + s - v;
   }
-  *part = block_sum(pre, tmp);
-  return block_sum(all, tmp);
-}
+  // Sum of a[0..n), and of a[0..upto) in *part.
+  __device__ __forceinline__ int sum_upto(const int* a, int n, int upto, int* part) const {
+    int all = 0, pre = 0;
+    for (int i = tid; i < n; i += kPgThreads) {
+      const int v = __ldcg(a + i);
+      all += v;
+      if (i < upto) pre += v;
+    }
+    *part = sum(pre);
+    return sum(all);
+  }
+};
 
 // The counts of chunk c, all loads in flight together: refs[k] of lane l is page 32 (warp + k kPgWarps) + l of it.
-__device__ __forceinline__ void load_chunk(const int32_t* ref, int P, int c, int (&refs)[kPgChunkWords / kPgWarps]) {
+__device__ __forceinline__ void load_chunk(const Group<1>& g, const int32_t* ref, int P, int c,
+                                           int (&refs)[kPgChunkWords / kPgWarps]) {
 #pragma unroll
   for (int k = 0; k < kPgChunkWords / kPgWarps; ++k) {
-    const int at = c * kPgChunk + 32 * ((int)(threadIdx.x >> 5) + k * kPgWarps) + (int)(threadIdx.x & 31);
+    const int at = c * kPgChunk + 32 * (g.warp() + k * kPgWarps) + g.lane();
     refs[k] = at < P ? __ldcg(ref + at) : -1;
   }
 }
@@ -158,31 +183,27 @@ __device__ __forceinline__ bool row_bounds(const PgResize& p, int b, int* keep, 
 }
 
 // Chunk c of the counts: bit maps and the number of free pages; row c of the table: the pages it needs.
-__global__ void __launch_bounds__(kPgThreads) resize_count_kernel(const PgResize p) {
-  __shared__ int tmp[kPgWarps];
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (c == 0 && threadIdx.x < 64) {
-    p.w.count[threadIdx.x] = 0;
-    if (p.stats && threadIdx.x < 4) p.stats[threadIdx.x] = 0;
+__device__ __forceinline__ void resize_count(const Group<1>& g, const PgResize& p, int c) {
+  if (c == 0 && g.tid < 64) {
+    p.w.count[g.tid] = 0;
+    if (p.stats && g.tid < 4) p.stats[g.tid] = 0;
   }
   if (c < p.chunks) {
     int n = 0, refs[kPgChunkWords / kPgWarps];
-    load_chunk(p.ref, p.P, c, refs);
+    load_chunk(g, p.ref, p.P, c, refs);
 #pragma unroll
     for (int k = 0; k < kPgChunkWords / kPgWarps; ++k) {
-      const int i = warp + k * kPgWarps, at = c * kPgChunk + 32 * i + lane, r = refs[k];
+      const int i = g.warp() + k * kPgWarps, at = c * kPgChunk + 32 * i + g.lane(), r = refs[k];
       const uint32_t free = __ballot_sync(0xffffffffu, at < p.P && r <= 0), shared = __ballot_sync(0xffffffffu, r > 1);
-      if (lane == 0) {
+      if (g.lane() == 0) {
         p.w.bits[c * kPgChunkWords + i] = free;
         p.w.bits[(p.chunks + c) * kPgChunkWords + i] = shared;
         n += __popc(free);
       }
       if (p.ref_out != p.ref && at < p.P) p.ref_out[at] = r;
     }
-    n = block_sum(n, tmp);
-    if (threadIdx.x == 0) p.w.chunk_n[c] = n;
+    n = g.sum(n);
+    if (g.tid == 0) p.w.chunk_n[c] = n;
   }
   if (c < p.B) {
     int keep, cap, n = 0;
@@ -191,14 +212,14 @@ __global__ void __launch_bounds__(kPgThreads) resize_count_kernel(const PgResize
         int pg[kPgDeep], r[kPgDeep];
 #pragma unroll
         for (int k = 0; k < kPgDeep; ++k) {
-          const int i = i0 + k * kPgThreads + threadIdx.x;
+          const int i = i0 + k * kPgThreads + g.tid;
           pg[k] = i < p.M ? __ldcg(p.table + (size_t)c * p.M + i) : -1;
         }
 #pragma unroll
         for (int k = 0; k < kPgDeep; ++k) r[k] = pg[k] >= 0 && pg[k] < p.P ? __ldcg(p.ref + pg[k]) : 0;
 #pragma unroll
         for (int k = 0; k < kPgDeep; ++k) {
-          const int i = i0 + k * kPgThreads + threadIdx.x;
+          const int i = i0 + k * kPgThreads + g.tid;
           if (i >= p.M) continue;
           const bool held = pg[k] >= 0 && pg[k] < p.P;
           if (pg[k] < -1 || pg[k] >= p.P || (!held && i < (keep + p.page - 1) / p.page)) set_error(p.err, kErrDeviceIndex);
@@ -206,25 +227,21 @@ __global__ void __launch_bounds__(kPgThreads) resize_count_kernel(const PgResize
           n += entry_of(i, held, r[k] > 1, keep, cap, p.page).fresh;
         }
       }
-    } else if (threadIdx.x == 0) {
+    } else if (g.tid == 0) {
       set_error(p.err, kErrDeviceIndex);
     }
-    n = block_sum(n, tmp);
-    if (threadIdx.x == 0) p.w.need[c] = n;
+    n = g.sum(n);
+    if (g.tid == 0) p.w.need[c] = n;
   }
 }
 
 // Row b: its new pages' numbers, its entries, the counts.
-__global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResize p) {
-  __shared__ int tmp[kPgWarps];
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.x;
+__device__ __forceinline__ void resize_assign(const Group<1>& g, const PgResize& p, int b) {
   int first, unused;
-  const int need = sum_upto(p.w.need, p.B, b, &first, tmp);
+  const int need = g.sum_upto(p.w.need, p.B, b, &first);
   const int mine = b < p.B ? __ldcg(p.w.need + b) : 0;
-  const int free = sum_upto(p.w.chunk_n, p.chunks, 0, &unused, tmp);
-  if (b == 0 && threadIdx.x == 0) {
+  const int free = g.sum_upto(p.w.chunk_n, p.chunks, 0, &unused);
+  if (b == 0 && g.tid == 0) {
     if (p.stats) p.stats[0] = need, p.stats[1] = free;
     if (need > free) set_error(p.err, kErrPages);
   }
@@ -235,40 +252,40 @@ __global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResiz
   int32_t* out = p.table_out + (size_t)b * p.M;
   if (!ok) {
     if (p.table_out != p.table)
-      for (int i = threadIdx.x; i < p.M; i += kPgThreads) out[i] = __ldcg(row + i);
+      for (int i = g.tid; i < p.M; i += kPgThreads) out[i] = __ldcg(row + i);
     return;
   }
   int* fresh = p.w.list + first;  // the pages of ranks first .. first + mine - 1
   if (mine > 0) {
-    __shared__ int before_s[kPgThreads];  // free pages below each chunk of the tile
+    int* before_s = g.sh->before;
     int below = 0;
     for (int c0 = 0; c0 < p.chunks && below < first + mine; c0 += kPgThreads) {
-      const int c = c0 + threadIdx.x;
+      const int c = c0 + g.tid;
       const int n = c < p.chunks ? __ldcg(p.w.chunk_n + c) : 0;
       int all;
-      const int at = below + block_prefix(n, tmp, &all);
-      before_s[threadIdx.x] = at;
-      const int skip = block_sum(c < p.chunks && at + n <= first, tmp);  // chunks that end before the row's first
+      const int at = below + g.prefix(n, &all);
+      before_s[g.tid] = at;
+      const int skip = g.sum(c < p.chunks && at + n <= first);  // chunks that end before the row's first
       for (int k = skip; k < kPgThreads && c0 + k < p.chunks && before_s[k] < first + mine; ++k) {
-        uint32_t word = threadIdx.x < kPgChunkWords
-                            ? __ldcg(p.w.bits + (size_t)(c0 + k) * kPgChunkWords + threadIdx.x) : 0u;
+        uint32_t word = g.tid < kPgChunkWords
+                            ? __ldcg(p.w.bits + (size_t)(c0 + k) * kPgChunkWords + g.tid) : 0u;
         int in_chunk;
-        int rank = before_s[k] + block_prefix(__popc(word), tmp, &in_chunk);
+        int rank = before_s[k] + g.prefix(__popc(word), &in_chunk);
         while (word) {
           const int bit = __ffs(word) - 1;
           word &= word - 1;
-          if (rank >= first && rank < first + mine) fresh[rank - first] = (c0 + k) * kPgChunk + 32 * threadIdx.x + bit;
+          if (rank >= first && rank < first + mine) fresh[rank - first] = (c0 + k) * kPgChunk + 32 * g.tid + bit;
           ++rank;
         }
       }
       below += all;
-      __syncthreads();
+      g.sync();
     }
-    __syncthreads();
+    g.sync();
   }
   const uint32_t* shared = p.w.bits + (size_t)p.chunks * kPgChunkWords;
-  __shared__ int fresh_s[kPgDeep][kPgWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto& fresh_s = g.sh->fresh;
+  const int lane = g.lane(), warp = g.warp();
   int given = 0, gone = 0;
   for (int i0 = 0; i0 < p.M; i0 += kPgThreads * kPgDeep) {
     int pg[kPgDeep];
@@ -276,24 +293,24 @@ __global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResiz
     Entry e[kPgDeep];
 #pragma unroll
     for (int k = 0; k < kPgDeep; ++k) {
-      const int i = i0 + k * kPgThreads + threadIdx.x;
+      const int i = i0 + k * kPgThreads + g.tid;
       pg[k] = i < p.M ? __ldcg(row + i) : -1;
     }
 #pragma unroll
     for (int k = 0; k < kPgDeep; ++k) bit[k] = pg[k] >= 0 && pg[k] < p.P ? __ldcg(shared + (pg[k] >> 5)) >> (pg[k] & 31) & 1u : 0u;
-    __syncthreads();  // the last round's counts are read
+    g.sync();  // the last round's counts are read
 #pragma unroll
     for (int k = 0; k < kPgDeep; ++k) {
-      const int i = i0 + k * kPgThreads + threadIdx.x;
+      const int i = i0 + k * kPgThreads + g.tid;
       e[k] = entry_of(i, pg[k] >= 0 && pg[k] < p.P, bit[k], keep, cap, p.page);
       if (i >= p.M) e[k].fresh = e[k].gone = e[k].copied = false;
       ballot[k] = __ballot_sync(0xffffffffu, e[k].fresh);
       if (lane == 0) fresh_s[k][warp] = __popc(ballot[k]);
     }
-    __syncthreads();
+    g.sync();
 #pragma unroll
     for (int k = 0; k < kPgDeep; ++k) {
-      const int i = i0 + k * kPgThreads + threadIdx.x;
+      const int i = i0 + k * kPgThreads + g.tid;
       int rank = given + __popc(ballot[k] & ((1u << lane) - 1u));
 #pragma unroll
       for (int w = 0; w < kPgWarps; ++w) {
@@ -319,9 +336,23 @@ __global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResiz
     }
   }
   if (p.stats) {
-    gone = block_sum(gone, tmp);
-    if (threadIdx.x == 0 && gone) atomicAdd(p.stats + 3, gone);
+    gone = g.sum(gone);
+    if (g.tid == 0 && gone) atomicAdd(p.stats + 3, gone);
   }
+}
+
+__global__ void __launch_bounds__(kPgThreads) resize_count_kernel(const PgResize p) {
+  __shared__ PgShared sh;
+  pdl_wait();
+  pdl_trigger();
+  resize_count(Group<1>(&sh), p, blockIdx.x);
+}
+
+__global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResize p) {
+  __shared__ PgShared sh;
+  pdl_wait();
+  pdl_trigger();
+  resize_assign(Group<1>(&sh), p, blockIdx.x);
 }
 
 struct PgCopy {
@@ -373,10 +404,8 @@ struct PgFork {
   int* err;
 };
 
-__global__ void __launch_bounds__(kPgThreads) fork_save_kernel(const PgFork p) {
-  pdl_wait();
-  pdl_trigger();
-  const size_t step = (size_t)gridDim.x * kPgThreads, at = (size_t)blockIdx.x * kPgThreads + threadIdx.x;
+__device__ __forceinline__ void fork_save(const PgFork& p) {
+  const size_t step = (size_t)gridDim.x * blockDim.x, at = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (p.table_out == p.table)
     for (size_t i = at; i < (size_t)p.B * p.M; i += step) p.old[i] = __ldcg(p.table + i);
   if (p.ref_out != p.ref)
@@ -384,20 +413,17 @@ __global__ void __launch_bounds__(kPgThreads) fork_save_kernel(const PgFork p) {
 }
 
 // Row b: takes its parent's pages; the pages that it held get one count for each of its children, less its own.
-__global__ void __launch_bounds__(kPgThreads) fork_rows_kernel(const PgFork p) {
-  __shared__ int tmp[kPgWarps];
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.x;
+template <int N>
+__device__ __forceinline__ void fork_row(const Group<N>& g, const PgFork& p, int b) {
   int children = 0;
-  for (int i = threadIdx.x; i < p.B; i += kPgThreads) children += __ldcg(p.parent + i) == b;
-  const int more = block_sum(children, tmp) - 1;
+  for (int i = g.tid; i < p.B; i += kPgThreads) children += __ldcg(p.parent + i) == b;
+  const int more = g.sum(children) - 1;
   const int from = __ldcg(p.parent + b);
   const bool has = from >= 0 && from < p.B;
-  if ((from < -1 || from >= p.B) && threadIdx.x == 0) set_error(p.err, kErrDeviceIndex);
+  if ((from < -1 || from >= p.B) && g.tid == 0) set_error(p.err, kErrDeviceIndex);
   const int32_t* table = p.table_out == p.table ? p.old : p.table;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < p.M; i += kPgThreads) {
+  for (int i = g.tid; i < p.M; i += kPgThreads) {
     const int mine = __ldcg(table + (size_t)b * p.M + i);
     if (mine >= 0 && mine < p.P) {
       if (more) atomicAdd(p.ref_out + mine, more);
@@ -406,6 +432,29 @@ __global__ void __launch_bounds__(kPgThreads) fork_rows_kernel(const PgFork p) {
     }
     p.table_out[(size_t)b * p.M + i] = has ? __ldcg(table + (size_t)from * p.M + i) : -1;
   }
+}
+
+__global__ void __launch_bounds__(kPgThreads) fork_save_kernel(const PgFork p) {
+  pdl_wait();
+  pdl_trigger();
+  fork_save(p);
+}
+
+__global__ void __launch_bounds__(kPgThreads) fork_rows_kernel(const PgFork p) {
+  __shared__ PgShared sh;
+  pdl_wait();
+  pdl_trigger();
+  fork_row(Group<1>(&sh), p, blockIdx.x);
+}
+
+__global__ void __cluster_dims__(kPgCluster) __launch_bounds__(kPgGroups * kPgThreads) fork_plan_kernel(const PgFork p) {
+  __shared__ PgShared sh[kPgGroups];
+  pdl_wait();
+  pdl_trigger();
+  fork_save(p);
+  cluster_sync();
+  const Group<kPgGroups> g(sh);
+  for (int b = blockIdx.x * kPgGroups + g.id; b < p.B; b += kPgCluster * kPgGroups) fork_row(g, p, b);
 }
 
 // ----------------------------------------------------------------------------- compact
@@ -419,60 +468,60 @@ struct PgCompact {
 };
 
 // Chunk c of the counts: its bit map and the number of live pages.
-__device__ __forceinline__ void compact_count(const PgCompact& p, int c, int* tmp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void compact_count(const Group<1>& g, const PgCompact& p, int c) {
   int n = 0, refs[kPgChunkWords / kPgWarps];
-  load_chunk(p.ref, p.P, c, refs);
+  load_chunk(g, p.ref, p.P, c, refs);
 #pragma unroll
   for (int k = 0; k < kPgChunkWords / kPgWarps; ++k) {
-    const int i = warp + k * kPgWarps;
+    const int i = g.warp() + k * kPgWarps;
     const uint32_t live = __ballot_sync(0xffffffffu, refs[k] > 0);
-    if (lane == 0) {
+    if (g.lane() == 0) {
       p.w.bits[c * kPgChunkWords + i] = live;
       n += __popc(live);
     }
   }
-  n = block_sum(n, tmp);
-  if (threadIdx.x == 0) p.w.chunk_n[c] = n;
+  n = g.sum(n);
+  if (g.tid == 0) p.w.chunk_n[c] = n;
 }
 
 __global__ void __launch_bounds__(kPgThreads) compact_count_kernel(const PgCompact p) {
-  __shared__ int tmp[kPgWarps];
+  __shared__ PgShared sh;
   pdl_wait();
   pdl_trigger();
-  compact_count(p, blockIdx.x, tmp);
+  compact_count(Group<1>(&sh), p, blockIdx.x);
 }
 
 // Chunk c: the k-th free page below the live count goes to list2[k], the k-th live one at or above it to
 // list[k].  Live pages below the count are as many as the count less the pages that move.
 __global__ void __launch_bounds__(kPgThreads) compact_list_kernel(const PgCompact p) {
-  __shared__ int tmp[kPgWarps];
+  __shared__ PgShared sh;
   pdl_wait();
   pdl_trigger();
+  const Group<1> g(&sh);
   const int c = blockIdx.x;
   if (p.chunks == 1) {  // a pool of one chunk needs no launch before this one
-    compact_count(p, 0, tmp);
-    __syncthreads();
+    compact_count(g, p, 0);
+    g.sync();
   }
   int before;
-  const int live = sum_upto(p.w.chunk_n, p.chunks, c, &before, tmp);
+  const int live = g.sum_upto(p.w.chunk_n, p.chunks, c, &before);
   // live pages below number `live`
   int under, all;
   const int cl = live / kPgChunk;  // the chunk of that number (may lie behind the last page)
-  sum_upto(p.w.chunk_n, p.chunks, cl, &under, tmp);
+  g.sum_upto(p.w.chunk_n, p.chunks, cl, &under);
   if (cl < p.chunks) {
-    const int word = threadIdx.x, rest = live - cl * kPgChunk - 32 * word;  // pages of this word below the number
+    const int word = g.tid, rest = live - cl * kPgChunk - 32 * word;  // pages of this word below the number
     uint32_t v = word < kPgChunkWords ? __ldcg(p.w.bits + cl * kPgChunkWords + word) : 0u;
     if (rest <= 0)
       v = 0u;
     else if (rest < 32)
       v &= (1u << rest) - 1u;
-    under += block_sum(__popc(v), tmp);
+    under += g.sum(__popc(v));
   }
-  uint32_t v = threadIdx.x < kPgChunkWords ? __ldcg(p.w.bits + c * kPgChunkWords + threadIdx.x) : 0u;
-  int rank = before + block_prefix(__popc(v), tmp, &all);  // live pages before this word
-  if (threadIdx.x < kPgChunkWords) {
-    const int at0 = c * kPgChunk + 32 * threadIdx.x;
+  uint32_t v = g.tid < kPgChunkWords ? __ldcg(p.w.bits + c * kPgChunkWords + g.tid) : 0u;
+  int rank = before + g.prefix(__popc(v), &all);  // live pages before this word
+  if (g.tid < kPgChunkWords) {
+    const int at0 = c * kPgChunk + 32 * g.tid;
     for (int i = 0; i < 32 && at0 + i < p.P; ++i) {
       const bool is = (v >> i) & 1u;
       const bool moves = is && at0 + i >= live;
@@ -482,7 +531,7 @@ __global__ void __launch_bounds__(kPgThreads) compact_list_kernel(const PgCompac
       rank += is;
     }
   }
-  if (c == 0 && threadIdx.x == 0) {
+  if (c == 0 && g.tid == 0) {
     p.w.count[0] = live - under;
     p.w.count[1] = live;
     if (p.stats) {
@@ -632,8 +681,13 @@ lsv_status spec_pages_fork(const int32_t* table, const int32_t* ref, const int32
   p.err = dc->err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (table_out == table || ref_out != ref) e = launch_pdl(fork_save_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, p);
-  if (e == cudaSuccess && B > 0) e = launch_pdl(fork_rows_kernel, dim3(B), dim3(kPgThreads), 0, s, p);
+  const bool save = table_out == table || ref_out != ref;
+  if (save && B <= kPgFewRows && (long long)B * M <= kPgFewInts && P <= kPgFewInts) {
+    e = launch_pdl(fork_plan_kernel, dim3(kPgCluster), dim3(kPgGroups * kPgThreads), 0, s, p);
+  } else {
+    if (save) e = launch_pdl(fork_save_kernel, dim3(dc->num_sms * 4), dim3(kPgThreads), 0, s, p);
+    if (e == cudaSuccess && B > 0) e = launch_pdl(fork_rows_kernel, dim3(B), dim3(kPgThreads), 0, s, p);
+  }
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }
 
