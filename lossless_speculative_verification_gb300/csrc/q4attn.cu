@@ -23,12 +23,13 @@
 //
 // A CTA's four warps take the steps (32 positions) of one chunk of one key head
 // in turn, each from a ring of its own; their states (maximum, sum, output) meet
-// in shared memory, those of the chunks as cut_of says.  Chunks begin at fixed positions and both forms add in
-// the same order, so a row's result does not depend on the other rows of the call.
+// in shared memory, those of the chunks as cut_of says.  Which positions are a chunk's goes by the capacity alone
+// and both forms add in the same order, so a row's result does not depend on the other rows of the call.
 // A step of 16 rows is 600 instructions, 160 of them dequantising; 16 x 32K
-// positions of 8 key heads take 135 us, 4.0 TB/s of cache, with 53 % of the issue
+// positions of 8 key heads take 133 us, 4.1 TB/s of cache, with 53 % of the issue
 // slots, 50 % of the ALU and 48 % of the tensor pipe taken: what bounds it is how
 // far three CTAs an SM (168 registers a thread) overlap them.
+#include <limits.h>
 #include <math.h>
 
 #include <type_traits>
@@ -47,6 +48,8 @@ constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
 constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
 constexpr float kQaLog2e = 1.4426950408889634f;
 constexpr uint64_t kQaDrainNs = 2000000000ull;
+constexpr int kQaOne = 4, kQaTwo = 3;  // CTAs an SM: up to eight rows, nine to sixteen
+constexpr int kQaSpread = 16;       // steps of a chunk from which on they are taken from all over the sequence
 constexpr int kQaCentre = 16;       // steps between two centrings
 constexpr int kQaCounters = 16384;  // tiles of rows whose CTAs may be counted; their counters lead the workspace
 constexpr int kQaMaxTiles = 8;      // tiles of 16 rows of a key head, at most (8 queries x 16 heads)
@@ -59,7 +62,9 @@ struct QaParams {
   const int32_t* ctx_len;  // [B]
   int B, Q, nh, nkv, grp, R, M, P, page_shift, rblocks;
   int mode;
-  int chunk, nchunk;  // positions of a chunk (a multiple of 16 kQaWarps), chunks of a sequence
+  int sorted;  // the CTAs take the sequences by falling length
+  int nchunk;  // chunks of a sequence
+  int apart, stride, span;  // positions between the starts of two chunks, between the steps of one, and that it spans
   float scale_log2;   // scale * log2(e)
   bf16* out;          // [B, Q, nh, D]
   int* arrived;       // [B * nkv * rblocks] CTAs that have written their state; 0 before and after a call
@@ -141,6 +146,27 @@ __device__ __forceinline__ uint32_t larger_scale(uint32_t s) {
 // Its exponent, at least -64.
 __device__ __forceinline__ float exponent_of(uint32_t bits) { return (float)max((int)(bits >> 7) - 127, -64); }
 
+// The sequence of the given rank by falling length (of equal ones the first comes first), and its length.
+__device__ __forceinline__ int2 by_length(const QaParams& p, int rank) {
+  __shared__ __align__(16) int len[kQaThreads];
+  __shared__ int2 found;
+  const int tid = threadIdx.x;
+  const int n = tid < p.B ? __ldcg(p.ctx_len + tid) : INT_MIN;
+  len[tid] = n;
+  __syncthreads();
+  if (tid < p.B) {
+    int before = 0;
+    for (int j = 0; j < p.B; j += 4) {  // (what is behind the last one is not longer than any, and comes later)
+      const int4 v = *reinterpret_cast<const int4*>(len + j);
+      before += (v.x > n || (v.x == n && j < tid)) + (v.y > n || (v.y == n && j + 1 < tid)) +
+                (v.z > n || (v.z == n && j + 2 < tid)) + (v.w > n || (v.w == n && j + 3 < tid));
+    }
+    if (before == rank) found = make_int2(tid, n);
+  }
+  __syncthreads();
+  return found;
+}
+
 // A warp's ring of S stages in shared memory, each the K steps of U blocks that it takes next, filled by untiled
 // bulk copies.
 template <int D, int NT, int U, int K, int S>
@@ -180,26 +206,37 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   if (lane < S) mbar_init(&full[lane], 1);
   fence_barrier_init();
   __syncwarp();
-  const int split = blockIdx.y;
-  const int rb = blockIdx.x % p.rblocks, bh = blockIdx.x / p.rblocks;
-  const int b = bh / p.nkv, h = bh - b * p.nkv;
+  const int tiles = p.nkv * p.rblocks;
+  int split = blockIdx.y, b = blockIdx.x / tiles, ht = blockIdx.x - b * tiles, n = 0;
+  if (p.sorted) {  // the longest sequence's chunks first
+    pdl_wait();
+    const int k = blockIdx.y * gridDim.x + blockIdx.x, per = tiles * p.nchunk, rank = k / per;
+    split = (k - rank * per) / tiles;
+    ht = k - rank * per - split * tiles;
+    const int2 s = by_length(p, rank);
+    b = s.x;
+    n = s.y;
+  }
+  const int h = ht / p.rblocks, rb = ht - h * p.rblocks, bh = b * p.nkv + h;
   const int r0 = rb * kRows, nrows = min(kRows, p.R - r0);
-  const int t_begin = split * p.chunk;
-  // step i of this warp is the U blocks from position first + i * kRound on, a stage K steps
+  const int t_begin = split * p.apart, stride = p.stride;
+  // step i of this warp is the U blocks from position first + i * stride on, a stage K steps
   const int first = t_begin + warp * kStep;
   const int per_shift = p.page_shift - 4;
-  const int cap = min(p.M << p.page_shift, t_begin + p.chunk);
+  const int cap = min(p.M << p.page_shift, t_begin + p.span);
   // lane l has block l % kBlocks of stage i + l / kBlocks
   auto pos_of = [&](int i) {
-    return first + ((i + lane / kBlocks) * K + lane % kBlocks / U) * kRound + 16 * (lane % U);
+    return first + ((i + lane / kBlocks) * K + lane % kBlocks / U) * stride + 16 * (lane % U);
   };
   auto entry_of = [&](int i) {
     const int pos = pos_of(i);
     return pos < cap ? __ldcg(p.table + (size_t)b * p.M + (pos >> p.page_shift)) : -1;
   };
-  pdl_wait();
+  if (!p.sorted) {
+    pdl_wait();
+    n = __ldcg(p.ctx_len + b);
+  }
   pdl_trigger();
-  const int n = __ldcg(p.ctx_len + b);
   int pg_now = entry_of(0);  // beside the length's load, before it is known how many of them there are
 
   // ---- the queries: warp w < NT makes the operands of tile w; column g is row r0 + 8 w + g, of which this lane
@@ -215,12 +252,12 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 
   const bool bad = n < 0 || n > (p.M << p.page_shift);
   if (bad && threadIdx.x == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
-  const int end = bad ? 0 : min(n, t_begin + p.chunk);
-  const int parts = bad ? 0 : (n + p.chunk - 1) / p.chunk;
+  const int end = bad ? 0 : min(n, t_begin + p.span);
+  const int parts = bad ? 0 : min((n + p.apart - 1) / p.apart, p.nchunk);
   if (p.mode >= kQaLast && split >= max(parts, 1)) return;  // nobody reads a state of it
 
   // ---- the ring
-  const int nsteps = first < end ? (end - first + kRound - 1) / kRound : 0;
+  const int nsteps = first < end ? (end - first + stride - 1) / stride : 0;
   const int nstages = (nsteps + K - 1) / K;
   auto checked = [&](int pg, int i) {  // the page of this lane's block, -1: none
     if (pos_of(i) >= end) return -1;
@@ -244,7 +281,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     }
     __syncwarp();
     if (there >> lane & 1u) {
-      const int blk = ((first + (i * K + l / U) * kRound) >> 4) + l % U;
+      const int blk = ((first + (i * K + l / U) * stride) >> 4) + l % U;
       bulk_load(ring + s * SM::kStage + l * L::kBytes,
                 p.pool + ((((size_t)pg * p.nkv + h) << per_shift) + (blk & ((1 << per_shift) - 1))) * L::kBytes, L::kBytes,
                 &full[s]);
@@ -569,7 +606,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll 1
     for (int k = 0; k < K && done * K + k < nsteps; ++k) {
       const uint8_t* blk = ring + st * SM::kStage + k * (U * L::kBytes);
-      const int pos0 = first + (done * K + k) * kRound;
+      const int pos0 = first + (done * K + k) * stride;
       const int gone = ~(there >> (k * U)) & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
       if (pos0 + kStep - 1 > n - p.Q || gone)
         step(std::true_type{}, blk, pos0, gone);
@@ -655,7 +692,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        int* count = p.arrived + blockIdx.x;
+        int* count = p.arrived + bh;  // (up to eight rows are one tile)
         last = atomicAdd(count, 1) == parts - 1;
         if (last) *count = 0;  // as the next call wants it
       }
@@ -706,7 +743,7 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
   const int bh = blockIdx.x, b = bh / p.nkv, h = bh - b * p.nkv;
   const int n = __ldcg(p.ctx_len + b);
   const bool bad = n < 0 || n > (p.M << p.page_shift);
-  const int parts = bad ? 0 : (n + p.chunk - 1) / p.chunk;
+  const int parts = bad ? 0 : min((n + p.apart - 1) / p.apart, p.nchunk);
   for (int i = blockIdx.y * kQcThreads + threadIdx.x; i < p.R * (D / 4); i += gridDim.y * kQcThreads) {
     const int row = i / (D / 4), c4 = i - row * (D / 4);
     merge_parts(p, parts, bh, row, D, c4).store(p, b, h, row, D, c4);
@@ -719,14 +756,19 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
 // an SM; one at least) times steps of a round.  Where all CTAs are on the GPU at once and a sequence has at most
 // eight, its chunks are a cluster; else the last CTA of up to eight merges them, for up to eight rows (clusters that
 // wait for room leave SMs idle), and otherwise a second kernel, about three steps more.  All add in the same order.
-// Measured, us: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 13.7, merged by the last 14.7,
-// 4 chunks 19.2, 16 by a kernel 14.0; 32 of up to 2304, 10 key heads: 2 chunks merged by the last 21.5, by a kernel 23.1,
-// in clusters 27.3, 1 chunk 27.4, 4 chunks 23.8; 16 of 32K, 8 key heads and 16 rows: 7 chunks by a kernel 135, 8 chunks
-// 139, 8 in clusters 166, 16 chunks 141; one of 300, 10 key heads: 4 chunks in a cluster 4.8, by a kernel 6.5.
+// The chunks of a cluster, and those of many steps, take every nchunk-th step of the whole sequence: equal shares
+// whatever its length (13 sequences of 3 to 9000 positions: 12.8 us, one behind the other 13.7; 32 of 360 to 4500,
+// two chunks of 18 steps: 33.1 and 36.9).  Short chunks lie one behind the other: a sequence that ends in the first
+// of them then starts only one CTA (32 of 360 to 2245, two chunks of 9 steps: 21.8 us, by turns 22.7).
+// Measured (one behind the other), us: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 13.7,
+// merged by the last 14.7, 4 chunks 19.2, 16 by a kernel 14.0; 32 of up to 2304, 10 key heads: 2 chunks merged by the
+// last 21.5, by a kernel 23.1, in clusters 27.3, 1 chunk 27.4, 4 chunks 23.8; 16 of 32K, 8 key heads and 16 rows: 7
+// chunks by a kernel 135 (by turns 133), 8 chunks 139, 8 in clusters 166, 16 chunks 141; one of 300, 10 key heads: 4
+// chunks in a cluster 4.8, by a kernel 6.5.
 // The cut goes by the capacity (the lengths are on the device) and not by Q or the shared heads, so a row is
 // summed in the same order alone and among others.
 struct Cut {
-  int chunk, nchunk, mode;
+  int nchunk, apart, stride, span, mode;
 };
 Cut cut_of(int B, int nkv, long long cap) {
   constexpr int kRound = 32 * kQaWarps, kSlots = 152 * 3, kCost = 3, kTwo = 3;
@@ -745,12 +787,15 @@ Cut cut_of(int B, int nkv, long long cap) {
   if (clustered(kQaCluster8)) consider(kQaCluster8);
   for (int r = 1; r <= 8 && pairs > 0; ++r) consider(r * kSlots / pairs);
   Cut c;
-  c.chunk = (int)(at * kRound);
   c.nchunk = (int)((steps + at - 1) / at);
   c.mode = c.nchunk == 1 ? kQaDirect
            : clustered(c.nchunk) ? kQaCluster
            : c.nchunk <= kQcUnroll && pairs * kQaMaxTiles <= kQaCounters ? kQaLast
                                                                          : kQaParts;
+  const bool spread = c.mode == kQaCluster || at >= kQaSpread;
+  c.apart = spread ? kRound : (int)(at * kRound);
+  c.stride = spread ? c.nchunk * kRound : kRound;
+  c.span = spread ? (int)(steps * kRound) : c.apart;
   return c;
 }
 
@@ -835,8 +880,10 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.page_shift = 4;
   while ((1 << p.page_shift) < page) ++p.page_shift;
   const Cut cut = cut_of(B, nkv, (long long)M * page);
-  p.chunk = cut.chunk;
   p.nchunk = cut.nchunk;
+  p.apart = cut.apart;
+  p.stride = cut.stride;
+  p.span = cut.span;
   // (merging up to sixteen rows keeps a last CTA for longer than a second kernel takes: 137 us for 133.5)
   p.mode = cut.mode == kQaLast && p.R > 8 ? kQaParts : cut.mode;
   p.scale_log2 = scale * kQaLog2e;
@@ -849,9 +896,15 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.wait_ns = wait_limit_ns();
   const bool two = p.R > 8;  // the rows of an MMA, or its columns (half the MMAs for up to eight rows)
   p.rblocks = two ? (p.R + 15) / 16 : 1;
+  // CTAs that find no room at once wait for others to leave: with the longest first, the short ones fill the end (64
+  // sequences of up to 2048 positions, 512 CTAs with room for 456: 37.9 -> 33.4 us; 16 of 32K of any length, 896 CTAs:
+  // 74.8 -> 70.0; 80 of about 2048: 54.9 -> 57.4, what sorting costs).  Where nearly all fit, sorting only brings the long ones together on
+  // the SMs that are free first (32 of up to 4608, 640 CTAs, room for 608: 33.1 -> 36.0).
+  p.sorted = B > 1 && B <= kQaThreads && p.mode != kQaCluster &&
+             10ll * B * nkv * p.rblocks * p.nchunk > 11ll * dc->num_sms * (two ? kQaTwo : kQaOne);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = d == 128 ? (two ? run<128, 2, 2, 2, 2, 3>(p, *dc, s) : run<128, 1, 2, 1, 3, 4>(p, *dc, s))
-                                 : (two ? run<64, 2, 2, 2, 2, 3>(p, *dc, s) : run<64, 1, 2, 1, 3, 4>(p, *dc, s));
+  const cudaError_t e = d == 128 ? (two ? run<128, 2, 2, 2, 2, kQaTwo>(p, *dc, s) : run<128, 1, 2, 1, 3, kQaOne>(p, *dc, s))
+                                 : (two ? run<64, 2, 2, 2, 2, kQaTwo>(p, *dc, s) : run<64, 1, 2, 1, 3, kQaOne>(p, *dc, s));
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }
 

@@ -220,6 +220,39 @@ def test_attention_however_the_chunks_meet(lens, nkv, page, M, d, Q, grp):
     assert int(ws[:65536].count_nonzero()) == 0
 
 
+# more CTAs than the GPU has room for take the sequences by length (up to 128 of them); chunks that lie one behind the
+# other, and chunks by turns over the whole sequence
+@pytest.mark.parametrize("B,nkv,page,M,top", [(70, 10, 16, 4, 64), (128, 6, 16, 4, 60), (129, 6, 16, 4, 60),
+                                              (20, 8, 128, 32, 2500), (16, 8, 256, 128, 1700)])
+@pytest.mark.parametrize("Q,grp", [(2, 1), (3, 3)])
+def test_attention_by_length(B, nkv, page, M, top, Q, grp):
+    rs = np.random.default_rng(B)
+    lens = rs.integers(0, top + 1, B)
+    lens[:6] = 0, top, 1, top, 0, 17
+    lens[-3:] = 17, top, 2
+    c = Cache(lens, nkv, 64, page, M=M)
+    q = queries(c, Q, grp)
+    got = check(c, q)
+    np.testing.assert_array_equal(c.attend(q), got)
+    wrong = c.lens.copy()                                       # lengths out of range, in the first and the last place
+    wrong[[0, B // 2, -1]] = M * page + 1, -1, np.iinfo(np.int32).max
+    c.ctx = i32(wrong)
+    ref = got.copy()
+    ref[[0, B // 2, -1]] = 0
+    np.testing.assert_array_equal(c.attend(q), ref)
+    assert api.get_device_error() == 7
+
+
+@pytest.mark.parametrize("lens,nkv,page,M", [((2100, 900, 0, 517), 64, 64, 36), ((3000, 17, 2049), 80, 128, 72)])
+def test_a_row_does_not_depend_on_the_others_in_any_cut(lens, nkv, page, M):
+    c = Cache(lens, nkv, 64, page, M=M)                         # two chunks or more of 9 and of 18 steps or so
+    q = queries(c, 8, 2)
+    all_rows = c.attend(q)
+    for j in (0, 6):
+        c.ctx = i32(np.maximum(c.lens - 7 + j, 0))
+        np.testing.assert_array_equal(c.attend(q[:, j:j + 1])[c.lens > 7, 0], all_rows[c.lens > 7, j])
+
+
 @pytest.mark.parametrize("Q,grp", [(1, 1), (3, 5)])
 def test_sums_over_the_longest_chunk(Q, grp):
     # 456 (sequence, key head) pairs: one chunk each, of 32768 positions; flat weights over values of mean 0, where a
