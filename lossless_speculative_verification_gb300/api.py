@@ -259,7 +259,7 @@ def spec_q4_read(pool, table, ctx_len, N, nkv, d, page, k=None, v=None, stream=N
     out = []
     for t, name in ((k, "k"), (v, "v")):
         if t is None:
-            t = torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device)
+            t = torch.empty_like(out[0]) if out else torch.empty((B, N, nkv, d), dtype=torch.bfloat16, device=pool.device)
         else:
             _need_shape(t, (B, N, nkv, d), name)
             _here(dev, (t, torch.bfloat16, name))

@@ -35,54 +35,73 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(amax << 16) * (1.0f / 7.0f)));
 }
 
-// A group's scale and the whole numbers by it: n = rint(x / s), ties to even.
-// x * (1 / s) may be off by an ulp or two; the rest x - q s is exact (q and s have 32 bits together, and the rest
-// few), and rest / s added to q rounds to x / s, exactly where that is a half (one correction of a quotient by its
-// remainder, as Markstein describes).  Adding 1.5 * 2^23 then rounds to even.  All of it runs on the FMA pipe: with
-// a division and conversions eight prompts of 1156 positions were appended in 28 us, with a test for ties in 24.
+// Scales that 1 / s and 7 steps do for.
+__device__ __forceinline__ bool plain_scale(uint32_t bits) { return bits >= kSmallScale && bits < 0x7F80u; }
+
+// A group's scale and its reciprocal (0 for a scale that is not plain: a position beside the new ones has one, and
+// must not reach the other half of their word).
 struct Step {
   uint32_t bits;
   float s, inv;
 };
-constexpr float kRound = 12582912.0f;
 __device__ __forceinline__ Step step_of(uint32_t bits) {
   Step r;
   r.bits = bits;
   r.s = __uint_as_float(bits << 16);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.inv) : "f"(r.s));
+  if (!plain_scale(bits)) r.inv = 0.0f;
   return r;
-}
-__device__ __forceinline__ float whole(const Step& r, float x) {
-  float q = x * r.inv;
-  q = fmaf(fmaf(-q, r.s, x), r.inv, q);
-  return (q + kRound) - kRound;
-}
-// Scales that 1 / s and 7 steps do for.
-__device__ __forceinline__ bool plain_scale(uint32_t bits) { return bits >= kSmallScale && bits < 0x7F80u; }
-
-// The nibbles of four values in 16 bits, the first in the lowest place.  kPlain: the scale is plain.
-template <bool kPlain>
-__device__ __forceinline__ uint32_t codes4(const Step& r, float x0, float x1, float x2, float x3) {
-  if (!kPlain && !plain_scale(r.bits)) {
-    // a scale of 0 or NaN: n = 0 for all; small scales, whose reciprocal may overflow and whose own rounding may
-    // leave more than 7 steps, divide
-    if (r.bits == 0u || r.bits >= 0x7F80u) return 0x8888u;
-    const float x[4] = {x0, x1, x2, x3};
-    uint32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x[i], r.s)), -8.0f), 7.0f)) + 8) << (4 * i);
-    return v;
-  }
-  // n0 + 16 n1 + 256 n2 + 4096 n3 + 0x8888 is exact in fp32
-  float v = fmaf(whole(r, x3), 4096.0f, kRound + 34952.0f);
-  v = fmaf(whole(r, x2), 256.0f, v);
-  v = fmaf(whole(r, x1), 16.0f, v);
-  v += whole(r, x0);
-  return __float_as_uint(v) & 0xFFFFu;
 }
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// rint(x / s), ties to even, of two values, in the low bits of fp32 that are 1.5 * 2^23 more; the scale is plain.
+// x and s have 8 significant bits, so that x / s is k + 1/2 exactly or at least 1/512 away from it:
+// x / s = X 2^a / (S 2^b)
+// differs by |2^(a+1) X - (2k+1) 2^b S| / (2^(b+1) S), where the numerator is a multiple of 2^b and S < 256, or
+// 2^(b-a-1) S >= 256 > X.  x * (1 / s), less than 2^-19 off, is added to 1536 and so becomes a multiple of 2^-13:
+// what was k + 1/2 is that again, and nothing else becomes it.  The second addition rounds to a whole number.
+// (Eight prompts of 1156 positions are appended in 12.9 us; a quotient corrected by its remainder: 15.5, a division:
+// 28.)
+constexpr float kSnap = 1536.0f, kRound = 12582912.0f;
+__device__ __forceinline__ void whole2(float inv0, float inv1, float x0, float x1, uint32_t* n0, uint32_t* n1) {
+  asm("{\n.reg .b64 x, i, c, r;\n"
+      "mov.b64 x, {%2, %3};\nmov.b64 i, {%4, %5};\nmov.b64 c, {%6, %6};\nmov.b64 r, {%7, %7};\n"
+      "fma.rn.f32x2 x, x, i, c;\nadd.rn.f32x2 x, x, r;\nmov.b64 {%0, %1}, x;\n}"
+      : "=r"(*n0), "=r"(*n1)
+      : "f"(x0), "f"(x1), "f"(inv0), "f"(inv1), "f"(kSnap), "f"(kRound - kSnap));
+}
+// Eight of them as the nibbles n + 8 of a word, the first in the lowest place: added up in their places, where the
+// bits of 1.5 * 2^23 and the 8s make one constant.
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&n)[8]) {
+  uint32_t w = n[7];
+#pragma unroll
+  for (int i = 6; i >= 0; --i) w = (w << 4) + n[i];
+  return w + (0x88888888u - 0x4B400000u * 0x11111111u);
+}
+// One code as a nibble, whatever the scale: of 0 or NaN, n = 0; small scales, whose reciprocal may overflow and whose
+// own rounding may leave more than 7 steps, divide.
+__device__ __forceinline__ uint32_t any_code(const Step& r, float x) {
+  if (r.bits == 0u || r.bits >= 0x7F80u) return 8u;
+  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, r.s)), -8.0f), 7.0f)) + 8);
+}
+// The word of eight values x[i] in the steps of r[i / 4].
+template <bool kPlain>
+__device__ __forceinline__ uint32_t codes8(const Step& r0, const Step& r1, const float (&x)[8]) {
+  if (kPlain) {
+    uint32_t n[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float inv = i < 4 ? r0.inv : r1.inv;
+      whole2(inv, inv, x[i], x[i + 1], &n[i], &n[i + 1]);
+    }
+    return word_of(n);
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w |= any_code(i < 4 ? r0 : r1, x[i]) << (4 * i);
+  return w;
+}
 
 struct QwParams {
   const int32_t* table;    // [B, M]
@@ -141,9 +160,11 @@ __device__ __forceinline__ void append_keys(const uint4 (&x)[Q4Block<D>::W], boo
   }
   auto words = [&](auto tag) {
 #pragma unroll
-    for (int j = 0; j < L::W; ++j)
-      out.w[j] = codes4<decltype(tag)::value>(st[j >> 1], lo_f(x[j].x), lo_f(x[j].y), lo_f(x[j].z), lo_f(x[j].w)) |
-                 codes4<decltype(tag)::value>(st[j >> 1], hi_f(x[j].x), hi_f(x[j].y), hi_f(x[j].z), hi_f(x[j].w)) << 16;
+    for (int j = 0; j < L::W; ++j) {
+      const float v[8] = {lo_f(x[j].x), lo_f(x[j].y), lo_f(x[j].z), lo_f(x[j].w),
+                          hi_f(x[j].x), hi_f(x[j].y), hi_f(x[j].z), hi_f(x[j].w)};
+      out.w[j] = codes8<decltype(tag)::value>(st[j >> 1], st[j >> 1], v);
+    }
   };
   if (__all_sync(0xffffffffu, plain || !in))  // (positions that are not there are not stored)
     words(std::true_type{});
@@ -183,11 +204,12 @@ __device__ __forceinline__ void append_values(const uint2 (&x)[2][Q4Block<D>::W]
     if (in[e] && g == 0) q4_store_scales<L::G>(blk + L::kVs + (8 * half + 2 * t + e) * 2 * L::G, sc);
   }
   auto words = [&](auto tag) {
-    constexpr bool kPlain = decltype(tag)::value;
 #pragma unroll
-    for (int m = 0; m < L::W; ++m)
-      out.w[m] = codes4<kPlain>(st[0][m >> 1], lo_f(x[0][m].x), hi_f(x[0][m].x), lo_f(x[0][m].y), hi_f(x[0][m].y)) |
-                 codes4<kPlain>(st[1][m >> 1], lo_f(x[1][m].x), hi_f(x[1][m].x), lo_f(x[1][m].y), hi_f(x[1][m].y)) << 16;
+    for (int m = 0; m < L::W; ++m) {
+      const float v[8] = {lo_f(x[0][m].x), hi_f(x[0][m].x), lo_f(x[0][m].y), hi_f(x[0][m].y),
+                          lo_f(x[1][m].x), hi_f(x[1][m].x), lo_f(x[1][m].y), hi_f(x[1][m].y)};
+      out.w[m] = codes8<decltype(tag)::value>(st[0][m >> 1], st[1][m >> 1], v);
+    }
   };
   if (__all_sync(0xffffffffu, plain))
     words(std::true_type{});
@@ -204,8 +226,9 @@ __device__ __forceinline__ void append_values(const uint2 (&x)[2][Q4Block<D>::W]
   }
 }
 
-// Twelve CTAs an SM: a CTA is one chain of loads (length, entry and rows, then the codes), and what is in flight on
-// an SM is what its CTAs have begun (eight prompts of 1156 positions: 16 us with ten, 15 with twelve).
+// Up to twelve CTAs an SM (37 to 40 registers): a CTA is one chain of loads (length, entry and rows, then the codes),
+// and what is in flight on an SM is what its CTAs have begun.  Eight prompts of 1156 positions move 60 MB in 12.9 us
+// (4.7 TB/s; blocks two or four a CTA: 13.1, 14.0), and are read back in 11.7.
 // A warp's share is a half block (8 positions) of the keys or of the values: the four parts of a block are the
 // CTA's warps.  32 x 4 positions of 10 heads were written and read back in 17.6 us with whole blocks a warp, in 9.2
 // with quarters: the call is as long as one warp's chain of loads, maxima and codes.
