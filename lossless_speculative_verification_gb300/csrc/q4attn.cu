@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   constexpr int W = L::W, G = L::G;
   constexpr int kRows = SM::kRows;
   constexpr int kStep = 16 * U;            // positions a warp takes at a time
-  constexpr int kRound = kStep * kQaWarps;
   constexpr int kBlocks = K * U;           // blocks of a stage
   constexpr int kBatch = 32 / kBlocks;     // stages whose pages the lanes hold
   extern __shared__ __align__(128) uint8_t smem[];
@@ -750,42 +749,45 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
   }
 }
 
-// The cut of a sequence: positions of a chunk, a whole number of steps of the four warps (128 positions), and
-// how the chunks meet.  Many chunks fill the GPU and make the chains of steps short, but each costs its CTA about
-// as much as three steps (queries, first loads, the states' meeting): the cut with the least rounds of CTAs (three
-// an SM; one at least) times steps of a round.  Where all CTAs are on the GPU at once and a sequence has at most
-// eight, its chunks are a cluster; else the last CTA of up to eight merges them, for up to eight rows (clusters that
-// wait for room leave SMs idle), and otherwise a second kernel, about three steps more.  All add in the same order.
+// The cut of a sequence: chunks of a whole number of steps of the four warps (128 positions), and how they meet.
+// The lengths are on the device and may be anything up to the capacity, so the cut weighs, in steps of a CTA that has
+// a third of an SM: half the capacity's steps and three for every chunk (queries, first loads, the states' meeting),
+// spread over the GPU; 0.3 of a chunk's steps, which stay behind when the rest is done, and 0.2 more where no CTA
+// waits for another (none is left to fill in); a tenth for every state that a second kernel merges; 0.03 for every
+// step of the rounds that full sequences would take.  (Fitted to 44 batches of 1 to 128 sequences of up to 1152 to
+// 131072 positions, each cut into 1 to 128 chunks: 3.5 % above the best of each, 17 % at most.  8 sequences of up to
+// 32K, 10 key heads: 6 chunks 75.7 us, 10 51.4, 12 44.6, 64 80.3; 64 of up to 8192, 8 key heads and 16 rows: 1 chunk
+// 108, 2 80.6, 4 90.5; 32 of up to 9216, 10 key heads: 2 chunks 61.3, 3 47.2, 6 54.1.)
+// Where all CTAs are on the GPU at once and a sequence has at most eight, its chunks are a cluster (one of 300, 10 key
+// heads: 4 chunks in a cluster 4.8 us, by a kernel 6.5); else the last CTA of up to eight merges them, for up to eight
+// rows (clusters that wait for room leave SMs idle: 2 chunks of 32 of up to 2304 merged by the last 21.5, by a kernel
+// 23.1, in clusters 27.3), and otherwise a second kernel.  All add in the same order.
 // The chunks of a cluster, and those of many steps, take every nchunk-th step of the whole sequence: equal shares
 // whatever its length (13 sequences of 3 to 9000 positions: 12.8 us, one behind the other 13.7; 32 of 360 to 4500,
 // two chunks of 18 steps: 33.1 and 36.9).  Short chunks lie one behind the other: a sequence that ends in the first
 // of them then starts only one CTA (32 of 360 to 2245, two chunks of 9 steps: 21.8 us, by turns 22.7).
-// Measured (one behind the other), us: 13 sequences of up to 9000 positions, 3 key heads: 8 chunks in a cluster 13.7,
-// merged by the last 14.7, 4 chunks 19.2, 16 by a kernel 14.0; 32 of up to 2304, 10 key heads: 2 chunks merged by the
-// last 21.5, by a kernel 23.1, in clusters 27.3, 1 chunk 27.4, 4 chunks 23.8; 16 of 32K, 8 key heads and 16 rows: 7
-// chunks by a kernel 135 (by turns 133), 8 chunks 139, 8 in clusters 166, 16 chunks 141; one of 300, 10 key heads: 4
-// chunks in a cluster 4.8, by a kernel 6.5.
-// The cut goes by the capacity (the lengths are on the device) and not by Q or the shared heads, so a row is
-// summed in the same order alone and among others.
+// The cut goes by the capacity and not by Q or the shared heads, so a row is summed in the same order alone and among
+// others.
 struct Cut {
   int nchunk, apart, stride, span, mode;
 };
 Cut cut_of(int B, int nkv, long long cap) {
-  constexpr int kRound = 32 * kQaWarps, kSlots = 152 * 3, kCost = 3, kTwo = 3;
+  constexpr int kRound = 32 * kQaWarps, kSlots = 152 * 3, kSmall = 16;
   const long long pairs = (long long)B * nkv, steps = (cap + kRound - 1) / kRound;
-  const long long most = (steps + kQaMaxSteps - 1) / kQaMaxSteps;
-  long long best = 1ll << 62, at = steps;
+  const long long least = (steps + kQaMaxSteps - 1) / kQaMaxSteps;
   auto clustered = [&](long long used) { return used <= kQaCluster8 && pairs * used <= kSlots; };
-  auto consider = [&](long long k) {
-    k = k < most ? most : k > steps ? steps : k;
-    const long long len = (steps + k - 1) / k, used = (steps + len - 1) / len;
-    const long long cost = (pairs * used > kSlots ? pairs * used : kSlots) * (len + kCost) +
-                           (used == 1 || clustered(used) ? 0 : (used <= kQcUnroll ? 1 : kTwo) * kSlots);
+  // up to sixteen chunks, and numbers around the one at which the sum below is least
+  const long long mid = (long long)sqrt(40.0 * kSlots * steps / (300.0 * pairs + 10.0 * kSlots));
+  long long best = 1ll << 62, at = steps;
+  for (int i = 1; i <= kSmall + 3; ++i) {
+    long long k = i <= kSmall ? i : mid * (i - kSmall + 2) / 4;
+    k = k < least ? least : k > steps ? steps : k;
+    const long long len = (steps + k - 1) / k, used = (steps + len - 1) / len, ctas = pairs * used;
+    const long long cost = pairs * 50 * steps + ctas * 300 +
+                           kSlots * ((10 * ctas <= 11 * kSlots ? 50 : 30) * len + (used > kQcUnroll ? 10 * used : 0) +
+                                     3 * ((ctas + kSlots - 1) / kSlots) * (len + 3));
     if (cost < best) best = cost, at = len;
-  };
-  consider(1);
-  if (clustered(kQaCluster8)) consider(kQaCluster8);
-  for (int r = 1; r <= 8 && pairs > 0; ++r) consider(r * kSlots / pairs);
+  }
   Cut c;
   c.nchunk = (int)((steps + at - 1) / at);
   c.mode = c.nchunk == 1 ? kQaDirect
@@ -898,8 +900,8 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.rblocks = two ? (p.R + 15) / 16 : 1;
   // CTAs that find no room at once wait for others to leave: with the longest first, the short ones fill the end (64
   // sequences of up to 2048 positions, 512 CTAs with room for 456: 37.9 -> 33.4 us; 16 of 32K of any length, 896 CTAs:
-  // 74.8 -> 70.0; 80 of about 2048: 54.9 -> 57.4, what sorting costs).  Where nearly all fit, sorting only brings the long ones together on
-  // the SMs that are free first (32 of up to 4608, 640 CTAs, room for 608: 33.1 -> 36.0).
+  // 91 -> 70.5; 80 of about 2048: 54.9 -> 57.4, what sorting costs).  Where nearly all fit, sorting only brings the
+  // long ones together on the SMs that are free first (32 of up to 4608, 640 CTAs, room for 608: 33.1 -> 36.0).
   p.sorted = B > 1 && B <= kQaThreads && p.mode != kQaCluster &&
              10ll * B * nkv * p.rblocks * p.nchunk > 11ll * dc->num_sms * (two ? kQaTwo : kQaOne);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -208,6 +208,9 @@ def test_attention_long(d, Q, nkv, grp, n):
     ((900, 1024, 1, 0, 517), 2, 64, 16),
     (tuple(range(30, 1230, 40)), 10, 64, 20),
     ((3000, 17, 9000, 6000), 1, 128, 80),
+    ((3000, 17, 9000, 0, 5000, 1) + (200,) * 20, 2, 128, 80),
+    ((20000, 30000), 2, 256, 128),
+    (tuple(range(30, 2200, 70)), 10, 64, 36),
 ])
 @pytest.mark.parametrize("d,Q,grp", [(64, 2, 1), (64, 3, 4), (128, 1, 2), (128, 1, 9)])
 def test_attention_however_the_chunks_meet(lens, nkv, page, M, d, Q, grp):
@@ -223,7 +226,8 @@ def test_attention_however_the_chunks_meet(lens, nkv, page, M, d, Q, grp):
 # more CTAs than the GPU has room for take the sequences by length (up to 128 of them); chunks that lie one behind the
 # other, and chunks by turns over the whole sequence
 @pytest.mark.parametrize("B,nkv,page,M,top", [(70, 10, 16, 4, 64), (128, 6, 16, 4, 60), (129, 6, 16, 4, 60),
-                                              (20, 8, 128, 32, 2500), (16, 8, 256, 128, 1700)])
+                                              (20, 8, 128, 32, 2500), (16, 8, 256, 128, 1700),
+                                              (36, 10, 64, 36, 2304)])
 @pytest.mark.parametrize("Q,grp", [(2, 1), (3, 3)])
 def test_attention_by_length(B, nkv, page, M, top, Q, grp):
     rs = np.random.default_rng(B)
@@ -253,30 +257,31 @@ def test_a_row_does_not_depend_on_the_others_in_any_cut(lens, nkv, page, M):
         np.testing.assert_array_equal(c.attend(q[:, j:j + 1])[c.lens > 7, 0], all_rows[c.lens > 7, j])
 
 
+@pytest.mark.parametrize("B", [57, 1200])
 @pytest.mark.parametrize("Q,grp", [(1, 1), (3, 5)])
-def test_sums_over_the_longest_chunk(Q, grp):
-    # 456 (sequence, key head) pairs: one chunk each, of 32768 positions; flat weights over values of mean 0, where a
-    # sum that loses its low bits shows.  32 MMAs between two times that the 8 S are taken off (32 * 2^-23 * 23 S),
+def test_sums_over_the_longest_chunk(Q, grp, B):
+    # 9600 (sequence, key head) pairs: one chunk each, of 32768 positions (456: a few); flat weights over values of mean
+    # 0, where a sum that loses its low bits shows.  32 MMAs between two times that the 8 S are taken off (32 * 2^-23 * 23 S),
     # 512 MMAs into an accumulator that has them off (512 * 2^-23 A)
-    lens = [0] * 56 + [32768]
+    lens = [0] * (B - 1) + [32768]
     rs = np.random.default_rng(0)
     k, v = (rs.normal(size=(1, 32768, 8, 64)) for _ in range(2))
     one = Cache([32768], 8, 64, 128, k=k, v=v)
-    q = np.zeros((57, Q, 8 * grp, 64), np.uint16)
-    q[56] = bits(rs.normal(size=(Q, 8 * grp, 64)) * 0.05)
-    table = np.full((57, one.M), -1, np.int32)
-    table[56] = one.tb
-    ws = api.spec_q4_attention_workspace(57, Q, one.M, 128, 8 * grp, 8, 64)
+    q = np.zeros((B, Q, 8 * grp, 64), np.uint16)
+    q[-1] = bits(rs.normal(size=(Q, 8 * grp, 64)) * 0.05)
+    table = np.full((B, one.M), -1, np.int32)
+    table[-1] = one.tb
+    ws = api.spec_q4_attention_workspace(B, Q, one.M, 128, 8 * grp, 8, 64)
     got = api.spec_q4_attention(dev(q), one.pool, i32(table), i32(lens), 8, 128, ws).float().cpu().numpy().astype(np.float64)
-    assert (got[:56] == 0).all()
+    assert (got[:-1] == 0).all()
     kf, vf = one.values()
-    ref, A = q4.attention(q4.bf16_f64(q[56:]), kf, vf, one.lens, 1 / 8)
+    ref, A = q4.attention(q4.bf16_f64(q[-1:]), kf, vf, one.lens, 1 / 8)
     S = np.repeat(q4.bf16_f64(q4.quantise(one.v)[1]), 64, -1).max()
     tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -11 * A + 32 * 2.0 ** -23 * 23 * S + (512 + 272) * 2.0 ** -23 * A
-    assert (np.abs(got[56:] - ref) <= tol).all()
+    assert (np.abs(got[-1:] - ref) <= tol).all()
     # over all elements little more than the rounding of the output, whose steps' rms is 2^-8 / sqrt(3) of the power of
     # two below a value, and so at most that of the value
-    assert np.linalg.norm(got[56:] - ref) <= 2.0 ** -8 / np.sqrt(3) * np.linalg.norm(ref)
+    assert np.linalg.norm(got[-1:] - ref) <= 2.0 ** -8 / np.sqrt(3) * np.linalg.norm(ref)
 
 
 def test_attention_peaked_and_scaled():
