@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   constexpr int kTiles = NT == 1 ? 2 * W : 4 * W;
   float o[kTiles][4];
   float cs[G][4];  // sum of P s of every group
-  float m_run[2] = {-INFINITY, -INFINITY}, base[2] = {0.0f, 0.0f};  // base: what P is 2^0 at
+  float m_run[2] = {-INFINITY, -INFINITY}, nbase[2] = {0.0f, 0.0f};  // -nbase: what P is 2^0 at
   float l_run[2][NT] = {};  // sums of P over this lane's positions (NT = 2: the even and the odd ones apart, so
                             // that both forms add in the same order)
 #pragma unroll
@@ -374,6 +374,15 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   auto step = [&](auto tag, const uint8_t* blk, int pos0, int gone) {
     constexpr bool kMasked = decltype(tag)::value;
     auto row_of = [](int c) { return NT == 1 ? (c & 1) : (c >> 1); };
+    // the scales that the elements c and c + 1 of a tile are of
+    auto scales_of = [](const uint32_t (&w)[2][G == 2 ? 2 : 1], int e, int c, int gr) {
+      if (NT == 1) {
+        const float s = q4_scale(w[c >> 1][0], gr);
+        return make_float2(s, s);
+      }
+      return G == 2 ? make_float2(q4_scale(w[e][0], gr), q4_scale(w[e][G - 1], gr))
+                    : make_float2(q4_scale(w[e][0], 0), q4_scale(w[e][0], 1));
+    };
     // ---- scores, before the row's factor
     float x[U][NT][4];
     {
@@ -429,10 +438,10 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
           for (int e = 0; e < NT; ++e)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float s = NT == 1 ? q4_scale(ks[u][c >> 1][0], gr)
-                                      : G == 2 ? q4_scale(ks[u][e][c & (G - 1)], gr) : q4_scale(ks[u][e][0], c & 1);
-              x[u][e][c] = gr == 0 ? __fmul_rn(acc[u][e][c], s) : fmaf(acc[u][e][c], s, x[u][e][c]);
+            for (int c = 0; c < 4; c += 2) {
+              const float2 s = scales_of(ks[u], e, c, gr), a = make_float2(acc[u][e][c], acc[u][e][c + 1]);
+              const float2 v = gr == 0 ? mul2(a, s) : fma2(a, s, make_float2(x[u][e][c], x[u][e][c + 1]));
+              x[u][e][c] = v.x, x[u][e][c + 1] = v.y;
             }
       }
     }
@@ -491,7 +500,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
         const float m = top[r] > m_run[r] + kQaSlack ? top[r] : m_run[r];
         corr[r] = m == -INFINITY ? 1.0f : ex2_ftz(m_run[r] - m);
         m_run[r] = m;
-        base[r] = m == -INFINITY ? 0.0f : m - kQaLift;
+        nbase[r] = m == -INFINITY ? 0.0f : kQaLift - m;
 #pragma unroll
         for (int i = 0; i < NT; ++i) l_run[r][i] *= corr[r];
       }
@@ -509,11 +518,17 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
 #pragma unroll
       for (int e = 0; e < NT; ++e)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v = ex2_ftz(fmaf(x[u][e][c], fq[row_of(c)], -base[row_of(c)]));
-          if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) v = 0.0f;
-          x[u][e][c] = v;
-          l_run[row_of(c)][NT == 1 ? 0 : (c & 1)] += v;
+        for (int c = 0; c < 4; c += 2) {
+          const int ra = row_of(c), rb = row_of(c + 1);
+          const float2 at = fma2(make_float2(x[u][e][c], x[u][e][c + 1]), make_float2(fq[ra], fq[rb]),
+                                 make_float2(nbase[ra], nbase[rb]));
+          float2 v = make_float2(ex2_ftz(at.x), ex2_ftz(at.y));
+          if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) v.x = 0.0f;
+          if (kMasked && (hidden >> (8 * u + 4 * e + c + 1) & 1u)) v.y = 0.0f;
+          x[u][e][c] = v.x, x[u][e][c + 1] = v.y;
+          float &la = l_run[ra][0], &lb = l_run[rb][NT - 1];
+          const float2 l = add2(make_float2(la, lb), v);
+          la = l.x, lb = l.y;
         }
     // ---- the weighted values
 #pragma unroll
@@ -539,11 +554,11 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
         for (int e = 0; e < NT; ++e) {
           float w[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float s = NT == 1 ? q4_scale(vs[c >> 1][0], gr)
-                                    : G == 2 ? q4_scale(vs[e][c & (G - 1)], gr) : q4_scale(vs[e][0], c & 1);
-            w[c] = x[u][e][c] * s;
+          for (int c = 0; c < 4; c += 2) {
+            const float2 v = mul2(make_float2(x[u][e][c], x[u][e][c + 1]), scales_of(vs, e, c, gr));
+            w[c] = v.x, w[c + 1] = v.y;
             if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
+            if (kMasked && (hidden >> (8 * u + 4 * e + c + 1) & 1u)) w[c + 1] = 0.0f;
           }
           pp[e][0] = pack_f16(w[0], w[1]);
           pp[e][1] = pack_f16(w[2], w[3]);
