@@ -25,9 +25,9 @@
 // in turn, each from a ring of its own; their states (maximum, sum, output) meet
 // in shared memory, those of the chunks as cut_of says.  Which positions are a chunk's goes by the capacity alone
 // and both forms add in the same order, so a row's result does not depend on the other rows of the call.
-// A step of 16 rows is 600 instructions, 160 of them dequantising; 16 x 32K
-// positions of 8 key heads take 133 us, 4.1 TB/s of cache, with 53 % of the issue
-// slots, 50 % of the ALU and 48 % of the tensor pipe taken: what bounds it is how
+// A step of 16 rows is 560 instructions, 160 of them dequantising; 16 x 32K
+// positions of 8 key heads take 132 us, 4.1 TB/s of cache, with 48 % of the issue
+// slots, 47 % of the ALU and 47 % of the tensor pipe taken: what bounds it is how
 // far three CTAs an SM (168 registers a thread) overlap them.
 #include <limits.h>
 #include <math.h>
