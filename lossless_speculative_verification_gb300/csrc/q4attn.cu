@@ -49,7 +49,8 @@ constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before th
 constexpr float kQaLog2e = 1.4426950408889634f;
 constexpr uint64_t kQaDrainNs = 2000000000ull;
 constexpr int kQaOne = 4, kQaTwo = 3;  // CTAs an SM: up to eight rows, nine to sixteen
-constexpr int kQaSpread = 16;       // steps of a chunk from which on they are taken from all over the sequence
+constexpr int kQaRound = 32 * kQaWarps;  // positions of a step of a chunk
+constexpr int kQaNear = 16;         // steps of chunks that share a CTA, at most
 constexpr int kQaCentre = 16;       // steps between two centrings
 constexpr int kQaCounters = 16384;  // tiles of rows whose CTAs may be counted; their counters lead the workspace
 constexpr int kQaMaxTiles = 8;      // tiles of 16 rows of a key head, at most (8 queries x 16 heads)
@@ -64,7 +65,6 @@ struct QaParams {
   int mode;
   int sorted;  // the CTAs take the sequences by falling length
   int nchunk;  // chunks of a sequence
-  int apart, stride, span;  // positions between the starts of two chunks, between the steps of one, and that it spans
   float scale_log2;   // scale * log2(e)
   bf16* out;          // [B, Q, nh, D]
   int* arrived;       // [B * nkv * rblocks] CTAs that have written their state; 0 before and after a call
@@ -81,7 +81,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // How the chunks' states meet: there is one chunk, the chunks' CTAs are a cluster, the last CTA of a tile of rows to
-// arrive merges them, or a second kernel does.
+// arrive merges them, or a second kernel does.  (Short ones may be groups of one CTA instead.)
 enum : int { kQaDirect = 0, kQaCluster = 1, kQaLast = 2, kQaParts = 3 };
 constexpr int kQaCluster8 = 8;  // chunks of a cluster, at most
 
@@ -152,7 +152,7 @@ __device__ __forceinline__ int2 by_length(const QaParams& p, int rank) {
   __shared__ int2 found;
   const int tid = threadIdx.x;
   const int n = tid < p.B ? __ldcg(p.ctx_len + tid) : INT_MIN;
-  len[tid] = n;
+  if (tid < kQaThreads) len[tid] = n;
   __syncthreads();
   if (tid < p.B) {
     int before = 0;
@@ -188,8 +188,8 @@ struct QaSmem {
   static constexpr int kTotal = kMlAll + kRows * 8;
 };
 
-template <int D, int NT, int U, int K, int S, int kPerSm>
-__global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaParams p) {
+template <int D, int NT, int U, int K, int S, int kPerSm, int kGroups>
+__global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q4_kernel(const QaParams p) {
   using L = Q4Block<D>;
   using SM = QaSmem<D, NT, U, K, S>;
   constexpr int W = L::W, G = L::G;
@@ -197,8 +197,16 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   constexpr int kStep = 16 * U;            // positions a warp takes at a time
   constexpr int kBlocks = K * U;           // blocks of a stage
   constexpr int kBatch = 32 / kBlocks;     // stages whose pages the lanes hold
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  const int group = kGroups > 1 ? (int)threadIdx.x / kQaThreads : 0, tid = (int)threadIdx.x - group * kQaThreads;
+  uint8_t* smem = smem_all + group * SM::kTotal;
+  auto group_sync = [&]() {
+    if (kGroups > 1)
+      named_bar_sync(1 + group, kQaThreads);
+    else
+      __syncthreads();
+  };
+  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * SM::kWarp;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars) + warp * S;
   int* here = reinterpret_cast<int*>(smem + SM::kHere) + warp * S;
@@ -206,23 +214,23 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
   fence_barrier_init();
   __syncwarp();
   const int tiles = p.nkv * p.rblocks;
-  int split = blockIdx.y, b = blockIdx.x / tiles, ht = blockIdx.x - b * tiles, n = 0;
+  int split = kGroups > 1 ? group : blockIdx.y, b = blockIdx.x / tiles, ht = blockIdx.x - b * tiles, n = 0;
   if (p.sorted) {  // the longest sequence's chunks first
     pdl_wait();
-    const int k = blockIdx.y * gridDim.x + blockIdx.x, per = tiles * p.nchunk, rank = k / per;
-    split = (k - rank * per) / tiles;
-    ht = k - rank * per - split * tiles;
+    const int k = blockIdx.y * gridDim.x + blockIdx.x, per = tiles * gridDim.y, rank = k / per;
+    if (kGroups == 1) split = (k - rank * per) / tiles;
+    ht = k - rank * per - (kGroups == 1 ? split * tiles : 0);
     const int2 s = by_length(p, rank);
     b = s.x;
     n = s.y;
   }
   const int h = ht / p.rblocks, rb = ht - h * p.rblocks, bh = b * p.nkv + h;
   const int r0 = rb * kRows, nrows = min(kRows, p.R - r0);
-  const int t_begin = split * p.apart, stride = p.stride;
+  const int stride = p.nchunk * kQaRound;
   // step i of this warp is the U blocks from position first + i * stride on, a stage K steps
-  const int first = t_begin + warp * kStep;
+  const int first = split * kQaRound + warp * kStep;
   const int per_shift = p.page_shift - 4;
-  const int cap = min(p.M << p.page_shift, t_begin + p.span);
+  const int cap = p.M << p.page_shift;
   // lane l has block l % kBlocks of stage i + l / kBlocks
   auto pos_of = [&](int i) {
     return first + ((i + lane / kBlocks) * K + lane % kBlocks / U) * stride + 16 * (lane % U);
@@ -250,10 +258,10 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
                 : make_uint4(0u, 0u, 0u, 0u);
 
   const bool bad = n < 0 || n > (p.M << p.page_shift);
-  if (bad && threadIdx.x == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
-  const int end = bad ? 0 : min(n, t_begin + p.span);
-  const int parts = bad ? 0 : min((n + p.apart - 1) / p.apart, p.nchunk);
-  if (p.mode >= kQaLast && split >= max(parts, 1)) return;  // nobody reads a state of it
+  if (bad && tid == 0 && split == 0 && h == 0 && rb == 0) set_error(p.err, kErrDeviceIndex);
+  const int end = bad ? 0 : n;
+  const int parts = bad ? 0 : min((n + kQaRound - 1) / kQaRound, p.nchunk);
+  if (kGroups == 1 && p.mode >= kQaLast && split >= max(parts, 1)) return;  // nobody reads a state of it
 
   // ---- the ring
   const int nsteps = first < end ? (end - first + stride - 1) / stride : 0;
@@ -342,7 +350,7 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       reinterpret_cast<int*>(qs + SM::kLim)[qr] = qr < nrows ? n - p.Q + (r0 + qr) / p.grp : -1;
     }
   }
-  __syncthreads();
+  group_sync();
 #pragma unroll 1
   for (int i = 1; i < S && i < nstages; ++i) issue(i, i);
   __syncwarp();
@@ -676,8 +684,8 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       }
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nrows * (D / 4); i += kQaThreads) {
+  group_sync();
+  for (int i = tid; i < nrows * (D / 4); i += kQaThreads) {
     const int r = i / (D / 4), c4 = i - r * (D / 4), row = r0 + r;
     float2 ml[kQaWarps];
     float4* at0 = reinterpret_cast<float4*>(smem + (r * SM::kStride + 4 * c4) * 4);
@@ -689,9 +697,9 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
     }
 #pragma unroll
     for (int w = 0; w < kQaWarps; ++w) acc.add(ml[w], *(at0 + w * (SM::kWarp / 16)));
-    if (p.mode == kQaDirect || (p.mode == kQaLast && parts <= 1)) {
+    if (kGroups == 1 && (p.mode == kQaDirect || (p.mode == kQaLast && parts <= 1))) {
       acc.store(p, b, h, row, D, c4);
-    } else if (p.mode != kQaCluster) {
+    } else if (kGroups == 1 && p.mode != kQaCluster) {
       const size_t at = ((size_t)bh * p.nchunk + split) * p.R + row;
       *reinterpret_cast<float4*>(p.o_part + at * D + 4 * c4) = acc.o;
       if (c4 == 0) *reinterpret_cast<float2*>(p.ml_part + at * 2) = make_float2(acc.m, acc.l);
@@ -699,6 +707,27 @@ __global__ void __launch_bounds__(kQaThreads, kPerSm) attn_q4_kernel(const QaPar
       *at0 = acc.o;  // nobody else reads this place of warp 0's state
       if (c4 == 0) *reinterpret_cast<float2*>(smem + SM::kMlAll + 8 * r) = make_float2(acc.m, acc.l);
     }
+  }
+  if constexpr (kGroups > 1) {  // the chunks are the CTA's groups
+    __syncthreads();
+    const int live = max(1, parts);
+    for (int i = threadIdx.x; i < nrows * (D / 4); i += kQaThreads * kGroups) {
+      const int r = i / (D / 4), c4 = i - r * (D / 4);
+      float2 ml[kGroups];
+      QaState acc;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        ml[k] = k < live ? *reinterpret_cast<const float2*>(smem_all + k * SM::kTotal + SM::kMlAll + 8 * r)
+                         : make_float2(-INFINITY, 0.0f);
+        acc.m = fmaxf(acc.m, ml[k].x);
+      }
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+        if (k < live)
+          acc.add(ml[k], *reinterpret_cast<const float4*>(smem_all + k * SM::kTotal + (r * SM::kStride + 4 * c4) * 4));
+      acc.store(p, b, h, r0 + r, D, c4);
+    }
+    return;
   }
   if constexpr (NT == 1) {
     if (p.mode == kQaLast && parts > 1) {
@@ -757,7 +786,7 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
   const int bh = blockIdx.x, b = bh / p.nkv, h = bh - b * p.nkv;
   const int n = __ldcg(p.ctx_len + b);
   const bool bad = n < 0 || n > (p.M << p.page_shift);
-  const int parts = bad ? 0 : min((n + p.apart - 1) / p.apart, p.nchunk);
+  const int parts = bad ? 0 : min((n + kQaRound - 1) / kQaRound, p.nchunk);
   for (int i = blockIdx.y * kQcThreads + threadIdx.x; i < p.R * (D / 4); i += gridDim.y * kQcThreads) {
     const int row = i / (D / 4), c4 = i - row * (D / 4);
     merge_parts(p, parts, bh, row, D, c4).store(p, b, h, row, D, c4);
@@ -777,18 +806,17 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
 // heads: 4 chunks in a cluster 4.8 us, by a kernel 6.5); else the last CTA of up to eight merges them, for up to eight
 // rows (clusters that wait for room leave SMs idle: 2 chunks of 32 of up to 2304 merged by the last 21.5, by a kernel
 // 23.1, in clusters 27.3), and otherwise a second kernel.  All add in the same order.
-// The chunks of a cluster, and those of many steps, take every nchunk-th step of the whole sequence: equal shares
-// whatever its length (13 sequences of 3 to 9000 positions: 12.8 us, one behind the other 13.7; 32 of 360 to 4500,
-// two chunks of 18 steps: 33.1 and 36.9).  Short chunks lie one behind the other: a sequence that ends in the first
-// of them then starts only one CTA (32 of 360 to 2245, two chunks of 9 steps: 21.8 us, by turns 22.7).
+// A chunk takes every nchunk-th step of the whole sequence: equal shares whatever its length (13 sequences of 3 to 9000
+// positions, eight chunks: 12.8 us, one behind the other 13.7; 32 of 360 to 4500, two: 33.1 and 36.9; 24 of 360 to
+// 2245, three chunks that last merged: 18.8 and 17.5).
 // The cut goes by the capacity and not by Q or the shared heads, so a row is summed in the same order alone and among
 // others.
 struct Cut {
-  int nchunk, apart, stride, span, mode;
+  int nchunk, steps, mode;  // chunks of a sequence, steps of a chunk, how they meet
 };
 Cut cut_of(int B, int nkv, long long cap) {
-  constexpr int kRound = 32 * kQaWarps, kSlots = 152 * 3, kSmall = 16;
-  const long long pairs = (long long)B * nkv, steps = (cap + kRound - 1) / kRound;
+  constexpr int kSlots = 152 * 3, kSmall = 16;
+  const long long pairs = (long long)B * nkv, steps = (cap + kQaRound - 1) / kQaRound;
   const long long least = (steps + kQaMaxSteps - 1) / kQaMaxSteps;
   auto clustered = [&](long long used) { return used <= kQaCluster8 && pairs * used <= kSlots; };
   // up to sixteen chunks, and numbers around the one at which the sum below is least
@@ -809,10 +837,7 @@ Cut cut_of(int B, int nkv, long long cap) {
            : clustered(c.nchunk) ? kQaCluster
            : c.nchunk <= kQcUnroll && pairs * kQaMaxTiles <= kQaCounters ? kQaLast
                                                                          : kQaParts;
-  const bool spread = c.mode == kQaCluster || at >= kQaSpread;
-  c.apart = spread ? kRound : (int)(at * kRound);
-  c.stride = spread ? c.nchunk * kRound : kRound;
-  c.span = spread ? (int)(steps * kRound) : c.apart;
+  c.steps = (int)at;
   return c;
 }
 
@@ -824,15 +849,15 @@ bool shape_ok(int B, int Q, int M, int page, int nh, int nkv, int d) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <int D, int NT, int U, int K, int S, int kPerSm>
+template <int D, int NT, int U, int K, int S, int kPerSm, int kGroups>
 cudaError_t run(const QaParams& p, const DeviceCtx& dc, cudaStream_t s) {
-  constexpr int kSmem = QaSmem<D, NT, U, K, S>::kTotal;
-  auto kernel = attn_q4_kernel<D, NT, U, K, S, kPerSm>;
+  constexpr int kSmem = QaSmem<D, NT, U, K, S>::kTotal * kGroups;
+  auto kernel = attn_q4_kernel<D, NT, U, K, S, kPerSm, kGroups>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kSmem, dc.device);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.B * p.nkv * p.rblocks, p.nchunk);
-  cfg.blockDim = dim3(kQaThreads);
+  cfg.gridDim = dim3(p.B * p.nkv * p.rblocks, kGroups > 1 ? 1 : p.nchunk);
+  cfg.blockDim = dim3(kQaThreads * kGroups);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -843,9 +868,9 @@ cudaError_t run(const QaParams& p, const DeviceCtx& dc, cudaStream_t s) {
   attr[1].val.clusterDim.y = p.nchunk;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.mode == kQaCluster ? 2 : 1;
+  cfg.numAttrs = kGroups == 1 && p.mode == kQaCluster ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (e != cudaSuccess || p.mode != kQaParts) return e;
+  if (e != cudaSuccess || kGroups > 1 || p.mode != kQaParts) return e;
   const int slices = (p.R * (D / 4) + kQcThreads - 1) / kQcThreads;
   return launch_pdl(attn_q4_combine_kernel<D>, dim3(p.B * p.nkv, slices), dim3(kQcThreads), 0, s, p);
 }
@@ -898,9 +923,6 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   while ((1 << p.page_shift) < page) ++p.page_shift;
   const Cut cut = cut_of(B, nkv, (long long)M * page);
   p.nchunk = cut.nchunk;
-  p.apart = cut.apart;
-  p.stride = cut.stride;
-  p.span = cut.span;
   // (merging up to sixteen rows keeps a last CTA for longer than a second kernel takes: 137 us for 133.5)
   p.mode = cut.mode == kQaLast && p.R > 8 ? kQaParts : cut.mode;
   p.scale_log2 = scale * kQaLog2e;
@@ -911,17 +933,31 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kQaCounters * 4 + round256(parts * d * 4));
   p.err = dc->err;
   p.wait_ns = wait_limit_ns();
+  // Two or four short chunks of up to eight rows are the groups of one CTA and meet in its shared memory, where neither
+  // a state nor a count goes through L2: 32 sequences of up to 2304 positions, two chunks of 9 steps, 19.7 us (merged by
+  // the last CTA 22.7), 32 of up to 1152 12.1 (14.9), 16 of up to 4096, four of 8, 17.9 (19.5).  Long chunks are as fast
+  // on several SMs, and faster where all are long (32 of 4200 to 4500, two of 18 steps: 49.2, as groups 51.3).
+  const bool near = p.R <= 8 && cut.mode >= kQaLast && cut.steps <= kQaNear;
+  const int groups = near && (cut.nchunk == 2 || cut.nchunk == 4) ? cut.nchunk : 1;
   const bool two = p.R > 8;  // the rows of an MMA, or its columns (half the MMAs for up to eight rows)
   p.rblocks = two ? (p.R + 15) / 16 : 1;
   // CTAs that find no room at once wait for others to leave: with the longest first, the short ones fill the end (64
   // sequences of up to 2048 positions, 512 CTAs with room for 456: 37.9 -> 33.4 us; 16 of 32K of any length, 896 CTAs:
   // 91 -> 70.5; 80 of about 2048: 54.9 -> 57.4, what sorting costs).  Where nearly all fit, sorting only brings the
-  // long ones together on the SMs that are free first (32 of up to 4608, 640 CTAs, room for 608: 33.1 -> 36.0).
-  p.sorted = B > 1 && B <= kQaThreads && p.mode != kQaCluster &&
-             10ll * B * nkv * p.rblocks * p.nchunk > 11ll * dc->num_sms * (two ? kQaTwo : kQaOne);
+  // long ones together on the SMs that are free first (32 of up to 4608, 640 CTAs, room for 608: 33.1 -> 36.0), unless
+  // a CTA has half an SM or all of it (32 of up to 2304, 320 CTAs, room for 304: 20.4 -> 19.7).
+  const long long ctas = (long long)B * nkv * p.rblocks * p.nchunk;
+  const long long room = (long long)dc->num_sms * (two ? kQaTwo : kQaOne);
+  p.sorted = B > 1 && B <= kQaThreads && p.mode != kQaCluster && (groups > 1 ? ctas > room : 10 * ctas > 11 * room);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = d == 128 ? (two ? run<128, 2, 2, 2, 2, kQaTwo>(p, *dc, s) : run<128, 1, 2, 1, 3, kQaOne>(p, *dc, s))
-                                 : (two ? run<64, 2, 2, 2, 2, kQaTwo>(p, *dc, s) : run<64, 1, 2, 1, 3, kQaOne>(p, *dc, s));
+  cudaError_t e;
+  if (groups == 2)
+    e = d == 128 ? run<128, 1, 2, 1, 3, kQaOne, 2>(p, *dc, s) : run<64, 1, 2, 1, 3, kQaOne, 2>(p, *dc, s);
+  else if (groups == 4)
+    e = d == 128 ? run<128, 1, 2, 1, 3, kQaOne, 4>(p, *dc, s) : run<64, 1, 2, 1, 3, kQaOne, 4>(p, *dc, s);
+  else
+    e = d == 128 ? (two ? run<128, 2, 2, 2, 2, kQaTwo, 1>(p, *dc, s) : run<128, 1, 2, 1, 3, kQaOne, 1>(p, *dc, s))
+                 : (two ? run<64, 2, 2, 2, 2, kQaTwo, 1>(p, *dc, s) : run<64, 1, 2, 1, 3, kQaOne, 1>(p, *dc, s));
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }
 

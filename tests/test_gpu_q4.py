@@ -201,8 +201,8 @@ def test_attention_long(d, Q, nkv, grp, n):
     check(c, queries(c, Q, grp))
 
 
-# how a sequence's chunks meet goes by the batch, the key heads and the capacity: one chunk; a cluster; the last CTA of
-# several rounds of them; a second kernel
+# how a sequence's chunks meet goes by the batch, the key heads and the capacity: one chunk; a cluster; two or four groups
+# of a CTA or the last CTA of several rounds of them; a second kernel
 @pytest.mark.parametrize("lens,nkv,page,M", [
     ((100, 0, 128), 2, 32, 4),
     ((900, 1024, 1, 0, 517), 2, 64, 16),
@@ -211,6 +211,8 @@ def test_attention_long(d, Q, nkv, grp, n):
     ((3000, 17, 9000, 0, 5000, 1) + (200,) * 20, 2, 128, 80),
     ((20000, 30000), 2, 256, 128),
     (tuple(range(30, 2200, 70)), 10, 64, 36),
+    (tuple(range(0, 1920, 80)), 10, 64, 36),
+    (tuple(range(1, 2100, 131)), 10, 64, 64),
 ])
 @pytest.mark.parametrize("d,Q,grp", [(64, 2, 1), (64, 3, 4), (128, 1, 2), (128, 1, 9)])
 def test_attention_however_the_chunks_meet(lens, nkv, page, M, d, Q, grp):
