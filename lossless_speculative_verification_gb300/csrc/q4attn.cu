@@ -32,6 +32,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -83,7 +84,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // How the chunks' states meet: there is one chunk, the chunks' CTAs are a cluster, the last CTA of a tile of rows to
 // arrive merges them, or a second kernel does.  (Short ones may be groups of one CTA instead.)
 enum : int { kQaDirect = 0, kQaCluster = 1, kQaLast = 2, kQaParts = 3 };
-constexpr int kQaCluster8 = 8;  // chunks of a cluster, at most
+constexpr int kQaWidth = 8, kQaWidthFew = 16;  // chunks of a cluster, at most: where there are many, where few
 
 // A state of four output columns of a row: maximum, sum, unnormalised output.
 struct QaState {
@@ -756,20 +757,30 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
     const uint32_t mine = smem_u32(smem);
     for (int i = split * kQaThreads + threadIdx.x; i < nrows * (D / 4); i += live * kQaThreads) {
       const int r = i / (D / 4), c4 = i - r * (D / 4);
-      float2 ml[kQaCluster8];
-      float4 v[kQaCluster8];
       QaState acc;
+      float2 ml[kQcUnroll];
+      float4 v[kQcUnroll];
+      auto take = [&](int k0) {  // eight states, brought to the common maximum and summed as merge_parts does
+        QaState all = acc;
 #pragma unroll
-      for (int k = 0; k < kQaCluster8; ++k)
-        if (k < live) {
-          const uint32_t at = mapa_shared(mine, k);
-          ml[k] = ld_shared_cluster_f2(at + SM::kMlAll + 8 * r);
-          v[k] = ld_shared_cluster_f4(at + (r * SM::kStride + 4 * c4) * 4);
-          acc.m = fmaxf(acc.m, ml[k].x);
+        for (int k = 0; k < kQcUnroll; ++k)
+          if (k0 + k < live) {
+            const uint32_t at = mapa_shared(mine, k0 + k);
+            ml[k] = ld_shared_cluster_f2(at + SM::kMlAll + 8 * r);
+            v[k] = ld_shared_cluster_f4(at + (r * SM::kStride + 4 * c4) * 4);
+            acc.m = fmaxf(acc.m, ml[k].x);
+          }
+        if (k0 > 0) {
+          acc.l = 0.0f;
+          acc.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          acc.add(make_float2(all.m, all.l), all.o);
         }
 #pragma unroll
-      for (int k = 0; k < kQaCluster8; ++k)
-        if (k < live) acc.add(ml[k], v[k]);
+        for (int k = 0; k < kQcUnroll; ++k)
+          if (k0 + k < live) acc.add(ml[k], v[k]);
+      };
+      take(0);
+      if (live > kQcUnroll) take(kQcUnroll);
       acc.store(p, b, h, r0 + r, D, c4);
     }
   }
@@ -803,7 +814,9 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
 // 32K, 10 key heads: 6 chunks 75.7 us, 10 51.4, 12 44.6, 64 80.3; 64 of up to 8192, 8 key heads and 16 rows: 1 chunk
 // 108, 2 80.6, 4 90.5; 32 of up to 9216, 10 key heads: 2 chunks 61.3, 3 47.2, 6 54.1.)
 // Where all CTAs are on the GPU at once and a sequence has at most eight, its chunks are a cluster (one of 300, 10 key
-// heads: 4 chunks in a cluster 4.8 us, by a kernel 6.5); else the last CTA of up to eight merges them, for up to eight
+// heads: 4 chunks in a cluster 4.8 us, by a kernel 6.5), and so are up to sixteen where two CTAs an SM would do (one
+// of 8100, 10 key heads: 8 chunks 11.7 us, 16 10.3, by a kernel 12.0; at 390 CTAs of clusters of eleven some wait: 13
+// sequences of 3 to 9000 15.5 for 12.7 with eight); else the last CTA of up to eight merges them, for up to eight
 // rows (clusters that wait for room leave SMs idle: 2 chunks of 32 of up to 2304 merged by the last 21.5, by a kernel
 // 23.1, in clusters 27.3), and otherwise a second kernel.  All add in the same order.
 // A chunk takes every nchunk-th step of the whole sequence: equal shares whatever its length (13 sequences of 3 to 9000
@@ -815,10 +828,12 @@ struct Cut {
   int nchunk, steps, mode;  // chunks of a sequence, steps of a chunk, how they meet
 };
 Cut cut_of(int B, int nkv, long long cap) {
-  constexpr int kSlots = 152 * 3, kSmall = 16;
+  constexpr int kSlots = 152 * 3, kFew = 152 * 2, kSmall = 16;
   const long long pairs = (long long)B * nkv, steps = (cap + kQaRound - 1) / kQaRound;
   const long long least = (steps + kQaMaxSteps - 1) / kQaMaxSteps;
-  auto clustered = [&](long long used) { return used <= kQaCluster8 && pairs * used <= kSlots; };
+  auto clustered = [&](long long used) {
+    return used <= kQaWidth ? pairs * used <= kSlots : used <= kQaWidthFew && pairs * used <= kFew;
+  };
   // up to sixteen chunks, and numbers around the one at which the sum below is least
   const long long mid = (long long)sqrt(40.0 * kSlots * steps / (300.0 * pairs + 10.0 * kSlots));
   long long best = 1ll << 62, at = steps;
@@ -827,7 +842,7 @@ Cut cut_of(int B, int nkv, long long cap) {
     k = k < least ? least : k > steps ? steps : k;
     const long long len = (steps + k - 1) / k, used = (steps + len - 1) / len, ctas = pairs * used;
     const long long cost = pairs * 50 * steps + ctas * 300 +
-                           kSlots * ((10 * ctas <= 11 * kSlots ? 50 : 30) * len + (used > kQcUnroll ? 10 * used : 0) +
+                           kSlots * ((10 * ctas <= 11 * kSlots ? 50 : 30) * len + (used > kQcUnroll && !clustered(used) ? 10 * used : 0) +
                                      3 * ((ctas + kSlots - 1) / kSlots) * (len + 3));
     if (cost < best) best = cost, at = len;
   }
@@ -855,6 +870,14 @@ cudaError_t run(const QaParams& p, const DeviceCtx& dc, cudaStream_t s) {
   auto kernel = attn_q4_kernel<D, NT, U, K, S, kPerSm, kGroups>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kSmem, dc.device);
   if (e != cudaSuccess) return e;
+  if (p.mode == kQaCluster && p.nchunk > kQaWidth) {  // to be asked for, once a kernel and device
+    static std::atomic<uint64_t> wide{0};
+    if (!(wide.load() >> dc.device & 1u)) {
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      wide |= 1ull << dc.device;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.B * p.nkv * p.rblocks, kGroups > 1 ? 1 : p.nchunk);
   cfg.blockDim = dim3(kQaThreads * kGroups);
