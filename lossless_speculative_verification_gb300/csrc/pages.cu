@@ -14,7 +14,7 @@
 // two bits a page (free, shared) and the rows to the number of pages they need;
 // the second begins each CTA with the sums of what lies before it.  The page
 // contents follow in a third, which streams a list of (source, destination)
-// pairs through the whole GPU.
+// pairs through the whole GPU.  Small tables are planned by one CTA or cluster.
 #include "internal.h"
 #include "lsv.h"
 #include "ptx.cuh"
@@ -29,7 +29,8 @@ constexpr int kPgChunkWords = kPgChunk / 32;
 constexpr int kPgMaxPages = 1 << 24;
 constexpr int kPgMaxRows = 1 << 16;
 // Forks of few rows, entries and counts are one launch of a cluster instead of two of a grid: 2.9 us for 2.6 on the
-// GPU, 7.9 for 9.6 with the host's calls (32 rows of 36).  (A resize in that form took 16.1 us for 13.4.)
+// GPU, 7.9 for 9.6 with the host's calls (32 rows of 36).  (A resize in that form took 16.1 us; one CTA plans it in 11.0 with
+// its copies.)
 constexpr int kPgCluster = 8;        // CTAs of the cluster
 constexpr int kPgGroups = 4;         // rows that each takes at a time
 constexpr int kPgFewRows = 64;
@@ -355,6 +356,127 @@ __global__ void __launch_bounds__(kPgThreads) resize_assign_kernel(const PgResiz
   resize_assign(Group<1>(&sh), p, blockIdx.x);
 }
 
+// A table of few entries over few pages: one CTA plans the whole turn in shared memory, entry k kPgSmall + t by thread t.
+// (32 rows of 36, 16 copies of 0.96 MB: 11.0 us with the copies, 13.4 with the two launches above; called from the host
+// 12.7 for 14.3.)
+constexpr int kPgSmall = 1024;
+constexpr int kPgSmallDeep = kPgChunk / kPgSmall;
+
+__global__ void __launch_bounds__(kPgSmall) resize_small_kernel(const PgResize p) {
+  __shared__ uint32_t free_s[kPgChunkWords], shared_s[kPgChunkWords];
+  __shared__ int free_before[kPgChunkWords];           // free pages before each word's
+  __shared__ int fresh_s[kPgSmallDeep * kPgSmall / 32];  // new pages of each warp's entries, then those before them
+  __shared__ int list[kPgChunk];                       // the free pages that are given out, in rising order
+  __shared__ int need_s, free_n, copies, gone_n;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, total = p.B * p.M;
+  pdl_wait();
+  pdl_trigger();
+  int ref[kPgSmallDeep], pg[kPgSmallDeep], keep[kPgSmallDeep], cap[kPgSmallDeep], entry[kPgSmallDeep];
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid, row = at / p.M;
+    ref[k] = at < p.P ? __ldcg(p.ref + at) : -1;
+    pg[k] = at < total ? __ldcg(p.table + at) : -1;
+    keep[k] = at < total ? __ldcg(p.keep + row) : 0;
+    cap[k] = at < total ? __ldcg(p.cap + row) : 0;
+    entry[k] = at - row * p.M;
+  }
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid;
+    const uint32_t free = __ballot_sync(0xffffffffu, at < p.P && ref[k] <= 0);
+    const uint32_t shared = __ballot_sync(0xffffffffu, ref[k] > 1);
+    if (lane == 0) {
+      free_s[at >> 5] = free;
+      shared_s[at >> 5] = shared;
+    }
+    if (p.ref_out != p.ref && at < p.P) p.ref_out[at] = ref[k];
+  }
+  if (tid == 0) copies = gone_n = 0;
+  __syncthreads();
+  Entry e[kPgSmallDeep];
+  uint32_t ballot[kPgSmallDeep], stays = 0;  // bit k: the entry's row is out of range and stays as it is
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const bool in = k * kPgSmall + tid < total, held = pg[k] >= 0 && pg[k] < p.P;
+    const bool ok = keep[k] >= 0 && cap[k] >= keep[k] && cap[k] <= (long long)p.M * p.page;
+    e[k] = Entry{held, false, false, false};
+    if (in && ok) {
+      const bool is_free = held && (free_s[pg[k] >> 5] >> (pg[k] & 31) & 1u);
+      if (pg[k] < -1 || pg[k] >= p.P || (!held && entry[k] < (keep[k] + p.page - 1) / p.page) || is_free)
+        set_error(p.err, kErrDeviceIndex);
+      e[k] = entry_of(entry[k], held, held && (shared_s[pg[k] >> 5] >> (pg[k] & 31) & 1u), keep[k], cap[k], p.page);
+    } else {
+      stays |= 1u << k;
+      if (in && entry[k] == 0) set_error(p.err, kErrDeviceIndex);
+    }
+    ballot[k] = __ballot_sync(0xffffffffu, e[k].fresh);
+    if (lane == 0) fresh_s[k * (kPgSmall / 32) + warp] = __popc(ballot[k]);
+  }
+  __syncthreads();
+  if (warp < 2) {  // prefixes of the 128 counts of new pages, and of free ones
+    constexpr int kEach = kPgChunkWords / 32;
+    int v[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      v[i] = warp == 0 ? fresh_s[lane * kEach + i] : __popc(free_s[lane * kEach + i]);
+      sum += v[i];
+    }
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    int before = upto - sum;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      (warp == 0 ? fresh_s : free_before)[lane * kEach + i] = before;
+      before += v[i];
+    }
+    if (lane == 31) (warp == 0 ? need_s : free_n) = upto;
+  }
+  __syncthreads();
+  const int need = need_s;
+  const bool enough = need <= free_n;
+  if (enough && tid < kPgChunkWords) {
+    int rank = free_before[tid];
+    for (uint32_t word = free_s[tid]; word && rank < need; word &= word - 1) list[rank++] = 32 * tid + __ffs(word) - 1;
+  }
+  __syncthreads();
+  int gone = 0;
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid;
+    if (at >= total) continue;
+    int to = pg[k];
+    if (enough && !(stays >> k & 1u)) {
+      to = e[k].held && !e[k].gone ? pg[k] : -1;
+      if (e[k].fresh) {
+        to = list[fresh_s[k * (kPgSmall / 32) + warp] + __popc(ballot[k] & ((1u << lane) - 1u))];
+        atomicAdd(p.ref_out + to, 1);
+        if (e[k].copied) {
+          const int c = atomicAdd(&copies, 1);  // any order: the copies are apart
+          p.w.src[c] = pg[k];
+          p.w.list2[c] = to;
+        }
+      }
+      if (e[k].gone) {
+        atomicSub(p.ref_out + pg[k], 1);
+        ++gone;
+      }
+    }
+    p.table_out[at] = to;
+  }
+  if (gone) atomicAdd(&gone_n, gone);
+  __syncthreads();
+  if (tid == 0) {
+    p.w.count[0] = copies;
+    if (p.stats) p.stats[0] = need, p.stats[1] = free_n, p.stats[2] = copies, p.stats[3] = gone_n;
+    if (!enough) set_error(p.err, kErrPages);
+  }
+}
+
 struct PgCopy {
   uint8_t* pool;  // [layers, P, page_bytes]
   const int *src, *dst, *count;
@@ -650,8 +772,13 @@ lsv_status spec_pages_resize(void* pool, int32_t layers, int64_t page_bytes, con
   c.page_bytes = (size_t)page_bytes;
   c.copied = stats_opt ? stats_opt + 2 : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(resize_count_kernel, dim3(B > p.chunks ? B : p.chunks), dim3(kPgThreads), 0, s, p);
-  if (e == cudaSuccess) e = launch_pdl(resize_assign_kernel, dim3(B > 0 ? B : 1), dim3(kPgThreads), 0, s, p);
+  cudaError_t e;
+  if (B > 0 && (long long)B * M <= kPgChunk && P <= kPgChunk) {
+    e = launch_pdl(resize_small_kernel, dim3(1), dim3(kPgSmall), 0, s, p);
+  } else {
+    e = launch_pdl(resize_count_kernel, dim3(B > p.chunks ? B : p.chunks), dim3(kPgThreads), 0, s, p);
+    if (e == cudaSuccess) e = launch_pdl(resize_assign_kernel, dim3(B > 0 ? B : 1), dim3(kPgThreads), 0, s, p);
+  }
   if (e == cudaSuccess && B > 0) e = launch_pdl(copy_pages_kernel, dim3(dc->num_sms * kPgCopyCtas), dim3(kPgThreads), 0, s, c);
   return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
 }

@@ -41,7 +41,7 @@ SIZES = [(1, 1, 1, 1), (3, 5, 40, 16), (7, 9, 130, 5), (33, 64, 3000, 3), (70, 3
 
 
 @pytest.mark.parametrize("place", [True, False])
-@pytest.mark.parametrize("B,M,P,page", SIZES)
+@pytest.mark.parametrize("B,M,P,page", SIZES + [(64, 64, 4096, 4), (241, 17, 4095, 2), (9, 40, 4097, 8)])
 def test_resize(B, M, P, page, place):
     rs = np.random.default_rng(B * M)
     for turn in range(3):
