@@ -29,8 +29,8 @@ constexpr int kPgChunkWords = kPgChunk / 32;
 constexpr int kPgMaxPages = 1 << 24;
 constexpr int kPgMaxRows = 1 << 16;
 // Forks of few rows, entries and counts are one launch of a cluster instead of two of a grid: 2.9 us for 2.6 on the
-// GPU, 7.9 for 9.6 with the host's calls (32 rows of 36).  (A resize in that form took 16.1 us; one CTA plans it in 11.0 with
-// its copies.)
+// GPU, 7.9 for 9.6 with the host's calls (32 rows of 36).  (A resize in that form took 16.1 us; one CTA plans it in
+// 11.0 with its copies.)
 constexpr int kPgCluster = 8;        // CTAs of the cluster
 constexpr int kPgGroups = 4;         // rows that each takes at a time
 constexpr int kPgFewRows = 64;
@@ -699,6 +699,110 @@ __global__ void __launch_bounds__(kPgThreads) compact_move_kernel(const PgCompac
   }
 }
 
+// A small pool: a cluster, each of whose CTAs plans all of it in shared memory and then does its share.  (300 pages of
+// 8.7 KB: 5.8 us for 8.1 with the two launches above, 14.6 for 16 called from the host.)
+constexpr long long kPgSmallBytes = 4 << 20;
+
+__global__ void __cluster_dims__(kPgCluster) __launch_bounds__(kPgSmall) compact_small_kernel(const PgCompact p) {
+  __shared__ uint32_t bits[kPgChunkWords];
+  __shared__ int before[kPgChunkWords];             // live pages before each word's
+  __shared__ uint16_t from[kPgChunk], free[kPgChunk];  // the pages that move, the numbers that they get
+  __shared__ int16_t to[kPgChunk];                  // new number of a live page, -1
+  __shared__ int refs[kPgChunk];
+  __shared__ int live_s;
+  const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  int ref[kPgSmallDeep], rank[kPgSmallDeep];
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid;
+    ref[k] = at < p.P ? __ldcg(p.ref + at) : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid;
+    const uint32_t live = __ballot_sync(0xffffffffu, ref[k] > 0);
+    if (lane == 0) bits[at >> 5] = live;
+    refs[at] = ref[k];
+  }
+  __syncthreads();
+  if (tid < 32) {
+    constexpr int kEach = kPgChunkWords / 32;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sum += __popc(bits[lane * kEach + i]);
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    int b = upto - sum;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      before[lane * kEach + i] = b;
+      b += __popc(bits[lane * kEach + i]);
+    }
+    if (lane == 31) live_s = upto;
+  }
+  __syncthreads();
+  const int live = live_s;
+  auto rank_of = [&](int at) { return before[at >> 5] + __popc(bits[at >> 5] & ((1u << (at & 31)) - 1u)); };
+  const int under = live < kPgChunk ? rank_of(live) : live;  // live pages below number `live`
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid;
+    rank[k] = rank_of(at);
+    if (ref[k] > 0 && at >= live) from[rank[k] - under] = at;
+    if (ref[k] <= 0 && at < live) free[at - rank[k]] = at;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid;
+    to[at] = ref[k] <= 0 ? -1 : at < live ? at : free[rank[k] - under];
+  }
+  __syncthreads();
+  cluster_sync();  // every CTA has read the counts
+#pragma unroll
+  for (int k = 0; k < kPgSmallDeep; ++k) {
+    const int at = k * kPgSmall + tid;
+    if (at >= p.P || (at >> 5) % kPgCluster != c) continue;
+    p.ref_out[at] = at >= live ? 0 : ref[k] > 0 ? ref[k] : refs[from[at - rank[k]]];
+    if (p.map) p.map[at] = to[at];
+  }
+  for (int i = c * kPgSmall + tid; i < p.B * p.M; i += kPgCluster * kPgSmall) {
+    const int pg = __ldcg(p.table + i), n = pg >= 0 && pg < p.P ? to[pg] : -1;
+    if (pg != -1 && n < 0) set_error(p.err, kErrDeviceIndex);  // no page, or one that is counted free
+    p.table_out[i] = n;
+  }
+  if (c == 0 && tid == 0 && p.stats) {
+    p.stats[0] = live;
+    p.stats[1] = live - under;
+    p.stats[2] = p.stats[3] = 0;
+  }
+  // vectors of every page that moves, in every layer, dealt over the cluster's threads
+  const int vecs = (int)(p.copy.page_bytes / 16), per = vecs * p.copy.layers;
+  const int all = (live - under) * per;
+  for (int i0 = c * kPgSmall + tid; i0 < all; i0 += kPgDeep * kPgCluster * kPgSmall) {
+    uint4 v[kPgDeep];
+    uint4* dst[kPgDeep];
+#pragma unroll
+    for (int u = 0; u < kPgDeep; ++u) {
+      const int i = i0 + u * kPgCluster * kPgSmall;
+      if (i >= all) continue;
+      const int k = i / per, l = (i - k * per) / vecs, at = i - k * per - l * vecs;
+      uint4* pool = reinterpret_cast<uint4*>(p.copy.pool) + (size_t)l * p.P * vecs + at;
+      v[u] = pool[(size_t)from[k] * vecs];
+      dst[u] = pool + (size_t)free[k] * vecs;
+    }
+#pragma unroll
+    for (int u = 0; u < kPgDeep; ++u)
+      if (i0 + u * kPgCluster * kPgSmall < all) *dst[u] = v[u];
+  }
+}
+
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 lsv_status pg_check(int32_t B, int32_t M, int32_t P) {
@@ -854,6 +958,10 @@ lsv_status spec_pages_compact(void* pool, int32_t layers, int64_t page_bytes, co
   p.copy.copied = nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
+  if (P <= kPgChunk && (long long)B * M <= kPgFewInts && (double)layers * P * page_bytes <= (double)kPgSmallBytes) {
+    e = launch_pdl(compact_small_kernel, dim3(kPgCluster), dim3(kPgSmall), 0, s, p);
+    return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+  }
   if (p.chunks > 1) e = launch_pdl(compact_count_kernel, dim3(p.chunks), dim3(kPgThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(compact_list_kernel, dim3(p.chunks), dim3(kPgThreads), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(compact_move_kernel, dim3(dc->num_sms * kPgCopyCtas), dim3(kPgThreads), 0, s, p);

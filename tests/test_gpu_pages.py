@@ -161,7 +161,7 @@ def test_fork_out_of_range_is_reported():
 
 
 @pytest.mark.parametrize("place", [True, False])
-@pytest.mark.parametrize("B,M,P,page", SIZES)
+@pytest.mark.parametrize("B,M,P,page", SIZES + [(8, 40, 250, 16), (8, 40, 300, 16), (64, 64, 4096, 4)])
 def test_compact(B, M, P, page, place):
     rs = np.random.default_rng(B + P)
     table, ref, _ = random_state(rs, B, M, P, page, B // 4)
