@@ -836,14 +836,16 @@ Cut cut_of(int B, int nkv, long long cap) {
   };
   // up to sixteen chunks, and numbers around the one at which the sum below is least
   const long long mid = (long long)sqrt(40.0 * kSlots * steps / (300.0 * pairs + 10.0 * kSlots));
-  long long best = 1ll << 62, at = steps;
+  long long best = 1ll << 62, at = steps, last = 0;
   for (int i = 1; i <= kSmall + 3; ++i) {
     long long k = i <= kSmall ? i : mid * (i - kSmall + 2) / 4;
     k = k < least ? least : k > steps ? steps : k;
+    if (k == last) continue;
+    last = k;
     const long long len = (steps + k - 1) / k, used = (steps + len - 1) / len, ctas = pairs * used;
+    const long long wait = (10 * ctas <= 11 * kSlots ? 50 : 30) * len, merge = used > kQcUnroll && !clustered(used) ? 10 * used : 0;
     const long long cost = pairs * 50 * steps + ctas * 300 +
-                           kSlots * ((10 * ctas <= 11 * kSlots ? 50 : 30) * len + (used > kQcUnroll && !clustered(used) ? 10 * used : 0) +
-                                     3 * ((ctas + kSlots - 1) / kSlots) * (len + 3));
+                           kSlots * (wait + merge + 3 * ((ctas + kSlots - 1) / kSlots) * (len + 3));
     if (cost < best) best = cost, at = len;
   }
   Cut c;
@@ -863,6 +865,12 @@ bool shape_ok(int B, int Q, int M, int page, int nh, int nkv, int d) {
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// The counters, and the states of the chunks of `pairs` key heads where they meet in memory.
+size_t ws_bytes_of(const Cut& cut, size_t pairs, int rows, int d) {
+  const size_t parts = cut.mode >= kQaLast ? pairs * cut.nchunk * rows : 0;
+  return kQaCounters * 4 + round256(parts * d * 4) + round256(parts * 2 * 4);
+}
 
 template <int D, int NT, int U, int K, int S, int kPerSm, int kGroups>
 cudaError_t run(const QaParams& p, const DeviceCtx& dc, cudaStream_t s) {
@@ -910,9 +918,7 @@ extern "C" {
 size_t spec_q4_attention_workspace_size(int32_t B, int32_t Q, int32_t M, int32_t page, int32_t nh, int32_t nkv,
                                         int32_t d) {
   if (!shape_ok(B, Q, M, page, nh, nkv, d)) return 0;
-  const Cut cut = cut_of(B, nkv, (long long)M * page);
-  const size_t parts = cut.mode >= kQaLast ? (size_t)B * nkv * cut.nchunk * (Q * (nh / nkv)) : 0;
-  return kQaCounters * 4 + round256(parts * d * 4) + round256(parts * 2 * 4);
+  return ws_bytes_of(cut_of(B, nkv, (long long)M * page), (size_t)B * nkv, Q * (nh / nkv), d);
 }
 
 lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* table, const int32_t* ctx_len, int32_t B,
@@ -920,12 +926,12 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
                              float scale, void* out, void* ws, size_t ws_bytes, lsv_stream stream) {
   if (B < 0 || Q < 1 || nh < 1 || nkv < 1 || d < 1 || page < 1 || M < 1 || P < 1 || !(scale > 0.f) || !isfinite(scale))
     return LSV_ERR_INVALID_ARG;
-  const size_t need = spec_q4_attention_workspace_size(B, Q, M, page, nh, nkv, d);
-  if (need == 0) return LSV_ERR_UNSUPPORTED;
+  if (!shape_ok(B, Q, M, page, nh, nkv, d)) return LSV_ERR_UNSUPPORTED;
   if (B == 0) return LSV_OK;
   if (!q || !pool || !table || !ctx_len || !out) return LSV_ERR_INVALID_ARG;
   if (!al16(q) || !al16(pool) || !al16(table) || !al16(ctx_len) || !al16(out)) return LSV_ERR_MISALIGNED;
-  if (!ws || ws_bytes < need) return LSV_ERR_WORKSPACE;
+  const Cut cut = cut_of(B, nkv, (long long)M * page);
+  if (!ws || ws_bytes < ws_bytes_of(cut, (size_t)B * nkv, Q * (nh / nkv), d)) return LSV_ERR_WORKSPACE;
   if (!al16(ws)) return LSV_ERR_MISALIGNED;
   DeviceCtx* dc = nullptr;
   if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
@@ -944,7 +950,6 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.P = P;
   p.page_shift = 4;
   while ((1 << p.page_shift) < page) ++p.page_shift;
-  const Cut cut = cut_of(B, nkv, (long long)M * page);
   p.nchunk = cut.nchunk;
   // (merging up to sixteen rows keeps a last CTA for longer than a second kernel takes: 137 us for 133.5)
   p.mode = cut.mode == kQaLast && p.R > 8 ? kQaParts : cut.mode;
