@@ -204,6 +204,52 @@ def test_compact_of_an_entry_without_a_live_page_is_reported():
     assert host(t).tolist() == [[0, -1, -1, -1]] and host(r).tolist() == [1, 1, 0, 0, 0]
 
 
+@pytest.mark.parametrize("place", [True, False])
+def test_the_forms_of_a_call_agree_on_what_is_wrong(place):
+    # small tables and pools take one launch; with pages or rows added that change nothing, the other form
+    rs = np.random.default_rng(5)
+    for turn in range(8):
+        B, M, P, page, more = 20, 30, 500, 8, 4096
+        table, ref, n = random_state(rs, B, M, P, page, B // 3)
+        keep = np.maximum(n - rs.integers(0, 2 * page, B), 0)
+        cap = np.minimum(keep + rs.integers(0, 3 * page, B), M * page)
+        if turn:
+            wrong = rs.random((B, M)) < 0.03
+            table = np.where(wrong, rs.choice([-2, 1 << 20, -1], (B, M)), table).astype(np.int32)
+            ref[rs.random(P) < 0.03] = 0                        # held pages that count as free
+            keep[rs.integers(0, B, 2)] = -1, M * page + 1
+            cap[rs.integers(0, B, 2)] = 0, M * page + 3
+        pool = rs.integers(0, 256, (2, P, 32)).astype(np.uint8)
+
+        def resize(extra):
+            t, r, kw = outputs(table, np.r_[ref, np.ones(extra, np.int32)], place)
+            dp = torch.from_numpy(np.concatenate([pool, np.zeros((2, extra, 32), np.uint8)], 1)).cuda()
+            st = torch.full((4,), -7, dtype=torch.int32, device="cuda")
+            a, b = api.spec_pages_resize(dp, t, r, i32(keep), i32(cap), page, api.spec_pages_workspace(B, M, P + extra),
+                                         stats=st, **kw)
+            return host(a), host(b)[:P], host(st), host(dp)[:, :P], api.get_device_error()
+
+        def compact(extra):
+            t, r, kw = outputs(table, np.r_[ref, np.zeros(extra, np.int32)], place)
+            dp = torch.from_numpy(np.concatenate([pool, np.zeros((2, extra, 32), np.uint8)], 1)).cuda()
+            mp = torch.full((P + extra,), -7, dtype=torch.int32, device="cuda")
+            a, b = api.spec_pages_compact(dp, t, r, api.spec_pages_workspace(B, M, P + extra), map=mp, **kw)
+            return host(a), host(b)[:P], host(mp)[:P], host(dp)[:, :int((ref > 0).sum())], api.get_device_error()
+
+        def fork(extra):
+            t, r, kw = outputs(np.r_[table, np.full((extra, M), -1, np.int32)], ref, place)
+            parent = np.r_[rs_parent, np.full(extra, -1)]
+            a, b = api.spec_pages_fork(t, r, i32(parent), api.spec_pages_workspace(B + extra, M, P), **kw)
+            return host(a)[:B], host(b), api.get_device_error()
+
+        rs_parent = rs.integers(-1, B, B)
+        if turn % 2:
+            rs_parent[3] = -4
+        for call, extra in ((resize, more), (compact, more), (fork, 50)):
+            for x, y in zip(call(0), call(extra)):
+                np.testing.assert_array_equal(x, y)
+
+
 def test_page_moves_beyond_4_gb():
     pb, P = 1 << 20, 5000
     pool = torch.empty((1, P, pb), dtype=torch.uint8, device="cuda")

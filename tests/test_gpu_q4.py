@@ -371,6 +371,31 @@ def test_pages_in_any_place_of_a_pool_beyond_4_gb():
     np.testing.assert_array_equal(got[0], torch.from_numpy(k[0, 250:300]).to(torch.bfloat16).float().numpy())
 
 
+@pytest.mark.parametrize("lens,nkv,M", [(tuple(range(5, 2165, 60)), 10, 36), (tuple(range(0, 1920, 80)), 10, 36),
+                                        ((4000,), 2, 64), ((900, 4000, 30), 80, 72), (tuple(range(70)), 10, 2)])
+@pytest.mark.parametrize("Q,grp", [(2, 1), (2, 5)])
+def test_a_captured_call_follows_the_lengths(lens, nkv, M, Q, grp):
+    c = Cache(lens, nkv, 64, 64, M=M)
+    q = dev(queries(c, Q, grp))
+    ws = api.spec_q4_attention_workspace(c.B, Q, M, 64, nkv * grp, nkv, 64)
+    out = torch.empty_like(q)
+
+    def call():
+        return api.spec_q4_attention(q, c.pool, c.table, c.ctx, nkv, 64, ws, out=out)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for turn in range(3):
+        c.ctx.copy_(i32(np.maximum(c.lens - 37 * turn * (np.arange(c.B) % 3), 0)))
+        graph.replay()
+        got = out.clone()
+        out.fill_(-7.0)
+        assert torch.equal(call(), got) and int(ws[:65536].count_nonzero()) == 0
+
+
 def test_attention_out_of_range_is_reported():
     c = Cache([100, 100, 100], 1, 64, 32)
     q = queries(c, 2, 1)
