@@ -15,11 +15,13 @@
 //   values: P times the position's scale is the f16 operand.  sum(P s) of every
 //   group, from one more MMA with ones, takes the 8 off every 16 steps, and the
 //   rows of the odd places are divided by 16 at the end.
-// To keep P s in the range of f16 whatever the scales are, the running maximum
-// is taken over score + exponent of the largest value scale, and P is 2^8 at it.
-// It follows the true one only where that rises by more than a factor 2^6 (the
-// sums are rescaled in few steps then): P s < 2^15, and what underflows is below
-// 2^-22 of the largest term.
+// To keep P s in the range of f16, P is 2^8 at a base, the running maximum of score + exponent of the value scale.
+// Where the scales of a step (its positions, both groups) are within 2^8 of each other, one base does for the sum
+// of P and for every group: the largest score plus the exponent of the largest scale, at most 2^8 above the largest
+// P s.  Elsewhere the sum's base is the largest score, each group's follows the group's own largest P s, and the
+// exponent of a scale goes into that of P (wide_step).  A base follows only where the maximum rises by more than
+// 2^6 (the sums are rescaled in few steps then): P s < 2^15, and what loses bits is below 2^-14 of the group's
+// largest term, what is lost below 2^-24.
 //
 // A CTA's four warps take the steps (32 positions) of one chunk of one key head
 // in turn, each from a ring of its own; their states (maximum, sum, output) meet
@@ -47,6 +49,9 @@ constexpr int kQaWarps = 4;
 constexpr int kQaThreads = kQaWarps * 32;
 constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
 constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
+// Value scales (bf16 bits) that one exponent does for: from 2^-64 to 2^64, none more than about 2^8 above another.
+constexpr uint32_t kQaScaleLow = (127 - 64) << 7, kQaScaleHigh = (127 + 64) << 7, kQaScaleSpan = 8 << 7;
+constexpr float kQaFar = 60.0f;  // how far (log2) a group's base may stand above the sum's in a state
 constexpr float kQaLog2e = 1.4426950408889634f;
 constexpr uint64_t kQaDrainNs = 2000000000ull;
 constexpr int kQaOne = 4, kQaTwo = 3;  // CTAs an SM: up to eight rows, nine to sixteen
@@ -137,15 +142,28 @@ __device__ __forceinline__ QaState merge_parts(const QaParams& p, int parts, int
   return all;
 }
 
-// Bits of the larger of a position's value scales, a NaN one left out.
-__device__ __forceinline__ uint32_t larger_scale(uint32_t s) {
-  const uint32_t a = s & 0xFFFFu, b = s >> 16, u = max(a, b);
-  if (u < 0x7F80u) return u;
-  const uint32_t v = min(a, b);
-  return v < 0x7F80u ? v : 0u;
+// The range of value scales (bf16 bits); nothing yet.
+struct QaRange {
+  uint32_t low = 0xFFFFu, high = 0u;
+  template <int G>
+  __device__ __forceinline__ void add(uint32_t s) {  // a position's scales
+    const uint32_t a = s & 0xFFFFu, b = G == 2 ? s >> 16 : a;
+    low = min(low, min(a, b));
+    high = max(high, max(a, b));
+  }
+  // One exponent does for them, and so for some or none of them; not for zeros and NaN.
+  __device__ __forceinline__ bool near() const {
+    return high <= kQaScaleHigh && low >= kQaScaleLow && low + kQaScaleSpan >= high;
+  }
+};
+// Exponent of a normal scale.
+__device__ __forceinline__ float exponent_of(uint32_t bits) { return (float)((int)(bits >> 7) - 127); }
+// A scale of any kind as mant * 2^e, mant below 2.
+__device__ __forceinline__ float any_exponent(uint32_t bits) { return (float)(max((int)(bits >> 7), 1) - 127); }
+__device__ __forceinline__ float any_mantissa(uint32_t bits) {
+  if (bits >= 0x7F80u) return __uint_as_float(0x7FC00000u);
+  return bits < 0x80u ? (float)bits * 0.0078125f : __uint_as_float((bits & 0x7Fu) << 16 | 0x3F800000u);
 }
-// Its exponent, at least -64.
-__device__ __forceinline__ float exponent_of(uint32_t bits) { return (float)max((int)(bits >> 7) - 127, -64); }
 
 // The sequence of the given rank by falling length (of equal ones the first comes first), and its length.
 __device__ __forceinline__ int2 by_length(const QaParams& p, int rank) {
@@ -186,7 +204,8 @@ struct QaSmem {
   static constexpr int kFq = kCi + NT * L::G * 64;            // [8 NT] what turns the scaled sums into log2 scores
   static constexpr int kLim = kFq + kRows * 4;                // [8 NT] last position the row sees
   static constexpr int kMlAll = kLim + kRows * 4;             // [8 NT][2] (maximum, sum) of the CTA
-  static constexpr int kTotal = kMlAll + kRows * 8;
+  static constexpr int kMg = kMlAll + kRows * 8;              // [warp][G][8 NT] what the groups' sums are relative to
+  static constexpr int kTotal = kMg + kQaWarps * L::G * kRows * 4;
 };
 
 template <int D, int NT, int U, int K, int S, int kPerSm, int kGroups>
@@ -377,115 +396,182 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
 #pragma unroll
     for (int c = 0; c < 4; ++c) cs[gr][c] = 0.0f;
 
-  // One step: the U blocks of a stage from position pos0 on.  Masked: some row does not see all of it, or a
-  // block is not there.  Element c of the scores' tile (u, e): NT = 1 (e = 0): position g + 8 (c / 2) and row
-  // c % 2; NT = 2: position 8 e + 2t + c % 2 and row c / 2, of this lane's.
-  auto step = [&](auto tag, const uint8_t* blk, int pos0, int gone) {
-    constexpr bool kMasked = decltype(tag)::value;
-    auto row_of = [](int c) { return NT == 1 ? (c & 1) : (c >> 1); };
-    // the scales that the elements c and c + 1 of a tile are of
-    auto scales_of = [](const uint32_t (&w)[2][G == 2 ? 2 : 1], int e, int c, int gr) {
-      if (NT == 1) {
-        const float s = q4_scale(w[c >> 1][0], gr);
-        return make_float2(s, s);
-      }
-      return G == 2 ? make_float2(q4_scale(w[e][0], gr), q4_scale(w[e][G - 1], gr))
-                    : make_float2(q4_scale(w[e][0], 0), q4_scale(w[e][0], 1));
-    };
-    // ---- scores, before the row's factor
-    float x[U][NT][4];
-    {
-      Q4Words<W> kw[U][2];
-      uint32_t ks[U][2][G == 2 ? 2 : 1];  // scales of this lane's positions: G = 2 [position], G = 1 both in one
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint8_t* bk = blk + u * L::kBytes;
-          kw[u][e] = q4_load<W>(bk + (32 * e + lane) * (4 * W));
-          if constexpr (NT == 1) {
-            ks[u][e][0] = q4_load_scales<G>(bk + L::kKs + (g + 8 * e) * 2 * G);
-          } else if constexpr (G == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(bk + L::kKs + (8 * e + 2 * t) * 4);
-            ks[u][e][0] = v.x, ks[u][e][1] = v.y;
-          } else {
-            ks[u][e][0] = *reinterpret_cast<const uint32_t*>(bk + L::kKs + (8 * e + 2 * t) * 2);
-          }
-        }
-#pragma unroll
-      for (int gr = 0; gr < G; ++gr) {
-        const float4 sv = *reinterpret_cast<const float4*>(qs + SM::kCi + (NT == 1 ? gr * 4 + t : gr * 8 + g) * 16);
-        float start[4] = {sv.x, sv.y, sv.z, sv.w};
-        float acc[U][NT][4];
-#pragma unroll
-        for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
-          uint4 qf[NT];
-#pragma unroll
-          for (int i = 0; i < NT; ++i) qf[i] = *reinterpret_cast<const uint4*>(qs + SM::kQf + ((NT * j + i) * 32 + lane) * 16);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if constexpr (NT == 1) {
-              const uint32_t a = kw[u][0].w[j], c = kw[u][1].w[j], a8 = a >> 8, c8 = c >> 8;
-              mma_f16_m16n8k16(acc[u][0], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[0].x,
-                               qf[0].y, j == 2 * gr ? start : acc[u][0]);
-              mma_f16_m16n8k16(acc[u][0], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
-                               qf[0].z, qf[0].w, acc[u][0]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t a = kw[u][e].w[j], a8 = a >> 8;
-                mma_f16_m16n8k16(acc[u][e], qf[0].x, qf[0].y, qf[0].z, qf[0].w, a & 0x000F000Fu, a & 0x00F000F0u,
-                                 j == 2 * gr ? start : acc[u][e]);
-                mma_f16_m16n8k16(acc[u][e], qf[NT - 1].x, qf[NT - 1].y, qf[NT - 1].z, qf[NT - 1].w, a8 & 0x000F000Fu,
-                                 a8 & 0x00F000F0u, acc[u][e]);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int e = 0; e < NT; ++e)
-#pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-              const float2 s = scales_of(ks[u], e, c, gr), a = make_float2(acc[u][e][c], acc[u][e][c + 1]);
-              const float2 v = gr == 0 ? mul2(a, s) : fma2(a, s, make_float2(x[u][e][c], x[u][e][c + 1]));
-              x[u][e][c] = v.x, x[u][e][c + 1] = v.y;
-            }
-      }
+  // One step: the U blocks of a stage from position pos0 on.  Element c of the scores' tile (u, e): NT = 1 (e = 0):
+  // position g + 8 (c / 2) and row c % 2; NT = 2: position 8 e + 2t + c % 2 and row c / 2, of this lane's.
+  auto row_of = [](int c) { return NT == 1 ? (c & 1) : (c >> 1); };
+  auto place_of = [&](int e, int c) { return NT == 1 ? g + 8 * (c >> 1) : 8 * e + 2 * t + (c & 1); };
+  // the scales that the elements c and c + 1 of a tile are of
+  auto scales_of = [](const uint32_t (&w)[2][G == 2 ? 2 : 1], int e, int c, int gr) {
+    if (NT == 1) {
+      const float s = q4_scale(w[c >> 1][0], gr);
+      return make_float2(s, s);
     }
-    // ---- the online softmax
-    uint32_t hidden = 0;  // bit 8 u + 4 e + c: the row does not see the position
-    uint32_t big[2] = {0u, 0u};  // the largest value scale of the step, of what the row sees
-    if (kMasked) {
-      const int lim[2] = {*reinterpret_cast<const int*>(qs + SM::kLim + row_a * 4),
-                          *reinterpret_cast<const int*>(qs + SM::kLim + row_b * 4)};
+    return G == 2 ? make_float2(q4_scale(w[e][0], gr), q4_scale(w[e][G - 1], gr))
+                  : make_float2(q4_scale(w[e][0], 0), q4_scale(w[e][0], 1));
+  };
+  // over the lanes that hold a row's elements
+  auto row_max = [](auto v, auto f) {
+#pragma unroll
+    for (int sh = NT == 1 ? 4 : 1; sh < (NT == 1 ? 32 : 4); sh <<= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, sh));
+    return v;
+  };
+  auto larger = [](auto a, auto b) { return max(a, b); };
+  auto smaller = [](auto a, auto b) { return min(a, b); };
+
+  // ---- scores, before the row's factor
+  auto scores = [&](const uint8_t* blk, float (&x)[U][NT][4]) {
+    Q4Words<W> kw[U][2];
+    uint32_t ks[U][2][G == 2 ? 2 : 1];  // scales of this lane's positions: G = 2 [position], G = 1 both in one
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint8_t* bk = blk + u * L::kBytes;
+        kw[u][e] = q4_load<W>(bk + (32 * e + lane) * (4 * W));
+        if constexpr (NT == 1) {
+          ks[u][e][0] = q4_load_scales<G>(bk + L::kKs + (g + 8 * e) * 2 * G);
+        } else if constexpr (G == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(bk + L::kKs + (8 * e + 2 * t) * 4);
+          ks[u][e][0] = v.x, ks[u][e][1] = v.y;
+        } else {
+          ks[u][e][0] = *reinterpret_cast<const uint32_t*>(bk + L::kKs + (8 * e + 2 * t) * 2);
+        }
+      }
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      const float4 sv = *reinterpret_cast<const float4*>(qs + SM::kCi + (NT == 1 ? gr * 4 + t : gr * 8 + g) * 16);
+      float start[4] = {sv.x, sv.y, sv.z, sv.w};
+      float acc[U][NT][4];
+#pragma unroll
+      for (int j = 2 * gr; j < 2 * gr + 2; ++j) {
+        uint4 qf[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) qf[i] = *reinterpret_cast<const uint4*>(qs + SM::kQf + ((NT * j + i) * 32 + lane) * 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if constexpr (NT == 1) {
+            const uint32_t a = kw[u][0].w[j], c = kw[u][1].w[j], a8 = a >> 8, c8 = c >> 8;
+            mma_f16_m16n8k16(acc[u][0], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, qf[0].x,
+                             qf[0].y, j == 2 * gr ? start : acc[u][0]);
+            mma_f16_m16n8k16(acc[u][0], a8 & 0x000F000Fu, c8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x00F000F0u,
+                             qf[0].z, qf[0].w, acc[u][0]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t a = kw[u][e].w[j], a8 = a >> 8;
+              mma_f16_m16n8k16(acc[u][e], qf[0].x, qf[0].y, qf[0].z, qf[0].w, a & 0x000F000Fu, a & 0x00F000F0u,
+                               j == 2 * gr ? start : acc[u][e]);
+              mma_f16_m16n8k16(acc[u][e], qf[NT - 1].x, qf[NT - 1].y, qf[NT - 1].z, qf[NT - 1].w, a8 & 0x000F000Fu,
+                               a8 & 0x00F000F0u, acc[u][e]);
+            }
+          }
+        }
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < NT; ++e)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int in_blk = NT == 1 ? g + 8 * (c >> 1) : 8 * e + 2 * t + (c & 1);
-            if (pos0 + 16 * u + in_blk > lim[row_of(c)] || (gone >> u & 1))
-              hidden |= 1u << (8 * u + 4 * e + c);
-            else
-              big[row_of(c)] = max(big[row_of(c)],
-                                   larger_scale(q4_load_scales<G>(blk + u * L::kBytes + L::kVs + in_blk * 2 * G)));
+          for (int c = 0; c < 4; c += 2) {
+            const float2 s = scales_of(ks[u], e, c, gr), a = make_float2(acc[u][e][c], acc[u][e][c + 1]);
+            const float2 v = gr == 0 ? mul2(a, s) : fma2(a, s, make_float2(x[u][e][c], x[u][e][c + 1]));
+            x[u][e][c] = v.x, x[u][e][c + 1] = v.y;
           }
+    }
+  };
+
+  // ---- the weighted values: weigh(u, e, gr, scales, w) gives the tile's weights P s of group gr
+  auto values = [&](const uint8_t* blk, auto weigh) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* bk = blk + u * L::kBytes;
+      const Q4Words<W> v0 = q4_load<W>(bk + L::kV + lane * (4 * W)), v1 = q4_load<W>(bk + L::kV + (32 + lane) * (4 * W));
+      uint32_t vs[2][G == 2 ? 2 : 1];  // like ks
 #pragma unroll
-        for (int sh = NT == 1 ? 4 : 1; sh < (NT == 1 ? 32 : 4); sh <<= 1)
-          big[r] = max(big[r], __shfl_xor_sync(0xffffffffu, big[r], sh));
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; u += 2) {
-        // lane l has position l of two blocks
-        const uint32_t s = q4_load_scales<G>(blk + (U == 1 ? 0 : u + (lane >> 4)) * L::kBytes + L::kVs + (lane & 15) * 2 * G);
-        big[0] = max(big[0], larger_scale(s));
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (NT == 1) {
+          vs[e][0] = q4_load_scales<G>(bk + L::kVs + (g + 8 * e) * 2 * G);
+        } else if constexpr (G == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(bk + L::kVs + (8 * e + 2 * t) * 4);
+          vs[e][0] = v.x, vs[e][1] = v.y;
+        } else {
+          vs[e][0] = *reinterpret_cast<const uint32_t*>(bk + L::kVs + (8 * e + 2 * t) * 2);
+        }
       }
-      big[0] = big[1] = __reduce_max_sync(0xffffffffu, big[0]);
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        uint32_t pp[NT][2];  // P s in f16: [e][row pair]
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
+          float w[4];
+          weigh(u, e, gr, vs, w);
+          pp[e][0] = pack_f16(w[0], w[1]);
+          pp[e][1] = pack_f16(w[2], w[3]);
+        }
+        if constexpr (NT == 1) {
+          const uint32_t b0 = movmatrix_trans(pp[0][0]), b1 = movmatrix_trans(pp[0][1]);
+          mma_f16_m16n8k16(cs[gr], 0x3C003C00u, 0u, 0x3C003C00u, 0u, b0, b1, cs[gr]);
+#pragma unroll
+          for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
+            const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+            mma_f16_m16n8k16(o[2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u, b0, b1, o[2 * m]);
+            mma_f16_m16n8k16(o[2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u, b0, b1,
+                             o[2 * m + 1]);
+          }
+        } else {
+          const uint32_t a0 = pp[0][0], a1 = pp[0][1], a2 = pp[NT - 1][0], a3 = pp[NT - 1][1];
+          mma_f16_m16n8k16(cs[gr], a0, a1, a2, a3, 0x3C003C00u, 0x3C003C00u, cs[gr]);
+#pragma unroll
+          for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
+            const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
+            mma_f16_m16n8k16(o[4 * m], a0, a1, a2, a3, a & 0x000F000Fu, c & 0x000F000Fu, o[4 * m]);
+            mma_f16_m16n8k16(o[4 * m + 1], a0, a1, a2, a3, a & 0x00F000F0u, c & 0x00F000F0u, o[4 * m + 1]);
+            mma_f16_m16n8k16(o[4 * m + 2], a0, a1, a2, a3, a8 & 0x000F000Fu, c8 & 0x000F000Fu, o[4 * m + 2]);
+            mma_f16_m16n8k16(o[4 * m + 3], a0, a1, a2, a3, a8 & 0x00F000F0u, c8 & 0x00F000F0u, o[4 * m + 3]);
+          }
+        }
+      }
+    }
+  };
+
+  // The elements' positions that their rows do not see (bit 8 u + 4 e + c), as every lane's row limits say.
+  auto hidden_of = [&](int pos0, int gone) {
+    const int lim[2] = {*reinterpret_cast<const int*>(qs + SM::kLim + row_a * 4),
+                        *reinterpret_cast<const int*>(qs + SM::kLim + row_b * 4)};
+    uint32_t hidden = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < NT; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (pos0 + 16 * u + place_of(e, c) > lim[row_of(c)] || (gone >> u & 1)) hidden |= 1u << (8 * u + 4 * e + c);
+    return hidden;
+  };
+  auto scale_at = [&](const uint8_t* blk, int u, int e, int c) {
+    return q4_load_scales<G>(blk + u * L::kBytes + L::kVs + place_of(e, c) * 2 * G);
+  };
+
+  // Softmax and values of a step whose scales are near each other.  Masked: some row does not see all of it, or a block
+  // is not there.  big: the largest scale of the step.
+  auto step = [&](auto tag, const uint8_t* blk, int pos0, int gone, uint32_t all_big, float (&x)[U][NT][4]) {
+    constexpr bool kMasked = decltype(tag)::value;
+    uint32_t hidden = 0;
+    uint32_t big[2] = {all_big, all_big};  // of what the row sees
+    if (kMasked) {
+      hidden = hidden_of(pos0, gone);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        QaRange seen;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < NT; ++e)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (row_of(c) == r && !(hidden >> (8 * u + 4 * e + c) & 1u)) seen.add<G>(scale_at(blk, u, e, c));
+        big[r] = row_max(seen.high, larger);
+      }
     }
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -496,12 +582,7 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
         for (int c = 0; c < 4; ++c)
           if (!kMasked || !(hidden >> (8 * u + 4 * e + c) & 1u)) top[row_of(c)] = fmaxf(top[row_of(c)], x[u][e][c]);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-      for (int sh = NT == 1 ? 4 : 1; sh < (NT == 1 ? 32 : 4); sh <<= 1)
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], sh));
-      top[r] = fmaf(top[r], fq[r], exponent_of(big[r]));
-    }
+    for (int r = 0; r < 2; ++r) top[r] = fmaf(row_max(top[r], larger), fq[r], exponent_of(big[r]));
     if (__any_sync(0xffffffffu, top[0] > m_run[0] + kQaSlack || top[1] > m_run[1] + kQaSlack)) {
       float corr[2];
 #pragma unroll
@@ -539,63 +620,114 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
           const float2 l = add2(make_float2(la, lb), v);
           la = l.x, lb = l.y;
         }
-    // ---- the weighted values
+    values(blk, [&](int u, int e, int gr, const uint32_t (&vs)[2][G == 2 ? 2 : 1], float (&w)[4]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint8_t* bk = blk + u * L::kBytes;
-      const Q4Words<W> v0 = q4_load<W>(bk + L::kV + lane * (4 * W)), v1 = q4_load<W>(bk + L::kV + (32 + lane) * (4 * W));
-      uint32_t vs[2][G == 2 ? 2 : 1];  // like ks
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (NT == 1) {
-          vs[e][0] = q4_load_scales<G>(bk + L::kVs + (g + 8 * e) * 2 * G);
-        } else if constexpr (G == 2) {
-          const uint2 v = *reinterpret_cast<const uint2*>(bk + L::kVs + (8 * e + 2 * t) * 4);
-          vs[e][0] = v.x, vs[e][1] = v.y;
-        } else {
-          vs[e][0] = *reinterpret_cast<const uint32_t*>(bk + L::kVs + (8 * e + 2 * t) * 2);
-        }
+      for (int c = 0; c < 4; c += 2) {
+        const float2 v = mul2(make_float2(x[u][e][c], x[u][e][c + 1]), scales_of(vs, e, c, gr));
+        w[c] = v.x, w[c + 1] = v.y;
+        if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
+        if (kMasked && (hidden >> (8 * u + 4 * e + c + 1) & 1u)) w[c + 1] = 0.0f;
       }
+    });
+  };
+
+  // The same where they are not, or were not in some step before: the sum of P and the sums of each group have a base
+  // of their own, m_run for the first and in shared memory for the others.  A row whose bases are still equal, and whose
+  // scales of this step are near each other, gets what `step` gives it, so that no row's result depends on another's.
+  float* bases = reinterpret_cast<float*>(smem + SM::kMg) + warp * G * kRows;  // [G][kRows], of use where `wide`
+  bool wide = false;
+  auto wide_step = [&](const uint8_t* blk, int pos0, int gone, const float (&x)[U][NT][4]) {
+    const uint32_t hidden = hidden_of(pos0, gone);
+    QaRange seen[2];
+    float top[2] = {-INFINITY, -INFINITY}, top_g[G][2];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) top_g[gr][0] = top_g[gr][1] = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < NT; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (hidden >> (8 * u + 4 * e + c) & 1u) continue;
+          const int r = row_of(c);
+          const uint32_t s = scale_at(blk, u, e, c);
+          seen[r].add<G>(s);
+          top[r] = fmaxf(top[r], x[u][e][c]);
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            const uint32_t sg = gr ? s >> 16 : s & 0xFFFFu;
+            if (sg != 0u && sg < 0x7F80u) top_g[gr][r] = fmaxf(top_g[gr][r], fmaf(x[u][e][c], fq[r], any_exponent(sg)));
+          }
+        }
+    bool same[2];      // one base for all sums of the row
+    float corr_g[G][2], nbase_g[G][2];
+    bool apart = false;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = r ? row_b : row_a;
+      seen[r].low = row_max(seen[r].low, smaller);
+      seen[r].high = row_max(seen[r].high, larger);
+      top[r] = row_max(top[r], larger);
+      float m_g[G];
+      same[r] = seen[r].near();
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
-        uint32_t pp[NT][2];  // P s in f16: [e][row pair]
+        top_g[gr][r] = row_max(top_g[gr][r], larger);
+        m_g[gr] = wide ? bases[gr * kRows + row] : m_run[r];
+        same[r] = same[r] && m_g[gr] == m_run[r];
+      }
+      top[r] = fmaf(top[r], fq[r], same[r] ? exponent_of(seen[r].high) : 0.0f);
+      const float m = top[r] > m_run[r] + kQaSlack ? top[r] : m_run[r];
+      const float corr = m == -INFINITY ? 1.0f : ex2_ftz(m_run[r] - m);
+      m_run[r] = m;
+      nbase[r] = m == -INFINITY ? 0.0f : kQaLift - m;
 #pragma unroll
-        for (int e = 0; e < NT; ++e) {
-          float w[4];
+      for (int i = 0; i < NT; ++i) l_run[r][i] *= corr;
 #pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            const float2 v = mul2(make_float2(x[u][e][c], x[u][e][c + 1]), scales_of(vs, e, c, gr));
-            w[c] = v.x, w[c + 1] = v.y;
-            if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) w[c] = 0.0f;  // whatever the scale is
-            if (kMasked && (hidden >> (8 * u + 4 * e + c + 1) & 1u)) w[c + 1] = 0.0f;
-          }
-          pp[e][0] = pack_f16(w[0], w[1]);
-          pp[e][1] = pack_f16(w[2], w[3]);
-        }
-        if constexpr (NT == 1) {
-          const uint32_t b0 = movmatrix_trans(pp[0][0]), b1 = movmatrix_trans(pp[0][1]);
-          mma_f16_m16n8k16(cs[gr], 0x3C003C00u, 0u, 0x3C003C00u, 0u, b0, b1, cs[gr]);
-#pragma unroll
-          for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
-            const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
-            mma_f16_m16n8k16(o[2 * m], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u, b0, b1, o[2 * m]);
-            mma_f16_m16n8k16(o[2 * m + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u, b0, b1,
-                             o[2 * m + 1]);
-          }
-        } else {
-          const uint32_t a0 = pp[0][0], a1 = pp[0][1], a2 = pp[NT - 1][0], a3 = pp[NT - 1][1];
-          mma_f16_m16n8k16(cs[gr], a0, a1, a2, a3, 0x3C003C00u, 0x3C003C00u, cs[gr]);
-#pragma unroll
-          for (int m = 2 * gr; m < 2 * gr + 2; ++m) {
-            const uint32_t a = v0.w[m], c = v1.w[m], a8 = a >> 8, c8 = c >> 8;
-            mma_f16_m16n8k16(o[4 * m], a0, a1, a2, a3, a & 0x000F000Fu, c & 0x000F000Fu, o[4 * m]);
-            mma_f16_m16n8k16(o[4 * m + 1], a0, a1, a2, a3, a & 0x00F000F0u, c & 0x00F000F0u, o[4 * m + 1]);
-            mma_f16_m16n8k16(o[4 * m + 2], a0, a1, a2, a3, a8 & 0x000F000Fu, c8 & 0x000F000Fu, o[4 * m + 2]);
-            mma_f16_m16n8k16(o[4 * m + 3], a0, a1, a2, a3, a8 & 0x00F000F0u, c8 & 0x00F000F0u, o[4 * m + 3]);
-          }
-        }
+      for (int gr = 0; gr < G; ++gr) {
+        const float up = same[r] ? top[r] : top_g[gr][r], mg = up > m_g[gr] + kQaSlack ? up : m_g[gr];
+        corr_g[gr][r] = mg == -INFINITY ? 1.0f : ex2_ftz(m_g[gr] - mg);
+        nbase_g[gr][r] = mg == -INFINITY ? 0.0f : kQaLift - mg;
+        bases[gr * kRows + row] = mg;  // (every lane of the row writes the same)
+        apart = apart || mg != m;
       }
     }
+    __syncwarp();
+    wide = __any_sync(0xffffffffu, apart);
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) cs[gr][c] *= corr_g[gr][row_of(c)];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[i][c] *= corr_g[(NT == 1 ? i / 2 : i / 4) >> 1][row_of(c)];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < NT; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (!(hidden >> (8 * u + 4 * e + c) & 1u)) {
+            const int r = row_of(c);
+            l_run[r][NT == 1 ? 0 : c & 1] += ex2_ftz(fmaf(x[u][e][c], fq[r], nbase[r]));
+          }
+    values(blk, [&](int u, int e, int gr, const uint32_t (&vs)[2][G == 2 ? 2 : 1], float (&w)[4]) {
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        const float2 s = scales_of(vs, e, c, gr);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // the scale's exponent goes into that of P: neither alone need be in the range of fp32
+          const int r = row_of(c + i);
+          const float sf = i ? s.y : s.x;
+          const uint32_t bits = __float_as_uint(sf) >> 16;
+          const float at = fmaf(x[u][e][c + i], fq[r], same[r] ? nbase_g[gr][r] : nbase_g[gr][r] + any_exponent(bits));
+          w[c + i] = bits == 0u || (hidden >> (8 * u + 4 * e + c + i) & 1u) ? 0.0f
+                                                                          : ex2_ftz(at) * (same[r] ? sf : any_mantissa(bits));
+        }
+      }
+    });
   };
 
   // Takes the 8 of the nibbles off what is summed so far.  Left to the end, the sums of n + 8 of a long chunk would
@@ -631,10 +763,24 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
       const uint8_t* blk = ring + st * SM::kStage + k * (U * L::kBytes);
       const int pos0 = first + (done * K + k) * stride;
       const int gone = ~(there >> (k * U)) & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
-      if (pos0 + kStep - 1 > n - p.Q || gone)
-        step(std::true_type{}, blk, pos0, gone);
+      const bool masked = pos0 + kStep - 1 > n - p.Q || gone;
+      float x[U][NT][4];
+      QaRange seen;  // by the row that sees most; lane l has position l of two blocks
+#pragma unroll
+      for (int u = 0; u < U; u += 2) {
+        const int ub = U == 1 ? 0 : u + (lane >> 4), at = 16 * ub + (lane & 15);
+        const uint32_t s = q4_load_scales<G>(blk + ub * L::kBytes + L::kVs + (lane & 15) * 2 * G);
+        if (!masked || (pos0 + at < n && !(gone >> ub & 1))) seen.add<G>(s);
+      }
+      seen.high = __reduce_max_sync(0xffffffffu, seen.high);
+      const bool near = __all_sync(0xffffffffu, seen.near()) && !wide;
+      scores(blk, x);
+      if (!near)
+        wide_step(blk, pos0, gone, x);
+      else if (masked)
+        step(std::true_type{}, blk, pos0, gone, seen.high, x);
       else
-        step(std::false_type{}, blk, pos0, 0);
+        step(std::false_type{}, blk, pos0, 0, seen.high, x);
       if ((done * K + k) % kQaCentre == kQaCentre - 1) centre();
     }
     __syncwarp();  // every lane has read the stage
@@ -656,32 +802,45 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int row = r ? row_b : row_a;
-    float l = l_run[r][0];
+    float l = l_run[r][0], m = m_run[r], back[G];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) back[gr] = 1.0f;
+    float back_l = 1.0f;
+    if (wide) {  // one base again: the sum's, or as near below the largest group's as keeps the outputs finite
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) m = fmaxf(m, bases[gr * kRows + row] - kQaFar);
+      if (m != -INFINITY) {
+        back_l = ex2_ftz(m_run[r] - m);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) back[gr] = ex2_ftz(bases[gr * kRows + row] - m);
+      }
+    }
     if constexpr (NT == 1) {
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (g == 0) *reinterpret_cast<float2*>(ml_w + 2 * row) = make_float2(m_run[r], l);
+      if (g == 0) *reinterpret_cast<float2*>(ml_w + 2 * row) = make_float2(m, l * back_l);
     } else {
       l += l_run[r][NT - 1];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (t == 0) *reinterpret_cast<float2*>(ml_w + 2 * row) = make_float2(m_run[r], l);
+      if (t == 0) *reinterpret_cast<float2*>(ml_w + 2 * row) = make_float2(m, l * back_l);
     }
 #pragma unroll
-    for (int m = 0; m < W; ++m) {
-      const float off = -8.0f * cs[m >> 1][NT == 1 ? r : 2 * r];
+    for (int w = 0; w < W; ++w) {
+      const float f = back[w >> 1], off = -8.0f * cs[w >> 1][NT == 1 ? r : 2 * r];
       constexpr float kEven = 16777216.0f, kOdd = 1048576.0f;
       if constexpr (NT == 1) {
-        *reinterpret_cast<float4*>(o_w + row * SM::kStride + 32 * m + 4 * g) =
-            make_float4(fmaf(o[2 * m][r], kEven, off), fmaf(o[2 * m][r + 2], kOdd, off),
-                        fmaf(o[2 * m + 1][r], kEven, off), fmaf(o[2 * m + 1][r + 2], kOdd, off));
+        *reinterpret_cast<float4*>(o_w + row * SM::kStride + 32 * w + 4 * g) =
+            make_float4(fmaf(o[2 * w][r], kEven, off) * f, fmaf(o[2 * w][r + 2], kOdd, off) * f,
+                        fmaf(o[2 * w + 1][r], kEven, off) * f, fmaf(o[2 * w + 1][r + 2], kOdd, off) * f);
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<float4*>(o_w + row * SM::kStride + 32 * m + 8 * t + 4 * c) =
-              make_float4(fmaf(o[4 * m][2 * r + c], kEven, off), fmaf(o[(4 * m + 1) % kTiles][2 * r + c], kOdd, off),
-                          fmaf(o[(4 * m + 2) % kTiles][2 * r + c], kEven, off), fmaf(o[(4 * m + 3) % kTiles][2 * r + c], kOdd, off));
+          *reinterpret_cast<float4*>(o_w + row * SM::kStride + 32 * w + 8 * t + 4 * c) =
+              make_float4(fmaf(o[4 * w][2 * r + c], kEven, off) * f, fmaf(o[(4 * w + 1) % kTiles][2 * r + c], kOdd, off) * f,
+                          fmaf(o[(4 * w + 2) % kTiles][2 * r + c], kEven, off) * f,
+                          fmaf(o[(4 * w + 3) % kTiles][2 * r + c], kOdd, off) * f);
       }
     }
   }
