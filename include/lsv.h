@@ -305,7 +305,8 @@ lsv_status spec_q4_attention(const void *q, const void *pool, const int32_t *tab
  *   (the outputs equal the inputs) and LSV_ERR_PAGES is raised.
  *   A row whose bounds are out of range stays as it is, and raises
  *   LSV_ERR_DEVICE_INDEX; so do an entry outside [-1, P), a kept position without
- *   a page (it gets one), and a held page that counts as free.
+ *   a page (it gets one), and a held page that counts as free.  Of both errors in
+ *   one call LSV_ERR_PAGES is raised.
  *   stats_opt [4] int32 (device): pages taken (or, with LSV_ERR_PAGES, needed),
  *   free pages before the call, pages copied, entries given back or replaced.
  * spec_pages_fork: row b takes the pages of row parent[b] (int32, device; -1: none)

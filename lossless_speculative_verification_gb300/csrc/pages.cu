@@ -43,6 +43,7 @@ constexpr int kPgCopyCtas = 2;
 
 struct PgWs {
   int* need;       // [B] pages a row takes
+  int* wrong;      // [B] whether a row's bounds or entries are out of range
   int* chunk_n;    // [chunks] free pages (resize) or live pages (compact) of a chunk
   uint32_t* bits;  // [2, words] bit maps: free, shared
   int* list;       // [max(B * M, P)] page numbers in order of rank (new pages; or the pages that move)
@@ -67,6 +68,7 @@ PgWs pg_layout(void* base, size_t B, size_t M, size_t P) {
   };
   const size_t chunks = (P + kPgChunk - 1) / kPgChunk, bm = B * M;
   w.need = reinterpret_cast<int*>(take(B));
+  w.wrong = reinterpret_cast<int*>(take(B));
   w.chunk_n = reinterpret_cast<int*>(take(chunks));
   w.bits = reinterpret_cast<uint32_t*>(take(2 * chunks * kPgChunkWords));
   w.list = reinterpret_cast<int*>(take(bm > P ? bm : P));
@@ -208,6 +210,7 @@ __device__ __forceinline__ void resize_count(const Group<1>& g, const PgResize& 
   }
   if (c < p.B) {
     int keep, cap, n = 0;
+    bool wrong = false;
     if (row_bounds(p, c, &keep, &cap)) {
       for (int i0 = 0; i0 < p.M; i0 += kPgThreads * kPgDeep) {
         int pg[kPgDeep], r[kPgDeep];
@@ -223,16 +226,20 @@ __device__ __forceinline__ void resize_count(const Group<1>& g, const PgResize& 
           const int i = i0 + k * kPgThreads + g.tid;
           if (i >= p.M) continue;
           const bool held = pg[k] >= 0 && pg[k] < p.P;
-          if (pg[k] < -1 || pg[k] >= p.P || (!held && i < (keep + p.page - 1) / p.page)) set_error(p.err, kErrDeviceIndex);
-          if (held && r[k] <= 0) set_error(p.err, kErrDeviceIndex);  // held, and counted free
+          wrong = wrong || pg[k] < -1 || pg[k] >= p.P || (!held && i < (keep + p.page - 1) / p.page);
+          wrong = wrong || (held && r[k] <= 0);  // held, and counted free
           n += entry_of(i, held, r[k] > 1, keep, cap, p.page).fresh;
         }
       }
-    } else if (g.tid == 0) {
-      set_error(p.err, kErrDeviceIndex);
+    } else {
+      wrong = true;
     }
     n = g.sum(n);
-    if (g.tid == 0) p.w.need[c] = n;
+    wrong = __syncthreads_or(wrong);
+    if (g.tid == 0) {
+      p.w.need[c] = n;
+      p.w.wrong[c] = wrong;
+    }
   }
 }
 
@@ -240,12 +247,14 @@ __device__ __forceinline__ void resize_count(const Group<1>& g, const PgResize& 
 __device__ __forceinline__ void resize_assign(const Group<1>& g, const PgResize& p, int b) {
   int first, unused;
   const int need = g.sum_upto(p.w.need, p.B, b, &first);
-  const int mine = b < p.B ? __ldcg(p.w.need + b) : 0;
+  const int mine = b < p.B ? __ldcg(p.w.need + b) : 0, wrong = b < p.B ? __ldcg(p.w.wrong + b) : 0;
   const int free = g.sum_upto(p.w.chunk_n, p.chunks, 0, &unused);
   if (b == 0 && g.tid == 0) {
     if (p.stats) p.stats[0] = need, p.stats[1] = free;
     if (need > free) set_error(p.err, kErrPages);
   }
+  // the error word keeps the first code: that nothing changed must not hide behind what is wrong with one row
+  if (wrong && need <= free && g.tid == 0) set_error(p.err, kErrDeviceIndex);
   if (b >= p.B) return;  // no rows at all
   int keep, cap;
   const bool ok = row_bounds(p, b, &keep, &cap) && need <= free;
@@ -396,6 +405,7 @@ __global__ void __launch_bounds__(kPgSmall) resize_small_kernel(const PgResize p
   __syncthreads();
   Entry e[kPgSmallDeep];
   uint32_t ballot[kPgSmallDeep], stays = 0;  // bit k: the entry's row is out of range and stays as it is
+  bool wrong = false;
 #pragma unroll
   for (int k = 0; k < kPgSmallDeep; ++k) {
     const bool in = k * kPgSmall + tid < total, held = pg[k] >= 0 && pg[k] < p.P;
@@ -404,11 +414,11 @@ __global__ void __launch_bounds__(kPgSmall) resize_small_kernel(const PgResize p
     if (in && ok) {
       const bool is_free = held && (free_s[pg[k] >> 5] >> (pg[k] & 31) & 1u);
       if (pg[k] < -1 || pg[k] >= p.P || (!held && entry[k] < (keep[k] + p.page - 1) / p.page) || is_free)
-        set_error(p.err, kErrDeviceIndex);
+        wrong = true;
       e[k] = entry_of(entry[k], held, held && (shared_s[pg[k] >> 5] >> (pg[k] & 31) & 1u), keep[k], cap[k], p.page);
     } else {
       stays |= 1u << k;
-      if (in && entry[k] == 0) set_error(p.err, kErrDeviceIndex);
+      wrong = wrong || in;
     }
     ballot[k] = __ballot_sync(0xffffffffu, e[k].fresh);
     if (lane == 0) fresh_s[k * (kPgSmall / 32) + warp] = __popc(ballot[k]);
@@ -439,6 +449,7 @@ __global__ void __launch_bounds__(kPgSmall) resize_small_kernel(const PgResize p
   __syncthreads();
   const int need = need_s;
   const bool enough = need <= free_n;
+  if (wrong && enough) set_error(p.err, kErrDeviceIndex);
   if (enough && tid < kPgChunkWords) {
     int rank = free_before[tid];
     for (uint32_t word = free_s[tid]; word && rank < need; word &= word - 1) list[rank++] = 32 * tid + __ffs(word) - 1;

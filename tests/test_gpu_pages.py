@@ -85,6 +85,31 @@ def test_resize_with_too_few_pages_changes_nothing(place):
     assert host(got).tolist() == [[0, 1, 3, -1], [2, 4, -1, -1]] and host(got_ref).tolist() == [1] * 5
 
 
+@pytest.mark.parametrize("place", [True, False])
+@pytest.mark.parametrize("extra", [0, 4096])                    # both forms of the call
+def test_too_few_pages_are_reported_whatever_else_is_wrong(extra, place):
+    good = np.array([[0, 1, -1, -1], [2, -1, -1, -1]], np.int32)
+    P = 5 + extra
+    for table, keep, cap in ((good, [-1, 3], [32, 32]), (good, [0, 9], [32, 32]),
+                             (np.where(good == 1, P, good), [0, 3], [32, 32]),
+                             (np.where(good == 1, 3, good), [16, 3], [32, 32])):   # page 3 is counted free
+        ref = np.r_[1, 1, 1, 0, 0, np.ones(extra)].astype(np.int32)
+        t, r, kw = outputs(table, ref, place)
+        pool = torch.zeros((1, P, 16), dtype=torch.uint8, device="cuda")
+        st = torch.zeros(4, dtype=torch.int32, device="cuda")
+        a, b = api.spec_pages_resize(pool, t, r, i32(keep), i32(cap), 8, api.spec_pages_workspace(2, 4, P), stats=st, **kw)
+        needed, free = host(st).tolist()[:2]
+        assert needed > free == 2 and host(st).tolist()[2:] == [0, 0]
+        assert api.get_device_error() == 8
+        np.testing.assert_array_equal(host(a), table)
+        np.testing.assert_array_equal(host(b), ref)
+        # the same with pages enough: what is wrong is reported
+        small = np.maximum(keep, 0) if keep[0] < 0 else keep
+        a, b = api.spec_pages_resize(pool, i32(table), r, i32(keep), i32(np.maximum(small, 0)), 8,
+                                     api.spec_pages_workspace(2, 4, P))
+        assert api.get_device_error() == 7
+
+
 def test_resize_many_pages_of_many_chunks():
     # every fourth page is free: ranks that reach over chunks of pages and rows that need thousands
     B, M, P, page = 4, 30000, 200000, 16
