@@ -23,7 +23,10 @@ paged 4-bit cache: one pool of pages for every layer, one page table for all of
 them (spec_q4_append, spec_q4_attention).  Then reserve() gives every sequence
 its pages before a pass and takes the rejected drafts' pages back after it,
 fork() lets sequences go on from one prefix, and compact() moves the live pages
-together (spec_pages_resize, spec_pages_fork, spec_pages_compact).
+together (spec_pages_resize, spec_pages_fork, spec_pages_compact).  Where the pool
+has too few free pages for a reserve(), the pages that a pass would write may still be
+other sequences' too, so verify() appends nothing until a reserve() succeeds: it looks
+at that call's counts on the device, also inside one graph with it.
 """
 from __future__ import annotations
 
@@ -73,6 +76,7 @@ class Decoder:
             self.table = torch.full((B, M), -1, dtype=torch.int32, device=device)
             self.ref = torch.zeros(P, dtype=torch.int32, device=device)
             self.pws = api.spec_pages_workspace(B, M, P, device)
+            self.room = torch.zeros(4, dtype=torch.int32, device=device)   # the last reserve()'s counts
         dw = dict(prob.draft)
         dw["emb"], dw["w_vocab"] = prob.emb, prob.w_vocab
         self.draft_w = {n: (self.emb if n == "emb" else self.w_vocab if n == "w_vocab" else _dev(dw[n], device))
@@ -96,8 +100,12 @@ class Decoder:
 
     def reserve(self, keep, cap, stats=None):
         """Pages for the positions 0..cap[b]-1 of every sequence, of which keep[b] are kept (int32 [B]); see
-        spec_pages_resize."""
-        api.spec_pages_resize(self.pool, self.table, self.ref, keep, cap, self.page, self.pws, stats=stats)
+        spec_pages_resize.  With too few free pages nothing changes, LSV_ERR_PAGES is in the error word
+        (api.get_device_error), room[0] (pages needed) is above room[1] (pages free), and verify() takes every
+        sequence for a slot without one until a reserve() succeeds.  stats [4] int32: a copy of room."""
+        api.spec_pages_resize(self.pool, self.table, self.ref, keep, cap, self.page, self.pws, stats=self.room)
+        if stats is not None:
+            stats.copy_(self.room)
 
     def fork(self, parent):
         """Sequence b goes on from sequence parent[b] (-1: none); int32 [B]."""
@@ -120,6 +128,7 @@ class Decoder:
             if self.cache == "q4":
                 b["aws"] = api.spec_q4_attention_workspace(B, Q, self.table.shape[1], self.page, self.nh, self.nh, self.hd,
                                                            dev)
+                b["none"], b["len"] = (torch.zeros(B, dtype=torch.int32, device=dev) for _ in range(2))
             else:
                 b["aws"] = api.spec_verify_attention_workspace(B, Q, self.L, self.nh, self.hd, dev)
             b["lws"] = api.spec_verify_lmhead_workspace(B, Q - 1, self.V, H, dev)
@@ -133,7 +142,8 @@ class Decoder:
         """One verify pass.  tokens [B, Q] int32: input 0 is each sequence's last committed token,
         inputs 1..Q-1 its drafts (drafts [B, Q-1] int32, the same tokens); ctx_after [B] int32: the
         cache lengths once the Q positions are appended (with the 4-bit cache reserve() comes before, and 0
-        stands for a slot without a sequence).  Returns the pass's buffers: argmax [B, Q]
+        stands for a slot without a sequence, as every length does where that call found too few pages: then
+        no page is written, and the outputs are of no use).  Returns the pass's buffers: argmax [B, Q]
         (the greedy token after each input), alen [B], comm [B, Q] (the rule's outputs), x [B*Q, H]
         (the last residual stream, the draft block's next input state)."""
         B, Q = tokens.shape
@@ -141,6 +151,9 @@ class Decoder:
         nh, hd = self.nh, self.hd
         api.gather_rows(self.emb, tokens.reshape(-1), out=b["x"])
         y = b["zero"]
+        if self.cache == "q4":
+            torch.where(self.room[0] <= self.room[1], ctx_after, b["none"], out=b["len"])
+            ctx_after = b["len"]
         for i, t in enumerate(self.layers):
             api.rmsnorm_residual(b["x"], y, h=b["h"])
             for n in ("q", "k", "v"):

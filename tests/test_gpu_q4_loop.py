@@ -143,6 +143,50 @@ def test_a_captured_step_over_pages():
         ctx = ctx + rs.integers(0, 4, B)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_pass_without_room_writes_nothing(captured):
+    """Four sequences share a prefix in a pool with no page left for their copies: the pass behind the failed reserve must
+    not write to what they share; once a sequence has ended the others go on as if nothing had been."""
+    dims = synth.MoeDims(0, 256, 8, 2, 1, 128)
+    prob = synth.decoder_problem(2, dims, V=2048, nh=2, I_draft=256, seed=7, out_scale=0.3, mimic_draft=True)
+    prompt = i32(np.random.default_rng(2).integers(0, prob.V, size=(1, PROMPT)).repeat(B, 0))
+    tk = np.random.default_rng(3).integers(0, prob.V, (B, 3))
+    tokens, drafts = i32(tk), i32(tk[:, 1:])
+    held = -(-PROMPT // PAGE)
+    room, tight = decoder(prob), decoder(prob, pages=held + 2)      # two copies of the last page, where four are wanted
+    for dec in (room, tight):
+        prefill(dec, prompt, [0])
+        dec.fork(i32([0] * B))
+        dec.verify(tokens, i32(np.zeros(B)), drafts)                # the buffers are made before the capture
+    keep, cap = i32(np.full(B, PROMPT)), i32(np.full(B, PROMPT + 3))
+    torch.cuda.synchronize()
+    before = [x.clone() for x in (tight.pool, tight.table, tight.ref)]
+    stats = torch.full((4,), -7, dtype=torch.int32, device="cuda")
+
+    def turn():
+        tight.reserve(keep, cap, stats)
+        return tight.verify(tokens, cap, drafts)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = turn()
+        graph.replay()
+    else:
+        out = turn()
+    assert api.get_device_error() == 8 and stats.tolist() == [4, 2, 0, 0]
+    for x, y in zip((tight.pool, tight.table, tight.ref), before):
+        assert torch.equal(x, y)
+    for n in (2, 3):                                                # those two sequences end
+        keep[n] = cap[n] = 0
+    graph.replay() if captured else turn()
+    assert api.get_device_error() == 0 and stats.tolist()[:2] == [2, 2]
+    room.reserve(keep, cap)
+    ref = room.verify(tokens, cap, drafts)
+    for n in ("argmax", "alen", "comm"):
+        assert torch.equal(out[n][:2], ref[n][:2])
+
+
 def test_filled_caches():
     dims = synth.MoeDims(0, 256, 8, 2, 1, 128)
     prob = synth.decoder_problem(2, dims, V=512, nh=2, I_draft=256, seed=6)
