@@ -178,7 +178,10 @@ class Decoder:
         return b
 
     def launches_per_verify(self, B: int, Q: int) -> int:
-        """Library kernel launches of one verify pass (the MoE layer: 3 up to 256 tokens; the bf16 cache)."""
+        """Library kernel launches of one verify pass over the bf16 caches (the MoE layer: 3 up to 256 tokens).  Over
+        4-bit pages the attention is one launch or two, as the library cuts the sequences, and no count is given."""
+        if self.cache != "bf16":
+            raise ValueError("launches_per_verify counts the pass over bf16 caches")
         T = B * Q
         moe = 3 if T <= 256 else (4 if T * self.prob.dims.k <= 8192 else 6)
         return 1 + len(self.layers) * (1 + 3 + 1 + 2 + 1 + 1 + moe) + 1 + 2

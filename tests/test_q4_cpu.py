@@ -244,3 +244,16 @@ def test_page_calls_refuse(lib):
 
 def test_status_names_the_empty_pool(lib):
     assert lib.lsv_status_string(8) == b"too few free pages"
+
+
+def test_the_launch_count_is_of_the_bf16_cache():
+    from lossless_speculative_verification_gb300 import synth
+    from lossless_speculative_verification_gb300.decoder import Decoder
+
+    dec = Decoder.__new__(Decoder)
+    dec.layers, dec.prob = [None] * 2, synth.decoder_problem(1, synth.MoeDims(0, 256, 8, 2, 1, 128), V=64, nh=2, I_draft=256)
+    dec.cache = "bf16"
+    assert dec.launches_per_verify(4, 2) == 1 + 2 * (1 + 3 + 1 + 2 + 1 + 1 + 3) + 1 + 2
+    dec.cache = "q4"
+    with pytest.raises(ValueError):
+        dec.launches_per_verify(4, 2)
