@@ -480,3 +480,36 @@ def test_wrappers_refuse():
             f()
     with pytest.raises(RuntimeError):
         api.spec_q4_attention(q, c.pool, c.table, c.ctx, 2, 16, ws[:16])
+
+
+# as above: one chunk, a cluster, two and four groups of a CTA, the last CTA of several, a second kernel
+# (On a GB300 a try of a wait lasts as long as the load; with tries that return at once the limit ran out in every call, and
+# these held as well.)
+@pytest.mark.parametrize("lens,nkv,page,M", [
+    ((100, 0, 128), 2, 32, 4),
+    ((3000, 17, 9000, 6000), 1, 128, 80),
+    (tuple(range(30, 2200, 70)), 10, 64, 36),
+    (tuple(range(1, 2100, 131)), 10, 64, 64),
+    (tuple(range(0, 1920, 80)), 10, 64, 36),
+    ((20000, 30000), 2, 256, 128),
+])
+@pytest.mark.parametrize("grp", [1, 9])
+def test_a_wait_that_runs_out_is_reported_and_the_workspace_serves_the_next_call(lens, nkv, page, M, grp):
+    c = Cache(lens, nkv, 128, page, M=M)
+    q = queries(c, 1, grp)
+    ws = api.spec_q4_attention_workspace(c.B, 1, M, page, nkv * grp, nkv, 128)
+    ref = c.attend(q, ws=ws)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    try:
+        api.set_wait_limit_ns(1)
+        for turn in range(3):
+            flush.fill_(turn)                                   # the pages come from memory again
+            got = c.attend(q, ws=ws)
+            err = api.get_device_error()
+            assert err in (0, 6)                                # a wait may end before anyone looks at the time
+            if err == 0:
+                np.testing.assert_array_equal(got, ref)
+            assert int(ws[:65536].count_nonzero()) == 0
+    finally:
+        api.set_wait_limit_ns(2000000000)
+    np.testing.assert_array_equal(c.attend(q, ws=ws), ref)
