@@ -22,6 +22,7 @@
 namespace lsv {
 namespace {
 
+constexpr int kErrPages = LSV_ERR_PAGES;  // a pool had fewer free pages than a call needed
 constexpr int kPgThreads = 256;
 constexpr int kPgWarps = kPgThreads / 32;
 constexpr int kPgChunk = 4096;  // pages a CTA reduces

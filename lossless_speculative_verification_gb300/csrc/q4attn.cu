@@ -41,6 +41,7 @@
 #include "lsv.h"
 #include "ptx.cuh"
 #include "q4.cuh"
+#include "q4ptx.cuh"
 
 namespace lsv {
 namespace {
