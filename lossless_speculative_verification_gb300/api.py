@@ -214,6 +214,12 @@ def _here(dev, *tensors):
     return ptrs
 
 
+def check_lengths(t, n, name):
+    """t is [n] int32 on the current device, contiguous."""
+    _here(torch.cuda.current_device(), (t, torch.int32, name))
+    _need_shape(t, (n,), name)
+
+
 def _stream_of(dev, stream):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 

@@ -103,6 +103,8 @@ class Decoder:
         spec_pages_resize.  With too few free pages nothing changes, LSV_ERR_PAGES is in the error word
         (api.get_device_error), room[0] (pages needed) is above room[1] (pages free), and verify() takes every
         sequence for a slot without one until a reserve() succeeds.  stats [4] int32: a copy of room."""
+        if stats is not None:
+            api.check_lengths(stats, 4, "stats")
         api.spec_pages_resize(self.pool, self.table, self.ref, keep, cap, self.page, self.pws, stats=self.room)
         if stats is not None:
             stats.copy_(self.room)
@@ -152,6 +154,7 @@ class Decoder:
         api.gather_rows(self.emb, tokens.reshape(-1), out=b["x"])
         y = b["zero"]
         if self.cache == "q4":
+            api.check_lengths(ctx_after, B, "ctx_after")
             torch.where(self.room[0] <= self.room[1], ctx_after, b["none"], out=b["len"])
             ctx_after = b["len"]
         for i, t in enumerate(self.layers):

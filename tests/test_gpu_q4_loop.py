@@ -187,6 +187,20 @@ def test_a_pass_without_room_writes_nothing(captured):
         assert torch.equal(out[n][:2], ref[n][:2])
 
 
+def test_the_decoder_refuses_lengths_and_counts_of_another_kind():
+    dims = synth.MoeDims(0, 256, 8, 2, 1, 128)
+    dec = decoder(synth.decoder_problem(1, dims, V=512, nh=2, I_draft=256, seed=6))
+    tokens, drafts = torch.zeros((B, 2), dtype=torch.int32, device="cuda"), torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    n = i32(np.full(B, 2))
+    for bad in (n[:1], n.long(), n[0], n.cpu(), i32(np.zeros((B, 2)))[:, 0]):
+        with pytest.raises(ValueError):
+            dec.verify(tokens, bad, drafts)
+    for bad in (n[:3], n.long(), i32(np.zeros((2, 4))), n.cpu()):
+        with pytest.raises(ValueError):
+            dec.reserve(n, n, bad)
+    assert bool((dec.table == -1).all()) and int(dec.pool.count_nonzero()) == 0
+
+
 def test_filled_caches():
     dims = synth.MoeDims(0, 256, 8, 2, 1, 128)
     prob = synth.decoder_problem(2, dims, V=512, nh=2, I_draft=256, seed=6)
