@@ -253,7 +253,7 @@ lsv_status spec_cache_append(const void *k_new, const void *v_new, void *k_cache
  *     out[b,j,h] = sum_{t <= p} softmax_t(scale * q[b,j,h].k[b,t,h']) v[b,t,h'],
  *     p = ctx_len[b] - Q + j, over the values that the codes stand for
  *   fp32 scores and sums; the weights P s enter the second product as f16, relative
- *   to the largest of their row and group of 64 dims: from 2^-14 of it down they lose
+ *   to the largest of their row and group of 64 dims: from 2^-10 of it down they lose
  *   bits.  A softmax weight below 2^-126 of its row's largest may count as none, and
  *   beside outputs above 2^60 in one group of a row those below 2^-60 in another may
  *   lose bits.  Rows that stand for nothing are zeros, and so are those of a length out of range;

@@ -19,9 +19,9 @@
 // Where the scales of a step (its positions, both groups) are within 2^8 of each other, one base does for the sum
 // of P and for every group: the largest score plus the exponent of the largest scale, at most 2^8 above the largest
 // P s.  Elsewhere the sum's base is the largest score, each group's follows the group's own largest P s, and the
-// exponent of a scale goes into that of P (wide_step).  A base follows only where the maximum rises by more than
-// 2^6 (the sums are rescaled in few steps then): P s < 2^15, and what loses bits is below 2^-14 of the group's
-// largest term, what is lost below 2^-24.
+// exponent of a scale goes into that of P (wide_step), until the bases are within 2^4 of each other at a step of
+// the first kind.  A base follows only where the maximum rises by more than 2^6 (the sums are rescaled in few steps
+// then): P s < 2^15, and what loses bits is below 2^-10 of the group's largest term, what is lost below 2^-20.
 //
 // A CTA's four warps take the steps (32 positions) of one chunk of one key head
 // in turn, each from a ring of its own; their states (maximum, sum, output) meet
@@ -52,6 +52,7 @@ constexpr float kQaLift = 8.0f;   // log2 of P at the running maximum
 constexpr float kQaSlack = 6.0f;  // how far a maximum may rise (log2) before the sums are rescaled
 // Value scales (bf16 bits) that one exponent does for: from 2^-64 to 2^64, none more than about 2^8 above another.
 constexpr uint32_t kQaScaleLow = (127 - 64) << 7, kQaScaleHigh = (127 + 64) << 7, kQaScaleSpan = 8 << 7;
+constexpr float kQaJoin = 4.0f, kQaJoinSum = 64.0f;  // how near (log2) groups' bases, and theirs and the sum's, become one
 constexpr float kQaFar = 60.0f;  // how far (log2) a group's base may stand above the sum's in a state
 constexpr float kQaLog2e = 1.4426950408889634f;
 constexpr uint64_t kQaDrainNs = 2000000000ull;
@@ -159,11 +160,13 @@ struct QaRange {
 };
 // Exponent of a normal scale.
 __device__ __forceinline__ float exponent_of(uint32_t bits) { return (float)((int)(bits >> 7) - 127); }
-// A scale of any kind as mant * 2^e, mant below 2.
-__device__ __forceinline__ float any_exponent(uint32_t bits) { return (float)(max((int)(bits >> 7), 1) - 127); }
-__device__ __forceinline__ float any_mantissa(uint32_t bits) {
-  if (bits >= 0x7F80u) return __uint_as_float(0x7FC00000u);
-  return bits < 0x80u ? (float)bits * 0.0078125f : __uint_as_float((bits & 0x7Fu) << 16 | 0x3F800000u);
+// A scale of any kind as mantissa * 2^exponent, the mantissa below 2 (NaN of NaN).
+__device__ __forceinline__ float any_exponent(uint32_t bits) {  // (2^23 + the exponent's field) - (2^23 + 127)
+  return __uint_as_float(0x4B000000u | max(bits >> 7, 1u)) - 8388735.0f;
+}
+__device__ __forceinline__ float any_mantissa(float s) {
+  const uint32_t bits = __float_as_uint(s), field = bits >> 23;
+  return field == 0u ? s * 0x1p126f : field == 255u ? s : __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
 }
 
 // The sequence of the given rank by falling length (of equal ones the first comes first), and its length.
@@ -633,12 +636,15 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
   };
 
   // The same where they are not, or were not in some step before: the sum of P and the sums of each group have a base
-  // of their own, m_run for the first and in shared memory for the others.  A row whose bases are still equal, and whose
-  // scales of this step are near each other, gets what `step` gives it, so that no row's result depends on another's.
+  // of their own, m_run for the first and in shared memory for the others.  Bases that have come near each other become
+  // one again at a step whose scales are near each other.  All that goes by the row alone: one whose bases are one gets
+  // what `step` gives it at such a step, whatever the rows beside it need.
   float* bases = reinterpret_cast<float*>(smem + SM::kMg) + warp * G * kRows;  // [G][kRows], of use where `wide`
   bool wide = false;
-  auto wide_step = [&](const uint8_t* blk, int pos0, int gone, const float (&x)[U][NT][4]) {
-    const uint32_t hidden = hidden_of(pos0, gone);
+  auto wide_step = [&](auto tag, const uint8_t* blk, int pos0, int gone, bool all_near, uint32_t all_big,
+                       const float (&x)[U][NT][4]) {
+    constexpr bool kMasked = decltype(tag)::value;
+    const uint32_t hidden = kMasked ? hidden_of(pos0, gone) : 0u;
     QaRange seen[2];
     float top[2] = {-INFINITY, -INFINITY}, top_g[G][2];
 #pragma unroll
@@ -648,45 +654,58 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
 #pragma unroll
       for (int e = 0; e < NT; ++e)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (hidden >> (8 * u + 4 * e + c) & 1u) continue;
-          const int r = row_of(c);
-          const uint32_t s = scale_at(blk, u, e, c);
-          seen[r].add<G>(s);
-          top[r] = fmaxf(top[r], x[u][e][c]);
+        for (int j = 0; j < 2; ++j) {  // this lane's positions, each of both rows
+          const uint32_t s = scale_at(blk, u, e, NT == 1 ? 2 * j : j);
+          float ex[G];  // nothing is relative to zeros and NaN
 #pragma unroll
           for (int gr = 0; gr < G; ++gr) {
             const uint32_t sg = gr ? s >> 16 : s & 0xFFFFu;
-            if (sg != 0u && sg < 0x7F80u) top_g[gr][r] = fmaxf(top_g[gr][r], fmaf(x[u][e][c], fq[r], any_exponent(sg)));
+            ex[gr] = sg == 0u || sg >= 0x7F80u ? -INFINITY : any_exponent(sg);
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int c = NT == 1 ? 2 * j + r : 2 * r + j;
+            if (kMasked && (hidden >> (8 * u + 4 * e + c) & 1u)) continue;
+            if (kMasked) seen[r].add<G>(s);
+            top[r] = fmaxf(top[r], x[u][e][c]);
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) top_g[gr][r] = fmaxf(top_g[gr][r], fmaf(x[u][e][c], fq[r], ex[gr]));
           }
         }
-    bool same[2];      // one base for all sums of the row
+    bool one[2];  // one base for all sums of the row
     float corr_g[G][2], nbase_g[G][2];
     bool apart = false;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = r ? row_b : row_a;
-      seen[r].low = row_max(seen[r].low, smaller);
-      seen[r].high = row_max(seen[r].high, larger);
+      if (kMasked) {
+        seen[r].low = row_max(seen[r].low, smaller);
+        seen[r].high = row_max(seen[r].high, larger);
+      }
+      const bool near = kMasked ? seen[r].near() : all_near, nothing = kMasked && seen[r].low == 0xFFFFu;
       top[r] = row_max(top[r], larger);
-      float m_g[G];
-      same[r] = seen[r].near();
+      const float near_top = fmaf(top[r], fq[r], exponent_of(kMasked ? seen[r].high : all_big));
+      float m_g[G], most = -INFINITY, least = INFINITY;
+      one[r] = near;
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
         top_g[gr][r] = row_max(top_g[gr][r], larger);
         m_g[gr] = wide ? bases[gr * kRows + row] : m_run[r];
-        same[r] = same[r] && m_g[gr] == m_run[r];
+        one[r] = one[r] && m_g[gr] == m_run[r];
+        most = fmaxf(most, fmaxf(m_g[gr], near_top));
+        least = fminf(least, fmaxf(m_g[gr], near_top));
       }
-      top[r] = fmaf(top[r], fq[r], same[r] ? exponent_of(seen[r].high) : 0.0f);
-      const float m = top[r] > m_run[r] + kQaSlack ? top[r] : m_run[r];
+      const bool join = near && !nothing && !one[r] && most - least <= kQaJoin && fabsf(most - m_run[r]) <= kQaJoinSum;
+      const float up = one[r] ? near_top : top[r] * fq[r], m = join ? most : up > m_run[r] + kQaSlack ? up : m_run[r];
       const float corr = m == -INFINITY ? 1.0f : ex2_ftz(m_run[r] - m);
       m_run[r] = m;
       nbase[r] = m == -INFINITY ? 0.0f : kQaLift - m;
 #pragma unroll
       for (int i = 0; i < NT; ++i) l_run[r][i] *= corr;
+      one[r] = one[r] || join;
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
-        const float up = same[r] ? top[r] : top_g[gr][r], mg = up > m_g[gr] + kQaSlack ? up : m_g[gr];
+        const float mg = one[r] ? m : top_g[gr][r] > m_g[gr] + kQaSlack ? top_g[gr][r] : m_g[gr];
         corr_g[gr][r] = mg == -INFINITY ? 1.0f : ex2_ftz(m_g[gr] - mg);
         nbase_g[gr][r] = mg == -INFINITY ? 0.0f : kQaLift - mg;
         bases[gr * kRows + row] = mg;  // (every lane of the row writes the same)
@@ -708,24 +727,22 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
 #pragma unroll
       for (int e = 0; e < NT; ++e)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (!(hidden >> (8 * u + 4 * e + c) & 1u)) {
-            const int r = row_of(c);
-            l_run[r][NT == 1 ? 0 : c & 1] += ex2_ftz(fmaf(x[u][e][c], fq[r], nbase[r]));
-          }
+        for (int c = 0; c < 4; ++c) {
+          const int r = row_of(c);
+          const float v = ex2_ftz(fmaf(x[u][e][c], fq[r], nbase[r]));
+          if (!kMasked || !(hidden >> (8 * u + 4 * e + c) & 1u)) l_run[r][NT == 1 ? 0 : c & 1] += v;
+        }
     values(blk, [&](int u, int e, int gr, const uint32_t (&vs)[2][G == 2 ? 2 : 1], float (&w)[4]) {
 #pragma unroll
       for (int c = 0; c < 4; c += 2) {
-        const float2 s = scales_of(vs, e, c, gr);
+        const float2 s2 = scales_of(vs, e, c, gr);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           // the scale's exponent goes into that of P: neither alone need be in the range of fp32
           const int r = row_of(c + i);
-          const float sf = i ? s.y : s.x;
-          const uint32_t bits = __float_as_uint(sf) >> 16;
-          const float at = fmaf(x[u][e][c + i], fq[r], same[r] ? nbase_g[gr][r] : nbase_g[gr][r] + any_exponent(bits));
-          w[c + i] = bits == 0u || (hidden >> (8 * u + 4 * e + c + i) & 1u) ? 0.0f
-                                                                          : ex2_ftz(at) * (same[r] ? sf : any_mantissa(bits));
+          const float s = i ? s2.y : s2.x, ex = any_exponent(__float_as_uint(s) >> 16), mant = any_mantissa(s);
+          const float p = ex2_ftz(fmaf(x[u][e][c + i], fq[r], one[r] ? nbase_g[gr][r] : nbase_g[gr][r] + ex));
+          w[c + i] = s == 0.0f || (kMasked && (hidden >> (8 * u + 4 * e + c + i) & 1u)) ? 0.0f : p * (one[r] ? s : mant);
         }
       }
     });
@@ -766,6 +783,7 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
       const int gone = ~(there >> (k * U)) & ((1 << U) - 1);  // blocks behind the end, or of a page out of range
       const bool masked = pos0 + kStep - 1 > n - p.Q || gone;
       float x[U][NT][4];
+      if (NT == 1) scores(blk, x);  // (page-shaped caches 20.6 us with the scales first; for sixteen rows 130.6, scores first 137)
       QaRange seen;  // by the row that sees most; lane l has position l of two blocks
 #pragma unroll
       for (int u = 0; u < U; u += 2) {
@@ -774,11 +792,16 @@ __global__ void __launch_bounds__(kQaThreads * kGroups, kPerSm / kGroups) attn_q
         if (!masked || (pos0 + at < n && !(gone >> ub & 1))) seen.add<G>(s);
       }
       seen.high = __reduce_max_sync(0xffffffffu, seen.high);
-      const bool near = __all_sync(0xffffffffu, seen.near()) && !wide;
-      scores(blk, x);
-      if (!near)
-        wide_step(blk, pos0, gone, x);
-      else if (masked)
+      const bool near = __all_sync(0xffffffffu, seen.near());
+      if (NT != 1) scores(blk, x);
+      if (__builtin_expect(!near || wide, 0)) {
+        // (one form of it where calls are short: what they do not run costs them too, one token 5.05 us, with both 5.2,
+        // with neither 4.9)
+        if (NT == 1 || masked)
+          wide_step(std::true_type{}, blk, pos0, gone, near, seen.high, x);
+        else
+          wide_step(std::false_type{}, blk, pos0, 0, near, seen.high, x);
+      } else if (masked)
         step(std::true_type{}, blk, pos0, gone, seen.high, x);
       else
         step(std::false_type{}, blk, pos0, 0, seen.high, x);

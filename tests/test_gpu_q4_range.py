@@ -169,3 +169,25 @@ def test_what_is_no_number_among_mixed_sizes(d, grp):
             assert np.isnan(got[0, 2:, grp:, 64:]).all()
         else:
             assert np.isfinite(got[0, 2:, grp:, 64:]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("factor", [0.0, 2.0 ** -40, 2.0 ** -12, 2.0 ** 12, 2.0 ** 40])
+def test_a_few_positions_of_another_size(d, factor):
+    """Steps of one size behind steps of several: the sums have one base again."""
+    rs = np.random.default_rng(3)
+    lens = np.array([1500, 1400, 700])
+    for both in (True, False):
+        v = rs.normal(size=(3, 1500, 2, d))
+        at = [0, 1, 33, 64, 100, 129, 640, 1390]
+        if both:
+            v[:, at] *= factor
+        else:
+            v[:, at, :, :64] *= factor
+        c = Cache(lens, 2, d, 64, v=v)
+        q = queries(c, 4, 4, std=3.0)
+        all_rows = check(c, q, what="both %s" % both)
+        for j in (0, 3):
+            c.ctx = i32(lens - 3 + j)
+            np.testing.assert_array_equal(c.attend(q[:, j:j + 1])[:, 0], all_rows[:, j])
+            np.testing.assert_array_equal(c.attend(q[:, j:j + 1, [1, 6]])[:, 0], all_rows[:, j][:, [1, 6]])
