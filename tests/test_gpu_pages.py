@@ -303,6 +303,63 @@ def test_no_rows():
     assert host(out).tolist() == [2] + [0] * 9
 
 
+def test_as_many_rows_as_there_may_be():
+    B, M, P, page = 65536, 2, 150000, 8
+    rs = np.random.default_rng(11)
+    table, ref, n = random_state(rs, B, M, P, page, 1000)
+    keep = np.maximum(n - rs.integers(0, 4, B), 0)
+    cap = np.minimum(keep + rs.integers(0, 4, B), M * page)
+    pool = rs.integers(0, 256, (1, P, 16)).astype(np.uint8)
+    ws = api.spec_pages_workspace(B, M, P)
+    t, r, dp = i32(table), i32(ref), torch.from_numpy(pool).cuda()
+    st = torch.zeros(4, dtype=torch.int32, device="cuda")
+    api.spec_pages_resize(dp, t, r, i32(keep), i32(cap), page, ws, stats=st)
+    table, ref, stats, ok = q4.resize(table, ref, keep, cap, page, pool)
+    assert ok and host(st).tolist() == stats
+    parent = rs.integers(-1, B, B)
+    parent[:2000] = 7
+    steps = [lambda: None, lambda: api.spec_pages_fork(t, r, i32(parent), ws), lambda: api.spec_pages_compact(dp, t, r, ws)]
+    for i, step in enumerate(steps):
+        step()
+        if i == 1:
+            table, ref = q4.fork(table, ref, parent)
+        if i == 2:
+            table, ref, _, stats = q4.compact(table, ref, pool)
+            pool = pool[:, :stats[0]]
+        np.testing.assert_array_equal(host(t), table)
+        np.testing.assert_array_equal(host(r), ref)
+        np.testing.assert_array_equal(host(dp)[:, :pool.shape[1]], pool)
+
+
+def test_turns_of_two_tables_at_once():
+    rs = np.random.default_rng(12)
+    sides = []
+    for B, M, P, page in ((20, 30, 900, 8), (90, 200, 9000, 8)):
+        table, ref, n = random_state(rs, B, M, P, page, B // 3)
+        keep, cap = n, np.minimum(n + 9, M * page)
+        pool = rs.integers(0, 256, (2, P, 64)).astype(np.uint8)
+        sides.append([i32(table), i32(ref), torch.from_numpy(pool).cuda(), i32(keep), i32(cap), i32(rs.integers(-1, B, B)),
+                      api.spec_pages_workspace(B, M, P), page, torch.cuda.Stream(), (table, ref, keep, cap, pool)])
+    torch.cuda.synchronize()
+    for turn in range(4):
+        for t, r, dp, kp, cp, pa, ws, page, stream, _ in sides:
+            api.spec_pages_resize(dp, t, r, kp, cp, page, ws, stream=stream)
+            api.spec_pages_fork(t, r, pa, ws, stream=stream)
+            api.spec_pages_compact(dp, t, r, ws, stream=stream)
+    torch.cuda.synchronize()
+    api.get_device_error()                                      # (a forked row may keep more than its parent had)
+    for t, r, dp, kp, cp, pa, ws, page, stream, (table, ref, keep, cap, pool) in sides:
+        alone = [i32(table), i32(ref), torch.from_numpy(pool).cuda()]
+        for turn in range(4):
+            api.spec_pages_resize(alone[2], *alone[:2], kp, cp, page, ws)
+            api.spec_pages_fork(*alone[:2], pa, ws)
+            api.spec_pages_compact(alone[2], *alone[:2], ws)
+        torch.cuda.synchronize()
+        api.get_device_error()
+        live = int((alone[1] > 0).sum())
+        assert torch.equal(t, alone[0]) and torch.equal(r, alone[1]) and torch.equal(dp[:, :live], alone[2][:, :live])
+
+
 def test_captured_turns():
     """A turn's resize and the fork after it in one graph, replayed on its own outputs."""
     rs = np.random.default_rng(3)

@@ -456,6 +456,28 @@ def test_empty_batch_streams_graphs_and_one_workspace_for_all():
         check(c, b, got=out.float().cpu().numpy().astype(np.float64), what=str(lens))
 
 
+def test_two_calls_at_once():
+    shapes = (((900, 1024, 1, 0, 517), 2, 64, 16, 1), (tuple(range(30, 2200, 70)), 10, 64, 36, 1),
+              (tuple(range(0, 1920, 80)), 10, 64, 36, 1), ((20000, 30000), 2, 256, 128, 9))
+    calls = []
+    for lens, nkv, page, M, grp in shapes:
+        c = Cache(lens, nkv, 64, page, M=M)
+        q = dev(queries(c, 1, grp))
+        ws = [api.spec_q4_attention_workspace(c.B, 1, M, page, nkv * grp, nkv, 64) for _ in range(2)]
+        ref = api.spec_q4_attention(q, c.pool, c.table, c.ctx, nkv, page, ws[0])
+        calls.append((c, q, ws, ref, [torch.empty_like(q) for _ in range(2)]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, ws, ref, out in calls:
+            for i, s in enumerate(streams):
+                api.spec_q4_attention(q, c.pool, c.table, c.ctx, c.nkv, c.page, ws[i], out=out[i], stream=s)
+    torch.cuda.synchronize()
+    for c, q, ws, ref, out in calls:
+        assert torch.equal(out[0], ref) and torch.equal(out[1], ref)
+        assert not any(int(w[:65536].count_nonzero()) for w in ws)
+
+
 def test_wrappers_refuse():
     c = Cache([20, 30], 2, 64, 16)
     q, ws = dev(queries(c, 2, 1)), api.spec_q4_attention_workspace(2, 2, c.M, 16, 2, 2, 64)
