@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kPgThreads) compact_move_kernel(const PgCompac
 }
 
 // A small pool: a cluster, each of whose CTAs plans all of it in shared memory and then does its share.  (300 pages of
-// 8.7 KB: 5.8 us for 8.1 with the two launches above, 14.6 for 16 called from the host.)
+// 8.7 KB: 5.8 us for 8.1 with the two launches above; called from one host 14.6 for 16, from others up to 20.)
 constexpr long long kPgSmallBytes = 4 << 20;
 
 __global__ void __cluster_dims__(kPgCluster) __launch_bounds__(kPgSmall) compact_small_kernel(const PgCompact p) {

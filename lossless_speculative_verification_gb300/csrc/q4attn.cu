@@ -25,12 +25,15 @@
 //
 // A CTA's four warps take the steps (32 positions) of one chunk of one key head
 // in turn, each from a ring of its own; their states (maximum, sum, output) meet
-// in shared memory, those of the chunks as cut_of says.  Which positions are a chunk's goes by the capacity alone
-// and both forms add in the same order, so a row's result does not depend on the other rows of the call.
-// A step of 16 rows is 560 instructions, 160 of them dequantising; 16 x 32K
-// positions of 8 key heads take 132 us, 4.1 TB/s of cache, with 48 % of the issue
-// slots, 47 % of the ALU and 47 % of the tensor pipe taken: what bounds it is how
-// far three CTAs an SM (168 registers a thread) overlap them.
+// in shared memory, those of the chunks as cut_of says.  Which positions are a chunk's goes by the batch, the key
+// heads and the capacity, and both forms add in the same order, so in calls of one batch size a row's result does
+// not depend on the other rows.
+// A step of 16 rows is 580 instructions, 160 of them dequantising; 16 x 32K
+// positions of 8 key heads take 131 us, 4.15 TB/s of cache, with 49 % of the issue
+// slots, 48 % of the ALU and 45 % of the tensor pipe taken: what bounds it is how
+// far three CTAs an SM (168 registers a thread) overlap them.  Where every step is
+// a wide one (one group of the values 2^-12 of the other) they take 283 us, where
+// one position in 64 is as much smaller 240, one in 4096 136.
 #include <limits.h>
 #include <math.h>
 
@@ -1005,8 +1008,8 @@ __global__ void __launch_bounds__(kQcThreads) attn_q4_combine_kernel(const QaPar
 // A chunk takes every nchunk-th step of the whole sequence: equal shares whatever its length (13 sequences of 3 to 9000
 // positions, eight chunks: 12.8 us, one behind the other 13.7; 32 of 360 to 4500, two: 33.1 and 36.9; 24 of 360 to
 // 2245, three chunks that last merged: 18.8 and 17.5).
-// The cut goes by the capacity and not by Q or the shared heads, so a row is summed in the same order alone and among
-// others.
+// The cut goes by the batch, the key heads and the capacity and not by Q or the shared heads, so in a batch of one size
+// a row is summed in the same order with few queries and with many.
 struct Cut {
   int nchunk, steps, mode;  // chunks of a sequence, steps of a chunk, how they meet
 };
@@ -1145,18 +1148,18 @@ lsv_status spec_q4_attention(const void* q, const void* pool, const int32_t* tab
   p.err = dc->err;
   p.wait_ns = wait_limit_ns();
   // Two or four short chunks of up to eight rows are the groups of one CTA and meet in its shared memory, where neither
-  // a state nor a count goes through L2: 32 sequences of up to 2304 positions, two chunks of 9 steps, 19.7 us (merged by
-  // the last CTA 22.7), 32 of up to 1152 12.1 (14.9), 16 of up to 4096, four of 8, 17.9 (19.5).  Long chunks are as fast
-  // on several SMs, and faster where all are long (32 of 4200 to 4500, two of 18 steps: 49.2, as groups 51.3).
+  // a state nor a count goes through L2: 32 sequences of up to 2304 positions, two chunks of 9 steps, 20.1 us (merged by
+  // the last CTA 23.0), 32 of up to 1152 12.5 (15.0), 16 of up to 4096, four of 8, 18.7 (19.9).  Long chunks are as fast
+  // on several SMs, and faster where all are long (32 of 4200 to 4500, two of 18 steps: 51.6, as groups 53.9).
   const bool near = p.R <= 8 && cut.mode >= kQaLast && cut.steps <= kQaNear;
   const int groups = near && (cut.nchunk == 2 || cut.nchunk == 4) ? cut.nchunk : 1;
   const bool two = p.R > 8;  // the rows of an MMA, or its columns (half the MMAs for up to eight rows)
   p.rblocks = two ? (p.R + 15) / 16 : 1;
   // CTAs that find no room at once wait for others to leave: with the longest first, the short ones fill the end (64
-  // sequences of up to 2048 positions, 512 CTAs with room for 456: 37.9 -> 33.4 us; 16 of 32K of any length, 896 CTAs:
-  // 91 -> 70.5; 80 of about 2048: 54.9 -> 57.4, what sorting costs).  Where nearly all fit, sorting only brings the
-  // long ones together on the SMs that are free first (32 of up to 4608, 640 CTAs, room for 608: 33.1 -> 36.0), unless
-  // a CTA has half an SM or all of it (32 of up to 2304, 320 CTAs, room for 304: 20.4 -> 19.7).
+  // sequences of up to 2048 positions, 512 CTAs with room for 456: 37.8 -> 33.0 us; 16 of 32K of any length, 896 CTAs:
+  // 92 -> 68.5; 80 of about 2048: 55.5 -> 57.3, what sorting costs).  Where nearly all fit, sorting only brings the
+  // long ones together on the SMs that are free first (32 of up to 4608, 640 CTAs, room for 608: 34.0 -> 36.5), unless
+  // a CTA has half an SM or all of it (32 of up to 2304, 320 CTAs, room for 304: 20.9 -> 20.1).
   const long long ctas = (long long)B * nkv * p.rblocks * p.nchunk;
   const long long room = (long long)dc->num_sms * (two ? kQaTwo : kQaOne);
   p.sorted = B > 1 && B <= kQaThreads && p.mode != kQaCluster && (groups > 1 ? ctas > room : 10 * ctas > 11 * room);
