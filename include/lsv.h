@@ -474,6 +474,58 @@ lsv_status spec_verify_accept_noalloc(const void *logits, const int32_t *drafts,
 lsv_status rmsnorm_residual(void *x, const void *y, void *h, int32_t T, int32_t H, float eps,
                             lsv_stream stream);
 
+/* The 8-bit form of rows and weights, and the products over it.
+ *
+ * 128 consecutive columns of a row, or a block of 128 x 128 of a weight, share a
+ * scale s: the smallest power of two, 2^-126 at least, with max |x| <= 448 s.  A
+ * code is e4m3(x / s), nearest, ties to even (the quotient is exact), and stands for
+ * code * s.  A group that holds a NaN or an infinity has s = NaN and stands for NaN.
+ * The last group of a row, and the last blocks of a weight, may be short.
+ *   codes [R, C] e4m3 bytes; scales [R, ceil(C/128)] fp32 (rows) or
+ *   [ceil(R/128), ceil(C/128)] (weights).  C % 16 == 0, 16 <= C <= 16384, R*C < 2^40.
+ * Device pointers, 16-byte aligned.  One launch each.
+ *
+ * quantize_q8_rows: x [R, C] bf16 as rows.   quantize_q8_weight: w [N, K] bf16.
+ * dequantize_q8: bf16(code * scale) of rows (rows_per_scale 1) or weights (128),
+ *   whatever the scales are.
+ * rmsnorm_residual_q8: rmsnorm_residual with its output in 8 bits,
+ *     x_out[t,:] = bf16(x[t,:] + y[t,:]),
+ *     h[t,:] = x_out[t,:] / sqrt(mean(x_out[t,:]^2) + eps) * gain  (fp32, never stored),
+ *   codes and scales of h as rows.  x_out may be x.  y NULL: no residual (h from x;
+ *   x_out is not written and may be NULL).  gain [H] bf16 or NULL (ones).  A row whose
+ *   squares do not sum to a finite fp32 value is not normalised as it should be.
+ * dense_matmul_q8: y [M, N] = bf16(sum over groups g of x_scales[m, g] *
+ *   w_scales[n / 128, g] * sum_{k in g} x[m, k] w[n, k]), x as rows, w as a weight, N of
+ *   any size.  The products of a group are summed on the tensor cores, the groups in
+ *   fp32 in a fixed order; scales may be any numbers whose products are normal fp32.  Up to 128
+ *   rows of x, a row's result does not depend on the others or on M.  No workspace. */
+lsv_status quantize_q8_rows(const void *x, int32_t R, int32_t C, void *codes, float *scales, lsv_stream stream);
+lsv_status quantize_q8_weight(const void *w, int32_t N, int32_t K, void *codes, float *scales, lsv_stream stream);
+lsv_status dequantize_q8(const void *codes, const float *scales, int32_t R, int32_t C, int32_t rows_per_scale,
+                         void *out, lsv_stream stream);
+lsv_status rmsnorm_residual_q8(const void *x, const void *y, const void *gain, void *x_out, void *codes, float *scales,
+                               int32_t T, int32_t H, float eps, lsv_stream stream);
+lsv_status dense_matmul_q8(const void *x, const float *x_scales, const void *w, const float *w_scales, void *y,
+                           int32_t M, int32_t N, int32_t K, lsv_stream stream);
+
+/* What is read off rows of logits beside their greedy token (spec_verify_accept):
+ *   logits [R, V] bf16, or fp32 where logits_fp32 is not 0
+ *   logprob [R] fp32 (or NULL): log softmax(logits[r])[tokens[r]], tokens [R] int32.
+ *     A token of -1 (what spec_verify_accept commits behind the last one) stands for
+ *     none: 0, so that a row of committed tokens adds up to their log probability.
+ *     Another one outside [0, V) raises LSV_ERR_DEVICE_INDEX and gives NaN.
+ *   entropy [R] fp32 (or NULL): of softmax(logits[r]), in nats
+ *   top_ids [R, n] int32, top_logprobs [R, n] fp32: the n largest logits, largest first,
+ *     equal ones by token, and their log probabilities; behind a vocabulary of fewer
+ *     than n, -1 and -inf.  0 <= n <= 32; for n = 0 both may be NULL.
+ * A logit of -inf is a token of probability 0 (-inf, and 0 in the entropy).  In a row of
+ * nothing else every log probability is -inf and the entropy 0.  A row with a NaN or
+ * +inf gives NaN, and -1 as its tokens.  fp32 arithmetic; deterministic.
+ * V <= 2^30, R >= 0.  Device pointers, 16-byte aligned; rows need no alignment of
+ * their own.  No workspace.  One launch. */
+lsv_status spec_logprobs(const void *logits, int32_t logits_fp32, const int32_t *tokens, int32_t R, int32_t V, int32_t n,
+                         float *logprob, float *entropy, int32_t *top_ids, float *top_logprobs, lsv_stream stream);
+
 /* Synchronise `stream`, return the current device's error word in *code_out
  * (an lsv_status value, 0 if none) and clear it. */
 lsv_status lsv_get_device_error(int32_t *code_out, lsv_stream stream);

@@ -77,6 +77,12 @@ SIGNATURES = {
     "spec_pages_resize": (I32, [P, I32, I64, P, P, P, P, I32, I32, I32, I32, P, P, P, P, SZ, P]),
     "spec_pages_fork": (I32, [P, P, P, I32, I32, I32, P, P, P, SZ, P]),
     "spec_pages_compact": (I32, [P, I32, I64, P, P, I32, I32, I32, P, P, P, P, P, SZ, P]),
+    "quantize_q8_rows": (I32, [P, I32, I32, P, P, P]),
+    "quantize_q8_weight": (I32, [P, I32, I32, P, P, P]),
+    "dequantize_q8": (I32, [P, P, I32, I32, I32, P, P]),
+    "rmsnorm_residual_q8": (I32, [P, P, P, P, P, P, I32, I32, ctypes.c_float, P]),
+    "dense_matmul_q8": (I32, [P, P, P, P, P, I32, I32, I32, P]),
+    "spec_logprobs": (I32, [P, I32, P, I32, I32, I32, P, P, P, P, P]),
     "rmsnorm_residual": (I32, [P, P, P, I32, I32, ctypes.c_float, P]),
     "lsv_get_device_error": (I32, [ctypes.POINTER(I32), P]),
     "lsv_set_wait_limit_ns": (I32, [U64]),

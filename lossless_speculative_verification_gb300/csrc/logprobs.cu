@@ -1,0 +1,456 @@
+// logprobs.cu -- what is read off rows of logits beside their greedy token: the log probability of a given token, the
+// entropy of the distribution, and the most likely tokens with their log probabilities.
+//
+//   m = max_v x_v,  S = sum_v e^(x_v - m),  D = sum_v (x_v - m) e^(x_v - m)
+//   log p_t = x_t - m - log S,   entropy = log S - D / S
+//
+// One pass over the logits with the running maximum, S and D of every thread (rescaled where a maximum rises), bound
+// by their bytes: about five instructions a logit, one of them an exponential.  The n most likely tokens cost nothing
+// in that pass but the place of each thread's maximum: every four threads are a group, the n-th largest of the groups'
+// maxima is a bound that the n largest logits reach, and none but the n groups at or above it have any, so that a
+// second look at those groups' logits (out of L2) collects little more than n candidates, which are ranked by counting.
+// Values and tokens form one 64-bit key (larger value first, then the lower token), so that equal logits, which bf16
+// makes frequent, are no special case.
+//
+// A row is one CTA, or a cluster of up to 16 where there are few rows: its CTAs take a piece each, and rank 0 joins
+// their sums and ranks their candidates, through distributed shared memory, in a fixed order.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "internal.h"
+#include "lsv.h"
+#include "ptx.cuh"
+#include "q4ptx.cuh"
+#include "q8.cuh"
+
+namespace lsv {
+namespace {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpGroups = kLpThreads / 4;
+constexpr int kLpBatch = 4;        // 16-byte vectors a thread takes at once
+constexpr int kLpMaxTop = 32;      // most alternatives
+constexpr int kLpCandidates = 1024;
+constexpr int kLpMaxCluster = 16;
+constexpr int kLpMinPiece = kLpThreads * 16;  // bytes of a CTA's piece of a row: a vector a thread
+static_assert(kLpMaxTop <= kLpGroups && kLpMaxCluster * kLpMaxTop <= kLpCandidates, "candidates");
+
+// Larger value first, then the lower token; never 0.  -0 and 0 are equal.
+__device__ __forceinline__ uint64_t lp_key(float x, int v) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return ((uint64_t)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32) | (uint32_t)~v;
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t u = (uint32_t)(k >> 32);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ int key_token(uint64_t k) { return (int)~(uint32_t)k; }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Sums over a part of a row, relative to its maximum.  A NaN or +infinity makes s NaN, and it stays so.
+struct Part {
+  float m, s, d;
+};
+__device__ __forceinline__ void move_to(Part& a, float m) {
+  if (a.s != 0.0f) {
+    const float by = a.m - m, c = ex2_ftz(by * kLog2e);
+    a.d = c > 0.0f || isnan(c) ? c * fmaf(by, a.s, a.d) : 0.0f;
+    a.s *= c;
+  }
+  a.m = m;
+}
+__device__ __forceinline__ Part join(Part a, Part b) {
+  const float m = max_nan(a.m, b.m);
+  move_to(a, m);
+  move_to(b, m);
+  return Part{m, a.s + b.s, a.d + b.d};
+}
+__device__ __forceinline__ void add_one(Part& a, float x) {
+  if (!(x <= a.m)) move_to(a, x);
+  if (a.m == -INFINITY) return;
+  const float t = max_nan(x - a.m, -1000.0f), e = ex2_ftz(t * kLog2e);
+  a.s += e;
+  a.d = fmaf(t, e, a.d);
+}
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<bf16> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kNone = 0xFF80FF80u;  // -inf, -inf
+  static __device__ __forceinline__ float2 two(const uint4& v, int i) {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpBatch]) {
+    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
+#pragma unroll
+    for (int i = 0; i < kLpBatch; ++i) {
+      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].x));
+      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].y));
+      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].z));
+      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].w));
+    }
+    return max_nan(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ float get(const bf16* p) { return __bfloat162float(*p); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;
+  static __device__ __forceinline__ float2 two(const uint4& v, int i) {
+    return i == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y))
+                  : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpBatch]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kLpBatch; ++i)
+      m = max_nan(max_nan(max_nan(m, __uint_as_float(v[i].x)), max_nan(__uint_as_float(v[i].y), __uint_as_float(v[i].z))),
+                  __uint_as_float(v[i].w));
+    return m;
+  }
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+};
+
+struct LpSmem {
+  uint64_t cand[kLpCandidates];
+  uint64_t group[kLpGroups];
+  uint64_t top[kLpMaxTop];
+  uint64_t all[kLpMaxCluster * kLpMaxTop];  // rank 0's: every rank's largest
+  Part parts[kLpMaxCluster];                // rank 0's: every rank's sums
+  Part warp[kLpWarps];
+  uint64_t best[kLpWarps];
+  int hot[kLpMaxTop];
+  uint64_t bound;
+  int ncand;
+};
+
+// The n largest of `cnt` different keys, in order, to dst (0 where there are fewer): each key's place is the number of
+// larger ones.
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, int cnt, uint64_t* dst, int n) {
+  for (int i = threadIdx.x; i < cnt; i += kLpThreads) {
+    const uint64_t k = keys[i];
+    if (k == 0) continue;
+    int r = 0;
+    for (int j = 0; j < cnt; ++j) r += keys[j] > k;
+    if (r < n) dst[r] = k;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits, const int32_t* tokens, int V, int n,
+                                                                 int cs, float* logprob, float* entropy, int32_t* top_ids,
+                                                                 float* top_logprobs, int* err) {
+  constexpr int N = Vec<T>::N;
+  __shared__ LpSmem sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x / cs, rank = blockIdx.x - row * cs;
+  if (cs > 1) cluster_arrive_relaxed();  // all of the cluster run before anything is sent to rank 0
+  pdl_wait();
+  pdl_trigger();
+  const T* x = logits + (size_t)row * V;
+  // Whole 16-byte vectors of the row lie from element `head` on; rank 0 takes the elements before them, the last
+  // rank those behind them.
+  const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T));
+  const int nv = (V - head) / N, tail = head + nv * N;
+  const T* xv = x + head;
+  const int k0 = (int)((long long)nv * rank / cs), k1 = (int)((long long)nv * (rank + 1) / cs);
+
+  // ------------------------------------------------------------ one pass: sums, and where the maximum is
+  Part a = {-INFINITY, 0.0f, 0.0f};
+  int at = k0 + tid;  // first vector of the batch with the first maximum
+  uint4 v[kLpBatch];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < kLpBatch; ++i) {
+      const int q = k + i * kLpThreads;
+      v[i] = q < k1 ? ld_stream128(xv + (size_t)q * N)
+                    : make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
+    }
+  };
+  float2 s2 = make_float2(0.f, 0.f), d2 = s2;
+  if (k0 + tid < k1) load(k0 + tid);
+  for (int k = k0 + tid; k < k1; k += kLpBatch * kLpThreads) {
+    uint4 u[kLpBatch];
+#pragma unroll
+    for (int i = 0; i < kLpBatch; ++i) u[i] = v[i];
+    if (k + kLpBatch * kLpThreads < k1) load(k + kLpBatch * kLpThreads);
+    const float bm = Vec<T>::max_of(u);
+    if (!(bm <= a.m)) {
+      a.s = s2.x + s2.y;
+      a.d = d2.x + d2.y;
+      move_to(a, bm);
+      s2 = make_float2(a.s, 0.f);
+      d2 = make_float2(a.d, 0.f);
+      at = k;
+    }
+    if (a.m == -INFINITY) continue;  // nothing but -inf so far
+    const float2 neg = make_float2(-a.m, -a.m);
+#pragma unroll
+    for (int i = 0; i < kLpBatch; ++i)
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        float2 t = add2(Vec<T>::two(u[i], j), neg);
+        // -inf counts as e^-1000 = 0, so that it adds 0 and not 0 * inf
+        t.x = max_nan(t.x, -1000.0f);
+        t.y = max_nan(t.y, -1000.0f);
+        const float2 l = mul2(t, make_float2(kLog2e, kLog2e));
+        const float2 e = make_float2(ex2_ftz(l.x), ex2_ftz(l.y));
+        s2 = add2(s2, e);
+        d2 = fma2(t, e, d2);
+      }
+  }
+  a.s = s2.x + s2.y;
+  a.d = d2.x + d2.y;
+  const float vmax = a.m;
+
+  // the elements outside whole vectors
+  int edge = -1;
+  if (rank == 0 && tid < head) edge = tid;
+  if (rank == cs - 1 && tid >= 32 && tid - 32 < V - tail) edge = tail + tid - 32;
+  const float ex = edge >= 0 ? Vec<T>::get(x + edge) : -INFINITY;
+  if (edge >= 0) add_one(a, ex);
+
+  // ------------------------------------------------------------ the CTA's sums
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Part b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.d = __shfl_xor_sync(0xffffffffu, a.d, o);
+    a = join(a, b);
+  }
+  if (lane == 0) sm.warp[warp] = a;
+  if (tid == 0) {
+    sm.ncand = 0;
+    sm.bound = 0;
+  }
+  if (tid < kLpMaxTop) {
+    sm.top[tid] = 0;
+    sm.hot[tid] = -1;
+  }
+
+  // ------------------------------------------------------------ the CTA's largest
+  if (n > 0) {
+    uint64_t key = 0;
+    if (k0 + tid < k1 && !isnan(vmax)) {
+      // the first element of the batch that equals the maximum
+      for (int i = 0; i < kLpBatch && key == 0; ++i) {
+        const int q = at + i * kLpThreads;
+        if (q >= k1) break;
+        const uint4 w = ld_plain128(xv + (size_t)q * N);
+#pragma unroll
+        for (int j = N / 2 - 1; j >= 0; --j) {
+          const float2 f = Vec<T>::two(w, j);
+          if (f.y == vmax) key = lp_key(f.y, head + q * N + 2 * j + 1);
+          if (f.x == vmax) key = lp_key(f.x, head + q * N + 2 * j);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+      key = other > key ? other : key;
+    }
+    if ((tid & 3) == 0) sm.group[tid >> 2] = key;
+    __syncthreads();
+    if (tid < kLpGroups) {
+      const uint64_t k = sm.group[tid];
+      int r = 0;
+      for (int j = 0; j < kLpGroups; ++j) r += sm.group[j] > k || (sm.group[j] == k && j < tid);
+      if (r < n) sm.hot[r] = tid;
+      if (r == n - 1) sm.bound = k;
+    }
+    __syncthreads();
+    const uint64_t bound = sm.bound;
+    const float bv = bound ? key_value(bound) : -INFINITY;
+    auto offer = [&](float f, int token) {
+      if (f < bv) return;
+      const uint64_t k = lp_key(f, token);
+      if (k < bound) return;
+      const int c = atomicAdd(&sm.ncand, 1);
+      if (c < kLpCandidates) sm.cand[c] = k;
+    };
+    if (edge >= 0) offer(ex, edge);
+    const int steps = (k1 - k0 + kLpThreads - 1) / kLpThreads;
+    for (int i = tid; i < n * 4 * steps; i += kLpThreads) {
+      // consecutive threads: the four threads of a group, then the groups, then the vectors
+      const int h = sm.hot[(i >> 2) % n];
+      const int q = k0 + (i >> 2) / n * kLpThreads + 4 * h + (i & 3);
+      if (h < 0 || q >= k1) continue;
+      const uint4 w = ld_plain128(xv + (size_t)q * N);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 f = Vec<T>::two(w, j);
+        offer(f.x, head + q * N + 2 * j);
+        offer(f.y, head + q * N + 2 * j + 1);
+      }
+    }
+    __syncthreads();
+    const int cnt = sm.ncand;
+    if (cnt <= kLpCandidates) {
+      rank_keys(sm.cand, cnt, sm.top, n);
+    } else {
+      // More candidates than there is room for (a few threads' logits all above everyone else's): the largest key
+      // below the last one, n times, over all of the piece.
+      uint64_t last = ~0ull;
+      for (int r = 0; r < n; ++r) {
+        uint64_t k = 0;
+        if (edge >= 0) {
+          const uint64_t e = lp_key(ex, edge);
+          if (e < last) k = e;
+        }
+        for (int q = k0 + tid; q < k1; q += kLpThreads) {
+          const uint4 w = ld_plain128(xv + (size_t)q * N);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float2 f = Vec<T>::two(w, j / 2);
+            const uint64_t e = lp_key(j & 1 ? f.y : f.x, head + q * N + j);
+            if (e < last && e > k) k = e;
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
+          k = other > k ? other : k;
+        }
+        __syncthreads();
+        if (lane == 0) sm.best[warp] = k;
+        __syncthreads();
+        for (int w = 0; w < kLpWarps; ++w) k = sm.best[w] > k ? sm.best[w] : k;
+        if (tid == 0) sm.top[r] = k;
+        if (k == 0) break;
+        last = k;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kLpWarps; ++w) a = join(a, sm.warp[w]);
+    sm.parts[0] = a;
+  }
+
+  // ------------------------------------------------------------ the cluster's
+  if (cs > 1) {
+    cluster_wait();
+    if (rank > 0) {
+      if (tid == 0) {
+        const uint32_t to = mapa_shared(smem_u32(&sm.parts[rank]), 0);
+        st_shared_cluster_f32(to, a.m);
+        st_shared_cluster_f32(to + 4, a.s);
+        st_shared_cluster_f32(to + 8, a.d);
+      }
+    }
+    if (tid < n) {
+      const uint32_t to = mapa_shared(smem_u32(&sm.all[rank * n + tid]), 0);
+      const uint64_t k = sm.top[tid];
+      st_shared_cluster_s32(to, (int)(uint32_t)k);
+      st_shared_cluster_s32(to + 4, (int)(uint32_t)(k >> 32));
+    }
+    cluster_sync();
+    if (rank > 0) return;
+    if (tid < n) sm.top[tid] = 0;
+    if (tid == 0) {
+      for (int r = 1; r < cs; ++r) a = join(a, sm.parts[r]);
+      sm.parts[0] = a;
+    }
+    __syncthreads();
+    rank_keys(sm.all, cs * n, sm.top, n);
+  }
+  __syncthreads();
+
+  // ------------------------------------------------------------ out
+  a = sm.parts[0];
+  const bool bad = isnan(a.s);      // a NaN or +infinity among the logits
+  const bool none = a.s == 0.0f;    // nothing but -inf
+  const float log_s = logf(a.s);
+  if (tid == 0) {
+    if (entropy) entropy[row] = bad ? NAN : none ? 0.0f : log_s - a.d / a.s;
+    if (logprob) {
+      const int t = tokens[row];
+      float p = 0.0f;  // -1: no token
+      if (t < -1 || t >= V) {
+        set_error(err, kErrDeviceIndex);
+        p = NAN;
+      } else if (t >= 0) {
+        p = bad ? NAN : none ? -INFINITY : (Vec<T>::get(x + t) - a.m) - log_s;
+      }
+      logprob[row] = p;
+    }
+  }
+  if (tid < n) {
+    const uint64_t k = sm.top[tid];
+    const bool there = k != 0 && !bad;
+    top_ids[(size_t)row * n + tid] = there ? key_token(k) : -1;
+    top_logprobs[(size_t)row * n + tid] = bad ? NAN : !there || none ? -INFINITY : (key_value(k) - a.m) - log_s;
+  }
+}
+
+template <typename T>
+cudaError_t launch_logprobs(const T* logits, const int32_t* tokens, int R, int V, int n, float* logprob, float* entropy,
+                            int32_t* top_ids, float* top_logprobs, const DeviceCtx& dc, cudaStream_t s) {
+  // As many CTAs a row as are on the GPU at once (four an SM), each with a vector a thread at least.
+  int cs = 1;
+  while (cs < kLpMaxCluster && (long long)R * cs * 2 <= 4ll * dc.num_sms &&
+         (long long)V * (long long)sizeof(T) >= 2ll * cs * kLpMinPiece)
+    cs *= 2;
+  auto* kernel = logprobs_kernel<T>;
+  static std::atomic<bool> wide[64];  // clusters of 16 allowed on the device
+  if (cs > 8 && !wide[dc.device].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    wide[dc.device].store(true);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)R * cs));
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, logits, tokens, V, n, cs, logprob, entropy, top_ids, top_logprobs, dc.err);
+}
+
+}  // namespace
+}  // namespace lsv
+
+using namespace lsv;
+
+extern "C" lsv_status spec_logprobs(const void* logits, int32_t logits_fp32, const int32_t* tokens, int32_t R, int32_t V,
+                                    int32_t n, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs,
+                                    lsv_stream stream) {
+  if (R < 0 || V <= 0 || n < 0) return LSV_ERR_INVALID_ARG;
+  if (n > kLpMaxTop || V > (1 << 30)) return LSV_ERR_UNSUPPORTED;
+  if (R == 0) return LSV_OK;
+  if (!logits || (logprob && !tokens) || (n > 0 && (!top_ids || !top_logprobs))) return LSV_ERR_INVALID_ARG;
+  const void* ptrs[] = {logits, tokens, logprob, entropy, top_ids, top_logprobs};
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) & 15) return LSV_ERR_MISALIGNED;
+  DeviceCtx* dc = nullptr;
+  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = logits_fp32 ? launch_logprobs(static_cast<const float*>(logits), tokens, R, V, n, logprob, entropy,
+                                                      top_ids, top_logprobs, *dc, s)
+                                    : launch_logprobs(static_cast<const bf16*>(logits), tokens, R, V, n, logprob, entropy,
+                                                      top_ids, top_logprobs, *dc, s);
+  return e == cudaSuccess ? LSV_OK : LSV_ERR_CUDA;
+}

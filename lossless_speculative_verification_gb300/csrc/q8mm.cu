@@ -1,0 +1,488 @@
+// q8mm.cu -- dense products of 8-bit rows and 8-bit weights,
+//   y[m, n] = bf16(sum_g sx[m, g] sw[n / 128, g] sum_{k in group g} x[m, k] w[n, k]),
+// groups of 128 columns.
+//
+// The inner sum is the tensor cores' (tcgen05, kind::f8f6f4: four instructions of 32 columns a group, fp32
+// accumulators in TMEM); the outer one, where the scales differ, is an fp32 FMA a group and output in registers.
+// Scales may be any fp32 values: the outer sum costs less than the MMAs that it runs beside (a group of a 128 x 256
+// tile takes the tensor cores 512 cycles, reading it from TMEM 256, its FMAs, two values an instruction, 128), so
+// nothing is won by asking for scales that the tensor cores could apply themselves.
+//
+// Orientation: 128 rows of x on the MMA's M side, TN weight rows on its N side.  A TMEM lane is then a row of x, a
+// thread's columns lie within one block of 128 weight rows, and the factor of a group is one number a thread.
+// Warp 0 issues TMA (both operands K-major, 128-byte swizzle: a stage is one group), warp 1 the MMAs, each group into
+// the next of 512 / TN accumulators, and warps 2..9 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
+//
+// Forms:
+// - few tiles: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank adds one
+//   slice of the columns up over the ranks, in rank order, through distributed shared memory;
+// - more tiles than SMs: persistent CTAs take them row tiles first, so that a weight tile is read from HBM once;
+// - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
+// All sums are of a fixed order: results are the same from run to run, and up to 128 rows a row's bits do not depend
+// on how many rows there are.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "lsv.h"
+#include "ptx.cuh"
+#include "q4ptx.cuh"
+#include "q8.cuh"
+#include "tmap.h"
+
+namespace lsv {
+namespace {
+
+constexpr int kMmThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 sums and output
+constexpr int kMmTile = 128;     // rows of x a CTA
+constexpr int kMmMaxStages = 12;
+constexpr int kMmRing = 200 * 1024;
+constexpr int kMmMaxSplit = 8;
+
+struct MmParams {
+  int M, N, K, G;      // G: groups of K
+  int nm, nitems;      // row tiles; tiles of the output
+  int ns;              // CTAs that share a tile's groups (cluster size; 1 for pairs)
+  int stages, a_bytes, stage_bytes;
+  int a_last, b_last;  // bytes of the boxes of the last row tile and the last weight tile
+  int wide;            // bytes of a row's aligned stores: 32, 16 or 2
+  const float* sx;
+  const float* sw;
+  bf16* y;
+  int* err;
+  uint64_t wait_ns;
+};
+
+struct MmMaps {
+  CUtensorMap x, x_last, w, w_last;
+};
+
+__device__ __forceinline__ void store32(bf16* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t mm_pack(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// CNT consecutive outputs of a row (n of them within the matrix), in the widest stores that their place allows.
+template <int CNT>
+__device__ __forceinline__ void store_row(bf16* p, const float (&f)[CNT], int n, int wide) {
+  static_assert(CNT == 16, "16 outputs");
+  if (n >= 16 && wide >= 16) {
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = mm_pack(f[2 * j], f[2 * j + 1]);
+    if (wide == 32) {
+      store32(p, v);
+    } else {
+      reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < n) p[j] = __float2bfloat16_rn(f[j]);
+  }
+}
+
+// TN: weight rows a tile.  PAIR: clusters of two CTAs on tiles of 256 rows; each loads its 128 rows of x and half of
+// the weight rows, counts its bytes on the leader's (rank 0's) stage barrier, the leader issues the MMAs of both, and
+// its commits release both CTAs' stages and accumulators; each CTA sums its own 128 rows.
+template <int TN, bool PAIR>
+__global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
+  constexpr int kBufs = 512 / TN < 8 ? 512 / TN : 8;  // accumulators
+  constexpr int kCols = TN / 2;                       // columns a thread
+  constexpr int kTileM = PAIR ? 2 * kMmTile : kMmTile;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[kBufs], tempty[kBufs], final_bar, recv_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool clustered = PAIR || p.ns > 1;
+  const uint32_t rank = clustered ? cluster_ctarank() : 0u;
+  const bool leader = !PAIR || rank == 0;
+  const int size = PAIR ? 2 : p.ns;
+  const int first = blockIdx.x / size, step = gridDim.x / size;
+  // this CTA's groups of each tile: a split's share, at least one (ns <= G)
+  const int g0 = PAIR ? 0 : (int)rank * p.G / p.ns, g1 = PAIR ? p.G : ((int)rank + 1) * p.G / p.ns;
+  const int ntn = (p.N + TN - 1) / TN;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < kBufs; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], PAIR ? 16 : 8);
+    }
+    mbar_init(&final_bar, 1);
+    mbar_init(&recv_bar, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&tmem_slot, kBufs * TN);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&tmem_slot, kBufs * TN);
+      tmem_relinquish();
+    }
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.x_last);
+    tma_prefetch_desc(&maps.w_last);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  if (clustered)
+    cluster_sync();  // every CTA's barriers exist before another signals them
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = tmem_slot;
+  pdl_trigger();
+  pdl_wait();  // x and w may come from the preceding kernels
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA
+    if (lane == 0) {
+      // weights that one row tile reads come once
+      const uint64_t pol_x = l2_policy_evict_last(), pol_w = p.nm == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int it = first; it < p.nitems && ok; it += step) {
+        const int tv = it / p.nm, tr = it - tv * p.nm;
+        const bool last_r = tr == p.nm - 1, last_v = tv == ntn - 1;
+        const CUtensorMap* xm = last_r ? &maps.x_last : &maps.x;
+        const CUtensorMap* wm = last_v ? &maps.w_last : &maps.w;
+        const int bytes = (last_r ? p.a_last : p.a_bytes) + (last_v ? p.b_last : TN / (PAIR ? 2 : 1) * 128);
+        const int row = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0);
+        const int col = tv * TN + (PAIR ? (int)rank * (TN / 2) : 0);
+        for (int g = g0; g < g1; ++g) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
+            set_error(p.err, kErrTimeout);
+            ok = false;
+            break;
+          }
+          uint8_t* a_s = smem + stage * p.stage_bytes;
+          if constexpr (PAIR) {
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+            tma_load_2d_pair(a_s, xm, fb, g * kQ8Group, row, pol_x);
+            tma_load_2d_pair(a_s + p.a_bytes, wm, fb, g * kQ8Group, col, pol_w);
+          } else {
+            mbar_arrive_expect_tx(&full[stage], bytes);
+            tma_load_2d(a_s, xm, &full[stage], g * kQ8Group, row, pol_x);
+            tma_load_2d(a_s + p.a_bytes, wm, &full[stage], g * kQ8Group, col, pol_w);
+          }
+          ++issued;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        abort_flag = 1;
+        __threadfence_block();
+        // the copies still in flight land before the CTA ends (the leader's barriers count a pair's)
+        if (leader)
+          for (int q = issued < p.stages ? 0 : issued - p.stages; q < issued; ++q)
+            mbar_wait(&full[q % p.stages], (uint32_t)(q / p.stages) & 1u, p.wait_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs (the leader's, for a pair)
+    if (lane == 0 && leader) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      const uint32_t idesc = idesc_e4m3_f32(kTileM, TN);
+      for (int it = first; it < p.nitems && ok; it += step) {
+        for (int g = g0; g < g1; ++g) {
+          const bool freed = PAIR ? mbar_wait_cluster(&tempty[buf], buf_phase ^ 1u, p.wait_ns)
+                                  : mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns);
+          if (!freed || !mbar_wait(&full[stage], phase, p.wait_ns)) {
+            set_error(p.err, kErrTimeout);
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t d = tmem_base + (uint32_t)(buf * TN);
+          const uint32_t a_s = smem_u32(smem + stage * p.stage_bytes), b_s = a_s + p.a_bytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (PAIR)
+              umma_e4m3_pair(d, sdesc_kmajor_sw128(a_s + kk * 32), sdesc_kmajor_sw128(b_s + kk * 32), idesc, kk ? 1u : 0u);
+            else
+              umma_e4m3(d, sdesc_kmajor_sw128(a_s + kk * 32), sdesc_kmajor_sw128(b_s + kk * 32), idesc, kk ? 1u : 0u);
+          }
+          if constexpr (PAIR) {
+            umma_commit_pair_mc(&empty[stage], 0x3);
+            umma_commit_pair_mc(&tfull[buf], 0x3);
+          } else {
+            umma_commit(&empty[stage]);
+            umma_commit(&tfull[buf]);
+          }
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) abort_flag = 1;
+      // every MMA has completed before TMEM and the ring are given up
+      if constexpr (PAIR)
+        umma_commit_pair_mc(&final_bar, 0x1);
+      else
+        umma_commit(&final_bar);
+      if (!mbar_wait(&final_bar, 0, p.wait_ns)) set_error(p.err, kErrTimeout);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ sums over the groups, output
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int c0 = half * kCols;
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    for (int it = first; it < p.nitems && ok; it += step) {
+      const int tv = it / p.nm, tr = it - tv * p.nm;
+      const int row0 = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0) + 32 * quarter;  // the warp's first row
+      const int row = row0 + lane;
+      const bool any = row0 < p.M, mine = row < p.M;
+      const int n0 = tv * TN + c0;
+      const float* sx = p.sx + (size_t)(mine ? row : 0) * p.G;
+      const float* sw = p.sw + (size_t)min(n0 / kQ8Group, (p.N - 1) / kQ8Group) * p.G;
+      float2 acc[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      float fx = ld_plain_f32(sx + g0), fw = ld_plain_f32(sw + g0);
+      for (int g = g0; g < g1; ++g) {
+        const float f = fx * fw;
+        if (g + 1 < g1) {
+          fx = ld_plain_f32(sx + g + 1);
+          fw = ld_plain_f32(sw + g + 1);
+        }
+        const bool got = PAIR ? mbar_wait_cluster(&tfull[buf], buf_phase, p.wait_ns)
+                              : mbar_wait(&tfull[buf], buf_phase, p.wait_ns);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (!got) set_error(p.err, kErrTimeout);
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        if (any) {
+          const uint32_t t = tmem_base + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(buf * TN + c0);
+          const float2 f2 = make_float2(f, f);
+          uint32_t r[2][16];
+          tmem_ld_32x32b_x16(t, r[0]);
+#pragma unroll
+          for (int i = 0; i < kCols / 16; ++i) {
+            tmem_ld_wait_for(r[i & 1]);
+            if (i + 1 < kCols / 16) tmem_ld_32x32b_x16(t + 16 * (i + 1), r[(i + 1) & 1]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[8 * i + j] = fma2(make_float2(__uint_as_float(r[i & 1][2 * j]), __uint_as_float(r[i & 1][2 * j + 1])),
+                                    f2, acc[8 * i + j]);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+          else
+            mbar_arrive(&tempty[buf]);
+        }
+        if (++buf == kBufs) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      if (!ok) abort_flag = 1;
+      if (PAIR || p.ns == 1) {
+        if (ok && mine) {
+          bf16* y = p.y + (size_t)row * p.N + n0;
+#pragma unroll
+          for (int i = 0; i < kCols / 16; ++i) {
+            float o[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              o[2 * j] = acc[8 * i + j].x;
+              o[2 * j + 1] = acc[8 * i + j].y;
+            }
+            const int n = p.N - n0 - 16 * i;
+            if (n > 0) store_row<16>(y + 16 * i, o, n, p.wide);
+          }
+        }
+      } else {
+        // The tile's columns are dealt to the ranks, TN / ns each.  recv[src][column / 4][row]: four columns a piece,
+        // consecutive lanes side by side.  The ring's bytes are free: every MMA that reads them is done before any
+        // accumulator of the last group is, and this CTA has one tile.  What a peer sends may come before this CTA's
+        // own ring is free, so the receive slots lie behind the ring.
+        float4* recv = reinterpret_cast<float4*>(smem + p.stages * p.stage_bytes);
+        const int cols4 = TN / p.ns / 4;
+        if (warp == 2 && lane == 0) {
+          // the other ranks' sums of this rank's columns, for the rows that exist
+          mbar_arrive_expect_tx(&recv_bar, (uint32_t)(p.ns - 1) * cols4 * min(kMmTile, p.M - tr * kTileM) * 16);
+        }
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+          const int c4 = c0 / 4 + j, dst = c4 / cols4;
+          const int at = ((int)rank * cols4 + c4 - dst * cols4) * kMmTile + 32 * quarter + lane;
+          const float4 v = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+          if (!mine) continue;
+          if (dst == (int)rank)
+            recv[at] = v;
+          else
+            st_async_f4(mapa_shared(smem_u32(recv + at), (uint32_t)dst), v, mapa_shared(smem_u32(&recv_bar), (uint32_t)dst));
+        }
+        named_bar_sync(1, 256);  // this CTA's own share is there, and the receive barrier is armed
+        const bool got = mbar_wait_cluster(&recv_bar, 0, p.wait_ns);
+        if (!got) set_error(p.err, kErrTimeout);
+        const int tid = threadIdx.x - 64;
+        for (int u = tid; got && u < cols4 * kMmTile; u += 256) {
+          const int rl = u & (kMmTile - 1), c4 = u / kMmTile;
+          const int m = tr * kTileM + rl, n = tv * TN + ((int)rank * cols4 + c4) * 4;
+          if (m >= p.M || n >= p.N) continue;
+          float4 s = recv[c4 * kMmTile + rl];
+          for (int q = 1; q < p.ns; ++q) {
+            const float4 v = recv[(q * cols4 + c4) * kMmTile + rl];
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+          }
+          bf16* y = p.y + (size_t)m * p.N + n;
+          if (p.wide >= 16) {
+            *reinterpret_cast<uint2*>(y) = make_uint2(mm_pack(s.x, s.y), mm_pack(s.z, s.w));
+          } else {
+            const float o[4] = {s.x, s.y, s.z, s.w};
+            for (int j = 0; j < 4 && n + j < p.N; ++j) y[j] = __float2bfloat16_rn(o[j]);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before_sync();
+  if (clustered)
+    cluster_sync();  // nobody's copies, MMAs or sums go to a CTA that has ended
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, kBufs * TN);
+    else
+      tmem_dealloc(tmem_base, kBufs * TN);
+  }
+}
+
+int round8(int v) { return (v + 7) / 8 * 8; }
+
+template <int TN, bool PAIR>
+cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const DeviceCtx& dc, cudaStream_t s) {
+  constexpr int kTileM = PAIR ? 2 * kMmTile : kMmTile, kBox = PAIR ? TN / 2 : TN;
+  const int ntn = (p.N + TN - 1) / TN;
+  p.nm = (p.M + kTileM - 1) / kTileM;
+  p.nitems = p.nm * ntn;
+  // Boxes of the last tiles hold what there is: a box that reaches far past its tensor makes every load of it slow.
+  // The MMA reads the whole tile; the rows behind a box are what is left of an earlier stage, and their results are
+  // never stored.  One row tile alone: the stage is no longer than its box.
+  const int tail_m = PAIR ? kMmTile : round8(p.M - (p.nm - 1) * kMmTile);
+  const int tail_n = PAIR ? kBox : round8(p.N - (ntn - 1) * TN);
+  const int rows = p.nm == 1 ? tail_m : kMmTile;
+  p.a_bytes = rows * 128;
+  p.a_last = tail_m * 128;
+  p.b_last = tail_n * 128;
+  p.stage_bytes = p.a_bytes + kBox * 128;
+  const int recv = p.ns > 1 ? kMmTile * TN * 4 : 0;
+  p.stages = (kMmRing - recv) / p.stage_bytes;
+  if (p.stages > kMmMaxStages) p.stages = kMmMaxStages;
+  // behind a short stage the MMA reads on, up to a whole tile of rows
+  const int smem = 1024 + p.stages * p.stage_bytes + (recv > 16384 ? recv : 16384);
+  MmMaps maps;
+  if (!make_map_bytes(&maps.x, x, p.M, p.K, (uint32_t)rows) || !make_map_bytes(&maps.x_last, x, p.M, p.K, (uint32_t)tail_m) ||
+      !make_map_bytes(&maps.w, w, p.N, p.K, kBox) || !make_map_bytes(&maps.w_last, w, p.N, p.K, (uint32_t)tail_n))
+    return cudaErrorInvalidValue;
+  auto* kernel = q8_matmul_kernel<TN, PAIR>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
+  if (e != cudaSuccess) return e;
+  const int size = PAIR ? 2 : p.ns;
+  const int most = dc.num_sms / size;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size * (p.nitems < most || p.ns > 1 ? p.nitems : most));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = size > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p);
+}
+
+cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw, bf16* y, int M, int N,
+                             int K, const DeviceCtx& dc, cudaStream_t s) {
+  MmParams p = {};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.G = (K + kQ8Group - 1) / kQ8Group;
+  p.ns = 1;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(y) | ((uintptr_t)N * 2);
+  p.wide = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 2;
+  p.sx = sx;
+  p.sw = sw;
+  p.y = y;
+  p.err = dc.err;
+  p.wait_ns = wait_limit_ns();
+  const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
+  if (M > kMmTile && 2 * pairs >= dc.num_sms) return launch_mm<256, true>(x, w, p, dc, s);
+  const long long tiles = (long long)((M + kMmTile - 1) / kMmTile) * ((N + 127) / 128);
+  // a tile's groups over as many CTAs as there are SMs for them
+  while (p.ns < kMmMaxSplit && 2 * p.ns <= p.G && 2 * p.ns * tiles <= dc.num_sms) p.ns *= 2;
+  return launch_mm<128, false>(x, w, p, dc, s);
+}
+
+}  // namespace
+}  // namespace lsv
+
+using namespace lsv;
+
+extern "C" lsv_status dense_matmul_q8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
+                                      int32_t M, int32_t N, int32_t K, lsv_stream stream) {
+  if (M < 0 || N < 0 || K <= 0) return LSV_ERR_INVALID_ARG;
+  if (K % 16 || K > kQ8MaxCols || ((long long)M + 127) / 128 * (((long long)N + 127) / 128) >= (1ll << 30))
+    return LSV_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return LSV_OK;
+  if (!x || !x_scales || !w || !w_scales || !y) return LSV_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, x_scales, w, w_scales, y};
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) & 15) return LSV_ERR_MISALIGNED;
+  DeviceCtx* dc = nullptr;
+  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
+  return launch_q8_matmul(static_cast<const uint8_t*>(x), x_scales, static_cast<const uint8_t*>(w), w_scales,
+                          static_cast<bf16*>(y), M, N, K, *dc, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LSV_OK
+             : LSV_ERR_CUDA;
+}
