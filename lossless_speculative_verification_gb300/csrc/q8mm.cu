@@ -11,7 +11,7 @@
 // Orientation: 128 rows of x on the MMA's M side, TN weight rows on its N side.  A TMEM lane is then a row of x, a
 // thread's columns lie within one block of 128 weight rows, and the factor of a group is one number a thread.
 // Warp 0 issues TMA (both operands K-major, 128-byte swizzle: a stage is one group), warp 1 the MMAs, each group into
-// the next of 512 / TN accumulators, and warps 2..9 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
+// the next of 512 / TN accumulators, and warps 4..11 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
 //
 // Forms:
 // - few tiles: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank adds one
@@ -32,7 +32,10 @@
 namespace lsv {
 namespace {
 
-constexpr int kMmThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 sums and output
+constexpr int kMmThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 sums and output
+// Registers: what a thread is launched with, and what the first warpgroup keeps and the other two get of the sum.
+constexpr int kMmRegs = 168, kMmRegsFew = 72, kMmRegsMany = 216;
+static_assert(128 * kMmRegsFew + 256 * kMmRegsMany <= 384 * kMmRegs, "register split");
 constexpr int kMmTile = 128;     // rows of x a CTA
 constexpr int kMmMaxStages = 12;
 constexpr int kMmRing = 200 * 1024;
@@ -151,9 +154,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   pdl_trigger();
   pdl_wait();  // x and w may come from the preceding kernels
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA
-    if (lane == 0) {
+  if (warp < 4) {
+    reg_dec<kMmRegsFew>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- TMA
       // weights that one row tile reads come once
       const uint64_t pol_x = l2_policy_evict_last(), pol_w = p.nm == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
       int stage = 0, issued = 0;
@@ -200,19 +204,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
             mbar_wait(&full[q % p.stages], (uint32_t)(q / p.stages) & 1u, p.wait_ns);
       }
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs (the leader's, for a pair)
-    if (lane == 0 && leader) {
+    if (warp == 1 && lane == 0 && leader) {
+      // ---------------------------------------------------------- MMAs (the leader's, for a pair)
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
       const uint32_t idesc = idesc_e4m3_f32(kTileM, TN);
       for (int it = first; it < p.nitems && ok; it += step) {
         for (int g = g0; g < g1; ++g) {
-          const bool freed = PAIR ? mbar_wait_cluster(&tempty[buf], buf_phase ^ 1u, p.wait_ns)
-                                  : mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns);
-          if (!freed || !mbar_wait(&full[stage], phase, p.wait_ns)) {
+          if (!mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns) || !mbar_wait(&full[stage], phase, p.wait_ns)) {
             set_error(p.err, kErrTimeout);
             ok = false;
             break;
@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     __syncwarp();
   } else {
     // ------------------------------------------------------------ sums over the groups, output
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    reg_inc<kMmRegsMany>();
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int c0 = half * kCols;
     int buf = 0;
     uint32_t buf_phase = 0;
@@ -278,8 +279,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           fx = ld_plain_f32(sx + g + 1);
           fw = ld_plain_f32(sw + g + 1);
         }
-        const bool got = PAIR ? mbar_wait_cluster(&tfull[buf], buf_phase, p.wait_ns)
-                              : mbar_wait(&tfull[buf], buf_phase, p.wait_ns);
+        const bool got = mbar_wait(&tfull[buf], buf_phase, p.wait_ns);
         if (!__all_sync(0xffffffffu, got)) {
           if (!got) set_error(p.err, kErrTimeout);
           ok = false;
@@ -289,23 +289,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         if (any) {
           const uint32_t t = tmem_base + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(buf * TN + c0);
           const float2 f2 = make_float2(f, f);
-          uint32_t r[2][16];
-          tmem_ld_32x32b_x16(t, r[0]);
+          uint32_t r[2][32];
+          tmem_ld_32x32b_x32(t, r[0]);
 #pragma unroll
-          for (int i = 0; i < kCols / 16; ++i) {
+          for (int i = 0; i < kCols / 32; ++i) {
             tmem_ld_wait_for(r[i & 1]);
-            if (i + 1 < kCols / 16) tmem_ld_32x32b_x16(t + 16 * (i + 1), r[(i + 1) & 1]);
+            if (i + 1 < kCols / 32) tmem_ld_32x32b_x32(t + 32 * (i + 1), r[(i + 1) & 1]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[8 * i + j] = fma2(make_float2(__uint_as_float(r[i & 1][2 * j]), __uint_as_float(r[i & 1][2 * j + 1])),
-                                    f2, acc[8 * i + j]);
+            for (int j = 0; j < 16; ++j)
+              acc[16 * i + j] = fma2(make_float2(__uint_as_float(r[i & 1][2 * j]), __uint_as_float(r[i & 1][2 * j + 1])),
+                                     f2, acc[16 * i + j]);
           }
         }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
           else
             mbar_arrive(&tempty[buf]);
         }
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         // own ring is free, so the receive slots lie behind the ring.
         float4* recv = reinterpret_cast<float4*>(smem + p.stages * p.stage_bytes);
         const int cols4 = TN / p.ns / 4;
-        if (warp == 2 && lane == 0) {
+        if (warp == 4 && lane == 0) {
           // the other ranks' sums of this rank's columns, for the rows that exist
           mbar_arrive_expect_tx(&recv_bar, (uint32_t)(p.ns - 1) * cols4 * min(kMmTile, p.M - tr * kTileM) * 16);
         }
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         named_bar_sync(1, 256);  // this CTA's own share is there, and the receive barrier is armed
         const bool got = mbar_wait_cluster(&recv_bar, 0, p.wait_ns);
         if (!got) set_error(p.err, kErrTimeout);
-        const int tid = threadIdx.x - 64;
+        const int tid = threadIdx.x - 128;
         for (int u = tid; got && u < cols4 * kMmTile; u += 256) {
           const int rl = u & (kMmTile - 1), c4 = u / kMmTile;
           const int m = tr * kTileM + rl, n = tv * TN + ((int)rank * cols4 + c4) * 4;
@@ -422,6 +422,12 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   auto* kernel = q8_matmul_kernel<TN, PAIR>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
   if (e != cudaSuccess) return e;
+  // a register split above the launch's own would wait for ever
+  static const bool split = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs >= kMmRegs;
+  }();
+  if (!split) return cudaErrorInvalidConfiguration;
   const int size = PAIR ? 2 : p.ns;
   const int most = dc.num_sms / size;
   cudaLaunchConfig_t cfg = {};
