@@ -38,7 +38,8 @@ constexpr int kMmRegs = 168, kMmRegsFew = 72, kMmRegsMany = 216;
 static_assert(128 * kMmRegsFew + 256 * kMmRegsMany <= 384 * kMmRegs, "register split");
 constexpr int kMmTile = 128;     // rows of x a CTA
 constexpr int kMmMaxStages = 12;
-constexpr int kMmRing = 200 * 1024;
+constexpr int kMmSmem = 225 * 1024;  // the ring and what lies behind it
+constexpr int kMmPanel = 32 * 128;   // bytes of 64 columns of a warp's 32 rows of output
 constexpr int kMmMaxSplit = 8;
 
 struct MmParams {
@@ -47,7 +48,7 @@ struct MmParams {
   int ns;              // CTAs that share a tile's groups (cluster size; 1 for pairs)
   int stages, a_bytes, stage_bytes;
   int a_last, b_last;  // bytes of the boxes of the last row tile and the last weight tile
-  int wide;            // bytes of a row's aligned stores: 32, 16 or 2
+  int aligned;         // rows of y start on 16 bytes: they are stored by TMA
   const float* sx;
   const float* sw;
   bf16* y;
@@ -56,39 +57,29 @@ struct MmParams {
 };
 
 struct MmMaps {
-  CUtensorMap x, x_last, w, w_last;
+  CUtensorMap x, x_last, w, w_last, y;
 };
-
-__device__ __forceinline__ void store32(bf16* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
 
 __device__ __forceinline__ uint32_t mm_pack(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// CNT consecutive outputs of a row (n of them within the matrix), in the widest stores that their place allows.
-template <int CNT>
-__device__ __forceinline__ void store_row(bf16* p, const float (&f)[CNT], int n, int wide) {
-  static_assert(CNT == 16, "16 outputs");
-  if (n >= 16 && wide >= 16) {
-    uint32_t v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = mm_pack(f[2 * j], f[2 * j + 1]);
-    if (wide == 32) {
-      store32(p, v);
-    } else {
-      reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (j < n) p[j] = __float2bfloat16_rn(f[j]);
+// Four groups' scales of a row, those from `g` (a multiple of 4) on that lie within [0, G).
+__device__ __forceinline__ float4 load_scales(const float* s, int g, int G) {
+  if (G % 4 == 0) {
+    const uint4 v = ld_plain128(s + g);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
   }
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  v.x = ld_plain_f32(s + g);
+  if (g + 1 < G) v.y = ld_plain_f32(s + g + 1);
+  if (g + 2 < G) v.z = ld_plain_f32(s + g + 2);
+  if (g + 3 < G) v.w = ld_plain_f32(s + g + 3);
+  return v;
+}
+__device__ __forceinline__ float scale_at(const float4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // TN: weight rows a tile.  PAIR: clusters of two CTAs on tiles of 256 rows; each loads its 128 rows of x and half of
@@ -258,27 +249,45 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     reg_inc<kMmRegsMany>();
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int c0 = half * kCols;
+    uint8_t* behind = smem + p.stages * p.stage_bytes;
+    uint8_t* panels = behind + (warp - 4) * (kCols / 64 * kMmPanel);
     int buf = 0;
     uint32_t buf_phase = 0;
     bool ok = true;
+    // Scales come four groups at a time, four groups and more before they are used, across tiles too.
+    auto row_of = [&](int it) { return it % p.nm * kTileM + (PAIR ? (int)rank * kMmTile : 0) + 32 * quarter; };
+    auto sx_of = [&](int it) { return p.sx + (size_t)min(row_of(it) + lane, p.M - 1) * p.G; };
+    auto sw_of = [&](int it) {
+      return p.sw + (size_t)min((it / p.nm * TN + c0) / kQ8Group, (p.N - 1) / kQ8Group) * p.G;
+    };
+    const int b0 = g0 & ~3;
+    float4 fx = make_float4(0.f, 0.f, 0.f, 0.f), fw = fx;
+    if (first < p.nitems) {
+      fx = load_scales(sx_of(first), b0, p.G);
+      fw = load_scales(sw_of(first), b0, p.G);
+    }
     for (int it = first; it < p.nitems && ok; it += step) {
       const int tv = it / p.nm, tr = it - tv * p.nm;
-      const int row0 = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0) + 32 * quarter;  // the warp's first row
+      const int row0 = row_of(it);  // the warp's first row
       const int row = row0 + lane;
       const bool any = row0 < p.M, mine = row < p.M;
       const int n0 = tv * TN + c0;
-      const float* sx = p.sx + (size_t)(mine ? row : 0) * p.G;
-      const float* sw = p.sw + (size_t)min(n0 / kQ8Group, (p.N - 1) / kQ8Group) * p.G;
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      float fx = ld_plain_f32(sx + g0), fw = ld_plain_f32(sw + g0);
+      float4 gx, gw;
       for (int g = g0; g < g1; ++g) {
-        const float f = fx * fw;
-        if (g + 1 < g1) {
-          fx = ld_plain_f32(sx + g + 1);
-          fw = ld_plain_f32(sw + g + 1);
+        if (g == g0 || (g & 3) == 0) {
+          gx = fx;
+          gw = fw;
+          const int next = (g & ~3) + 4;
+          const bool same = next < g1;
+          if (same || it + step < p.nitems) {
+            fx = load_scales(sx_of(same ? it : it + step), same ? next : b0, p.G);
+            fw = load_scales(sw_of(same ? it : it + step), same ? next : b0, p.G);
+          }
         }
+        const float f = scale_at(gx, g & 3) * scale_at(gw, g & 3);
         const bool got = mbar_wait(&tfull[buf], buf_phase, p.wait_ns);
         if (!__all_sync(0xffffffffu, got)) {
           if (!got) set_error(p.err, kErrTimeout);
@@ -316,18 +325,31 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
       }
       if (!ok) abort_flag = 1;
       if (PAIR || p.ns == 1) {
-        if (ok && mine) {
+        if (ok && any && p.aligned) {
+          // to shared memory as 128-byte rows, 16-byte pieces swizzled as TMA has them, and out while the next tile runs
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kCols / 8; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = mm_pack(acc[4 * i + j].x, acc[4 * i + j].y);
+            *reinterpret_cast<uint4*>(panels + i / 8 * kMmPanel + lane * 128 + (((i & 7) ^ (lane & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < kCols / 64; ++i)
+              if (n0 + 64 * i < p.N) tma_store_2d(&maps.y, panels + i * kMmPanel, n0 + 64 * i, row0);
+          }
+        } else if (ok && mine) {
           bf16* y = p.y + (size_t)row * p.N + n0;
 #pragma unroll
-          for (int i = 0; i < kCols / 16; ++i) {
-            float o[16];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              o[2 * j] = acc[8 * i + j].x;
-              o[2 * j + 1] = acc[8 * i + j].y;
-            }
-            const int n = p.N - n0 - 16 * i;
-            if (n > 0) store_row<16>(y + 16 * i, o, n, p.wide);
+          for (int j = 0; j < kCols / 2; ++j) {
+            if (n0 + 2 * j < p.N) y[2 * j] = __float2bfloat16_rn(acc[j].x);
+            if (n0 + 2 * j + 1 < p.N) y[2 * j + 1] = __float2bfloat16_rn(acc[j].y);
           }
         }
       } else {
@@ -335,7 +357,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         // consecutive lanes side by side.  The ring's bytes are free: every MMA that reads them is done before any
         // accumulator of the last group is, and this CTA has one tile.  What a peer sends may come before this CTA's
         // own ring is free, so the receive slots lie behind the ring.
-        float4* recv = reinterpret_cast<float4*>(smem + p.stages * p.stage_bytes);
+        float4* recv = reinterpret_cast<float4*>(behind);
         const int cols4 = TN / p.ns / 4;
         if (warp == 4 && lane == 0) {
           // the other ranks' sums of this rank's columns, for the rows that exist
@@ -366,7 +388,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
           }
           bf16* y = p.y + (size_t)m * p.N + n;
-          if (p.wide >= 16) {
+          if (p.aligned) {
             *reinterpret_cast<uint2*>(y) = make_uint2(mm_pack(s.x, s.y), mm_pack(s.z, s.w));
           } else {
             const float o[4] = {s.x, s.y, s.z, s.w};
@@ -375,6 +397,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -410,15 +433,19 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   p.a_last = tail_m * 128;
   p.b_last = tail_n * 128;
   p.stage_bytes = p.a_bytes + kBox * 128;
-  const int recv = p.ns > 1 ? kMmTile * TN * 4 : 0;
-  p.stages = (kMmRing - recv) / p.stage_bytes;
+  // behind the ring: the receive slots of a split, or the output's panels; and behind a short stage the MMA reads on, up
+  // to a whole tile of rows
+  const int behind = p.ns > 1 ? kMmTile * TN * 4 : kMmTile * TN * 2;
+  static_assert(kMmTile * TN * 2 >= kMmTile * 128, "room behind the last stage");
+  p.stages = (kMmSmem - 1024 - behind) / p.stage_bytes;
   if (p.stages > kMmMaxStages) p.stages = kMmMaxStages;
-  // behind a short stage the MMA reads on, up to a whole tile of rows
-  const int smem = 1024 + p.stages * p.stage_bytes + (recv > 16384 ? recv : 16384);
+  const int smem = 1024 + p.stages * p.stage_bytes + behind;
   MmMaps maps;
   if (!make_map_bytes(&maps.x, x, p.M, p.K, (uint32_t)rows) || !make_map_bytes(&maps.x_last, x, p.M, p.K, (uint32_t)tail_m) ||
       !make_map_bytes(&maps.w, w, p.N, p.K, kBox) || !make_map_bytes(&maps.w_last, w, p.N, p.K, (uint32_t)tail_n))
     return cudaErrorInvalidValue;
+  maps.y = maps.x;
+  if (p.aligned && !make_map_out(&maps.y, p.y, p.M, p.N)) return cudaErrorInvalidValue;
   auto* kernel = q8_matmul_kernel<TN, PAIR>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
   if (e != cudaSuccess) return e;
@@ -455,8 +482,7 @@ cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w
   p.K = K;
   p.G = (K + kQ8Group - 1) / kQ8Group;
   p.ns = 1;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(y) | ((uintptr_t)N * 2);
-  p.wide = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 2;
+  p.aligned = N % 8 == 0;
   p.sx = sx;
   p.sw = sw;
   p.y = y;

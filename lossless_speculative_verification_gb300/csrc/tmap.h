@@ -54,6 +54,11 @@ inline bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D bf16 tensor [rows, cols] (cols contiguous, a multiple of 8) that tiles of 64 columns x 32 rows are stored to.
+inline bool make_map_out(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols) {
+  return make_map(m, base, rows, cols, 32);
+}
+
 // Gate/up weights as pairs: the gate row r and its up row r + half_rows of a
 // [.., cols] bf16 matrix, viewed as dims {cols, 2, rows}.  A box {64, 2, 64}
 // stages 64 features as 128 interleaved rows (gate 0, up 0, gate 1, up 1, ...)
