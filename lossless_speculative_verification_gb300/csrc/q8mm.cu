@@ -94,7 +94,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[kBufs], tempty[kBufs], final_bar, recv_bar;
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool clustered = PAIR || p.ns > 1;
   const uint32_t rank = clustered ? cluster_ctarank() : 0u;
@@ -116,7 +115,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     }
     mbar_init(&final_bar, 1);
     mbar_init(&recv_bar, 1);
-    abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -147,10 +145,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
 
   if (warp < 4) {
     reg_dec<kMmRegsFew>();
-    if (warp == 0 && lane == 0) {
+    // Both loops are run by the whole warp, and one lane issues.
+    if (warp == 0) {
       // ---------------------------------------------------------- TMA
       // weights that one row tile reads come once
       const uint64_t pol_x = l2_policy_evict_last(), pol_w = p.nm == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+      const uint32_t fb0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -163,22 +163,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         const int row = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0);
         const int col = tv * TN + (PAIR ? (int)rank * (TN / 2) : 0);
         for (int g = g0; g < g1; ++g) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
-            set_error(p.err, kErrTimeout);
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns))) {
             ok = false;
             break;
           }
-          uint8_t* a_s = smem + stage * p.stage_bytes;
-          if constexpr (PAIR) {
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
-            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-            tma_load_2d_pair(a_s, xm, fb, g * kQ8Group, row, pol_x);
-            tma_load_2d_pair(a_s + p.a_bytes, wm, fb, g * kQ8Group, col, pol_w);
-          } else {
-            mbar_arrive_expect_tx(&full[stage], bytes);
-            tma_load_2d(a_s, xm, &full[stage], g * kQ8Group, row, pol_x);
-            tma_load_2d(a_s + p.a_bytes, wm, &full[stage], g * kQ8Group, col, pol_w);
+          if (elect_one()) {
+            uint8_t* a_s = smem + stage * p.stage_bytes;
+            if constexpr (PAIR) {
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+              tma_load_2d_pair(a_s, xm, fb0 + 8 * stage, g * kQ8Group, row, pol_x);
+              tma_load_2d_pair(a_s + p.a_bytes, wm, fb0 + 8 * stage, g * kQ8Group, col, pol_w);
+            } else {
+              mbar_arrive_expect_tx(&full[stage], bytes);
+              tma_load_2d(a_s, xm, &full[stage], g * kQ8Group, row, pol_x);
+              tma_load_2d(a_s + p.a_bytes, wm, &full[stage], g * kQ8Group, col, pol_w);
+            }
           }
+          __syncwarp();
           ++issued;
           if (++stage == p.stages) {
             stage = 0;
@@ -186,45 +187,49 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           }
         }
       }
-      if (!ok) {
-        abort_flag = 1;
-        __threadfence_block();
+      if (!ok && lane == 0) {
+        set_error(p.err, kErrTimeout);
         // the copies still in flight land before the CTA ends (the leader's barriers count a pair's)
         if (leader)
           for (int q = issued < p.stages ? 0 : issued - p.stages; q < issued; ++q)
             mbar_wait(&full[q % p.stages], (uint32_t)(q / p.stages) & 1u, p.wait_ns);
       }
-    }
-    if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
       // ---------------------------------------------------------- MMAs (the leader's, for a pair)
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
-      const uint32_t idesc = idesc_e4m3_f32(kTileM, TN);
+      constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, TN);
+      const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem)), b0 = sdesc_kmajor_sw128(smem_u32(smem) + p.a_bytes);
       for (int it = first; it < p.nitems && ok; it += step) {
         for (int g = g0; g < g1; ++g) {
-          if (!mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns) || !mbar_wait(&full[stage], phase, p.wait_ns)) {
-            set_error(p.err, kErrTimeout);
+          const bool got =
+              mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns) && mbar_wait(&full[stage], phase, p.wait_ns);
+          if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t d = tmem_base + (uint32_t)(buf * TN);
-          const uint32_t a_s = smem_u32(smem + stage * p.stage_bytes), b_s = a_s + p.a_bytes;
+          if (elect_one()) {
+            const uint32_t d = tmem_base + (uint32_t)(buf * TN);
+            // descriptors hold addresses in units of 16 bytes; a step of 32 columns is two
+            const uint64_t at = (uint64_t)(uint32_t)(stage * (p.stage_bytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if constexpr (PAIR)
-              umma_e4m3_pair(d, sdesc_kmajor_sw128(a_s + kk * 32), sdesc_kmajor_sw128(b_s + kk * 32), idesc, kk ? 1u : 0u);
-            else
-              umma_e4m3(d, sdesc_kmajor_sw128(a_s + kk * 32), sdesc_kmajor_sw128(b_s + kk * 32), idesc, kk ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              if constexpr (PAIR)
+                umma_e4m3_pair(d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, kk ? 1u : 0u);
+              else
+                umma_e4m3(d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, kk ? 1u : 0u);
+            }
+            if constexpr (PAIR) {
+              umma_commit_pair_mc(&tfull[buf], 0x3);
+              umma_commit_pair_mc(&empty[stage], 0x3);
+            } else {
+              umma_commit(&tfull[buf]);
+              umma_commit(&empty[stage]);
+            }
           }
-          if constexpr (PAIR) {
-            umma_commit_pair_mc(&empty[stage], 0x3);
-            umma_commit_pair_mc(&tfull[buf], 0x3);
-          } else {
-            umma_commit(&empty[stage]);
-            umma_commit(&tfull[buf]);
-          }
+          __syncwarp();
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
@@ -235,13 +240,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           }
         }
       }
-      if (!ok) abort_flag = 1;
       // every MMA has completed before TMEM and the ring are given up
-      if constexpr (PAIR)
-        umma_commit_pair_mc(&final_bar, 0x1);
-      else
-        umma_commit(&final_bar);
-      if (!mbar_wait(&final_bar, 0, p.wait_ns)) set_error(p.err, kErrTimeout);
+      if (elect_one()) {
+        if (!ok) set_error(p.err, kErrTimeout);
+        if constexpr (PAIR)
+          umma_commit_pair_mc(&final_bar, 0x1);
+        else
+          umma_commit(&final_bar);
+        if (!mbar_wait(&final_bar, 0, p.wait_ns)) set_error(p.err, kErrTimeout);
+      }
     }
     __syncwarp();
   } else {
@@ -323,7 +330,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           buf_phase ^= 1u;
         }
       }
-      if (!ok) abort_flag = 1;
       if (PAIR || p.ns == 1) {
         if (ok && any && p.aligned) {
           // to shared memory as 128-byte rows, 16-byte pieces swizzled as TMA has them, and out while the next tile runs
