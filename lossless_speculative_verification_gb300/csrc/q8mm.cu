@@ -11,7 +11,9 @@
 // Orientation: 128 rows of x on the MMA's M side, TN weight rows on its N side.  A TMEM lane is then a row of x, a
 // thread's columns lie within one block of 128 weight rows, and the factor of a group is one number a thread.
 // Warp 0 issues TMA (both operands K-major, 128-byte swizzle: a stage is one group), warp 1 the MMAs, each group into
-// the next of 512 / TN accumulators, and warps 4..11 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
+// the next of 512 / TN accumulators, warps 2 and 3 bring the scales, multiplied, four groups at a time (a row's scales
+// lie far from the next row's: such loads hold up every other access to shared memory of the warp that issues them), and
+// warps 4..11 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
 //
 // Forms:
 // - few tiles: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank adds one
@@ -33,13 +35,20 @@ namespace lsv {
 namespace {
 
 constexpr int kMmThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 sums and output
-// Registers: what a thread is launched with, and what the first warpgroup keeps and the other two get of the sum.
-constexpr int kMmRegs = 168, kMmRegsFew = 72, kMmRegsMany = 216;
-static_assert(128 * kMmRegsFew + 256 * kMmRegsMany <= 384 * kMmRegs, "register split");
+// Registers: what a thread is launched with, and what the first warpgroup keeps and the other two get of the sum (the
+// pair's sums take more; at 128 columns the first warpgroup has the more to hold).
+constexpr int kMmRegs = 168;
+constexpr int mm_regs_few(bool pair) { return pair ? 72 : 88; }
+constexpr int mm_regs_many(bool pair) { return pair ? 216 : 208; }
+static_assert(128 * mm_regs_few(true) + 256 * mm_regs_many(true) <= 384 * kMmRegs, "register split");
+static_assert(128 * mm_regs_few(false) + 256 * mm_regs_many(false) <= 384 * kMmRegs, "register split");
 constexpr int kMmTile = 128;     // rows of x a CTA
 constexpr int kMmMaxStages = 12;
 constexpr int kMmSmem = 225 * 1024;  // the ring and what lies behind it
 constexpr int kMmPanel = 32 * 128;   // bytes of 64 columns of a warp's 32 rows of output
+constexpr int kMmBlock = 4;          // groups whose scales are brought at once
+constexpr int kMmScaleSlots = 4;     // blocks of scales in shared memory
+constexpr int kMmScaleBytes = kMmScaleSlots * kMmBlock * kMmTile * 2 * 4;
 constexpr int kMmMaxSplit = 8;
 
 struct MmParams {
@@ -78,9 +87,6 @@ __device__ __forceinline__ float4 load_scales(const float* s, int g, int G) {
   if (g + 3 < G) v.w = ld_plain_f32(s + g + 3);
   return v;
 }
-__device__ __forceinline__ float scale_at(const float4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
 
 // TN: weight rows a tile.  PAIR: clusters of two CTAs on tiles of 256 rows; each loads its 128 rows of x and half of
 // the weight rows, counts its bytes on the leader's (rank 0's) stage barrier, the leader issues the MMAs of both, and
@@ -92,7 +98,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   constexpr int kTileM = PAIR ? 2 * kMmTile : kMmTile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[kBufs], tempty[kBufs], final_bar, recv_bar;
+  __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[kBufs], tempty[kBufs], sfull[kMmScaleSlots],
+      sempty[kMmScaleSlots], final_bar, recv_bar;
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool clustered = PAIR || p.ns > 1;
@@ -112,6 +119,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     for (int a = 0; a < kBufs; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], PAIR ? 16 : 8);
+    }
+    for (int q = 0; q < kMmScaleSlots; ++q) {
+      mbar_init(&sfull[q], 2);
+      mbar_init(&sempty[q], 8);
     }
     mbar_init(&final_bar, 1);
     mbar_init(&recv_bar, 1);
@@ -140,11 +151,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = tmem_slot;
+  // [slot][group of four][half of the columns][row]
+  float* scales = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);
+  uint8_t* behind = reinterpret_cast<uint8_t*>(scales) + kMmScaleBytes;
   pdl_trigger();
   pdl_wait();  // x and w may come from the preceding kernels
 
   if (warp < 4) {
-    reg_dec<kMmRegsFew>();
+    reg_dec<mm_regs_few(PAIR)>();
     // Both loops are run by the whole warp, and one lane issues.
     if (warp == 0) {
       // ---------------------------------------------------------- TMA
@@ -250,105 +264,141 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         if (!mbar_wait(&final_bar, 0, p.wait_ns)) set_error(p.err, kErrTimeout);
       }
     }
+    if (warp >= 2) {
+      // ---------------------------------------------------------- scales: 64 rows a warp, two a lane
+      const int r0 = (warp - 2) * 64 + lane;
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int it = first; it < p.nitems && ok; it += step) {
+        const int tv = it / p.nm, tr = it - tv * p.nm;
+        const int row = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0) + r0;
+        const float* sx0 = p.sx + (size_t)min(row, p.M - 1) * p.G;
+        const float* sx1 = p.sx + (size_t)min(row + 32, p.M - 1) * p.G;
+        const int nb = (p.N - 1) / kQ8Group;
+        const float* sw0 = p.sw + (size_t)min(tv * TN / kQ8Group, nb) * p.G;
+        const float* sw1 = p.sw + (size_t)min((tv * TN + kCols) / kQ8Group, nb) * p.G;
+        for (int g = g0 & ~3; g < g1; g += kMmBlock) {
+          const float4 x0 = load_scales(sx0, g, p.G), x1 = load_scales(sx1, g, p.G);
+          const float4 w0 = load_scales(sw0, g, p.G), w1 = load_scales(sw1, g, p.G);
+          if (!__all_sync(0xffffffffu, mbar_wait(&sempty[slot], phase ^ 1u, p.wait_ns))) {
+            ok = false;
+            break;
+          }
+          float* d = scales + slot * (kMmBlock * 2 * kMmTile) + r0;
+          const float xs[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
+          const float ws[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              d[(2 * i + h) * kMmTile] = xs[0][i] * ws[h][i];
+              d[(2 * i + h) * kMmTile + 32] = xs[1][i] * ws[h][i];
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull[slot]);
+          if (++slot == kMmScaleSlots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+    }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ sums over the groups, output
-    reg_inc<kMmRegsMany>();
+    reg_inc<mm_regs_many(PAIR)>();
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int c0 = half * kCols;
-    uint8_t* behind = smem + p.stages * p.stage_bytes;
-    uint8_t* panels = behind + (warp - 4) * (kCols / 64 * kMmPanel);
-    int buf = 0;
-    uint32_t buf_phase = 0;
+    uint8_t* panel = behind + (warp - 4) * kMmPanel;
+    int buf = 0, slot = 0;
+    uint32_t buf_phase = 0, slot_phase = 0;
     bool ok = true;
-    // Scales come four groups at a time, four groups and more before they are used, across tiles too.
-    auto row_of = [&](int it) { return it % p.nm * kTileM + (PAIR ? (int)rank * kMmTile : 0) + 32 * quarter; };
-    auto sx_of = [&](int it) { return p.sx + (size_t)min(row_of(it) + lane, p.M - 1) * p.G; };
-    auto sw_of = [&](int it) {
-      return p.sw + (size_t)min((it / p.nm * TN + c0) / kQ8Group, (p.N - 1) / kQ8Group) * p.G;
+    const uint32_t leaders_tempty = PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
+    // The accumulators are read 32 columns at a time, one piece ahead of the sums, from one group into the next and from
+    // one tile into the next: a wait for a group and the latency of a read run beside the sums of what was read before.
+    // A thread whose row does not exist reads what is there, and stores nothing.
+    const uint32_t t_row = tmem_base + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0;
+    constexpr int kPieces = kCols / 32;
+    static_assert(kPieces % 2 == 0, "a group begins in r[0]");
+    uint32_t r[2][32];
+    int left = first < p.nitems ? ((p.nitems - 1 - first) / step + 1) * (g1 - g0) : 0;  // groups not begun
+    auto begin = [&]() {
+      --left;
+      const bool got = mbar_wait(&tfull[buf], buf_phase, p.wait_ns);
+      ok = __all_sync(0xffffffffu, got);
+      tc_fence_after_sync();
+      tmem_ld_32x32b_x32(t_row + (uint32_t)(buf * TN), r[0]);
     };
-    const int b0 = g0 & ~3;
-    float4 fx = make_float4(0.f, 0.f, 0.f, 0.f), fw = fx;
-    if (first < p.nitems) {
-      fx = load_scales(sx_of(first), b0, p.G);
-      fw = load_scales(sw_of(first), b0, p.G);
-    }
+    if (left > 0) begin();
     for (int it = first; it < p.nitems && ok; it += step) {
       const int tv = it / p.nm, tr = it - tv * p.nm;
-      const int row0 = row_of(it);  // the warp's first row
+      const int row0 = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0) + 32 * quarter;  // the warp's first row
       const int row = row0 + lane;
       const bool any = row0 < p.M, mine = row < p.M;
       const int n0 = tv * TN + c0;
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      float4 gx, gw;
       for (int g = g0; g < g1; ++g) {
-        if (g == g0 || (g & 3) == 0) {
-          gx = fx;
-          gw = fw;
-          const int next = (g & ~3) + 4;
-          const bool same = next < g1;
-          if (same || it + step < p.nitems) {
-            fx = load_scales(sx_of(same ? it : it + step), same ? next : b0, p.G);
-            fw = load_scales(sw_of(same ? it : it + step), same ? next : b0, p.G);
-          }
-        }
-        const float f = scale_at(gx, g & 3) * scale_at(gw, g & 3);
-        const bool got = mbar_wait(&tfull[buf], buf_phase, p.wait_ns);
-        if (!__all_sync(0xffffffffu, got)) {
-          if (!got) set_error(p.err, kErrTimeout);
+        bool got = true;
+        if (g == g0 || (g & 3) == 0) got = mbar_wait(&sfull[slot], slot_phase, p.wait_ns);
+        const float f = scales[((slot * kMmBlock + (g & 3)) * 2 + half) * kMmTile + 32 * quarter + lane];
+        if (!__all_sync(0xffffffffu, got && ok)) {
           ok = false;
           break;
         }
-        tc_fence_after_sync();
-        if (any) {
-          const uint32_t t = tmem_base + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(buf * TN + c0);
-          const float2 f2 = make_float2(f, f);
-          uint32_t r[2][32];
-          tmem_ld_32x32b_x32(t, r[0]);
+        const float2 f2 = make_float2(f, f);
 #pragma unroll
-          for (int i = 0; i < kCols / 32; ++i) {
-            tmem_ld_wait_for(r[i & 1]);
-            if (i + 1 < kCols / 32) tmem_ld_32x32b_x32(t + 32 * (i + 1), r[(i + 1) & 1]);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[16 * i + j] = fma2(make_float2(__uint_as_float(r[i & 1][2 * j]), __uint_as_float(r[i & 1][2 * j + 1])),
-                                     f2, acc[16 * i + j]);
+        for (int i = 0; i < kPieces; ++i) {
+          tmem_ld_wait_for(r[i & 1]);
+          if (i + 1 < kPieces) {
+            tmem_ld_32x32b_x32(t_row + (uint32_t)(buf * TN + 32 * (i + 1)), r[(i + 1) & 1]);
+          } else {
+            // all of the accumulators are read
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if (PAIR && !leader)
+                mbar_arrive_cluster_relaxed(leaders_tempty + 8 * buf);
+              else
+                mbar_arrive(&tempty[buf]);
+              if ((g & 3) == 3 || g + 1 == g1) mbar_arrive(&sempty[slot]);
+            }
+            if (++buf == kBufs) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
+            if (left > 0) begin();
           }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[16 * i + j] = fma2(make_float2(__uint_as_float(r[i & 1][2 * j]), __uint_as_float(r[i & 1][2 * j + 1])),
+                                   f2, acc[16 * i + j]);
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR)
-            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
-          else
-            mbar_arrive(&tempty[buf]);
-        }
-        if (++buf == kBufs) {
-          buf = 0;
-          buf_phase ^= 1u;
+        if (((g & 3) == 3 || g + 1 == g1) && ++slot == kMmScaleSlots) {
+          slot = 0;
+          slot_phase ^= 1u;
         }
       }
       if (PAIR || p.ns == 1) {
         if (ok && any && p.aligned) {
           // to shared memory as 128-byte rows, 16-byte pieces swizzled as TMA has them, and out while the next tile runs
-          if (lane == 0) bulk_wait_read();
-          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < kCols / 8; ++i) {
-            uint32_t v[4];
+          for (int q = 0; q < kCols / 64; ++q) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = mm_pack(acc[4 * i + j].x, acc[4 * i + j].y);
-            *reinterpret_cast<uint4*>(panels + i / 8 * kMmPanel + lane * 128 + (((i & 7) ^ (lane & 7)) << 4)) =
-                make_uint4(v[0], v[1], v[2], v[3]);
-          }
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
+            for (int i = 0; i < 8; ++i) {
+              uint32_t v[4];
 #pragma unroll
-            for (int i = 0; i < kCols / 64; ++i)
-              if (n0 + 64 * i < p.N) tma_store_2d(&maps.y, panels + i * kMmPanel, n0 + 64 * i, row0);
+              for (int j = 0; j < 4; ++j) v[j] = mm_pack(acc[32 * q + 4 * i + j].x, acc[32 * q + 4 * i + j].y);
+              *reinterpret_cast<uint4*>(panel + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0 && n0 + 64 * q < p.N) tma_store_2d(&maps.y, panel, n0 + 64 * q, row0);
           }
         } else if (ok && mine) {
           bf16* y = p.y + (size_t)row * p.N + n0;
@@ -403,6 +453,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         }
       }
     }
+    if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+    tmem_ld_wait();  // what a wait that ran out left in flight
     if (lane == 0) bulk_wait_all();
   }
 
@@ -441,8 +493,8 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   p.stage_bytes = p.a_bytes + kBox * 128;
   // behind the ring: the receive slots of a split, or the output's panels; and behind a short stage the MMA reads on, up
   // to a whole tile of rows
-  const int behind = p.ns > 1 ? kMmTile * TN * 4 : kMmTile * TN * 2;
-  static_assert(kMmTile * TN * 2 >= kMmTile * 128, "room behind the last stage");
+  const int behind = kMmScaleBytes + (p.ns > 1 ? kMmTile * TN * 4 : 8 * kMmPanel);
+  static_assert(kMmScaleBytes + 8 * kMmPanel >= kMmTile * 128, "room behind the last stage");
   p.stages = (kMmSmem - 1024 - behind) / p.stage_bytes;
   if (p.stages > kMmMaxStages) p.stages = kMmMaxStages;
   const int smem = 1024 + p.stages * p.stage_bytes + behind;
