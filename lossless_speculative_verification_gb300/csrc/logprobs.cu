@@ -36,7 +36,7 @@ constexpr int kLpMaxTop = 32;      // most alternatives
 constexpr int kLpCandidates = 1024;
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpMinPiece = kLpThreads * 16;  // bytes of a CTA's piece of a row: a vector a thread
-static_assert(kLpMaxTop <= kLpGroups && kLpMaxCluster * kLpMaxTop <= kLpCandidates, "candidates");
+static_assert(kLpMaxTop <= kLpGroups && kLpMaxTop == 32 && kLpMaxCluster <= 2 * kLpWarps && kLpWarps <= 32, "lists");
 
 // Larger value first, then the lower token; never 0.  -0 and 0 are equal.
 __device__ __forceinline__ uint64_t lp_key(float x, int v) {
@@ -74,6 +74,17 @@ __device__ __forceinline__ Part join(Part a, Part b) {
   move_to(a, m);
   move_to(b, m);
   return Part{m, a.s + b.s, a.d + b.d};
+}
+// The sums of `width` lanes (a power of two), in each of them.
+__device__ __forceinline__ Part join_lanes(Part a, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) {
+    Part b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.d = __shfl_xor_sync(0xffffffffu, a.d, o);
+    a = join(a, b);
+  }
+  return a;
 }
 __device__ __forceinline__ void add_one(Part& a, float x) {
   if (!(x <= a.m)) move_to(a, x);
@@ -128,8 +139,7 @@ struct Vec<float> {
 struct LpSmem {
   uint64_t cand[kLpCandidates];
   uint64_t group[kLpGroups];
-  uint64_t top[kLpMaxTop];
-  uint64_t all[kLpMaxCluster * kLpMaxTop];  // rank 0's: every rank's largest
+  uint64_t top[kLpMaxCluster][kLpMaxTop];   // the CTA's largest in order, 0 behind them; rank 0's: every rank's
   Part parts[kLpMaxCluster];                // rank 0's: every rank's sums
   Part warp[kLpWarps];
   uint64_t best[kLpWarps];
@@ -137,6 +147,17 @@ struct LpSmem {
   uint64_t bound;
   int ncand;
 };
+
+// Two lists of 32 keys in falling order, one a lane and the other from its end: the 32 largest, in falling order.
+__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b_reversed, int lane) {
+  uint64_t k = a > b_reversed ? a : b_reversed;  // rises and then falls, or the other way round
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
+    k = ((lane & o) == 0) == (other > k) ? other : k;
+  }
+  return k;
+}
 
 // The n largest of `cnt` different keys, in order, to dst (0 where there are fewer): each key's place is the number of
 // larger ones.
@@ -177,7 +198,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i) {
       const int q = k + i * kLpThreads;
-      v[i] = q < k1 ? ld_stream128(xv + (size_t)q * N)
+      v[i] = q < k1 ? ld_plain128(xv + (size_t)q * N)
                     : make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
     }
   };
@@ -225,21 +246,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
   if (edge >= 0) add_one(a, ex);
 
   // ------------------------------------------------------------ the CTA's sums
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Part b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.d = __shfl_xor_sync(0xffffffffu, a.d, o);
-    a = join(a, b);
-  }
+  a = join_lanes(a, 32);
   if (lane == 0) sm.warp[warp] = a;
   if (tid == 0) {
     sm.ncand = 0;
     sm.bound = 0;
   }
   if (tid < kLpMaxTop) {
-    sm.top[tid] = 0;
+    sm.top[0][tid] = 0;
     sm.hot[tid] = -1;
   }
 
@@ -267,12 +281,19 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
     }
     if ((tid & 3) == 0) sm.group[tid >> 2] = key;
     __syncthreads();
-    if (tid < kLpGroups) {
-      const uint64_t k = sm.group[tid];
+    {
+      // a group's place among them: each of its threads counts a quarter
+      const int i = tid >> 2;
+      const uint64_t k = sm.group[i];
       int r = 0;
-      for (int j = 0; j < kLpGroups; ++j) r += sm.group[j] > k || (sm.group[j] == k && j < tid);
-      if (r < n) sm.hot[r] = tid;
-      if (r == n - 1) sm.bound = k;
+#pragma unroll
+      for (int j = (tid & 3); j < kLpGroups; j += 4) r += sm.group[j] > k || (sm.group[j] == k && j < i);
+      r += __shfl_xor_sync(0xffffffffu, r, 1);
+      r += __shfl_xor_sync(0xffffffffu, r, 2);
+      if ((tid & 3) == 0) {
+        if (r < n) sm.hot[r] = i;
+        if (r == n - 1) sm.bound = k;
+      }
     }
     __syncthreads();
     const uint64_t bound = sm.bound;
@@ -302,7 +323,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
     __syncthreads();
     const int cnt = sm.ncand;
     if (cnt <= kLpCandidates) {
-      rank_keys(sm.cand, cnt, sm.top, n);
+      rank_keys(sm.cand, cnt, sm.top[0], n);
     } else {
       // More candidates than there is room for (a few threads' logits all above everyone else's): the largest key
       // below the last one, n times, over all of the piece.
@@ -331,44 +352,48 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
         if (lane == 0) sm.best[warp] = k;
         __syncthreads();
         for (int w = 0; w < kLpWarps; ++w) k = sm.best[w] > k ? sm.best[w] : k;
-        if (tid == 0) sm.top[r] = k;
+        if (tid == 0) sm.top[0][r] = k;
         if (k == 0) break;
         last = k;
       }
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kLpWarps; ++w) a = join(a, sm.warp[w]);
-    sm.parts[0] = a;
+  if (warp == 0) {
+    a = join_lanes(sm.warp[lane & (kLpWarps - 1)], kLpWarps);
+    if (lane == 0) sm.parts[0] = a;
   }
 
   // ------------------------------------------------------------ the cluster's
   if (cs > 1) {
     cluster_wait();
-    if (rank > 0) {
-      if (tid == 0) {
+    if (rank > 0 && warp == 0) {
+      if (lane == 0) {
         const uint32_t to = mapa_shared(smem_u32(&sm.parts[rank]), 0);
         st_shared_cluster_f32(to, a.m);
         st_shared_cluster_f32(to + 4, a.s);
         st_shared_cluster_f32(to + 8, a.d);
       }
-    }
-    if (tid < n) {
-      const uint32_t to = mapa_shared(smem_u32(&sm.all[rank * n + tid]), 0);
-      const uint64_t k = sm.top[tid];
-      st_shared_cluster_s32(to, (int)(uint32_t)k);
-      st_shared_cluster_s32(to + 4, (int)(uint32_t)(k >> 32));
+      if (n > 0) {
+        const uint32_t to = mapa_shared(smem_u32(&sm.top[rank][lane]), 0);
+        const uint64_t k = sm.top[0][lane];
+        st_shared_cluster_s32(to, (int)(uint32_t)k);
+        st_shared_cluster_s32(to + 4, (int)(uint32_t)(k >> 32));
+      }
     }
     cluster_sync();
     if (rank > 0) return;
-    if (tid < n) sm.top[tid] = 0;
-    if (tid == 0) {
-      for (int r = 1; r < cs; ++r) a = join(a, sm.parts[r]);
-      sm.parts[0] = a;
+    if (warp == 0) {
+      a = join_lanes(sm.parts[lane & (cs - 1)], cs);
+      __syncwarp();
+      if (lane == 0) sm.parts[0] = a;
     }
-    __syncthreads();
-    rank_keys(sm.all, cs * n, sm.top, n);
+    // the ranks' lists, two by two
+    for (int o = 1; n > 0 && o < cs; o *= 2) {
+      const int r = 2 * o * warp;
+      if (r < cs) sm.top[r][lane] = merge_lists(sm.top[r][lane], sm.top[r + o][31 - lane], lane);
+      __syncthreads();
+    }
   }
   __syncthreads();
 
@@ -392,7 +417,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
     }
   }
   if (tid < n) {
-    const uint64_t k = sm.top[tid];
+    const uint64_t k = sm.top[0][tid];
     const bool there = k != 0 && !bad;
     top_ids[(size_t)row * n + tid] = there ? key_token(k) : -1;
     top_logprobs[(size_t)row * n + tid] = bad ? NAN : !there || none ? -INFINITY : (key_value(k) - a.m) - log_s;
