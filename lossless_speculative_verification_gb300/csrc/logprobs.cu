@@ -5,12 +5,14 @@
 //   log p_t = x_t - m - log S,   entropy = log S - D / S
 //
 // One pass over the logits with the running maximum, S and D of every thread (rescaled where a maximum rises), bound
-// by their bytes: about five instructions a logit, one of them an exponential.  The n most likely tokens cost nothing
-// in that pass but the place of each thread's maximum: every four threads are a group, the n-th largest of the groups'
-// maxima is a bound that the n largest logits reach, and none but the n groups at or above it have any, so that a
-// second look at those groups' logits (out of L2) collects little more than n candidates, which are ranked by counting.
-// Values and tokens form one 64-bit key (larger value first, then the lower token), so that equal logits, which bf16
-// makes frequent, are no special case.
+// by their bytes: about five instructions a logit, one of them an exponential.
+//
+// The n most likely tokens come of the same pass.  Values and tokens form one 64-bit key (larger value first, then the
+// lower token), so that equal logits, which bf16 makes frequent, are no special case.  They lie in the n vectors (16
+// bytes of logits) of the largest maxima, so that vectors are collected, by keys of their maxima and places.  Of the
+// first logits of every thread, 64 groups of threads give a bound, the n-th largest of their maxima, which n vectors
+// reach and few others; where many have come all the same, the n-th largest of them is the new bound.  At the end the
+// vectors, some dozens, are ranked by counting, and the logits of the first n of them, from the bound on, once more.
 //
 // A row is one CTA, or a cluster of up to 16 where there are few rows: its CTAs take a piece each, and rank 0 joins
 // their sums and ranks their candidates, through distributed shared memory, in a fixed order.
@@ -33,7 +35,9 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpGroups = kLpThreads / 4;
 constexpr int kLpBatch = 4;        // 16-byte vectors a thread takes at once
 constexpr int kLpMaxTop = 32;      // most alternatives
-constexpr int kLpCandidates = 1024;
+static_assert(kLpBatch == 4, "max_of");
+constexpr int kLpCandidates = 1024;  // room for the vectors that are collected
+constexpr int kLpMany = 256;         // so many, and the bound rises
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpMinPiece = kLpThreads * 16;  // bytes of a CTA's piece of a row: a vector a thread
 static_assert(kLpMaxTop <= kLpGroups && kLpMaxTop == 32 && kLpMaxCluster <= 2 * kLpWarps && kLpWarps <= 32, "lists");
@@ -69,20 +73,14 @@ __device__ __forceinline__ void move_to(Part& a, float m) {
   }
   a.m = m;
 }
-__device__ __forceinline__ Part join(Part a, Part b) {
-  const float m = max_nan(a.m, b.m);
-  move_to(a, m);
-  move_to(b, m);
-  return Part{m, a.s + b.s, a.d + b.d};
-}
-// The sums of `width` lanes (a power of two), in each of them.
+// The sums of `width` lanes (a power of two), in each of them: their maximum first, then every lane's share of it.
 __device__ __forceinline__ Part join_lanes(Part a, int width) {
+  float m = a.m;
+  for (int o = width / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  move_to(a, m);
   for (int o = width / 2; o > 0; o >>= 1) {
-    Part b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.d = __shfl_xor_sync(0xffffffffu, a.d, o);
-    a = join(a, b);
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+    a.d += __shfl_xor_sync(0xffffffffu, a.d, o);
   }
   return a;
 }
@@ -104,15 +102,17 @@ struct Vec<bf16> {
     const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
+  typedef __nv_bfloat162 Two;
+  static __device__ __forceinline__ Two two_max(const uint4& v) {
+    const Two* t = reinterpret_cast<const Two*>(&v);
+    return __hmax2_nan(__hmax2_nan(t[0], t[1]), __hmax2_nan(t[2], t[3]));
+  }
+  static __device__ __forceinline__ float max_of(const uint4& v) {
+    const Two m = two_max(v);
+    return max_nan(__low2float(m), __high2float(m));
+  }
   static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpBatch]) {
-    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
-#pragma unroll
-    for (int i = 0; i < kLpBatch; ++i) {
-      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].x));
-      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].y));
-      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].z));
-      m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].w));
-    }
+    const Two m = __hmax2_nan(__hmax2_nan(two_max(v[0]), two_max(v[1])), __hmax2_nan(two_max(v[2]), two_max(v[3])));
     return max_nan(__low2float(m), __high2float(m));
   }
   static __device__ __forceinline__ float get(const bf16* p) { return __bfloat162float(*p); }
@@ -125,13 +125,11 @@ struct Vec<float> {
     return i == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y))
                   : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
+  static __device__ __forceinline__ float max_of(const uint4& v) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
   static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpBatch]) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kLpBatch; ++i)
-      m = max_nan(max_nan(max_nan(m, __uint_as_float(v[i].x)), max_nan(__uint_as_float(v[i].y), __uint_as_float(v[i].z))),
-                  __uint_as_float(v[i].w));
-    return m;
+    return max_nan(max_nan(max_of(v[0]), max_of(v[1])), max_nan(max_of(v[2]), max_of(v[3])));
   }
   static __device__ __forceinline__ float get(const float* p) { return *p; }
 };
@@ -143,7 +141,6 @@ struct LpSmem {
   Part parts[kLpMaxCluster];                // rank 0's: every rank's sums
   Part warp[kLpWarps];
   uint64_t best[kLpWarps];
-  int hot[kLpMaxTop];
   uint64_t bound;
   int ncand;
 };
@@ -160,14 +157,18 @@ __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b_reversed,
 }
 
 // The n largest of `cnt` different keys, in order, to dst (0 where there are fewer): each key's place is the number of
-// larger ones.
+// larger ones, counted by 8, 4, 2 or 1 threads.
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int cnt, uint64_t* dst, int n) {
-  for (int i = threadIdx.x; i < cnt; i += kLpThreads) {
-    const uint64_t k = keys[i];
-    if (k == 0) continue;
+  const int by = cnt <= 32 ? 8 : cnt <= 64 ? 4 : cnt <= 128 ? 2 : 1;
+  const int each = kLpThreads / by, part = threadIdx.x % by;
+  for (int i0 = 0; i0 < cnt; i0 += each) {
+    const int i = i0 + threadIdx.x / by;
+    const uint64_t k = i < cnt ? keys[i] : 0;
     int r = 0;
-    for (int j = 0; j < cnt; ++j) r += keys[j] > k;
-    if (r < n) dst[r] = k;
+#pragma unroll 4
+    for (int j = part; j < cnt; j += by) r += keys[j] > k;
+    for (int o = 1; o < by; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if (part == 0 && k != 0 && r < n) dst[r] = k;
   }
 }
 
@@ -190,25 +191,46 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
   const T* xv = x + head;
   const int k0 = (int)((long long)nv * rank / cs), k1 = (int)((long long)nv * (rank + 1) / cs);
 
-  // ------------------------------------------------------------ one pass: sums, and where the maximum is
+  // what the end needs of global memory comes meanwhile
+  int token = -1;
+  float at_token = 0.0f;
+  if (logprob && rank == 0 && tid == 0) {
+    token = tokens[row];
+    if (token >= 0 && token < V) at_token = Vec<T>::get(x + token);
+  }
+
+  // ------------------------------------------------------------ one pass: sums, and the candidates
   Part a = {-INFINITY, 0.0f, 0.0f};
-  int at = k0 + tid;  // first vector of the batch with the first maximum
   uint4 v[kLpBatch];
   auto load = [&](int k) {
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i) {
       const int q = k + i * kLpThreads;
-      v[i] = q < k1 ? ld_plain128(xv + (size_t)q * N)
+      v[i] = q < k1 ? ld_stream128(xv + (size_t)q * N)
                     : make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
     }
   };
+  load(k0 + tid);
+  if (tid == 0) {
+    sm.ncand = 0;
+    sm.bound = 0;
+  }
+  if (tid < kLpMaxTop) sm.top[0][tid] = 0;
+  uint64_t bound = 0;  // the key of a vector: its largest logit, then its place
+  float bv = -INFINITY;
+  auto set_bound = [&]() {
+    bound = sm.bound;
+    bv = bound ? key_value(bound) : -INFINITY;
+  };
   float2 s2 = make_float2(0.f, 0.f), d2 = s2;
-  if (k0 + tid < k1) load(k0 + tid);
-  for (int k = k0 + tid; k < k1; k += kLpBatch * kLpThreads) {
+  const int batches = (k1 - k0 + kLpBatch * kLpThreads - 1) / (kLpBatch * kLpThreads);
+#pragma unroll 1
+  for (int b = 0; b < batches; ++b) {
+    const int k = k0 + tid + b * (kLpBatch * kLpThreads);
     uint4 u[kLpBatch];
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i) u[i] = v[i];
-    if (k + kLpBatch * kLpThreads < k1) load(k + kLpBatch * kLpThreads);
+    if (b + 1 < batches) load(k + kLpBatch * kLpThreads);
     const float bm = Vec<T>::max_of(u);
     if (!(bm <= a.m)) {
       a.s = s2.x + s2.y;
@@ -216,27 +238,84 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
       move_to(a, bm);
       s2 = make_float2(a.s, 0.f);
       d2 = make_float2(a.d, 0.f);
-      at = k;
     }
-    if (a.m == -INFINITY) continue;  // nothing but -inf so far
-    const float2 neg = make_float2(-a.m, -a.m);
+    if (a.m != -INFINITY) {  // else nothing but -inf so far
+      const float2 neg = make_float2(-a.m, -a.m);
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i)
+      for (int i = 0; i < kLpBatch; ++i)
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        float2 t = add2(Vec<T>::two(u[i], j), neg);
-        // -inf counts as e^-1000 = 0, so that it adds 0 and not 0 * inf
-        t.x = max_nan(t.x, -1000.0f);
-        t.y = max_nan(t.y, -1000.0f);
-        const float2 l = mul2(t, make_float2(kLog2e, kLog2e));
-        const float2 e = make_float2(ex2_ftz(l.x), ex2_ftz(l.y));
-        s2 = add2(s2, e);
-        d2 = fma2(t, e, d2);
+        for (int j = 0; j < N / 2; ++j) {
+          float2 t = add2(Vec<T>::two(u[i], j), neg);
+          // -inf counts as e^-1000 = 0, so that it adds 0 and not 0 * inf
+          t.x = max_nan(t.x, -1000.0f);
+          t.y = max_nan(t.y, -1000.0f);
+          const float2 l = mul2(t, make_float2(kLog2e, kLog2e));
+          const float2 e = make_float2(ex2_ftz(l.x), ex2_ftz(l.y));
+          s2 = add2(s2, e);
+          d2 = fma2(t, e, d2);
+        }
+    }
+    if (n == 0) continue;
+    if (b == 0) {
+      // the first bound: each thread's vector of the largest maximum, and the groups' places among them
+      uint64_t key = 0;
+      if (k < k1 && !isnan(bm)) {
+        int first = 0;
+#pragma unroll
+        for (int i = kLpBatch - 1; i > 0; --i)
+          if (Vec<T>::max_of(u[i]) == bm) first = i;
+        if (Vec<T>::max_of(u[0]) == bm) first = 0;
+        key = lp_key(bm, k + first * kLpThreads);
       }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+        key = other > key ? other : key;
+      }
+      if ((tid & 3) == 0) sm.group[tid >> 2] = key;
+      __syncthreads();
+      int r = 0;
+#pragma unroll
+      for (int j = 0; j < kLpGroups; j += 4) {
+        const uint64_t other = sm.group[j + (tid & 3)];
+        r += other > key || (other == key && j + (tid & 3) < (tid >> 2));
+      }
+      r += __shfl_xor_sync(0xffffffffu, r, 1);
+      r += __shfl_xor_sync(0xffffffffu, r, 2);
+      if ((tid & 3) == 0 && r == n - 1) sm.bound = key;
+      __syncthreads();
+      set_bound();
+    }
+    if (bm >= bv) {
+#pragma unroll
+      for (int i = 0; i < kLpBatch; ++i) {
+        const int q = k + i * kLpThreads;
+        const float vm = Vec<T>::max_of(u[i]);
+        if (q >= k1 || vm < bv) continue;
+        const uint64_t key = lp_key(vm, q);
+        if (key < bound) continue;
+        const int c = atomicAdd(&sm.ncand, 1);
+        if (c < kLpCandidates) sm.cand[c] = key;
+      }
+    }
+    if ((b & 3) == 3 && b + 1 < batches) {
+      __syncthreads();
+      const int cnt = sm.ncand;
+      if (cnt > kLpMany && cnt <= kLpCandidates) {
+        rank_keys(sm.cand, cnt, sm.group, n);
+        __syncthreads();
+        if (tid < n) sm.cand[tid] = sm.group[tid];
+        if (tid == 0) {
+          sm.ncand = n;
+          sm.bound = sm.group[n - 1];
+        }
+      }
+      __syncthreads();
+      set_bound();
+    }
   }
   a.s = s2.x + s2.y;
   a.d = d2.x + d2.y;
-  const float vmax = a.m;
 
   // the elements outside whole vectors
   int edge = -1;
@@ -245,87 +324,31 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
   const float ex = edge >= 0 ? Vec<T>::get(x + edge) : -INFINITY;
   if (edge >= 0) add_one(a, ex);
 
-  // ------------------------------------------------------------ the CTA's sums
   a = join_lanes(a, 32);
   if (lane == 0) sm.warp[warp] = a;
-  if (tid == 0) {
-    sm.ncand = 0;
-    sm.bound = 0;
-  }
-  if (tid < kLpMaxTop) {
-    sm.top[0][tid] = 0;
-    sm.hot[tid] = -1;
-  }
-
-  // ------------------------------------------------------------ the CTA's largest
   if (n > 0) {
-    uint64_t key = 0;
-    if (k0 + tid < k1 && !isnan(vmax)) {
-      // the first element of the batch that equals the maximum
-      for (int i = 0; i < kLpBatch && key == 0; ++i) {
-        const int q = at + i * kLpThreads;
-        if (q >= k1) break;
-        const uint4 w = ld_plain128(xv + (size_t)q * N);
-#pragma unroll
-        for (int j = N / 2 - 1; j >= 0; --j) {
-          const float2 f = Vec<T>::two(w, j);
-          if (f.y == vmax) key = lp_key(f.y, head + q * N + 2 * j + 1);
-          if (f.x == vmax) key = lp_key(f.x, head + q * N + 2 * j);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-      key = other > key ? other : key;
-    }
-    if ((tid & 3) == 0) sm.group[tid >> 2] = key;
-    __syncthreads();
-    {
-      // a group's place among them: each of its threads counts a quarter
-      const int i = tid >> 2;
-      const uint64_t k = sm.group[i];
-      int r = 0;
-#pragma unroll
-      for (int j = (tid & 3); j < kLpGroups; j += 4) r += sm.group[j] > k || (sm.group[j] == k && j < i);
-      r += __shfl_xor_sync(0xffffffffu, r, 1);
-      r += __shfl_xor_sync(0xffffffffu, r, 2);
-      if ((tid & 3) == 0) {
-        if (r < n) sm.hot[r] = i;
-        if (r == n - 1) sm.bound = k;
-      }
-    }
-    __syncthreads();
-    const uint64_t bound = sm.bound;
-    const float bv = bound ? key_value(bound) : -INFINITY;
-    auto offer = [&](float f, int token) {
-      if (f < bv) return;
-      const uint64_t k = lp_key(f, token);
-      if (k < bound) return;
-      const int c = atomicAdd(&sm.ncand, 1);
-      if (c < kLpCandidates) sm.cand[c] = k;
-    };
-    if (edge >= 0) offer(ex, edge);
-    const int steps = (k1 - k0 + kLpThreads - 1) / kLpThreads;
-    for (int i = tid; i < n * 4 * steps; i += kLpThreads) {
-      // consecutive threads: the four threads of a group, then the groups, then the vectors
-      const int h = sm.hot[(i >> 2) % n];
-      const int q = k0 + (i >> 2) / n * kLpThreads + 4 * h + (i & 3);
-      if (h < 0 || q >= k1) continue;
-      const uint4 w = ld_plain128(xv + (size_t)q * N);
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        const float2 f = Vec<T>::two(w, j);
-        offer(f.x, head + q * N + 2 * j);
-        offer(f.y, head + q * N + 2 * j + 1);
-      }
-    }
     __syncthreads();
     const int cnt = sm.ncand;
     if (cnt <= kLpCandidates) {
-      rank_keys(sm.cand, cnt, sm.top[0], n);
+      rank_keys(sm.cand, cnt, sm.group, n);  // the n vectors
+      __syncthreads();
+      // their logits, a thread each, and those outside vectors
+      const uint64_t least = cnt >= n ? sm.group[n - 1] : 0;
+      const float lv = least ? key_value(least) : -INFINITY;
+      if (tid == 0) sm.ncand = 0;
+      __syncthreads();
+      auto offer = [&](float f, int t) {
+        if (!(f < lv)) sm.cand[atomicAdd(&sm.ncand, 1)] = lp_key(f, t);
+      };
+      if (tid < min(n, cnt) * N) {
+        const int t = head + key_token(sm.group[tid / N]) * N + tid % N;
+        offer(Vec<T>::get(x + t), t);
+      }
+      if (edge >= 0) offer(ex, edge);
+      __syncthreads();
+      rank_keys(sm.cand, sm.ncand, sm.top[0], n);
     } else {
-      // More candidates than there is room for (a few threads' logits all above everyone else's): the largest key
+      // More vectors than there is room for (logits that rise along the row): the largest key
       // below the last one, n times, over all of the piece.
       uint64_t last = ~0ull;
       for (int r = 0; r < n; ++r) {
@@ -405,13 +428,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
   if (tid == 0) {
     if (entropy) entropy[row] = bad ? NAN : none ? 0.0f : log_s - a.d / a.s;
     if (logprob) {
-      const int t = tokens[row];
       float p = 0.0f;  // -1: no token
-      if (t < -1 || t >= V) {
+      if (token < -1 || token >= V) {
         set_error(err, kErrDeviceIndex);
         p = NAN;
-      } else if (t >= 0) {
-        p = bad ? NAN : none ? -INFINITY : (Vec<T>::get(x + t) - a.m) - log_s;
+      } else if (token >= 0) {
+        p = bad ? NAN : none ? -INFINITY : (at_token - a.m) - log_s;
       }
       logprob[row] = p;
     }
