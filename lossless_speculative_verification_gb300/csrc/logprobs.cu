@@ -30,17 +30,17 @@
 namespace lsv {
 namespace {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpGroups = kLpThreads / 4;
+constexpr int kLpWide = 1024, kLpMiddle = 512, kLpNarrow = 256;  // threads a CTA
+constexpr int kLpGroups = 64;
 constexpr int kLpBatch = 4;        // 16-byte vectors a thread takes at once
 constexpr int kLpMaxTop = 32;      // most alternatives
 static_assert(kLpBatch == 4, "max_of");
 constexpr int kLpCandidates = 1024;  // room for the vectors that are collected
 constexpr int kLpMany = 256;         // so many, and the bound rises
 constexpr int kLpMaxCluster = 16;
-constexpr int kLpMinPiece = kLpThreads * 16;  // bytes of a CTA's piece of a row: a vector a thread
-static_assert(kLpMaxTop <= kLpGroups && kLpMaxTop == 32 && kLpMaxCluster <= 2 * kLpWarps && kLpWarps <= 32, "lists");
+constexpr int kLpFew = 128;          // vectors whose logits are looked at without ranking them first
+static_assert(kLpWide <= kLpCandidates, "the threads' largest");
+static_assert(kLpMaxTop <= kLpGroups && kLpMaxTop == 32 && kLpMaxCluster <= 2 * kLpNarrow / 32, "lists");
 
 // Larger value first, then the lower token; never 0.  -0 and 0 are equal.
 __device__ __forceinline__ uint64_t lp_key(float x, int v) {
@@ -134,15 +134,16 @@ struct Vec<float> {
   static __device__ __forceinline__ float get(const float* p) { return *p; }
 };
 
-struct LpSmem {
-  uint64_t cand[kLpCandidates];
+struct __align__(16) LpSmem {
+  uint64_t cand[kLpCandidates];  // at first the threads' largest vectors
+  uint64_t last[kLpFew * 8 + 16];
   uint64_t group[kLpGroups];
   uint64_t top[kLpMaxCluster][kLpMaxTop];   // the CTA's largest in order, 0 behind them; rank 0's: every rank's
   Part parts[kLpMaxCluster];                // rank 0's: every rank's sums
-  Part warp[kLpWarps];
-  uint64_t best[kLpWarps];
+  Part warp[kLpWide / 32];
+  uint64_t best[kLpWide / 32];
   uint64_t bound;
-  int ncand;
+  int ncand, nlast;  // vectors; logits at the end
 };
 
 // Two lists of 32 keys in falling order, one a lane and the other from its end: the 32 largest, in falling order.
@@ -157,26 +158,32 @@ __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b_reversed,
 }
 
 // The n largest of `cnt` different keys, in order, to dst (0 where there are fewer): each key's place is the number of
-// larger ones, counted by 8, 4, 2 or 1 threads.
+// larger ones, counted by 1 to 32 threads.
+template <int THREADS>
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int cnt, uint64_t* dst, int n) {
-  const int by = cnt <= 32 ? 8 : cnt <= 64 ? 4 : cnt <= 128 ? 2 : 1;
-  const int each = kLpThreads / by, part = threadIdx.x % by;
+  int by = 32;
+  while (by > 1 && by * cnt > THREADS) by >>= 1;
+  const int each = THREADS / by, part = threadIdx.x & (by - 1);
   for (int i0 = 0; i0 < cnt; i0 += each) {
-    const int i = i0 + threadIdx.x / by;
+    const int i = i0 + (int)threadIdx.x / by;
     const uint64_t k = i < cnt ? keys[i] : 0;
     int r = 0;
 #pragma unroll 4
-    for (int j = part; j < cnt; j += by) r += keys[j] > k;
+    for (int j = 2 * part; j < cnt; j += 2 * by) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(keys + j);
+      r += (two.x > k) + (j + 1 < cnt && two.y > k);
+    }
     for (int o = 1; o < by; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (part == 0 && k != 0 && r < n) dst[r] = k;
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits, const int32_t* tokens, int V, int n,
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const T* logits, const int32_t* tokens, int V, int n,
                                                                  int cs, float* logprob, float* entropy, int32_t* top_ids,
                                                                  float* top_logprobs, int* err) {
   constexpr int N = Vec<T>::N;
+  constexpr int kWarps = THREADS / 32, kInGroup = THREADS / kLpGroups;
   __shared__ LpSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / cs, rank = blockIdx.x - row * cs;
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
   auto load = [&](int k) {
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i) {
-      const int q = k + i * kLpThreads;
+      const int q = k + i * THREADS;
       v[i] = q < k1 ? ld_stream128(xv + (size_t)q * N)
                     : make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
     }
@@ -213,6 +220,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
   load(k0 + tid);
   if (tid == 0) {
     sm.ncand = 0;
+    sm.nlast = 0;
     sm.bound = 0;
   }
   if (tid < kLpMaxTop) sm.top[0][tid] = 0;
@@ -223,14 +231,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
     bv = bound ? key_value(bound) : -INFINITY;
   };
   float2 s2 = make_float2(0.f, 0.f), d2 = s2;
-  const int batches = (k1 - k0 + kLpBatch * kLpThreads - 1) / (kLpBatch * kLpThreads);
+  const int batches = (k1 - k0 + kLpBatch * THREADS - 1) / (kLpBatch * THREADS);
 #pragma unroll 1
   for (int b = 0; b < batches; ++b) {
-    const int k = k0 + tid + b * (kLpBatch * kLpThreads);
+    const int k = k0 + tid + b * (kLpBatch * THREADS);
     uint4 u[kLpBatch];
 #pragma unroll
     for (int i = 0; i < kLpBatch; ++i) u[i] = v[i];
-    if (b + 1 < batches) load(k + kLpBatch * kLpThreads);
+    if (b + 1 < batches) load(k + kLpBatch * THREADS);
     const float bm = Vec<T>::max_of(u);
     if (!(bm <= a.m)) {
       a.s = s2.x + s2.y;
@@ -265,31 +273,33 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
         for (int i = kLpBatch - 1; i > 0; --i)
           if (Vec<T>::max_of(u[i]) == bm) first = i;
         if (Vec<T>::max_of(u[0]) == bm) first = 0;
-        key = lp_key(bm, k + first * kLpThreads);
+        key = lp_key(bm, k + first * THREADS);
       }
+      // group g: the threads g, g + 64, .., so that a short row makes as many groups as it has vectors
+      sm.cand[tid] = key;
+      __syncthreads();
+      const int mine = tid / kInGroup, part = tid % kInGroup;
+      key = sm.cand[part * kLpGroups + mine];
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
+      for (int o = 1; o < kInGroup; o <<= 1) {
         const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
         key = other > key ? other : key;
       }
-      if ((tid & 3) == 0) sm.group[tid >> 2] = key;
+      if (part == 0) sm.group[mine] = key;
       __syncthreads();
       int r = 0;
 #pragma unroll
-      for (int j = 0; j < kLpGroups; j += 4) {
-        const uint64_t other = sm.group[j + (tid & 3)];
-        r += other > key || (other == key && j + (tid & 3) < (tid >> 2));
-      }
-      r += __shfl_xor_sync(0xffffffffu, r, 1);
-      r += __shfl_xor_sync(0xffffffffu, r, 2);
-      if ((tid & 3) == 0 && r == n - 1) sm.bound = key;
+      for (int j = part; j < kLpGroups; j += kInGroup) r += sm.group[j] > key || (sm.group[j] == key && j < mine);
+#pragma unroll
+      for (int o = 1; o < kInGroup; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+      if (part == 0 && r == n - 1) sm.bound = key;
       __syncthreads();
       set_bound();
     }
     if (bm >= bv) {
 #pragma unroll
       for (int i = 0; i < kLpBatch; ++i) {
-        const int q = k + i * kLpThreads;
+        const int q = k + i * THREADS;
         const float vm = Vec<T>::max_of(u[i]);
         if (q >= k1 || vm < bv) continue;
         const uint64_t key = lp_key(vm, q);
@@ -302,7 +312,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
       __syncthreads();
       const int cnt = sm.ncand;
       if (cnt > kLpMany && cnt <= kLpCandidates) {
-        rank_keys(sm.cand, cnt, sm.group, n);
+        rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
         __syncthreads();
         if (tid < n) sm.cand[tid] = sm.group[tid];
         if (tid == 0) {
@@ -330,23 +340,26 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
     __syncthreads();
     const int cnt = sm.ncand;
     if (cnt <= kLpCandidates) {
-      rank_keys(sm.cand, cnt, sm.group, n);  // the n vectors
-      __syncthreads();
-      // their logits, a thread each, and those outside vectors
-      const uint64_t least = cnt >= n ? sm.group[n - 1] : 0;
-      const float lv = least ? key_value(least) : -INFINITY;
-      if (tid == 0) sm.ncand = 0;
-      __syncthreads();
+      // The logits of the vectors, of the first n of them where they are many, from the bound on.
+      const uint64_t* from = sm.cand;
+      int vectors = cnt;
+      if (cnt > kLpFew) {
+        rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
+        __syncthreads();
+        from = sm.group;
+        vectors = n;
+        bv = key_value(sm.group[n - 1]);
+      }
       auto offer = [&](float f, int t) {
-        if (!(f < lv)) sm.cand[atomicAdd(&sm.ncand, 1)] = lp_key(f, t);
+        if (!(f < bv)) sm.last[atomicAdd(&sm.nlast, 1)] = lp_key(f, t);
       };
-      if (tid < min(n, cnt) * N) {
-        const int t = head + key_token(sm.group[tid / N]) * N + tid % N;
+      for (int i = tid; i < vectors * N; i += THREADS) {
+        const int t = head + key_token(from[i / N]) * N + i % N;
         offer(Vec<T>::get(x + t), t);
       }
       if (edge >= 0) offer(ex, edge);
       __syncthreads();
-      rank_keys(sm.cand, sm.ncand, sm.top[0], n);
+      rank_keys<THREADS>(sm.last, sm.nlast, sm.top[0], n);
     } else {
       // More vectors than there is room for (logits that rise along the row): the largest key
       // below the last one, n times, over all of the piece.
@@ -357,7 +370,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
           const uint64_t e = lp_key(ex, edge);
           if (e < last) k = e;
         }
-        for (int q = k0 + tid; q < k1; q += kLpThreads) {
+        for (int q = k0 + tid; q < k1; q += THREADS) {
           const uint4 w = ld_plain128(xv + (size_t)q * N);
 #pragma unroll
           for (int j = 0; j < N; ++j) {
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
         __syncthreads();
         if (lane == 0) sm.best[warp] = k;
         __syncthreads();
-        for (int w = 0; w < kLpWarps; ++w) k = sm.best[w] > k ? sm.best[w] : k;
+        for (int w = 0; w < kWarps; ++w) k = sm.best[w] > k ? sm.best[w] : k;
         if (tid == 0) sm.top[0][r] = k;
         if (k == 0) break;
         last = k;
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
   }
   __syncthreads();
   if (warp == 0) {
-    a = join_lanes(sm.warp[lane & (kLpWarps - 1)], kLpWarps);
+    a = join_lanes(sm.warp[lane & (kWarps - 1)], kWarps);
     if (lane == 0) sm.parts[0] = a;
   }
 
@@ -449,21 +462,28 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const T* logits
 template <typename T>
 cudaError_t launch_logprobs(const T* logits, const int32_t* tokens, int R, int V, int n, float* logprob, float* entropy,
                             int32_t* top_ids, float* top_logprobs, const DeviceCtx& dc, cudaStream_t s) {
-  // As many CTAs a row as are on the GPU at once (four an SM), each with a vector a thread at least.
+  // Many rows: narrow CTAs, four an SM; up to two rows an SM, so many that they fill it; few rows (a quarter of the SMs
+  // at most): narrow ones again, as many a row (a cluster) as are on the GPU at once, each with a vector a thread at
+  // least.  Of 129280 bf16 logits and 20 tokens: one row 5.7 us (a cluster of 8 wide CTAs 7.7), 16 rows 7.5 (13.9), 128
+  // rows 13.9 (clusters of 4 narrow ones 17.1), 300 rows 27 (narrow 36).  Rows of one batch gain nothing from threads.
+  const long long bytes = (long long)V * (long long)sizeof(T);
+  const bool few = 4ll * R <= dc.num_sms, wide = !few && R <= dc.num_sms;
+  const bool narrow = few || R > 2 * dc.num_sms || bytes <= kLpNarrow * kLpBatch * 16;
+  const int threads = narrow ? kLpNarrow : wide ? kLpWide : kLpMiddle;
   int cs = 1;
-  while (cs < kLpMaxCluster && (long long)R * cs * 2 <= 4ll * dc.num_sms &&
-         (long long)V * (long long)sizeof(T) >= 2ll * cs * kLpMinPiece)
+  while (cs < kLpMaxCluster && (long long)R * cs * 2 * threads <= 1024ll * dc.num_sms && bytes >= 2ll * cs * threads * 16)
     cs *= 2;
-  auto* kernel = logprobs_kernel<T>;
-  static std::atomic<bool> wide[64];  // clusters of 16 allowed on the device
-  if (cs > 8 && !wide[dc.device].load()) {
+  auto* kernel = narrow ? logprobs_kernel<T, kLpNarrow>
+                        : wide ? logprobs_kernel<T, kLpWide> : logprobs_kernel<T, kLpMiddle>;
+  static std::atomic<bool> asked[64];  // clusters of 16 allowed on the device
+  if (cs > 8 && !asked[dc.device].load()) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    wide[dc.device].store(true);
+    asked[dc.device].store(true);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)R * cs));
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
