@@ -20,7 +20,7 @@ namespace lsv {
 namespace {
 
 constexpr int kQ8Slot = 256;     // columns that a warp takes at once
-constexpr int kQ8Vecs = 8;       // slots a warp holds at most (many rows)
+constexpr int kQ8Vecs = 2;       // slots a warp holds at most
 constexpr int kQ8MaxWarps = 32;  // warps a row
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -73,7 +73,7 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
 // to 32 bits left out, from the residual of m r^2), so that h is off by little more than its own rounding: codes
 // next to a tie then fall as the formula has them but for 2^-24 of the values next to it.
 template <int VECS, bool NORM>
-__global__ void __launch_bounds__(VECS == 1 ? 1024 : 256) q8_rows_kernel(const bf16* x, const bf16* __restrict__ y, bf16* x_out,
+__global__ void __launch_bounds__(1024) q8_rows_kernel(const bf16* x, const bf16* __restrict__ y, bf16* x_out,
                                                        const bf16* __restrict__ gain, uint8_t* __restrict__ codes,
                                                        float* __restrict__ scales, int T, int H, int wpr, int rows,
                                                        float eps) {
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256) q8_weight_kernel(const bf16* __restrict__
 }
 
 // ------------------------------------------------------------------------------------------------ back
-constexpr int kQ8ReadPieces = 4;  // 16 codes a piece, four pieces a thread
+constexpr int kQ8ReadPieces = 4;  // 8 codes a piece (a 16-byte store), four pieces a thread
 
 __device__ __forceinline__ uint32_t values2(uint32_t two, float s) {
   uint32_t h;
@@ -222,46 +222,40 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const uint8_t* __restrict_
                                                       int R, int C, int by) {
   pdl_wait();
   pdl_trigger();
-  const int per = C / 16, G = (C + kQ8Group - 1) / kQ8Group;
+  const int per = C / 8, G = (C + kQ8Group - 1) / kQ8Group;
   const long long p0 = (long long)blockIdx.x * (256 * kQ8ReadPieces);
   const int row0 = (int)(p0 / per);
   const int col0 = (int)(p0 - (long long)row0 * per);
-  uint4 v[kQ8ReadPieces];
+  uint2 v[kQ8ReadPieces];
   float s[kQ8ReadPieces];
   size_t at[kQ8ReadPieces];
   bool live[kQ8ReadPieces];
 #pragma unroll
   for (int i = 0; i < kQ8ReadPieces; ++i) {
     const int c = col0 + (int)threadIdx.x + 256 * i;
-    const int dr = c / per, row = row0 + dr, col = (c - dr * per) * 16;
+    const int dr = c / per, row = row0 + dr, col = (c - dr * per) * 8;
     live[i] = row < R;
     at[i] = (size_t)row * C + col;
     if (!live[i]) continue;
-    v[i] = ld_stream128(codes + at[i]);
+    v[i] = ld_stream64(codes + at[i]);
     s[i] = ld_plain_f32(scales + (size_t)(row / by) * G + col / kQ8Group);
   }
 #pragma unroll
   for (int i = 0; i < kQ8ReadPieces; ++i) {
     if (!live[i]) continue;
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t o[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      o[2 * j] = values2(w[j] & 0xFFFFu, s[i]);
-      o[2 * j + 1] = values2(w[j] >> 16, s[i]);
-    }
-    uint4* d = reinterpret_cast<uint4*>(out + at[i]);
-    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(out + at[i]) =
+        make_uint4(values2(v[i].x & 0xFFFFu, s[i]), values2(v[i].x >> 16, s[i]), values2(v[i].y & 0xFFFFu, s[i]),
+                   values2(v[i].y >> 16, s[i]));
   }
 }
 
 cudaError_t launch_rows(bool norm, const bf16* x, const bf16* y, bf16* x_out, const bf16* gain, uint8_t* codes,
                         float* scales, int T, int H, float eps, const DeviceCtx& dc, cudaStream_t s) {
   const int slots = (H + kQ8Slot - 1) / kQ8Slot;
-  // A slot a warp where all warps are on the GPU at once (64 an SM): nothing waits for a second load.  More rows
-  // than that: up to eight slots a warp, all in flight, and fewer barriers.
-  const bool wide = (long long)T * slots > 64ll * dc.num_sms || slots > kQ8MaxWarps;
+  // One slot a warp for short rows, two for longer ones, which then have fewer warps to meet: the norm of 9760 x 1280
+  // takes 18.1 us with one and 18.5 with two, of 1500 x 7168 18.7 and 18.0; quantising 9760 x 1280 alone, where no warp
+  // waits for another, 10.7 and 9.0, and 60000 x 208, a slot a row, 10.7 and 11.4.
+  const bool wide = slots > (norm ? 8 : 1);
   const int vecs = wide ? kQ8Vecs : 1;
   const int wpr = (slots + vecs - 1) / vecs;
   const int rows = wpr >= 8 ? 1 : 8 / wpr;
@@ -341,7 +335,7 @@ lsv_status dequantize_q8(const void* codes, const float* scales, int32_t R, int3
   if (st != LSV_OK || R == 0) return st;
   if (!codes || !scales || !out) return LSV_ERR_INVALID_ARG;
   if (!aligned({codes, scales, out})) return LSV_ERR_MISALIGNED;
-  const long long pieces = (long long)R * (C / 16), per = 256 * kQ8ReadPieces;
+  const long long pieces = (long long)R * (C / 8), per = 256 * kQ8ReadPieces;
   return launch_pdl(q8_read_kernel, dim3((unsigned)((pieces + per - 1) / per)), dim3(256), 0,
                     reinterpret_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(codes), scales,
                     static_cast<bf16*>(out), R, C, rows_per_scale) == cudaSuccess
