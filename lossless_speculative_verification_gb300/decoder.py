@@ -27,6 +27,13 @@ together (spec_pages_resize, spec_pages_fork, spec_pages_compact).  Where the po
 has too few free pages for a reserve(), the pages that a pass would write may still be
 other sequences' too, so verify() appends nothing until a reserve() succeeds: it looks
 at that call's counts on the device, also inside one graph with it.
+
+With weights="q8" the projections and the output layer are held in 8 bits: the norms
+before them write 8-bit rows (rmsnorm_residual_q8), the attention's output is quantised
+(quantize_q8_rows), the products are dense_matmul_q8, and the greedy tokens come from the
+output layer's logits (spec_verify_accept).  The experts and the draft block stay as they
+are.  verify(logprobs=n) adds the committed tokens' log probabilities, the entropies and
+the n most likely tokens of every position (spec_logprobs).
 """
 from __future__ import annotations
 
@@ -45,14 +52,18 @@ def _dev(bits, device):
 class Decoder:
     """Device weights and per-layer key/value caches of a synthetic decoder (synth.DecoderProblem):
     [B, L, nh, d] bf16, or with cache="q4" pages of `page` positions, `pages` of them (as many as B
-    sequences of L positions need unless given), all free at first.  verify() runs one verify pass
-    over Q positions per sequence, for the first tokens.shape[0] <= B sequences."""
+    sequences of L positions need unless given), all free at first.  weights="q8": projections and output
+    layer in 8 bits.  verify() runs one verify pass over Q positions per sequence, for the first
+    tokens.shape[0] <= B sequences."""
 
-    def __init__(self, prob, B: int, L: int, device="cuda", cache: str = "bf16", page: int = 64, pages: int | None = None):
+    def __init__(self, prob, B: int, L: int, device="cuda", cache: str = "bf16", page: int = 64, pages: int | None = None,
+                 weights: str = "bf16"):
         if cache not in ("bf16", "q4"):
             raise ValueError("cache must be 'bf16' or 'q4'")
+        if weights not in ("bf16", "q8"):
+            raise ValueError("weights must be 'bf16' or 'q8'")
         self.prob, self.B, self.L, self.device = prob, B, L, device
-        self.cache, self.page = cache, page
+        self.cache, self.page, self.weights = cache, page, weights
         d = prob.dims
         self.H, self.nh = d.H, prob.nh
         self.hd = d.H // prob.nh
@@ -62,6 +73,8 @@ class Decoder:
         self.layers = []
         for lw in prob.layers:
             t = {n: _dev(lw[n], device) for n in ("w_q", "w_k", "w_v", "w_o")}
+            if weights == "q8":
+                t = {n: api.quantize_q8_weight(w) for n, w in t.items()}
             t["moe"] = api.weights(*[_dev(lw[n], device) for n in ("w_router", "w_gate_up", "w_down", "ws_gate_up",
                                                                     "ws_down")])
             if cache == "bf16":
@@ -77,6 +90,7 @@ class Decoder:
             self.ref = torch.zeros(P, dtype=torch.int32, device=device)
             self.pws = api.spec_pages_workspace(B, M, P, device)
             self.room = torch.zeros(4, dtype=torch.int32, device=device)   # the last reserve()'s counts
+        self.vocab_q8 = api.quantize_q8_weight(self.w_vocab) if weights == "q8" else None
         dw = dict(prob.draft)
         dw["emb"], dw["w_vocab"] = prob.emb, prob.w_vocab
         self.draft_w = {n: (self.emb if n == "emb" else self.w_vocab if n == "w_vocab" else _dev(dw[n], device))
@@ -133,21 +147,36 @@ class Decoder:
                 b["none"], b["len"] = (torch.zeros(B, dtype=torch.int32, device=dev) for _ in range(2))
             else:
                 b["aws"] = api.spec_verify_attention_workspace(B, Q, self.L, self.nh, self.hd, dev)
-            b["lws"] = api.spec_verify_lmhead_workspace(B, Q - 1, self.V, H, dev)
+            if self.weights == "q8":
+                for n in ("hq", "aq"):   # 8-bit rows: the norm's, the attention's
+                    b[n] = (torch.zeros((T, H), dtype=torch.float8_e4m3fn, device=dev),
+                            torch.zeros(api.q8_scales_shape(T, H), device=dev))
+                b["lws"] = api.spec_verify_workspace(B, Q - 1, self.V, dev)
+            else:
+                b["lws"] = api.spec_verify_lmhead_workspace(B, Q - 1, self.V, H, dev)
             b["argmax"] = torch.zeros((B, Q), dtype=torch.int32, device=dev)
             b["alen"] = torch.zeros(B, dtype=torch.int32, device=dev)
             b["comm"] = torch.zeros((B, Q), dtype=torch.int32, device=dev)
             self._bufs[(B, Q)] = b
         return self._bufs[(B, Q)]
 
-    def verify(self, tokens, ctx_after, drafts):
+    def _logits(self, b):
+        """The pass's logits [B, Q, V], made when they are first asked for."""
+        if "logits" not in b:
+            b["logits"] = torch.empty((*b["argmax"].shape, self.V), dtype=torch.bfloat16, device=self.device)
+        return b["logits"]
+
+    def verify(self, tokens, ctx_after, drafts, logprobs: int | None = None):
         """One verify pass.  tokens [B, Q] int32: input 0 is each sequence's last committed token,
         inputs 1..Q-1 its drafts (drafts [B, Q-1] int32, the same tokens); ctx_after [B] int32: the
         cache lengths once the Q positions are appended (with the 4-bit cache reserve() comes before, and 0
         stands for a slot without a sequence, as every length does where that call found too few pages: then
         no page is written, and the outputs are of no use).  Returns the pass's buffers: argmax [B, Q]
         (the greedy token after each input), alen [B], comm [B, Q] (the rule's outputs), x [B*Q, H]
-        (the last residual stream, the draft block's next input state)."""
+        (the last residual stream, the draft block's next input state).  logprobs=n adds logprob [B, Q]
+        (of comm's tokens; 0 behind the last), entropy [B, Q], top_ids and top_logprobs [B, Q, n], of the
+        bf16 logits after each input (with bf16 weights a second product with the output layer, whose
+        logits the greedy search does not round; V a multiple of 8)."""
         B, Q = tokens.shape
         b = self.buffers(B, Q)
         nh, hd = self.nh, self.hd
@@ -158,9 +187,14 @@ class Decoder:
             torch.where(self.room[0] <= self.room[1], ctx_after, b["none"], out=b["len"])
             ctx_after = b["len"]
         for i, t in enumerate(self.layers):
-            api.rmsnorm_residual(b["x"], y, h=b["h"])
-            for n in ("q", "k", "v"):
-                api.dense_matmul(b["h"], t["w_" + n], out=b[n])
+            if self.weights == "q8":
+                api.rmsnorm_residual_q8(b["x"], y if i else None, codes=b["hq"][0], scales=b["hq"][1])
+                for n in ("q", "k", "v"):
+                    api.dense_matmul_q8(*b["hq"], *t["w_" + n], out=b[n])
+            else:
+                api.rmsnorm_residual(b["x"], y, h=b["h"])
+                for n in ("q", "k", "v"):
+                    api.dense_matmul(b["h"], t["w_" + n], out=b[n])
             if self.cache == "q4":
                 api.spec_q4_append(b["k"].view(B, Q, nh, hd), b["v"].view(B, Q, nh, hd), self.pool[i], self.table[:B],
                                    ctx_after, self.page)
@@ -171,20 +205,40 @@ class Decoder:
                 api.spec_cache_append(b["k"].view(B, Q, nh, hd), b["v"].view(B, Q, nh, hd), kc, vc, ctx_after)
                 api.spec_verify_attention(b["q"].view(B, Q, nh, hd), kc, vc, ctx_after, b["aws"],
                                           out=b["a"].view(B, Q, nh, hd))
-            api.dense_matmul(b["a"], t["w_o"], out=b["o"])
+            if self.weights == "q8":
+                api.quantize_q8_rows(b["a"], *b["aq"])
+                api.dense_matmul_q8(*b["aq"], *t["w_o"], out=b["o"])
+            else:
+                api.dense_matmul(b["a"], t["w_o"], out=b["o"])
             api.rmsnorm_residual(b["x"], b["o"], h=b["h"])
             api.moe_verify_layer(b["h"], t["moe"], b["sh"], b["mws"], out=b["y"])
             y = b["y"]
-        api.rmsnorm_residual(b["x"], y, h=b["h"])
-        api.spec_verify_lmhead(b["h"], self.w_vocab, drafts, b["lws"], Q - 1, argmax=b["argmax"],
-                               accept_len=b["alen"], committed=b["comm"])
+        if self.weights == "q8":
+            logits = self._logits(b)
+            api.rmsnorm_residual_q8(b["x"], y if self.layers else None, codes=b["hq"][0], scales=b["hq"][1])
+            api.dense_matmul_q8(*b["hq"], *self.vocab_q8, out=logits.view(B * Q, self.V))
+            api.spec_verify_accept(logits, drafts, b["lws"], argmax=b["argmax"], accept_len=b["alen"], committed=b["comm"])
+        else:
+            api.rmsnorm_residual(b["x"], y, h=b["h"])
+            api.spec_verify_lmhead(b["h"], self.w_vocab, drafts, b["lws"], Q - 1, argmax=b["argmax"],
+                                   accept_len=b["alen"], committed=b["comm"])
+        if logprobs is not None:
+            logits = self._logits(b)
+            if self.weights != "q8":
+                api.dense_matmul(b["h"], self.w_vocab, out=logits.view(B * Q, self.V))
+            outs = ("logprob", "entropy", "top_ids", "top_logprobs")
+            made = b.setdefault(("logprobs", logprobs), {})
+            b.update(zip(outs, api.spec_logprobs(logits, b["comm"], logprobs, **made)))
+            made.update((n, b[n]) for n in outs)
         return b
 
     def launches_per_verify(self, B: int, Q: int) -> int:
-        """Library kernel launches of one verify pass over the bf16 caches (the MoE layer: 3 up to 256 tokens).  Over
-        4-bit pages the attention is one launch or two, as the library cuts the sequences, and no count is given."""
+        """Library kernel launches of one verify pass over the bf16 caches, without log probabilities (the MoE layer:
+        3 up to 256 tokens).  Over 4-bit pages the attention is one launch or two, as the library cuts the sequences, and
+        no count is given."""
         if self.cache != "bf16":
             raise ValueError("launches_per_verify counts the pass over bf16 caches")
         T = B * Q
         moe = 3 if T <= 256 else (4 if T * self.prob.dims.k <= 8192 else 6)
-        return 1 + len(self.layers) * (1 + 3 + 1 + 2 + 1 + 1 + moe) + 1 + 2
+        q8 = 1 if self.weights == "q8" else 0    # the attention's rows quantised; the output layer apart from the search
+        return 1 + len(self.layers) * (1 + 3 + 1 + 2 + q8 + 1 + 1 + moe) + 1 + q8 + 2

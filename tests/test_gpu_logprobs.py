@@ -1,0 +1,220 @@
+"""Log probabilities, entropies and the most likely tokens (spec_logprobs) on the GPU against oracle/q8.py in 64 bits.
+
+Tokens are exact.  The tolerance of the numbers: a logit's e^(x - m) is off by 2^-22 (the exponential), by the rounding of
+x - m where it has one and of its product with log2 e, 2^-23 |x - m| together, and by a rescaling where a maximum
+rose, 2^-22 and 2^-23 of its exponent again: as a share of S = sum e^(x - m), 2^-21 + 2^-22 D with D = sum p (m - x).
+The sums are of at most n = V / 512 + 40 roundings of 2^-24 (a thread adds every other logit that it takes).  With
+r = 2^-21 + 2^-22 D + n 2^-24 the logarithm of S is off by r and its own rounding; a log probability by that and its
+roundings, 2^-23 (|x - m| + log S); the entropy log S - D by r (1 + 2 D) and 2^-23 (log S + D).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q8
+from lossless_speculative_verification_gb300 import api
+
+from gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = {torch.bfloat16: float(torch.finfo(torch.bfloat16).min), torch.float32: float(torch.finfo(torch.float32).min)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+    yield
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
+
+
+def check(x, n, tokens=None, what=""):
+    """x [R, V] on the host, of the type to test."""
+    R, V = x.shape
+    rs = np.random.default_rng(V)
+    if tokens is None:
+        tokens = rs.integers(-1, V, R)
+    got = api.spec_logprobs(x.cuda(), torch.from_numpy(tokens.astype(np.int32)).cuda(), n)
+    lp, ent, ids, tops = (t.cpu().numpy().astype(np.float64) for t in got)
+    f = x.double().numpy()
+    rlp, rent, rids, rtops = q8.logprobs(f, tokens, n)
+    np.testing.assert_array_equal(ids, rids, err_msg=what)
+    with np.errstate(invalid="ignore", over="ignore"):
+        m = f.max(1)
+        e = np.exp(f - m[:, None])
+        log_s = np.log(e.sum(1))
+        D = np.nansum(np.where(e > 0, e * (m[:, None] - f), 0), 1) / e.sum(1)
+        r = 2.0 ** -21 + 2.0 ** -22 * D + (V / 512 + 40) * 2.0 ** -24
+        size = lambda v: np.where(np.isfinite(v), np.abs(v), 0) + 2 * np.abs(log_s).reshape((-1,) + (1,) * (v.ndim - 1))
+        tol = {"lp": r + 2.0 ** -23 * size(rlp), "tops": r[:, None] + 2.0 ** -23 * size(rtops),
+               "ent": r * (1 + 2 * D) + 2.0 ** -23 * (np.abs(log_s) + D)}
+    for name, g, w in (("lp", lp, rlp), ("ent", ent, rent), ("tops", tops, rtops)):
+        fine = np.isfinite(w)
+        np.testing.assert_array_equal(np.isnan(g), np.isnan(w), err_msg=what + name)
+        np.testing.assert_array_equal(g[~fine & ~np.isnan(w)], w[~fine & ~np.isnan(w)], err_msg=what + name)
+        off, most = np.abs(g[fine] - w[fine]), np.nan_to_num(tol[name][fine], nan=0.0)   # (nothing allowed: exact)
+        assert (off <= most).all(), "%s %s: worst %.3g of its tolerance" % (what, name, np.max(off / np.maximum(most, 1e-300)))
+    return got
+
+
+def logits(seed, R, V, dtype, spread=3.0, peaks=5):
+    g = torch.Generator().manual_seed(seed)
+    x = spread * torch.randn((R, V), generator=g)
+    x[torch.arange(R)[:, None], torch.randint(0, V, (R, peaks), generator=g)] += 8
+    return x.to(dtype)
+
+
+TYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 8, 9, 16, 31, 63, 64, 65, 100, 255, 513, 1000, 2049, 8191, 8193, 40007])
+def test_vocabularies_of_every_end(V, dtype):
+    # odd ones begin rows on every byte that a value may
+    for n in (0, 1, 5, 32):
+        check(logits(V, 5, V, dtype), n, what="V %d n %d " % (V, n))
+
+
+# the forms: clusters of 16, 8, 4, 2 narrow CTAs, of wide ones, one wide, middle or narrow CTA a row; rows of one batch
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,V", [(1, 129280), (2, 70001), (4, 32000), (16, 129280), (37, 20000), (50, 60001), (60, 129280),
+                                 (100, 33333), (152, 30000), (200, 40001), (304, 20000), (700, 9001), (3000, 257)])
+def test_every_form(R, V, dtype):
+    check(logits(R, R, V, dtype), 20, what="%d x %d " % (R, V))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,V", [(1, 129280), (40, 30001), (130, 17000), (310, 4001), (3, 200)])
+def test_rows_that_are_no_ordinary_ones(R, V, dtype):
+    g = torch.Generator().manual_seed(R)
+    x = logits(1, R, V, dtype)
+    kinds = [
+        ("equal", lambda: torch.zeros(V)),
+        ("few values", lambda: torch.randint(0, 3, (V,), generator=g).float()),
+        ("rising", lambda: torch.arange(V) * 1e-3),
+        ("falling", lambda: -torch.arange(V) * 1e-3),
+        ("nothing allowed", lambda: torch.full((V,), -torch.inf)),
+        ("one allowed", lambda: torch.where(torch.arange(V) == V // 2, 1.5, -torch.inf)),
+        ("three allowed", lambda: torch.where(torch.arange(V) % (V // 3) == 7, 2.0, -torch.inf)),
+        ("all of the lowest", lambda: torch.full((V,), LOWEST[dtype])),
+        ("lowest but two", lambda: torch.where(torch.arange(V) < 2, 0.25, LOWEST[dtype])),
+        ("lowest and -inf", lambda: torch.where(torch.arange(V) % 3 == 0, LOWEST[dtype], -torch.inf)),
+        ("zeros of both signs", lambda: torch.where(torch.arange(V) % 2 == 0, -0.0, 0.0)),
+        ("far apart", lambda: torch.where(torch.arange(V) % 7 == 0, 3e4, -3e4)),
+        ("a peak of certainty", lambda: torch.where(torch.arange(V) == V - 1, 60.0, 0.0)),
+        ("a NaN", lambda: torch.where(torch.arange(V) == V // 3, torch.nan, 1.0)),
+        ("an infinity", lambda: torch.where(torch.arange(V) == V - 2, torch.inf, 1.0)),
+        ("largest values", lambda: torch.where(torch.arange(V) % 5 == 0, -LOWEST[dtype], 0.0)),
+    ]
+    for k, (name, make) in enumerate(kinds):
+        y = x.clone()
+        y[k % R] = make().to(dtype)          # beside rows that are
+        for n in (1, 32):
+            check(y, n, what=name + " ")
+
+
+def test_more_vectors_than_there_is_room_for():
+    # every vector's largest above all before it: each is collected, until there is no room
+    for R, V in ((1, 262144), (130, 120000), (400, 100000)):
+        x = (torch.arange(V).float() * 1e-4).expand(R, V).contiguous()
+        check(x, 32)
+    x = torch.arange(120000).flip(0).float().expand(2, -1).contiguous() * 1e-4
+    check(x, 32)
+
+
+def test_the_largest_in_one_place():
+    # the n largest side by side, in one thread's vectors, at the ends, in the elements outside vectors
+    for V in (129283, 4099):
+        x = torch.randn((6, V), generator=torch.Generator().manual_seed(3))
+        for r, at in enumerate((0, V - 40, 8 * 256, V // 2, 5, V - 33)):
+            x[r, at:at + 33] = 10 + torch.randperm(33).float() / 8
+        for dtype in TYPES:
+            check(x.to(dtype), 32)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_tokens(dtype):
+    x = logits(4, 4, 1000, dtype)
+    lp = check(x, 3, np.array([-1, 0, 999, -1]))[0]
+    assert float(lp[0]) == 0 and float(lp[3]) == 0
+    got = api.spec_logprobs(x.cuda(), torch.tensor([0, 1000, -2, 5], dtype=torch.int32, device="cuda"), 0)
+    assert api.get_device_error() == 7
+    assert torch.isnan(got[0]).tolist() == [False, True, True, False] and bool(torch.isfinite(got[1]).all())
+    x3 = x.view(2, 2, 1000)
+    got = api.spec_logprobs(x3.cuda(), torch.zeros((2, 2), dtype=torch.int32, device="cuda"), 4)
+    assert [tuple(t.shape) for t in got] == [(2, 2), (2, 2), (2, 2, 4), (2, 2, 4)]
+
+
+def test_committed_tokens_add_up():
+    B, K, V = 5, 3, 5000
+    x = logits(6, B * (K + 1), V, torch.bfloat16).view(B, K + 1, V).cuda()
+    drafts = x[:, :K].argmax(-1).to(torch.int32)
+    drafts[1, 1] = (drafts[1, 1] + 1) % V
+    drafts[4, 0] = (drafts[4, 0] + 1) % V
+    alen, comm = api.spec_verify_accept(x, drafts.contiguous(), api.spec_verify_workspace(B, K, V))
+    assert alen.tolist() == [3, 1, 3, 3, 0]
+    lp, _, ids, tops = api.spec_logprobs(x, comm, 1)
+    want = torch.log_softmax(x.double(), -1).amax(-1)
+    live = torch.arange(K + 1, device="cuda")[None] <= alen[:, None]
+    assert bool((ids[..., 0][live] == comm[live]).all()) and torch.equal(tops[..., 0][live], lp[live])
+    torch.testing.assert_close(lp.double(), torch.where(live, want, 0), rtol=0, atol=2e-5)
+    assert bool((lp[~live] == 0).all())
+
+
+def test_the_same_twice_and_at_once_and_replayed():
+    x = logits(7, 128, 129280, torch.bfloat16).cuda()
+    t = torch.arange(128, dtype=torch.int32, device="cuda")
+    ref = api.spec_logprobs(x, t, 20)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a = api.spec_logprobs(x, t, 20)
+        b = api.spec_logprobs(x, t, 20, stream=s)
+        torch.cuda.synchronize()
+        for p, q, r in zip(a, b, ref):
+            assert torch.equal(p.view(torch.int32), r.view(torch.int32)) and torch.equal(q.view(torch.int32), r.view(torch.int32))
+    outs = dict(zip(("logprob", "entropy", "top_ids", "top_logprobs"), [torch.zeros_like(r) for r in ref]))
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            api.spec_logprobs(x, t, 20, **outs)
+        for _ in range(2):
+            x.copy_(logits(8, 128, 129280, torch.bfloat16))
+            g.replay()
+            for p, q in zip(outs.values(), api.spec_logprobs(x, t, 20)):
+                assert torch.equal(p.view(torch.int32), q.view(torch.int32))
+    s.synchronize()
+
+
+def test_places_past_32_bits():
+    R, V = 17000, 129280
+    x = torch.empty((R, V), dtype=torch.bfloat16, device="cuda").fill_(-5.0)
+    last = logits(9, 3, V, torch.bfloat16)
+    x[-3:] = last.cuda()
+    t = torch.full((R,), 17, dtype=torch.int32, device="cuda")
+    got = api.spec_logprobs(x, t, 4)
+    want = api.spec_logprobs(last.cuda(), t[-3:].clone(), 4)
+    assert torch.equal(got[2][-3:], want[2])
+    assert torch.allclose(got[0][-3:], want[0], rtol=0, atol=1e-4) and torch.allclose(got[3][-3:], want[3], rtol=0, atol=1e-4)
+    assert bool((got[2][:-3] == torch.arange(4, dtype=torch.int32, device="cuda")).all())
+    assert torch.allclose(got[1][:-3], torch.full_like(got[1][:-3], float(np.log(V))), rtol=0, atol=1e-4)
+
+
+def test_refusals():
+    x = torch.zeros((2, 100), dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for bad in (x.half(), x.cpu(), x.t(), x[:, :50]):
+        with pytest.raises(ValueError):
+            api.spec_logprobs(bad, t, 3)
+    for bad in (t.long(), t[:1], t.cpu()):
+        with pytest.raises(ValueError):
+            api.spec_logprobs(x, bad, 3)
+    with pytest.raises(api._ffi.LsvError):
+        api.spec_logprobs(x, t, 33)
+    with pytest.raises(ValueError):
+        api.spec_logprobs(x, t, 3, top_ids=torch.zeros((2, 4), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        api.spec_logprobs(x, t, 3, entropy=torch.zeros(2, dtype=torch.float64, device="cuda"))
+    got = api.spec_logprobs(x[:0], t[:0], 3)
+    assert [tuple(o.shape) for o in got] == [(0,), (0,), (0, 3), (0, 3)]

@@ -1,0 +1,124 @@
+"""The speculative loop with 8-bit projections and output layer (Decoder(weights="q8")): the committed stream equals plain
+greedy decoding with the same weights, token for token, over both caches (a row's products do not depend on the rows
+beside it); and the log probabilities that a pass adds."""
+import numpy as np
+import pytest
+import torch
+
+from lossless_speculative_verification_gb300 import api, synth
+from lossless_speculative_verification_gb300.decoder import Decoder
+
+from gpu_util import need_gpu
+import test_gpu_q4_loop as q4loop
+import test_gpu_spec_loop as loop
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+    yield
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
+
+
+def problem(seed, out_scale):
+    dims = synth.MoeDims(0, 256, 8, 2, 1, 128)
+    return synth.decoder_problem(2, dims, V=2048, nh=2, I_draft=256, seed=seed, out_scale=out_scale, mimic_draft=True)
+
+
+@pytest.mark.parametrize("seed", [0, 1])
+def test_speculative_loop_commits_the_greedy_sequence(seed):
+    seen = set()
+    for out_scale in (0.05, 0.6):
+        prob = problem(seed, out_scale)
+        dec = Decoder(prob, loop.B, L=loop.P + 4 * loop.N_NEW + 32, weights="q8")
+        prompt = torch.from_numpy(np.random.default_rng(seed + 7).integers(0, prob.V, (loop.B, loop.P)).astype(np.int32)).cuda()
+        ref = loop.greedy(dec, prompt)
+        for K in (1, 2, 3):
+            got, lengths = loop.speculative(dec, prompt, K)
+            np.testing.assert_array_equal(got, ref, err_msg="K=%d, out_scale %g" % (K, out_scale))
+            seen |= {(K, int(n)) for n in lengths}
+    assert (3, 3) in seen and any(n < K for K, n in seen), sorted(seen)
+
+
+def test_passes_over_pages_and_contiguous_caches():
+    # one token at a time and four, over 4-bit pages
+    prob = problem(2, 0.3)
+    B, L, n = 3, 64, 12
+    tokens = torch.from_numpy(np.random.default_rng(3).integers(0, prob.V, (B, n)).astype(np.int32)).cuda()
+    none = torch.zeros((B, 0), dtype=torch.int32, device="cuda")
+    seen = []
+    for Q in (1, 4):
+        dec = Decoder(prob, B, L, cache="q4", page=16, weights="q8")
+        rows = []
+        for i in range(0, n, Q):
+            dec.reserve(q4loop.i32([i] * B), q4loop.i32([i + Q] * B))
+            part = tokens[:, i:i + Q].contiguous()
+            b = dec.verify(part, q4loop.i32([i + Q] * B), part[:, 1:].contiguous() if Q > 1 else none)
+            rows.append(b["argmax"].clone())
+        seen.append(torch.cat(rows, 1))
+    assert torch.equal(*seen)
+
+
+@pytest.mark.parametrize("weights", ["bf16", "q8"])
+def test_log_probabilities_of_a_pass(weights):
+    prob = problem(4, 0.6)
+    B, Q, n = 4, 4, 6
+    dec = Decoder(prob, B, 64, weights=weights)
+    tokens = torch.from_numpy(np.random.default_rng(5).integers(0, prob.V, (B, Q)).astype(np.int32)).cuda()
+    after = torch.full((B,), Q, dtype=torch.int32, device="cuda")
+    drafts = tokens[:, 1:].contiguous()
+    plain = {k: v.clone() for k, v in dec.verify(tokens, after, drafts).items() if k in ("argmax", "alen", "comm")}
+    b = dec.verify(tokens, after, drafts, logprobs=n)
+    for k, v in plain.items():
+        assert torch.equal(b[k], v)
+    logp = torch.log_softmax(b["logits"].double(), -1)
+    live = b["comm"] >= 0
+    want = torch.gather(logp, 2, b["comm"].clamp(min=0).long()[..., None])[..., 0]
+    # of the logits that are rounded to bf16: the numbers to fp32's roundings
+    torch.testing.assert_close(b["logprob"].double(), torch.where(live, want, 0), rtol=0, atol=2e-5)
+    torch.testing.assert_close(b["entropy"].double(), -(logp.exp() * logp).sum(-1), rtol=0, atol=5e-5)
+    top = torch.gather(logp, 2, b["top_ids"].long())
+    torch.testing.assert_close(b["top_logprobs"].double(), top, rtol=0, atol=2e-5)
+    assert b["top_ids"].shape == (B, Q, n)
+    if weights == "q8":
+        assert torch.equal(b["top_ids"][..., 0], b["argmax"])
+        # the norm and the product in 8 bits, as an output layer does them: the pass's logits are the calls'
+        h = api.rmsnorm_residual_q8(b["x"])
+        again = api.dense_matmul_q8(*h, *dec.vocab_q8).view(B, Q, -1)
+        assert torch.equal(again, b["logits"])
+    first = {k: b[k].data_ptr() for k in ("logprob", "top_ids")}
+    again = dec.verify(tokens, after, drafts, logprobs=n)
+    assert {k: again[k].data_ptr() for k in first} == first         # a pass's buffers are kept
+    assert dec.verify(tokens, after, drafts, logprobs=0)["top_ids"].shape == (B, Q, 0)
+
+
+def test_a_pass_replayed():
+    prob = problem(6, 0.6)
+    dec = Decoder(prob, 2, 64, weights="q8")
+    tokens = torch.zeros((2, 3), dtype=torch.int32, device="cuda")
+    after = torch.full((2,), 3, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    rs = np.random.default_rng(7)
+    with torch.cuda.stream(s):
+        dec.verify(tokens, after, tokens[:, 1:].contiguous(), logprobs=3)
+        drafts = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            b = dec.verify(tokens, after, drafts, logprobs=3)
+        for _ in range(2):
+            tokens.copy_(torch.from_numpy(rs.integers(0, prob.V, (2, 3)).astype(np.int32)))
+            drafts.copy_(tokens[:, 1:])
+            g.replay()
+            got = {k: b[k].clone() for k in ("argmax", "comm", "logprob", "entropy", "top_ids", "top_logprobs")}
+            want = dec.verify(tokens, after, drafts, logprobs=3)
+            for k, v in got.items():
+                assert torch.equal(v, want[k]), k
+    s.synchronize()
+
+
+def test_refusals():
+    with pytest.raises(ValueError):
+        Decoder(problem(0, 0.5), 1, 16, weights="fp8")
