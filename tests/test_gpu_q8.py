@@ -272,6 +272,26 @@ def test_quantised_normed_multiplied_and_read_in_a_graph():
     s.synchronize()
 
 
+# many calls without a wait between them, each of whose CTAs begin as those of the one before end
+@pytest.mark.parametrize("M,N,K", [(128, 129280, 1280), (100, 20000, 400), (1, 1280, 1280), (700, 9728, 1296)])
+def test_call_behind_call(M, N, K):
+    x, xs, w, ws = cuda(*operands(4, M, N, K))
+    want = api.dense_matmul_q8(x, xs, w, ws)
+    out = [torch.empty_like(want) for _ in range(3)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for i in range(24):
+                api.dense_matmul_q8(x, xs, w, ws, out=out[i % 3])
+        for _ in range(4):
+            g.replay()
+    s.synchronize()
+    for o in out:
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16))
+
+
 def test_two_calls_at_once():
     a, b = (cuda(*operands(k, 128, 30000, 1280)) for k in (1, 2))
     ra, rb = api.dense_matmul_q8(*a), api.dense_matmul_q8(*b)
