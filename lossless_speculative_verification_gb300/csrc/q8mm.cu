@@ -10,22 +10,21 @@
 //
 // Orientation: 128 rows of x on the MMA's M side, TN weight rows on its N side.  A TMEM lane is then a row of x, a
 // thread's columns lie within one block of 128 weight rows, and the factor of a group is one number a thread.
-// Warp 0 issues TMA (both operands K-major, 128-byte swizzle: a stage is one group), warps 1 and 2 the MMAs, each group
-// into the next of 512 / TN accumulators, warp 3 brings the scales, multiplied, four groups at a time (a row's scales lie
-// far from the next row's: such loads hold up every other access to shared memory of the warp that issues them), and warps
-// 4..11 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
-//
-// What bounds it is how soon an accumulator is free again: 512 columns of TMEM hold two groups of 256, and an MMA may begin
-// when the sums have read what it overwrites.  So two warps issue MMAs (one alone takes 550 cycles a group, waits and
-// commits included): with 256 columns each its own half, which is handed over and read apart from the other, with 128
-// columns every other group.
+// Warp 0 issues TMA (both operands K-major, 128-byte swizzle: a stage is one group), warp 1 the MMAs, each group into
+// the next of 512 / TN accumulators, warps 2 and 3 bring the scales, multiplied, four groups at a time (a row's scales
+// lie far from the next row's: such loads hold up every other access to shared memory of the warp that issues them), and
+// warps 4..11 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
 //
 // Forms:
 // - few tiles: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank adds one
 //   slice of the columns up over the ranks, in rank order, through distributed shared memory;
 // - more tiles than SMs: persistent CTAs take them row tiles first, so that a weight tile is read from HBM once;
-// - many rows: tiles of 128 x 256.  (Pairs of CTAs on 256 x 256, which load a third less, took the same time: loading is
-//   not what bounds it.)
+// - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
+//
+// What bounds the pairs is the sums' own loop, some 180 instructions a warp and group that wait on one another (a group
+// takes 1.1 K cycles, its MMAs 512): 2440 x 129280 x 1280 takes 422 us (1.92 PFLOP/s), 4879 x 1280 x 7168 59 us, of which
+// the FMAs alone are 9 and waiting for the scales 5.  One CTA a tile of 128 x 256 with two warps that issue MMAs: 460 and
+// 63 us; twice the warps with half the columns each: 479 and 68; accumulators handed over in halves: 417 and 63.
 // All sums are of a fixed order: results are the same from run to run, and up to 128 rows a row's bits do not depend
 // on how many rows there are.
 #include <cuda_bf16.h>
@@ -40,28 +39,27 @@
 namespace lsv {
 namespace {
 
-constexpr int kMmThreads = 384;  // warp 0 TMA, warps 1, 2 MMAs, warp 3 scales, warps 4..11 sums and output
-// Registers: what a thread is launched with, and what the first warpgroup keeps and the other two get of the sum (256
-// columns take more for the sums).
+constexpr int kMmThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 4..11 sums and output
+// Registers: what a thread is launched with, and what the first warpgroup keeps and the other two get of the sum (the
+// pair's sums take more; at 128 columns the first warpgroup has the more to hold).
 constexpr int kMmRegs = 168;
-constexpr int mm_regs_few(int tn) { return tn == 256 ? 72 : 88; }
-constexpr int mm_regs_many(int tn) { return tn == 256 ? 216 : 208; }
-static_assert(128 * mm_regs_few(256) + 256 * mm_regs_many(256) <= 384 * kMmRegs, "register split");
-static_assert(128 * mm_regs_few(128) + 256 * mm_regs_many(128) <= 384 * kMmRegs, "register split");
-constexpr int kMmTile = 128;         // rows of x a CTA
+constexpr int mm_regs_few(bool pair) { return pair ? 72 : 88; }
+constexpr int mm_regs_many(bool pair) { return pair ? 216 : 208; }
+static_assert(128 * mm_regs_few(true) + 256 * mm_regs_many(true) <= 384 * kMmRegs, "register split");
+static_assert(128 * mm_regs_few(false) + 256 * mm_regs_many(false) <= 384 * kMmRegs, "register split");
+constexpr int kMmTile = 128;     // rows of x a CTA
 constexpr int kMmMaxStages = 12;
 constexpr int kMmSmem = 225 * 1024;  // the ring and what lies behind it
+constexpr int kMmPanel = 32 * 128;   // bytes of 64 columns of a warp's 32 rows of output
 constexpr int kMmBlock = 4;          // groups whose scales are brought at once
 constexpr int kMmScaleSlots = 4;     // blocks of scales in shared memory
 constexpr int kMmScaleBytes = kMmScaleSlots * kMmBlock * kMmTile * 2 * 4;
-constexpr int kMmPanel = 32 * 64;    // bytes of 32 columns of a warp's 32 rows of output
-constexpr int kMmPanels = 8;         // one for each warp
 constexpr int kMmMaxSplit = 8;
 
 struct MmParams {
   int M, N, K, G;      // G: groups of K
   int nm, nitems;      // row tiles; tiles of the output
-  int ns;              // CTAs that share a tile's groups (cluster size)
+  int ns;              // CTAs that share a tile's groups (cluster size; 1 for pairs)
   int stages, a_bytes, stage_bytes;
   int a_last, b_last;  // bytes of the boxes of the last row tile and the last weight tile
   int aligned;         // rows of y start on 16 bytes: they are stored by TMA
@@ -95,47 +93,54 @@ __device__ __forceinline__ float4 load_scales(const float* s, int g, int G) {
   return v;
 }
 
-// TN: weight rows a tile, 128 or 256.
-template <int TN>
+// TN: weight rows a tile.  PAIR: clusters of two CTAs on tiles of 256 rows; each loads its 128 rows of x and half of
+// the weight rows, counts its bytes on the leader's (rank 0's) stage barrier, the leader issues the MMAs of both, and
+// its commits release both CTAs' stages and accumulators; each CTA sums its own 128 rows.
+template <int TN, bool PAIR>
 __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
-  constexpr int kBufs = 512 / TN;      // accumulators
-  constexpr int kCols = TN / 2;        // columns a thread
-  constexpr int kHalves = TN / 128;    // parts of an accumulator that are handed over apart
+  constexpr int kBufs = 512 / TN < 8 ? 512 / TN : 8;  // accumulators
+  constexpr int kCols = TN / 2;                       // columns a thread
+  constexpr int kTileM = PAIR ? 2 * kMmTile : kMmTile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[kBufs * kHalves], tempty[kBufs * kHalves],
-      sfull[kMmScaleSlots], sempty[kMmScaleSlots], final_bar[2], recv_bar;
+  __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[kBufs], tempty[kBufs], sfull[kMmScaleSlots],
+      sempty[kMmScaleSlots], final_bar, recv_bar;
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool clustered = p.ns > 1;
-  const int rank = clustered ? (int)cluster_ctarank() : 0;
-  const int first = blockIdx.x / p.ns, step = gridDim.x / p.ns;
+  const bool clustered = PAIR || p.ns > 1;
+  const uint32_t rank = clustered ? cluster_ctarank() : 0u;
+  const bool leader = !PAIR || rank == 0;
+  const int size = PAIR ? 2 : p.ns;
+  const int first = blockIdx.x / size, step = gridDim.x / size;
   // this CTA's groups of each tile: a split's share, at least one (ns <= G)
-  const int g0 = rank * p.G / p.ns, g1 = (rank + 1) * p.G / p.ns;
+  const int g0 = PAIR ? 0 : (int)rank * p.G / p.ns, g1 = PAIR ? p.G : ((int)rank + 1) * p.G / p.ns;
   const int ntn = (p.N + TN - 1) / TN;
-  const int groups = first < p.nitems ? ((p.nitems - 1 - first) / step + 1) * (g1 - g0) : 0;  // of all tiles
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kHalves);
+      mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < kBufs * kHalves; ++a) {
+    for (int a = 0; a < kBufs; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 8 / kHalves);
+      mbar_init(&tempty[a], PAIR ? 16 : 8);
     }
     for (int q = 0; q < kMmScaleSlots; ++q) {
-      mbar_init(&sfull[q], 1);
+      mbar_init(&sfull[q], 2);
       mbar_init(&sempty[q], 8);
     }
-    mbar_init(&final_bar[0], 1);
-    mbar_init(&final_bar[1], 1);
+    mbar_init(&final_bar, 1);
     mbar_init(&recv_bar, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, kBufs * TN);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&tmem_slot, kBufs * TN);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&tmem_slot, kBufs * TN);
+      tmem_relinquish();
+    }
   }
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&maps.x);
@@ -158,12 +163,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   pdl_wait();  // x and w may come from the preceding kernels
 
   if (warp < 4) {
-    reg_dec<mm_regs_few(TN)>();
-    // The loops of warps 0..2 are run by whole warps, and one lane issues.
+    reg_dec<mm_regs_few(PAIR)>();
+    // Both loops are run by the whole warp, and one lane issues.
     if (warp == 0) {
       // ---------------------------------------------------------- TMA
       // weights that one row tile reads come once
       const uint64_t pol_x = l2_policy_evict_last(), pol_w = p.nm == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+      const uint32_t fb0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -172,7 +178,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         const bool last_r = tr == p.nm - 1, last_v = tv == ntn - 1;
         const CUtensorMap* xm = last_r ? &maps.x_last : &maps.x;
         const CUtensorMap* wm = last_v ? &maps.w_last : &maps.w;
-        const int bytes = (last_r ? p.a_last : p.a_bytes) + (last_v ? p.b_last : TN * 128);
+        const int bytes = (last_r ? p.a_last : p.a_bytes) + (last_v ? p.b_last : TN / (PAIR ? 2 : 1) * 128);
+        const int row = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0);
+        const int col = tv * TN + (PAIR ? (int)rank * (TN / 2) : 0);
         for (int g = g0; g < g1; ++g) {
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns))) {
             ok = false;
@@ -180,9 +188,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           }
           if (elect_one()) {
             uint8_t* a_s = smem + stage * p.stage_bytes;
-            mbar_arrive_expect_tx(&full[stage], bytes);
-            tma_load_2d(a_s, xm, &full[stage], g * kQ8Group, tr * kMmTile, pol_x);
-            tma_load_2d(a_s + p.a_bytes, wm, &full[stage], g * kQ8Group, tv * TN, pol_w);
+            if constexpr (PAIR) {
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+              tma_load_2d_pair(a_s, xm, fb0 + 8 * stage, g * kQ8Group, row, pol_x);
+              tma_load_2d_pair(a_s + p.a_bytes, wm, fb0 + 8 * stage, g * kQ8Group, col, pol_w);
+            } else {
+              mbar_arrive_expect_tx(&full[stage], bytes);
+              tma_load_2d(a_s, xm, &full[stage], g * kQ8Group, row, pol_x);
+              tma_load_2d(a_s + p.a_bytes, wm, &full[stage], g * kQ8Group, col, pol_w);
+            }
           }
           __syncwarp();
           ++issued;
@@ -194,90 +208,98 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
       }
       if (!ok && lane == 0) {
         set_error(p.err, kErrTimeout);
-        // the copies still in flight land before the CTA ends
-        for (int q = issued < p.stages ? 0 : issued - p.stages; q < issued; ++q)
-          mbar_wait(&full[q % p.stages], (uint32_t)(q / p.stages) & 1u, p.wait_ns);
+        // the copies still in flight land before the CTA ends (the leader's barriers count a pair's)
+        if (leader)
+          for (int q = issued < p.stages ? 0 : issued - p.stages; q < issued; ++q)
+            mbar_wait(&full[q % p.stages], (uint32_t)(q / p.stages) & 1u, p.wait_ns);
       }
-    } else if (warp < 3) {
-      // ---------------------------------------------------------- MMAs: half `who` of every group, or every other group
-      const int who = warp - 1;
-      constexpr int kStep = 2 / kHalves;
-      const int skip = kHalves == 1 ? who : 0, part = kHalves == 1 ? 0 : who;
-      int stage = skip, buf = skip;
+    } else if (warp == 1 && leader) {
+      // ---------------------------------------------------------- MMAs (the leader's, for a pair)
+      int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
-      constexpr uint32_t idesc = idesc_e4m3_f32(kMmTile, 128);
-      const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem)),
-                     b0 = sdesc_kmajor_sw128(smem_u32(smem) + p.a_bytes + part * (128 * 128));
-      for (int q = skip; q < groups; q += kStep) {
-        const bool got = mbar_wait(&full[stage], phase, p.wait_ns) &&
-                         mbar_wait(&tempty[buf * kHalves + part], buf_phase ^ 1u, p.wait_ns);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        if (elect_one()) {
-          const uint32_t d = tmem_base + (uint32_t)(buf * TN + part * 128);
-          // descriptors hold addresses in units of 16 bytes; a step of 32 columns is two
-          const uint64_t at = (uint64_t)(uint32_t)(stage * (p.stage_bytes >> 4));
+      constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, TN);
+      const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem)), b0 = sdesc_kmajor_sw128(smem_u32(smem) + p.a_bytes);
+      for (int it = first; it < p.nitems && ok; it += step) {
+        for (int g = g0; g < g1; ++g) {
+          const bool got =
+              mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns) && mbar_wait(&full[stage], phase, p.wait_ns);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const uint32_t d = tmem_base + (uint32_t)(buf * TN);
+            // descriptors hold addresses in units of 16 bytes; a step of 32 columns is two
+            const uint64_t at = (uint64_t)(uint32_t)(stage * (p.stage_bytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_e4m3(d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, kk ? 1u : 0u);
-          umma_commit(&tfull[buf * kHalves + part]);
-          umma_commit(&empty[stage]);
-        }
-        __syncwarp();
-        stage += kStep;
-        if (stage >= p.stages) {
-          stage -= p.stages;
-          phase ^= 1u;
-        }
-        buf += kStep;
-        if (buf >= kBufs) {
-          buf -= kBufs;
-          buf_phase ^= 1u;
+            for (int kk = 0; kk < 4; ++kk) {
+              if constexpr (PAIR)
+                umma_e4m3_pair(d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, kk ? 1u : 0u);
+              else
+                umma_e4m3(d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, kk ? 1u : 0u);
+            }
+            if constexpr (PAIR) {
+              umma_commit_pair_mc(&tfull[buf], 0x3);
+              umma_commit_pair_mc(&empty[stage], 0x3);
+            } else {
+              umma_commit(&tfull[buf]);
+              umma_commit(&empty[stage]);
+            }
+          }
+          __syncwarp();
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
         }
       }
       // every MMA has completed before TMEM and the ring are given up
       if (elect_one()) {
         if (!ok) set_error(p.err, kErrTimeout);
-        umma_commit(&final_bar[who]);
-        if (!mbar_wait(&final_bar[who], 0, p.wait_ns)) set_error(p.err, kErrTimeout);
+        if constexpr (PAIR)
+          umma_commit_pair_mc(&final_bar, 0x1);
+        else
+          umma_commit(&final_bar);
+        if (!mbar_wait(&final_bar, 0, p.wait_ns)) set_error(p.err, kErrTimeout);
       }
-    } else {
-      // ---------------------------------------------------------- scales: four rows a lane
+    }
+    if (warp >= 2) {
+      // ---------------------------------------------------------- scales: 64 rows a warp, two a lane
+      const int r0 = (warp - 2) * 64 + lane;
       int slot = 0;
       uint32_t phase = 0;
       bool ok = true;
-      const int nb = (p.N - 1) / kQ8Group;
       for (int it = first; it < p.nitems && ok; it += step) {
         const int tv = it / p.nm, tr = it - tv * p.nm;
-        const float* sx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sx[i] = p.sx + (size_t)min(tr * kMmTile + lane + 32 * i, p.M - 1) * p.G;
+        const int row = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0) + r0;
+        const float* sx0 = p.sx + (size_t)min(row, p.M - 1) * p.G;
+        const float* sx1 = p.sx + (size_t)min(row + 32, p.M - 1) * p.G;
+        const int nb = (p.N - 1) / kQ8Group;
         const float* sw0 = p.sw + (size_t)min(tv * TN / kQ8Group, nb) * p.G;
         const float* sw1 = p.sw + (size_t)min((tv * TN + kCols) / kQ8Group, nb) * p.G;
         for (int g = g0 & ~3; g < g1; g += kMmBlock) {
-          float4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = load_scales(sx[i], g, p.G);
+          const float4 x0 = load_scales(sx0, g, p.G), x1 = load_scales(sx1, g, p.G);
           const float4 w0 = load_scales(sw0, g, p.G), w1 = load_scales(sw1, g, p.G);
           if (!__all_sync(0xffffffffu, mbar_wait(&sempty[slot], phase ^ 1u, p.wait_ns))) {
             ok = false;
             break;
           }
-          float* d = scales + slot * (kMmBlock * 2 * kMmTile) + lane;
+          float* d = scales + slot * (kMmBlock * 2 * kMmTile) + r0;
+          const float xs[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
+          const float ws[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            d[32 * i] = x[i].x * w0.x;
-            d[32 * i + kMmTile] = x[i].x * w1.x;
-            d[32 * i + 2 * kMmTile] = x[i].y * w0.y;
-            d[32 * i + 3 * kMmTile] = x[i].y * w1.y;
-            d[32 * i + 4 * kMmTile] = x[i].z * w0.z;
-            d[32 * i + 5 * kMmTile] = x[i].z * w1.z;
-            d[32 * i + 6 * kMmTile] = x[i].w * w0.w;
-            d[32 * i + 7 * kMmTile] = x[i].w * w1.w;
-          }
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              d[(2 * i + h) * kMmTile] = xs[0][i] * ws[h][i];
+              d[(2 * i + h) * kMmTile + 32] = xs[1][i] * ws[h][i];
+            }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sfull[slot]);
           if (++slot == kMmScaleSlots) {
@@ -291,14 +313,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     __syncwarp();
   } else {
     // ------------------------------------------------------------ sums over the groups, output
-    reg_inc<mm_regs_many(TN)>();
+    reg_inc<mm_regs_many(PAIR)>();
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const int c0 = half * kCols, part = kHalves == 1 ? 0 : half;
+    const int c0 = half * kCols;
     uint8_t* panel = behind + (warp - 4) * kMmPanel;
-    const float* my_scales = scales + half * kMmTile + 32 * quarter + lane;
     int buf = 0, slot = 0;
     uint32_t buf_phase = 0, slot_phase = 0;
     bool ok = true;
+    const uint32_t leaders_tempty = PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
     // The accumulators are read 32 columns at a time, one piece ahead of the sums, from one group into the next and from
     // one tile into the next: a wait for a group and the latency of a read run beside the sums of what was read before.
     // A thread whose row does not exist reads what is there, and stores nothing.
@@ -306,24 +328,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     constexpr int kPieces = kCols / 32;
     static_assert(kPieces % 2 == 0, "a group begins in r[0]");
     uint32_t r[2][32];
-    int left = groups;  // groups not begun
-    int next = g0;      // the next one to begin, within its tile
-    float f_next = 0.0f;
+    int left = first < p.nitems ? ((p.nitems - 1 - first) / step + 1) * (g1 - g0) : 0;  // groups not begun
     auto begin = [&]() {
       --left;
-      bool got = mbar_wait(&tfull[buf * kHalves + part], buf_phase, p.wait_ns);
+      const bool got = mbar_wait(&tfull[buf], buf_phase, p.wait_ns);
+      ok = __all_sync(0xffffffffu, got);
       tc_fence_after_sync();
       tmem_ld_32x32b_x32(t_row + (uint32_t)(buf * TN), r[0]);
-      if (next == g0 || (next & 3) == 0) got = got && mbar_wait(&sfull[slot], slot_phase, p.wait_ns);
-      f_next = my_scales[(slot * kMmBlock + (next & 3)) * (2 * kMmTile)];
-      ok = __all_sync(0xffffffffu, got);
-      ++next;
     };
     if (left > 0) begin();
     // (a split's warps meet behind its one tile, whatever became of their waits)
     for (int it = first; it < p.nitems && (ok || p.ns > 1); it += step) {
       const int tv = it / p.nm, tr = it - tv * p.nm;
-      const int row0 = tr * kMmTile + 32 * quarter;  // the warp's first row
+      const int row0 = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0) + 32 * quarter;  // the warp's first row
       const int row = row0 + lane;
       const bool any = row0 < p.M, mine = row < p.M;
       const int n0 = tv * TN + c0;
@@ -331,8 +348,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
       for (int g = g0; g < g1; ++g) {
-        if (!ok) break;
-        const float2 f2 = make_float2(f_next, f_next);
+        bool got = true;
+        if (g == g0 || (g & 3) == 0) got = mbar_wait(&sfull[slot], slot_phase, p.wait_ns);
+        const float f = scales[((slot * kMmBlock + (g & 3)) * 2 + half) * kMmTile + 32 * quarter + lane];
+        if (!__all_sync(0xffffffffu, got && ok)) {
+          ok = false;
+          break;
+        }
+        const float2 f2 = make_float2(f, f);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           tmem_ld_wait_for(r[i & 1]);
@@ -340,22 +363,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
             tmem_ld_32x32b_x32(t_row + (uint32_t)(buf * TN + 32 * (i + 1)), r[(i + 1) & 1]);
           } else {
             // all of the accumulators are read
-            const bool last = g + 1 == g1, block = last || (g & 3) == 3;
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(&tempty[buf * kHalves + part]);
-              if (block) mbar_arrive(&sempty[slot]);
+              if (PAIR && !leader)
+                mbar_arrive_cluster_relaxed(leaders_tempty + 8 * buf);
+              else
+                mbar_arrive(&tempty[buf]);
+              if ((g & 3) == 3 || g + 1 == g1) mbar_arrive(&sempty[slot]);
             }
             if (++buf == kBufs) {
               buf = 0;
               buf_phase ^= 1u;
             }
-            if (block && ++slot == kMmScaleSlots) {
-              slot = 0;
-              slot_phase ^= 1u;
-            }
-            if (last) next = g0;
             if (left > 0) begin();
           }
 #pragma unroll
@@ -363,25 +383,28 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
             acc[16 * i + j] = fma2(make_float2(__uint_as_float(r[i & 1][2 * j]), __uint_as_float(r[i & 1][2 * j + 1])),
                                    f2, acc[16 * i + j]);
         }
+        if (((g & 3) == 3 || g + 1 == g1) && ++slot == kMmScaleSlots) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
       }
-      if (p.ns == 1) {
+      if (PAIR || p.ns == 1) {
         if (ok && any && p.aligned) {
-          // to shared memory as rows of 64 bytes, 16-byte pieces swizzled as TMA has them, and out while the next tile
-          // runs
+          // to shared memory as 128-byte rows, 16-byte pieces swizzled as TMA has them, and out while the next tile runs
 #pragma unroll
-          for (int q = 0; q < kCols / 32; ++q) {
+          for (int q = 0; q < kCols / 64; ++q) {
             if (lane == 0) bulk_wait_read();
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
               uint32_t v[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] = mm_pack(acc[16 * q + 4 * i + j].x, acc[16 * q + 4 * i + j].y);
-              *reinterpret_cast<uint4*>(panel + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+              for (int j = 0; j < 4; ++j) v[j] = mm_pack(acc[32 * q + 4 * i + j].x, acc[32 * q + 4 * i + j].y);
+              *reinterpret_cast<uint4*>(panel + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
             }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0 && n0 + 32 * q < p.N) tma_store_2d(&maps.y, panel, n0 + 32 * q, row0);
+            if (lane == 0 && n0 + 64 * q < p.N) tma_store_2d(&maps.y, panel, n0 + 64 * q, row0);
           }
         } else if (ok && mine) {
           bf16* y = p.y + (size_t)row * p.N + n0;
@@ -393,21 +416,22 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         }
       } else {
         // The tile's columns are dealt to the ranks, TN / ns each.  recv[src][column / 4][row]: four columns a piece,
-        // consecutive lanes side by side.  What a peer sends may come before this CTA's own MMAs are done, so the
-        // receive slots lie behind the ring.
+        // consecutive lanes side by side.  The ring's bytes are free: every MMA that reads them is done before any
+        // accumulator of the last group is, and this CTA has one tile.  What a peer sends may come before this CTA's
+        // own ring is free, so the receive slots lie behind the ring.
         float4* recv = reinterpret_cast<float4*>(behind);
         const int cols4 = TN / p.ns / 4;
         if (warp == 4 && lane == 0) {
           // the other ranks' sums of this rank's columns, for the rows that exist
-          mbar_arrive_expect_tx(&recv_bar, (uint32_t)(p.ns - 1) * cols4 * min(kMmTile, p.M - tr * kMmTile) * 16);
+          mbar_arrive_expect_tx(&recv_bar, (uint32_t)(p.ns - 1) * cols4 * min(kMmTile, p.M - tr * kTileM) * 16);
         }
 #pragma unroll
         for (int j = 0; j < kCols / 4; ++j) {
           const int c4 = c0 / 4 + j, dst = c4 / cols4;
-          const int at = (rank * cols4 + c4 - dst * cols4) * kMmTile + 32 * quarter + lane;
+          const int at = ((int)rank * cols4 + c4 - dst * cols4) * kMmTile + 32 * quarter + lane;
           const float4 v = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
           if (!mine) continue;
-          if (dst == rank)
+          if (dst == (int)rank)
             recv[at] = v;
           else
             st_async_f4(mapa_shared(smem_u32(recv + at), (uint32_t)dst), v, mapa_shared(smem_u32(&recv_bar), (uint32_t)dst));
@@ -418,7 +442,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         const int tid = threadIdx.x - 128;
         for (int u = tid; got && u < cols4 * kMmTile; u += 256) {
           const int rl = u & (kMmTile - 1), c4 = u / kMmTile;
-          const int m = tr * kMmTile + rl, n = tv * TN + (rank * cols4 + c4) * 4;
+          const int m = tr * kTileM + rl, n = tv * TN + ((int)rank * cols4 + c4) * 4;
           if (m >= p.M || n >= p.N) continue;
           float4 s = recv[c4 * kMmTile + rl];
           for (int q = 1; q < p.ns; ++q) {
@@ -443,48 +467,50 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   __syncwarp();
   tc_fence_before_sync();
   if (clustered)
-    cluster_sync();  // nobody's sums go to a CTA that has ended
+    cluster_sync();  // nobody's copies, MMAs or sums go to a CTA that has ended
   else
     __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, kBufs * TN);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, kBufs * TN);
+    else
+      tmem_dealloc(tmem_base, kBufs * TN);
   }
 }
 
 int round8(int v) { return (v + 7) / 8 * 8; }
 
-template <int TN>
+template <int TN, bool PAIR>
 cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const DeviceCtx& dc, cudaStream_t s) {
+  constexpr int kTileM = PAIR ? 2 * kMmTile : kMmTile, kBox = PAIR ? TN / 2 : TN;
   const int ntn = (p.N + TN - 1) / TN;
-  p.nm = (p.M + kMmTile - 1) / kMmTile;
+  p.nm = (p.M + kTileM - 1) / kTileM;
   p.nitems = p.nm * ntn;
   // Boxes of the last tiles hold what there is: a box that reaches far past its tensor makes every load of it slow.
   // The MMA reads the whole tile; the rows behind a box are what is left of an earlier stage, and their results are
   // never stored.  One row tile alone: the stage is no longer than its box.
-  const int tail_m = round8(p.M - (p.nm - 1) * kMmTile), tail_n = round8(p.N - (ntn - 1) * TN);
+  const int tail_m = PAIR ? kMmTile : round8(p.M - (p.nm - 1) * kMmTile);
+  const int tail_n = PAIR ? kBox : round8(p.N - (ntn - 1) * TN);
   const int rows = p.nm == 1 ? tail_m : kMmTile;
   p.a_bytes = rows * 128;
   p.a_last = tail_m * 128;
   p.b_last = tail_n * 128;
-  p.stage_bytes = p.a_bytes + TN * 128;
-  // behind the ring: the scales, the receive slots of a split or the output's panels; and behind a short stage the MMA
-  // reads on, up to a whole tile of rows
-  const int behind = kMmScaleBytes + (p.ns > 1 ? kMmTile * TN * 4 : kMmPanels * kMmPanel);
-  static_assert(kMmScaleBytes >= kMmTile * 128, "room behind the last stage");
+  p.stage_bytes = p.a_bytes + kBox * 128;
+  // behind the ring: the receive slots of a split, or the output's panels; and behind a short stage the MMA reads on, up
+  // to a whole tile of rows
+  const int behind = kMmScaleBytes + (p.ns > 1 ? kMmTile * TN * 4 : 8 * kMmPanel);
+  static_assert(kMmScaleBytes + 8 * kMmPanel >= kMmTile * 128, "room behind the last stage");
   p.stages = (kMmSmem - 1024 - behind) / p.stage_bytes;
   if (p.stages > kMmMaxStages) p.stages = kMmMaxStages;
-  // Where the MMA warps take every other group, a stage has to be one warp's: a warp that met it as the other's could find
-  // the stage's barrier a whole round behind, which its parity does not tell from the round it waits for.
-  if (TN == 128) p.stages &= ~1;
   const int smem = 1024 + p.stages * p.stage_bytes + behind;
   MmMaps maps;
   if (!make_map_bytes(&maps.x, x, p.M, p.K, (uint32_t)rows) || !make_map_bytes(&maps.x_last, x, p.M, p.K, (uint32_t)tail_m) ||
-      !make_map_bytes(&maps.w, w, p.N, p.K, TN) || !make_map_bytes(&maps.w_last, w, p.N, p.K, (uint32_t)tail_n))
+      !make_map_bytes(&maps.w, w, p.N, p.K, kBox) || !make_map_bytes(&maps.w_last, w, p.N, p.K, (uint32_t)tail_n))
     return cudaErrorInvalidValue;
   maps.y = maps.x;
-  if (p.aligned && p.ns == 1 && !make_map_out(&maps.y, p.y, p.M, p.N)) return cudaErrorInvalidValue;
-  auto* kernel = q8_matmul_kernel<TN>;
+  if (p.aligned && !make_map_out(&maps.y, p.y, p.M, p.N)) return cudaErrorInvalidValue;
+  auto* kernel = q8_matmul_kernel<TN, PAIR>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
   if (e != cudaSuccess) return e;
   // a register split above the launch's own would wait for ever
@@ -493,8 +519,10 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
     return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs >= kMmRegs;
   }();
   if (!split) return cudaErrorInvalidConfiguration;
+  const int size = PAIR ? 2 : p.ns;
+  const int most = dc.num_sms / size;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ns > 1 ? p.ns * p.nitems : p.nitems < dc.num_sms ? p.nitems : dc.num_sms);
+  cfg.gridDim = dim3(size * (p.nitems < most || p.ns > 1 ? p.nitems : most));
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -502,11 +530,11 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.ns;
+  attr[1].val.clusterDim.x = size;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.ns > 1 ? 2 : 1;
+  cfg.numAttrs = size > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
@@ -524,12 +552,12 @@ cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w
   p.y = y;
   p.err = dc.err;
   p.wait_ns = wait_limit_ns();
-  const long long rows = (M + kMmTile - 1) / kMmTile, tiles = rows * ((N + 127) / 128);
-  // Many rows, and tiles of 128 x 256 for three quarters of the SMs: those.
-  if (rows > 1 && 4 * rows * ((N + 255) / 256) >= 3ll * dc.num_sms) return launch_mm<256>(x, w, p, dc, s);
+  const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
+  if (M > kMmTile && 2 * pairs >= dc.num_sms) return launch_mm<256, true>(x, w, p, dc, s);
+  const long long tiles = (long long)((M + kMmTile - 1) / kMmTile) * ((N + 127) / 128);
   // a tile's groups over as many CTAs as there are SMs for them
   while (p.ns < kMmMaxSplit && 2 * p.ns <= p.G && 2 * p.ns * tiles <= dc.num_sms) p.ns *= 2;
-  return launch_mm<128>(x, w, p, dc, s);
+  return launch_mm<128, false>(x, w, p, dc, s);
 }
 
 }  // namespace

@@ -54,17 +54,9 @@ inline bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D bf16 tensor [rows, cols] (cols contiguous, a multiple of 8) that boxes of 32 columns x 32 rows are stored to, from
-// rows of 64 bytes with the 64-byte swizzle.
+// 2-D bf16 tensor [rows, cols] (cols contiguous, a multiple of 8) that tiles of 64 columns x 32 rows are stored to.
 inline bool make_map_out(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * 2};
-  const cuuint32_t box[2] = {32, 32};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return make_map(m, base, rows, cols, 32);
 }
 
 // Gate/up weights as pairs: the gate row r and its up row r + half_rows of a
