@@ -104,6 +104,8 @@ class LsvError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load liblsv.so; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -564,27 +564,28 @@ def q8_scales_shape(rows, cols, weight=False):
 
 
 def _q8_outputs(x, codes, scales, weight):
-    """Check or make the codes and scales of x."""
-    if x.dim() != 2:
+    """Check or make the codes and scales of x; and its sizes."""
+    size = x.shape
+    if len(size) != 2:
         raise ValueError("an 8-bit matrix has two dimensions")
-    shape = q8_scales_shape(*x.shape, weight)
+    R, C = size
+    shape = (-(-R // 128) if weight else R, -(-C // 128))
     if codes is None:
-        codes = torch.empty(x.shape, dtype=E4M3, device=x.device)
-    elif codes.shape != x.shape:
-        raise ValueError("codes must have shape %s, got %s" % (tuple(x.shape), tuple(codes.shape)))
+        codes = torch.empty(size, dtype=E4M3, device=x.device)
+    elif codes.shape != size:
+        raise ValueError("codes must have shape %s, got %s" % (tuple(size), tuple(codes.shape)))
     if scales is None:
         scales = torch.empty(shape, dtype=F32, device=x.device)
     elif scales.shape != shape:
         raise ValueError("scales must have shape %s, got %s" % (shape, tuple(scales.shape)))
-    return codes, scales
+    return codes, scales, R, C
 
 
 def quantize_q8_rows(x, codes=None, scales=None, stream=None):
     """x [R, C] bf16 in 8 bits, a scale for 128 columns of a row: (codes [R, C] e4m3, scales [R, ceil(C/128)])."""
     dev = torch.cuda.current_device()
-    codes, scales = _q8_outputs(x, codes, scales, False)
+    codes, scales, R, C = _q8_outputs(x, codes, scales, False)
     xp, cp, sp = _here(dev, (x, BF16, "x"), (codes, E4M3, "codes"), (scales, F32, "scales"))
-    R, C = x.shape
     check("quantize_q8_rows", _ffi.load().quantize_q8_rows(xp, R, C, cp, sp, _stream_of(dev, stream)))
     return codes, scales
 
@@ -593,9 +594,8 @@ def quantize_q8_weight(w, codes=None, scales=None, stream=None):
     """w [N, K] bf16 in 8 bits, a scale for a block of 128 x 128: (codes [N, K] e4m3,
     scales [ceil(N/128), ceil(K/128)])."""
     dev = torch.cuda.current_device()
-    codes, scales = _q8_outputs(w, codes, scales, True)
+    codes, scales, N, K = _q8_outputs(w, codes, scales, True)
     wp, cp, sp = _here(dev, (w, BF16, "w"), (codes, E4M3, "codes"), (scales, F32, "scales"))
-    N, K = w.shape
     check("quantize_q8_weight", _ffi.load().quantize_q8_weight(wp, N, K, cp, sp, _stream_of(dev, stream)))
     return codes, scales
 
@@ -603,15 +603,17 @@ def quantize_q8_weight(w, codes=None, scales=None, stream=None):
 def dequantize_q8(codes, scales, out=None, stream=None):
     """bf16 values of an 8-bit matrix, rows or weight by the shape of its scales."""
     dev = torch.cuda.current_device()
-    if codes.dim() != 2:
+    size = codes.shape
+    if len(size) != 2:
         raise ValueError("codes must be [R, C]")
-    R, C = codes.shape
-    by = 1 if scales.shape == q8_scales_shape(R, C) else 128
-    if by == 128:
+    R, C = size
+    by = 1
+    if scales.shape != (R, -(-C // 128)):
+        by = 128
         _need_shape(scales, q8_scales_shape(R, C, True), "scales")
     if out is None:
         out = torch.empty((R, C), dtype=BF16, device=codes.device)
-    elif out.shape != (R, C):
+    elif out.shape != size:
         raise ValueError("out must have shape %s, got %s" % ((R, C), tuple(out.shape)))
     cp, sp, op = _here(dev, (codes, E4M3, "codes"), (scales, F32, "scales"), (out, BF16, "out"))
     check("dequantize_q8", _ffi.load().dequantize_q8(cp, sp, R, C, by, op, _stream_of(dev, stream)))
@@ -622,13 +624,13 @@ def rmsnorm_residual_q8(x, y=None, gain=None, x_out=None, codes=None, scales=Non
     """x_out = bf16(x + y) (in place unless x_out is given; y None: no residual, x stays), and RMSNorm(x_out) * gain
     as 8-bit rows: (codes [T, H] e4m3, scales [T, ceil(H/128)])."""
     dev = torch.cuda.current_device()
-    codes, scales = _q8_outputs(x, codes, scales, False)
+    codes, scales, T, H = _q8_outputs(x, codes, scales, False)
     if x_out is None:
         x_out = x
     if x_out.shape != x.shape or (y is not None and y.shape != x.shape):
         raise ValueError("x, y and x_out must have one shape")
-    T, H = x.shape
-    _need_shape(gain, (H,), "gain")
+    if gain is not None:
+        _need_shape(gain, (H,), "gain")
     xp, yp, gp, op, cp, sp = _here(dev, (x, BF16, "x"), (y, BF16, "y"), (gain, BF16, "gain"), (x_out, BF16, "x_out"),
                                    (codes, E4M3, "codes"), (scales, F32, "scales"))
     check("rmsnorm_residual_q8", _ffi.load().rmsnorm_residual_q8(xp, yp, gp, op, cp, sp, T, H, eps,
@@ -640,19 +642,21 @@ def dense_matmul_q8(x, x_scales, w, w_scales, out=None, stream=None):
     """out [M, N] = bf16(X W^T) of 8-bit rows X (x [M, K] e4m3, x_scales [M, ceil(K/128)]) and an 8-bit weight W
     (w [N, K] e4m3, w_scales [ceil(N/128), ceil(K/128)])."""
     dev = torch.cuda.current_device()
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 2 or xs[1] != ws[1]:
         raise ValueError("x [M, K] and w [N, K] must have the same K")
-    M, K = x.shape
-    N = w.shape[0]
-    if x_scales.shape != q8_scales_shape(M, K) or w_scales.shape != q8_scales_shape(N, K, True):
+    M, K = xs
+    N = ws[0]
+    G = -(-K // 128)
+    if x_scales.shape != (M, G) or w_scales.shape != (-(-N // 128), G):
         raise ValueError("x_scales must be %s and w_scales %s" % (q8_scales_shape(M, K), q8_scales_shape(N, K, True)))
     if out is None:
         out = torch.empty((M, N), dtype=BF16, device=x.device)
     elif out.shape != (M, N):
         raise ValueError("out must have shape %s, got %s" % ((M, N), tuple(out.shape)))
-    xp, xs, wp, ws, op = _here(dev, (x, E4M3, "x"), (x_scales, F32, "x_scales"), (w, E4M3, "w"),
-                               (w_scales, F32, "w_scales"), (out, BF16, "out"))
-    check("dense_matmul_q8", _ffi.load().dense_matmul_q8(xp, xs, wp, ws, op, M, N, K, _stream_of(dev, stream)))
+    ptrs = _here(dev, (x, E4M3, "x"), (x_scales, F32, "x_scales"), (w, E4M3, "w"), (w_scales, F32, "w_scales"),
+                 (out, BF16, "out"))
+    check("dense_matmul_q8", _ffi.load().dense_matmul_q8(*ptrs, M, N, K, _stream_of(dev, stream)))
     return out
 
 
@@ -661,24 +665,28 @@ def spec_logprobs(logits, tokens, n=0, logprob=None, entropy=None, top_ids=None,
     probability of tokens [...] (int32; -1: none, 0), the entropy of the distribution in nats, and its n most likely
     tokens (n <= 32)."""
     dev = torch.cuda.current_device()
-    if logits.dim() < 1 or logits.dtype not in (BF16, F32):
+    dtype, shape = logits.dtype, logits.shape
+    if not shape or (dtype != BF16 and dtype != F32):
         raise ValueError("logits must be [..., V], bf16 or fp32")
-    lead, V = logits.shape[:-1], logits.shape[-1]
-    tops = (*lead, n)
+    lead, tops = shape[:-1], (*shape[:-1], n)
     if tokens.shape != lead:
         raise ValueError("tokens must have shape %s, got %s" % (tuple(lead), tuple(tokens.shape)))
-    out = []
-    for t, dtype, shape, name in ((logprob, F32, lead, "logprob"), (entropy, F32, lead, "entropy"),
-                                  (top_ids, torch.int32, tops, "top_ids"), (top_logprobs, F32, tops, "top_logprobs")):
+
+    def have(t, dtype, shape, name):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=logits.device)
-        elif t.shape != shape:
+            return torch.empty(shape, dtype=dtype, device=logits.device)
+        if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-        out.append((t, dtype, name))
-    lp, tk, pp, ep, ip, qp = _here(dev, (logits, logits.dtype, "logits"), (tokens, torch.int32, "tokens"), *out)
-    check("spec_logprobs", _ffi.load().spec_logprobs(lp, logits.dtype == F32, tk, tokens.numel(), V, n, pp, ep, ip, qp,
+        return t
+
+    logprob, entropy = have(logprob, F32, lead, "logprob"), have(entropy, F32, lead, "entropy")
+    top_ids, top_logprobs = have(top_ids, torch.int32, tops, "top_ids"), have(top_logprobs, F32, tops, "top_logprobs")
+    lp, tk, pp, ep, ip, qp = _here(dev, (logits, dtype, "logits"), (tokens, torch.int32, "tokens"), (logprob, F32, "logprob"),
+                                   (entropy, F32, "entropy"), (top_ids, torch.int32, "top_ids"),
+                                   (top_logprobs, F32, "top_logprobs"))
+    check("spec_logprobs", _ffi.load().spec_logprobs(lp, dtype == F32, tk, tokens.numel(), shape[-1], n, pp, ep, ip, qp,
                                                      _stream_of(dev, stream)))
-    return tuple(t for t, _, _ in out)
+    return logprob, entropy, top_ids, top_logprobs
 
 
 def get_device_error(stream=None) -> int:

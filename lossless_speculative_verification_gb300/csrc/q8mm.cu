@@ -505,11 +505,15 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   if (p.stages > kMmMaxStages) p.stages = kMmMaxStages;
   const int smem = 1024 + p.stages * p.stage_bytes + behind;
   MmMaps maps;
-  if (!make_map_bytes(&maps.x, x, p.M, p.K, (uint32_t)rows) || !make_map_bytes(&maps.x_last, x, p.M, p.K, (uint32_t)tail_m) ||
-      !make_map_bytes(&maps.w, w, p.N, p.K, kBox) || !make_map_bytes(&maps.w_last, w, p.N, p.K, (uint32_t)tail_n))
+  if (!make_map_bytes(&maps.x, x, p.M, p.K, (uint32_t)rows) || !make_map_bytes(&maps.w, w, p.N, p.K, kBox))
+    return cudaErrorInvalidValue;
+  maps.x_last = maps.x;
+  maps.w_last = maps.w;
+  if ((tail_m != rows && !make_map_bytes(&maps.x_last, x, p.M, p.K, (uint32_t)tail_m)) ||
+      (tail_n != kBox && !make_map_bytes(&maps.w_last, w, p.N, p.K, (uint32_t)tail_n)))
     return cudaErrorInvalidValue;
   maps.y = maps.x;
-  if (p.aligned && !make_map_out(&maps.y, p.y, p.M, p.N)) return cudaErrorInvalidValue;
+  if (p.aligned && p.ns == 1 && !make_map_out(&maps.y, p.y, p.M, p.N)) return cudaErrorInvalidValue;
   auto* kernel = q8_matmul_kernel<TN, PAIR>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
   if (e != cudaSuccess) return e;
