@@ -34,6 +34,7 @@
 #include "ptx.cuh"
 #include "q4ptx.cuh"
 #include "q8.cuh"
+#include "q8ptx.cuh"
 #include "tmap.h"
 
 namespace lsv {
@@ -55,6 +56,8 @@ constexpr int kMmBlock = 4;          // groups whose scales are brought at once
 constexpr int kMmScaleSlots = 4;     // blocks of scales in shared memory
 constexpr int kMmScaleBytes = kMmScaleSlots * kMmBlock * kMmTile * 2 * 4;
 constexpr int kMmMaxSplit = 8;
+// What is in flight when a wait has run out is waited for this long, however short the limit of the waits.
+constexpr uint64_t kMmDrainNs = 2000000000ull;
 
 struct MmParams {
   int M, N, K, G;      // G: groups of K
@@ -106,6 +109,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[kBufs], tempty[kBufs], sfull[kMmScaleSlots],
       sempty[kMmScaleSlots], final_bar, recv_bar;
   __shared__ uint32_t tmem_slot;
+  __shared__ int gave_up, sent[2];  // a wait of this CTA or its pair ran out; groups loaded, of the pair's (sent[0]: own)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool clustered = PAIR || p.ns > 1;
   const uint32_t rank = clustered ? cluster_ctarank() : 0u;
@@ -131,6 +135,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     }
     mbar_init(&final_bar, 1);
     mbar_init(&recv_bar, 1);
+    gave_up = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -159,6 +164,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   // [slot][group of four][half of the columns][row]
   float* scales = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);
   uint8_t* behind = reinterpret_cast<uint8_t*>(scales) + kMmScaleBytes;
+  const uint64_t drain_ns = p.wait_ns > kMmDrainNs ? p.wait_ns : kMmDrainNs;
+  // By one lane of a role whose wait ran out, which issues nothing more; the others' waits run out after it.
+  auto give_up = [&]() {
+    set_error(p.err, kErrTimeout);
+    if constexpr (PAIR) {
+      st_shared_cluster_s32(mapa_shared(smem_u32(&gave_up), 0), 1);
+      st_shared_cluster_s32(mapa_shared(smem_u32(&gave_up), 1), 1);
+    } else {
+      gave_up = 1;
+    }
+  };
+  auto group_bytes = [&](int it) {  // of a group of tile `it`, a CTA's
+    const int tv = it / p.nm, tr = it - tv * p.nm;
+    return (tr == p.nm - 1 ? p.a_last : p.a_bytes) + (tv == ntn - 1 ? p.b_last : TN / (PAIR ? 2 : 1) * 128);
+  };
   pdl_trigger();
   pdl_wait();  // x and w may come from the preceding kernels
 
@@ -178,7 +198,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         const bool last_r = tr == p.nm - 1, last_v = tv == ntn - 1;
         const CUtensorMap* xm = last_r ? &maps.x_last : &maps.x;
         const CUtensorMap* wm = last_v ? &maps.w_last : &maps.w;
-        const int bytes = (last_r ? p.a_last : p.a_bytes) + (last_v ? p.b_last : TN / (PAIR ? 2 : 1) * 128);
+        const int bytes = group_bytes(it);
         const int row = tr * kTileM + (PAIR ? (int)rank * kMmTile : 0);
         const int col = tv * TN + (PAIR ? (int)rank * (TN / 2) : 0);
         for (int g = g0; g < g1; ++g) {
@@ -206,12 +226,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           }
         }
       }
-      if (!ok && lane == 0) {
-        set_error(p.err, kErrTimeout);
-        // the copies still in flight land before the CTA ends (the leader's barriers count a pair's)
-        if (leader)
-          for (int q = issued < p.stages ? 0 : issued - p.stages; q < issued; ++q)
-            mbar_wait(&full[q % p.stages], (uint32_t)(q / p.stages) & 1u, p.wait_ns);
+      if (lane == 0) {
+        if (!ok) give_up();
+        if constexpr (PAIR)
+          st_shared_cluster_s32(mapa_shared(smem_u32(&sent[rank]), 0), issued);
+        else
+          sent[0] = issued;
       }
     } else if (warp == 1 && leader) {
       // ---------------------------------------------------------- MMAs (the leader's, for a pair)
@@ -261,12 +281,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
       }
       // every MMA has completed before TMEM and the ring are given up
       if (elect_one()) {
-        if (!ok) set_error(p.err, kErrTimeout);
+        if (!ok) give_up();
         if constexpr (PAIR)
           umma_commit_pair_mc(&final_bar, 0x1);
         else
           umma_commit(&final_bar);
-        if (!mbar_wait(&final_bar, 0, p.wait_ns)) set_error(p.err, kErrTimeout);
+        if (!mbar_wait(&final_bar, 0, drain_ns)) set_error(p.err, kErrTimeout);
       }
     }
     if (warp >= 2) {
@@ -308,7 +328,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           }
         }
       }
-      if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+      if (!ok && lane == 0) give_up();
     }
     __syncwarp();
   } else {
@@ -437,7 +457,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
             st_async_f4(mapa_shared(smem_u32(recv + at), (uint32_t)dst), v, mapa_shared(smem_u32(&recv_bar), (uint32_t)dst));
         }
         named_bar_sync(1, 256);  // this CTA's own share is there, and the receive barrier is armed
-        const bool got = mbar_wait_cluster(&recv_bar, 0, p.wait_ns);
+        const bool got = mbar_wait_cluster(&recv_bar, 0, drain_ns);  // (it is also the sums on their way here)
         if (!got) set_error(p.err, kErrTimeout);
         const int tid = threadIdx.x - 128;
         for (int u = tid; got && u < cols4 * kMmTile; u += 256) {
@@ -459,7 +479,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         }
       }
     }
-    if (!ok && lane == 0) set_error(p.err, kErrTimeout);
+    if (!ok && lane == 0) give_up();
     tmem_ld_wait();  // what a wait that ran out left in flight
     if (lane == 0) bulk_wait_all();
   }
@@ -470,6 +490,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     cluster_sync();  // nobody's copies, MMAs or sums go to a CTA that has ended
   else
     __syncthreads();
+  if (gave_up) {
+    // The copies still in flight land before a CTA ends; nobody issues any more.  A pair's are counted together, on the
+    // leader's barriers: there a group that only one of the two asked for is made up for.
+    if (threadIdx.x == 0 && leader) {
+      const int n = g1 - g0, mine = sent[0], theirs = PAIR ? sent[1] : mine, most = max(mine, theirs);
+      for (int q = mine; q < most; ++q)
+        mbar_arrive_expect_tx(&full[q % p.stages], group_bytes(first + q / n * step));
+      for (int q = theirs; q < most; ++q)
+        mbar_complete_tx(&full[q % p.stages], group_bytes(first + q / n * step));
+      for (int q = max(0, most - p.stages); q < most; ++q)
+        if (!mbar_wait(&full[q % p.stages], (uint32_t)(q / p.stages) & 1u, drain_ns)) set_error(p.err, kErrTimeout);
+    }
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after_sync();
     if constexpr (PAIR)
@@ -477,6 +512,20 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
     else
       tmem_dealloc(tmem_base, kBufs * TN);
   }
+}
+
+// 2-D tensor of bytes [rows, cols] (cols contiguous, a multiple of 16), box = 128 columns x box_rows, 128-byte
+// swizzle, zero fill outside the tensor.
+bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int round8(int v) { return (v + 7) / 8 * 8; }
@@ -513,7 +562,7 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
       (tail_n != kBox && !make_map_bytes(&maps.w_last, w, p.N, p.K, (uint32_t)tail_n)))
     return cudaErrorInvalidValue;
   maps.y = maps.x;
-  if (p.aligned && p.ns == 1 && !make_map_out(&maps.y, p.y, p.M, p.N)) return cudaErrorInvalidValue;
+  if (p.aligned && p.ns == 1 && !make_map(&maps.y, p.y, p.M, p.N, 32)) return cudaErrorInvalidValue;
   auto* kernel = q8_matmul_kernel<TN, PAIR>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
   if (e != cudaSuccess) return e;

@@ -40,25 +40,6 @@ inline bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t c
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D tensor of bytes [rows, cols] (cols contiguous, a multiple of 16), box = 128 columns x box_rows, 128-byte
-// swizzle, zero fill outside the tensor.
-inline bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 2-D bf16 tensor [rows, cols] (cols contiguous, a multiple of 8) that tiles of 64 columns x 32 rows are stored to.
-inline bool make_map_out(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols) {
-  return make_map(m, base, rows, cols, 32);
-}
-
 // Gate/up weights as pairs: the gate row r and its up row r + half_rows of a
 // [.., cols] bf16 matrix, viewed as dims {cols, 2, rows}.  A box {64, 2, 64}
 // stages 64 features as 128 interleaved rows (gate 0, up 0, gate 1, up 1, ...)

@@ -292,6 +292,26 @@ def test_call_behind_call(M, N, K):
         assert torch.equal(o.view(torch.int16), want.view(torch.int16))
 
 
+# A split, persistent CTAs, and pairs whose last tiles are short
+@pytest.mark.parametrize("M,N,K", [(5, 1280, 1296), (1, 129280, 1280), (128, 40000, 656), (700, 9728, 1296), (129, 40001, 400)])
+def test_a_product_whose_waits_run_out_says_so_and_the_next_call_is_right(M, N, K):
+    ops = cuda(*operands(M + N, M, N, K))
+    ref = api.dense_matmul_q8(*ops).view(torch.int16).clone()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    try:
+        api.set_wait_limit_ns(1)
+        for turn in range(4):
+            flush.fill_(turn)                                   # the operands come from memory again
+            got = api.dense_matmul_q8(*ops)
+            err = api.get_device_error()
+            assert err in (0, 6)                                # a wait may end before anyone looks at the time
+            if err == 0:
+                assert torch.equal(got.view(torch.int16), ref)
+    finally:
+        api.set_wait_limit_ns(2000000000)
+    assert torch.equal(api.dense_matmul_q8(*ops).view(torch.int16), ref)
+
+
 def test_two_calls_at_once():
     a, b = (cuda(*operands(k, 128, 30000, 1280)) for k in (1, 2))
     ra, rb = api.dense_matmul_q8(*a), api.dense_matmul_q8(*b)
