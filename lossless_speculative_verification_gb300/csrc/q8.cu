@@ -7,13 +7,19 @@
 // bf16 values meet exact ties that the scale's own rounding decides), and it costs no precision: e4m3 is a floating
 // format, and only values below 2^-13 of a group's largest lose a bit more than with the finest scale.
 //
-// All four kernels are bound by their bytes.  16 lanes x 8 columns (one 16-byte load a lane) are a group, so that its
-// maximum meets in four shuffles and nothing is read twice.
+// All four kernels are bound by their bytes, and have few instructions to spare beside them (values go two at a time
+// wherever there is an instruction for it).  16 lanes x 8 columns (one 16-byte load a lane) are a group, so that its
+// maximum meets in four shuffles and nothing is read twice.  Of 9760 x 1280, with what is read and written over the
+// time: the residual and norm 16.1 us, 5.4 TB/s; quantising 8.2 us, 4.6; reading back 7.0 us, 5.3.  A weight of
+// 129280 x 1280 72 us, 6.9.  One row of 1280: 1.7, 1.3 and 1.0 us.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "lsv.h"
 #include "ptx.cuh"
+#include "q4ptx.cuh"
 #include "q8.cuh"
 
 namespace lsv {
@@ -23,13 +29,11 @@ constexpr int kQ8Slot = 256;     // columns that a warp takes at once
 constexpr int kQ8Vecs = 2;       // slots a warp holds at most
 constexpr int kQ8MaxWarps = 32;  // warps a row
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// Eight values are four pairs, which the FP32 pipes take two at a time.
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -37,14 +41,30 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// |x| as bits: ordered like the values, and at or above 0x7F800000 for an infinity or a NaN.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// The sum of two pairs of bf16 values, rounded to bf16 (as their sum in 32 bits rounded would be: where that is not
+// exact, one value is below half a step of the other).
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 s =
+      __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
 
-__device__ __forceinline__ uint32_t max8(const float (&f)[8]) {
-  uint32_t m = abs_bits(f[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = max(m, abs_bits(f[i]));
-  return m;
+// The largest |x| as bits: ordered like the values, and above 0x7F800000 where one is a NaN.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ uint32_t max8(const float2 (&f)[4]) {
+  const float a = max_abs(max_abs(f[0].x, f[0].y), max_abs(f[1].x, f[1].y));
+  const float b = max_abs(max_abs(f[2].x, f[2].y), max_abs(f[3].x, f[3].y));
+  return __float_as_uint(max_abs(a, b));
+}
+// The same of eight bf16 values, whose bits are ordered like them too: two at a time.
+__device__ __forceinline__ uint32_t max8(const uint4& v) {
+  const uint32_t m =
+      __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  return max(m << 16, m & 0xFFFF0000u);
 }
 
 // The scale of a group whose largest |x| has these bits, and its reciprocal: 448 = 1.75 * 2^8.
@@ -54,116 +74,128 @@ __device__ __forceinline__ float scale_of(uint32_t amax, float& inv) {
   return __uint_as_float(amax >= 0x7F800000u ? 0x7FC00000u : (uint32_t)e << 23);
 }
 
-__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t cvt4(float2 a, float2 b) {
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
-  return make_uint2(cvt4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                    cvt4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+__device__ __forceinline__ uint2 codes8(const float2 (&f)[4], float inv) {
+  const float2 by = make_float2(inv, inv);
+  return make_uint2(cvt4(mul2(f[0], by), mul2(f[1], by)), cvt4(mul2(f[2], by), mul2(f[3], by)));
 }
 
 // ------------------------------------------------------------------------------------------------ rows
 // A row is `wpr` warps, `rows` rows are a CTA; warp w of a row takes the slots w, w + wpr, .. of 256 columns, VECS at
 // most, and holds them in registers between the sum of squares and the codes, so that x, y and the output move once.
+// MANY (rows that are a CTA each): a CTA takes one after the other, and loads the next while it works on this one.
 //
-// The normalised value is f / sqrt(mean f^2 + eps) with the root's reciprocal as a pair r + r2 (r2: what rounding r
-// to 32 bits left out, from the residual of m r^2), so that h is off by little more than its own rounding: codes
-// next to a tie then fall as the formula has them but for 2^-24 of the values next to it.
-template <int VECS, bool NORM>
+// The normalised value is f / sqrt(mean f^2 + eps) with the root's reciprocal as a pair r + r2 (r2: what the
+// approximation r left out, from the residual of m r^2), so that h is off by little more than its own rounding: codes
+// next to a tie then fall as the formula has them but for 2^-24 of the values next to it.  by_h + by_h2 is 1 / H.
+template <int VECS, bool NORM, bool MANY>
 __global__ void __launch_bounds__(1024) q8_rows_kernel(const bf16* x, const bf16* __restrict__ y, bf16* x_out,
                                                        const bf16* __restrict__ gain, uint8_t* __restrict__ codes,
                                                        float* __restrict__ scales, int T, int H, int wpr, int rows,
-                                                       float eps) {
-  __shared__ float part[kQ8MaxWarps];
+                                                       float eps, float by_h, float by_h2) {
+  __shared__ float part[MANY ? 2 : 1][kQ8MaxWarps];  // (two: a warp may be a row ahead of another)
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rl = warp / wpr, w = warp - rl * wpr;
-  const int t = blockIdx.x * rows + rl;
-  const bool live = t < T;
   const int G = (H + kQ8Group - 1) / kQ8Group;
-  const size_t base = (size_t)t * H;
-  uint4 v[VECS];
+  int t = blockIdx.x * rows + rl, turn = 0;
+  uint4 v[VECS], u[VECS], nv[VECS], nu[VECS];  // x and y of this row and of the next
+  auto load = [&](uint4(&a)[VECS], uint4(&b)[VECS], int t) {
 #pragma unroll
-  for (int i = 0; i < VECS; ++i) {
-    const int c = (w + i * wpr) * kQ8Slot + lane * 8;
-    v[i] = live && c < H ? ld_stream128(x + base + c) : make_uint4(0, 0, 0, 0);
-  }
-  float r = 1.0f, r2 = 0.0f;
-  if constexpr (NORM) {
-    float ss = 0.0f;
-    if (y) {
-      uint4 u[VECS];
+    for (int i = 0; i < VECS; ++i) {
+      const int c = (w + i * wpr) * kQ8Slot + lane * 8;
+      const bool there = t < T && c < H;
+      a[i] = there ? ld_stream128(x + (size_t)t * H + c) : make_uint4(0, 0, 0, 0);
+      if (NORM && y) b[i] = there ? ld_stream128(y + (size_t)t * H + c) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load(v, u, t);
+  while (true) {
+    const bool live = t < T;
+    const size_t base = (size_t)t * H;
+    const int t_next = t + (int)gridDim.x;
+    if constexpr (MANY) load(nv, nu, t_next);
+    float r = 1.0f, r2 = 0.0f;
+    if constexpr (NORM) {
+      float2 sq = make_float2(0.0f, 0.0f);
+      if (y) {
 #pragma unroll
-      for (int i = 0; i < VECS; ++i) {
-        const int c = (w + i * wpr) * kQ8Slot + lane * 8;
-        u[i] = live && c < H ? ld_stream128(y + base + c) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < VECS; ++i) {
+          const int c = (w + i * wpr) * kQ8Slot + lane * 8;
+          v[i] = make_uint4(add_bf16x2(v[i].x, u[i].x), add_bf16x2(v[i].y, u[i].y), add_bf16x2(v[i].z, u[i].z),
+                            add_bf16x2(v[i].w, u[i].w));
+          if (live && c < H) *reinterpret_cast<uint4*>(x_out + base + c) = v[i];
+        }
       }
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
-        const int c = (w + i * wpr) * kQ8Slot + lane * 8;
-        float a[8], b[8];
-        unpack8(v[i], a);
-        unpack8(u[i], b);
-        v[i] = make_uint4(pack2(a[0] + b[0], a[1] + b[1]), pack2(a[2] + b[2], a[3] + b[3]),
-                          pack2(a[4] + b[4], a[5] + b[5]), pack2(a[6] + b[6], a[7] + b[7]));
-        if (live && c < H) *reinterpret_cast<uint4*>(x_out + base + c) = v[i];
+        float2 f[4];
+        unpack8(v[i], f);
+        // squares of bf16 are exact in 32 bits
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sq = fma2(f[j], f[j], sq);
       }
+      float ss = sq.x + sq.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (wpr > 1) {
+        if (lane == 0) part[turn][warp] = ss;
+        __syncthreads();
+        ss = lane < wpr ? part[turn][rl * wpr + lane] : 0.0f;
+        if (MANY) turn ^= 1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      }
+      const float m = fmaf(ss, by_h, fmaf(ss, by_h2, eps));
+      r = rsqrtf(m);
+      const float q = m * r;
+      // 1 - m r^2, exact but for its own rounding; a mean of zero, infinity or NaN has no correction
+      const float left = fmaf(-q, r, 1.0f) - fmaf(m, r, -q) * r;
+      r2 = 0.5f * r * left;
+      if (!(fabsf(r2) < r)) r2 = 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-      float f[8];
+      const int slot = w + i * wpr;
+      if (slot * kQ8Slot >= H) break;
+      const int c = slot * kQ8Slot + lane * 8;
+  float2 f[4];
+      uint32_t m;
       unpack8(v[i], f);
-      // pairwise: squares of bf16 are exact in 32 bits
-      const float p0 = fmaf(f[1], f[1], f[0] * f[0]), p1 = fmaf(f[3], f[3], f[2] * f[2]);
-      const float p2 = fmaf(f[5], f[5], f[4] * f[4]), p3 = fmaf(f[7], f[7], f[6] * f[6]);
-      ss += (p0 + p1) + (p2 + p3);
-    }
+      if constexpr (NORM) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (wpr > 1) {
-      if (lane == 0) part[warp] = ss;
-      __syncthreads();
-      ss = lane < wpr ? part[rl * wpr + lane] : 0.0f;
+        for (int j = 0; j < 4; ++j) f[j] = fma2(f[j], make_float2(r2, r2), mul2(f[j], make_float2(r, r)));
+        if (gain && c < H) {
+          float2 g[4];
+          unpack8(ld_plain128(gain + c), g);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    }
-    const float m = ss / (float)H + eps;
-    r = 1.0f / sqrtf(m);
-    const float q = m * r;
-    // 1 - m r^2, exact but for its own rounding; a mean of zero, infinity or NaN has no correction
-    const float left = fmaf(-q, r, 1.0f) - fmaf(m, r, -q) * r;
-    r2 = 0.5f * r * left;
-    if (!(fabsf(r2) < r)) r2 = 0.0f;
-  }
+          for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], g[j]);
+        }
+        m = max8(f);
+      } else {
+        m = max8(v[i]);
+      }
 #pragma unroll
-  for (int i = 0; i < VECS; ++i) {
-    const int slot = w + i * wpr;
-    if (slot * kQ8Slot >= H) break;
-    const int c = slot * kQ8Slot + lane * 8;
-    float f[8];
-    unpack8(v[i], f);
-    if constexpr (NORM) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = fmaf(f[j], r2, f[j] * r);
-      if (gain && c < H) {
-        float g[8];
-        unpack8(ld_plain128(gain + c), g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= g[j];
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float inv;
+      const float s = scale_of(m, inv);
+      if (live && c < H) {
+        *reinterpret_cast<uint2*>(codes + base + c) = codes8(f, inv);
+        if ((lane & 15) == 0) scales[(size_t)t * G + c / kQ8Group] = s;
       }
     }
-    uint32_t m = max8(f);
+    if (!MANY || t_next >= T) break;
+    t = t_next;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float inv;
-    const float s = scale_of(m, inv);
-    if (live && c < H) {
-      *reinterpret_cast<uint2*>(codes + base + c) = codes8(f, inv);
-      if ((lane & 15) == 0) scales[(size_t)t * G + c / kQ8Group] = s;
+    for (int i = 0; i < VECS; ++i) {
+      v[i] = nv[i];
+      u[i] = nu[i];
     }
   }
 }
@@ -184,11 +216,7 @@ __global__ void __launch_bounds__(256) q8_weight_kernel(const bf16* __restrict__
                                     : make_uint4(0, 0, 0, 0);
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float f[8];
-    unpack8(v[i], f);
-    m = max(m, max8(f));
-  }
+  for (int i = 0; i < 8; ++i) m = max(m, max8(v[i]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -200,7 +228,7 @@ __global__ void __launch_bounds__(256) q8_weight_kernel(const bf16* __restrict__
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (c >= K || n0 + 16 * i >= N) continue;
-    float f[8];
+    float2 f[4];
     unpack8(v[i], f);
     *reinterpret_cast<uint2*>(codes + (size_t)(n0 + 16 * i) * K + c) = codes8(f, inv);
   }
@@ -217,33 +245,38 @@ __device__ __forceinline__ uint32_t values2(uint32_t two, float s) {
   return pack2(f.x * s, f.y * s);
 }
 
+// Quotients of the pieces' places by the pieces a row, `per`, as products with 2^64 / per and 2^32 / per rounded up:
+// exact for places whose product with per is below 2^64 and 2^32.  (Divisions took a third of the time: 4879 x 1280
+// 5.8 us with them, 4.4 without.)
+struct Q8Read {
+  long long pieces;
+  int per, G, shift;  // shift: 0, or 7 where 128 rows share a scale
+  uint64_t by_per64;
+  uint32_t by_per32;
+};
+
 __global__ void __launch_bounds__(256) q8_read_kernel(const uint8_t* __restrict__ codes,
                                                       const float* __restrict__ scales, bf16* __restrict__ out,
-                                                      int R, int C, int by) {
+                                                      const Q8Read p) {
   pdl_wait();
   pdl_trigger();
-  const int per = C / 8, G = (C + kQ8Group - 1) / kQ8Group;
   const long long p0 = (long long)blockIdx.x * (256 * kQ8ReadPieces);
-  const int row0 = (int)(p0 / per);
-  const int col0 = (int)(p0 - (long long)row0 * per);
+  const long long row0 = (long long)__umul64hi((uint64_t)p0, p.by_per64);
+  const int col0 = (int)(p0 - row0 * p.per) + (int)threadIdx.x;
+  const long long q0 = p0 + threadIdx.x;
   uint2 v[kQ8ReadPieces];
   float s[kQ8ReadPieces];
-  size_t at[kQ8ReadPieces];
-  bool live[kQ8ReadPieces];
 #pragma unroll
   for (int i = 0; i < kQ8ReadPieces; ++i) {
-    const int c = col0 + (int)threadIdx.x + 256 * i;
-    const int dr = c / per, row = row0 + dr, col = (c - dr * per) * 8;
-    live[i] = row < R;
-    at[i] = (size_t)row * C + col;
-    if (!live[i]) continue;
-    v[i] = ld_stream64(codes + at[i]);
-    s[i] = ld_plain_f32(scales + (size_t)(row / by) * G + col / kQ8Group);
+    if (q0 + 256 * i >= p.pieces) break;
+    const int c = col0 + 256 * i, dr = (int)__umulhi((uint32_t)c, p.by_per32);
+    v[i] = ld_stream64(codes + 8 * (q0 + 256 * i));
+    s[i] = ld_plain_f32(scales + ((row0 + dr) >> p.shift) * p.G + (c - dr * p.per) / (kQ8Group / 8));
   }
 #pragma unroll
   for (int i = 0; i < kQ8ReadPieces; ++i) {
-    if (!live[i]) continue;
-    *reinterpret_cast<uint4*>(out + at[i]) =
+    if (q0 + 256 * i >= p.pieces) break;
+    *reinterpret_cast<uint4*>(out + 8 * (q0 + 256 * i)) =
         make_uint4(values2(v[i].x & 0xFFFFu, s[i]), values2(v[i].x >> 16, s[i]), values2(v[i].y & 0xFFFFu, s[i]),
                    values2(v[i].y >> 16, s[i]));
   }
@@ -252,19 +285,26 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const uint8_t* __restrict_
 cudaError_t launch_rows(bool norm, const bf16* x, const bf16* y, bf16* x_out, const bf16* gain, uint8_t* codes,
                         float* scales, int T, int H, float eps, const DeviceCtx& dc, cudaStream_t s) {
   const int slots = (H + kQ8Slot - 1) / kQ8Slot;
-  // One slot a warp for short rows, two for longer ones, which then have fewer warps to meet: the norm of 9760 x 1280
-  // takes 18.1 us with one and 18.5 with two, of 1500 x 7168 18.7 and 18.0; quantising 9760 x 1280 alone, where no warp
-  // waits for another, 10.7 and 9.0, and 60000 x 208, a slot a row, 10.7 and 11.4.
-  const bool wide = slots > (norm ? 8 : 1);
+  // One slot a warp for short rows, two for longer ones, which then have fewer warps to meet: the norm of 1500 x 7168
+  // takes 17.4 us with one and 14.9 with two, of 9760 x 1280 16.1 with either; quantising 9760 x 1280 alone 10.6 and 8.3,
+  // 60000 x 208, a slot a row, 10.3 and 11.3.  Rows of more than eight slots one after the other, two CTAs an SM: the norm
+  // of 1500 x 7168 13.9 us (a CTA a row 14.9), of 3000 x 4096 15.4 (15.7), of 733 x 7120 9.0 (8.8).
+  const bool wide = slots > (norm ? 8 : 1), many = slots > 8;
   const int vecs = wide ? kQ8Vecs : 1;
   const int wpr = (slots + vecs - 1) / vecs;
   const int rows = wpr >= 8 ? 1 : 8 / wpr;
-  const dim3 grid((T + rows - 1) / rows), block(32 * wpr * rows);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, block, 0, s, x, y, x_out, gain, codes, scales, T, H, wpr, rows, eps);
+  const int ctas = (T + rows - 1) / rows, threads = 32 * wpr * rows;
+  const float by_h = (float)(1.0 / H), by_h2 = (float)(1.0 / H - by_h);
+  auto go = [&](auto kernel, int grid) {
+    return launch_pdl(kernel, dim3(grid), dim3(threads), 0, s, x, y, x_out, gain, codes, scales, T, H, wpr, rows, eps, by_h,
+                      by_h2);
   };
-  if (norm) return wide ? go(q8_rows_kernel<kQ8Vecs, true>) : go(q8_rows_kernel<1, true>);
-  return wide ? go(q8_rows_kernel<kQ8Vecs, false>) : go(q8_rows_kernel<1, false>);
+  if (many) {
+    const int grid = std::min(ctas, dc.num_sms * (1024 / threads));
+    return norm ? go(q8_rows_kernel<kQ8Vecs, true, true>, grid) : go(q8_rows_kernel<kQ8Vecs, false, true>, grid);
+  }
+  if (norm) return go(q8_rows_kernel<1, true, false>, ctas);
+  return wide ? go(q8_rows_kernel<kQ8Vecs, false, false>, ctas) : go(q8_rows_kernel<1, false, false>, ctas);
 }
 
 // Sizes of an 8-bit matrix.
@@ -335,10 +375,17 @@ lsv_status dequantize_q8(const void* codes, const float* scales, int32_t R, int3
   if (st != LSV_OK || R == 0) return st;
   if (!codes || !scales || !out) return LSV_ERR_INVALID_ARG;
   if (!aligned({codes, scales, out})) return LSV_ERR_MISALIGNED;
-  const long long pieces = (long long)R * (C / 8), per = 256 * kQ8ReadPieces;
-  return launch_pdl(q8_read_kernel, dim3((unsigned)((pieces + per - 1) / per)), dim3(256), 0,
+  Q8Read p;
+  p.per = C / 8;
+  p.pieces = (long long)R * p.per;
+  p.G = (C + kQ8Group - 1) / kQ8Group;
+  p.shift = rows_per_scale == 1 ? 0 : 7;
+  p.by_per64 = ~0ull / p.per + 1;
+  p.by_per32 = ~0u / p.per + 1;
+  const long long a_cta = 256 * kQ8ReadPieces;
+  return launch_pdl(q8_read_kernel, dim3((unsigned)((p.pieces + a_cta - 1) / a_cta)), dim3(256), 0,
                     reinterpret_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(codes), scales,
-                    static_cast<bf16*>(out), R, C, rows_per_scale) == cudaSuccess
+                    static_cast<bf16*>(out), p) == cudaSuccess
              ? LSV_OK
              : LSV_ERR_CUDA;
 }
