@@ -11,8 +11,9 @@
 // lower token), so that equal logits, which bf16 makes frequent, are no special case.  They lie in the n vectors (16
 // bytes of logits) of the largest maxima, so that vectors are collected, by keys of their maxima and places.  Of the
 // first logits of every thread, 64 groups of threads give a bound, the n-th largest of their maxima, which n vectors
-// reach and few others; where many have come all the same, the n-th largest of them is the new bound.  At the end the
-// vectors, some dozens, are ranked by counting, and the logits of the first n of them, from the bound on, once more.
+// reach and few others; every fourth batch the n-th largest of what has come is the new one (2440 x 100277 fp32 156 us
+// with it, 168 without).  At the end the vectors, some dozens, are ranked by counting, and the logits of the first n of
+// them, from the bound on, once more.
 //
 // A row is one CTA, or a cluster of up to 16 where there are few rows: its CTAs take a piece each, and rank 0 joins
 // their sums and ranks their candidates, through distributed shared memory, in a fixed order.
@@ -36,7 +37,6 @@ constexpr int kLpBatch = 4;        // 16-byte vectors a thread takes at once
 constexpr int kLpMaxTop = 32;      // most alternatives
 static_assert(kLpBatch == 4, "max_of");
 constexpr int kLpCandidates = 1024;  // room for the vectors that are collected
-constexpr int kLpMany = 256;         // so many, and the bound rises
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpFew = 128;          // vectors whose logits are looked at without ranking them first
 static_assert(kLpWide <= kLpCandidates, "the threads' largest");
@@ -59,15 +59,28 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Sums over a part of a row, relative to its maximum.  A NaN or +infinity makes s NaN, and it stays so.
+// e^(x - m) is 2^l with l = x log2 e + c, c = -m log2 e as it is rounded: one FMA a logit, and what the rounding of c
+// leaves out is the same factor in every term (`left_out` of its logarithm).  Maxima of 1e37 and more, where c could
+// overflow, take l = 2^-90 (x - m): logits that differ at all differ by 1024 there.
+__device__ __forceinline__ bool huge(float m) { return !(fabsf(m) < 1e37f); }
+__device__ __forceinline__ float2 line(float m) {  // l = x * .x + .y
+  const float by = huge(m) ? 0x1p-90f : kLog2e;
+  return make_float2(by, __fmul_rn(-m, by));
+}
+__device__ __forceinline__ float left_out(float m) { return huge(m) ? 0.0f : fmaf(m, kLog2e, __fmul_rn(-m, kLog2e)); }
+
+// Sums over a part of a row, relative to its maximum m: s = sum 2^l, d = sum l 2^l.  A NaN or +infinity makes s NaN, and
+// it stays so.
 struct Part {
   float m, s, d;
 };
 __device__ __forceinline__ void move_to(Part& a, float m) {
   if (a.s != 0.0f) {
-    const float by = a.m - m, c = ex2_ftz(by * kLog2e);
+    const float by =
+        huge(a.m) || huge(m) ? (a.m - m) * kLog2e : __fadd_rn(__fmul_rn(-m, kLog2e), __fmul_rn(a.m, kLog2e));
+    const float c = ex2_ftz(by);
     a.d = c > 0.0f || isnan(c) ? c * fmaf(by, a.s, a.d) : 0.0f;
     a.s *= c;
   }
@@ -87,9 +100,15 @@ __device__ __forceinline__ Part join_lanes(Part a, int width) {
 __device__ __forceinline__ void add_one(Part& a, float x) {
   if (!(x <= a.m)) move_to(a, x);
   if (a.m == -INFINITY) return;
-  const float t = max_nan(x - a.m, -1000.0f), e = ex2_ftz(t * kLog2e);
+  const float2 at = line(a.m);
+  const float l = huge(a.m) ? max_nan(x - a.m, -1000.0f) : max_nan(fmaf(x, at.x, at.y), -1000.0f), e = ex2_ftz(l);
   a.s += e;
-  a.d = fmaf(t, e, a.d);
+  a.d = fmaf(l, e, a.d);
+}
+// Logits below it add nothing to s; raised to it they add nothing to d either, where -inf and the type's lowest value
+// would add 0 * inf: m - 1000, or low enough for the rounding to bf16.  (Huge maxima have d = 0 instead.)
+__device__ __forceinline__ float lowest_that_adds(float m) {
+  return huge(m) ? -INFINITY : m - fmaxf(1000.0f, fabsf(m) * 0x1p-5f);
 }
 
 template <typename T>
@@ -115,6 +134,12 @@ struct Vec<bf16> {
     const Two m = __hmax2_nan(__hmax2_nan(two_max(v[0]), two_max(v[1])), __hmax2_nan(two_max(v[2]), two_max(v[3])));
     return max_nan(__low2float(m), __high2float(m));
   }
+  static __device__ __forceinline__ Two low(float f) { return __float2bfloat162_rn(f); }
+  static __device__ __forceinline__ void raise(uint4& v, Two low) {
+    Two* t = reinterpret_cast<Two*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = __hmax2_nan(t[i], low);
+  }
   static __device__ __forceinline__ float get(const bf16* p) { return __bfloat162float(*p); }
 };
 template <>
@@ -130,6 +155,12 @@ struct Vec<float> {
   }
   static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpBatch]) {
     return max_nan(max_nan(max_of(v[0]), max_of(v[1])), max_nan(max_of(v[2]), max_of(v[3])));
+  }
+  static __device__ __forceinline__ float low(float f) { return f; }
+  static __device__ __forceinline__ void raise(uint4& v, float low) {
+    float* t = reinterpret_cast<float*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = max_nan(t[i], low);
   }
   static __device__ __forceinline__ float get(const float* p) { return *p; }
 };
@@ -161,11 +192,11 @@ __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b_reversed,
 // larger ones, counted by 1 to 32 threads.
 template <int THREADS>
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int cnt, uint64_t* dst, int n) {
-  int by = 32;
-  while (by > 1 && by * cnt > THREADS) by >>= 1;
-  const int each = THREADS / by, part = threadIdx.x & (by - 1);
+  int log_by = 5;
+  while (log_by > 0 && cnt << log_by > THREADS) --log_by;
+  const int by = 1 << log_by, each = THREADS >> log_by, part = threadIdx.x & (by - 1);
   for (int i0 = 0; i0 < cnt; i0 += each) {
-    const int i = i0 + (int)threadIdx.x / by;
+    const int i = i0 + ((int)threadIdx.x >> log_by);
     const uint64_t k = i < cnt ? keys[i] : 0;
     int r = 0;
 #pragma unroll 4
@@ -230,7 +261,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     bound = sm.bound;
     bv = bound ? key_value(bound) : -INFINITY;
   };
-  float2 s2 = make_float2(0.f, 0.f), d2 = s2;
+  float2 s2 = make_float2(0.f, 0.f), d2 = s2, at = s2;
+  auto low = Vec<T>::low(-INFINITY);
   const int batches = (k1 - k0 + kLpBatch * THREADS - 1) / (kLpBatch * THREADS);
 #pragma unroll 1
   for (int b = 0; b < batches; ++b) {
@@ -246,26 +278,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       move_to(a, bm);
       s2 = make_float2(a.s, 0.f);
       d2 = make_float2(a.d, 0.f);
+      at = line(a.m);
+      low = Vec<T>::low(lowest_that_adds(a.m));
     }
-    if (a.m != -INFINITY) {  // else nothing but -inf so far
-      const float2 neg = make_float2(-a.m, -a.m);
-#pragma unroll
-      for (int i = 0; i < kLpBatch; ++i)
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          float2 t = add2(Vec<T>::two(u[i], j), neg);
-          // -inf counts as e^-1000 = 0, so that it adds 0 and not 0 * inf
-          t.x = max_nan(t.x, -1000.0f);
-          t.y = max_nan(t.y, -1000.0f);
-          const float2 l = mul2(t, make_float2(kLog2e, kLog2e));
-          const float2 e = make_float2(ex2_ftz(l.x), ex2_ftz(l.y));
-          s2 = add2(s2, e);
-          d2 = fma2(t, e, d2);
-        }
-    }
-    if (n == 0) continue;
-    if (b == 0) {
-      // the first bound: each thread's vector of the largest maximum, and the groups' places among them
+    if (b == 0 && n > 0) {
+      // The first bound: each thread's vector of the largest maximum, a group's largest of them (of fewer threads where
+      // there are few vectors), and the groups' places among themselves, below.
       uint64_t key = 0;
       if (k < k1 && !isnan(bm)) {
         int first = 0;
@@ -275,18 +293,34 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         if (Vec<T>::max_of(u[0]) == bm) first = 0;
         key = lp_key(bm, k + first * THREADS);
       }
-      // group g: the threads g, g + 64, .., so that a short row makes as many groups as it has vectors
-      sm.cand[tid] = key;
-      __syncthreads();
-      const int mine = tid / kInGroup, part = tid % kInGroup;
-      key = sm.cand[part * kLpGroups + mine];
-#pragma unroll
-      for (int o = 1; o < kInGroup; o <<= 1) {
+      int o = 1;
+      for (; o < kInGroup && o * kLpGroups < k1 - k0; o <<= 1) {
         const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
         key = other > key ? other : key;
       }
-      if (part == 0) sm.group[mine] = key;
+      if ((tid & (o - 1)) == 0 && tid < o * kLpGroups) sm.group[tid / o] = key;
+    }
+    if (a.m != -INFINITY) {  // else nothing but -inf so far
+      const float2 mul = make_float2(at.x, at.x), add = make_float2(at.y, at.y);
+#pragma unroll
+      for (int i = 0; i < kLpBatch; ++i) {
+        uint4 w = u[i];
+        Vec<T>::raise(w, low);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          const float2 l = fma2(Vec<T>::two(w, j), mul, add);
+          const float2 e = make_float2(ex2_ftz(l.x), ex2_ftz(l.y));
+          s2 = add2(s2, e);
+          d2 = fma2(l, e, d2);
+        }
+      }
+      if (huge(a.m)) d2 = make_float2(0.f, 0.f);
+    }
+    if (n == 0) continue;
+    if (b == 0) {
       __syncthreads();
+      const int mine = tid / kInGroup, part = tid % kInGroup;  // a group is ranked by so many
+      const uint64_t key = sm.group[mine];
       int r = 0;
 #pragma unroll
       for (int j = part; j < kLpGroups; j += kInGroup) r += sm.group[j] > key || (sm.group[j] == key && j < mine);
@@ -311,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     if ((b & 3) == 3 && b + 1 < batches) {
       __syncthreads();
       const int cnt = sm.ncand;
-      if (cnt > kLpMany && cnt <= kLpCandidates) {
+      if (cnt > 2 * n + 8 && cnt <= kLpCandidates) {
         rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
         __syncthreads();
         if (tid < n) sm.cand[tid] = sm.group[tid];
@@ -334,26 +368,34 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   const float ex = edge >= 0 ? Vec<T>::get(x + edge) : -INFINITY;
   if (edge >= 0) add_one(a, ex);
 
+  if (n > 0) __syncthreads();  // every candidate is there
+  const int cnt = n > 0 ? sm.ncand : 0;
+  // The logits of the vectors, of the first n of them where they are many, from the bound on.
+  const uint64_t* from = sm.cand;
+  int vectors = cnt;
+  if (cnt > kLpFew && cnt <= kLpCandidates) {
+    rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
+    __syncthreads();
+    from = sm.group;
+    vectors = n;
+    bv = key_value(sm.group[n - 1]);
+  }
+  const bool room = cnt <= kLpCandidates;
+  int t0 = -1;
+  float f0 = 0.0f;
+  if (room && tid < vectors * N) {
+    t0 = head + key_token(from[tid / N]) * N + tid % N;
+    f0 = Vec<T>::get(x + t0);  // on its way while the lanes' sums are joined
+  }
   a = join_lanes(a, 32);
   if (lane == 0) sm.warp[warp] = a;
   if (n > 0) {
-    __syncthreads();
-    const int cnt = sm.ncand;
-    if (cnt <= kLpCandidates) {
-      // The logits of the vectors, of the first n of them where they are many, from the bound on.
-      const uint64_t* from = sm.cand;
-      int vectors = cnt;
-      if (cnt > kLpFew) {
-        rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
-        __syncthreads();
-        from = sm.group;
-        vectors = n;
-        bv = key_value(sm.group[n - 1]);
-      }
+    if (room) {
       auto offer = [&](float f, int t) {
         if (!(f < bv)) sm.last[atomicAdd(&sm.nlast, 1)] = lp_key(f, t);
       };
-      for (int i = tid; i < vectors * N; i += THREADS) {
+      if (t0 >= 0) offer(f0, t0);
+      for (int i = tid + THREADS; i < vectors * N; i += THREADS) {
         const int t = head + key_token(from[i / N]) * N + i % N;
         offer(Vec<T>::get(x + t), t);
       }
@@ -394,17 +436,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       }
     }
   }
-  __syncthreads();
-  if (warp == 0) {
+  if (n == 0 || !room) __syncthreads();  // the warps' sums are there
+  if (warp == kWarps - 1) {              // (the others rank)
     a = join_lanes(sm.warp[lane & (kWarps - 1)], kWarps);
     if (lane == 0) sm.parts[0] = a;
   }
+  __syncthreads();
 
   // ------------------------------------------------------------ the cluster's
   if (cs > 1) {
     cluster_wait();
     if (rank > 0 && warp == 0) {
       if (lane == 0) {
+        a = sm.parts[0];
         const uint32_t to = mapa_shared(smem_u32(&sm.parts[rank]), 0);
         st_shared_cluster_f32(to, a.m);
         st_shared_cluster_f32(to + 4, a.s);
@@ -437,25 +481,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   a = sm.parts[0];
   const bool bad = isnan(a.s);      // a NaN or +infinity among the logits
   const bool none = a.s == 0.0f;    // nothing but -inf
-  const float log_s = logf(a.s);
-  if (tid == 0) {
-    if (entropy) entropy[row] = bad ? NAN : none ? 0.0f : log_s - a.d / a.s;
-    if (logprob) {
-      float p = 0.0f;  // -1: no token
-      if (token < -1 || token >= V) {
-        set_error(err, kErrDeviceIndex);
-        p = NAN;
-      } else if (token >= 0) {
-        p = bad ? NAN : none ? -INFINITY : (at_token - a.m) - log_s;
-      }
-      logprob[row] = p;
+  const float log_s = logf(a.s), log_sum = log_s - left_out(a.m) * kLn2;
+  if (tid == 0 && logprob) {
+    float p = 0.0f;  // -1: no token
+    if (token < -1 || token >= V) {
+      set_error(err, kErrDeviceIndex);
+      p = NAN;
+    } else if (token >= 0) {
+      p = bad ? NAN : none ? -INFINITY : (at_token - a.m) - log_sum;
     }
+    logprob[row] = p;
   }
+  if (tid == 32 && entropy) entropy[row] = bad ? NAN : none ? 0.0f : fmaf(-kLn2, a.d / a.s, log_s);
   if (tid < n) {
     const uint64_t k = sm.top[0][tid];
     const bool there = k != 0 && !bad;
     top_ids[(size_t)row * n + tid] = there ? key_token(k) : -1;
-    top_logprobs[(size_t)row * n + tid] = bad ? NAN : !there || none ? -INFINITY : (key_value(k) - a.m) - log_s;
+    top_logprobs[(size_t)row * n + tid] = bad ? NAN : !there || none ? -INFINITY : (key_value(k) - a.m) - log_sum;
   }
 }
 
@@ -464,14 +506,17 @@ cudaError_t launch_logprobs(const T* logits, const int32_t* tokens, int R, int V
                             int32_t* top_ids, float* top_logprobs, const DeviceCtx& dc, cudaStream_t s) {
   // Many rows: narrow CTAs, four an SM; up to two rows an SM, so many that they fill it; few rows (a quarter of the SMs
   // at most): narrow ones again, as many a row (a cluster) as are on the GPU at once, each with a vector a thread at
-  // least.  Of 129280 bf16 logits and 20 tokens: one row 5.7 us (a cluster of 8 wide CTAs 7.7), 16 rows 7.5 (13.9), 128
-  // rows 13.9 (clusters of 4 narrow ones 17.1), 300 rows 27 (narrow 36).  Rows of one batch gain nothing from threads.
+  // least.  Of 129280 bf16 logits and 20 tokens: 128 rows 13.3 us (clusters of 4 narrow ones 17.2, of 2 middle ones
+  // 15.0), 300 rows 21.4 (narrow 25.2), 600 rows and 5 tokens 33.2 (middle 35.3).  Rows of one batch gain nothing from
+  // threads.  Clusters of 16 are not placed everywhere at once: one row 5.2 us (8: 5.6), 10 rows 6.1 (6.8), 32 rows 10.9
+  // (8: 7.6).
   const long long bytes = (long long)V * (long long)sizeof(T);
   const bool few = 4ll * R <= dc.num_sms, wide = !few && R <= dc.num_sms;
   const bool narrow = few || R > 2 * dc.num_sms || bytes <= kLpNarrow * kLpBatch * 16;
   const int threads = narrow ? kLpNarrow : wide ? kLpWide : kLpMiddle;
+  const int most = 10ll * R <= dc.num_sms ? kLpMaxCluster : kLpMaxCluster / 2;
   int cs = 1;
-  while (cs < kLpMaxCluster && (long long)R * cs * 2 * threads <= 1024ll * dc.num_sms && bytes >= 2ll * cs * threads * 16)
+  while (cs < most && (long long)R * cs * 2 * threads <= 1024ll * dc.num_sms && bytes >= 2ll * cs * threads * 16)
     cs *= 2;
   auto* kernel = narrow ? logprobs_kernel<T, kLpNarrow>
                         : wide ? logprobs_kernel<T, kLpWide> : logprobs_kernel<T, kLpMiddle>;
