@@ -56,6 +56,8 @@ class Decoder:
     layer in 8 bits.  verify() runs one verify pass over Q positions per sequence, for the first
     tokens.shape[0] <= B sequences."""
 
+    weights = "bf16"
+
     def __init__(self, prob, B: int, L: int, device="cuda", cache: str = "bf16", page: int = 64, pages: int | None = None,
                  weights: str = "bf16"):
         if cache not in ("bf16", "q4"):
