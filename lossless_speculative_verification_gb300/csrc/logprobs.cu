@@ -62,14 +62,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // e^(x - m) is 2^l with l = x log2 e + c, c = -m log2 e as it is rounded: one FMA a logit, and what the rounding of c
-// leaves out is the same factor in every term (`left_out` of its logarithm).  Maxima of 1e37 and more, where c could
-// overflow, take l = 2^-90 (x - m): logits that differ at all differ by 1024 there.
-__device__ __forceinline__ bool huge(float m) { return !(fabsf(m) < 1e37f); }
-__device__ __forceinline__ float2 line(float m) {  // l = x * .x + .y
-  const float by = huge(m) ? 0x1p-90f : kLog2e;
-  return make_float2(by, __fmul_rn(-m, by));
-}
-__device__ __forceinline__ float left_out(float m) { return huge(m) ? 0.0f : fmaf(m, kLog2e, __fmul_rn(-m, kLog2e)); }
+// leaves out is the same factor in every term (its logarithm to base 2).  For a maximum of 2^16 and more, where that
+// factor may be anything, l = (x - m) log2 e, two operations.
+__device__ __forceinline__ bool large(float m) { return !(fabsf(m) < 65536.0f); }
+__device__ __forceinline__ float left_out(float m) { return large(m) ? 0.0f : fmaf(m, kLog2e, __fmul_rn(-m, kLog2e)); }
 
 // Sums over a part of a row, relative to its maximum m: s = sum 2^l, d = sum l 2^l.  A NaN or +infinity makes s NaN, and
 // it stays so.
@@ -78,9 +74,7 @@ struct Part {
 };
 __device__ __forceinline__ void move_to(Part& a, float m) {
   if (a.s != 0.0f) {
-    const float by =
-        huge(a.m) || huge(m) ? (a.m - m) * kLog2e : __fadd_rn(__fmul_rn(-m, kLog2e), __fmul_rn(a.m, kLog2e));
-    const float c = ex2_ftz(by);
+    const float by = (a.m - m) * kLog2e + (left_out(m) - left_out(a.m)), c = ex2_ftz(by);
     a.d = c > 0.0f || isnan(c) ? c * fmaf(by, a.s, a.d) : 0.0f;
     a.s *= c;
   }
@@ -100,17 +94,12 @@ __device__ __forceinline__ Part join_lanes(Part a, int width) {
 __device__ __forceinline__ void add_one(Part& a, float x) {
   if (!(x <= a.m)) move_to(a, x);
   if (a.m == -INFINITY) return;
-  const float2 at = line(a.m);
-  const float l = huge(a.m) ? max_nan(x - a.m, -1000.0f) : max_nan(fmaf(x, at.x, at.y), -1000.0f), e = ex2_ftz(l);
+  // (-inf counts as e^-1000 = 0, so that it adds 0 and not 0 * inf)
+  const float l = max_nan(large(a.m) ? (x - a.m) * kLog2e : fmaf(x, kLog2e, __fmul_rn(-a.m, kLog2e)), -1000.0f);
+  const float e = ex2_ftz(l);
   a.s += e;
   a.d = fmaf(l, e, a.d);
 }
-// Logits below it add nothing to s; raised to it they add nothing to d either, where -inf and the type's lowest value
-// would add 0 * inf: m - 1000, or low enough for the rounding to bf16.  (Huge maxima have d = 0 instead.)
-__device__ __forceinline__ float lowest_that_adds(float m) {
-  return huge(m) ? -INFINITY : m - fmaxf(1000.0f, fabsf(m) * 0x1p-5f);
-}
-
 template <typename T>
 struct Vec;
 template <>
@@ -261,8 +250,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     bound = sm.bound;
     bv = bound ? key_value(bound) : -INFINITY;
   };
-  float2 s2 = make_float2(0.f, 0.f), d2 = s2, at = s2;
-  auto low = Vec<T>::low(-INFINITY);
+  float2 s2 = make_float2(0.f, 0.f), d2 = s2;
+  float c = 0.0f;                   // of l
+  auto low = Vec<T>::low(0.0f);
   const int batches = (k1 - k0 + kLpBatch * THREADS - 1) / (kLpBatch * THREADS);
 #pragma unroll 1
   for (int b = 0; b < batches; ++b) {
@@ -278,8 +268,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       move_to(a, bm);
       s2 = make_float2(a.s, 0.f);
       d2 = make_float2(a.d, 0.f);
-      at = line(a.m);
-      low = Vec<T>::low(lowest_that_adds(a.m));
+      c = __fmul_rn(-a.m, kLog2e);
+      // logits below it add nothing to s; raised to it they add nothing to d either, where -inf and the type's lowest
+      // value would add 0 * inf
+      low = Vec<T>::low(a.m - 1000.0f);
     }
     if (b == 0 && n > 0) {
       // The first bound: each thread's vector of the largest maximum, a group's largest of them (of fewer threads where
@@ -300,8 +292,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       }
       if ((tid & (o - 1)) == 0 && tid < o * kLpGroups) sm.group[tid / o] = key;
     }
-    if (a.m != -INFINITY) {  // else nothing but -inf so far
-      const float2 mul = make_float2(at.x, at.x), add = make_float2(at.y, at.y);
+    if (!large(a.m)) {
+      const float2 mul = make_float2(kLog2e, kLog2e), add = make_float2(c, c);
 #pragma unroll
       for (int i = 0; i < kLpBatch; ++i) {
         uint4 w = u[i];
@@ -314,7 +306,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
           d2 = fma2(l, e, d2);
         }
       }
-      if (huge(a.m)) d2 = make_float2(0.f, 0.f);
+    } else if (a.m != -INFINITY) {  // (nothing but -inf so far)
+      // read once more, so that this rare form takes no registers from the other
+#pragma unroll 1
+      for (int q = k; q < min(k1, k + kLpBatch * THREADS); q += THREADS) {
+        const uint4 w = ld_plain128(xv + (size_t)q * N);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          const float2 f = Vec<T>::two(w, j);
+          const float2 l = make_float2(max_nan((f.x - a.m) * kLog2e, -1000.0f), max_nan((f.y - a.m) * kLog2e, -1000.0f));
+          const float2 e = make_float2(ex2_ftz(l.x), ex2_ftz(l.y));
+          s2 = add2(s2, e);
+          d2 = fma2(l, e, d2);
+        }
+      }
     }
     if (n == 0) continue;
     if (b == 0) {

@@ -84,6 +84,23 @@ def test_every_form(R, V, dtype):
     check(logits(R, R, V, dtype), 20, what="%d x %d " % (R, V))
 
 
+@pytest.mark.parametrize("R,V", [(1, 129280), (70, 9001), (400, 3001)])
+def test_logits_of_any_size(R, V):
+    # what the sums are relative to is a product with log2 e: rows around and beyond the size where its rounding counts
+    for k, at in enumerate((0.0, 700.0, -65000.0, 65535.5, -65536.0, 65536.0, 1e5, -3e6, 1e7, -1e9, 1e12, 3e38, -3e38)):
+        x = logits(k, R, V, torch.float32, spread=1.0)
+        step = float(np.spacing(np.float32(abs(at) + 32)))      # so that logits there are not all the same
+        check((x * max(1.0, step) + at).clamp(-3.3e38, 3.3e38), 7, what="around %g " % at)
+    # half of a row around each size
+    x = logits(9, R, V, torch.float32, spread=1.0)
+    x[:, V // 2:] += 65530.0
+    x[:, :V // 2] += 65538.0
+    check(x, 7, what="around 2^16 ")
+    check(torch.cat([x[:, V // 2:], x[:, :V // 2]], 1), 7, what="around 2^16, rising ")
+    check(logits(10, R, V, torch.bfloat16, spread=900.0), 7, what="wide ")
+    check(logits(11, R, V, torch.bfloat16, spread=1e6), 7, what="far ")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("R,V", [(1, 129280), (40, 30001), (130, 17000), (310, 4001), (3, 200)])
 def test_rows_that_are_no_ordinary_ones(R, V, dtype):
