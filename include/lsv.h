@@ -482,7 +482,7 @@ lsv_status rmsnorm_residual(void *x, const void *y, void *h, int32_t T, int32_t 
  * code * s.  A group that holds a NaN or an infinity has s = NaN and stands for NaN.
  * The last group of a row, and the last blocks of a weight, may be short.
  *   codes [R, C] e4m3 bytes; scales [R, ceil(C/128)] fp32 (rows) or
- *   [ceil(R/128), ceil(C/128)] (weights).  C % 16 == 0, 16 <= C <= 16384, R*C < 2^40.
+ *   [ceil(R/128), ceil(C/128)] (weights).  C % 16 == 0, 16 <= C <= 16384, R <= 2^26.
  * Device pointers, 16-byte aligned.  One launch each.
  *
  * quantize_q8_rows: x [R, C] bf16 as rows.   quantize_q8_weight: w [N, K] bf16.
@@ -496,7 +496,7 @@ lsv_status rmsnorm_residual(void *x, const void *y, void *h, int32_t T, int32_t 
  *   squares do not sum to a finite fp32 value is not normalised as it should be.
  * dense_matmul_q8: y [M, N] = bf16(sum over groups g of x_scales[m, g] *
  *   w_scales[n / 128, g] * sum_{k in g} x[m, k] w[n, k]), x as rows, w as a weight, N of
- *   any size.  The products of a group are summed on the tensor cores, the groups in
+ *   any size up to 2^26.  The products of a group are summed on the tensor cores, the groups in
  *   fp32 in a fixed order; scales may be any numbers whose products are normal fp32.  Up to 128
  *   rows of x, a row's result does not depend on the others or on M.  No workspace. */
 lsv_status quantize_q8_rows(const void *x, int32_t R, int32_t C, void *codes, float *scales, lsv_stream stream);

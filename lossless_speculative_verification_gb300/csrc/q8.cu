@@ -310,7 +310,7 @@ cudaError_t launch_rows(bool norm, const bf16* x, const bf16* y, bf16* x_out, co
 // Sizes of an 8-bit matrix.
 lsv_status check_q8(int64_t rows, int64_t cols) {
   if (rows < 0 || cols <= 0) return LSV_ERR_INVALID_ARG;
-  if (cols % 16 || cols > kQ8MaxCols || rows * cols >= (1ll << 40)) return LSV_ERR_UNSUPPORTED;
+  if (cols % 16 || cols > kQ8MaxCols || rows > kQ8MaxRows) return LSV_ERR_UNSUPPORTED;
   return LSV_OK;
 }
 

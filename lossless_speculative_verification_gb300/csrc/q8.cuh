@@ -7,7 +7,8 @@
 namespace lsv {
 
 constexpr int kQ8Group = 128;      // columns (of a weight: rows and columns) that share a scale
-constexpr int kQ8MaxCols = 16384;  // columns of a row
+constexpr int kQ8MaxCols = 16384;    // columns of a row
+constexpr int kQ8MaxRows = 1 << 26;  // rows of a matrix
 
 // Loads of what an earlier kernel of the stream wrote.  A kernel that is launched before that one ends may not take
 // them through the read-only path (what it loads must not change while it runs), which the compiler picks for

@@ -29,6 +29,8 @@
 // on how many rows there are.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "lsv.h"
 #include "ptx.cuh"
@@ -567,11 +569,14 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
   if (e != cudaSuccess) return e;
   // a register split above the launch's own would wait for ever
-  static const bool split = [&] {
+  static std::atomic<bool> split{false};
+  if (!split.load(std::memory_order_relaxed)) {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs >= kMmRegs;
-  }();
-  if (!split) return cudaErrorInvalidConfiguration;
+    e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < kMmRegs) return cudaErrorInvalidConfiguration;
+    split.store(true, std::memory_order_relaxed);
+  }
   const int size = PAIR ? 2 : p.ns;
   const int most = dc.num_sms / size;
   cudaLaunchConfig_t cfg = {};
@@ -621,7 +626,8 @@ using namespace lsv;
 extern "C" lsv_status dense_matmul_q8(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
                                       int32_t M, int32_t N, int32_t K, lsv_stream stream) {
   if (M < 0 || N < 0 || K <= 0) return LSV_ERR_INVALID_ARG;
-  if (K % 16 || K > kQ8MaxCols || ((long long)M + 127) / 128 * (((long long)N + 127) / 128) >= (1ll << 30))
+  if (K % 16 || K > kQ8MaxCols || M > kQ8MaxRows || N > kQ8MaxRows ||
+      ((long long)M + 127) / 128 * (((long long)N + 127) / 128) >= (1ll << 30))
     return LSV_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return LSV_OK;
   if (!x || !x_scales || !w || !w_scales || !y) return LSV_ERR_INVALID_ARG;

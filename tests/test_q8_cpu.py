@@ -95,6 +95,7 @@ def test_refusals(lib):
         assert f(odd, 4, 128, p, p, None) == 3
         assert f(p, 4, 128, odd, p, None) == 3
         assert f(p, 2 ** 31 - 1, 16384, p, p, None) == 2        # 2^45 values
+        assert f(p, 2 ** 26 + 1, 16, p, p, None) == 2
         assert f(None, 0, 128, None, None, None) == 0
     assert lib.dequantize_q8(p, p, 4, 128, 2, p, None) == 1     # rows of a scale: 1 or 128
     assert lib.dequantize_q8(p, p, 4, 100, 1, p, None) == 2
@@ -115,6 +116,8 @@ def test_refusals(lib):
     assert mm(p, None, p, p, p, 4, 8, 128, None) == 1
     assert mm(p, p, odd, p, p, 4, 8, 128, None) == 3
     assert mm(p, p, p, p, p, 2 ** 31 - 1, 2 ** 31 - 1, 128, None) == 2
+    assert mm(p, p, p, p, p, 2 ** 31 - 1, 1, 16, None) == 2
+    assert mm(p, p, p, p, p, 1, 2 ** 31 - 1, 16, None) == 2
     assert mm(None, None, None, None, None, 0, 8, 128, None) == 0
     assert mm(None, None, None, None, None, 4, 0, 128, None) == 0
     lp = lib.spec_logprobs
