@@ -21,9 +21,12 @@
 // - more tiles than SMs: persistent CTAs take them row tiles first, so that a weight tile is read from HBM once;
 // - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
 //
+// Output goes by TMA while the next tile runs where its rows begin on 16 bytes; others are written by the warps, whole
+// rows at a time (2440 x 129279 x 1280 578 us; each thread its own row 3036).
+//
 // What bounds the pairs is the sums' own loop, some 180 instructions a warp and group that wait on one another (a group
-// takes 1.1 K cycles, its MMAs 512): 2440 x 129280 x 1280 takes 422 us (1.92 PFLOP/s), 4879 x 1280 x 7168 59 us, of which
-// the FMAs alone are 9 and waiting for the scales 5.  One CTA a tile of 128 x 256 with two warps that issue MMAs: 460 and
+// takes 1.1 K cycles, its MMAs 512): 2440 x 129280 x 1280 takes 426 us (1.90 PFLOP/s), 4879 x 1280 x 7168 59 us, of
+// which the FMAs alone are 9 and waiting for the scales 5.  One CTA a tile of 128 x 256 with two warps that issue MMAs: 460 and
 // 63 us; twice the warps with half the columns each: 479 and 68; accumulators handed over in halves: 417 and 63.
 // All sums are of a fixed order: results are the same from run to run, and up to 128 rows a row's bits do not depend
 // on how many rows there are.
@@ -58,6 +61,7 @@ constexpr int kMmBlock = 4;          // groups whose scales are brought at once
 constexpr int kMmScaleSlots = 4;     // blocks of scales in shared memory
 constexpr int kMmScaleBytes = kMmScaleSlots * kMmBlock * kMmTile * 2 * 4;
 constexpr int kMmMaxSplit = 8;
+constexpr int kMmRowsAtOnce = 8;     // rows of output that a warp holds on their way to where TMA does not store
 // What is in flight when a wait has run out is waited for this long, however short the limit of the waits.
 constexpr uint64_t kMmDrainNs = 2000000000ull;
 
@@ -83,6 +87,41 @@ __device__ __forceinline__ uint32_t mm_pack(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
+
+// A warp's `rows` x `cols` (64 at most) of output from rows of 128 bytes, 16-byte pieces swizzled, to rows of y that begin
+// anywhere: a row's values by the whole warp, two a lane from its first 4-byte boundary on.  What depends on where a row
+// begins is the same in every other row.
+__device__ __forceinline__ void store_panel(const uint8_t* panel, bf16* y, int N, int cols, int rows, int lane) {
+  uint16_t* to = reinterpret_cast<uint16_t*>(y) + 2 * lane;
+  int odd[2];
+  bool both[2], one[2], first[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    odd[k] = ((int)(reinterpret_cast<uintptr_t>(y) >> 1) ^ (k & N)) & 1;
+    both[k] = 2 * lane + odd[k] + 1 < cols;
+    one[k] = 2 * lane + odd[k] + 1 == cols;
+    first[k] = odd[k] && lane == 0 && cols > 0;
+  }
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += kMmRowsAtOnce) {
+    uint32_t two[kMmRowsAtOnce], next[kMmRowsAtOnce];
+#pragma unroll
+    for (int i = 0; i < kMmRowsAtOnce; ++i)  // (rows of the panel that do not exist are read, and not stored)
+      two[i] = *reinterpret_cast<const uint32_t*>(panel + (r0 + i) * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
+#pragma unroll
+    for (int i = 0; i < kMmRowsAtOnce; ++i) next[i] = __shfl_down_sync(0xffffffffu, two[i], 1);
+#pragma unroll
+    for (int i = 0; i < kMmRowsAtOnce; ++i, to += N) {
+      const int k = i & 1;
+      const uint32_t v = __byte_perm(two[i], next[i], odd[k] ? 0x5432 : 0x3210);
+      const bool there = r0 + i < rows;
+      if (there && both[k]) *reinterpret_cast<uint32_t*>(to + odd[k]) = v;
+      if (there && one[k]) to[odd[k]] = (uint16_t)v;
+      if (there && first[k]) *to = (uint16_t)two[i];
+    }
+  }
+}
+static_assert(kMmRowsAtOnce % 8 == 0, "the swizzle's period");
 
 // Four groups' scales of a row, those from `g` (a multiple of 4) on that lie within [0, G).
 __device__ __forceinline__ float4 load_scales(const float* s, int g, int G) {
@@ -411,11 +450,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         }
       }
       if (PAIR || p.ns == 1) {
-        if (ok && any && p.aligned) {
+        if (ok && any) {
           // to shared memory as 128-byte rows, 16-byte pieces swizzled as TMA has them, and out while the next tile runs
 #pragma unroll
           for (int q = 0; q < kCols / 64; ++q) {
-            if (lane == 0) bulk_wait_read();
+            if (p.aligned && lane == 0) bulk_wait_read();
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -424,16 +463,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
               for (int j = 0; j < 4; ++j) v[j] = mm_pack(acc[32 * q + 4 * i + j].x, acc[32 * q + 4 * i + j].y);
               *reinterpret_cast<uint4*>(panel + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
             }
-            fence_proxy_async_shared();
+            if (p.aligned) fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0 && n0 + 64 * q < p.N) tma_store_2d(&maps.y, panel, n0 + 64 * q, row0);
-          }
-        } else if (ok && mine) {
-          bf16* y = p.y + (size_t)row * p.N + n0;
-#pragma unroll
-          for (int j = 0; j < kCols / 2; ++j) {
-            if (n0 + 2 * j < p.N) y[2 * j] = __float2bfloat16_rn(acc[j].x);
-            if (n0 + 2 * j + 1 < p.N) y[2 * j + 1] = __float2bfloat16_rn(acc[j].y);
+            const int n = n0 + 64 * q;
+            if (!p.aligned)
+              store_panel(panel, p.y + (size_t)row0 * p.N + n, p.N, min(64, p.N - n), min(32, p.M - row0), lane);
+            else if (lane == 0 && n < p.N)
+              tma_store_2d(&maps.y, panel, n, row0);
           }
         }
       } else {
@@ -462,6 +498,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         const bool got = mbar_wait_cluster(&recv_bar, 0, drain_ns);  // (it is also the sums on their way here)
         if (!got) set_error(p.err, kErrTimeout);
         const int tid = threadIdx.x - 128;
+        uint8_t* staged = smem;  // rows that TMA's alignment does not hold for: [row][column], in the free ring
+        const int stride = cols4 * 8 + 8, cols = min(4 * cols4, p.N - (tv * TN + (int)rank * cols4 * 4));
         for (int u = tid; got && u < cols4 * kMmTile; u += 256) {
           const int rl = u & (kMmTile - 1), c4 = u / kMmTile;
           const int m = tr * kTileM + rl, n = tv * TN + ((int)rank * cols4 + c4) * 4;
@@ -471,12 +509,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
             const float4 v = recv[(q * cols4 + c4) * kMmTile + rl];
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
           }
-          bf16* y = p.y + (size_t)m * p.N + n;
-          if (p.aligned) {
-            *reinterpret_cast<uint2*>(y) = make_uint2(mm_pack(s.x, s.y), mm_pack(s.z, s.w));
-          } else {
-            const float o[4] = {s.x, s.y, s.z, s.w};
-            for (int j = 0; j < 4 && n + j < p.N; ++j) y[j] = __float2bfloat16_rn(o[j]);
+          const uint2 v = make_uint2(mm_pack(s.x, s.y), mm_pack(s.z, s.w));
+          *reinterpret_cast<uint2*>(p.aligned ? reinterpret_cast<uint8_t*>(p.y + (size_t)m * p.N + n)
+                                              : staged + rl * stride + c4 * 8) = v;
+        }
+        if (!p.aligned) {
+          // neighbouring values by neighbouring lanes
+          named_bar_sync(1, 256);
+          const int log_w = __ffs(4 * cols4) - 1, there = min(kMmTile, p.M - tr * kTileM) << log_w;
+          bf16* y = p.y + (size_t)(tr * kTileM) * p.N + tv * TN + (int)rank * cols4 * 4;
+#pragma unroll 4
+          for (int u = tid; u < there; u += 256) {
+            const int rl = u >> log_w, c = u - (rl << log_w);
+            if (got && c < cols) y[(size_t)rl * p.N + c] = *reinterpret_cast<const bf16*>(staged + rl * stride + c * 2);
           }
         }
       }
