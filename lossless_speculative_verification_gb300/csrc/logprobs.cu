@@ -31,15 +31,13 @@
 namespace lsv {
 namespace {
 
-constexpr int kLpWide = 1024, kLpMiddle = 512, kLpNarrow = 256;  // threads a CTA
+constexpr int kLpWide = 512, kLpNarrow = 256;  // threads a CTA
 constexpr int kLpGroups = 64;
-constexpr int kLpBatch = 4;        // 16-byte vectors a thread takes at once
+constexpr int kLpLong = 8, kLpShort = 4;  // 16-byte vectors a thread takes at once
 constexpr int kLpMaxTop = 32;      // most alternatives
-static_assert(kLpBatch == 4, "max_of");
 constexpr int kLpCandidates = 1024;  // room for the vectors that are collected
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpFew = 128;          // vectors whose logits are looked at without ranking them first
-static_assert(kLpWide <= kLpCandidates, "the threads' largest");
 static_assert(kLpMaxTop <= kLpGroups && kLpMaxTop == 32 && kLpMaxCluster <= 2 * kLpNarrow / 32, "lists");
 
 // Larger value first, then the lower token; never 0.  -0 and 0 are equal.
@@ -119,9 +117,16 @@ struct Vec<bf16> {
     const Two m = two_max(v);
     return max_nan(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpBatch]) {
-    const Two m = __hmax2_nan(__hmax2_nan(two_max(v[0]), two_max(v[1])), __hmax2_nan(two_max(v[2]), two_max(v[3])));
-    return max_nan(__low2float(m), __high2float(m));
+  template <int B>
+  static __device__ __forceinline__ float max_of(const uint4 (&v)[B]) {
+    Two m[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) m[i] = two_max(v[i]);
+#pragma unroll
+    for (int o = 1; o < B; o *= 2)
+#pragma unroll
+      for (int i = 0; i < B; i += 2 * o) m[i] = __hmax2_nan(m[i], m[i + o]);
+    return max_nan(__low2float(m[0]), __high2float(m[0]));
   }
   static __device__ __forceinline__ Two low(float f) { return __float2bfloat162_rn(f); }
   static __device__ __forceinline__ void raise(uint4& v, Two low) {
@@ -142,8 +147,16 @@ struct Vec<float> {
   static __device__ __forceinline__ float max_of(const uint4& v) {
     return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
-  static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpBatch]) {
-    return max_nan(max_nan(max_of(v[0]), max_of(v[1])), max_nan(max_of(v[2]), max_of(v[3])));
+  template <int B>
+  static __device__ __forceinline__ float max_of(const uint4 (&v)[B]) {
+    float m[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) m[i] = max_of(v[i]);
+#pragma unroll
+    for (int o = 1; o < B; o *= 2)
+#pragma unroll
+      for (int i = 0; i < B; i += 2 * o) m[i] = max_nan(m[i], m[i + o]);
+    return m[0];
   }
   static __device__ __forceinline__ float low(float f) { return f; }
   static __device__ __forceinline__ void raise(uint4& v, float low) {
@@ -184,7 +197,8 @@ __device__ __forceinline__ void rank_keys(const uint64_t* keys, int cnt, uint64_
   int log_by = 5;
   while (log_by > 0 && cnt << log_by > THREADS) --log_by;
   const int by = 1 << log_by, each = THREADS >> log_by, part = threadIdx.x & (by - 1);
-  for (int i0 = 0; i0 < cnt; i0 += each) {
+  // (warps that have no key left are done)
+  for (int i0 = 0; i0 + ((int)(threadIdx.x & ~31u) >> log_by) < cnt; i0 += each) {
     const int i = i0 + ((int)threadIdx.x >> log_by);
     const uint64_t k = i < cnt ? keys[i] : 0;
     int r = 0;
@@ -198,10 +212,12 @@ __device__ __forceinline__ void rank_keys(const uint64_t* keys, int cnt, uint64_
   }
 }
 
-template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const T* logits, const int32_t* tokens, int V, int n,
-                                                                 int cs, float* logprob, float* entropy, int32_t* top_ids,
-                                                                 float* top_logprobs, int* err) {
+// CTAs of THREADS that take BATCH vectors a thread at once: 16 KB of logits in flight and as much again behind them, four
+// CTAs an SM, or 32 KB and two, or 64 KB and one.
+template <typename T, int THREADS, int BATCH>
+__global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
+    logprobs_kernel(const T* logits, const int32_t* tokens, int V, int n, int cs, float* logprob, float* entropy,
+                    int32_t* top_ids, float* top_logprobs, int* err) {
   constexpr int N = Vec<T>::N;
   constexpr int kWarps = THREADS / 32, kInGroup = THREADS / kLpGroups;
   __shared__ LpSmem sm;
@@ -228,10 +244,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
 
   // ------------------------------------------------------------ one pass: sums, and the candidates
   Part a = {-INFINITY, 0.0f, 0.0f};
-  uint4 v[kLpBatch];
+  uint4 v[BATCH];
   auto load = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const int q = k + i * THREADS;
       v[i] = q < k1 ? ld_stream128(xv + (size_t)q * N)
                     : make_uint4(Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone, Vec<T>::kNone);
@@ -253,14 +269,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   float2 s2 = make_float2(0.f, 0.f), d2 = s2;
   float c = 0.0f;                   // of l
   auto low = Vec<T>::low(0.0f);
-  const int batches = (k1 - k0 + kLpBatch * THREADS - 1) / (kLpBatch * THREADS);
+  const int batches = (k1 - k0 + BATCH * THREADS - 1) / (BATCH * THREADS);
 #pragma unroll 1
   for (int b = 0; b < batches; ++b) {
-    const int k = k0 + tid + b * (kLpBatch * THREADS);
-    uint4 u[kLpBatch];
+    const int k = k0 + tid + b * (BATCH * THREADS);
+    uint4 u[BATCH];
 #pragma unroll
-    for (int i = 0; i < kLpBatch; ++i) u[i] = v[i];
-    if (b + 1 < batches) load(k + kLpBatch * THREADS);
+    for (int i = 0; i < BATCH; ++i) u[i] = v[i];
+    if (b + 1 < batches) load(k + BATCH * THREADS);
     const float bm = Vec<T>::max_of(u);
     if (!(bm <= a.m)) {
       a.s = s2.x + s2.y;
@@ -280,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       if (k < k1 && !isnan(bm)) {
         int first = 0;
 #pragma unroll
-        for (int i = kLpBatch - 1; i > 0; --i)
+        for (int i = BATCH - 1; i > 0; --i)
           if (Vec<T>::max_of(u[i]) == bm) first = i;
         if (Vec<T>::max_of(u[0]) == bm) first = 0;
         key = lp_key(bm, k + first * THREADS);
@@ -295,7 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     if (!large(a.m)) {
       const float2 mul = make_float2(kLog2e, kLog2e), add = make_float2(c, c);
 #pragma unroll
-      for (int i = 0; i < kLpBatch; ++i) {
+      for (int i = 0; i < BATCH; ++i) {
         uint4 w = u[i];
         Vec<T>::raise(w, low);
 #pragma unroll
@@ -309,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     } else if (a.m != -INFINITY) {  // (nothing but -inf so far)
       // read once more, so that this rare form takes no registers from the other
 #pragma unroll 1
-      for (int q = k; q < min(k1, k + kLpBatch * THREADS); q += THREADS) {
+      for (int q = k; q < min(k1, k + BATCH * THREADS); q += THREADS) {
         const uint4 w = ld_plain128(xv + (size_t)q * N);
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     }
     if (bm >= bv) {
 #pragma unroll
-      for (int i = 0; i < kLpBatch; ++i) {
+      for (int i = 0; i < BATCH; ++i) {
         const int q = k + i * THREADS;
         const float vm = Vec<T>::max_of(u[i]);
         if (q >= k1 || vm < bv) continue;
@@ -509,22 +525,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
 template <typename T>
 cudaError_t launch_logprobs(const T* logits, const int32_t* tokens, int R, int V, int n, float* logprob, float* entropy,
                             int32_t* top_ids, float* top_logprobs, const DeviceCtx& dc, cudaStream_t s) {
-  // Many rows: narrow CTAs, four an SM; up to two rows an SM, so many that they fill it; few rows (a quarter of the SMs
-  // at most): narrow ones again, as many a row (a cluster) as are on the GPU at once, each with a vector a thread at
-  // least.  Of 129280 bf16 logits and 20 tokens: 128 rows 13.3 us (clusters of 4 narrow ones 17.2, of 2 middle ones
-  // 15.0), 300 rows 21.4 (narrow 25.2), 600 rows and 5 tokens 33.2 (middle 35.3).  Rows of one batch gain nothing from
-  // threads.  Clusters of 16 are not placed everywhere at once: one row 5.2 us (8: 5.6), 10 rows 6.1 (6.8), 32 rows 10.9
-  // (8: 7.6).
+  // Many rows: narrow CTAs, four an SM; up to two rows an SM, so many that they fill it, and a row an SM, half the threads
+  // with twice the vectors, which halves what every warp does once a row; few rows (a quarter of the SMs at most): narrow
+  // ones again, as many a row (a cluster) as are on the GPU at once, each with a vector a thread at least.  Of 129280 bf16
+  // logits and 20 tokens: 128 rows 12.2 us (1024 threads 13.1, clusters of 4 narrow ones 17), 300 rows 20.8 (narrow 25),
+  // 600 rows and 5 tokens 33 (half the threads 34, wide 35).  Rows of one batch gain nothing from threads.  Clusters of
+  // 16 are not placed everywhere at once: one row 5.1 us (8: 5.6), 10 rows 6.1 (6.8), 32 rows 10.9 (8: 7.6).
   const long long bytes = (long long)V * (long long)sizeof(T);
-  const bool few = 4ll * R <= dc.num_sms, wide = !few && R <= dc.num_sms;
-  const bool narrow = few || R > 2 * dc.num_sms || bytes <= kLpNarrow * kLpBatch * 16;
-  const int threads = narrow ? kLpNarrow : wide ? kLpWide : kLpMiddle;
+  const bool few = 4ll * R <= dc.num_sms;
+  const bool narrow = few || R > 2 * dc.num_sms || bytes <= kLpNarrow * kLpShort * 16, one = !narrow && R <= dc.num_sms;
+  const int threads = narrow ? kLpNarrow : kLpWide, an_sm = narrow ? 4 : one ? 1 : 2;
   const int most = 10ll * R <= dc.num_sms ? kLpMaxCluster : kLpMaxCluster / 2;
   int cs = 1;
-  while (cs < most && (long long)R * cs * 2 * threads <= 1024ll * dc.num_sms && bytes >= 2ll * cs * threads * 16)
-    cs *= 2;
-  auto* kernel = narrow ? logprobs_kernel<T, kLpNarrow>
-                        : wide ? logprobs_kernel<T, kLpWide> : logprobs_kernel<T, kLpMiddle>;
+  while (cs < most && (long long)R * cs * 2 <= (long long)an_sm * dc.num_sms && bytes >= 2ll * cs * threads * 16) cs *= 2;
+  auto* kernel = narrow ? logprobs_kernel<T, kLpNarrow, kLpShort>
+                        : one ? logprobs_kernel<T, kLpWide, kLpLong> : logprobs_kernel<T, kLpWide, kLpShort>;
   static std::atomic<bool> asked[64];  // clusters of 16 allowed on the device
   if (cs > 8 && !asked[dc.device].load()) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
