@@ -10,11 +10,9 @@
 // All four kernels are bound by their bytes, and have few instructions to spare beside them (values go two at a time
 // wherever there is an instruction for it).  16 lanes x 8 columns (one 16-byte load a lane) are a group, so that its
 // maximum meets in four shuffles and nothing is read twice.  Of 9760 x 1280, with what is read and written over the
-// time: the residual and norm 16.1 us, 5.4 TB/s; quantising 8.2 us, 4.6; reading back 7.0 us, 5.3.  A weight of
-// 129280 x 1280 72 us, 6.9.  One row of 1280: 1.7, 1.3 and 1.0 us.
+// time: the residual and norm 15.7 us, 5.6 TB/s; quantising 7.6 us, 5.0; reading back 7.0 us, 5.4.  A weight of
+// 129280 x 1280 72 us, 6.9.  One row of 1280: 1.6, 1.2 and 0.9 us.
 #include <cuda_bf16.h>
-
-#include <algorithm>
 
 #include "internal.h"
 #include "lsv.h"
@@ -88,114 +86,96 @@ __device__ __forceinline__ uint2 codes8(const float2 (&f)[4], float inv) {
 // ------------------------------------------------------------------------------------------------ rows
 // A row is `wpr` warps, `rows` rows are a CTA; warp w of a row takes the slots w, w + wpr, .. of 256 columns, VECS at
 // most, and holds them in registers between the sum of squares and the codes, so that x, y and the output move once.
-// MANY (rows that are a CTA each): a CTA takes one after the other, and loads the next while it works on this one.
 //
 // The normalised value is f / sqrt(mean f^2 + eps) with the root's reciprocal as a pair r + r2 (r2: what the
 // approximation r left out, from the residual of m r^2), so that h is off by little more than its own rounding: codes
 // next to a tie then fall as the formula has them but for 2^-24 of the values next to it.  by_h + by_h2 is 1 / H.
-template <int VECS, bool NORM, bool MANY>
+template <int VECS, bool NORM>
 __global__ void __launch_bounds__(1024) q8_rows_kernel(const bf16* x, const bf16* __restrict__ y, bf16* x_out,
                                                        const bf16* __restrict__ gain, uint8_t* __restrict__ codes,
-                                                       float* __restrict__ scales, int T, int H, int wpr, int rows,
-                                                       float eps, float by_h, float by_h2) {
-  __shared__ float part[MANY ? 2 : 1][kQ8MaxWarps];  // (two: a warp may be a row ahead of another)
+                                                       float* __restrict__ scales, int T, int H, float eps,
+                                                       float by_h, float by_h2) {
+  __shared__ float part[kQ8MaxWarps];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rl = warp / wpr, w = warp - rl * wpr;
-  const int G = (H + kQ8Group - 1) / kQ8Group;
-  int t = blockIdx.x * rows + rl, turn = 0;
-  uint4 v[VECS], u[VECS], nv[VECS], nu[VECS];  // x and y of this row and of the next
-  auto load = [&](uint4(&a)[VECS], uint4(&b)[VECS], int t) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, wpr = blockDim.x >> 5, first = threadIdx.y * wpr;
+  const int G = (uint32_t)(H + kQ8Group - 1) / kQ8Group;
+  const int t = blockIdx.x * blockDim.y + threadIdx.y;
+  const bool live = t < T;
+  const size_t base = (size_t)t * H;
+  uint4 v[VECS], u[VECS];
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      const int c = (w + i * wpr) * kQ8Slot + lane * 8;
-      const bool there = t < T && c < H;
-      a[i] = there ? ld_stream128(x + (size_t)t * H + c) : make_uint4(0, 0, 0, 0);
-      if (NORM && y) b[i] = there ? ld_stream128(y + (size_t)t * H + c) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  load(v, u, t);
-  while (true) {
-    const bool live = t < T;
-    const size_t base = (size_t)t * H;
-    const int t_next = t + (int)gridDim.x;
-    if constexpr (MANY) load(nv, nu, t_next);
-    float r = 1.0f, r2 = 0.0f;
-    if constexpr (NORM) {
-      float2 sq = make_float2(0.0f, 0.0f);
-      if (y) {
-#pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-          const int c = (w + i * wpr) * kQ8Slot + lane * 8;
-          v[i] = make_uint4(add_bf16x2(v[i].x, u[i].x), add_bf16x2(v[i].y, u[i].y), add_bf16x2(v[i].z, u[i].z),
-                            add_bf16x2(v[i].w, u[i].w));
-          if (live && c < H) *reinterpret_cast<uint4*>(x_out + base + c) = v[i];
-        }
-      }
+  for (int i = 0; i < VECS; ++i) {
+    const int c = (w + i * wpr) * kQ8Slot + lane * 8;
+    v[i] = live && c < H ? ld_stream128(x + base + c) : make_uint4(0, 0, 0, 0);
+    if (NORM && y) u[i] = live && c < H ? ld_stream128(y + base + c) : make_uint4(0, 0, 0, 0);
+  }
+  float r = 1.0f, r2 = 0.0f;
+  if constexpr (NORM) {
+    float2 sq = make_float2(0.0f, 0.0f);
+    if (y) {
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
-        float2 f[4];
-        unpack8(v[i], f);
-        // squares of bf16 are exact in 32 bits
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sq = fma2(f[j], f[j], sq);
+        const int c = (w + i * wpr) * kQ8Slot + lane * 8;
+        v[i] = make_uint4(add_bf16x2(v[i].x, u[i].x), add_bf16x2(v[i].y, u[i].y), add_bf16x2(v[i].z, u[i].z),
+                          add_bf16x2(v[i].w, u[i].w));
+        if (live && c < H) *reinterpret_cast<uint4*>(x_out + base + c) = v[i];
       }
-      float ss = sq.x + sq.y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (wpr > 1) {
-        if (lane == 0) part[turn][warp] = ss;
-        __syncthreads();
-        ss = lane < wpr ? part[turn][rl * wpr + lane] : 0.0f;
-        if (MANY) turn ^= 1;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      }
-      const float m = fmaf(ss, by_h, fmaf(ss, by_h2, eps));
-      r = rsqrtf(m);
-      const float q = m * r;
-      // 1 - m r^2, exact but for its own rounding; a mean of zero, infinity or NaN has no correction
-      const float left = fmaf(-q, r, 1.0f) - fmaf(m, r, -q) * r;
-      r2 = 0.5f * r * left;
-      if (!(fabsf(r2) < r)) r2 = 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-      const int slot = w + i * wpr;
-      if (slot * kQ8Slot >= H) break;
-      const int c = slot * kQ8Slot + lane * 8;
-  float2 f[4];
-      uint32_t m;
+      float2 f[4];
       unpack8(v[i], f);
-      if constexpr (NORM) {
+      // squares of bf16 are exact in 32 bits
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = fma2(f[j], make_float2(r2, r2), mul2(f[j], make_float2(r, r)));
-        if (gain && c < H) {
-          float2 g[4];
-          unpack8(ld_plain128(gain + c), g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], g[j]);
-        }
-        m = max8(f);
-      } else {
-        m = max8(v[i]);
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float inv;
-      const float s = scale_of(m, inv);
-      if (live && c < H) {
-        *reinterpret_cast<uint2*>(codes + base + c) = codes8(f, inv);
-        if ((lane & 15) == 0) scales[(size_t)t * G + c / kQ8Group] = s;
-      }
+      for (int j = 0; j < 4; ++j) sq = fma2(f[j], f[j], sq);
     }
-    if (!MANY || t_next >= T) break;
-    t = t_next;
+    float ss = sq.x + sq.y;
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      v[i] = nv[i];
-      u[i] = nu[i];
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (wpr > 1) {
+      if (lane == 0) part[first + w] = ss;
+      __syncthreads();
+      const int lanes = 1 << (32 - __clz(wpr - 1)), of = lane & (lanes - 1);  // (as many as hold a value a warp)
+      ss = of < wpr ? part[first + of] : 0.0f;
+      for (int o = 1; o < lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
+    const float m = fmaf(ss, by_h, fmaf(ss, by_h2, eps));
+    r = rsqrtf(m);
+    const float q = m * r;
+    // 1 - m r^2, exact but for its own rounding; a mean of zero, infinity or NaN has no correction
+    const float left = fmaf(-q, r, 1.0f) - fmaf(m, r, -q) * r;
+    r2 = 0.5f * r * left;
+    if (!(fabsf(r2) < r)) r2 = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int slot = w + i * wpr;
+    if (slot * kQ8Slot >= H) break;
+    const int c = slot * kQ8Slot + lane * 8;
+float2 f[4];
+    uint32_t m;
+    unpack8(v[i], f);
+    if constexpr (NORM) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = fma2(f[j], make_float2(r2, r2), mul2(f[j], make_float2(r, r)));
+      if (gain && c < H) {
+        float2 g[4];
+        unpack8(ld_plain128(gain + c), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], g[j]);
+      }
+      m = max8(f);
+    } else {
+      m = max8(v[i]);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float inv;
+    const float s = scale_of(m, inv);
+    if (live && c < H) {
+      *reinterpret_cast<uint2*>(codes + base + c) = codes8(f, inv);
+      if ((lane & 15) == 0) scales[(size_t)t * G + c / kQ8Group] = s;
     }
   }
 }
@@ -242,7 +222,8 @@ __device__ __forceinline__ uint32_t values2(uint32_t two, float s) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack2(f.x * s, f.y * s);
+  const float2 x = mul2(f, make_float2(s, s));
+  return pack2(x.x, x.y);
 }
 
 // Quotients of the pieces' places by the pieces a row, `per`, as products with 2^64 / per and 2^32 / per rounded up:
@@ -261,50 +242,45 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const uint8_t* __restrict_
   pdl_wait();
   pdl_trigger();
   const long long p0 = (long long)blockIdx.x * (256 * kQ8ReadPieces);
-  const long long row0 = (long long)__umul64hi((uint64_t)p0, p.by_per64);
-  const int col0 = (int)(p0 - row0 * p.per) + (int)threadIdx.x;
-  const long long q0 = p0 + threadIdx.x;
+  const int row0 = (int)__umul64hi((uint64_t)p0, p.by_per64);
+  const int col0 = (int)(p0 - (long long)row0 * p.per) + (int)threadIdx.x;
+  const int left = (int)min(p.pieces - p0, 256ll * kQ8ReadPieces) - (int)threadIdx.x;  // this thread's have places below
+  const uint8_t* from = codes + 8 * (p0 + threadIdx.x);
+  bf16* to = out + 8 * (p0 + threadIdx.x);
   uint2 v[kQ8ReadPieces];
   float s[kQ8ReadPieces];
 #pragma unroll
   for (int i = 0; i < kQ8ReadPieces; ++i) {
-    if (q0 + 256 * i >= p.pieces) break;
+    if (256 * i >= left) break;
     const int c = col0 + 256 * i, dr = (int)__umulhi((uint32_t)c, p.by_per32);
-    v[i] = ld_stream64(codes + 8 * (q0 + 256 * i));
-    s[i] = ld_plain_f32(scales + ((row0 + dr) >> p.shift) * p.G + (c - dr * p.per) / (kQ8Group / 8));
+    v[i] = ld_stream64(from + 8 * 256 * i);
+    s[i] = ld_plain_f32(scales + (size_t)(uint32_t)((row0 + dr) >> p.shift) * p.G +
+                        (uint32_t)(c - dr * p.per) / (kQ8Group / 8));
   }
 #pragma unroll
   for (int i = 0; i < kQ8ReadPieces; ++i) {
-    if (q0 + 256 * i >= p.pieces) break;
-    *reinterpret_cast<uint4*>(out + 8 * (q0 + 256 * i)) =
-        make_uint4(values2(v[i].x & 0xFFFFu, s[i]), values2(v[i].x >> 16, s[i]), values2(v[i].y & 0xFFFFu, s[i]),
-                   values2(v[i].y >> 16, s[i]));
+    if (256 * i >= left) break;
+    *reinterpret_cast<uint4*>(to + 8 * 256 * i) = make_uint4(values2(v[i].x & 0xFFFFu, s[i]), values2(v[i].x >> 16, s[i]),
+                                                             values2(v[i].y & 0xFFFFu, s[i]), values2(v[i].y >> 16, s[i]));
   }
 }
 
 cudaError_t launch_rows(bool norm, const bf16* x, const bf16* y, bf16* x_out, const bf16* gain, uint8_t* codes,
-                        float* scales, int T, int H, float eps, const DeviceCtx& dc, cudaStream_t s) {
+                        float* scales, int T, int H, float eps, cudaStream_t s) {
   const int slots = (H + kQ8Slot - 1) / kQ8Slot;
   // One slot a warp for short rows, two for longer ones, which then have fewer warps to meet: the norm of 1500 x 7168
-  // takes 17.4 us with one and 14.9 with two, of 9760 x 1280 16.1 with either; quantising 9760 x 1280 alone 10.6 and 8.3,
-  // 60000 x 208, a slot a row, 10.3 and 11.3.  Rows of more than eight slots one after the other, two CTAs an SM: the norm
-  // of 1500 x 7168 13.9 us (a CTA a row 14.9), of 3000 x 4096 15.4 (15.7), of 733 x 7120 9.0 (8.8).
-  const bool wide = slots > (norm ? 8 : 1), many = slots > 8;
-  const int vecs = wide ? kQ8Vecs : 1;
+  // takes 16.4 us with one and 14.1 with two, of one row of 1280 1.6 and 1.8, of 9760 x 1280 15.5 with either; quantising
+  // 9760 x 1280 alone, where no warp waits for another, 10.5 and 7.6.
+  const int vecs = slots > (norm ? 8 : 1) ? kQ8Vecs : 1;
   const int wpr = (slots + vecs - 1) / vecs;
   const int rows = wpr >= 8 ? 1 : 8 / wpr;
-  const int ctas = (T + rows - 1) / rows, threads = 32 * wpr * rows;
   const float by_h = (float)(1.0 / H), by_h2 = (float)(1.0 / H - by_h);
-  auto go = [&](auto kernel, int grid) {
-    return launch_pdl(kernel, dim3(grid), dim3(threads), 0, s, x, y, x_out, gain, codes, scales, T, H, wpr, rows, eps, by_h,
-                      by_h2);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3((T + rows - 1) / rows), dim3(32 * wpr, rows), 0, s, x, y, x_out, gain, codes, scales, T,
+                      H, eps, by_h, by_h2);
   };
-  if (many) {
-    const int grid = std::min(ctas, dc.num_sms * (1024 / threads));
-    return norm ? go(q8_rows_kernel<kQ8Vecs, true, true>, grid) : go(q8_rows_kernel<kQ8Vecs, false, true>, grid);
-  }
-  if (norm) return go(q8_rows_kernel<1, true, false>, ctas);
-  return wide ? go(q8_rows_kernel<kQ8Vecs, false, false>, ctas) : go(q8_rows_kernel<1, false, false>, ctas);
+  if (norm) return vecs > 1 ? go(q8_rows_kernel<kQ8Vecs, true>) : go(q8_rows_kernel<1, true>);
+  return vecs > 1 ? go(q8_rows_kernel<kQ8Vecs, false>) : go(q8_rows_kernel<1, false>);
 }
 
 // Sizes of an 8-bit matrix.
@@ -332,10 +308,8 @@ lsv_status quantize_q8_rows(const void* x, int32_t R, int32_t C, void* codes, fl
   if (st != LSV_OK || R == 0) return st;
   if (!x || !codes || !scales) return LSV_ERR_INVALID_ARG;
   if (!aligned({x, codes, scales})) return LSV_ERR_MISALIGNED;
-  DeviceCtx* dc = nullptr;
-  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
   return launch_rows(false, static_cast<const bf16*>(x), nullptr, nullptr, nullptr, static_cast<uint8_t*>(codes), scales,
-                     R, C, 0.0f, *dc, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                     R, C, 0.0f, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? LSV_OK
              : LSV_ERR_CUDA;
 }
@@ -347,10 +321,8 @@ lsv_status rmsnorm_residual_q8(const void* x, const void* y, const void* gain, v
   if (st != LSV_OK || T == 0) return st;
   if (!x || !codes || !scales || (y && !x_out)) return LSV_ERR_INVALID_ARG;
   if (!aligned({x, y, gain, x_out, codes, scales})) return LSV_ERR_MISALIGNED;
-  DeviceCtx* dc = nullptr;
-  if (device_ctx(&dc) != cudaSuccess) return LSV_ERR_CUDA;
   return launch_rows(true, static_cast<const bf16*>(x), static_cast<const bf16*>(y), static_cast<bf16*>(x_out),
-                     static_cast<const bf16*>(gain), static_cast<uint8_t*>(codes), scales, T, H, eps, *dc,
+                     static_cast<const bf16*>(gain), static_cast<uint8_t*>(codes), scales, T, H, eps,
                      reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? LSV_OK
              : LSV_ERR_CUDA;
