@@ -22,12 +22,14 @@
 // - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
 //
 // Output goes by TMA while the next tile runs where its rows begin on 16 bytes; others are written by the warps, whole
-// rows at a time (2440 x 129279 x 1280 578 us; each thread its own row 3036).
+// rows at a time (2440 x 129279 x 1280 563 us; each thread its own row 3036).
 //
-// What bounds the pairs is the sums' own loop, some 180 instructions a warp and group that wait on one another (a group
-// takes 1.1 K cycles, its MMAs 512): 2440 x 129280 x 1280 takes 426 us (1.90 PFLOP/s), 4879 x 1280 x 7168 59 us, of
-// which the FMAs alone are 9 and waiting for the scales 5.  One CTA a tile of 128 x 256 with two warps that issue MMAs: 460 and
-// 63 us; twice the warps with half the columns each: 479 and 68; accumulators handed over in halves: 417 and 63.
+// What bounds the pairs is the way of a group through two accumulators of 256 columns: by time stamps 830 cycles from an
+// accumulator's release to the end of its next group (MMAs 512), 770 until it is read, 100 until that is known, and two
+// groups share them, 0.9 K cycles each; the sums' own loop, some 180 instructions a warp and group, takes as long.
+// 2440 x 129280 x 1280 413 us (1.95 PFLOP/s), 4879 x 1280 x 7168 57 us.  One CTA a tile of 128 x 256 with two warps that
+// issue MMAs: 460 and 63; twice the warps with half the columns each: 479 and 68; accumulators handed over in halves: 417
+// and 63; pairs on 256 x 192 with twelve warps 472 and 55, on 256 x 128 with four accumulators 540 and 64.
 // All sums are of a fixed order: results are the same from run to run, and up to 128 rows a row's bits do not depend
 // on how many rows there are.
 #include <cuda_bf16.h>
@@ -283,8 +285,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
       const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem)), b0 = sdesc_kmajor_sw128(smem_u32(smem) + p.a_bytes);
       for (int it = first; it < p.nitems && ok; it += step) {
         for (int g = g0; g < g1; ++g) {
+          // the accumulators last: what they come from is there by then, and nothing is left to ask for between them and
+          // the MMAs (the other way round 426 us for 413)
           const bool got =
-              mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns) && mbar_wait(&full[stage], phase, p.wait_ns);
+              mbar_wait(&full[stage], phase, p.wait_ns) && mbar_wait(&tempty[buf], buf_phase ^ 1u, p.wait_ns);
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             break;
