@@ -217,6 +217,17 @@ def test_products_write_their_rows_alone():
         assert bool((room[:2048] == 7).all()) and bool((room[2048 + M * N:] == 7).all())
 
 
+# rows of every alignment, out of persistent CTAs, of pairs and of a split's CTAs; the values beside them stay
+@pytest.mark.parametrize("M,N,K", [(100, 19456, 144), (600, 9728, 144), (77, 1000, 1296), (4000, 16, 144)])
+def test_rows_that_begin_anywhere(M, N, K):
+    for more in (1, 2, 3, 4, 5, 6, 7):
+        ops = operands(more, M, N + more, K)
+        room = torch.full((M * (N + more) + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+        got = api.dense_matmul_q8(*cuda(*ops), out=room[2048:2048 + M * (N + more)].view(M, N + more))
+        check_product(ops, got, "N %d " % (N + more))
+        assert bool((room[:2048] == 7).all()) and bool((room[2048 + M * (N + more):] == 7).all())
+
+
 @pytest.mark.parametrize("N,K", [(1280, 1280), (1001, 2064), (20000, 400), (130, 7168)])
 def test_a_rows_bits_do_not_depend_on_the_others(N, K):
     x, xs, w, ws = cuda(*operands(3, 128, N, K))
