@@ -16,8 +16,8 @@
 // warps 4..11 add the groups up: warp w the lanes 32 (w % 4).., half the columns.
 //
 // Forms:
-// - few tiles: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank adds one
-//   slice of the columns up over the ranks, in rank order, through distributed shared memory;
+// - few tiles and many groups: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank
+//   adds one slice of the columns up over the ranks, in rank order, through distributed shared memory;
 // - more tiles than SMs: persistent CTAs take them row tiles first, so that a weight tile is read from HBM once;
 // - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
 //
@@ -502,8 +502,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         const bool got = mbar_wait_cluster(&recv_bar, 0, drain_ns);  // (it is also the sums on their way here)
         if (!got) set_error(p.err, kErrTimeout);
         const int tid = threadIdx.x - 128;
-        uint8_t* staged = smem;  // rows that TMA's alignment does not hold for: [row][column], in the free ring
-        const int stride = cols4 * 8 + 8, cols = min(4 * cols4, p.N - (tv * TN + (int)rank * cols4 * 4));
+        uint8_t* staged = smem;  // where TMA's alignment does not hold: rows of 128 bytes, swizzled, in the free ring
         for (int u = tid; got && u < cols4 * kMmTile; u += 256) {
           const int rl = u & (kMmTile - 1), c4 = u / kMmTile;
           const int m = tr * kTileM + rl, n = tv * TN + ((int)rank * cols4 + c4) * 4;
@@ -515,18 +514,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           }
           const uint2 v = make_uint2(mm_pack(s.x, s.y), mm_pack(s.z, s.w));
           *reinterpret_cast<uint2*>(p.aligned ? reinterpret_cast<uint8_t*>(p.y + (size_t)m * p.N + n)
-                                              : staged + rl * stride + c4 * 8) = v;
+                                              : staged + rl * 128 + (((c4 >> 1) ^ (rl & 7)) << 4) + (c4 & 1) * 8) = v;
         }
         if (!p.aligned) {
-          // neighbouring values by neighbouring lanes
           named_bar_sync(1, 256);
-          const int log_w = __ffs(4 * cols4) - 1, there = min(kMmTile, p.M - tr * kTileM) << log_w;
-          bf16* y = p.y + (size_t)(tr * kTileM) * p.N + tv * TN + (int)rank * cols4 * 4;
-#pragma unroll 4
-          for (int u = tid; u < there; u += 256) {
-            const int rl = u >> log_w, c = u - (rl << log_w);
-            if (got && c < cols) y[(size_t)rl * p.N + c] = *reinterpret_cast<const bf16*>(staged + rl * stride + c * 2);
-          }
+          const int r0 = (warp - 4) * (kMmTile / 8), m = tr * kTileM + r0, n = tv * TN + (int)rank * cols4 * 4;
+          if (__all_sync(0xffffffffu, got) && m < p.M)
+            store_panel(staged + r0 * 128, p.y + (size_t)m * p.N + n, p.N, min(4 * cols4, p.N - n),
+                        min(kMmTile / 8, p.M - m), lane);
         }
       }
     }
@@ -645,6 +640,29 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
+// Clusters of `size` CTAs of the split form that the device holds at once (its SMs come in groups of uneven size).
+int clusters_at_once(int size, const DeviceCtx& dc) {
+  static std::atomic<int> known[64][kMmMaxSplit + 1];
+  int n = known[dc.device][size].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  auto* kernel = q8_matmul_kernel<128, false>;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), kMmSmem, dc.device) != cudaSuccess) return 0;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = kMmSmem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  known[dc.device][size].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw, bf16* y, int M, int N,
                              int K, const DeviceCtx& dc, cudaStream_t s) {
   MmParams p = {};
@@ -661,9 +679,16 @@ cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w
   p.wait_ns = wait_limit_ns();
   const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
   if (M > kMmTile && 2 * pairs >= dc.num_sms) return launch_mm<256, true>(x, w, p, dc, s);
+  // A tile's groups over several CTAs, as far as their clusters are on the GPU at once.  A group takes 0.33 us and the
+  // exchange 2.5 to 3.  128 x 1280 x K, us with 1, 2, 4 and 8 CTAs: K = 512 4.6, 7.1, 6.3; 1280 6.7, 8.0, 6.7, 7.2; 2048 8.8,
+  // 9.0, 7.2, 7.6; 7168 22.6, 15.9, 10.7, 9.2.  Clusters that do not fit at once: 128 x 2048 x 4096 15.3 with 8, 8.9 with 4.
   const long long tiles = (long long)((M + kMmTile - 1) / kMmTile) * ((N + 127) / 128);
-  // a tile's groups over as many CTAs as there are SMs for them
-  while (p.ns < kMmMaxSplit && 2 * p.ns <= p.G && 2 * p.ns * tiles <= dc.num_sms) p.ns *= 2;
+  if (p.G >= 24 && tiles <= clusters_at_once(8, dc))
+    p.ns = 8;
+  else if (p.G >= 12 && tiles <= clusters_at_once(4, dc))
+    p.ns = 4;
+  else if (p.G >= 20 && tiles <= clusters_at_once(2, dc))
+    p.ns = 2;
   return launch_mm<128, false>(x, w, p, dc, s);
 }
 

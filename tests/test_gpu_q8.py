@@ -201,7 +201,8 @@ def test_products(M, N, K):
 @pytest.mark.parametrize("M,N,K", [
     (5, 19500, 128), (100, 9000, 400), (64, 5000, 640), (3, 130, 16384), (128, 2048, 4112),
     (130, 10000, 400), (4000, 300, 272), (512, 9728, 144), (700, 9729, 400), (2049, 4104, 272), (2560, 2048, 1296),
-    (257, 19456, 16), (300, 40000, 128),
+    (257, 19456, 16), (300, 40000, 128), (5, 1001, 3088), (128, 1280, 7168), (300, 2304, 2576), (300, 2301, 2576),
+    (500, 1100, 1552),
 ])
 def test_products_of_every_form(M, N, K):
     ops = operands(N, M, N, K)
@@ -218,7 +219,7 @@ def test_products_write_their_rows_alone():
 
 
 # rows of every alignment, out of persistent CTAs, of pairs and of a split's CTAs; the values beside them stay
-@pytest.mark.parametrize("M,N,K", [(100, 19456, 144), (600, 9728, 144), (77, 1000, 1296), (4000, 16, 144)])
+@pytest.mark.parametrize("M,N,K", [(100, 19456, 144), (600, 9728, 144), (77, 1000, 1296), (77, 1000, 1552), (4000, 16, 144)])
 def test_rows_that_begin_anywhere(M, N, K):
     for more in (1, 2, 3, 4, 5, 6, 7):
         ops = operands(more, M, N + more, K)
@@ -228,7 +229,7 @@ def test_rows_that_begin_anywhere(M, N, K):
         assert bool((room[:2048] == 7).all()) and bool((room[2048 + M * (N + more):] == 7).all())
 
 
-@pytest.mark.parametrize("N,K", [(1280, 1280), (1001, 2064), (20000, 400), (130, 7168)])
+@pytest.mark.parametrize("N,K", [(1280, 1280), (1001, 2064), (20000, 400), (130, 7168), (8000, 2576)])
 def test_a_rows_bits_do_not_depend_on_the_others(N, K):
     x, xs, w, ws = cuda(*operands(3, 128, N, K))
     whole = api.dense_matmul_q8(x, xs, w, ws)
@@ -284,7 +285,7 @@ def test_quantised_normed_multiplied_and_read_in_a_graph():
 
 
 # many calls without a wait between them, each of whose CTAs begin as those of the one before end
-@pytest.mark.parametrize("M,N,K", [(128, 129280, 1280), (100, 20000, 400), (1, 1280, 1280), (700, 9728, 1296)])
+@pytest.mark.parametrize("M,N,K", [(128, 129280, 1280), (100, 20000, 400), (1, 1280, 1280), (1, 1280, 4096), (200, 4096, 2560), (700, 9728, 1296)])
 def test_call_behind_call(M, N, K):
     x, xs, w, ws = cuda(*operands(4, M, N, K))
     want = api.dense_matmul_q8(x, xs, w, ws)
@@ -304,7 +305,7 @@ def test_call_behind_call(M, N, K):
 
 
 # A split, persistent CTAs, and pairs whose last tiles are short
-@pytest.mark.parametrize("M,N,K", [(5, 1280, 1296), (1, 129280, 1280), (128, 40000, 656), (700, 9728, 1296), (129, 40001, 400)])
+@pytest.mark.parametrize("M,N,K", [(5, 1280, 1296), (5, 1280, 3088), (300, 2301, 2576), (1, 129280, 1280), (128, 40000, 656), (700, 9728, 1296), (129, 40001, 400)])
 def test_a_product_whose_waits_run_out_says_so_and_the_next_call_is_right(M, N, K):
     ops = cuda(*operands(M + N, M, N, K))
     ref = api.dense_matmul_q8(*ops).view(torch.int16).clone()
