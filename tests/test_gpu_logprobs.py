@@ -76,10 +76,10 @@ def test_vocabularies_of_every_end(V, dtype):
         check(logits(V, 5, V, dtype), n, what="V %d n %d " % (V, n))
 
 
-# the forms: clusters of 16, 8, 4, 2 narrow CTAs, of wide ones, one wide, middle or narrow CTA a row; rows of one batch
+# the forms: clusters of 16, 8, 4, 2 narrow CTAs, of wide ones, one wide, middle, narrow or tiny CTA a row; rows of one batch
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("R,V", [(1, 129280), (2, 70001), (4, 32000), (16, 129280), (37, 20000), (50, 60001), (60, 129280),
-                                 (100, 33333), (152, 30000), (200, 40001), (304, 20000), (700, 9001), (3000, 257)])
+                                 (100, 33333), (152, 30000), (200, 40001), (304, 20000), (700, 9001), (3000, 257), (320, 3999), (1300, 7001), (1220, 15000)])
 def test_every_form(R, V, dtype):
     check(logits(R, R, V, dtype), 20, what="%d x %d " % (R, V))
 
