@@ -526,19 +526,31 @@ template <typename T>
 cudaError_t launch_logprobs(const T* logits, const int32_t* tokens, int R, int V, int n, float* logprob, float* entropy,
                             int32_t* top_ids, float* top_logprobs, const DeviceCtx& dc, cudaStream_t s) {
   // Many rows: narrow CTAs, four an SM; up to two rows an SM, so many that they fill it, and a row an SM, half the threads
-  // with twice the vectors, which halves what every warp does once a row; few rows (a quarter of the SMs at most): narrow
-  // ones again, as many a row (a cluster) as are on the GPU at once, each with a vector a thread at least.  Of 129280 bf16
-  // logits and 20 tokens: 128 rows 12.2 us (1024 threads 13.1, clusters of 4 narrow ones 17), 300 rows 20.8 (narrow 25),
-  // 600 rows and 5 tokens 33 (half the threads 34, wide 35).  Rows of one batch gain nothing from threads.  Clusters of
-  // 16 are not placed everywhere at once: one row 5.1 us (8: 5.6), 10 rows 6.1 (6.8), 32 rows 10.9 (8: 7.6).
+  // with twice the vectors (wide), which halves what every warp does once a row, in clusters as far as they are on the GPU
+  // at once.  Few rows (a quarter of the SMs at most) of less than 3/4 of a wide CTA's batch each: narrow ones again, as
+  // many a row (a cluster) as are there at once, each with a vector a thread at least.  Of 129280 bf16 logits and 20
+  // tokens: 24 rows 6.6 us (narrow 7.4; of 60000 logits 30 rows 6.3 and 5.7), 128 rows 12.2 (1024 threads 13.1, clusters
+  // of 4 narrow ones 17), 300 rows 20.8 (narrow 25), 600 rows and 5 tokens 33 (half the threads 34, wide 35).  Rows of one
+  // batch gain nothing from threads.  Clusters of 16 narrow ones: one row 5.1 us (8: 5.6), 10 rows 6.1 (6.8), 32 rows 10.9
+  // (8: 7.6).
   const long long bytes = (long long)V * (long long)sizeof(T);
   const bool few = 4ll * R <= dc.num_sms;
-  const bool narrow = few || R > 2 * dc.num_sms || bytes <= kLpNarrow * kLpShort * 16, one = !narrow && R <= dc.num_sms;
-  const int most = 10ll * R <= dc.num_sms ? kLpMaxCluster : kLpMaxCluster / 2, an_sm = narrow ? 4 : one ? 1 : 2;
-  int threads = narrow ? kLpNarrow : kLpWide, cs = 1;
-  while (cs < most && (long long)R * cs * 2 <= (long long)an_sm * dc.num_sms && bytes >= 2ll * cs * threads * 16) cs *= 2;
-  auto* kernel = narrow ? logprobs_kernel<T, kLpNarrow, kLpShort>
-                        : one ? logprobs_kernel<T, kLpWide, kLpLong> : logprobs_kernel<T, kLpWide, kLpShort>;
+  auto* wide = logprobs_kernel<T, kLpWide, kLpLong>;
+  static ClustersAtOnce at_once;
+  int wide_cs = 1;
+  while (wide_cs < kLpMaxCluster / 2 && bytes >= 2ll * wide_cs * kLpWide * 16 &&
+         R <= at_once.of(reinterpret_cast<const void*>(wide), 2 * wide_cs, kLpWide, 0, dc.device))
+    wide_cs *= 2;
+  const bool one = R <= dc.num_sms && bytes > kLpNarrow * kLpShort * 16 &&
+                   (!few || bytes >= (long long)wide_cs * (kLpWide * kLpLong * 16 * 3 / 4));
+  const bool narrow = !one && (few || R > 2 * dc.num_sms || bytes <= kLpNarrow * kLpShort * 16);
+  int threads = kLpWide, cs = one ? wide_cs : 1;
+  if (narrow) {
+    threads = kLpNarrow;
+    const int most = 10ll * R <= dc.num_sms ? kLpMaxCluster : kLpMaxCluster / 2;
+    while (cs < most && (long long)R * cs * 2 <= 4ll * dc.num_sms && bytes >= 2ll * cs * threads * 16) cs *= 2;
+  }
+  auto* kernel = narrow ? logprobs_kernel<T, kLpNarrow, kLpShort> : one ? wide : logprobs_kernel<T, kLpWide, kLpShort>;
   // Short rows: what is done once a row is most of it, and tiny CTAs, eight an SM, have twice the rows at it.  Rows of one
   // of their batches (8 KB), or of four where there are more rows than fit at once: 2000 x 200 bf16 11.2 us (narrow 16.7),
   // 2301 x 5910 17.5 (23.3), 2440 x 16384 26.1 (30.5); 700 x 8192 12.0 (9.3).

@@ -62,7 +62,6 @@ constexpr int kMmPanel = 32 * 128;   // bytes of 64 columns of a warp's 32 rows 
 constexpr int kMmBlock = 4;          // groups whose scales are brought at once
 constexpr int kMmScaleSlots = 4;     // blocks of scales in shared memory
 constexpr int kMmScaleBytes = kMmScaleSlots * kMmBlock * kMmTile * 2 * 4;
-constexpr int kMmMaxSplit = 8;
 constexpr int kMmRowsAtOnce = 8;     // rows of output that a warp holds on their way to where TMA does not store
 // What is in flight when a wait has run out is waited for this long, however short the limit of the waits.
 constexpr uint64_t kMmDrainNs = 2000000000ull;
@@ -640,29 +639,6 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
   return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
-// Clusters of `size` CTAs of the split form that the device holds at once (its SMs come in groups of uneven size).
-int clusters_at_once(int size, const DeviceCtx& dc) {
-  static std::atomic<int> known[64][kMmMaxSplit + 1];
-  int n = known[dc.device][size].load(std::memory_order_relaxed);
-  if (n > 0) return n;
-  auto* kernel = q8_matmul_kernel<128, false>;
-  if (ensure_smem_attr(reinterpret_cast<const void*>(kernel), kMmSmem, dc.device) != cudaSuccess) return 0;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = size;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(size);
-  cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = kMmSmem;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
-  known[dc.device][size].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw, bf16* y, int M, int N,
                              int K, const DeviceCtx& dc, cudaStream_t s) {
   MmParams p = {};
@@ -683,12 +659,14 @@ cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w
   // exchange 2.5 to 3.  128 x 1280 x K, us with 1, 2, 4 and 8 CTAs: K = 512 4.6, 7.1, 6.3; 1280 6.7, 8.0, 6.7, 7.2; 2048 8.8,
   // 9.0, 7.2, 7.6; 7168 22.6, 15.9, 10.7, 9.2.  Clusters that do not fit at once: 128 x 2048 x 4096 15.3 with 8, 8.9 with 4.
   const long long tiles = (long long)((M + kMmTile - 1) / kMmTile) * ((N + 127) / 128);
-  if (p.G >= 24 && tiles <= clusters_at_once(8, dc))
-    p.ns = 8;
-  else if (p.G >= 12 && tiles <= clusters_at_once(4, dc))
-    p.ns = 4;
-  else if (p.G >= 20 && tiles <= clusters_at_once(2, dc))
-    p.ns = 2;
+  if (p.G >= 12) {
+    static ClustersAtOnce at_once;
+    const void* split = reinterpret_cast<const void*>(q8_matmul_kernel<128, false>);
+    const cudaError_t e = ensure_smem_attr(split, kMmSmem, dc.device);
+    if (e != cudaSuccess) return e;
+    auto fit = [&](int size) { return tiles <= at_once.of(split, size, kMmThreads, kMmSmem, dc.device); };
+    p.ns = p.G >= 24 && fit(8) ? 8 : fit(4) ? 4 : p.G >= 20 && fit(2) ? 2 : 1;
+  }
   return launch_mm<128, false>(x, w, p, dc, s);
 }
 
