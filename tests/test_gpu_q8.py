@@ -304,7 +304,8 @@ def test_call_behind_call(M, N, K):
         assert torch.equal(o.view(torch.int16), want.view(torch.int16))
 
 
-# A split, persistent CTAs, and pairs whose last tiles are short
+# One CTA a tile, splits over eight and two CTAs, persistent CTAs, and pairs whose last tiles are short.  (On a GB300 a try of a
+# wait lasts as long as the load; with tries that return at once the limit ran out in every call, and these held as well.)
 @pytest.mark.parametrize("M,N,K", [(5, 1280, 1296), (5, 1280, 3088), (300, 2301, 2576), (1, 129280, 1280), (128, 40000, 656), (700, 9728, 1296), (129, 40001, 400)])
 def test_a_product_whose_waits_run_out_says_so_and_the_next_call_is_right(M, N, K):
     ops = cuda(*operands(M + N, M, N, K))
