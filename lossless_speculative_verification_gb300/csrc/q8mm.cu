@@ -4,9 +4,8 @@
 //
 // The inner sum is the tensor cores' (tcgen05, kind::f8f6f4: four instructions of 32 columns a group, fp32
 // accumulators in TMEM); the outer one, where the scales differ, is an fp32 FMA a group and output in registers.
-// Scales may be any fp32 values: the outer sum costs less than the MMAs that it runs beside (a group of a 128 x 256
-// tile takes the tensor cores 512 cycles, reading it from TMEM 256, its FMAs, two values an instruction, 128), so
-// nothing is won by asking for scales that the tensor cores could apply themselves.
+// Scales may be any fp32 values (the tensor cores' own block scaling takes powers of two): beside a group of a 128 x 256
+// tile, 512 cycles of MMAs, the sums read TMEM for 256 cycles and have 128 of FMAs, two values an instruction.
 //
 // Orientation: 128 rows of x on the MMA's M side, TN weight rows on its N side.  A TMEM lane is then a row of x, a
 // thread's columns lie within one block of 128 weight rows, and the factor of a group is one number a thread.
@@ -18,7 +17,8 @@
 // Forms:
 // - few tiles and many groups: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank
 //   adds one slice of the columns up over the ranks, in rank order, through distributed shared memory;
-// - more tiles than SMs: persistent CTAs take them row tiles first, so that a weight tile is read from HBM once;
+// - else a CTA a tile, and with more tiles than SMs persistent CTAs that take them row tiles first, so that a weight tile
+//   is read from HBM once;
 // - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
 //
 // Output goes by TMA while the next tile runs where its rows begin on 16 bytes; others are written by the warps, whole
