@@ -653,12 +653,18 @@ cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w
   p.y = y;
   p.err = dc.err;
   p.wait_ns = wait_limit_ns();
+  // Pairs save a sixth of the time from some ten groups on and little of few; half of one's rows are idle where the row
+  // tiles are odd.  Us with pairs and without: 2440 x 20000 x 1280 71 and 84, x 256 31 and 30; 1100 x 20000 x 1280 40 and 42;
+  // 600 x 20000 x 4096 67 and 71, x 512 17 and 15; 300 x 40000 x 1280 35 and 30, 300 x 20000 x 4096 51 and 49.
+  const int row_tiles = (M + kMmTile - 1) / kMmTile;
   const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
-  if (M > kMmTile && 2 * pairs >= dc.num_sms) return launch_mm<256, true>(x, w, p, dc, s);
+  if (row_tiles > 1 && 2 * pairs >= dc.num_sms &&
+      (row_tiles % 2 == 0 || (row_tiles > 3 && (long long)row_tiles * p.G >= 64)))
+    return launch_mm<256, true>(x, w, p, dc, s);
   // A tile's groups over several CTAs, as far as their clusters are on the GPU at once.  A group takes 0.33 us and the
   // exchange 2.5 to 3.  128 x 1280 x K, us with 1, 2, 4 and 8 CTAs: K = 512 4.6, 7.1, 6.3; 1280 6.7, 8.0, 6.7, 7.2; 2048 8.8,
   // 9.0, 7.2, 7.6; 7168 22.6, 15.9, 10.7, 9.2.  Clusters that do not fit at once: 128 x 2048 x 4096 15.3 with 8, 8.9 with 4.
-  const long long tiles = (long long)((M + kMmTile - 1) / kMmTile) * ((N + 127) / 128);
+  const long long tiles = (long long)row_tiles * ((N + 127) / 128);
   if (p.G >= 12) {
     static ClustersAtOnce at_once;
     const void* split = reinterpret_cast<const void*>(q8_matmul_kernel<128, false>);

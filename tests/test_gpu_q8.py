@@ -202,7 +202,7 @@ def test_products(M, N, K):
     (5, 19500, 128), (100, 9000, 400), (64, 5000, 640), (3, 130, 16384), (128, 2048, 4112),
     (130, 10000, 400), (4000, 300, 272), (512, 9728, 144), (700, 9729, 400), (2049, 4104, 272), (2560, 2048, 1296),
     (257, 19456, 16), (300, 40000, 128), (5, 1001, 3088), (128, 1280, 7168), (300, 2304, 2576), (300, 2301, 2576),
-    (500, 1100, 1552),
+    (500, 1100, 1552), (300, 40000, 144), (600, 13000, 400), (600, 13001, 1680), (640, 13000, 1680),
 ])
 def test_products_of_every_form(M, N, K):
     ops = operands(N, M, N, K)
