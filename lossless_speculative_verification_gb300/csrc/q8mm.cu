@@ -22,7 +22,7 @@
 // - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
 //
 // Output goes by TMA while the next tile runs where its rows begin on 16 bytes; others are written by the warps, whole
-// rows at a time (2440 x 129279 x 1280 563 us; each thread its own row 3036).
+// rows at a time (2440 x 129279 x 1280 503 us; each thread its own row 3036).
 //
 // What bounds the pairs is the way of a group through two accumulators of 256 columns: by time stamps 830 cycles from an
 // accumulator's release to the end of its next group (MMAs 512), 770 until it is read, 100 until that is known, and two
@@ -90,36 +90,53 @@ __device__ __forceinline__ uint32_t mm_pack(float a, float b) {
 }
 
 // A warp's `rows` x `cols` (64 at most) of output from rows of 128 bytes, 16-byte pieces swizzled, to rows of y that begin
-// anywhere: a row's values by the whole warp, two a lane from its first 4-byte boundary on.  What depends on where a row
-// begins is the same in every other row.
+// anywhere.  Where they begin on 8 bytes, two rows at once, four values a lane; else a row at once, two values a lane from
+// its first 4-byte boundary on, and the values beside those at the end, a row a lane.  Rows of the panel that do not exist
+// are read, and not stored.
 __device__ __forceinline__ void store_panel(const uint8_t* panel, bf16* y, int N, int cols, int rows, int lane) {
-  uint16_t* to = reinterpret_cast<uint16_t*>(y) + 2 * lane;
-  int odd[2];
-  bool both[2], one[2], first[2];
+  if (N % 4 == 0) {
+    const int l = lane & 15, h = lane >> 4;
+    bf16* to = y + (size_t)h * N + 4 * l;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 2 * kMmRowsAtOnce) {
+      uint2 four[kMmRowsAtOnce];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    odd[k] = ((int)(reinterpret_cast<uintptr_t>(y) >> 1) ^ (k & N)) & 1;
-    both[k] = 2 * lane + odd[k] + 1 < cols;
-    one[k] = 2 * lane + odd[k] + 1 == cols;
-    first[k] = odd[k] && lane == 0 && cols > 0;
+      for (int i = 0; i < kMmRowsAtOnce; ++i) {
+        const int r = r0 + 2 * i + h;
+        four[i] = *reinterpret_cast<const uint2*>(panel + r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kMmRowsAtOnce; ++i, to += 2 * (size_t)N)
+        if (r0 + 2 * i + h < rows && 4 * l < cols) *reinterpret_cast<uint2*>(to) = four[i];
+    }
+    return;
   }
+  // (what depends on where a row begins is the same in every other row)
+  const int odd0 = (int)(reinterpret_cast<uintptr_t>(y) >> 1) & 1, odd1 = odd0 ^ (N & 1);
+  const bool both[2] = {2 * lane + odd0 + 1 < cols, 2 * lane + odd1 + 1 < cols};
+  bf16* to = y + 2 * lane;
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += kMmRowsAtOnce) {
     uint32_t two[kMmRowsAtOnce], next[kMmRowsAtOnce];
 #pragma unroll
-    for (int i = 0; i < kMmRowsAtOnce; ++i)  // (rows of the panel that do not exist are read, and not stored)
+    for (int i = 0; i < kMmRowsAtOnce; ++i)
       two[i] = *reinterpret_cast<const uint32_t*>(panel + (r0 + i) * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
 #pragma unroll
     for (int i = 0; i < kMmRowsAtOnce; ++i) next[i] = __shfl_down_sync(0xffffffffu, two[i], 1);
 #pragma unroll
     for (int i = 0; i < kMmRowsAtOnce; ++i, to += N) {
-      const int k = i & 1;
-      const uint32_t v = __byte_perm(two[i], next[i], odd[k] ? 0x5432 : 0x3210);
-      const bool there = r0 + i < rows;
-      if (there && both[k]) *reinterpret_cast<uint32_t*>(to + odd[k]) = v;
-      if (there && one[k]) to[odd[k]] = (uint16_t)v;
-      if (there && first[k]) *to = (uint16_t)two[i];
+      const int odd = i & 1 ? odd1 : odd0;
+      const uint32_t v = __byte_perm(two[i], next[i], odd ? 0x5432 : 0x3210);
+      if (r0 + i < rows && both[i & 1]) *reinterpret_cast<uint32_t*>(to + odd) = v;
     }
+  }
+  if (N % 2 && lane < rows) {
+    const int odd = lane & 1 ? odd1 : odd0, last = cols - 1;
+    const uint8_t* row = panel + lane * 128;
+    bf16* out = y + (size_t)lane * N;
+    if (odd && cols > 0) out[0] = *reinterpret_cast<const bf16*>(row + ((lane & 7) << 4));
+    if (cols > odd && (cols - odd) % 2)
+      out[last] = *reinterpret_cast<const bf16*>(row + (((last >> 3) ^ (lane & 7)) << 4) + (last & 7) * 2);
   }
 }
 static_assert(kMmRowsAtOnce % 8 == 0, "the swizzle's period");
