@@ -98,6 +98,7 @@ class Decoder:
         self.draft_w = {n: (self.emb if n == "emb" else self.w_vocab if n == "w_vocab" else _dev(dw[n], device))
                         for n in api.DRAFT_WEIGHTS}
         self._bufs = {}
+        self._read = {}   # what logprobs=n reads off a pass of (B, Q), by n
 
     def fill_caches(self, seed: int):
         """N(0, 1) keys and values everywhere (the entries of a prefix that is not replayed)."""
@@ -160,13 +161,14 @@ class Decoder:
             b["alen"] = torch.zeros(B, dtype=torch.int32, device=dev)
             b["comm"] = torch.zeros((B, Q), dtype=torch.int32, device=dev)
             self._bufs[(B, Q)] = b
+            self._read[(B, Q)] = {}
         return self._bufs[(B, Q)]
 
-    def _logits(self, b):
-        """The pass's logits [B, Q, V], made when they are first asked for."""
-        if "logits" not in b:
-            b["logits"] = torch.empty((*b["argmax"].shape, self.V), dtype=torch.bfloat16, device=self.device)
-        return b["logits"]
+    def _logits(self, buffers, B, Q):
+        """Logits [B, Q, V] among these buffers, made when they are first asked for."""
+        if "logits" not in buffers:
+            buffers["logits"] = torch.empty((B, Q, self.V), dtype=torch.bfloat16, device=self.device)
+        return buffers["logits"]
 
     def verify(self, tokens, ctx_after, drafts, logprobs: int | None = None):
         """One verify pass.  tokens [B, Q] int32: input 0 is each sequence's last committed token,
@@ -175,10 +177,11 @@ class Decoder:
         stands for a slot without a sequence, as every length does where that call found too few pages: then
         no page is written, and the outputs are of no use).  Returns the pass's buffers: argmax [B, Q]
         (the greedy token after each input), alen [B], comm [B, Q] (the rule's outputs), x [B*Q, H]
-        (the last residual stream, the draft block's next input state).  logprobs=n adds logprob [B, Q]
-        (of comm's tokens; 0 behind the last), entropy [B, Q], top_ids and top_logprobs [B, Q, n], of the
-        bf16 logits after each input (with bf16 weights a second product with the output layer, whose
-        logits the greedy search does not round; V a multiple of 8)."""
+        (the last residual stream, the draft block's next input state), with 8-bit weights logits
+        [B, Q, V].  logprobs=n returns beside them logprob [B, Q] (of comm's tokens; 0 behind the last),
+        entropy [B, Q], top_ids and top_logprobs [B, Q, n], of the bf16 logits after each input, and these
+        (with bf16 weights a second product with the output layer, whose logits the greedy search does not
+        round; V a multiple of 8).  They are kept apart for each n: a pass without them returns none."""
         B, Q = tokens.shape
         b = self.buffers(B, Q)
         nh, hd = self.nh, self.hd
@@ -216,7 +219,7 @@ class Decoder:
             api.moe_verify_layer(b["h"], t["moe"], b["sh"], b["mws"], out=b["y"])
             y = b["y"]
         if self.weights == "q8":
-            logits = self._logits(b)
+            logits = self._logits(b, B, Q)
             api.rmsnorm_residual_q8(b["x"], y if self.layers else None, codes=b["hq"][0], scales=b["hq"][1])
             api.dense_matmul_q8(*b["hq"], *self.vocab_q8, out=logits.view(B * Q, self.V))
             api.spec_verify_accept(logits, drafts, b["lws"], argmax=b["argmax"], accept_len=b["alen"], committed=b["comm"])
@@ -224,15 +227,16 @@ class Decoder:
             api.rmsnorm_residual(b["x"], y, h=b["h"])
             api.spec_verify_lmhead(b["h"], self.w_vocab, drafts, b["lws"], Q - 1, argmax=b["argmax"],
                                    accept_len=b["alen"], committed=b["comm"])
-        if logprobs is not None:
-            logits = self._logits(b)
-            if self.weights != "q8":
-                api.dense_matmul(b["h"], self.w_vocab, out=logits.view(B * Q, self.V))
-            outs = ("logprob", "entropy", "top_ids", "top_logprobs")
-            made = b.setdefault(("logprobs", logprobs), {})
-            b.update(zip(outs, api.spec_logprobs(logits, b["comm"], logprobs, **made)))
-            made.update((n, b[n]) for n in outs)
-        return b
+        if logprobs is None:
+            return b
+        read = self._read[(B, Q)]
+        if self.weights != "q8":
+            logits = self._logits(read, B, Q)
+            api.dense_matmul(b["h"], self.w_vocab, out=logits.view(B * Q, self.V))
+        outs = read.setdefault(logprobs, {})
+        outs.update(zip(("logprob", "entropy", "top_ids", "top_logprobs"),
+                        api.spec_logprobs(logits, b["comm"], logprobs, **outs)))
+        return {**b, "logits": logits, **outs}
 
     def launches_per_verify(self, B: int, Q: int) -> int:
         """Library kernel launches of one verify pass over the bf16 caches, without log probabilities (the MoE layer:

@@ -95,6 +95,26 @@ def test_log_probabilities_of_a_pass(weights):
     assert dec.verify(tokens, after, drafts, logprobs=0)["top_ids"].shape == (B, Q, 0)
 
 
+@pytest.mark.parametrize("weights", ["bf16", "q8"])
+def test_a_pass_returns_its_own_numbers_alone(weights):
+    prob = problem(8, 0.6)
+    B, Q = 2, 3
+    dec = Decoder(prob, B, 64, weights=weights)
+    rs = np.random.default_rng(9)
+    tokens = [torch.from_numpy(rs.integers(0, prob.V, (B, Q)).astype(np.int32)).cuda() for _ in range(2)]
+    after = torch.full((B,), Q, dtype=torch.int32, device="cuda")
+    keys = {"logprob", "entropy", "top_ids", "top_logprobs"}
+    before = set(dec.verify(tokens[0], after, tokens[0][:, 1:].contiguous()))
+    assert not keys & before
+    first = dec.verify(tokens[0], after, tokens[0][:, 1:].contiguous(), logprobs=4)
+    assert keys | {"logits"} <= set(first)
+    # a pass without them returns none, of an earlier pass's neither, nor the earlier pass's logits
+    assert set(dec.verify(tokens[1], after, tokens[1][:, 1:].contiguous())) == before
+    # and what the earlier pass returned still has its own, of its n
+    other = dec.verify(tokens[1], after, tokens[1][:, 1:].contiguous(), logprobs=2)
+    assert first["top_ids"].shape == (B, Q, 4) and other["top_ids"].shape == (B, Q, 2)
+
+
 def test_a_pass_replayed():
     prob = problem(6, 0.6)
     dec = Decoder(prob, 2, 64, weights="q8")
