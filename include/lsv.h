@@ -520,7 +520,8 @@ lsv_status dense_matmul_q8(const void *x, const float *x_scales, const void *w, 
  *     than n, -1 and -inf.  0 <= n <= 32; for n = 0 both may be NULL.
  * A logit of -inf is a token of probability 0 (-inf, and 0 in the entropy).  In a row of
  * nothing else every log probability is -inf and the entropy 0.  A row with a NaN or
- * +inf gives NaN, and -1 as its tokens.  fp32 arithmetic; deterministic.
+ * +inf gives NaN, and -1 as its tokens.  fp32 arithmetic; deterministic; no log probability
+ * is above 0 and no entropy below.
  * V <= 2^30, R >= 0.  Device pointers, 16-byte aligned; rows need no alignment of
  * their own.  No workspace.  One launch. */
 lsv_status spec_logprobs(const void *logits, int32_t logits_fp32, const int32_t *tokens, int32_t R, int32_t V, int32_t n,

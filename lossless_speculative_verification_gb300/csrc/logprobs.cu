@@ -503,22 +503,31 @@ __global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
   const bool bad = isnan(a.s);      // a NaN or +infinity among the logits
   const bool none = a.s == 0.0f;    // nothing but -inf
   const float log_s = logf(a.s), log_sum = log_s - left_out(a.m) * kLn2;
+  // What is next to certain has a log probability next to 0, and rounding may put it above (an entropy below): neither
+  // leaves the side that it lies on.
+  auto log_p = [&](float x) {
+    const float p = (x - a.m) - log_sum;
+    return p > 0.0f ? 0.0f : p;
+  };
   if (tid == 0 && logprob) {
     float p = 0.0f;  // -1: no token
     if (token < -1 || token >= V) {
       set_error(err, kErrDeviceIndex);
       p = NAN;
     } else if (token >= 0) {
-      p = bad ? NAN : none ? -INFINITY : (at_token - a.m) - log_sum;
+      p = bad ? NAN : none ? -INFINITY : log_p(at_token);
     }
     logprob[row] = p;
   }
-  if (tid == 32 && entropy) entropy[row] = bad ? NAN : none ? 0.0f : fmaf(-kLn2, a.d / a.s, log_s);
+  if (tid == 32 && entropy) {
+    const float h = none ? 0.0f : fmaf(-kLn2, a.d / a.s, log_s);
+    entropy[row] = bad ? NAN : h < 0.0f ? 0.0f : h;
+  }
   if (tid < n) {
     const uint64_t k = sm.top[0][tid];
     const bool there = k != 0 && !bad;
     top_ids[(size_t)row * n + tid] = there ? key_token(k) : -1;
-    top_logprobs[(size_t)row * n + tid] = bad ? NAN : !there || none ? -INFINITY : (key_value(k) - a.m) - log_sum;
+    top_logprobs[(size_t)row * n + tid] = bad ? NAN : !there || none ? -INFINITY : log_p(key_value(k));
   }
 }
 

@@ -131,6 +131,21 @@ def test_rows_that_are_no_ordinary_ones(R, V, dtype):
             check(y, n, what=name + " ")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,V", [(64, 1000), (3, 129280), (400, 9001)])
+def test_log_probabilities_are_never_above_0_and_entropies_never_below(R, V, dtype):
+    # one allowed token, and one that outweighs the others by far: log S is 0 but for roundings
+    g = torch.Generator().manual_seed(V)
+    at = torch.randint(0, V, (R,), generator=g)
+    peak = 5 * torch.randn(R, generator=g)
+    for rest, more in ((-torch.inf, 0.0), (0.0, 60.0), (-900.0, 40.0)):
+        x = torch.full((R, V), rest)
+        x[torch.arange(R), at] = peak + more
+        lp, ent, ids, tops = check(x.to(dtype), 2, at.numpy(), what="rest %g " % rest)
+        assert bool((lp <= 0).all()) and bool((tops <= 0).all()) and bool((ent >= 0).all())
+        assert torch.equal(ids[:, 0].cpu(), at.int()) and torch.equal(lp, tops[:, 0])
+
+
 def test_more_vectors_than_there_is_room_for():
     # every vector's largest above all before it: each is collected, until there is no room
     for R, V in ((1, 262144), (130, 120000), (400, 100000)):
