@@ -497,8 +497,9 @@ lsv_status rmsnorm_residual(void *x, const void *y, void *h, int32_t T, int32_t 
  * dense_matmul_q8: y [M, N] = bf16(sum over groups g of x_scales[m, g] *
  *   w_scales[n / 128, g] * sum_{k in g} x[m, k] w[n, k]), x as rows, w as a weight, N of
  *   any size up to 2^26.  The products of a group are summed on the tensor cores, the groups in
- *   fp32 in a fixed order; scales may be any numbers whose products are normal fp32.  Up to 128
- *   rows of x, a row's result does not depend on the others or on M.  No workspace. */
+ *   fp32 in a fixed order; scales may be any numbers whose products are normal fp32.  Up to 256
+ *   rows of x, a row's result does not depend on the others or on M; beyond them, with K above
+ *   1408, its last bits may.  No workspace. */
 lsv_status quantize_q8_rows(const void *x, int32_t R, int32_t C, void *codes, float *scales, lsv_stream stream);
 lsv_status quantize_q8_weight(const void *w, int32_t N, int32_t K, void *codes, float *scales, lsv_stream stream);
 lsv_status dequantize_q8(const void *codes, const float *scales, int32_t R, int32_t C, int32_t rows_per_scale,

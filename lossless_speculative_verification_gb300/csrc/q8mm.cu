@@ -16,7 +16,7 @@
 //
 // Forms:
 // - few tiles and many groups: K is split over the CTAs of a cluster (up to 8), each sums its groups, and every rank
-//   adds one slice of the columns up over the ranks, in rank order, through distributed shared memory;
+//   adds one slice of the columns up over the ranks, by twos and in rank order, through distributed shared memory;
 // - else a CTA a tile, and with more tiles than SMs persistent CTAs that take them row tiles first, so that a weight tile
 //   is read from HBM once;
 // - many rows: pairs of CTAs (cta_group::2) on tiles of 256 x 256, which halves what an SM loads for a product.
@@ -30,8 +30,8 @@
 // 2440 x 129280 x 1280 413 us (1.95 PFLOP/s), 4879 x 1280 x 7168 57 us.  One CTA a tile of 128 x 256 with two warps that
 // issue MMAs: 460 and 63; twice the warps with half the columns each: 479 and 68; accumulators handed over in halves: 417
 // and 63; pairs on 256 x 192 with twelve warps 472 and 55, on 256 x 128 with four accumulators 540 and 64.
-// All sums are of a fixed order: results are the same from run to run, and up to 128 rows a row's bits do not depend
-// on how many rows there are.
+// All sums are of a fixed order: results are the same from run to run, and up to 256 rows a row's bits do not depend
+// on how many rows there are, as a verify pass of several positions a sequence and a decoding step of one want it.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -56,6 +56,7 @@ constexpr int mm_regs_many(bool pair) { return pair ? 216 : 208; }
 static_assert(128 * mm_regs_few(true) + 256 * mm_regs_many(true) <= 384 * kMmRegs, "register split");
 static_assert(128 * mm_regs_few(false) + 256 * mm_regs_many(false) <= 384 * kMmRegs, "register split");
 constexpr int kMmTile = 128;     // rows of x a CTA
+constexpr int kMmSameRows = 256;  // up to so many rows of x, a row's bits do not depend on their number
 constexpr int kMmMaxStages = 12;
 constexpr int kMmSmem = 225 * 1024;  // the ring and what lies behind it
 constexpr int kMmPanel = 32 * 128;   // bytes of 64 columns of a warp's 32 rows of output
@@ -158,9 +159,13 @@ __device__ __forceinline__ float4 load_scales(const float* s, int g, int G) {
 // TN: weight rows a tile.  PAIR: clusters of two CTAs on tiles of 256 rows; each loads its 128 rows of x and half of
 // the weight rows, counts its bytes on the leader's (rank 0's) stage barrier, the leader issues the MMAs of both, and
 // its commits release both CTAs' stages and accumulators; each CTA sums its own 128 rows.
-template <int TN, bool PAIR>
+// TWO: the CTA's groups are the shares of two CTAs of a split twice as wide, and are added up as those two and then their
+// exchange would: share by share (the first one's sums wait in TMEM, in place of the last accumulator), then the two.
+template <int TN, bool PAIR, bool TWO>
 __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_constant__ MmMaps maps, const MmParams p) {
-  constexpr int kBufs = 512 / TN < 8 ? 512 / TN : 8;  // accumulators
+  static_assert(!(PAIR && TWO), "a pair has no accumulator to spare");
+  constexpr int kTmemCols = 512;
+  constexpr int kBufs = kTmemCols / TN - (TWO ? 1 : 0);  // accumulators
   constexpr int kCols = TN / 2;                       // columns a thread
   constexpr int kTileM = PAIR ? 2 * kMmTile : kMmTile;
   extern __shared__ uint8_t smem_raw[];
@@ -177,6 +182,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   const int first = blockIdx.x / size, step = gridDim.x / size;
   // this CTA's groups of each tile: a split's share, at least one (ns <= G)
   const int g0 = PAIR ? 0 : (int)rank * p.G / p.ns, g1 = PAIR ? p.G : ((int)rank + 1) * p.G / p.ns;
+  const int second = (2 * (int)rank + 1) * p.G / (2 * p.ns);  // TWO: where the second share begins
   const int ntn = (p.N + TN - 1) / TN;
 
   if (threadIdx.x == 0) {
@@ -199,10 +205,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   }
   if (warp == 1) {
     if constexpr (PAIR) {
-      tmem_alloc_pair(&tmem_slot, kBufs * TN);
+      tmem_alloc_pair(&tmem_slot, kTmemCols);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(&tmem_slot, kBufs * TN);
+      tmem_alloc(&tmem_slot, kTmemCols);
       tmem_relinquish();
     }
   }
@@ -436,6 +442,22 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           ok = false;
           break;
         }
+        if constexpr (TWO) {
+          if (g == second) {
+#pragma unroll
+            for (int q = 0; q < kCols / 16; ++q) {
+              uint32_t v[16];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                v[2 * j] = __float_as_uint(acc[8 * q + j].x);
+                v[2 * j + 1] = __float_as_uint(acc[8 * q + j].y);
+                acc[8 * q + j] = make_float2(0.f, 0.f);
+              }
+              tmem_st_32x32b_x16(t_row + (uint32_t)(kBufs * TN + 16 * q), v);
+            }
+            tmem_st_wait();
+          }
+        }
         const float2 f2 = make_float2(f, f);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
@@ -467,6 +489,18 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
         if (((g & 3) == 3 || g + 1 == g1) && ++slot == kMmScaleSlots) {
           slot = 0;
           slot_phase ^= 1u;
+        }
+      }
+      if constexpr (TWO) {
+#pragma unroll
+        for (int q = 0; q < kCols / 16; ++q) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(t_row + (uint32_t)(kBufs * TN + 16 * q), v);
+          tmem_ld_wait_for(v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            acc[8 * q + j] =
+                add2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), acc[8 * q + j]);
         }
       }
       if (PAIR || p.ns == 1) {
@@ -523,10 +557,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
           const int rl = u & (kMmTile - 1), c4 = u / kMmTile;
           const int m = tr * kTileM + rl, n = tv * TN + ((int)rank * cols4 + c4) * 4;
           if (m >= p.M || n >= p.N) continue;
-          float4 s = recv[c4 * kMmTile + rl];
-          for (int q = 1; q < p.ns; ++q) {
-            const float4 v = recv[(q * cols4 + c4) * kMmTile + rl];
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+          // shares by twos, as half as many CTAs have them, and then in rank order
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int q = 0; q < p.ns; q += TWO ? 1 : 2) {
+            float4 v = recv[(q * cols4 + c4) * kMmTile + rl];
+            if (!TWO) {
+              const float4 w = recv[((q + 1) * cols4 + c4) * kMmTile + rl];
+              v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+            }
+            if (q == 0) {
+              s = v;
+            } else {
+              s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            }
           }
           const uint2 v = make_uint2(mm_pack(s.x, s.y), mm_pack(s.z, s.w));
           *reinterpret_cast<uint2*>(p.aligned ? reinterpret_cast<uint8_t*>(p.y + (size_t)m * p.N + n)
@@ -570,9 +613,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
   if (warp == 1) {
     tc_fence_after_sync();
     if constexpr (PAIR)
-      tmem_dealloc_pair(tmem_base, kBufs * TN);
+      tmem_dealloc_pair(tmem_base, kTmemCols);
     else
-      tmem_dealloc(tmem_base, kBufs * TN);
+      tmem_dealloc(tmem_base, kTmemCols);
   }
 }
 
@@ -592,7 +635,7 @@ bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t co
 
 int round8(int v) { return (v + 7) / 8 * 8; }
 
-template <int TN, bool PAIR>
+template <int TN, bool PAIR, bool TWO>
 cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const DeviceCtx& dc, cudaStream_t s) {
   constexpr int kTileM = PAIR ? 2 * kMmTile : kMmTile, kBox = PAIR ? TN / 2 : TN;
   const int ntn = (p.N + TN - 1) / TN;
@@ -625,7 +668,7 @@ cudaError_t launch_mm(const uint8_t* x, const uint8_t* w, MmParams p, const Devi
     return cudaErrorInvalidValue;
   maps.y = maps.x;
   if (p.aligned && p.ns == 1 && !make_map(&maps.y, p.y, p.M, p.N, 32)) return cudaErrorInvalidValue;
-  auto* kernel = q8_matmul_kernel<TN, PAIR>;
+  auto* kernel = q8_matmul_kernel<TN, PAIR, TWO>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, dc.device);
   if (e != cudaSuccess) return e;
   // a register split above the launch's own would wait for ever
@@ -677,20 +720,32 @@ cudaError_t launch_q8_matmul(const uint8_t* x, const float* sx, const uint8_t* w
   const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
   if (row_tiles > 1 && 2 * pairs >= dc.num_sms &&
       (row_tiles % 2 == 0 || (row_tiles > 3 && (long long)row_tiles * p.G >= 64)))
-    return launch_mm<256, true>(x, w, p, dc, s);
+    return launch_mm<256, true, false>(x, w, p, dc, s);
   // A tile's groups over several CTAs, as far as their clusters are on the GPU at once.  A group takes 0.33 us and the
   // exchange 2.5 to 3.  128 x 1280 x K, us with 1, 2, 4 and 8 CTAs: K = 512 4.6, 7.1, 6.3; 1280 6.7, 8.0, 6.7, 7.2; 2048 8.8,
   // 9.0, 7.2, 7.6; 7168 22.6, 15.9, 10.7, 9.2.  Clusters that do not fit at once: 128 x 2048 x 4096 15.3 with 8, 8.9 with 4.
-  const long long tiles = (long long)row_tiles * ((N + 127) / 128);
+  const long long weight_tiles = (N + 127) / 128, tiles = row_tiles * weight_tiles;
+  bool two = false;
   if (p.G >= 12) {
     static ClustersAtOnce at_once;
-    const void* split = reinterpret_cast<const void*>(q8_matmul_kernel<128, false>);
+    const void* split = reinterpret_cast<const void*>(q8_matmul_kernel<128, false, false>);
     const cudaError_t e = ensure_smem_attr(split, kMmSmem, dc.device);
     if (e != cudaSuccess) return e;
-    auto fit = [&](int size) { return tiles <= at_once.of(split, size, kMmThreads, kMmSmem, dc.device); };
-    p.ns = p.G >= 24 && fit(8) ? 8 : fit(4) ? 4 : p.G >= 20 && fit(2) ? 2 : 1;
+    auto fit = [&](long long clusters, int size) {
+      return clusters <= at_once.of(split, size, kMmThreads, kMmSmem, dc.device);
+    };
+    // Up to kMmSameRows the shares that are added up go by N and K alone, as one row tile has them, so that a row's bits do
+    // not depend on how many rows there are; where twice as many clusters do not fit, CTAs take two shares each.  It costs
+    // 0.9 us and more where the tiles themselves would ask for another split: 256 x 1280 x 7168 12.6 (11.7), 256 x 4096 x
+    // 4096 14.1 (12.9), x 1536 10.1 (7.7).  (Pairs, above, have weight tiles for all of the SMs: far more than clusters fit,
+    // so that one row tile is not split either.)
+    const bool same = M <= kMmSameRows;
+    const long long of = same ? weight_tiles : tiles;
+    p.ns = p.G >= 24 && fit(of, 8) ? 8 : fit(of, 4) ? 4 : p.G >= 20 && fit(of, 2) ? 2 : 1;
+    two = same && p.ns > 1 && !fit(tiles, p.ns);
+    if (two) p.ns /= 2;
   }
-  return launch_mm<128, false>(x, w, p, dc, s);
+  return two ? launch_mm<128, false, true>(x, w, p, dc, s) : launch_mm<128, false, false>(x, w, p, dc, s);
 }
 
 }  // namespace

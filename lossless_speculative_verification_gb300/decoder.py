@@ -31,8 +31,11 @@ at that call's counts on the device, also inside one graph with it.
 With weights="q8" the projections and the output layer are held in 8 bits: the norms
 before them write 8-bit rows (rmsnorm_residual_q8), the attention's output is quantised
 (quantize_q8_rows), the products are dense_matmul_q8, and the greedy tokens come from the
-output layer's logits (spec_verify_accept).  The experts and the draft block stay as they
-are.  verify(logprobs=n) adds the committed tokens' log probabilities, the entropies and
+output layer's logits (spec_verify_accept), which are rounded to bf16 before that search: of
+equal ones the lower token, where bf16 weights compare the unrounded sums.  A row's products
+are the same in passes of up to 256 positions (B * Q), as the loop's equality with greedy
+decoding needs; in larger ones, from a hidden size of 1424 on, their last bits may differ.  The
+experts and the draft block stay as they are.  verify(logprobs=n) adds the committed tokens' log probabilities, the entropies and
 the n most likely tokens of every position (spec_logprobs).
 """
 from __future__ import annotations

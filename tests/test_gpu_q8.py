@@ -240,6 +240,21 @@ def test_a_rows_bits_do_not_depend_on_the_others(N, K):
     assert torch.equal(api.dense_matmul_q8(x, xs, w, ws).view(torch.int16), whole.view(torch.int16))
 
 
+# K over eight, four and two CTAs (where clusters of them for two row tiles fit at once and where not), whole, and pairs of
+# CTAs; short last groups, weight tiles and rows of y that TMA does not take
+@pytest.mark.parametrize("N,K", [(1280, 7168), (1001, 3088), (640, 4096), (2048, 2048), (4096, 4096), (4099, 1552), (2304, 2576),
+                                 (5120, 5120), (7168, 2576), (8000, 2000), (12000, 1424), (20000, 2048), (1280, 1280)])
+def test_a_rows_bits_do_not_depend_on_the_others_up_to_256(N, K):
+    ops = operands(3, 256, N, K)
+    x, xs, w, ws = cuda(*ops)
+    whole = api.dense_matmul_q8(x, xs, w, ws)
+    check_product(ops, whole)
+    for M in (1, 65, 128, 129, 160, 200, 255):
+        at = slice(256 - M, 256)
+        part = api.dense_matmul_q8(x[at].clone(), xs[at].clone(), w, ws)
+        assert torch.equal(part.view(torch.int16), whole[at].view(torch.int16)), M
+
+
 def test_of_codes_and_powers_of_two_small_products_are_exact():
     # whole numbers whose sums fit 24 bits, outputs that fit 8
     rs = np.random.default_rng(5)

@@ -62,6 +62,25 @@ def test_passes_over_pages_and_contiguous_caches():
     assert torch.equal(*seen)
 
 
+def test_passes_of_many_rows():
+    # projections whose K is split over CTAs, two shares a CTA where there are more than 128 rows: a pass of two positions
+    # of 96 sequences gives what two of one position give
+    dims = synth.MoeDims(0, 2560, 8, 2, 1, 128)
+    prob = synth.decoder_problem(1, dims, V=2048, nh=20, I_draft=256, seed=10, out_scale=0.3)
+    B, Q = 96, 2
+    tokens = torch.from_numpy(np.random.default_rng(11).integers(0, prob.V, (B, Q)).astype(np.int32)).cuda()
+    none = torch.zeros((B, 0), dtype=torch.int32, device="cuda")
+    at = lambda n: torch.full((B,), n, dtype=torch.int32, device="cuda")
+    one, two = (Decoder(prob, B, 16, weights="q8") for _ in range(2))
+    b = two.verify(tokens, at(Q), tokens[:, 1:].contiguous())
+    for i in range(Q):
+        a = one.verify(tokens[:, i:i + 1].contiguous(), at(i + 1), none)
+        for n in ("q", "k", "v", "o"):
+            assert torch.equal(a[n].view(B, -1), b[n].view(B, Q, -1)[:, i]), n
+        assert torch.equal(a["logits"][:, 0], b["logits"][:, i])
+        assert torch.equal(a["argmax"][:, 0], b["argmax"][:, i])
+
+
 @pytest.mark.parametrize("weights", ["bf16", "q8"])
 def test_log_probabilities_of_a_pass(weights):
     prob = problem(4, 0.6)
