@@ -12,8 +12,10 @@
 // bytes of logits) of the largest maxima, so that vectors are collected, by keys of their maxima and places.  Of the
 // first logits of every thread, 64 groups of threads give a bound, the n-th largest of their maxima, which n vectors
 // reach and few others; every fourth batch the n-th largest of what has come is the new one (2440 x 100277 fp32 156 us
-// with it, 168 without).  At the end the vectors, some dozens, are ranked by counting, and the logits of the first n of
-// them, from the bound on, once more.
+// with it, 168 without).  Where more come than there is room for, the bound rises by what has come, and the vectors are
+// collected again behind the pass: with the first quarter of the row masked, 128 x 129280 with 20 tokens 29 us (12.5
+// without a mask; a pass over the row for each token 268), 400 x 50000 with 32 37 us (26; 578).  At the end the vectors,
+// some dozens, are ranked by counting, and the logits of the first n of them, from the bound on, once more.
 //
 // A row is one CTA, or a cluster of up to 16 where there are few rows: its CTAs take a piece each, and rank 0 joins
 // their sums and ranks their candidates, through distributed shared memory, in a fixed order.
@@ -38,6 +40,7 @@ constexpr int kLpMaxTop = 32;      // most alternatives
 constexpr int kLpCandidates = 1024;  // room for the vectors that are collected
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpFew = 128;          // vectors whose logits are looked at without ranking them first
+constexpr int kLpPeriod = 4;         // batches between two looks at how many vectors have come (a power of two)
 static_assert(kLpMaxTop <= kLpGroups && kLpMaxTop == 32 && kLpMaxCluster <= 2 * kLpNarrow / 32, "lists");
 
 // Larger value first, then the lower token; never 0.  -0 and 0 are equal.
@@ -174,9 +177,9 @@ struct __align__(16) LpSmem {
   uint64_t top[kLpMaxCluster][kLpMaxTop];   // the CTA's largest in order, 0 behind them; rank 0's: every rank's
   Part parts[kLpMaxCluster];                // rank 0's: every rank's sums
   Part warp[kLpWide / 32];
-  uint64_t best[kLpWide / 32];
   uint64_t bound;
-  int ncand, nlast;  // vectors; logits at the end
+  int2 ncand;  // vectors, and whether some have been left out for want of room
+  int nlast;   // logits at the end
 };
 
 // Two lists of 32 keys in falling order, one a lane and the other from its end: the 32 largest, in falling order.
@@ -209,6 +212,83 @@ __device__ __forceinline__ void rank_keys(const uint64_t* keys, int cnt, uint64_
     }
     for (int o = 1; o < by; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (part == 0 && k != 0 && r < n) dst[r] = k;
+  }
+}
+
+// A thread's key to its group's largest (groups of a power of two of lanes); and, a barrier later, the bound from the
+// groups, the n-th largest of them, where it is above the one that there is.
+__device__ __forceinline__ void to_groups(LpSmem& sm, uint64_t key, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) {
+    const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+    key = other > key ? other : key;
+  }
+  if ((threadIdx.x & (lanes - 1)) == 0 && threadIdx.x < lanes * kLpGroups) sm.group[threadIdx.x / lanes] = key;
+}
+template <int THREADS>
+__device__ __forceinline__ void bound_of_groups(LpSmem& sm, int n, uint64_t bound) {
+  constexpr int kInGroup = THREADS / kLpGroups;
+  const int mine = threadIdx.x / kInGroup, part = threadIdx.x % kInGroup;  // a group is ranked by so many
+  const uint64_t key = sm.group[mine];
+  int r = 0;
+#pragma unroll
+  for (int j = part; j < kLpGroups; j += kInGroup) r += sm.group[j] > key || (sm.group[j] == key && j < mine);
+#pragma unroll
+  for (int o = 1; o < kInGroup; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  if (part == 0 && r == n - 1 && key > bound) sm.bound = key;
+}
+
+// The groups' largest of the vectors that found room.
+template <int THREADS>
+__device__ __forceinline__ void groups_of_list(LpSmem& sm) {
+  uint64_t key = 0;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < kLpCandidates; i += THREADS) key = sm.cand[i] > key ? sm.cand[i] : key;
+  to_groups(sm, key, THREADS / kLpGroups);
+}
+
+// More vectors came than there is room for (the row begins far below the rest, as masks leave it, or rises): those of the
+// places q0 to q1 once more, from a bound on that leaves few: that of the last ones' groups, and where it leaves too many,
+// once the groups' over all of the places.  Every other look leaves out 500 vectors more, at least: the rest of what found
+// room.  All threads, after a barrier; the caller takes the bound and the number of vectors from sm.
+template <typename T, int THREADS, int BATCH>
+__device__ __forceinline__ void collect_again(LpSmem& sm, const T* xv, int q0, int q1, int n) {
+  auto keys = [&](auto with) {  // each of this thread's
+#pragma unroll 1
+    for (int q = q0 + (int)threadIdx.x; q < q1; q += BATCH * THREADS) {
+      uint4 w[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (q + i * THREADS < q1) w[i] = ld_plain128(xv + (size_t)(q + i * THREADS) * Vec<T>::N);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (q + i * THREADS < q1) with(lp_key(Vec<T>::max_of(w[i]), q + i * THREADS));
+    }
+  };
+  bool many = sm.ncand.x > kLpCandidates;  // (else: the bound has been taken from what came before)
+#pragma unroll 1
+  for (int turn = 0;; ++turn) {
+    const uint64_t below = sm.bound;
+    if (turn == 1) {
+      uint64_t key = 0;
+      keys([&](uint64_t other) { key = other > key ? other : key; });
+      to_groups(sm, key, THREADS / kLpGroups);
+    } else if (many) {
+      groups_of_list<THREADS>(sm);
+    }
+    __syncthreads();
+    if (many) bound_of_groups<THREADS>(sm, n, below);
+    if (threadIdx.x == 0) sm.ncand.x = 0;
+    __syncthreads();
+    const uint64_t bound = sm.bound;
+    keys([&](uint64_t key) {
+      if (key < bound) return;
+      const int c = atomicAdd(&sm.ncand.x, 1);
+      if (c < kLpCandidates) sm.cand[c] = key;
+    });
+    __syncthreads();
+    many = sm.ncand.x > kLpCandidates;
+    if (!many) return;
+    __syncthreads();
   }
 }
 
@@ -255,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
   };
   load(k0 + tid);
   if (tid == 0) {
-    sm.ncand = 0;
+    sm.ncand = make_int2(0, 0);
     sm.nlast = 0;
     sm.bound = 0;
   }
@@ -301,12 +381,9 @@ __global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
         if (Vec<T>::max_of(u[0]) == bm) first = 0;
         key = lp_key(bm, k + first * THREADS);
       }
-      int o = 1;
-      for (; o < kInGroup && o * kLpGroups < k1 - k0; o <<= 1) {
-        const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-        key = other > key ? other : key;
-      }
-      if ((tid & (o - 1)) == 0 && tid < o * kLpGroups) sm.group[tid / o] = key;
+      int lanes = 1;
+      while (lanes < kInGroup && lanes * kLpGroups < k1 - k0) lanes <<= 1;
+      to_groups(sm, key, lanes);
     }
     if (!large(a.m)) {
       const float2 mul = make_float2(kLog2e, kLog2e), add = make_float2(c, c);
@@ -340,14 +417,7 @@ __global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
     if (n == 0) continue;
     if (b == 0) {
       __syncthreads();
-      const int mine = tid / kInGroup, part = tid % kInGroup;  // a group is ranked by so many
-      const uint64_t key = sm.group[mine];
-      int r = 0;
-#pragma unroll
-      for (int j = part; j < kLpGroups; j += kInGroup) r += sm.group[j] > key || (sm.group[j] == key && j < mine);
-#pragma unroll
-      for (int o = 1; o < kInGroup; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-      if (part == 0 && r == n - 1) sm.bound = key;
+      bound_of_groups<THREADS>(sm, n, 0);
       __syncthreads();
       set_bound();
     }
@@ -359,19 +429,27 @@ __global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
         if (q >= k1 || vm < bv) continue;
         const uint64_t key = lp_key(vm, q);
         if (key < bound) continue;
-        const int c = atomicAdd(&sm.ncand, 1);
+        const int c = atomicAdd(&sm.ncand.x, 1);
         if (c < kLpCandidates) sm.cand[c] = key;
       }
     }
-    if ((b & 3) == 3 && b + 1 < batches) {
+    if ((b + 1) % kLpPeriod == 0 && b + 1 < batches) {
       __syncthreads();
-      const int cnt = sm.ncand;
-      if (cnt > 2 * n + 8 && cnt <= kLpCandidates) {
+      const int cnt = sm.ncand.x;
+      if (__builtin_expect(cnt > kLpCandidates, 0)) {
+        // too many: the bound rises all the same, and they are collected again behind the pass
+        groups_of_list<THREADS>(sm);
+        __syncthreads();
+        bound_of_groups<THREADS>(sm, n, bound);
+        if (tid == 0) {
+          sm.ncand = make_int2(0, 1);
+        }
+      } else if (cnt > 2 * n + 8) {
         rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
         __syncthreads();
         if (tid < n) sm.cand[tid] = sm.group[tid];
         if (tid == 0) {
-          sm.ncand = n;
+          sm.ncand.x = n;
           sm.bound = sm.group[n - 1];
         }
       }
@@ -390,74 +468,45 @@ __global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
   if (edge >= 0) add_one(a, ex);
 
   if (n > 0) __syncthreads();  // every candidate is there
-  const int cnt = n > 0 ? sm.ncand : 0;
+  const int2 came = n > 0 ? sm.ncand : make_int2(0, 0);
+  int cnt = came.x;
+  if (__builtin_expect(came.y != 0 || cnt > kLpCandidates, 0)) {
+    collect_again<T, THREADS, BATCH>(sm, xv, k0, k1, n);
+    cnt = sm.ncand.x;
+    set_bound();
+  }
   // The logits of the vectors, of the first n of them where they are many, from the bound on.
   const uint64_t* from = sm.cand;
   int vectors = cnt;
-  if (cnt > kLpFew && cnt <= kLpCandidates) {
+  if (cnt > kLpFew) {
     rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
     __syncthreads();
     from = sm.group;
     vectors = n;
     bv = key_value(sm.group[n - 1]);
   }
-  const bool room = cnt <= kLpCandidates;
   int t0 = -1;
   float f0 = 0.0f;
-  if (room && tid < vectors * N) {
+  if (tid < vectors * N) {
     t0 = head + key_token(from[tid / N]) * N + tid % N;
     f0 = Vec<T>::get(x + t0);  // on its way while the lanes' sums are joined
   }
   a = join_lanes(a, 32);
   if (lane == 0) sm.warp[warp] = a;
   if (n > 0) {
-    if (room) {
-      auto offer = [&](float f, int t) {
-        if (!(f < bv)) sm.last[atomicAdd(&sm.nlast, 1)] = lp_key(f, t);
-      };
-      if (t0 >= 0) offer(f0, t0);
-      for (int i = tid + THREADS; i < vectors * N; i += THREADS) {
-        const int t = head + key_token(from[i / N]) * N + i % N;
-        offer(Vec<T>::get(x + t), t);
-      }
-      if (edge >= 0) offer(ex, edge);
-      __syncthreads();
-      rank_keys<THREADS>(sm.last, sm.nlast, sm.top[0], n);
-    } else {
-      // More vectors than there is room for (logits that rise along the row): the largest key
-      // below the last one, n times, over all of the piece.
-      uint64_t last = ~0ull;
-      for (int r = 0; r < n; ++r) {
-        uint64_t k = 0;
-        if (edge >= 0) {
-          const uint64_t e = lp_key(ex, edge);
-          if (e < last) k = e;
-        }
-        for (int q = k0 + tid; q < k1; q += THREADS) {
-          const uint4 w = ld_plain128(xv + (size_t)q * N);
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const float2 f = Vec<T>::two(w, j / 2);
-            const uint64_t e = lp_key(j & 1 ? f.y : f.x, head + q * N + j);
-            if (e < last && e > k) k = e;
-          }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
-          k = other > k ? other : k;
-        }
-        __syncthreads();
-        if (lane == 0) sm.best[warp] = k;
-        __syncthreads();
-        for (int w = 0; w < kWarps; ++w) k = sm.best[w] > k ? sm.best[w] : k;
-        if (tid == 0) sm.top[0][r] = k;
-        if (k == 0) break;
-        last = k;
-      }
+    auto offer = [&](float f, int t) {
+      if (!(f < bv)) sm.last[atomicAdd(&sm.nlast, 1)] = lp_key(f, t);
+    };
+    if (t0 >= 0) offer(f0, t0);
+    for (int i = tid + THREADS; i < vectors * N; i += THREADS) {
+      const int t = head + key_token(from[i / N]) * N + i % N;
+      offer(Vec<T>::get(x + t), t);
     }
+    if (edge >= 0) offer(ex, edge);
+    __syncthreads();
+    rank_keys<THREADS>(sm.last, sm.nlast, sm.top[0], n);
   }
-  if (n == 0 || !room) __syncthreads();  // the warps' sums are there
+  if (n == 0) __syncthreads();  // the warps' sums are there
   if (warp == kWarps - 1) {              // (the others rank)
     a = join_lanes(sm.warp[lane & (kWarps - 1)], kWarps);
     if (lane == 0) sm.parts[0] = a;

@@ -155,6 +155,65 @@ def test_more_vectors_than_there_is_room_for():
     check(x, 32)
 
 
+def behind(m, what, low):
+    """Logits whose first m a mask has set to `low`."""
+    return torch.where(torch.arange(what.shape[-1]) < m, torch.tensor(low), what)
+
+
+# a row in one wide CTA, in middle, narrow and tiny ones, in clusters of both; pieces of less than one batch of vectors, of
+# a whole number of periods and of more
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,V", [(1, 262144), (3, 129280), (30, 60001), (130, 129280), (200, 70001), (330, 65536), (1300, 16384)])
+def test_first_logits_far_below_the_rest(R, V, dtype):
+    x = logits(R, R, V, dtype)
+    steps = torch.arange(V)
+    kinds = [behind(m, 3 * torch.randn(V), low)
+             for m in (V // 40, V // 8, V // 4 + 3, V // 2, V - 700) for low in (-torch.inf, LOWEST[dtype], -1e9, -1e4, -999.0, -30.0)]
+    kinds += [
+        behind(V // 4, torch.full((V,), 2.5), -torch.inf),              # as many equal ones as there are
+        behind(V // 4, torch.full((V,), 2.5), -30.0),
+        behind(V // 4, (steps % 97).float(), -30.0),
+        behind(V // 3, steps * 1e-3, -30.0),                            # rising behind the mask
+        torch.floor(steps / 4096) + torch.randn(V) * 0.1,               # each stretch above the one before it
+        # all of what rises in a few threads' vectors, of either type: few groups have any of it
+        torch.where(steps // 8 % 128 == 5, steps * 1e-3, -30.0),
+        torch.where(steps // 4 % 512 == 5, steps * 1e-3, -30.0),
+        torch.where(steps // 2048 % 2 == 0, steps * 1e-3, -torch.inf),
+    ]
+    at = np.random.default_rng(V).permutation(max(R, len(kinds)))[:len(kinds)] % R
+    for n in (1, 20, 32) if R <= 3 else (32,):
+        for part in range(0, len(kinds), max(1, R // 2)):               # some beside rows that are ordinary
+            y = x[:min(R, 40)].clone()
+            for r, k in zip(at[part:], kinds[part:part + max(1, R // 2)]):
+                y[r % len(y)] = k.to(dtype)
+            check(y if R <= 40 else torch.cat([y] * (R // len(y) + 1))[:R], n, what="kinds from %d " % part)
+
+
+def test_first_logits_far_below_the_rest_cost_no_more_than_a_second_look():
+    def us(x, n):
+        t = torch.zeros(x.shape[0], dtype=torch.int32, device="cuda")
+        outs = api.spec_logprobs(x, t, n)
+        times = []
+        for _ in range(7):
+            torch.cuda.synchronize()
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(20):
+                api.spec_logprobs(x, t, n, *outs)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) / 20 * 1e3)
+        return min(times)
+
+    for R, V, dtype, n in ((128, 129280, torch.bfloat16, 20), (400, 50000, torch.bfloat16, 32), (1000, 100277, torch.float32, 5)):
+        x = logits(R, 1, V, dtype).cuda().expand(R, V).contiguous()
+        ordinary = us(x, n)
+        for low in (-torch.inf, -1e9, -30.0):
+            x[:, :V // 4] = low
+            # read once or twice more, without sums; a pass for each of the n largest took 7 to 22 times as long
+            assert us(x, n) < 4 * ordinary, (R, V, low)
+
+
 def test_the_largest_in_one_place():
     # the n largest side by side, in one thread's vectors, at the ends, in the elements outside vectors
     for V in (129283, 4099):
