@@ -41,6 +41,7 @@ constexpr int kLpCandidates = 1024;  // room for the vectors that are collected
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpFew = 128;          // vectors whose logits are looked at without ranking them first
 constexpr int kLpPeriod = 4;         // batches between two looks at how many vectors have come (a power of two)
+constexpr float kLpNoBound = -1000.0f;  // a bound that a mask may have left so low
 static_assert(kLpMaxTop <= kLpGroups && kLpMaxTop == 32 && kLpMaxCluster <= 2 * kLpNarrow / 32, "lists");
 
 // Larger value first, then the lower token; never 0.  -0 and 0 are equal.
@@ -475,10 +476,11 @@ __global__ void __launch_bounds__(THREADS, 4096 / (THREADS * BATCH))
     cnt = sm.ncand.x;
     set_bound();
   }
-  // The logits of the vectors, of the first n of them where they are many, from the bound on.
+  // The logits of the vectors, of the first n of them where they are many (or theirs would be, above no bound to speak of),
+  // from the bound on.
   const uint64_t* from = sm.cand;
   int vectors = cnt;
-  if (cnt > kLpFew) {
+  if (cnt > (bv < kLpNoBound ? n : kLpFew)) {
     rank_keys<THREADS>(sm.cand, cnt, sm.group, n);
     __syncthreads();
     from = sm.group;

@@ -212,6 +212,11 @@ def test_first_logits_far_below_the_rest_cost_no_more_than_a_second_look():
             x[:, :V // 4] = low
             # read once or twice more, without sums; a pass for each of the n largest took 7 to 22 times as long
             assert us(x, n) < 4 * ordinary, (R, V, low)
+    # fewer allowed than are asked for: those that are not take no ranking of hundreds (9 times as long)
+    x = logits(1, 100, 9001, torch.bfloat16).cuda()
+    ordinary = us(x, 20)
+    for low in (-torch.inf, LOWEST[torch.bfloat16]):
+        assert us(torch.where(torch.arange(9001, device="cuda") % 900 == 7, x, low), 20) < 3 * ordinary, low
 
 
 def test_the_largest_in_one_place():
