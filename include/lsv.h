@@ -533,7 +533,8 @@ lsv_status spec_logprobs(const void *logits, int32_t logits_fp32, const int32_t 
 lsv_status lsv_get_device_error(int32_t *code_out, lsv_stream stream);
 
 /* Upper bound, in nanoseconds, of every bounded wait inside the kernels
- * (default 2e9).  Process-wide; takes effect for launches after the call. */
+ * (default 2e9).  Process-wide; takes effect for launches after the call.  What
+ * dense_matmul_q8 has in flight when one has run out is waited for up to 2 s. */
 lsv_status lsv_set_wait_limit_ns(uint64_t ns);
 
 /* Launch one CTA that waits on a flag nothing ever sets, using the same

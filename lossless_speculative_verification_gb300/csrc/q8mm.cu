@@ -66,6 +66,8 @@ constexpr int kMmScaleBytes = kMmScaleSlots * kMmBlock * kMmTile * 2 * 4;
 constexpr int kMmRowsAtOnce = 8;     // rows of output that a warp holds on their way to where TMA does not store
 // What is in flight when a wait has run out is waited for this long, however short the limit of the waits.
 constexpr uint64_t kMmDrainNs = 2000000000ull;
+// A limit below this is there to run out: then a tile's first stage is waited for awake, so that it does.
+constexpr uint64_t kMmShortNs = 1000;
 
 struct MmParams {
   int M, N, K, G;      // G: groups of K
@@ -306,6 +308,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) q8_matmul_kernel(const __grid_c
       constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, TN);
       const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem)), b0 = sdesc_kmajor_sw128(smem_u32(smem) + p.a_bytes);
       for (int it = first; it < p.nitems && ok; it += step) {
+        if (p.wait_ns < kMmShortNs) {
+          ok = __all_sync(0xffffffffu, mbar_wait_awake(&full[stage], phase, p.wait_ns));
+          if (!ok) break;
+        }
         for (int g = g0; g < g1; ++g) {
           // the accumulators last: what they come from is there by then, and nothing is left to ask for between them and
           // the MMAs (the other way round 426 us for 413)

@@ -97,6 +97,24 @@ __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) 
   asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
+// mbar_wait without the sleep of its tries, which on a GB300 lasts for as long as a load from memory takes, whatever time
+// they are given: a shorter limit is kept to.
+__device__ __forceinline__ bool mbar_wait_awake(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t deadline = globaltimer_ns() + limit_ns;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer_ns() > deadline) return false;
+  }
+}
+
 // Registers a thread of the calling warpgroup's warps (all of them execute it).  The block's sum may never be above
 // what it was launched with.
 template <int R>

@@ -340,6 +340,32 @@ def test_a_product_whose_waits_run_out_says_so_and_the_next_call_is_right(M, N, 
     assert torch.equal(api.dense_matmul_q8(*ops).view(torch.int16), ref)
 
 
+# the same forms, and two shares a CTA (of a split, and whole): a limit far below a load from memory does run out, in every
+# one, and the call behind it in the stream is right, as are those after it
+@pytest.mark.parametrize("M,N,K", [(5, 1280, 1296), (5, 1280, 3088), (300, 2301, 2576), (1, 129280, 1280), (128, 40000, 656),
+                                   (700, 9728, 1296), (129, 40001, 400), (200, 4096, 2560), (256, 5120, 5120), (1, 16, 16)])
+def test_a_limit_below_a_load_runs_out(M, N, K):
+    ops = cuda(*operands(M + N, M, N, K))
+    ref = api.dense_matmul_q8(*ops).view(torch.int16).clone()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    seen = []
+    try:
+        for turn in range(4):
+            flush.fill_(turn)
+            api.set_wait_limit_ns((1, 100)[turn % 2])
+            api.dense_matmul_q8(*ops)
+            api.set_wait_limit_ns(2000000000)
+            behind = api.dense_matmul_q8(*ops)
+            seen.append(api.get_device_error())
+            assert torch.equal(behind.view(torch.int16), ref)
+    finally:
+        api.set_wait_limit_ns(2000000000)
+    assert 6 in seen and set(seen) <= {0, 6}, seen
+    for _ in range(3):
+        assert torch.equal(api.dense_matmul_q8(*ops).view(torch.int16), ref)
+    assert api.get_device_error() == 0
+
+
 def test_two_calls_at_once():
     a, b = (cuda(*operands(k, 128, 30000, 1280)) for k in (1, 2))
     ra, rb = api.dense_matmul_q8(*a), api.dense_matmul_q8(*b)
