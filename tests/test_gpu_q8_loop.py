@@ -1,6 +1,8 @@
 """The speculative loop with 8-bit projections and output layer (Decoder(weights="q8")): the committed stream equals plain
 greedy decoding with the same weights, token for token, over both caches (a row's products do not depend on the rows
 beside it); and the log probabilities that a pass adds."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -132,6 +134,28 @@ def test_a_pass_returns_its_own_numbers_alone(weights):
     # and what the earlier pass returned still has its own, of its n
     other = dec.verify(tokens[1], after, tokens[1][:, 1:].contiguous(), logprobs=2)
     assert first["top_ids"].shape == (B, Q, 4) and other["top_ids"].shape == (B, Q, 2)
+
+
+@pytest.mark.parametrize("weights", ["bf16", "q8"])
+@pytest.mark.parametrize("B,Q", [(2, 3), (1, 1)])
+def test_launches_of_a_pass(weights, B, Q):
+    # the kernels of a captured pass, which has nothing else in it, are as many as the decoder says
+    dec = Decoder(problem(12, 0.3), B, 64, weights=weights)
+    tokens = torch.zeros((B, Q), dtype=torch.int32, device="cuda")
+    after = torch.full((B,), Q, dtype=torch.int32, device="cuda")
+    drafts = torch.zeros((B, Q - 1), dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        dec.verify(tokens, after, drafts)
+        g = torch.cuda.CUDAGraph(keep_graph=True)
+        with torch.cuda.graph(g, stream=s):
+            dec.verify(tokens, after, drafts)
+    n = ctypes.c_size_t(0)
+    runtime = ctypes.CDLL("libcudart.so.13")
+    assert runtime.cudaGraphGetNodes(ctypes.c_void_p(g.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+    assert n.value == dec.launches_per_verify(B, Q)
+    s.synchronize()
 
 
 def test_a_pass_replayed():
