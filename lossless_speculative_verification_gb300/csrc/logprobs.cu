@@ -4,8 +4,10 @@
 //   m = max_v x_v,  S = sum_v e^(x_v - m),  D = sum_v (x_v - m) e^(x_v - m)
 //   log p_t = x_t - m - log S,   entropy = log S - D / S
 //
-// One pass over the logits with the running maximum, S and D of every thread (rescaled where a maximum rises), bound
-// by their bytes: about five instructions a logit, one of them an exponential.
+// One pass over the logits with the running maximum, S and D of every thread (rescaled where a maximum rises): some eight
+// instructions a logit in the pass, one of them an exponential, and half as many again for what is done once a row.  Many
+// rows are bound by their bytes (2440 x 100277 fp32 156 us, 0.92 of the copy's rate; 2440 x 129280 bf16 121 us, 0.77), a
+// row an SM by those instructions and the row's chain of steps.
 //
 // The n most likely tokens come of the same pass.  Values and tokens form one 64-bit key (larger value first, then the
 // lower token), so that equal logits, which bf16 makes frequent, are no special case.  They lie in the n vectors (16
@@ -589,10 +591,10 @@ cudaError_t launch_logprobs(const T* logits, const int32_t* tokens, int R, int V
   // with twice the vectors (wide), which halves what every warp does once a row, in clusters as far as they are on the GPU
   // at once.  Few rows (a quarter of the SMs at most) of less than 3/4 of a wide CTA's batch each: narrow ones again, as
   // many a row (a cluster) as are there at once, each with a vector a thread at least.  Of 129280 bf16 logits and 20
-  // tokens: 24 rows 6.6 us (narrow 7.4; of 60000 logits 30 rows 6.3 and 5.7), 128 rows 12.2 (1024 threads 13.1, clusters
-  // of 4 narrow ones 17), 300 rows 20.8 (narrow 25), 600 rows and 5 tokens 33 (half the threads 34, wide 35).  Rows of one
-  // batch gain nothing from threads.  Clusters of 16 narrow ones: one row 5.1 us (8: 5.6), 10 rows 6.1 (6.8), 32 rows 10.9
-  // (8: 7.6).
+  // tokens: 24 rows 6.8 us (narrow 7.6; of 60000 logits 30 rows 6.3 and 5.9), 32 rows 6.7 (narrow 7.7), 128 rows 12.5
+  // (clusters of 4 narrow ones 17.1), 300 rows 21.3 (narrow 24.2), 600 rows and 5 tokens narrow 33.2 (twice the threads
+  // 35.3, wide 41.1).  Rows of one batch gain nothing from threads.  Clusters of 16 narrow ones: one row 5.4 us (8: 6.5),
+  // 10 rows 6.2 (6.9).
   const long long bytes = (long long)V * (long long)sizeof(T);
   const bool few = 4ll * R <= dc.num_sms;
   auto* wide = logprobs_kernel<T, kLpWide, kLpLong>;
@@ -612,8 +614,8 @@ cudaError_t launch_logprobs(const T* logits, const int32_t* tokens, int R, int V
   }
   auto* kernel = narrow ? logprobs_kernel<T, kLpNarrow, kLpShort> : one ? wide : logprobs_kernel<T, kLpWide, kLpShort>;
   // Short rows: what is done once a row is most of it, and tiny CTAs, eight an SM, have twice the rows at it.  Rows of one
-  // of their batches (8 KB), or of four where there are more rows than fit at once: 2000 x 200 bf16 11.2 us (narrow 16.7),
-  // 2301 x 5910 17.5 (23.3), 2440 x 16384 26.1 (30.5); 700 x 8192 12.0 (9.3).
+  // of their batches (8 KB), or of four where there are more rows than fit at once: 2000 x 200 bf16 11.9 us (narrow 17.5),
+  // 2301 x 5910 17.8 (23.9), 2440 x 16384 26.7 (31.5); 700 x 8192 12.3 (9.6).
   if (narrow && cs == 1 && bytes <= (R > 8 * dc.num_sms ? 4 : 1) * kLpTiny * kLpShort * 16) {
     kernel = logprobs_kernel<T, kLpTiny, kLpShort>;
     threads = kLpTiny;

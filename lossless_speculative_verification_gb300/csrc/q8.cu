@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(1024) q8_rows_kernel(const bf16* x, const bf16
     const int slot = w + i * wpr;
     if (slot * kQ8Slot >= H) break;
     const int c = slot * kQ8Slot + lane * 8;
-float2 f[4];
+    float2 f[4];
     uint32_t m;
     unpack8(v[i], f);
     if constexpr (NORM) {

@@ -4,8 +4,10 @@
 //
 // The inner sum is the tensor cores' (tcgen05, kind::f8f6f4: four instructions of 32 columns a group, fp32
 // accumulators in TMEM); the outer one, where the scales differ, is an fp32 FMA a group and output in registers.
-// Scales may be any fp32 values (the tensor cores' own block scaling takes powers of two): beside a group of a 128 x 256
-// tile, 512 cycles of MMAs, the sums read TMEM for 256 cycles and have 128 of FMAs, two values an instruction.
+// Scales may be any fp32 numbers whose products, sx sw, are normal ones: the kernel forms them before it multiplies the
+// sums.  (The tensor cores' own block scaling takes powers of two alone, as the quantisers write them; there is no form
+// for it.)  Beside a group of a 128 x 256 tile, 512 cycles of MMAs, the sums read TMEM for 256 cycles and have 128 of FMAs,
+// two values an instruction.
 //
 // Orientation: 128 rows of x on the MMA's M side, TN weight rows on its N side.  A TMEM lane is then a row of x, a
 // thread's columns lie within one block of 128 weight rows, and the factor of a group is one number a thread.
