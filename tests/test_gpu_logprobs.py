@@ -189,6 +189,29 @@ def test_first_logits_far_below_the_rest(R, V, dtype):
             check(y if R <= 40 else torch.cat([y] * (R // len(y) + 1))[:R], n, what="kinds from %d " % part)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,V", [(1, 262144), (130, 129280), (330, 65536), (1300, 16384)])
+def test_what_is_no_number_in_a_row_that_is_collected_again(R, V, dtype):
+    steps = torch.arange(V) * 1e-3
+    kinds = [behind(V // 4, 3 * torch.randn(V), -30.0), steps]
+    x = logits(3, R, V, dtype)
+    t = torch.zeros(R, dtype=torch.int32, device="cuda")
+    bad = []
+    for k, (kind, what, at) in enumerate((kind, what, at) for kind in kinds for what in (torch.nan, torch.inf)
+                                         for at in (0, V // 4 + 1, V - 1)):
+        r = (7 * k) % R
+        x[r] = kind.to(dtype)
+        x[r, at] = what
+        bad.append(r)
+        got = api.spec_logprobs(x.cuda(), t, 32)
+        rows = sorted(set(bad))
+        assert bool(torch.isnan(got[0][rows]).all()) and bool(torch.isnan(got[1][rows]).all())
+        assert bool((got[2][rows] == -1).all()) and bool(torch.isnan(got[3][rows]).all())
+        if R > len(rows):
+            well = [r for r in range(R) if r not in rows]
+            assert bool(torch.isfinite(got[3][well]).all()) and bool(torch.isfinite(got[1][well]).all())
+
+
 def test_first_logits_far_below_the_rest_cost_no_more_than_a_second_look():
     def us(x, n):
         t = torch.zeros(x.shape[0], dtype=torch.int32, device="cuda")
