@@ -34,9 +34,10 @@ before them write 8-bit rows (rmsnorm_residual_q8), the attention's output is qu
 output layer's logits (spec_verify_accept), which are rounded to bf16 before that search: of
 equal ones the lower token, where bf16 weights compare the unrounded sums.  A row's products
 are the same in passes of up to 256 positions (B * Q), as the loop's equality with greedy
-decoding needs; in larger ones, from a hidden size of 1424 on, their last bits may differ.  The
-experts and the draft block stay as they are.  verify(logprobs=n) adds the committed tokens' log probabilities, the entropies and
-the n most likely tokens of every position (spec_logprobs).
+decoding needs; in larger ones, from a hidden size of 1424 on, their last bits may differ.
+The experts and the draft block stay as they are.  verify(logprobs=n) adds the committed
+tokens' log probabilities, the entropies and the n most likely tokens of every position
+(spec_logprobs).
 """
 from __future__ import annotations
 
