@@ -306,6 +306,30 @@ def test_the_same_twice_and_at_once_and_replayed():
     s.synchronize()
 
 
+@pytest.mark.parametrize("R,V,dtype", [(1, 262144, torch.bfloat16), (128, 129280, torch.bfloat16), (400, 50000, torch.float32)])
+def test_rows_that_are_collected_again_are_the_same_twice_and_at_once_and_replayed(R, V, dtype):
+    # which vectors find room first differs from run to run
+    x = torch.stack([behind(V // 4, 3 * torch.randn(V), -30.0), torch.arange(V) * 1e-3]).to(dtype)
+    x = torch.cat([x] * ((R + 1) // 2))[:R].cuda()
+    t = torch.arange(R, dtype=torch.int32, device="cuda")
+    ref = api.spec_logprobs(x, t, 32)
+    same = lambda got: all(torch.equal(p.view(torch.int32), r.view(torch.int32)) for p, r in zip(got, ref))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        a, b = api.spec_logprobs(x, t, 32), api.spec_logprobs(x, t, 32, stream=s)
+        torch.cuda.synchronize()
+        assert same(a) and same(b)
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs = [api.spec_logprobs(x, t, 32) for _ in range(3)]
+        for _ in range(4):
+            g.replay()
+    s.synchronize()
+    assert all(same(o) for o in outs)
+
+
 def test_places_past_32_bits():
     R, V = 17000, 129280
     x = torch.empty((R, V), dtype=torch.bfloat16, device="cuda").fill_(-5.0)

@@ -379,6 +379,22 @@ def test_two_calls_at_once():
         assert torch.equal(oa, ra) and torch.equal(ob, rb)
 
 
+# clusters of both, two shares a CTA and one, beside each other
+@pytest.mark.parametrize("M,N,K", [(256, 4096, 4096), (200, 1280, 7168), (256, 5120, 5120), (128, 1280, 7168)])
+def test_two_split_calls_at_once(M, N, K):
+    a, b = cuda(*operands(1, M, N, K)), cuda(*operands(2, 128, 1280, 4096))
+    ra, rb = api.dense_matmul_q8(*a), api.dense_matmul_q8(*b)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(s):
+            oa = [api.dense_matmul_q8(*a) for _ in range(3)]
+        ob = [api.dense_matmul_q8(*b, stream=t) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o.view(torch.int16), ra.view(torch.int16)) for o in oa)
+        assert all(torch.equal(o.view(torch.int16), rb.view(torch.int16)) for o in ob)
+
+
 # ---------------------------------------------------------------------------------------------- large
 def test_places_past_32_bits():
     R, C = 140000, 16384                                             # 2.3e9 values
